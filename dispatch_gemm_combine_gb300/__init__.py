@@ -21,7 +21,8 @@ __all__ = [
     "moe_set_wait_timeout_ns", "moe_kernel_launch_count", "moe_profile_enable",
     "moe_profile_read", "moe_profile_kernel_name", "Shape", "alloc_plan", "workspace", "plan", "ffn_fwd", "ffn_bwd",
     "bias_struct", "check_device_error", "moe_gather_rows", "moe_combine_rows", "gather_rows",
-    "combine_rows",
+    "combine_rows", "moe_rms_norm_workspace_size", "moe_rms_norm_fwd", "moe_rms_norm_bwd",
+    "rms_norm_workspace", "rms_norm_fwd", "rms_norm_bwd",
 ]
 
 MOE_OK = 0
@@ -115,6 +116,13 @@ def lib():
     L.moe_gather_rows.restype = ctypes.c_int
     L.moe_combine_rows.argtypes = [S, P, P, P, ctypes.c_int32, P, P]
     L.moe_combine_rows.restype = ctypes.c_int
+    I64, I32, F32, SZ = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+    L.moe_rms_norm_workspace_size.argtypes = [I64, I32]
+    L.moe_rms_norm_workspace_size.restype = SZ
+    L.moe_rms_norm_fwd.argtypes = [I64, I32, I32, P, P, P, F32, P, P, P, P, P]
+    L.moe_rms_norm_fwd.restype = ctypes.c_int
+    L.moe_rms_norm_bwd.argtypes = [I64, I32, I32, P, P, P, P, P, P, P, P, SZ, P]
+    L.moe_rms_norm_bwd.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -201,6 +209,21 @@ def moe_plan_noalloc(shape, topk_idx, plan, stream):
                    ctypes.c_void_p]
     fn.restype = ctypes.c_int
     return fn(ctypes.byref(shape), topk_idx, ctypes.byref(plan), stream)
+
+
+def moe_rms_norm_workspace_size(T, H):
+    return lib().moe_rms_norm_workspace_size(T, H)
+
+
+def moe_rms_norm_fwd(T, H, dtype, x, residual, weight, eps, y, y_scale, total, rstd, stream):
+    return lib().moe_rms_norm_fwd(T, H, dtype, x, residual, weight, eps, y, y_scale, total, rstd,
+                                  stream)
+
+
+def moe_rms_norm_bwd(T, H, dtype, dy, d_total, total, rstd, weight, dx, dweight, ws, ws_bytes,
+                     stream):
+    return lib().moe_rms_norm_bwd(T, H, dtype, dy, d_total, total, rstd, weight, dx, dweight, ws,
+                                  ws_bytes, stream)
 
 
 # ---------------------------------------------------------------- torch helpers
@@ -311,6 +334,74 @@ def combine_rows(shape, inv, src, dst, topk_w=None, stream=None):
     import torch
     _check(moe_combine_rows(shape, _ptr(inv), _ptr(topk_w), _ptr(src), src.dtype == torch.float32,
                             _ptr(dst), _stream(stream)), "moe_combine_rows")
+
+
+def _storage_dtype(where, t):
+    import torch
+    if t.dtype is torch.bfloat16:
+        return MOE_BF16
+    if t.dtype is torch.float32:
+        return MOE_FP32
+    raise ValueError("%s: bfloat16 or float32 expected, got %s" % (where, t.dtype))
+
+
+def _dense(where, name, t, shape, dtype):
+    """The tensor's address, after a check that it is what the call reads or
+    writes: this shape and dtype, dense and row-major, on the GPU.  None passes."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError("%s: %s must be a dense %s tensor of shape %s on the GPU, got %s %s%s" % (
+            where, name, dtype, tuple(shape), t.dtype, tuple(t.shape),
+            "" if t.is_contiguous() else " (strided)"))
+    return t.data_ptr()
+
+
+def rms_norm_workspace(T, H, device="cuda"):
+    """Zero-filled workspace of rms_norm_bwd for at most T rows of H columns."""
+    import torch
+    n = moe_rms_norm_workspace_size(T, H)
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_rms_norm_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def rms_norm_fwd(x, weight, y, eps=1e-6, residual=None, total=None, rstd=None, y_scale=None,
+                 stream=None):
+    """y = rms_norm(x + residual) * weight over the last axis of x [T,H].  y is
+    in x's dtype, or with y_scale [T,H/32] (uint8) e4m3 codes [T,H] (uint8 or
+    float8_e4m3fn); total [T,H] and rstd [T] (fp32) receive x + residual and
+    1 / rms, which the backward wants."""
+    import torch
+    T, H = x.shape
+    w, dt, shape = "rms_norm_fwd", x.dtype, x.shape
+    code = _storage_dtype(w, x)
+    ydt = dt
+    if y_scale is not None:
+        ydt = torch.float8_e4m3fn if y.dtype is torch.float8_e4m3fn else torch.uint8
+    _check(lib().moe_rms_norm_fwd(
+        T, H, code, _dense(w, "x", x, shape, dt), _dense(w, "residual", residual, shape, dt),
+        _dense(w, "weight", weight, (H,), dt), eps, _dense(w, "y", y, shape, ydt),
+        _dense(w, "y_scale", y_scale, (T, H // 32), torch.uint8),
+        _dense(w, "total", total, shape, dt), _dense(w, "rstd", rstd, (T,), torch.float32),
+        _stream(stream)), "moe_rms_norm_fwd")
+
+
+def rms_norm_bwd(dy, total, rstd, weight, dx, dweight=None, d_total=None, ws=None, stream=None):
+    """Gradient of rms_norm_fwd: dx [T,H] (of x and of the residual) and dweight
+    [H] (fp32, None for a frozen weight), from dy, the forward's total and rstd,
+    and d_total, the gradient that reaches total from elsewhere (or None).  ws:
+    rms_norm_workspace(T, H), needed with dweight."""
+    import torch
+    T, H = dy.shape
+    w, dt, shape = "rms_norm_bwd", dy.dtype, dy.shape
+    code = _storage_dtype(w, dy)
+    _check(lib().moe_rms_norm_bwd(
+        T, H, code, _dense(w, "dy", dy, shape, dt), _dense(w, "d_total", d_total, shape, dt),
+        _dense(w, "total", total, shape, dt), _dense(w, "rstd", rstd, (T,), torch.float32),
+        _dense(w, "weight", weight, (H,), dt), _dense(w, "dx", dx, shape, dt),
+        _dense(w, "dweight", dweight, (H,), torch.float32), _ptr(ws),
+        0 if ws is None else ws.numel(), _stream(stream)), "moe_rms_norm_bwd")
 
 
 def check_device_error(ws, stream=None):

@@ -25,4 +25,30 @@ cudaError_t abi_tracked_plan(const int* idx, int64_t Tk, int E, int* counts, int
                              cudaStream_t st);
 cudaError_t abi_tracked_memset(void* p, int value, size_t bytes, cudaStream_t st);
 
+// Kernel kinds of the operators outside api.cu, for the launch counter and the
+// event timer (their names: api.cu).
+enum AbiKind : int {
+  kAbiNormFwd = 0, kAbiNormBwd, kNumAbiKinds
+};
+
+// Launch accounting around a launcher of `nkernels` kernels, as moe.h
+// describes it (an event pair is recorded when the timer is on).
+struct AbiTrack {
+  int kind;
+  cudaEvent_t a, b;
+};
+AbiTrack abi_track_begin(AbiKind kind, cudaStream_t st);
+void abi_track_end(const AbiTrack& t, int nkernels, cudaStream_t st);
+
+template <typename F>
+cudaError_t abi_tracked(AbiKind kind, int nkernels, cudaStream_t st, F&& launch) {
+  const AbiTrack t = abi_track_begin(kind, st);
+  const cudaError_t e = launch();
+  abi_track_end(t, nkernels, st);
+  return e;
+}
+
+inline bool abi_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline size_t abi_align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
 }  // namespace moe

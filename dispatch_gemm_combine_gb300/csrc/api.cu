@@ -85,13 +85,15 @@ std::atomic<uint64_t> g_timeout_ns{2000000000ull};
 enum Kind : int {
   kKPlan = 0, kKOffsets, kKGather, kKFwdGateUp, kKFwdDown, kKCombine, kKDgradDown, kKDwReduce,
   kKWgradDown, kKDgradGateUp, kKWgradGateUp, kKMemset, kKTranspose, kKRoute, kKBiasDot,
-  kKBiasGrad, kKSplitSelect, kKGatherIndex, kKCombineDense, kNumKinds
+  kKBiasGrad, kKSplitSelect, kKGatherIndex, kKCombineDense,
+  kKAbi0,   // the kinds of abi_internal.h follow
+  kNumKinds = kKAbi0 + kNumAbiKinds
 };
 const char* const kKindNames[kNumKinds] = {
     "plan", "padded_offsets", "gather_rows", "gemm_fwd_gate_up_act", "gemm_fwd_down_scale",
     "combine", "gemm_dgrad_down_act_bwd", "dw_reduce", "gemm_wgrad_down", "gemm_dgrad_gate_up",
     "gemm_wgrad_gate_up", "memset", "transpose_f32", "route", "bias_slot_dot", "bias_colsum",
-    "split_select", "gather_index", "combine_dense"};
+    "split_select", "gather_index", "combine_dense", "norm_fwd", "norm_bwd"};
 
 std::atomic<uint64_t> g_launches{0};
 std::atomic<int> g_profile{0};
@@ -116,24 +118,35 @@ cudaEvent_t pool_event() {
   return e;
 }
 
+// An event pair on the launching stream when the timer is on, recorded before
+// (begin) and after (end) a launcher; end also counts its kernels.
+AbiTrack track_begin(int kind, cudaStream_t st) {
+  AbiTrack t{kind, nullptr, nullptr};
+  if (g_profile.load(std::memory_order_relaxed)) {
+    std::lock_guard<std::mutex> lk(g_prof_mu);
+    t.a = pool_event();
+    t.b = pool_event();
+    if (t.a && t.b) cudaEventRecord(t.a, st);
+  }
+  return t;
+}
+
+void track_end(const AbiTrack& t, int nkernels, cudaStream_t st) {
+  g_launches.fetch_add(static_cast<uint64_t>(nkernels), std::memory_order_relaxed);
+  if (t.a && t.b) {
+    cudaEventRecord(t.b, st);
+    std::lock_guard<std::mutex> lk(g_prof_mu);
+    g_prof_pending.push_back({t.kind, t.a, t.b});
+  }
+}
+
 // Run one launcher, counting its kernels and, when the timer is on,
 // bracketing it with events on the launching stream.
 template <typename F>
 cudaError_t tracked(int kind, int nkernels, cudaStream_t st, F&& launch) {
-  cudaEvent_t a = nullptr, b = nullptr;
-  if (g_profile.load(std::memory_order_relaxed)) {
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    a = pool_event();
-    b = pool_event();
-    if (a && b) cudaEventRecord(a, st);
-  }
+  const AbiTrack t = track_begin(kind, st);
   const cudaError_t e = launch();
-  g_launches.fetch_add(static_cast<uint64_t>(nkernels), std::memory_order_relaxed);
-  if (a && b) {
-    cudaEventRecord(b, st);
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    g_prof_pending.push_back({kind, a, b});
-  }
+  track_end(t, nkernels, st);
   return e;
 }
 
@@ -462,6 +475,10 @@ cudaError_t abi_tracked_plan(const int* idx, int64_t Tk, int E, int* counts, int
     return launch_plan(idx, Tk, E, counts, offsets, perm, inv, poff, blkhist, err, st);
   });
 }
+
+AbiTrack abi_track_begin(AbiKind kind, cudaStream_t st) { return track_begin(kKAbi0 + kind, st); }
+
+void abi_track_end(const AbiTrack& t, int nkernels, cudaStream_t st) { track_end(t, nkernels, st); }
 
 cudaError_t abi_tracked_memset(void* p, int value, size_t bytes, cudaStream_t st) {
   return tracked(kKMemset, 1, st, [&] { return cudaMemsetAsync(p, value, bytes, st); });

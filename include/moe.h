@@ -300,6 +300,54 @@ const char* moe_status_string(moe_status status);
 moe_status moe_plan_noalloc(const moe_shape* shape, const int32_t* topk_idx,
                             const moe_plan_t* plan, moe_stream_t stream);
 
+/* ---- around the layer: the pages describe the expert layer alone; these are
+ * the steps that a block built on it runs next to it ---- */
+
+/* Blocks of 32 values with one power-of-two scale ("microscaled"), wherever a
+ * call below takes or gives 8- or 4-bit values:
+ *   value = code * 2^(byte - 127), byte in 0..254; byte 255 stands for NaN (the
+ *   whole block).  A quantiser takes the smallest scale with
+ *   max |v| <= 448 * scale (e4m3 codes, one byte each) or 6 * scale (e2m1
+ *   codes, two per byte, the lower one in the low four bits), so it clips
+ *   nothing, and rounds v / scale to the nearest code, ties to even.  A block
+ *   that holds an infinity or a NaN gets byte 255. */
+
+/* RMS norm of the sum of x and the residual stream:
+ *   r = x + residual,  rs = 1 / sqrt(mean over the row of r^2 + eps),
+ *   y = r * rs * weight.
+ *   x, residual [T,H] and weight [H] in `dtype` (moe_dtype); residual may be
+ *     NULL (r = x).
+ *   y: [T,H] in `dtype`, or with y_scale != NULL e4m3 codes [T,H] with their
+ *     scale bytes y_scale [T,H/32].
+ *   total [T,H] in `dtype` and rstd [T] fp32: r (rounded once) and rs; each may
+ *     be NULL.  The norm is of r before that rounding.  The backward wants both.
+ * Requirements: 0 <= T < 2^31; H a multiple of 8 (of 32 with y_scale), at most
+ * 32768; eps >= 0; 16-byte aligned tensors.  total may be x or residual, and y
+ * may be x or residual where it has their type; no other overlap.  Squares are
+ * summed in fp32.  T = 0 is a no-op. */
+moe_status moe_rms_norm_fwd(int64_t T, int32_t H, int32_t dtype, const void* x,
+                            const void* residual, const void* weight, float eps, void* y,
+                            uint8_t* y_scale, void* total, float* rstd, moe_stream_t stream);
+
+/* Bytes of workspace for the weight's gradient (0 for bad dimensions). */
+size_t moe_rms_norm_workspace_size(int64_t T, int32_t H);
+
+/* Gradient of the norm.  With xhat = total * rstd and n = dy * weight:
+ *   dx = rstd * (n - xhat * mean over the row of (n * xhat)) + d_total,
+ *   dweight[h] = sum over the rows of dy * xhat.
+ *   dy, total, d_total [T,H], weight [H] in `dtype`; total and rstd as the
+ *     forward gave them (x itself where there was no residual); d_total is the
+ *     gradient that reaches r from elsewhere (the residual stream), or NULL.
+ *   dx [T,H] in `dtype`: the gradient of x and of the residual alike; it may be
+ *     dy or d_total.
+ *   dweight [H] fp32, or NULL for a frozen weight (ws may then be NULL).  The
+ *     sum runs in a fixed order that depends on T, H and the device only.
+ * T = 0 zero-fills dweight. */
+moe_status moe_rms_norm_bwd(int64_t T, int32_t H, int32_t dtype, const void* dy,
+                            const void* d_total, const void* total, const float* rstd,
+                            const void* weight, void* dx, float* dweight, void* ws,
+                            size_t ws_bytes, moe_stream_t stream);
+
 /* ---- measurement helpers (no counterpart in the pages; they serve the
  * roofline accounting of the benchmark) ---- */
 
