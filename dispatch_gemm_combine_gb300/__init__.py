@@ -22,7 +22,10 @@ __all__ = [
     "moe_profile_read", "moe_profile_kernel_name", "Shape", "alloc_plan", "workspace", "plan", "ffn_fwd", "ffn_bwd",
     "bias_struct", "check_device_error", "moe_gather_rows", "moe_combine_rows", "gather_rows",
     "combine_rows", "moe_rms_norm_workspace_size", "moe_rms_norm_fwd", "moe_rms_norm_bwd",
-    "rms_norm_workspace", "rms_norm_fwd", "rms_norm_bwd",
+    "rms_norm_workspace", "rms_norm_fwd", "rms_norm_bwd", "MoeGrad",
+    "moe_grad_clip_workspace_size", "moe_grad_clip", "grad_table", "grad_clip_workspace",
+    "grad_clip", "moe_mx_quantize", "moe_mx_dequantize", "mx_alloc", "mx_quantize",
+    "mx_dequantize",
 ]
 
 MOE_OK = 0
@@ -60,6 +63,11 @@ class MoeBias(ctypes.Structure):
     """moe_bias_t: optional per-expert biases and their gradient outputs."""
     _fields_ = [("b_gate_up", ctypes.c_void_p), ("b_down", ctypes.c_void_p),
                 ("db_gate_up", ctypes.c_void_p), ("db_down", ctypes.c_void_p)]
+
+
+class MoeGrad(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -123,6 +131,15 @@ def lib():
     L.moe_rms_norm_fwd.restype = ctypes.c_int
     L.moe_rms_norm_bwd.argtypes = [I64, I32, I32, P, P, P, P, P, P, P, P, SZ, P]
     L.moe_rms_norm_bwd.restype = ctypes.c_int
+    G = ctypes.POINTER(MoeGrad)
+    L.moe_grad_clip_workspace_size.argtypes = [G, I64]
+    L.moe_grad_clip_workspace_size.restype = SZ
+    L.moe_grad_clip.argtypes = [G, I64, F32, P, P, SZ, P]
+    L.moe_grad_clip.restype = ctypes.c_int
+    L.moe_mx_quantize.argtypes = [P, I32, I64, I64, I64, P, P, P]
+    L.moe_mx_quantize.restype = ctypes.c_int
+    L.moe_mx_dequantize.argtypes = [P, P, I64, I64, I64, I32, P, P]
+    L.moe_mx_dequantize.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -224,6 +241,22 @@ def moe_rms_norm_bwd(T, H, dtype, dy, d_total, total, rstd, weight, dx, dweight,
                      stream):
     return lib().moe_rms_norm_bwd(T, H, dtype, dy, d_total, total, rstd, weight, dx, dweight, ws,
                                   ws_bytes, stream)
+
+
+def moe_grad_clip_workspace_size(grads, n):
+    return lib().moe_grad_clip_workspace_size(grads, n)
+
+
+def moe_grad_clip(grads, n, max_norm, norm_out, ws, ws_bytes, stream):
+    return lib().moe_grad_clip(grads, n, max_norm, norm_out, ws, ws_bytes, stream)
+
+
+def moe_mx_quantize(w, dtype, E, K, N, codes, scales, stream):
+    return lib().moe_mx_quantize(w, dtype, E, K, N, codes, scales, stream)
+
+
+def moe_mx_dequantize(codes, scales, E, K, N, dtype, w, stream):
+    return lib().moe_mx_dequantize(codes, scales, E, K, N, dtype, w, stream)
 
 
 # ---------------------------------------------------------------- torch helpers
@@ -402,6 +435,73 @@ def rms_norm_bwd(dy, total, rstd, weight, dx, dweight=None, d_total=None, ws=Non
         _dense(w, "weight", weight, (H,), dt), _dense(w, "dx", dx, shape, dt),
         _dense(w, "dweight", dweight, (H,), torch.float32), _ptr(ws),
         0 if ws is None else ws.numel(), _stream(stream)), "moe_rms_norm_bwd")
+
+
+def grad_table(grads, out=None):
+    """The list of gradients that grad_clip works on: an array of MoeGrad over
+    dense tensors (bf16 or fp32, mixed as they come).  out: the tensors that
+    receive the scaled gradients, None for in place, False for the norm alone.
+    The table keeps addresses, not tensors: build it again when they move."""
+    grads = list(grads)
+    out = grads if out is None else ([None] * len(grads) if out is False else list(out))
+    if len(out) != len(grads):
+        raise ValueError("grad_table: %d outputs for %d gradients" % (len(out), len(grads)))
+    t = (MoeGrad * max(1, len(grads)))()
+    for i, (g, o) in enumerate(zip(grads, out)):
+        code = _storage_dtype("grad_table", g)
+        t[i] = MoeGrad(_dense("grad_table", "gradient %d" % i, g, g.shape, g.dtype),
+                       _dense("grad_table", "output %d" % i, o, g.shape, g.dtype), g.numel(), code)
+    t.count = len(grads)
+    return t
+
+
+def grad_clip_workspace(table, device="cuda"):
+    """Zero-filled workspace of grad_clip for this table."""
+    import torch
+    n = moe_grad_clip_workspace_size(table, table.count)
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_grad_clip_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def grad_clip(table, max_norm, norm, ws, stream=None):
+    """Scale the table's gradients so that their global norm is at most max_norm.
+    norm [2] (fp32, on the GPU) receives the norm before and the factor applied
+    (1 where nothing is clipped, or where the norm is not finite)."""
+    import torch
+    _check(lib().moe_grad_clip(table, table.count, max_norm,
+                               _dense("grad_clip", "norm", norm, (2,), torch.float32), _ptr(ws),
+                               ws.numel(), _stream(stream)), "moe_grad_clip")
+
+
+def mx_alloc(E, K, N, device="cuda"):
+    """(codes [E,N,K/2], scales [E,N,K/32]), uint8, for weights [E,K,N]."""
+    import torch
+    return (torch.empty((E, N, K // 2), dtype=torch.uint8, device=device),
+            torch.empty((E, N, K // 32), dtype=torch.uint8, device=device))
+
+
+def mx_quantize(w, codes, scales, stream=None):
+    """Microscaled 4-bit codes and scale bytes (mx_alloc) of weights w [E,K,N]."""
+    import torch
+    E, K, N = w.shape
+    f = "mx_quantize"
+    _check(lib().moe_mx_quantize(
+        _dense(f, "w", w, w.shape, w.dtype), _storage_dtype(f, w), E, K, N,
+        _dense(f, "codes", codes, (E, N, K // 2), torch.uint8),
+        _dense(f, "scales", scales, (E, N, K // 32), torch.uint8), _stream(stream)),
+        "moe_mx_quantize")
+
+
+def mx_dequantize(codes, scales, w, stream=None):
+    """The values of microscaled codes, into w [E,K,N] (bf16 or fp32)."""
+    import torch
+    E, K, N = w.shape
+    f = "mx_dequantize"
+    _check(lib().moe_mx_dequantize(
+        _dense(f, "codes", codes, (E, N, K // 2), torch.uint8),
+        _dense(f, "scales", scales, (E, N, K // 32), torch.uint8), E, K, N, _storage_dtype(f, w),
+        _dense(f, "w", w, w.shape, w.dtype), _stream(stream)), "moe_mx_dequantize")
 
 
 def check_device_error(ws, stream=None):

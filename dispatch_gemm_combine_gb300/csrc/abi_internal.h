@@ -28,7 +28,8 @@ cudaError_t abi_tracked_memset(void* p, int value, size_t bytes, cudaStream_t st
 // Kernel kinds of the operators outside api.cu, for the launch counter and the
 // event timer (their names: api.cu).
 enum AbiKind : int {
-  kAbiNormFwd = 0, kAbiNormBwd, kNumAbiKinds
+  kAbiNormFwd = 0, kAbiNormBwd, kAbiGradNorm, kAbiGradScale, kAbiMxQuantize, kAbiMxDequantize,
+  kNumAbiKinds
 };
 
 // Launch accounting around a launcher of `nkernels` kernels, as moe.h

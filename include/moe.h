@@ -348,6 +348,47 @@ moe_status moe_rms_norm_bwd(int64_t T, int32_t H, int32_t dtype, const void* dy,
                             const void* weight, void* dx, float* dweight, void* ws,
                             size_t ws_bytes, moe_stream_t stream);
 
+/* One gradient of a list: n elements of `dtype` (moe_dtype) at src, to be
+ * written scaled to dst (src itself: in place; NULL: only the norm is wanted).
+ * The struct lives in host memory; src and dst are device pointers, aligned to
+ * their elements (16-byte aligned ones are faster). */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t n;
+  int32_t dtype;
+} moe_grad_t;
+
+/* Bytes of workspace of moe_grad_clip for this list (0 for a bad list).  It is
+ * zero-filled by the caller before its first use and 256-byte aligned. */
+size_t moe_grad_clip_workspace_size(const moe_grad_t* grads, int64_t n);
+
+/* Global norm of a list of gradients, and clipping by it:
+ *   norm = sqrt(sum over all elements of all tensors of g^2),
+ *   coef = min(1, max_norm / (norm + 1e-6)),  dst = coef * src.
+ *   norm_out [2] fp32 (device): norm, coef.
+ * The squares are summed in fp32 and double in a fixed order, in range for every
+ * finite fp32 gradient.  A norm that is not finite (a gradient holds an
+ * infinity or a NaN) gives coef = 1: the gradients come through unscaled and
+ * norm_out tells the caller to skip the step.  max_norm >= 0 (infinity: never
+ * clips).  dst is src or does not overlap any src.  The list is read before the
+ * call returns.  An empty list has the norm 0. */
+moe_status moe_grad_clip(const moe_grad_t* grads, int64_t n, float max_norm, float* norm_out,
+                         void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Expert weights in microscaled 4-bit (blocks of 32 along K, the contraction of
+ * x @ w):
+ *   w [E,K,N] in `dtype` (moe_dtype), as w_gate_up (K = H, N = 2I) and w_down
+ *     (K = I, N = H) are;
+ *   codes [E,N,K/2]: e2m1, K innermost;  scales [E,N,K/32]: the blocks' bytes.
+ * K a multiple of 32, N of 8; w and codes 16-byte aligned; E = 0 is a no-op.
+ * moe_mx_dequantize gives the codes' values, rounded once to `dtype` (bf16 holds
+ * them exactly while scale byte + code stay in its range). */
+moe_status moe_mx_quantize(const void* w, int32_t dtype, int64_t E, int64_t K, int64_t N,
+                           uint8_t* codes, uint8_t* scales, moe_stream_t stream);
+moe_status moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t E, int64_t K,
+                             int64_t N, int32_t dtype, void* w, moe_stream_t stream);
+
 /* ---- measurement helpers (no counterpart in the pages; they serve the
  * roofline accounting of the benchmark) ---- */
 

@@ -43,3 +43,56 @@ def test_rms_norm_helper_refusals(L):
         L.rms_norm_fwd(x, w, x)
     with pytest.raises(ValueError):           # a type that is not held
         L.rms_norm_fwd(x.double(), w, x)
+
+
+def test_grad_clip_refusals(L):
+    def table(*entries):
+        return (L.MoeGrad * len(entries))(*[L.MoeGrad(*e) for e in entries])
+
+    good = table((16, 16, 5, L.MOE_FP32), (18, 34, 7, L.MOE_BF16), (None, None, 0, L.MOE_FP32))
+    size = L.moe_grad_clip_workspace_size(good, 3)
+    assert size > 0 and L.moe_grad_clip_workspace_size(None, 0) > 0
+    for bad in (table((None, 16, 5, L.MOE_FP32)), table((18, 16, 5, L.MOE_FP32)),
+                table((16, 18, 5, L.MOE_FP32)), table((17, 16, 5, L.MOE_BF16)),
+                table((16, 16, -1, L.MOE_FP32)), table((16, 16, 5, 9))):
+        assert L.moe_grad_clip_workspace_size(bad, 1) == 0
+        assert L.moe_grad_clip(bad, 1, 1.0, 16, 256, 1 << 30, None) == L.MOE_ERR_INVALID_ARG
+    args = dict(grads=good, n=3, max_norm=1.0, norm_out=16, ws=256, ws_bytes=size, stream=None)
+    for bad in (dict(n=-1), dict(grads=None), dict(max_norm=-1.0), dict(max_norm=float("nan")),
+                dict(norm_out=None), dict(norm_out=18), dict(ws=None), dict(ws=272)):
+        assert L.moe_grad_clip(**dict(args, **bad)) == L.MOE_ERR_INVALID_ARG, bad
+    assert L.moe_grad_clip(**dict(args, ws_bytes=size - 1)) == L.MOE_ERR_WORKSPACE
+    many = table(*[(16, 16, 5, L.MOE_FP32)] * 200)
+    assert L.moe_grad_clip_workspace_size(many, 200) > size
+
+
+def test_mx_refusals(L):
+    ok = dict(w=16, dtype=L.MOE_BF16, E=2, K=64, N=16, codes=16, scales=1, stream=None)
+    for bad in (dict(K=48), dict(K=0), dict(N=12), dict(N=0), dict(E=-1), dict(dtype=5),
+                dict(w=None), dict(codes=None), dict(scales=None), dict(w=8), dict(codes=8),
+                dict(E=1 << 40)):
+        assert L.moe_mx_quantize(**dict(ok, **bad)) == L.MOE_ERR_INVALID_ARG, bad
+        assert L.moe_mx_dequantize(**dict(ok, **bad)) == L.MOE_ERR_INVALID_ARG, bad
+    assert L.moe_mx_quantize(**dict(ok, E=0, w=None, codes=None, scales=None)) == L.MOE_OK
+    assert L.moe_mx_quantize(**dict(ok, E=0, K=48)) == L.MOE_ERR_INVALID_ARG
+
+
+def test_grad_struct_layout(L, tmp_path):
+    import ctypes
+    import os
+    import shutil
+    import subprocess
+    cc = shutil.which("gcc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src, exe = tmp_path / "g.c", tmp_path / "g"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "moe.h"\nint main(void) {'
+                   'printf("%zu %zu %zu %zu %zu", sizeof(moe_grad_t), offsetof(moe_grad_t, src),'
+                   'offsetof(moe_grad_t, dst), offsetof(moe_grad_t, n), offsetof(moe_grad_t, dtype));'
+                   'return 0; }\n')
+    subprocess.run([cc, "-std=c99", "-Wall", "-Werror", "-I", os.path.join(root, "include"),
+                    str(src), "-o", str(exe)], check=True)
+    got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True).stdout.split()]
+    assert got == [ctypes.sizeof(L.MoeGrad)] + [getattr(L.MoeGrad, f).offset
+                                                for f in ("src", "dst", "n", "dtype")]
