@@ -25,7 +25,8 @@ __all__ = [
     "rms_norm_workspace", "rms_norm_fwd", "rms_norm_bwd", "MoeGrad",
     "moe_grad_clip_workspace_size", "moe_grad_clip", "grad_table", "grad_clip_workspace",
     "grad_clip", "moe_mx_quantize", "moe_mx_dequantize", "mx_alloc", "mx_quantize",
-    "mx_dequantize",
+    "mx_dequantize", "MoeMxWeights", "moe_few_workspace_size", "moe_ffn_few", "few_workspace",
+    "mx_struct", "ffn_few",
 ]
 
 MOE_OK = 0
@@ -68,6 +69,11 @@ class MoeBias(ctypes.Structure):
 class MoeGrad(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64),
                 ("dtype", ctypes.c_int32)]
+
+
+class MoeMxWeights(ctypes.Structure):
+    _fields_ = [("codes_gate_up", ctypes.c_void_p), ("scales_gate_up", ctypes.c_void_p),
+                ("codes_down", ctypes.c_void_p), ("scales_down", ctypes.c_void_p)]
 
 
 class MoeError(RuntimeError):
@@ -140,6 +146,10 @@ def lib():
     L.moe_mx_quantize.restype = ctypes.c_int
     L.moe_mx_dequantize.argtypes = [P, P, I64, I64, I64, I32, P, P]
     L.moe_mx_dequantize.restype = ctypes.c_int
+    L.moe_few_workspace_size.argtypes = [S]
+    L.moe_few_workspace_size.restype = SZ
+    L.moe_ffn_few.argtypes = [S, P, P, P, P, P, P, ctypes.POINTER(MoeMxWeights), B, P, P, SZ, P]
+    L.moe_ffn_few.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -257,6 +267,16 @@ def moe_mx_quantize(w, dtype, E, K, N, codes, scales, stream):
 
 def moe_mx_dequantize(codes, scales, E, K, N, dtype, w, stream):
     return lib().moe_mx_dequantize(codes, scales, E, K, N, dtype, w, stream)
+
+
+def moe_few_workspace_size(shape):
+    return lib().moe_few_workspace_size(ctypes.byref(shape))
+
+
+def moe_ffn_few(shape, x, x_scale, topk_idx, topk_w, w_gate_up, w_down, mx, bias, y, ws, ws_bytes,
+                stream):
+    return lib().moe_ffn_few(ctypes.byref(shape), x, x_scale, topk_idx, topk_w, w_gate_up, w_down,
+                             _byref(mx), _byref(bias), y, ws, ws_bytes, stream)
 
 
 # ---------------------------------------------------------------- torch helpers
@@ -502,6 +522,47 @@ def mx_dequantize(codes, scales, w, stream=None):
         _dense(f, "codes", codes, (E, N, K // 2), torch.uint8),
         _dense(f, "scales", scales, (E, N, K // 32), torch.uint8), E, K, N, _storage_dtype(f, w),
         _dense(f, "w", w, w.shape, w.dtype), _stream(stream)), "moe_mx_dequantize")
+
+
+def few_workspace(shape, device="cuda"):
+    """Zero-filled workspace of ffn_few for this shape (T <= 128)."""
+    import torch
+    n = moe_few_workspace_size(shape)
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_few_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def mx_struct(codes_gate_up, scales_gate_up, codes_down, scales_down):
+    """MoeMxWeights over the tensors mx_quantize filled for w_gate_up and w_down."""
+    import torch
+    ts = (codes_gate_up, scales_gate_up, codes_down, scales_down)
+    for name, t in zip(("codes_gate_up", "scales_gate_up", "codes_down", "scales_down"), ts):
+        _dense("mx_struct", name, t, t.shape, torch.uint8)
+    return MoeMxWeights(*[t.data_ptr() for t in ts])
+
+
+def ffn_few(shape, x, topk_idx, topk_w, w_gate_up, w_down, y, ws, stream=None, bias=None,
+            x_scale=None, mx=None):
+    """y = layer(x) for at most 128 tokens (inference).  x [T,H] in the storage
+    dtype, or e4m3 codes (uint8 or float8_e4m3fn) with x_scale [T,H/32]; the
+    weights as ffn_fwd takes them, or None for both with mx (see mx_struct);
+    bias: see bias_struct; ws: few_workspace(shape)."""
+    import torch
+    f, T, H, I, E, k = "ffn_few", shape.T, shape.H, shape.I, shape.E, shape.k
+    dt = torch.float32 if shape.dtype == MOE_FP32 else torch.bfloat16
+    xdt = dt
+    if x_scale is not None:
+        xdt = torch.float8_e4m3fn if x.dtype is torch.float8_e4m3fn else torch.uint8
+    _check(lib().moe_ffn_few(
+        ctypes.byref(shape), _dense(f, "x", x, (T, H), xdt),
+        _dense(f, "x_scale", x_scale, (T, H // 32), torch.uint8),
+        _dense(f, "topk_idx", topk_idx, (T, k), torch.int32),
+        _dense(f, "topk_w", topk_w, (T, k), torch.float32),
+        _dense(f, "w_gate_up", w_gate_up, (E, H, 2 * I), dt),
+        _dense(f, "w_down", w_down, (E, I, H), dt), _byref(mx), _byref(bias),
+        _dense(f, "y", y, (T, H), torch.float32 if shape.out_fp32 else dt), _ptr(ws), ws.numel(),
+        _stream(stream)), "moe_ffn_few")
 
 
 def check_device_error(ws, stream=None):

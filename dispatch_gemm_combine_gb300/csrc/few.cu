@@ -1,0 +1,873 @@
+// The whole expert layer for a few tokens, in two kernels:
+//
+//   gate_up:  a[s]  = act(x[s / k] Wgu[e_s] (+ b_gate_up))      for every slot s
+//   down:     y[t]  = sum_j w[t,j] (a[t k + j] Wd[e] (+ b_down))
+//
+// With a few rows per expert the layer reads each touched expert's weights once
+// and does next to nothing with them: it is bound by HBM, not by the tensor
+// cores.  So the weights go from global memory straight into registers, as
+// operands of warp-level matrix instructions (weights on the 16-row side, up to
+// 8 tokens per instruction on the other), with no shared-memory ring between,
+// and everything else is arranged to keep loads in flight and every SM busy to
+// the end:
+//
+// Work.  A unit is (expert and up to 8 NT of its rows, tile of weight columns)
+// and takes KS steps along the contraction.  All units' steps, laid end to end,
+// are cut into equal runs, one per block (two blocks per SM), so a single token
+// on four experts spreads as evenly as a batch on all of them.  A unit cut by a
+// run's end is summed from its blocks' parts, in block order, by the block that
+// finishes last: the same bits every time.  The down kernel joins the parts, the
+// k experts and the routing weights of a column tile in one such step.
+//
+// Dispatch.  Every block builds the plan it needs from topk_idx in shared
+// memory (a stable counting sort of at most 4096 slots), so there is no plan
+// kernel and no gather.  The down kernel does this while the gate_up kernel
+// ends (programmatic launch), and waits only before it reads a.
+//
+// Precision.  Products accumulate in fp32.  a is rounded to bf16 between the
+// kernels for bf16 storage, as the layer for many tokens does (it is an operand
+// of the bf16 product); it stays fp32 for fp32 storage, whose products run in
+// fp32 on the CUDA cores.
+#include <algorithm>
+#include <atomic>
+
+#include "abi_internal.h"
+#include "common.cuh"
+#include "mx.cuh"
+#include "vec.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 128;
+constexpr int kMaxSlots = kMaxTokens * 32;   // k <= 32
+constexpr int kMaxE = 1024;
+constexpr int kMaxChunks = kMaxE + kMaxSlots / 8;
+constexpr int kMaxGrid = 512;
+
+struct FewArgs {
+  const void* x;
+  const uint8_t* x_scale;
+  const int* idx;
+  const float* topk_w;
+  const void* w;           // this kernel's weights, or codes
+  const uint8_t* scales;   // the codes' scale bytes
+  const void* bias;        // this kernel's bias, or null
+  void* act;               // [Tk, I]
+  float* part;             // parts of cut units: 2 per block
+  float* o;                // [Tk, H] products of whole units
+  void* y;
+  unsigned* counters;      // this kernel's; 0 between calls
+  int* err;
+  int T, H, I, E, k, act_kind, interleaved, out_fp32;
+  float limit, alpha;
+};
+
+// ------------------------------------------------------------------ plan
+struct Plan {
+  uint32_t off[kMaxE + 1];     // exclusive sums: chunks << 16 | rows
+  uint16_t slot[kMaxSlots];    // slots sorted by expert, by slot within one
+  uint16_t rank[kMaxSlots];    // a slot's row within its expert
+  uint16_t chunk_e[kMaxChunks];
+  uint32_t span[kMaxChunks];   // down kernel: a unit's blocks, see combine
+  uint32_t warp[8];
+  int chunks;
+  int last;
+};
+
+// A chunk is up to `rows` rows of one expert.  All blocks build the same plan.
+__device__ void build_plan(Plan& p, const int* __restrict__ idx, int Tk, int E, int rows, int* err) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (int e = tid; e <= E; e += kThreads) p.off[e] = 0;
+  __syncthreads();
+  if (tid < 32) {
+    for (int s0 = 0; s0 < Tk; s0 += 32) {
+      const int s = s0 + lane;
+      int e = s < Tk ? __ldg(idx + s) : -1;
+      if (s < Tk && (e < 0 || e >= E)) {
+        record_error(err, kErrBadIndex);
+        e = -1;
+      }
+      const unsigned same = __match_any_sync(0xffffffffu, e);
+      const int before = __popc(same & ((1u << lane) - 1u));
+      uint32_t base = 0;
+      if (e >= 0) base = p.off[e];
+      __syncwarp();
+      if (e >= 0) {
+        p.rank[s] = static_cast<uint16_t>(base + before);
+        if (before == 0) p.off[e] = base + __popc(same);
+      }
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  // exclusive scan over the experts, four per thread
+  uint32_t v[4], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = tid * 4 + i;
+    const uint32_t c = e < E ? p.off[e] : 0;
+    v[i] = sum;
+    sum += c | (((c + rows - 1) / rows) << 16);
+  }
+  uint32_t inc = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) p.warp[tid >> 5] = inc;
+  __syncthreads();
+  uint32_t base = inc - sum;
+  for (int w = 0; w < (tid >> 5); ++w) base += p.warp[w];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = tid * 4 + i;
+    if (e < E) {
+      const uint32_t b = base + v[i];
+      const uint32_t end = base + (i < 3 ? v[i + 1] : sum);
+      p.off[e] = b;
+      for (uint32_t c = b >> 16; c < (end >> 16); ++c) p.chunk_e[c] = static_cast<uint16_t>(e);
+      if (e == E - 1) {
+        p.off[E] = end;
+        p.chunks = static_cast<int>(end >> 16);
+      }
+    }
+  }
+  __syncthreads();
+  for (int s = tid; s < Tk; s += kThreads) {
+    const int e = __ldg(idx + s);
+    if (e >= 0 && e < E) p.slot[(p.off[e] & 0xffffu) + p.rank[s]] = static_cast<uint16_t>(s);
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------------ products
+// Each kind of weight: FG column groups of WF columns by KG shares of the
+// contraction make the block's eight warps; a step takes STEP values of the
+// contraction per warp.  Lane (g, t) = (lane / 4, lane % 4) holds weight columns
+// of row group g and every fourth part of the contraction, in whatever order
+// suits the loads: the token side uses the same order.
+
+__device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Weights: read once, never written by the layer.
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// Token rows and activations.  The down kernel reads what the gate_up kernel
+// wrote while it was already running, so these are plain loads in program order,
+// after its wait.
+__device__ __forceinline__ uint32_t ld_u32(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 ld_u64(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 ld_u128(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// Two e4m3 codes times a power-of-two scale as bf16 (exact but for results below
+// bf16's normal range).
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two, float scale) {
+  const __half2_raw h =
+      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xffffu), __NV_E4M3);
+  const float2 f = __half22float2(__half2(h));
+  return pack_bf16(f.x * scale, f.y * scale);
+}
+
+// A token row (or a slot's activations) as the product reads it.
+template <bool X8>
+struct Row {
+  const void* p = nullptr;             // null: no such row, zeros
+  const uint8_t* scale = nullptr;
+  __device__ __forceinline__ uint2 bf16x4(int k) const {
+    if (!p) return make_uint2(0, 0);
+    if (!X8) return ld_u64(static_cast<const __nv_bfloat16*>(p) + k);
+    const uint32_t c = ld_u32(static_cast<const uint8_t*>(p) + k);
+    const float s = mx_scale(__ldg(scale + (k >> 5)));
+    return make_uint2(e4m3_pair(c, s), e4m3_pair(c >> 16, s));
+  }
+  __device__ __forceinline__ uint4 bf16x8(int k) const {
+    if (!p) return make_uint4(0, 0, 0, 0);
+    if (!X8) return ld_u128(static_cast<const __nv_bfloat16*>(p) + k);
+    const uint2 c = ld_u64(static_cast<const uint8_t*>(p) + k);
+    const float s = mx_scale(__ldg(scale + (k >> 5)));
+    return make_uint4(e4m3_pair(c.x, s), e4m3_pair(c.x >> 16, s), e4m3_pair(c.y, s),
+                      e4m3_pair(c.y >> 16, s));
+  }
+  __device__ __forceinline__ float4 f32x4(int k) const {
+    if (!X8) {
+      const uint4 v = ld_u128(static_cast<const float*>(p) + k);
+      return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                         __uint_as_float(v.w));
+    }
+    const uint32_t c = ld_u32(static_cast<const uint8_t*>(p) + k);
+    const float s = mx_scale(__ldg(scale + (k >> 5)));
+    const float2 lo = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>(c & 0xffffu), __NV_E4M3)));
+    const float2 hi = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>(c >> 16), __NV_E4M3)));
+    return make_float4(lo.x * s, lo.y * s, hi.x * s, hi.y * s);
+  }
+};
+
+// bf16 weights [K, ld], columns innermost.  A lane loads 16 bytes (8 columns) of
+// four rows of the contraction; pairs along the contraction, as the instruction
+// wants them, come from two rows by byte permutes.  Columns 2 i and 2 i + 1 of
+// the lane are rows g and g + 8 of instruction i.
+struct Bf16 {
+  using Store = __nv_bfloat16;
+  static constexpr int WF = 64, FG = 2, KG = 4, STEP = 16;
+  static constexpr bool kRowPerLane = true;   // lane (g, t) reads rows g, g + 8, ...
+  template <int NT, bool X8>
+  static __device__ __forceinline__ void run(const void* w, const uint8_t*, int64_t ld, int col,
+                                             int ncol, int K, int s0, int s1, int kg,
+                                             const Row<X8>* rows, int nt_act, float* red) {
+    constexpr int U = NT == 1 ? 4 : 2;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float acc[4][NT][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][n][q] = 0.f;
+    const bool col_ok = 8 * g < ncol;
+    const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(w) + col + 8 * g;
+    for (int s = s0; s < s1; s += U) {
+      uint4 v[U][4];
+      uint2 xb[U][NT];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = ((s + u) * KG + kg) * STEP + 4 * t;
+        const bool ok = s + u < s1 && k < K;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          v[u][r] = ok && col_ok ? ldg_stream(base + (k + r) * ld) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          xb[u][n] = ok && n < nt_act ? rows[n].bf16x4(k) : make_uint2(0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t* w0 = &v[u][0].x;
+        const uint32_t* w1 = &v[u][1].x;
+        const uint32_t* w2 = &v[u][2].x;
+        const uint32_t* w3 = &v[u][3].x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a0 = __byte_perm(w0[i], w1[i], 0x5410), a1 = __byte_perm(w0[i], w1[i], 0x7632);
+          const uint32_t a2 = __byte_perm(w2[i], w3[i], 0x5410), a3 = __byte_perm(w2[i], w3[i], 0x7632);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            if (n < nt_act) mma16816(acc[i][n], a0, a1, a2, a3, xb[u][n].x, xb[u][n].y);
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (n < nt_act) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float* d = red + n * (WF * 8) + i * 128 + g * 8 + 2 * t;
+          *reinterpret_cast<float2*>(d) = make_float2(acc[i][n][0], acc[i][n][1]);
+          *reinterpret_cast<float2*>(d + 64) = make_float2(acc[i][n][2], acc[i][n][3]);
+        }
+      }
+  }
+  // where column f (of the group), token n of a row tile lies in `red`
+  static __device__ __forceinline__ int at(int f, int n) { return (f & 7) * 64 + (f >> 3) * 8 + n; }
+};
+
+// fp32 weights [K, ld]: the same loads (4 columns per lane), products on the
+// CUDA cores in fp32; the four lanes of a group hold shares of the contraction.
+struct F32 {
+  using Store = float;
+  static constexpr int WF = 32, FG = 2, KG = 4, STEP = 16;
+  static constexpr bool kRowPerLane = false;   // every lane reads all rows
+  template <int NT, bool X8>
+  static __device__ __forceinline__ void run(const void* w, const uint8_t*, int64_t ld, int col,
+                                             int ncol, int K, int s0, int s1, int kg,
+                                             const Row<X8>* rows, int nrows, float* red) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const bool col_ok = 4 * g < ncol;
+    float acc[8][4];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[n][c] = 0.f;
+    const float* base = static_cast<const float*>(w) + col + 4 * g;
+    for (int s = s0; s < s1; ++s) {
+      const int k = (s * KG + kg) * STEP + 4 * t;
+      const bool ok = k < K;
+      float v[4][4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint4 q = ok && col_ok ? ldg_stream(base + (k + r) * ld) : make_uint4(0, 0, 0, 0);
+        v[r][0] = __uint_as_float(q.x), v[r][1] = __uint_as_float(q.y);
+        v[r][2] = __uint_as_float(q.z), v[r][3] = __uint_as_float(q.w);
+      }
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+        if (n < nrows && ok) {
+          const float4 x = rows[n].f32x4(k);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            acc[n][c] = fmaf(x.w, v[3][c], fmaf(x.z, v[2][c], fmaf(x.y, v[1][c], fmaf(x.x, v[0][c], acc[n][c]))));
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        acc[n][c] += __shfl_xor_sync(0xffffffffu, acc[n][c], 1);
+        acc[n][c] += __shfl_xor_sync(0xffffffffu, acc[n][c], 2);
+        if ((n >> 1) == t) red[(4 * g + c) * 8 + n] = acc[n][c];
+      }
+  }
+  static __device__ __forceinline__ int at(int f, int n) { return f * 8 + n; }
+};
+
+// Microscaled e2m1 weights: codes [N, K/2] and scale bytes [N, K/32], the
+// contraction innermost.  A lane loads whole blocks of 32 (16 bytes) of columns
+// g, g + 8, g + 16 and g + 24, so each load has one scale.  Two codes four apart
+// in a word lie 16 bits apart: their sign and magnitude bits are moved to bit 15
+// and bits 8..6 of both halves at once, which reads as the value times 2^-126 in
+// bf16 (0.5 is a subnormal there), and one exact bf16 product by 2^(126 + q)
+// gives the weight.  Scales above 2 would need a larger factor than bf16 has
+// and take a second product.
+struct Mx {
+  using Store = __nv_bfloat16;
+  static constexpr int WF = 32, FG = 4, KG = 2, STEP = 128;
+  static constexpr bool kRowPerLane = true;
+  static __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  // Codes j and j + 4 of a word as bf16 values times 2^-126.
+  template <int J>
+  static __device__ __forceinline__ uint32_t spread(uint32_t w) {
+    const uint32_t sign = J == 3 ? w : w << (12 - 4 * J);
+    const uint32_t mag = J < 2 ? w << (6 - 4 * J) : w >> (4 * J - 6);
+    return (sign & 0x80008000u) | (mag & 0x01c001c0u);
+  }
+  template <int NT, bool X8>
+  static __device__ __forceinline__ void run(const void* w, const uint8_t* scales, int64_t, int col,
+                                             int ncol, int K, int s0, int s1, int kg,
+                                             const Row<X8>* rows, int nt_act, float* red) {
+    constexpr int U = NT == 1 ? 2 : 1;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int nb = K >> 5;
+    const int64_t cld = K >> 1;
+    float acc[2][NT][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[m][n][q] = 0.f;
+    const uint8_t* cp = static_cast<const uint8_t*>(w) + (static_cast<int64_t>(col) + g) * cld;
+    const uint8_t* sp = scales + (static_cast<int64_t>(col) + g) * nb;
+    for (int s = s0; s < s1; s += U) {
+      uint4 v[U][4];
+      uint32_t f[U][4];
+      bool large = false;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int b = ((s + u) * KG + kg) * 4 + t;
+        const bool ok = s + u < s1 && b < nb;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool in = ok && 8 * r < ncol;
+          v[u][r] = in ? ldg_stream(cp + 8 * r * cld + 16 * b) : make_uint4(0, 0, 0, 0);
+          f[u][r] = in ? __ldg(sp + static_cast<int64_t>(8 * r) * nb + b) : 0u;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) large = large || f[u][r] > 128u;
+      if (__any_sync(0xffffffffu, large))
+        step<NT, X8, U, true>(v, f, s, s1, kg, t, nb, rows, nt_act, acc);
+      else
+        step<NT, X8, U, false>(v, f, s, s1, kg, t, nb, rows, nt_act, acc);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (n < nt_act) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          float* d = red + n * (WF * 8) + m * 128 + g * 8 + 2 * t;
+          *reinterpret_cast<float2*>(d) = make_float2(acc[m][n][0], acc[m][n][1]);
+          *reinterpret_cast<float2*>(d + 64) = make_float2(acc[m][n][2], acc[m][n][3]);
+        }
+      }
+  }
+  template <int NT, bool X8, int U, bool LARGE>
+  static __device__ __forceinline__ void step(const uint4 (&v)[U][4], const uint32_t (&f)[U][4],
+                                              int s, int s1, int kg, int t, int nb,
+                                              const Row<X8>* rows, int nt_act,
+                                              float (&acc)[2][NT][4]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = ((s + u) * KG + kg) * 4 + t;
+      const bool ok = s + u < s1 && b < nb;
+      uint32_t f1[4], f2[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t sb = f[u][r];
+        f1[r] = ((LARGE ? min(sb, 128u) : sb) + 126u) * 0x00800080u;
+        if (LARGE)
+          f2[r] = sb == 255u ? 0x7fc07fc0u : (sb > 128u ? (sb - 1u) * 0x00800080u : 0x3f803f80u);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t xb[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint4 x = ok && n < nt_act ? rows[n].bf16x8(32 * b + 8 * q) : make_uint4(0, 0, 0, 0);
+          xb[n][0] = __byte_perm(x.x, x.z, 0x5410);   // values 0 and 4
+          xb[n][1] = __byte_perm(x.x, x.z, 0x7632);   // 1 and 5
+          xb[n][2] = __byte_perm(x.y, x.w, 0x5410);   // 2 and 6
+          xb[n][3] = __byte_perm(x.y, x.w, 0x7632);   // 3 and 7
+        }
+        uint32_t a[4][4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t wd = q == 0 ? v[u][r].x : (q == 1 ? v[u][r].y : (q == 2 ? v[u][r].z : v[u][r].w));
+          a[r][0] = mul2(spread<0>(wd), f1[r]);
+          a[r][1] = mul2(spread<1>(wd), f1[r]);
+          a[r][2] = mul2(spread<2>(wd), f1[r]);
+          a[r][3] = mul2(spread<3>(wd), f1[r]);
+          if (LARGE) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[r][j] = mul2(a[r][j], f2[r]);
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            if (n < nt_act) {
+              mma16816(acc[m][n], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], xb[n][0], xb[n][1]);
+              mma16816(acc[m][n], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], xb[n][2], xb[n][3]);
+            }
+      }
+    }
+  }
+  static __device__ __forceinline__ int at(int f, int n) { return (f >> 3) * 64 + (f & 7) * 8 + n; }
+};
+
+// ------------------------------------------------------------------ kernels
+__device__ __forceinline__ float load_elem(const __nv_bfloat16* p, int64_t i) { return __bfloat162float(p[i]); }
+__device__ __forceinline__ float load_elem(const float* p, int64_t i) { return p[i]; }
+
+__device__ __forceinline__ float sigmoid_exact(float v) { return 1.f / (1.f + expf(-v)); }
+
+// A NaN stays a NaN through the clamps.
+__device__ __forceinline__ float activate(const FewArgs& a, float gate, float up) {
+  if (a.act_kind == MOE_ACT_SWIGLU) return gate * sigmoid_exact(gate) * up;
+  const float gc = gate > a.limit ? a.limit : gate;
+  const float uc = up > a.limit ? a.limit : (up < -a.limit ? -a.limit : up);
+  return (uc + 1.f) * gc * sigmoid_exact(a.alpha * gc);
+}
+
+// First step of block c's run, and the block whose run holds step s.
+__device__ __forceinline__ int64_t run_begin(int64_t steps, int c, int grid) { return steps * c / grid; }
+__device__ __forceinline__ int block_of_step(int64_t steps, int64_t s, int grid) {
+  return static_cast<int>(((s + 1) * grid - 1) / steps);
+}
+
+// PHASE 0: gate_up and activation; 1: down and combine.
+template <class W, int PHASE, int NT, bool X8>
+__global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant__ FewArgs a) {
+  using S = typename W::Store;
+  constexpr int ROWS = 8 * NT;
+  constexpr int GROUP = W::WF * ROWS;          // results of one column group
+  constexpr int UNIT = W::FG * GROUP;
+  constexpr int CW = W::FG * W::WF;            // weight columns of a unit
+  constexpr int OUT = PHASE == 0 ? CW / 2 : CW;
+  extern __shared__ float4 red4[];
+  float* red = reinterpret_cast<float*>(red4);
+  __shared__ Plan p;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int fg = warp % W::FG, kg = warp / W::FG;
+  const int me = blockIdx.x;
+  if (PHASE == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  const int Tk = a.T * a.k;
+  build_plan(p, a.idx, Tk, a.E, ROWS, PHASE == 0 ? a.err : nullptr);
+
+  const int K = PHASE == 0 ? a.H : a.I;                // contraction
+  const int N = PHASE == 0 ? 2 * a.I : a.H;            // weight columns
+  const int n_out = PHASE == 0 ? a.I : a.H;
+  const int tiles = (n_out + OUT - 1) / OUT;
+  const int KS = (K + W::KG * W::STEP - 1) / (W::KG * W::STEP);
+  const int64_t steps = static_cast<int64_t>(p.chunks) * tiles * KS;
+  // no more runs than steps: a unit's blocks are consecutive and each has a share
+  const int grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), steps));
+  const int64_t end = me < grid ? run_begin(steps, me + 1, grid) : 0;
+  if (PHASE == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  for (int64_t s = me < grid ? run_begin(steps, me, grid) : 0; s < end;) {
+    const int64_t unit = s / KS;
+    const int64_t u0 = unit * KS;
+    const int ks0 = static_cast<int>(s - u0);
+    const int ks1 = static_cast<int>(min(static_cast<int64_t>(KS), end - u0));
+    const int chunk = static_cast<int>(unit / tiles), tile = static_cast<int>(unit % tiles);
+    const int e = p.chunk_e[chunk];
+    const int first = static_cast<int>(p.off[e] & 0xffffu) + (chunk - static_cast<int>(p.off[e] >> 16)) * ROWS;
+    const int nrows = min(ROWS, static_cast<int>(p.off[e + 1] & 0xffffu) - first);
+    const int nt_act = (nrows + 7) >> 3;
+
+    // this warp's columns
+    int col, ncol;
+    if (PHASE == 0 && !a.interleaved) {
+      constexpr int HALF = W::FG / 2;
+      const int o = tile * OUT + (fg % HALF) * W::WF;
+      col = (fg / HALF) * a.I + o;
+      ncol = a.I - o;
+    } else {
+      col = tile * CW + fg * W::WF;
+      ncol = N - col;
+    }
+    Row<X8> rows[W::kRowPerLane ? NT : 8];
+#pragma unroll
+    for (int i = 0; i < (W::kRowPerLane ? NT : 8); ++i) {
+      const int r = W::kRowPerLane ? 8 * i + (lane >> 2) : i;
+      if (r < nrows) {
+        const int slot = p.slot[first + r];
+        const int64_t row = PHASE == 0 ? slot / a.k : slot;
+        if (X8) {
+          rows[i].p = static_cast<const uint8_t*>(a.x) + row * K;
+          rows[i].scale = a.x_scale + row * (K >> 5);
+        } else {
+          rows[i].p = static_cast<const S*>(a.x) + row * K;
+        }
+      }
+    }
+    if (ncol > 0) {
+      const int64_t we = static_cast<int64_t>(e) * K * N;   // weights of the experts before
+      const void* w = sizeof(S) == 4 ? static_cast<const void*>(static_cast<const float*>(a.w) + we)
+                      : W::STEP == 128
+                          ? static_cast<const void*>(static_cast<const uint8_t*>(a.w) + we / 2)
+                          : static_cast<const void*>(static_cast<const __nv_bfloat16*>(a.w) + we);
+      W::template run<NT, X8>(w, W::STEP == 128 ? a.scales + we / 32 : nullptr, N, col, ncol, K, ks0,
+                              ks1, kg, rows, W::kRowPerLane ? nt_act : nrows,
+                              red + kg * UNIT + fg * GROUP);
+    }
+    __syncthreads();
+
+    // add the shares of the contraction; a cut unit's sum goes to its part
+    const bool whole = ks1 - ks0 == KS;
+    const int c0 = whole ? me : block_of_step(steps, u0, grid);
+    const bool at_begin = run_begin(steps, me, grid) >= u0;
+    float* part = a.part + (2 * static_cast<int64_t>(me) + (at_begin ? 0 : 1)) * UNIT;
+    const int per = nt_act * W::WF * 8;   // results in use, per column group
+    for (int i = tid * 4; i < W::FG * per; i += kThreads * 4) {
+      const int q = (i / per) * GROUP + i % per;
+      float4 v = *reinterpret_cast<const float4*>(red + q);
+#pragma unroll
+      for (int j = 1; j < W::KG; ++j) {
+        const float4 o = *reinterpret_cast<const float4*>(red + j * UNIT + q);
+        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+      }
+      if (whole)
+        *reinterpret_cast<float4*>(red + q) = v;
+      else
+        *reinterpret_cast<float4*>(part + q) = v;
+    }
+
+    if (PHASE == 0) {
+      bool mine = true;
+      if (!whole) {
+        const int c1 = block_of_step(steps, u0 + KS - 1, grid);
+        __syncthreads();
+        if (tid == 0) {
+          __threadfence();
+          p.last = atomicAdd(a.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
+          if (p.last) a.counters[c0] = 0;
+          __threadfence();
+        }
+        __syncthreads();
+        mine = p.last != 0;
+        if (mine) {
+          const int cut = run_begin(steps, c0, grid) >= u0 ? 0 : 1;
+          for (int i = tid * 4; i < W::FG * per; i += kThreads * 4) {
+            const int q = (i / per) * GROUP + i % per;
+            float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + (2 * static_cast<int64_t>(c0) + cut) * UNIT + q));
+            for (int c = c0 + 1; c <= c1; ++c) {
+              const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part + 2 * static_cast<int64_t>(c) * UNIT + q));
+              v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+            }
+            *reinterpret_cast<float4*>(red + q) = v;
+          }
+        }
+      }
+      __syncthreads();
+      if (mine) {
+        for (int i = tid; i < OUT * nrows; i += kThreads) {
+          const int f = i % OUT, r = i / OUT;
+          const int feature = tile * OUT + f;
+          if (feature >= a.I) continue;
+          const int cg = a.interleaved ? 2 * f : f, cu = a.interleaved ? 2 * f + 1 : f + OUT;
+          const float* q = red + (r >> 3) * (W::WF * 8);
+          float gate = q[(cg / W::WF) * GROUP + W::at(cg % W::WF, r & 7)];
+          float up = q[(cu / W::WF) * GROUP + W::at(cu % W::WF, r & 7)];
+          if (a.bias) {
+            const S* b = static_cast<const S*>(a.bias) + static_cast<int64_t>(e) * N;
+            gate += load_elem(b, a.interleaved ? 2 * feature : feature);
+            up += load_elem(b, a.interleaved ? 2 * feature + 1 : a.I + feature);
+          }
+          static_cast<S*>(a.act)[static_cast<int64_t>(p.slot[first + r]) * a.I + feature] =
+              static_cast<S>(activate(a, gate, up));
+        }
+      }
+    } else {
+      if (whole) {
+        __syncthreads();
+        for (int i = tid; i < OUT * nrows; i += kThreads) {
+          const int f = i % OUT, r = i / OUT;
+          if (tile * OUT + f < a.H)
+            a.o[static_cast<int64_t>(p.slot[first + r]) * a.H + tile * OUT + f] =
+                red[(r >> 3) * (W::WF * 8) + (f / W::WF) * GROUP + W::at(f % W::WF, r & 7)];
+        }
+      }
+      __syncthreads();
+      if (tid == 0) {
+        __threadfence();
+        const unsigned all = static_cast<unsigned>(p.chunks) * KS, mine = ks1 - ks0;
+        p.last = atomicAdd(a.counters + tile, mine) + mine == all;
+        if (p.last) a.counters[tile] = 0;
+        __threadfence();
+      }
+      __syncthreads();
+      if (p.last) {
+        // every product of this column tile is there: the blocks of each chunk's
+        // unit (first | last << 15 | whether the first one's part is its second)
+        for (int c = tid; c < p.chunks; c += kThreads) {
+          const int64_t b0 = (static_cast<int64_t>(c) * tiles + tile) * KS;
+          const int f0 = block_of_step(steps, b0, grid), f1 = block_of_step(steps, b0 + KS - 1, grid);
+          p.span[c] = f0 | (f1 << 15) | (run_begin(steps, f0, grid) < b0 ? 1u << 30 : 0u);
+        }
+        __syncthreads();
+        for (int i = tid; i < a.T * OUT; i += kThreads) {
+          const int f = i % OUT, tok = i / OUT;
+          const int c = tile * OUT + f;
+          if (c >= a.H) continue;
+          float y = 0.f;
+          for (int j = 0; j < a.k; ++j) {
+            const int slot = tok * a.k + j;
+            const int se = __ldg(a.idx + slot);
+            if (se < 0 || se >= a.E) continue;
+            const int rank = p.rank[slot];
+            const uint32_t sp = p.span[(p.off[se] >> 16) + rank / ROWS];
+            const int f0 = sp & 0x7fff, f1 = (sp >> 15) & 0x7fff;
+            float v;
+            if (f0 == f1) {
+              v = __ldcg(a.o + static_cast<int64_t>(slot) * a.H + c);
+            } else {
+              const int r = rank % ROWS;
+              const int q = (r >> 3) * (W::WF * 8) + (f / W::WF) * GROUP + W::at(f % W::WF, r & 7);
+              v = __ldcg(a.part + (2 * static_cast<int64_t>(f0) + (sp >> 30)) * UNIT + q);
+              for (int b = f0 + 1; b <= f1; ++b) v += __ldcg(a.part + 2 * static_cast<int64_t>(b) * UNIT + q);
+            }
+            if (a.bias) v += load_elem(static_cast<const S*>(a.bias), static_cast<int64_t>(se) * a.H + c);
+            y = fmaf(__ldg(a.topk_w + slot), v, y);
+          }
+          const int64_t at = static_cast<int64_t>(tok) * a.H + c;
+          if (a.out_fp32)
+            static_cast<float*>(a.y)[at] = y;
+          else
+            static_cast<S*>(a.y)[at] = static_cast<S>(y);
+        }
+      }
+    }
+    __syncthreads();
+    s = u0 + ks1;
+  }
+  // no row at all (every id out of range): y is still written
+  if (PHASE == 1 && steps == 0) {
+    for (int64_t i = me * static_cast<int64_t>(kThreads) + tid; i < static_cast<int64_t>(a.T) * a.H;
+         i += static_cast<int64_t>(gridDim.x) * kThreads) {
+      if (a.out_fp32)
+        static_cast<float*>(a.y)[i] = 0.f;
+      else
+        static_cast<S*>(a.y)[i] = static_cast<S>(0.f);
+    }
+  }
+}
+
+template <class W, int PHASE, int NT, bool X8>
+cudaError_t launch(const FewArgs& a, int grid, cudaStream_t st) {
+  constexpr int smem = W::KG * W::FG * W::WF * 8 * NT * 4;
+  static std::atomic<uint64_t> ready{0};   // one bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(few_kernel<W, PHASE, NT, X8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = PHASE == 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, few_kernel<W, PHASE, NT, X8>, a);
+}
+
+template <class W, int PHASE, bool X8>
+cudaError_t launch_nt(const FewArgs& a, int nt, int grid, cudaStream_t st) {
+  if constexpr (W::kRowPerLane) {
+    if (nt > 1) return launch<W, PHASE, 4, X8>(a, grid, st);
+  }
+  return launch<W, PHASE, 1, X8>(a, grid, st);
+}
+
+// Row tiles of 8 tokens per unit: one holds every row of an expert that a token
+// names once when T <= 8; beyond that four, of which a unit runs only those that
+// its rows fill.
+int row_tiles(const moe_shape* s) { return s->dtype == MOE_FP32 || s->T <= 8 ? 1 : 4; }
+
+struct FewLayout {
+  size_t counters0, counters1, act, part, o, total;
+};
+FewLayout few_layout(const moe_shape* s) {
+  FewLayout L;
+  size_t off = 256;   // the error word
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = abi_align256(off + bytes);
+    return at;
+  };
+  const size_t Tk = static_cast<size_t>(s->T) * s->k;
+  L.counters0 = take(sizeof(unsigned) * kMaxGrid);
+  L.counters1 = take(sizeof(unsigned) * ((s->H + 63) / 64));
+  L.act = take((s->dtype == MOE_FP32 ? 4 : 2) * Tk * s->I);
+  L.part = take(sizeof(float) * 2 * kMaxGrid * 128 * 8 * row_tiles(s));
+  L.o = take(sizeof(float) * Tk * s->H);
+  L.total = off;
+  return L;
+}
+
+bool few_shape_ok(const moe_shape* s) { return abi_shape_ok(s) && s->T <= kMaxTokens; }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_few_workspace_size(const moe_shape* shape) {
+  return few_shape_ok(shape) ? few_layout(shape).total : 0;
+}
+
+moe_status moe_ffn_few(const moe_shape* s, const void* x, const uint8_t* x_scale,
+                       const int32_t* topk_idx, const float* topk_w, const void* w_gate_up,
+                       const void* w_down, const moe_mx_weights_t* mx, const moe_bias_t* bias,
+                       void* y, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  if (!abi_shape_ok(s) || !ws || (reinterpret_cast<uintptr_t>(ws) & 255)) return MOE_ERR_INVALID_ARG;
+  if (mx ? (w_gate_up || w_down) : (!w_gate_up || !w_down)) return MOE_ERR_INVALID_ARG;
+  if (mx) {
+    if (!mx->codes_gate_up || !mx->scales_gate_up || !mx->codes_down || !mx->scales_down ||
+        !abi_aligned16(mx->codes_gate_up) || !abi_aligned16(mx->codes_down) || s->H % 32 || s->I % 32)
+      return MOE_ERR_INVALID_ARG;
+    if (s->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  }
+  if (x_scale && s->H % 32) return MOE_ERR_INVALID_ARG;
+  if (s->T == 0) return MOE_OK;
+  if (!x || !topk_idx || !topk_w || !y) return MOE_ERR_INVALID_ARG;
+  for (const void* q : {x, w_gate_up, w_down, static_cast<const void*>(y)})
+    if (!abi_aligned16(q)) return MOE_ERR_INVALID_ARG;
+  if (bias && (!abi_aligned16(bias->b_gate_up) || !abi_aligned16(bias->b_down)))
+    return MOE_ERR_INVALID_ARG;
+  if (s->T > kMaxTokens) return MOE_ERR_UNSUPPORTED;
+  const FewLayout L = few_layout(s);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  int sms = 0;
+  const moe_status ds = abi_device_sms(&sms);
+  if (ds != MOE_OK) return ds;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int grid = std::min(kMaxGrid, 2 * sms);
+  char* base = static_cast<char*>(ws);
+
+  FewArgs a = {};
+  a.x = x;
+  a.x_scale = x_scale;
+  a.idx = topk_idx;
+  a.topk_w = topk_w;
+  a.w = mx ? mx->codes_gate_up : w_gate_up;
+  a.scales = mx ? mx->scales_gate_up : nullptr;
+  a.bias = bias ? bias->b_gate_up : nullptr;
+  a.act = base + L.act;
+  a.part = reinterpret_cast<float*>(base + L.part);
+  a.o = reinterpret_cast<float*>(base + L.o);
+  a.y = y;
+  a.counters = reinterpret_cast<unsigned*>(base + L.counters0);
+  a.err = reinterpret_cast<int*>(base);
+  a.T = static_cast<int>(s->T);
+  a.H = s->H, a.I = s->I, a.E = s->E, a.k = s->k;
+  a.act_kind = s->act;
+  a.interleaved = s->gate_up_layout == MOE_GATE_UP_INTERLEAVED;
+  a.out_fp32 = s->out_fp32;
+  a.limit = s->clamp_limit;
+  a.alpha = s->alpha;
+  const int nt = row_tiles(s);
+
+  cudaError_t e = abi_tracked(kAbiFewGateUp, 1, st, [&] {
+    if (s->dtype == MOE_FP32)
+      return x_scale ? launch_nt<F32, 0, true>(a, nt, grid, st) : launch_nt<F32, 0, false>(a, nt, grid, st);
+    if (mx)
+      return x_scale ? launch_nt<Mx, 0, true>(a, nt, grid, st) : launch_nt<Mx, 0, false>(a, nt, grid, st);
+    return x_scale ? launch_nt<Bf16, 0, true>(a, nt, grid, st) : launch_nt<Bf16, 0, false>(a, nt, grid, st);
+  });
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  a.x = a.act;
+  a.x_scale = nullptr;
+  a.w = mx ? mx->codes_down : w_down;
+  a.scales = mx ? mx->scales_down : nullptr;
+  a.bias = bias ? bias->b_down : nullptr;
+  a.counters = reinterpret_cast<unsigned*>(base + L.counters1);
+  e = abi_tracked(kAbiFewDown, 1, st, [&] {
+    if (s->dtype == MOE_FP32) return launch_nt<F32, 1, false>(a, nt, grid, st);
+    if (mx) return launch_nt<Mx, 1, false>(a, nt, grid, st);
+    return launch_nt<Bf16, 1, false>(a, nt, grid, st);
+  });
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -9,7 +9,8 @@ library's kernels.
 import torch
 
 from . import (MOE_BF16, MOE_FP32, Shape, alloc_plan, bias_struct, check_device_error, ffn_bwd,
-               ffn_fwd, moe_saved_size, plan, route, workspace)
+               ffn_few, ffn_fwd, few_workspace, moe_saved_size, mx_alloc, mx_quantize, mx_struct,
+               plan, route, workspace)
 
 _TORCH_DTYPE = {MOE_BF16: torch.bfloat16, MOE_FP32: torch.float32}
 
@@ -55,6 +56,32 @@ class LayerRunner:
                 bias_struct(b_gate_up, b_down))
         return self.y
 
+    def quantize(self, w_gate_up, w_down, stream=None):
+        """Keep both weights in microscaled 4-bit for few(): (codes, scales) of
+        w_gate_up and of w_down.  Call it again when the weights change."""
+        E, H, I = self.shape.E, self.shape.H, self.shape.I
+        self.mx_t = mx_alloc(E, H, 2 * I, self.device) + mx_alloc(E, I, H, self.device)
+        mx_quantize(w_gate_up, *self.mx_t[:2], stream=stream)
+        mx_quantize(w_down, *self.mx_t[2:], stream=stream)
+        self.mx_s = mx_struct(*self.mx_t)
+        return self.mx_t
+
+    def few(self, x, topk_idx, topk_w, w_gate_up=None, w_down=None, x_scale=None, stream=None,
+            b_gate_up=None, b_down=None):
+        """y = layer(x) for at most 128 tokens, without a plan or a saved context.
+        Without weights, on the 4-bit ones that quantize() keeps.  x may be e4m3
+        codes with x_scale, as rms_norm_fwd gives them."""
+        if getattr(self, "ws_few", None) is None:
+            self.ws_few = few_workspace(self.shape, self.device)
+        mx = None
+        if w_gate_up is None and w_down is None:
+            mx = getattr(self, "mx_s", None)
+            if mx is None:
+                raise ValueError("few: no weights given, and quantize() has not been called")
+        ffn_few(self.shape, x, topk_idx, topk_w, w_gate_up, w_down, self.y, self.ws_few, stream,
+                bias_struct(b_gate_up, b_down), x_scale, mx)
+        return self.y
+
     def backward(self, dy, x, topk_idx, topk_w, w_gate_up, w_down, stream=None, recompute=False,
                  b_gate_up=None, b_down=None):
         """Gradients of <dy, y>: (dx, d_topk_w, dw_gate_up, dw_down), and with
@@ -81,6 +108,7 @@ class LayerRunner:
         return out + (self.db_gate_up, self.db_down) if with_bias else out
 
     def check(self, stream=None):
-        for ws in (self.ws_plan, self.ws_fwd, self.ws_bwd, getattr(self, "ws_bwd_recompute", None)):
+        for ws in (self.ws_plan, self.ws_fwd, self.ws_bwd, getattr(self, "ws_bwd_recompute", None),
+                   getattr(self, "ws_few", None)):
             if ws is not None:
                 check_device_error(ws, stream)

@@ -389,6 +389,39 @@ moe_status moe_mx_quantize(const void* w, int32_t dtype, int64_t E, int64_t K, i
 moe_status moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t E, int64_t K,
                              int64_t N, int32_t dtype, void* w, moe_stream_t stream);
 
+/* Both projections' weights in microscaled 4-bit, as moe_mx_quantize makes them
+ * from w_gate_up (columns in the shape's gate_up_layout) and w_down. */
+typedef struct {
+  const uint8_t* codes_gate_up;    /* [E,2I,H/2] */
+  const uint8_t* scales_gate_up;   /* [E,2I,H/32] */
+  const uint8_t* codes_down;       /* [E,H,I/2] */
+  const uint8_t* scales_down;      /* [E,H,I/32] */
+} moe_mx_weights_t;
+
+/* Bytes of workspace of moe_ffn_few (0 for an invalid shape or T > 128). */
+size_t moe_few_workspace_size(const moe_shape* shape);
+
+/* The forward pass of the layer for a few tokens (inference), in two kernels
+ * that read each touched expert's weights once: the y of moe_ffn_fwd, without
+ * its plan, gather and grouped rows.
+ *   T <= 128 (more: MOE_ERR_UNSUPPORTED); moe_ffn_fwd is the faster one where
+ *     experts get dozens of rows each.
+ *   x [T,H] in the storage dtype, or with x_scale != NULL e4m3 codes [T,H] with
+ *     their scale bytes [T,H/32] (H a multiple of 32), as moe_rms_norm_fwd gives.
+ *   Weights: w_gate_up [E,H,2I] and w_down [E,I,H] in the storage dtype with
+ *     mx = NULL, or mx with both NULL (dtype MOE_BF16; H and I multiples of 32).
+ *   bias: NULL, or per-expert biases (b_gate_up and b_down are read).
+ *   y [T,H] in the storage dtype, or fp32 with out_fp32.
+ * With dtype MOE_FP32 the products run in fp32 (not TF32).  With MOE_BF16 the
+ * activation is rounded to bf16 before the down product, as in moe_ffn_fwd.  An
+ * expert id outside [0,E) records MOE_ERR_BAD_INDEX in the workspace and its
+ * slot contributes nothing.  The sums run in an order that depends on the shape,
+ * the ids and the device only.  ws: moe_few_workspace_size(shape) bytes. */
+moe_status moe_ffn_few(const moe_shape* shape, const void* x, const uint8_t* x_scale,
+                       const int32_t* topk_idx, const float* topk_w, const void* w_gate_up,
+                       const void* w_down, const moe_mx_weights_t* mx, const moe_bias_t* bias,
+                       void* y, void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* ---- measurement helpers (no counterpart in the pages; they serve the
  * roofline accounting of the benchmark) ---- */
 

@@ -96,3 +96,30 @@ def test_grad_struct_layout(L, tmp_path):
     got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True).stdout.split()]
     assert got == [ctypes.sizeof(L.MoeGrad)] + [getattr(L.MoeGrad, f).offset
                                                 for f in ("src", "dst", "n", "dtype")]
+
+
+def test_ffn_few_refusals(L):
+    s = L.Shape(4, 64, 64, 8, 2)
+    size = L.moe_few_workspace_size(s)
+    assert size >= 8 * 64 * 2 + 8 * 64 * 4
+    assert L.moe_few_workspace_size(L.Shape(128, 64, 64, 8, 2)) > size
+    for bad in (dict(T=129), dict(H=12), dict(T=-1)):
+        assert L.moe_few_workspace_size(L.Shape(**dict(dict(T=4, H=64, I=64, E=8, k=2), **bad))) == 0
+    ok = dict(shape=s, x=16, x_scale=None, topk_idx=16, topk_w=16, w_gate_up=16, w_down=16, mx=None,
+              bias=None, y=16, ws=256, ws_bytes=size, stream=None)
+    mx = L.MoeMxWeights(16, 1, 16, 1)
+    for bad in (dict(x=None), dict(topk_idx=None), dict(topk_w=None), dict(w_gate_up=None),
+                dict(w_down=None), dict(y=None), dict(ws=None), dict(ws=128), dict(x=8), dict(y=8),
+                dict(w_gate_up=8), dict(w_down=8), dict(mx=mx),
+                dict(bias=L.MoeBias(8, None, None, None)),
+                dict(w_gate_up=None, w_down=None, mx=L.MoeMxWeights(16, None, 16, 1)),
+                dict(w_gate_up=None, w_down=None, mx=L.MoeMxWeights(16, 1, 8, 1)),
+                dict(w_gate_up=None, w_down=None, mx=mx, shape=L.Shape(4, 64, 40, 8, 2)),
+                dict(w_gate_up=None, w_down=None, mx=mx, shape=L.Shape(4, 72, 64, 8, 2)),
+                dict(x_scale=1, shape=L.Shape(4, 72, 64, 8, 2))):
+        assert L.moe_ffn_few(**dict(ok, **bad)) == L.MOE_ERR_INVALID_ARG, bad
+    assert L.moe_ffn_few(**dict(ok, ws_bytes=size - 1)) == L.MOE_ERR_WORKSPACE
+    assert L.moe_ffn_few(**dict(ok, shape=L.Shape(129, 64, 64, 8, 2))) == L.MOE_ERR_UNSUPPORTED
+    f32 = L.Shape(4, 64, 64, 8, 2, dtype=L.MOE_FP32)
+    assert L.moe_ffn_few(**dict(ok, shape=f32, w_gate_up=None, w_down=None, mx=mx)) == L.MOE_ERR_UNSUPPORTED
+    assert L.moe_ffn_few(**dict(ok, shape=L.Shape(0, 64, 64, 8, 2), x=None, y=None)) == L.MOE_OK
