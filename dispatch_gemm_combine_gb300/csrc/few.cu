@@ -45,6 +45,8 @@ constexpr int kMaxSlots = kMaxTokens * 32;   // k <= 32
 constexpr int kMaxE = 1024;
 constexpr int kMaxChunks = kMaxE + kMaxSlots / 8;
 constexpr int kMaxGrid = 512;
+constexpr int kNowhere = 0xffff;
+static_assert(kMaxChunks * 32 < kNowhere, "a slot's place fits 16 bits");
 
 struct FewArgs {
   const void* x;
@@ -68,7 +70,7 @@ struct FewArgs {
 struct Plan {
   uint32_t off[kMaxE + 1];     // exclusive sums: chunks << 16 | rows
   uint16_t slot[kMaxSlots];    // slots sorted by expert, by slot within one
-  uint16_t rank[kMaxSlots];    // a slot's row within its expert
+  uint16_t where[kMaxSlots];   // a slot's chunk * 32 + row in it; kNowhere: bad id
   uint16_t chunk_e[kMaxChunks];
   uint32_t span[kMaxChunks];   // down kernel: a unit's blocks, see combine
   uint32_t warp[8];
@@ -76,26 +78,29 @@ struct Plan {
   int last;
 };
 
-// A chunk is up to `rows` rows of one expert.  All blocks build the same plan.
+// A chunk is up to `rows` (8 or 32) rows of one expert.  All blocks build the
+// same plan.
 __device__ void build_plan(Plan& p, const int* __restrict__ idx, int Tk, int E, int rows, int* err) {
   const int tid = threadIdx.x, lane = tid & 31;
-  for (int e = tid; e <= E; e += kThreads) p.off[e] = 0;
+  for (int e = tid; e < E; e += kThreads) p.off[e] = 0;
+  for (int s = tid; s < Tk; s += kThreads) {
+    const int e = __ldg(idx + s);
+    const bool ok = e >= 0 && e < E;
+    if (!ok) record_error(err, kErrBadIndex);
+    p.slot[s] = static_cast<uint16_t>(ok ? e : kNowhere);   // the expert, for now
+  }
   __syncthreads();
   if (tid < 32) {
     for (int s0 = 0; s0 < Tk; s0 += 32) {
       const int s = s0 + lane;
-      int e = s < Tk ? __ldg(idx + s) : -1;
-      if (s < Tk && (e < 0 || e >= E)) {
-        record_error(err, kErrBadIndex);
-        e = -1;
-      }
+      const int e = s < Tk ? p.slot[s] : kNowhere;
       const unsigned same = __match_any_sync(0xffffffffu, e);
       const int before = __popc(same & ((1u << lane) - 1u));
       uint32_t base = 0;
-      if (e >= 0) base = p.off[e];
+      if (e != kNowhere) base = p.off[e];
       __syncwarp();
-      if (e >= 0) {
-        p.rank[s] = static_cast<uint16_t>(base + before);
+      if (e != kNowhere) {
+        p.where[s] = static_cast<uint16_t>(base + before);   // the row within the expert, for now
         if (before == 0) p.off[e] = base + __popc(same);
       }
       __syncwarp();
@@ -118,6 +123,11 @@ __device__ void build_plan(Plan& p, const int* __restrict__ idx, int Tk, int E, 
     if (lane >= d) inc += o;
   }
   if (lane == 31) p.warp[tid >> 5] = inc;
+  // the slots' experts move to registers: their array takes the sorted slots
+  uint16_t mine[kMaxSlots / kThreads];
+#pragma unroll
+  for (int i = 0; i < kMaxSlots / kThreads; ++i)
+    if (tid + i * kThreads < Tk) mine[i] = p.slot[tid + i * kThreads];
   __syncthreads();
   uint32_t base = inc - sum;
   for (int w = 0; w < (tid >> 5); ++w) base += p.warp[w];
@@ -136,9 +146,19 @@ __device__ void build_plan(Plan& p, const int* __restrict__ idx, int Tk, int E, 
     }
   }
   __syncthreads();
-  for (int s = tid; s < Tk; s += kThreads) {
-    const int e = __ldg(idx + s);
-    if (e >= 0 && e < E) p.slot[(p.off[e] & 0xffffu) + p.rank[s]] = static_cast<uint16_t>(s);
+#pragma unroll
+  for (int i = 0; i < kMaxSlots / kThreads; ++i) {
+    const int s = tid + i * kThreads;
+    if (s < Tk) {
+      int at = kNowhere;
+      if (mine[i] != kNowhere) {
+        const uint32_t o = p.off[mine[i]];
+        const int r = p.where[s];
+        p.slot[(o & 0xffffu) + r] = static_cast<uint16_t>(s);
+        at = (static_cast<int>(o >> 16) + r / rows) * 32 + r % rows;
+      }
+      p.where[s] = static_cast<uint16_t>(at);
+    }
   }
   __syncthreads();
 }
@@ -241,12 +261,13 @@ struct Row {
 struct Bf16 {
   using Store = __nv_bfloat16;
   static constexpr int WF = 64, FG = 2, KG = 4, STEP = 16;
+  static constexpr int PITCH = FG * WF + 1;   // of the results [row][column] in shared memory
   static constexpr bool kRowPerLane = true;   // lane (g, t) reads rows g, g + 8, ...
   template <int NT, bool X8>
   static __device__ __forceinline__ void run(const void* w, const uint8_t*, int64_t ld, int col,
                                              int ncol, int K, int s0, int s1, int kg,
-                                             const Row<X8>* rows, int nt_act, float* red) {
-    constexpr int U = NT == 1 ? 4 : 2;
+                                             const Row<X8>* rows, int, float* red) {
+    constexpr int U = NT == 1 ? 4 : (NT == 2 ? 2 : 1);
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float acc[4][NT][4];
 #pragma unroll
@@ -269,7 +290,7 @@ struct Bf16 {
           v[u][r] = ok && col_ok ? ldg_stream(base + (k + r) * ld) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          xb[u][n] = ok && n < nt_act ? rows[n].bf16x4(k) : make_uint2(0, 0);
+          xb[u][n] = ok ? rows[n].bf16x4(k) : make_uint2(0, 0);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -282,24 +303,19 @@ struct Bf16 {
           const uint32_t a0 = __byte_perm(w0[i], w1[i], 0x5410), a1 = __byte_perm(w0[i], w1[i], 0x7632);
           const uint32_t a2 = __byte_perm(w2[i], w3[i], 0x5410), a3 = __byte_perm(w2[i], w3[i], 0x7632);
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            if (n < nt_act) mma16816(acc[i][n], a0, a1, a2, a3, xb[u][n].x, xb[u][n].y);
+          for (int n = 0; n < NT; ++n) mma16816(acc[i][n], a0, a1, a2, a3, xb[u][n].x, xb[u][n].y);
         }
       }
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-      if (n < nt_act) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float* d = red + n * (WF * 8) + i * 128 + g * 8 + 2 * t;
-          *reinterpret_cast<float2*>(d) = make_float2(acc[i][n][0], acc[i][n][1]);
-          *reinterpret_cast<float2*>(d + 64) = make_float2(acc[i][n][2], acc[i][n][3]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        float* d = red + (8 * n + 2 * t) * PITCH + 8 * g + 2 * i;
+        d[0] = acc[i][n][0], d[PITCH] = acc[i][n][1];
+        d[1] = acc[i][n][2], d[PITCH + 1] = acc[i][n][3];
       }
   }
-  // where column f (of the group), token n of a row tile lies in `red`
-  static __device__ __forceinline__ int at(int f, int n) { return (f & 7) * 64 + (f >> 3) * 8 + n; }
 };
 
 // fp32 weights [K, ld]: the same loads (4 columns per lane), products on the
@@ -307,6 +323,7 @@ struct Bf16 {
 struct F32 {
   using Store = float;
   static constexpr int WF = 32, FG = 2, KG = 4, STEP = 16;
+  static constexpr int PITCH = FG * WF + 1;   // of the results [row][column] in shared memory
   static constexpr bool kRowPerLane = false;   // every lane reads all rows
   template <int NT, bool X8>
   static __device__ __forceinline__ void run(const void* w, const uint8_t*, int64_t ld, int col,
@@ -345,10 +362,9 @@ struct F32 {
       for (int c = 0; c < 4; ++c) {
         acc[n][c] += __shfl_xor_sync(0xffffffffu, acc[n][c], 1);
         acc[n][c] += __shfl_xor_sync(0xffffffffu, acc[n][c], 2);
-        if ((n >> 1) == t) red[(4 * g + c) * 8 + n] = acc[n][c];
+        if ((n >> 1) == t) red[n * PITCH + 4 * g + c] = acc[n][c];
       }
   }
-  static __device__ __forceinline__ int at(int f, int n) { return f * 8 + n; }
 };
 
 // Microscaled e2m1 weights: codes [N, K/2] and scale bytes [N, K/32], the
@@ -362,6 +378,7 @@ struct F32 {
 struct Mx {
   using Store = __nv_bfloat16;
   static constexpr int WF = 32, FG = 4, KG = 2, STEP = 128;
+  static constexpr int PITCH = FG * WF + 1;   // of the results [row][column] in shared memory
   static constexpr bool kRowPerLane = true;
   static __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -378,7 +395,7 @@ struct Mx {
   template <int NT, bool X8>
   static __device__ __forceinline__ void run(const void* w, const uint8_t* scales, int64_t, int col,
                                              int ncol, int K, int s0, int s1, int kg,
-                                             const Row<X8>* rows, int nt_act, float* red) {
+                                             const Row<X8>* rows, int, float* red) {
     constexpr int U = NT == 1 ? 2 : 1;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int nb = K >> 5;
@@ -412,26 +429,23 @@ struct Mx {
 #pragma unroll
         for (int r = 0; r < 4; ++r) large = large || f[u][r] > 128u;
       if (__any_sync(0xffffffffu, large))
-        step<NT, X8, U, true>(v, f, s, s1, kg, t, nb, rows, nt_act, acc);
+        step<NT, X8, U, true>(v, f, s, s1, kg, t, nb, rows, acc);
       else
-        step<NT, X8, U, false>(v, f, s, s1, kg, t, nb, rows, nt_act, acc);
+        step<NT, X8, U, false>(v, f, s, s1, kg, t, nb, rows, acc);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-      if (n < nt_act) {
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          float* d = red + n * (WF * 8) + m * 128 + g * 8 + 2 * t;
-          *reinterpret_cast<float2*>(d) = make_float2(acc[m][n][0], acc[m][n][1]);
-          *reinterpret_cast<float2*>(d + 64) = make_float2(acc[m][n][2], acc[m][n][3]);
-        }
+      for (int m = 0; m < 2; ++m) {
+        float* d = red + (8 * n + 2 * t) * PITCH + 16 * m + g;
+        d[0] = acc[m][n][0], d[PITCH] = acc[m][n][1];
+        d[8] = acc[m][n][2], d[PITCH + 8] = acc[m][n][3];
       }
   }
   template <int NT, bool X8, int U, bool LARGE>
   static __device__ __forceinline__ void step(const uint4 (&v)[U][4], const uint32_t (&f)[U][4],
                                               int s, int s1, int kg, int t, int nb,
-                                              const Row<X8>* rows, int nt_act,
-                                              float (&acc)[2][NT][4]) {
+                                              const Row<X8>* rows, float (&acc)[2][NT][4]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int b = ((s + u) * KG + kg) * 4 + t;
@@ -449,7 +463,7 @@ struct Mx {
         uint32_t xb[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint4 x = ok && n < nt_act ? rows[n].bf16x8(32 * b + 8 * q) : make_uint4(0, 0, 0, 0);
+          const uint4 x = ok ? rows[n].bf16x8(32 * b + 8 * q) : make_uint4(0, 0, 0, 0);
           xb[n][0] = __byte_perm(x.x, x.z, 0x5410);   // values 0 and 4
           xb[n][1] = __byte_perm(x.x, x.z, 0x7632);   // 1 and 5
           xb[n][2] = __byte_perm(x.y, x.w, 0x5410);   // 2 and 6
@@ -471,15 +485,13 @@ struct Mx {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            if (n < nt_act) {
+          for (int n = 0; n < NT; ++n) {
               mma16816(acc[m][n], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], xb[n][0], xb[n][1]);
               mma16816(acc[m][n], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], xb[n][2], xb[n][3]);
             }
       }
     }
   }
-  static __device__ __forceinline__ int at(int f, int n) { return (f >> 3) * 64 + (f & 7) * 8 + n; }
 };
 
 // ------------------------------------------------------------------ kernels
@@ -496,10 +508,41 @@ __device__ __forceinline__ float activate(const FewArgs& a, float gate, float up
   return (uc + 1.f) * gc * sigmoid_exact(a.alpha * gc);
 }
 
-// First step of block c's run, and the block whose run holds step s.
-__device__ __forceinline__ int64_t run_begin(int64_t steps, int c, int grid) { return steps * c / grid; }
-__device__ __forceinline__ int block_of_step(int64_t steps, int64_t s, int grid) {
-  return static_cast<int>(((s + 1) * grid - 1) / steps);
+// All units' steps cut into `grid` runs, the first `more` of them one step longer.
+struct Runs {
+  int grid, len, more;
+  __device__ __forceinline__ Runs(int steps, int blocks) {
+    // no more runs than steps: a unit's blocks are consecutive and each has a share
+    grid = min(blocks, steps);
+    len = grid ? steps / grid : 0;
+    more = steps - len * grid;
+  }
+  __device__ __forceinline__ int begin(int c) const { return c * len + min(c, more); }
+  __device__ __forceinline__ int block_of(int s) const {
+    const int head = more * (len + 1);
+    return s < head ? s / (len + 1) : more + (s - head) / len;
+  }
+};
+
+// The products of one unit's share for `tiles` row tiles, in the smallest
+// instance that holds them.
+template <class W, int NT, bool X8>
+__device__ __forceinline__ void run_tiles(int tiles, const void* w, const uint8_t* scales, int64_t ld,
+                                          int col, int ncol, int K, int s0, int s1, int kg,
+                                          const Row<X8>* rows, int nrows, float* red) {
+  if constexpr (NT >= 4) {
+    if (tiles > 2) {
+      W::template run<4, X8>(w, scales, ld, col, ncol, K, s0, s1, kg, rows, nrows, red);
+      return;
+    }
+  }
+  if constexpr (NT >= 2) {
+    if (tiles > 1) {
+      W::template run<2, X8>(w, scales, ld, col, ncol, K, s0, s1, kg, rows, nrows, red);
+      return;
+    }
+  }
+  W::template run<1, X8>(w, scales, ld, col, ncol, K, s0, s1, kg, rows, nrows, red);
 }
 
 // PHASE 0: gate_up and activation; 1: down and combine.
@@ -507,9 +550,9 @@ template <class W, int PHASE, int NT, bool X8>
 __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant__ FewArgs a) {
   using S = typename W::Store;
   constexpr int ROWS = 8 * NT;
-  constexpr int GROUP = W::WF * ROWS;          // results of one column group
-  constexpr int UNIT = W::FG * GROUP;
   constexpr int CW = W::FG * W::WF;            // weight columns of a unit
+  constexpr int UNIT = ROWS * CW;              // results of a unit, [row][column]
+  constexpr int SHARE = ROWS * W::PITCH;       // one share's results in shared memory
   constexpr int OUT = PHASE == 0 ? CW / 2 : CW;
   extern __shared__ float4 red4[];
   float* red = reinterpret_cast<float*>(red4);
@@ -528,22 +571,19 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   const int n_out = PHASE == 0 ? a.I : a.H;
   const int tiles = (n_out + OUT - 1) / OUT;
   const int KS = (K + W::KG * W::STEP - 1) / (W::KG * W::STEP);
-  const int64_t steps = static_cast<int64_t>(p.chunks) * tiles * KS;
-  // no more runs than steps: a unit's blocks are consecutive and each has a share
-  const int grid = static_cast<int>(min(static_cast<int64_t>(gridDim.x), steps));
-  const int64_t end = me < grid ? run_begin(steps, me + 1, grid) : 0;
+  const Runs runs(p.chunks * tiles * KS, gridDim.x);
+  const int end = me < runs.grid ? runs.begin(me + 1) : 0;
   if (PHASE == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  for (int64_t s = me < grid ? run_begin(steps, me, grid) : 0; s < end;) {
-    const int64_t unit = s / KS;
-    const int64_t u0 = unit * KS;
-    const int ks0 = static_cast<int>(s - u0);
-    const int ks1 = static_cast<int>(min(static_cast<int64_t>(KS), end - u0));
-    const int chunk = static_cast<int>(unit / tiles), tile = static_cast<int>(unit % tiles);
+  for (int s = me < runs.grid ? runs.begin(me) : 0; s < end;) {
+    const int unit = s / KS;
+    const int u0 = unit * KS;
+    const int ks0 = s - u0;
+    const int ks1 = min(KS, end - u0);
+    const int chunk = unit / tiles, tile = unit % tiles;
     const int e = p.chunk_e[chunk];
     const int first = static_cast<int>(p.off[e] & 0xffffu) + (chunk - static_cast<int>(p.off[e] >> 16)) * ROWS;
     const int nrows = min(ROWS, static_cast<int>(p.off[e + 1] & 0xffffu) - first);
-    const int nt_act = (nrows + 7) >> 3;
 
     // this warp's columns
     int col, ncol;
@@ -577,36 +617,33 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
                       : W::STEP == 128
                           ? static_cast<const void*>(static_cast<const uint8_t*>(a.w) + we / 2)
                           : static_cast<const void*>(static_cast<const __nv_bfloat16*>(a.w) + we);
-      W::template run<NT, X8>(w, W::STEP == 128 ? a.scales + we / 32 : nullptr, N, col, ncol, K, ks0,
-                              ks1, kg, rows, W::kRowPerLane ? nt_act : nrows,
-                              red + kg * UNIT + fg * GROUP);
+      run_tiles<W, NT, X8>((nrows + 7) >> 3, w, W::STEP == 128 ? a.scales + we / 32 : nullptr, N, col,
+                           ncol, K, ks0, ks1, kg, rows, nrows, red + kg * SHARE + fg * W::WF);
     }
     __syncthreads();
 
-    // add the shares of the contraction; a cut unit's sum goes to its part
+    // add the shares of the contraction; a cut unit's sum goes to its part, a
+    // whole one stays (gate_up) or goes to its rows (down)
     const bool whole = ks1 - ks0 == KS;
-    const int c0 = whole ? me : block_of_step(steps, u0, grid);
-    const bool at_begin = run_begin(steps, me, grid) >= u0;
-    float* part = a.part + (2 * static_cast<int64_t>(me) + (at_begin ? 0 : 1)) * UNIT;
-    const int per = nt_act * W::WF * 8;   // results in use, per column group
-    for (int i = tid * 4; i < W::FG * per; i += kThreads * 4) {
-      const int q = (i / per) * GROUP + i % per;
-      float4 v = *reinterpret_cast<const float4*>(red + q);
+    const int c0 = whole ? me : runs.block_of(u0);
+    float* part = a.part + (2 * static_cast<int64_t>(me) + (runs.begin(me) >= u0 ? 0 : 1)) * UNIT;
+    for (int i = tid; i < nrows * CW; i += kThreads) {
+      const int f = i % CW, r = i / CW, q = r * W::PITCH + f;
+      float v = red[q];
 #pragma unroll
-      for (int j = 1; j < W::KG; ++j) {
-        const float4 o = *reinterpret_cast<const float4*>(red + j * UNIT + q);
-        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-      }
-      if (whole)
-        *reinterpret_cast<float4*>(red + q) = v;
-      else
-        *reinterpret_cast<float4*>(part + q) = v;
+      for (int j = 1; j < W::KG; ++j) v += red[j * SHARE + q];
+      if (!whole)
+        part[i] = v;
+      else if (PHASE == 0)
+        red[q] = v;
+      else if (tile * OUT + f < a.H)
+        a.o[static_cast<int64_t>(p.slot[first + r]) * a.H + tile * OUT + f] = v;
     }
 
     if (PHASE == 0) {
       bool mine = true;
       if (!whole) {
-        const int c1 = block_of_step(steps, u0 + KS - 1, grid);
+        const int c1 = runs.block_of(u0 + KS - 1);
         __syncthreads();
         if (tid == 0) {
           __threadfence();
@@ -617,15 +654,11 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
         __syncthreads();
         mine = p.last != 0;
         if (mine) {
-          const int cut = run_begin(steps, c0, grid) >= u0 ? 0 : 1;
-          for (int i = tid * 4; i < W::FG * per; i += kThreads * 4) {
-            const int q = (i / per) * GROUP + i % per;
-            float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + (2 * static_cast<int64_t>(c0) + cut) * UNIT + q));
-            for (int c = c0 + 1; c <= c1; ++c) {
-              const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part + 2 * static_cast<int64_t>(c) * UNIT + q));
-              v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-            }
-            *reinterpret_cast<float4*>(red + q) = v;
+          const float* head = a.part + (2 * static_cast<int64_t>(c0) + (runs.begin(c0) >= u0 ? 0 : 1)) * UNIT;
+          for (int i = tid; i < nrows * CW; i += kThreads) {
+            float v = __ldcg(head + i);
+            for (int c = c0 + 1; c <= c1; ++c) v += __ldcg(a.part + 2 * static_cast<int64_t>(c) * UNIT + i);
+            red[i / CW * W::PITCH + i % CW] = v;
           }
         }
       }
@@ -635,10 +668,9 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
           const int f = i % OUT, r = i / OUT;
           const int feature = tile * OUT + f;
           if (feature >= a.I) continue;
-          const int cg = a.interleaved ? 2 * f : f, cu = a.interleaved ? 2 * f + 1 : f + OUT;
-          const float* q = red + (r >> 3) * (W::WF * 8);
-          float gate = q[(cg / W::WF) * GROUP + W::at(cg % W::WF, r & 7)];
-          float up = q[(cu / W::WF) * GROUP + W::at(cu % W::WF, r & 7)];
+          const float* q = red + r * W::PITCH;
+          float gate = q[a.interleaved ? 2 * f : f];
+          float up = q[a.interleaved ? 2 * f + 1 : f + OUT];
           if (a.bias) {
             const S* b = static_cast<const S*>(a.bias) + static_cast<int64_t>(e) * N;
             gate += load_elem(b, a.interleaved ? 2 * feature : feature);
@@ -649,15 +681,6 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
         }
       }
     } else {
-      if (whole) {
-        __syncthreads();
-        for (int i = tid; i < OUT * nrows; i += kThreads) {
-          const int f = i % OUT, r = i / OUT;
-          if (tile * OUT + f < a.H)
-            a.o[static_cast<int64_t>(p.slot[first + r]) * a.H + tile * OUT + f] =
-                red[(r >> 3) * (W::WF * 8) + (f / W::WF) * GROUP + W::at(f % W::WF, r & 7)];
-        }
-      }
       __syncthreads();
       if (tid == 0) {
         __threadfence();
@@ -671,40 +694,49 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
         // every product of this column tile is there: the blocks of each chunk's
         // unit (first | last << 15 | whether the first one's part is its second)
         for (int c = tid; c < p.chunks; c += kThreads) {
-          const int64_t b0 = (static_cast<int64_t>(c) * tiles + tile) * KS;
-          const int f0 = block_of_step(steps, b0, grid), f1 = block_of_step(steps, b0 + KS - 1, grid);
-          p.span[c] = f0 | (f1 << 15) | (run_begin(steps, f0, grid) < b0 ? 1u << 30 : 0u);
+          const int b0 = (c * tiles + tile) * KS;
+          const int f0 = runs.block_of(b0), f1 = runs.block_of(b0 + KS - 1);
+          p.span[c] = f0 | (f1 << 15) | (runs.begin(f0) < b0 ? 1u << 30 : 0u);
         }
         __syncthreads();
-        for (int i = tid; i < a.T * OUT; i += kThreads) {
-          const int f = i % OUT, tok = i / OUT;
+        for (int i = tid; i < a.T * (OUT / 4); i += kThreads) {
+          const int f = i % (OUT / 4) * 4, tok = i / (OUT / 4);
           const int c = tile * OUT + f;
           if (c >= a.H) continue;
-          float y = 0.f;
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
           for (int j = 0; j < a.k; ++j) {
             const int slot = tok * a.k + j;
-            const int se = __ldg(a.idx + slot);
-            if (se < 0 || se >= a.E) continue;
-            const int rank = p.rank[slot];
-            const uint32_t sp = p.span[(p.off[se] >> 16) + rank / ROWS];
+            const int at = p.where[slot];
+            if (at == kNowhere) continue;
+            const uint32_t sp = p.span[at >> 5];
             const int f0 = sp & 0x7fff, f1 = (sp >> 15) & 0x7fff;
-            float v;
+            const int q = (at & 31) * CW + f;
+            float4 v;
             if (f0 == f1) {
-              v = __ldcg(a.o + static_cast<int64_t>(slot) * a.H + c);
+              v = __ldcg(reinterpret_cast<const float4*>(a.o + static_cast<int64_t>(slot) * a.H + c));
             } else {
-              const int r = rank % ROWS;
-              const int q = (r >> 3) * (W::WF * 8) + (f / W::WF) * GROUP + W::at(f % W::WF, r & 7);
-              v = __ldcg(a.part + (2 * static_cast<int64_t>(f0) + (sp >> 30)) * UNIT + q);
-              for (int b = f0 + 1; b <= f1; ++b) v += __ldcg(a.part + 2 * static_cast<int64_t>(b) * UNIT + q);
+              v = __ldcg(reinterpret_cast<const float4*>(a.part + (2 * static_cast<int64_t>(f0) + (sp >> 30)) * UNIT + q));
+#pragma unroll 4
+              for (int b = f0 + 1; b <= f1; ++b) {
+                const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part + 2 * static_cast<int64_t>(b) * UNIT + q));
+                v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+              }
             }
-            if (a.bias) v += load_elem(static_cast<const S*>(a.bias), static_cast<int64_t>(se) * a.H + c);
-            y = fmaf(__ldg(a.topk_w + slot), v, y);
+            if (a.bias) {
+              const S* b = static_cast<const S*>(a.bias) + static_cast<int64_t>(p.chunk_e[at >> 5]) * a.H + c;
+              v.x += load_elem(b, 0), v.y += load_elem(b, 1), v.z += load_elem(b, 2), v.w += load_elem(b, 3);
+            }
+            const float w = __ldg(a.topk_w + slot);
+            y.x = fmaf(w, v.x, y.x), y.y = fmaf(w, v.y, y.y);
+            y.z = fmaf(w, v.z, y.z), y.w = fmaf(w, v.w, y.w);
           }
           const int64_t at = static_cast<int64_t>(tok) * a.H + c;
-          if (a.out_fp32)
-            static_cast<float*>(a.y)[at] = y;
+          if (a.out_fp32 || sizeof(S) == 4)
+            *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = y;
           else
-            static_cast<S*>(a.y)[at] = static_cast<S>(y);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.y) + at) =
+                make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
         }
       }
     }
@@ -712,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     s = u0 + ks1;
   }
   // no row at all (every id out of range): y is still written
-  if (PHASE == 1 && steps == 0) {
+  if (PHASE == 1 && runs.grid == 0) {
     for (int64_t i = me * static_cast<int64_t>(kThreads) + tid; i < static_cast<int64_t>(a.T) * a.H;
          i += static_cast<int64_t>(gridDim.x) * kThreads) {
       if (a.out_fp32)
@@ -725,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
 
 template <class W, int PHASE, int NT, bool X8>
 cudaError_t launch(const FewArgs& a, int grid, cudaStream_t st) {
-  constexpr int smem = W::KG * W::FG * W::WF * 8 * NT * 4;
+  constexpr int smem = W::KG * W::PITCH * 8 * NT * 4;
   static std::atomic<uint64_t> ready{0};   // one bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -783,7 +815,14 @@ FewLayout few_layout(const moe_shape* s) {
   return L;
 }
 
-bool few_shape_ok(const moe_shape* s) { return abi_shape_ok(s) && s->T <= kMaxTokens; }
+// Few tokens, and steps that 32 bits count: the smallest units are 32 outputs by
+// 64 values of the contraction.
+bool few_size_ok(const moe_shape* s) {
+  const int64_t wide = std::max(s->H, s->I) / 32 + 1, deep = std::max(s->H, s->I) / 64 + 1;
+  return s->T <= kMaxTokens &&
+         std::min<int64_t>(s->T * s->k, s->E + s->T * s->k / 8) * wide * deep < (1ll << 31);
+}
+bool few_shape_ok(const moe_shape* s) { return abi_shape_ok(s) && few_size_ok(s); }
 
 }  // namespace
 }  // namespace moe
@@ -815,7 +854,7 @@ moe_status moe_ffn_few(const moe_shape* s, const void* x, const uint8_t* x_scale
     if (!abi_aligned16(q)) return MOE_ERR_INVALID_ARG;
   if (bias && (!abi_aligned16(bias->b_gate_up) || !abi_aligned16(bias->b_down)))
     return MOE_ERR_INVALID_ARG;
-  if (s->T > kMaxTokens) return MOE_ERR_UNSUPPORTED;
+  if (!few_size_ok(s)) return MOE_ERR_UNSUPPORTED;
   const FewLayout L = few_layout(s);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   int sms = 0;

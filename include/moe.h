@@ -398,7 +398,8 @@ typedef struct {
   const uint8_t* scales_down;      /* [E,H,I/32] */
 } moe_mx_weights_t;
 
-/* Bytes of workspace of moe_ffn_few (0 for an invalid shape or T > 128). */
+/* Bytes of workspace of moe_ffn_few (0 for an invalid shape, T > 128, or H and I
+ * in the ten thousands at once). */
 size_t moe_few_workspace_size(const moe_shape* shape);
 
 /* The forward pass of the layer for a few tokens (inference), in two kernels
