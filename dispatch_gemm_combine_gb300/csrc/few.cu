@@ -46,6 +46,8 @@ constexpr int kMaxE = 1024;
 constexpr int kMaxChunks = kMaxE + kMaxSlots / 8;
 constexpr int kMaxGrid = 512;
 constexpr int kNowhere = 0xffff;
+// the largest plan_bytes(): every chunk, slot and expert there can be
+constexpr int kMostPlanBytes = 4 * kMaxChunks + 4 * kMaxE + 6 * kMaxChunks + 4 * kMaxSlots + 64;
 static_assert(kMaxChunks * 32 < kNowhere, "a slot's place fits 16 bits");
 
 struct FewArgs {
@@ -62,26 +64,94 @@ struct FewArgs {
   void* y;
   unsigned* counters;      // this kernel's; 0 between calls
   int* err;
-  int T, H, I, E, k, act_kind, interleaved, out_fp32;
+  int T, H, I, E, k, rows, act_kind, interleaved, out_fp32;   // rows: of a chunk
   float limit, alpha;
 };
 
 // ------------------------------------------------------------------ plan
+// A chunk is up to `rows` (8 or 32) rows of one expert; chunks are ordered by
+// expert, rows by slot.
+// Its arrays lie in dynamic shared memory, sized for the call (what they do not
+// take is L1 cache for the token rows).
 struct Plan {
-  uint32_t off[kMaxE + 1];     // exclusive sums: chunks << 16 | rows
-  uint16_t slot[kMaxSlots];    // slots sorted by expert, by slot within one
-  uint16_t where[kMaxSlots];   // a slot's chunk * 32 + row in it; kNowhere: bad id
-  uint16_t chunk_e[kMaxChunks];
-  uint32_t span[kMaxChunks];   // down kernel: a unit's blocks, see combine
+  uint16_t* slot;         // [Tk] slots in the order of the rows
+  uint16_t* where;        // [Tk] a slot's chunk * 32 + row in it; kNowhere: bad id
+  uint16_t* chunk_e;      // [chunks_max]
+  uint16_t* chunk_first;  // [chunks_max]
+  uint16_t* chunk_rows;   // [chunks_max]
+  uint32_t* span;         // [chunks_max] down kernel: a unit's blocks, see combine
+  uint32_t* off;          // [E] scratch: the experts' first chunk << 16 | first row
+  int chunks;
+};
+struct PlanSmall {
   uint32_t warp[8];
   int chunks;
-  int last;
+  int last[2];
 };
 
-// A chunk is up to `rows` (8 or 32) rows of one expert.  All blocks build the
-// same plan.
-__device__ void build_plan(Plan& p, const int* __restrict__ idx, int Tk, int E, int rows, int* err) {
+__host__ __device__ __forceinline__ int chunks_max(int Tk, int E, int rows) {
+  return (Tk < E ? Tk : E) + Tk / rows;
+}
+__host__ __device__ __forceinline__ int plan_bytes(int Tk, int E, int rows) {
+  const int c = (chunks_max(Tk, E, rows) + 1) & ~1, s = (Tk + 1) & ~1;
+  return (4 * c + 4 * (Tk <= 32 ? 0 : E) + 2 * 3 * c + 2 * 2 * s + 15) & ~15;
+}
+__device__ __forceinline__ Plan plan_at(void* base, int Tk, int E, int rows) {
+  const int c = (chunks_max(Tk, E, rows) + 1) & ~1, s = (Tk + 1) & ~1;
+  Plan p;
+  p.span = static_cast<uint32_t*>(base);
+  p.off = p.span + c;
+  p.chunk_e = reinterpret_cast<uint16_t*>(p.off + (Tk <= 32 ? 0 : E));
+  p.chunk_first = p.chunk_e + c;
+  p.chunk_rows = p.chunk_first + c;
+  p.slot = p.chunk_rows + c;
+  p.where = p.slot + s;
+  p.chunks = 0;
+  return p;
+}
+
+// One warp, a slot per lane: positions by counting.
+__device__ __forceinline__ void build_plan_warp(const Plan& p, PlanSmall& ps,
+                                                const int* __restrict__ idx, int Tk, int E,
+                                                int rows, int* err) {
+  const int lane = threadIdx.x & 31;
+  int e = lane < Tk ? __ldg(idx + lane) : E;
+  if (lane < Tk && (e < 0 || e >= E)) {
+    record_error(err, kErrBadIndex);
+    e = E;                                     // sorts last
+  }
+  const unsigned same = __match_any_sync(0xffffffffu, e);
+  const int rank = __popc(same & ((1u << lane) - 1u));
+  const int pos_e = e * 32 + lane;             // order of the rows
+  const bool head = e < E && rank % rows == 0; // a chunk's first row
+  const int head_key = head ? pos_e : 0x7fffffff;
+  int pos = 0, heads = 0;
+  for (int i = 0; i < Tk; ++i) {
+    const int o = __shfl_sync(0xffffffffu, pos_e, i), h = __shfl_sync(0xffffffffu, head_key, i);
+    pos += o < pos_e;
+    heads += h <= pos_e;
+  }
+  if (lane < Tk) p.where[lane] = static_cast<uint16_t>(e < E ? (heads - 1) * 32 + rank % rows : kNowhere);
+  if (e < E) p.slot[pos] = static_cast<uint16_t>(lane);
+  if (head) {
+    p.chunk_e[heads - 1] = static_cast<uint16_t>(e);
+    p.chunk_first[heads - 1] = static_cast<uint16_t>(pos);
+    p.chunk_rows[heads - 1] = static_cast<uint16_t>(min(rows, __popc(same) - rank));
+  }
+  const unsigned hb = __ballot_sync(0xffffffffu, head);
+  if (lane == 0) ps.chunks = __popc(hb);
+}
+
+// All blocks build the same plan.
+__device__ __forceinline__ void build_plan(Plan& p, PlanSmall& ps, const int* __restrict__ idx, int Tk,
+                                           int E, int rows, int* err) {
   const int tid = threadIdx.x, lane = tid & 31;
+  if (Tk <= 32) {
+    if (tid < 32) build_plan_warp(p, ps, idx, Tk, E, rows, err);
+    __syncthreads();
+    p.chunks = ps.chunks;
+    return;
+  }
   for (int e = tid; e < E; e += kThreads) p.off[e] = 0;
   for (int s = tid; s < Tk; s += kThreads) {
     const int e = __ldg(idx + s);
@@ -122,7 +192,7 @@ __device__ void build_plan(Plan& p, const int* __restrict__ idx, int Tk, int E, 
     const uint32_t o = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += o;
   }
-  if (lane == 31) p.warp[tid >> 5] = inc;
+  if (lane == 31) ps.warp[tid >> 5] = inc;
   // the slots' experts move to registers: their array takes the sorted slots
   uint16_t mine[kMaxSlots / kThreads];
 #pragma unroll
@@ -130,7 +200,7 @@ __device__ void build_plan(Plan& p, const int* __restrict__ idx, int Tk, int E, 
     if (tid + i * kThreads < Tk) mine[i] = p.slot[tid + i * kThreads];
   __syncthreads();
   uint32_t base = inc - sum;
-  for (int w = 0; w < (tid >> 5); ++w) base += p.warp[w];
+  for (int w = 0; w < (tid >> 5); ++w) base += ps.warp[w];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int e = tid * 4 + i;
@@ -138,11 +208,13 @@ __device__ void build_plan(Plan& p, const int* __restrict__ idx, int Tk, int E, 
       const uint32_t b = base + v[i];
       const uint32_t end = base + (i < 3 ? v[i + 1] : sum);
       p.off[e] = b;
-      for (uint32_t c = b >> 16; c < (end >> 16); ++c) p.chunk_e[c] = static_cast<uint16_t>(e);
-      if (e == E - 1) {
-        p.off[E] = end;
-        p.chunks = static_cast<int>(end >> 16);
+      const int first = b & 0xffffu, c0 = b >> 16, n = static_cast<int>(end & 0xffffu) - first;
+      for (int c = 0; c * rows < n; ++c) {
+        p.chunk_e[c0 + c] = static_cast<uint16_t>(e);
+        p.chunk_first[c0 + c] = static_cast<uint16_t>(first + c * rows);
+        p.chunk_rows[c0 + c] = static_cast<uint16_t>(min(rows, n - c * rows));
       }
+      if (e == E - 1) ps.chunks = static_cast<int>(end >> 16);
     }
   }
   __syncthreads();
@@ -161,6 +233,14 @@ __device__ void build_plan(Plan& p, const int* __restrict__ idx, int Tk, int E, 
     }
   }
   __syncthreads();
+  p.chunks = ps.chunks;
+}
+
+// Adds to a counter after the block's earlier writes, and before its later reads.
+__device__ __forceinline__ unsigned join_add(unsigned* p, unsigned v) {
+  unsigned old;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
 }
 
 // ------------------------------------------------------------------ products
@@ -254,6 +334,28 @@ struct Row {
   }
 };
 
+// A block of 32 values of a token row as it lies in memory, for use a little later.
+template <bool X8>
+struct RawBlock {
+  uint4 v[X8 ? 2 : 4];
+  uint32_t byte;
+  __device__ __forceinline__ void load(const Row<X8>& r, int b, bool ok) {
+    const bool in = ok && r.p;
+#pragma unroll
+    for (int i = 0; i < (X8 ? 2 : 4); ++i)
+      v[i] = in ? ld_u128(static_cast<const uint8_t*>(r.p) + (X8 ? 32 : 64) * static_cast<int64_t>(b) + 16 * i)
+                : make_uint4(0, 0, 0, 0);
+    byte = X8 && in ? __ldg(r.scale + b) : 127u;
+  }
+  __device__ __forceinline__ uint4 bf16x8(int q) const {
+    if (!X8) return v[q % (X8 ? 2 : 4)];
+    const uint4& c = v[(q >> 1) % 2];
+    const uint32_t lo = q & 1 ? c.z : c.x, hi = q & 1 ? c.w : c.y;
+    const float s = mx_scale(byte);
+    return make_uint4(e4m3_pair(lo, s), e4m3_pair(lo >> 16, s), e4m3_pair(hi, s), e4m3_pair(hi >> 16, s));
+  }
+};
+
 // bf16 weights [K, ld], columns innermost.  A lane loads 16 bytes (8 columns) of
 // four rows of the contraction; pairs along the contraction, as the instruction
 // wants them, come from two rows by byte permutes.  Columns 2 i and 2 i + 1 of
@@ -267,7 +369,7 @@ struct Bf16 {
   static __device__ __forceinline__ void run(const void* w, const uint8_t*, int64_t ld, int col,
                                              int ncol, int K, int s0, int s1, int kg,
                                              const Row<X8>* rows, int, float* red) {
-    constexpr int U = NT == 1 ? 4 : (NT == 2 ? 2 : 1);
+    constexpr int U = NT <= 2 ? 2 : 1;   // steps per buffer; two buffers take turns
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float acc[4][NT][4];
 #pragma unroll
@@ -278,34 +380,42 @@ struct Bf16 {
         for (int q = 0; q < 4; ++q) acc[i][n][q] = 0.f;
     const bool col_ok = 8 * g < ncol;
     const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(w) + col + 8 * g;
-    for (int s = s0; s < s1; s += U) {
-      uint4 v[U][4];
-      uint2 xb[U][NT];
+    uint4 v[2][U][4];
+    uint2 xb[2][U][NT];
+    auto load = [&](int buf, int s) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int k = ((s + u) * KG + kg) * STEP + 4 * t;
         const bool ok = s + u < s1 && k < K;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          v[u][r] = ok && col_ok ? ldg_stream(base + (k + r) * ld) : make_uint4(0, 0, 0, 0);
+          v[buf][u][r] = ok && col_ok ? ldg_stream(base + (k + r) * ld) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          xb[u][n] = ok ? rows[n].bf16x4(k) : make_uint2(0, 0);
+        for (int n = 0; n < NT; ++n) xb[buf][u][n] = ok ? rows[n].bf16x4(k) : make_uint2(0, 0);
       }
+    };
+    auto multiply = [&](int buf) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const uint32_t* w0 = &v[u][0].x;
-        const uint32_t* w1 = &v[u][1].x;
-        const uint32_t* w2 = &v[u][2].x;
-        const uint32_t* w3 = &v[u][3].x;
+        const uint32_t* w0 = &v[buf][u][0].x;
+        const uint32_t* w1 = &v[buf][u][1].x;
+        const uint32_t* w2 = &v[buf][u][2].x;
+        const uint32_t* w3 = &v[buf][u][3].x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t a0 = __byte_perm(w0[i], w1[i], 0x5410), a1 = __byte_perm(w0[i], w1[i], 0x7632);
           const uint32_t a2 = __byte_perm(w2[i], w3[i], 0x5410), a3 = __byte_perm(w2[i], w3[i], 0x7632);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816(acc[i][n], a0, a1, a2, a3, xb[u][n].x, xb[u][n].y);
+          for (int n = 0; n < NT; ++n) mma16816(acc[i][n], a0, a1, a2, a3, xb[buf][u][n].x, xb[buf][u][n].y);
         }
       }
+    };
+    load(0, s0);
+    for (int s = s0; s < s1; s += 2 * U) {
+      load(1, s + U);
+      multiply(0);
+      load(0, s + 2 * U);
+      multiply(1);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -396,7 +506,10 @@ struct Mx {
   static __device__ __forceinline__ void run(const void* w, const uint8_t* scales, int64_t, int col,
                                              int ncol, int K, int s0, int s1, int kg,
                                              const Row<X8>* rows, int, float* red) {
-    constexpr int U = NT == 1 ? 2 : 1;
+    // the token rows' loads go ahead with the weights' where registers allow (16
+    // for a step's weights, 16 for a row tile's tokens, twice); two buffers take
+    // turns
+    constexpr bool EARLY = NT == 1;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int nb = K >> 5;
     const int64_t cld = K >> 1;
@@ -409,29 +522,40 @@ struct Mx {
         for (int q = 0; q < 4; ++q) acc[m][n][q] = 0.f;
     const uint8_t* cp = static_cast<const uint8_t*>(w) + (static_cast<int64_t>(col) + g) * cld;
     const uint8_t* sp = scales + (static_cast<int64_t>(col) + g) * nb;
-    for (int s = s0; s < s1; s += U) {
-      uint4 v[U][4];
-      uint32_t f[U][4];
+    uint4 v[2][4];
+    uint32_t f[2][4];
+    RawBlock<X8> x[2][EARLY ? NT : 1];
+    auto load = [&](int buf, int s) {
+      const int b = (s * KG + kg) * 4 + t;
+      const bool ok = s < s1 && b < nb;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const bool in = ok && 8 * r < ncol;
+        v[buf][r] = in ? ldg_stream(cp + 8 * r * cld + 16 * b) : make_uint4(0, 0, 0, 0);
+        f[buf][r] = in ? __ldg(sp + static_cast<int64_t>(8 * r) * nb + b) : 0u;
+      }
+      if (EARLY)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[buf][n].load(rows[n], b, ok);
+    };
+    auto multiply = [&](int buf, int s) {
+      const int b = (s * KG + kg) * 4 + t;
+      const bool ok = s < s1 && b < nb;
       bool large = false;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int b = ((s + u) * KG + kg) * 4 + t;
-        const bool ok = s + u < s1 && b < nb;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const bool in = ok && 8 * r < ncol;
-          v[u][r] = in ? ldg_stream(cp + 8 * r * cld + 16 * b) : make_uint4(0, 0, 0, 0);
-          f[u][r] = in ? __ldg(sp + static_cast<int64_t>(8 * r) * nb + b) : 0u;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) large = large || f[u][r] > 128u;
+      for (int r = 0; r < 4; ++r) large = large || f[buf][r] > 128u;
       if (__any_sync(0xffffffffu, large))
-        step<NT, X8, U, true>(v, f, s, s1, kg, t, nb, rows, acc);
+        step<NT, X8, EARLY, true>(v[buf], f[buf], x[buf], b, ok, rows, acc);
       else
-        step<NT, X8, U, false>(v, f, s, s1, kg, t, nb, rows, acc);
+        step<NT, X8, EARLY, false>(v[buf], f[buf], x[buf], b, ok, rows, acc);
+    };
+    load(0, s0);
+    for (int s = s0; s < s1; s += 2) {
+      load(1, s + 1);
+      multiply(0, s);
+      if (s + 1 >= s1) break;
+      load(0, s + 2);
+      multiply(1, s + 1);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -442,54 +566,48 @@ struct Mx {
         d[8] = acc[m][n][2], d[PITCH + 8] = acc[m][n][3];
       }
   }
-  template <int NT, bool X8, int U, bool LARGE>
-  static __device__ __forceinline__ void step(const uint4 (&v)[U][4], const uint32_t (&f)[U][4],
-                                              int s, int s1, int kg, int t, int nb,
+  template <int NT, bool X8, bool EARLY, bool LARGE>
+  static __device__ __forceinline__ void step(const uint4 (&v)[4], const uint32_t (&f)[4],
+                                              const RawBlock<X8>* x, int b, bool ok,
                                               const Row<X8>* rows, float (&acc)[2][NT][4]) {
+    uint32_t f1[4], f2[4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int b = ((s + u) * KG + kg) * 4 + t;
-      const bool ok = s + u < s1 && b < nb;
-      uint32_t f1[4], f2[4];
+    for (int r = 0; r < 4; ++r) {
+      f1[r] = ((LARGE ? min(f[r], 128u) : f[r]) + 126u) * 0x00800080u;
+      if (LARGE)
+        f2[r] = f[r] == 255u ? 0x7fc07fc0u : (f[r] > 128u ? (f[r] - 1u) * 0x00800080u : 0x3f803f80u);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t xb[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4 xv = EARLY ? x[n].bf16x8(q) : (ok ? rows[n].bf16x8(32 * b + 8 * q) : make_uint4(0, 0, 0, 0));
+        xb[n][0] = __byte_perm(xv.x, xv.z, 0x5410);   // values 0 and 4
+        xb[n][1] = __byte_perm(xv.x, xv.z, 0x7632);   // 1 and 5
+        xb[n][2] = __byte_perm(xv.y, xv.w, 0x5410);   // 2 and 6
+        xb[n][3] = __byte_perm(xv.y, xv.w, 0x7632);   // 3 and 7
+      }
+      uint32_t a[4][4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const uint32_t sb = f[u][r];
-        f1[r] = ((LARGE ? min(sb, 128u) : sb) + 126u) * 0x00800080u;
-        if (LARGE)
-          f2[r] = sb == 255u ? 0x7fc07fc0u : (sb > 128u ? (sb - 1u) * 0x00800080u : 0x3f803f80u);
+        const uint32_t wd = q == 0 ? v[r].x : (q == 1 ? v[r].y : (q == 2 ? v[r].z : v[r].w));
+        a[r][0] = mul2(spread<0>(wd), f1[r]);
+        a[r][1] = mul2(spread<1>(wd), f1[r]);
+        a[r][2] = mul2(spread<2>(wd), f1[r]);
+        a[r][3] = mul2(spread<3>(wd), f1[r]);
+        if (LARGE) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a[r][j] = mul2(a[r][j], f2[r]);
+        }
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t xb[NT][4];
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint4 x = ok ? rows[n].bf16x8(32 * b + 8 * q) : make_uint4(0, 0, 0, 0);
-          xb[n][0] = __byte_perm(x.x, x.z, 0x5410);   // values 0 and 4
-          xb[n][1] = __byte_perm(x.x, x.z, 0x7632);   // 1 and 5
-          xb[n][2] = __byte_perm(x.y, x.w, 0x5410);   // 2 and 6
-          xb[n][3] = __byte_perm(x.y, x.w, 0x7632);   // 3 and 7
+          mma16816(acc[m][n], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], xb[n][0], xb[n][1]);
+          mma16816(acc[m][n], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], xb[n][2], xb[n][3]);
         }
-        uint32_t a[4][4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t wd = q == 0 ? v[u][r].x : (q == 1 ? v[u][r].y : (q == 2 ? v[u][r].z : v[u][r].w));
-          a[r][0] = mul2(spread<0>(wd), f1[r]);
-          a[r][1] = mul2(spread<1>(wd), f1[r]);
-          a[r][2] = mul2(spread<2>(wd), f1[r]);
-          a[r][3] = mul2(spread<3>(wd), f1[r]);
-          if (LARGE) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a[r][j] = mul2(a[r][j], f2[r]);
-          }
-        }
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-              mma16816(acc[m][n], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], xb[n][0], xb[n][1]);
-              mma16816(acc[m][n], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], xb[n][2], xb[n][3]);
-            }
-      }
     }
   }
 };
@@ -545,45 +663,177 @@ __device__ __forceinline__ void run_tiles(int tiles, const void* w, const uint8_
   W::template run<1, X8>(w, scales, ld, col, ncol, K, s0, s1, kg, rows, nrows, red);
 }
 
-// PHASE 0: gate_up and activation; 1: down and combine.
+// Floats of `red`: the shares' results, or the 256 threads' sums of the combine.
+template <class W>
+__host__ __device__ __forceinline__ int red_floats(int rows) {
+  const int n = (W::KG * W::PITCH * rows + 3) & ~3;
+  return n > 4 * kThreads ? n : 4 * kThreads;
+}
+
+// The activation of a unit's results, red[row][column], into its rows of a.act.
+template <class W>
+__device__ __forceinline__ void finish_gate_up(const FewArgs& a, const Plan& p, const float* red,
+                                               int chunk, int tile) {
+  using S = typename W::Store;
+  constexpr int OUT = W::FG * W::WF / 2;
+  const int first = p.chunk_first[chunk], nrows = p.chunk_rows[chunk];
+  const S* b = a.bias ? static_cast<const S*>(a.bias) + static_cast<int64_t>(p.chunk_e[chunk]) * 2 * a.I : nullptr;
+  for (int i = threadIdx.x; i < OUT * nrows; i += kThreads) {
+    const int f = i % OUT, r = i / OUT;
+    const int feature = tile * OUT + f;
+    if (feature >= a.I) continue;
+    const float* q = red + r * W::PITCH;
+    float gate = q[a.interleaved ? 2 * f : f];
+    float up = q[a.interleaved ? 2 * f + 1 : f + OUT];
+    if (b) {
+      gate += load_elem(b, a.interleaved ? 2 * feature : feature);
+      up += load_elem(b, a.interleaved ? 2 * feature + 1 : a.I + feature);
+    }
+    static_cast<S*>(a.act)[static_cast<int64_t>(p.slot[first + r]) * a.I + feature] =
+        static_cast<S>(activate(a, gate, up));
+  }
+}
+
+__device__ __forceinline__ void add4(float4& v, const float4& o) {
+  v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+}
+__device__ __forceinline__ float4 ldcg4(const float* p) { return __ldcg(reinterpret_cast<const float4*>(p)); }
+
+template <class S>
+__device__ __forceinline__ void store_y(const FewArgs& a, int tok, int c, const float4& y) {
+  if (c >= a.H) return;
+  const int64_t at = static_cast<int64_t>(tok) * a.H + c;
+  if (a.out_fp32 || sizeof(S) == 4)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = y;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.y) + at) =
+        make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+}
+
+// y of one column tile from every chunk's products: whole units' in a.o, cut
+// ones' in their blocks' parts.
+template <class W>
+__device__ __forceinline__ void combine_tile(const FewArgs& a, const Plan& p, const Runs& runs, int KS,
+                                             int tile, float* red) {
+  using S = typename W::Store;
+  constexpr int CW = W::FG * W::WF, V = CW / 4;
+  const int UNIT = a.rows * CW;
+  // the blocks of each chunk's unit: first | last << 15 | whether the first one's
+  // part is its second
+  for (int c = threadIdx.x; c < p.chunks; c += kThreads) {
+    const int b0 = (tile * p.chunks + c) * KS;
+    const int f0 = runs.block_of(b0), f1 = runs.block_of(b0 + KS - 1);
+    p.span[c] = f0 | (f1 << 15) | (runs.begin(f0) < b0 ? 1u << 30 : 0u);
+  }
+  __syncthreads();
+  // With few tokens a token's choices are shared out over `groups` threads (every
+  // groups-th choice each) whose sums are added in order.
+  const int items = a.T * V;
+  const int groups = max(1, min(a.k, kThreads / items));
+  float4* sums = reinterpret_cast<float4*>(red);
+  for (int i = threadIdx.x; i < items * groups; i += kThreads) {
+    const int f = i % V * 4, tok = i / V % a.T, group = i / items;
+    const int c = tile * CW + f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < a.H) {
+#pragma unroll 4
+      for (int j = group; j < a.k; j += groups) {
+        const int slot = tok * a.k + j;
+        const int at = p.where[slot];
+        if (at == kNowhere) continue;
+        const float w = __ldg(a.topk_w + slot);
+        const uint32_t sp = p.span[at >> 5];
+        const int f0 = sp & 0x7fff, n = static_cast<int>((sp >> 15) & 0x7fff) - f0;
+        const int q = (at & 31) * CW + f;
+        const float* head = n ? a.part + (2 * static_cast<int64_t>(f0) + (sp >> 30)) * UNIT + q
+                              : a.o + static_cast<int64_t>(slot) * a.H + c;
+        const float* next = a.part + 2 * static_cast<int64_t>(f0 + 1) * UNIT + q;
+        float4 v = ldcg4(head), o[3], bias = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int b = 0; b < 3; ++b)
+          o[b] = b < n ? ldcg4(next + 2 * static_cast<int64_t>(b) * UNIT) : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (a.bias) {
+          const S* b = static_cast<const S*>(a.bias) + static_cast<int64_t>(p.chunk_e[at >> 5]) * a.H + c;
+          bias = make_float4(load_elem(b, 0), load_elem(b, 1), load_elem(b, 2), load_elem(b, 3));
+        }
+#pragma unroll
+        for (int b = 0; b < 3; ++b) add4(v, o[b]);
+        for (int b = 3; b < n; ++b) add4(v, ldcg4(next + 2 * static_cast<int64_t>(b) * UNIT));
+        add4(v, bias);
+        y.x = fmaf(w, v.x, y.x), y.y = fmaf(w, v.y, y.y);
+        y.z = fmaf(w, v.z, y.z), y.w = fmaf(w, v.w, y.w);
+      }
+    }
+    if (groups == 1)
+      store_y<S>(a, tok, c, y);
+    else
+      sums[i] = y;
+  }
+  if (groups > 1) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < items; i += kThreads) {
+      float4 y = sums[i];
+      for (int g = 1; g < groups; ++g) add4(y, sums[g * items + i]);
+      store_y<S>(a, i / V, tile * CW + i % V * 4, y);
+    }
+  }
+  __syncthreads();   // p.span and red are free again
+}
+
+// PHASE 0: gate_up and activation; a cut unit is finished by the last of its
+// blocks.  PHASE 1: down and combine; a column tile is finished by the last of
+// its blocks.  Units are ordered by tile, then chunk: a run covers few tiles, and
+// experts with many rows and with few mix in every run.  A block counts itself in
+// at the end of its run, once, for the pieces at its two ends; the pieces between
+// are its own alone.
 template <class W, int PHASE, int NT, bool X8>
 __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant__ FewArgs a) {
   using S = typename W::Store;
-  constexpr int ROWS = 8 * NT;
   constexpr int CW = W::FG * W::WF;            // weight columns of a unit
-  constexpr int UNIT = ROWS * CW;              // results of a unit, [row][column]
-  constexpr int SHARE = ROWS * W::PITCH;       // one share's results in shared memory
+  const int UNIT = a.rows * CW;                // results of a unit, [row][column]
+  const int SHARE = a.rows * W::PITCH;         // one share's results in shared memory
   constexpr int OUT = PHASE == 0 ? CW / 2 : CW;
   extern __shared__ float4 red4[];
   float* red = reinterpret_cast<float*>(red4);
-  __shared__ Plan p;
+  __shared__ PlanSmall ps;
+  Plan p = plan_at(red + red_floats<W>(a.rows), a.T * a.k, a.E, a.rows);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int fg = warp % W::FG, kg = warp / W::FG;
   const int me = blockIdx.x;
   if (PHASE == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const int Tk = a.T * a.k;
-  build_plan(p, a.idx, Tk, a.E, ROWS, PHASE == 0 ? a.err : nullptr);
+  build_plan(p, ps, a.idx, a.T * a.k, a.E, a.rows, PHASE == 0 ? a.err : nullptr);
 
   const int K = PHASE == 0 ? a.H : a.I;                // contraction
   const int N = PHASE == 0 ? 2 * a.I : a.H;            // weight columns
-  const int n_out = PHASE == 0 ? a.I : a.H;
-  const int tiles = (n_out + OUT - 1) / OUT;
+  const int tiles = ((PHASE == 0 ? a.I : a.H) + OUT - 1) / OUT;
   const int KS = (K + W::KG * W::STEP - 1) / (W::KG * W::STEP);
-  const Runs runs(p.chunks * tiles * KS, gridDim.x);
-  const int end = me < runs.grid ? runs.begin(me + 1) : 0;
+  const int chunks = p.chunks;
+  const Runs runs(chunks * tiles * KS, gridDim.x);
   if (PHASE == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (me >= runs.grid) {
+    // no row at all (every id out of range): y is still written
+    if (PHASE == 1 && runs.grid == 0) {
+      for (int64_t i = me * static_cast<int64_t>(kThreads) + tid; i < static_cast<int64_t>(a.T) * a.H;
+           i += static_cast<int64_t>(gridDim.x) * kThreads) {
+        if (a.out_fp32)
+          static_cast<float*>(a.y)[i] = 0.f;
+        else
+          static_cast<S*>(a.y)[i] = static_cast<S>(0.f);
+      }
+    }
+    return;
+  }
+  const int begin = runs.begin(me), end = runs.begin(me + 1);
 
-  for (int s = me < runs.grid ? runs.begin(me) : 0; s < end;) {
+  for (int s = begin; s < end;) {
     const int unit = s / KS;
     const int u0 = unit * KS;
     const int ks0 = s - u0;
     const int ks1 = min(KS, end - u0);
-    const int chunk = unit / tiles, tile = unit % tiles;
-    const int e = p.chunk_e[chunk];
-    const int first = static_cast<int>(p.off[e] & 0xffffu) + (chunk - static_cast<int>(p.off[e] >> 16)) * ROWS;
-    const int nrows = min(ROWS, static_cast<int>(p.off[e + 1] & 0xffffu) - first);
+    const int chunk = unit % chunks, tile = unit / chunks;
+    const int e = p.chunk_e[chunk], first = p.chunk_first[chunk], nrows = p.chunk_rows[chunk];
 
     // this warp's columns
     int col, ncol;
@@ -596,6 +846,9 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       col = tile * CW + fg * W::WF;
       ncol = N - col;
     }
+    // the biases that the finishing block will want (128-byte lines)
+    if (a.bias && lane == 0 && kg == 0 && ncol > 0)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const S*>(a.bias) + static_cast<int64_t>(e) * N + col));
     Row<X8> rows[W::kRowPerLane ? NT : 8];
 #pragma unroll
     for (int i = 0; i < (W::kRowPerLane ? NT : 8); ++i) {
@@ -625,8 +878,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     // add the shares of the contraction; a cut unit's sum goes to its part, a
     // whole one stays (gate_up) or goes to its rows (down)
     const bool whole = ks1 - ks0 == KS;
-    const int c0 = whole ? me : runs.block_of(u0);
-    float* part = a.part + (2 * static_cast<int64_t>(me) + (runs.begin(me) >= u0 ? 0 : 1)) * UNIT;
+    float* part = a.part + (2 * static_cast<int64_t>(me) + (begin >= u0 ? 0 : 1)) * UNIT;
     for (int i = tid; i < nrows * CW; i += kThreads) {
       const int f = i % CW, r = i / CW, q = r * W::PITCH + f;
       float v = red[q];
@@ -639,132 +891,67 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       else if (tile * OUT + f < a.H)
         a.o[static_cast<int64_t>(p.slot[first + r]) * a.H + tile * OUT + f] = v;
     }
-
-    if (PHASE == 0) {
-      bool mine = true;
-      if (!whole) {
-        const int c1 = runs.block_of(u0 + KS - 1);
-        __syncthreads();
-        if (tid == 0) {
-          __threadfence();
-          p.last = atomicAdd(a.counters + c0, 1u) == static_cast<unsigned>(c1 - c0);
-          if (p.last) a.counters[c0] = 0;
-          __threadfence();
-        }
-        __syncthreads();
-        mine = p.last != 0;
-        if (mine) {
-          const float* head = a.part + (2 * static_cast<int64_t>(c0) + (runs.begin(c0) >= u0 ? 0 : 1)) * UNIT;
-          for (int i = tid; i < nrows * CW; i += kThreads) {
-            float v = __ldcg(head + i);
-            for (int c = c0 + 1; c <= c1; ++c) v += __ldcg(a.part + 2 * static_cast<int64_t>(c) * UNIT + i);
-            red[i / CW * W::PITCH + i % CW] = v;
-          }
-        }
-      }
-      __syncthreads();
-      if (mine) {
-        for (int i = tid; i < OUT * nrows; i += kThreads) {
-          const int f = i % OUT, r = i / OUT;
-          const int feature = tile * OUT + f;
-          if (feature >= a.I) continue;
-          const float* q = red + r * W::PITCH;
-          float gate = q[a.interleaved ? 2 * f : f];
-          float up = q[a.interleaved ? 2 * f + 1 : f + OUT];
-          if (a.bias) {
-            const S* b = static_cast<const S*>(a.bias) + static_cast<int64_t>(e) * N;
-            gate += load_elem(b, a.interleaved ? 2 * feature : feature);
-            up += load_elem(b, a.interleaved ? 2 * feature + 1 : a.I + feature);
-          }
-          static_cast<S*>(a.act)[static_cast<int64_t>(p.slot[first + r]) * a.I + feature] =
-              static_cast<S>(activate(a, gate, up));
-        }
-      }
-    } else {
-      __syncthreads();
-      if (tid == 0) {
-        __threadfence();
-        const unsigned all = static_cast<unsigned>(p.chunks) * KS, mine = ks1 - ks0;
-        p.last = atomicAdd(a.counters + tile, mine) + mine == all;
-        if (p.last) a.counters[tile] = 0;
-        __threadfence();
-      }
-      __syncthreads();
-      if (p.last) {
-        // every product of this column tile is there: the blocks of each chunk's
-        // unit (first | last << 15 | whether the first one's part is its second)
-        for (int c = tid; c < p.chunks; c += kThreads) {
-          const int b0 = (c * tiles + tile) * KS;
-          const int f0 = runs.block_of(b0), f1 = runs.block_of(b0 + KS - 1);
-          p.span[c] = f0 | (f1 << 15) | (runs.begin(f0) < b0 ? 1u << 30 : 0u);
-        }
-        __syncthreads();
-        for (int i = tid; i < a.T * (OUT / 4); i += kThreads) {
-          const int f = i % (OUT / 4) * 4, tok = i / (OUT / 4);
-          const int c = tile * OUT + f;
-          if (c >= a.H) continue;
-          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int j = 0; j < a.k; ++j) {
-            const int slot = tok * a.k + j;
-            const int at = p.where[slot];
-            if (at == kNowhere) continue;
-            const uint32_t sp = p.span[at >> 5];
-            const int f0 = sp & 0x7fff, f1 = (sp >> 15) & 0x7fff;
-            const int q = (at & 31) * CW + f;
-            float4 v;
-            if (f0 == f1) {
-              v = __ldcg(reinterpret_cast<const float4*>(a.o + static_cast<int64_t>(slot) * a.H + c));
-            } else {
-              v = __ldcg(reinterpret_cast<const float4*>(a.part + (2 * static_cast<int64_t>(f0) + (sp >> 30)) * UNIT + q));
-#pragma unroll 4
-              for (int b = f0 + 1; b <= f1; ++b) {
-                const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part + 2 * static_cast<int64_t>(b) * UNIT + q));
-                v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-              }
-            }
-            if (a.bias) {
-              const S* b = static_cast<const S*>(a.bias) + static_cast<int64_t>(p.chunk_e[at >> 5]) * a.H + c;
-              v.x += load_elem(b, 0), v.y += load_elem(b, 1), v.z += load_elem(b, 2), v.w += load_elem(b, 3);
-            }
-            const float w = __ldg(a.topk_w + slot);
-            y.x = fmaf(w, v.x, y.x), y.y = fmaf(w, v.y, y.y);
-            y.z = fmaf(w, v.z, y.z), y.w = fmaf(w, v.w, y.w);
-          }
-          const int64_t at = static_cast<int64_t>(tok) * a.H + c;
-          if (a.out_fp32 || sizeof(S) == 4)
-            *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = y;
-          else
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.y) + at) =
-                make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
-        }
-      }
-    }
     __syncthreads();
+    if (PHASE == 0 && whole) {
+      finish_gate_up<W>(a, p, red, chunk, tile);
+      __syncthreads();
+    }
+    // a tile that lies in this run alone
+    if (PHASE == 1 && chunk == chunks - 1 && ks1 == KS && begin <= tile * chunks * KS)
+      combine_tile<W>(a, p, runs, KS, tile, red);
     s = u0 + ks1;
   }
-  // no row at all (every id out of range): y is still written
-  if (PHASE == 1 && runs.grid == 0) {
-    for (int64_t i = me * static_cast<int64_t>(kThreads) + tid; i < static_cast<int64_t>(a.T) * a.H;
-         i += static_cast<int64_t>(gridDim.x) * kThreads) {
-      if (a.out_fp32)
-        static_cast<float*>(a.y)[i] = 0.f;
-      else
-        static_cast<S*>(a.y)[i] = static_cast<S>(0.f);
+
+  // the pieces at the run's ends: piece 0 its first unit (tile), 1 its last
+  const int per = PHASE == 0 ? KS : chunks * KS;       // steps of a unit (tile)
+  const int p0 = begin / per, p1 = (end - 1) / per;
+  if (tid < 2) {
+    const int piece = tid ? p1 : p0;
+    const int lo = max(begin, piece * per), hi = min(end, (piece + 1) * per);
+    int last = 0;
+    if (hi - lo < per && (tid == 0 || p1 != p0)) {
+      // a unit's counter is its first block's (a block is the first of at most one cut unit)
+      unsigned* c = a.counters + (PHASE == 0 ? runs.block_of(piece * per) : piece);
+      last = join_add(c, hi - lo) + (hi - lo) == static_cast<unsigned>(per);
+      if (last) *c = 0;
     }
+    ps.last[tid] = last;
+  }
+  __syncthreads();
+  for (int i = 0; i < 2; ++i) {
+    if (!ps.last[i]) continue;
+    const int piece = i ? p1 : p0;
+    if (PHASE == 1) {
+      combine_tile<W>(a, p, runs, KS, piece, red);
+      continue;
+    }
+    const int chunk = piece % chunks;
+    const int nrows = p.chunk_rows[chunk];
+    const int c0 = runs.block_of(piece * KS), c1 = runs.block_of(piece * KS + KS - 1);
+    const float* head = a.part + (2 * static_cast<int64_t>(c0) + (runs.begin(c0) >= piece * KS ? 0 : 1)) * UNIT;
+    for (int j = tid; j < nrows * CW; j += kThreads) {
+      float v = __ldcg(head + j);
+#pragma unroll 4
+      for (int c = c0 + 1; c <= c1; ++c) v += __ldcg(a.part + 2 * static_cast<int64_t>(c) * UNIT + j);
+      red[j / CW * W::PITCH + j % CW] = v;
+    }
+    __syncthreads();
+    finish_gate_up<W>(a, p, red, chunk, piece / chunks);
+    __syncthreads();
   }
 }
 
 template <class W, int PHASE, int NT, bool X8>
 cudaError_t launch(const FewArgs& a, int grid, cudaStream_t st) {
-  constexpr int smem = W::KG * W::PITCH * 8 * NT * 4;
+  const int smem = red_floats<W>(a.rows) * 4 + plan_bytes(a.T * a.k, a.E, a.rows);
+  const int most = red_floats<W>(8 * NT) * 4 + kMostPlanBytes;
   static std::atomic<uint64_t> ready{0};   // one bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(few_kernel<W, PHASE, NT, X8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(few_kernel<W, PHASE, NT, X8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
@@ -789,10 +976,12 @@ cudaError_t launch_nt(const FewArgs& a, int nt, int grid, cudaStream_t st) {
   return launch<W, PHASE, 1, X8>(a, grid, st);
 }
 
-// Row tiles of 8 tokens per unit: one holds every row of an expert that a token
-// names once when T <= 8; beyond that four, of which a unit runs only those that
-// its rows fill.
-int row_tiles(const moe_shape* s) { return s->dtype == MOE_FP32 || s->T <= 8 ? 1 : 4; }
+// Row tiles of 8 tokens per unit, at most four (registers): as many as hold an
+// expert's rows when every token names it once, so its weights are read once.  A
+// unit runs only the tiles that its rows fill.
+int row_tiles(const moe_shape* s) {
+  return s->dtype == MOE_FP32 ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, (s->T + 7) / 8)));
+}
 
 struct FewLayout {
   size_t counters0, counters1, act, part, o, total;
@@ -886,6 +1075,7 @@ moe_status moe_ffn_few(const moe_shape* s, const void* x, const uint8_t* x_scale
   a.limit = s->clamp_limit;
   a.alpha = s->alpha;
   const int nt = row_tiles(s);
+  a.rows = 8 * nt;
 
   cudaError_t e = abi_tracked(kAbiFewGateUp, 1, st, [&] {
     if (s->dtype == MOE_FP32)
