@@ -29,7 +29,7 @@ cudaError_t abi_tracked_memset(void* p, int value, size_t bytes, cudaStream_t st
 // event timer (their names: api.cu).
 enum AbiKind : int {
   kAbiNormFwd = 0, kAbiNormBwd, kAbiGradNorm, kAbiGradScale, kAbiMxQuantize, kAbiMxDequantize,
-  kAbiFewGateUp, kAbiFewDown, kNumAbiKinds
+  kAbiFewGateUp, kAbiFewDown, kAbiFewRows, kNumAbiKinds
 };
 
 // Launch accounting around a launcher of `nkernels` kernels, as moe.h

@@ -94,7 +94,8 @@ const char* const kKindNames[kNumKinds] = {
     "combine", "gemm_dgrad_down_act_bwd", "dw_reduce", "gemm_wgrad_down", "gemm_dgrad_gate_up",
     "gemm_wgrad_gate_up", "memset", "transpose_f32", "route", "bias_slot_dot", "bias_colsum",
     "split_select", "gather_index", "combine_dense", "norm_fwd", "norm_bwd",
-    "grad_norm", "grad_scale", "mx_quantize", "mx_dequantize", "few_gate_up", "few_down"};
+    "grad_norm", "grad_scale", "mx_quantize", "mx_dequantize", "few_gate_up", "few_down",
+    "few_rows"};
 
 std::atomic<uint64_t> g_launches{0};
 std::atomic<int> g_profile{0};

@@ -58,7 +58,10 @@ struct FewArgs {
   const void* w;           // this kernel's weights, or codes
   const uint8_t* scales;   // the codes' scale bytes
   const void* bias;        // this kernel's bias, or null
-  void* act;               // [Tk, I]
+  void* act;               // [Tk, I]: storage type; fp16 with 4-bit weights, and
+  uint8_t* act_scale;      // [Tk, I/32] its blocks' scale bytes, and
+  int* act_top;            // [Tk] the largest of each row's
+  const int* top;          // of the fp16 rows in x
   float* part;             // parts of cut units: 2 per block
   float* o;                // [Tk, H] products of whole units
   void* y;
@@ -258,6 +261,10 @@ __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
 // Weights: read once, never written by the layer.
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 v;
@@ -267,9 +274,13 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   return v;
 }
 
-// Token rows and activations.  The down kernel reads what the gate_up kernel
-// wrote while it was already running, so these are plain loads in program order,
-// after its wait.
+// Token rows and activations.  A kernel may start before the one that writes them
+// has ended, so these are plain loads in program order, after its wait.
+__device__ __forceinline__ uint32_t ld_u8(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t ld_u32(const void* p) {
   uint32_t v;
   asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -289,87 +300,41 @@ __device__ __forceinline__ uint4 ld_u128(const void* p) {
   return v;
 }
 
-// Two e4m3 codes times a power-of-two scale as bf16 (exact but for results below
-// bf16's normal range).
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t two, float scale) {
-  const __half2_raw h =
-      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xffffu), __NV_E4M3);
-  const float2 f = __half22float2(__half2(h));
-  return pack_bf16(f.x * scale, f.y * scale);
-}
+// Waits for the kernel before (returns at once when it has ended).
+__device__ __forceinline__ void wait_for_rows() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // A token row (or a slot's activations) as the product reads it.
-template <bool X8>
 struct Row {
-  const void* p = nullptr;             // null: no such row, zeros
-  const uint8_t* scale = nullptr;
-  __device__ __forceinline__ uint2 bf16x4(int k) const {
-    if (!p) return make_uint2(0, 0);
-    if (!X8) return ld_u64(static_cast<const __nv_bfloat16*>(p) + k);
-    const uint32_t c = ld_u32(static_cast<const uint8_t*>(p) + k);
-    const float s = mx_scale(__ldg(scale + (k >> 5)));
-    return make_uint2(e4m3_pair(c, s), e4m3_pair(c >> 16, s));
-  }
-  __device__ __forceinline__ uint4 bf16x8(int k) const {
-    if (!p) return make_uint4(0, 0, 0, 0);
-    if (!X8) return ld_u128(static_cast<const __nv_bfloat16*>(p) + k);
-    const uint2 c = ld_u64(static_cast<const uint8_t*>(p) + k);
-    const float s = mx_scale(__ldg(scale + (k >> 5)));
-    return make_uint4(e4m3_pair(c.x, s), e4m3_pair(c.x >> 16, s), e4m3_pair(c.y, s),
-                      e4m3_pair(c.y >> 16, s));
-  }
-  __device__ __forceinline__ float4 f32x4(int k) const {
-    if (!X8) {
-      const uint4 v = ld_u128(static_cast<const float*>(p) + k);
-      return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
-                         __uint_as_float(v.w));
-    }
-    const uint32_t c = ld_u32(static_cast<const uint8_t*>(p) + k);
-    const float s = mx_scale(__ldg(scale + (k >> 5)));
-    const float2 lo = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
-        static_cast<__nv_fp8x2_storage_t>(c & 0xffffu), __NV_E4M3)));
-    const float2 hi = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
-        static_cast<__nv_fp8x2_storage_t>(c >> 16), __NV_E4M3)));
-    return make_float4(lo.x * s, lo.y * s, hi.x * s, hi.y * s);
-  }
-};
-
-// A block of 32 values of a token row as it lies in memory, for use a little later.
-template <bool X8>
-struct RawBlock {
-  uint4 v[X8 ? 2 : 4];
-  uint32_t byte;
-  __device__ __forceinline__ void load(const Row<X8>& r, int b, bool ok) {
-    const bool in = ok && r.p;
-#pragma unroll
-    for (int i = 0; i < (X8 ? 2 : 4); ++i)
-      v[i] = in ? ld_u128(static_cast<const uint8_t*>(r.p) + (X8 ? 32 : 64) * static_cast<int64_t>(b) + 16 * i)
-                : make_uint4(0, 0, 0, 0);
-    byte = X8 && in ? __ldg(r.scale + b) : 127u;
-  }
-  __device__ __forceinline__ uint4 bf16x8(int q) const {
-    if (!X8) return v[q % (X8 ? 2 : 4)];
-    const uint4& c = v[(q >> 1) % 2];
-    const uint32_t lo = q & 1 ? c.z : c.x, hi = q & 1 ? c.w : c.y;
-    const float s = mx_scale(byte);
-    return make_uint4(e4m3_pair(lo, s), e4m3_pair(lo >> 16, s), e4m3_pair(hi, s), e4m3_pair(hi >> 16, s));
-  }
+  const void* p;
+  const uint8_t* scale = nullptr;   // of fp16 rows: null, or a byte per block of 32
+  int top = 127;                    // of fp16 rows: the row's byte, the largest of its blocks'
 };
 
 // bf16 weights [K, ld], columns innermost.  A lane loads 16 bytes (8 columns) of
 // four rows of the contraction; pairs along the contraction, as the instruction
 // wants them, come from two rows by byte permutes.  Columns 2 i and 2 i + 1 of
-// the lane are rows g and g + 8 of instruction i.
+// the lane are rows g and g + 8 of instruction i.  Past the contraction's end the
+// tokens are zero and the weights any valid ones; columns past the end and rows
+// that a unit does not have are computed from others' and never read.
 struct Bf16 {
   using Store = __nv_bfloat16;
   static constexpr int WF = 64, FG = 2, KG = 4, STEP = 16;
   static constexpr int PITCH = FG * WF + 1;   // of the results [row][column] in shared memory
+  static constexpr bool kHalfRows = false;
   static constexpr bool kRowPerLane = true;   // lane (g, t) reads rows g, g + 8, ...
-  template <int NT, bool X8>
+  static constexpr int kMaxTiles = 2;
+  // A unit's first two steps of this warp: 16 rows of 128 bytes each.
+  static __device__ __forceinline__ void prefetch(const void* w, const uint8_t*, int64_t first, int64_t ld,
+                                                  int col, int ncol, int K, int kg) {
+    const int lane = threadIdx.x & 31, k = ((lane >> 4) * KG + kg) * STEP + (lane & 15);
+    if (ncol > 0 && k < K) prefetch_l2(static_cast<const __nv_bfloat16*>(w) + first + k * ld + col);
+  }
+  template <int NT>
   static __device__ __forceinline__ void run(const void* w, const uint8_t*, int64_t ld, int col,
                                              int ncol, int K, int s0, int s1, int kg,
-                                             const Row<X8>* rows, int, float* red) {
-    constexpr int U = NT <= 2 ? 2 : 1;   // steps per buffer; two buffers take turns
+                                             const Row* rows, int nrows, float* red) {
+    constexpr int U = NT == 1 ? 2 : 1;   // steps per buffer; two buffers take turns
+    const bool both = NT > 1 && nrows > 8;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float acc[4][NT][4];
 #pragma unroll
@@ -378,25 +343,33 @@ struct Bf16 {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[i][n][q] = 0.f;
-    const bool col_ok = 8 * g < ncol;
-    const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(w) + col + 8 * g;
+    const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(w) + col + (8 * g < ncol ? 8 * g : 0);
     uint4 v[2][U][4];
     uint2 xb[2][U][NT];
-    auto load = [&](int buf, int s) {
+    auto load_w = [&](int buf, int s) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = ((s + u) * KG + kg) * STEP + 4 * t;
-        const bool ok = s + u < s1 && k < K;
+      for (int u = 0; u < U; ++u)
+        if (s + u < s1) {
+          const __nv_bfloat16* p = base + min(((s + u) * KG + kg) * STEP + 4 * t, K - 4) * ld;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          v[buf][u][r] = ok && col_ok ? ldg_stream(base + (k + r) * ld) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) xb[buf][u][n] = ok ? rows[n].bf16x4(k) : make_uint2(0, 0);
-      }
+          for (int r = 0; r < 4; ++r) v[buf][u][r] = ldg_stream(p + r * ld);
+        }
     };
-    auto multiply = [&](int buf) {
+    auto load_x = [&](int buf, int s) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (s + u < s1) {
+          const int k = ((s + u) * KG + kg) * STEP + 4 * t;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            if (n == 0 || both)
+              xb[buf][u][n] = k < K ? ld_u64(static_cast<const __nv_bfloat16*>(rows[n].p) + k) : make_uint2(0, 0);
+        }
+    };
+    auto multiply = [&](int buf, int s) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
+        if (s + u >= s1) continue;
         const uint32_t* w0 = &v[buf][u][0].x;
         const uint32_t* w1 = &v[buf][u][1].x;
         const uint32_t* w2 = &v[buf][u][2].x;
@@ -406,16 +379,21 @@ struct Bf16 {
           const uint32_t a0 = __byte_perm(w0[i], w1[i], 0x5410), a1 = __byte_perm(w0[i], w1[i], 0x7632);
           const uint32_t a2 = __byte_perm(w2[i], w3[i], 0x5410), a3 = __byte_perm(w2[i], w3[i], 0x7632);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816(acc[i][n], a0, a1, a2, a3, xb[buf][u][n].x, xb[buf][u][n].y);
+          for (int n = 0; n < NT; ++n)
+            if (n == 0 || both) mma16816(acc[i][n], a0, a1, a2, a3, xb[buf][u][n].x, xb[buf][u][n].y);
         }
       }
     };
-    load(0, s0);
+    load_w(0, s0);
+    wait_for_rows();
+    load_x(0, s0);
     for (int s = s0; s < s1; s += 2 * U) {
-      load(1, s + U);
-      multiply(0);
-      load(0, s + 2 * U);
-      multiply(1);
+      load_w(1, s + U);
+      load_x(1, s + U);
+      multiply(0, s);
+      load_w(0, s + 2 * U);
+      load_x(0, s + 2 * U);
+      multiply(1, s + U);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -434,11 +412,16 @@ struct F32 {
   using Store = float;
   static constexpr int WF = 32, FG = 2, KG = 4, STEP = 16;
   static constexpr int PITCH = FG * WF + 1;   // of the results [row][column] in shared memory
+  static constexpr bool kHalfRows = false;
   static constexpr bool kRowPerLane = false;   // every lane reads all rows
-  template <int NT, bool X8>
+  static constexpr int kMaxTiles = 1;
+  static __device__ __forceinline__ void prefetch(const void*, const uint8_t*, int64_t, int64_t, int, int,
+                                                  int, int) {}
+  template <int NT>
   static __device__ __forceinline__ void run(const void* w, const uint8_t*, int64_t ld, int col,
                                              int ncol, int K, int s0, int s1, int kg,
-                                             const Row<X8>* rows, int nrows, float* red) {
+                                             const Row* rows, int nrows, float* red) {
+    wait_for_rows();
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const bool col_ok = 4 * g < ncol;
     float acc[8][4];
@@ -460,10 +443,13 @@ struct F32 {
 #pragma unroll
       for (int n = 0; n < 8; ++n)
         if (n < nrows && ok) {
-          const float4 x = rows[n].f32x4(k);
+          const uint4 q = ld_u128(static_cast<const float*>(rows[n].p) + k);
+          const float x[4] = {__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z),
+                              __uint_as_float(q.w)};
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            acc[n][c] = fmaf(x.w, v[3][c], fmaf(x.z, v[2][c], fmaf(x.y, v[1][c], fmaf(x.x, v[0][c], acc[n][c]))));
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[n][c] = fmaf(x[r], v[r][c], acc[n][c]);
         }
     }
 #pragma unroll
@@ -478,41 +464,97 @@ struct F32 {
 };
 
 // Microscaled e2m1 weights: codes [N, K/2] and scale bytes [N, K/32], the
-// contraction innermost.  A lane loads whole blocks of 32 (16 bytes) of columns
-// g, g + 8, g + 16 and g + 24, so each load has one scale.  Two codes four apart
-// in a word lie 16 bits apart: their sign and magnitude bits are moved to bit 15
-// and bits 8..6 of both halves at once, which reads as the value times 2^-126 in
-// bf16 (0.5 is a subnormal there), and one exact bf16 product by 2^(126 + q)
-// gives the weight.  Scales above 2 would need a larger factor than bf16 has
-// and take a second product.
+// contraction innermost; token rows in fp16 with a power of two per row (and
+// possibly per block of 32).
+//
+// At HBM's rate an SM gets some 44 weights a clock and issues 128 operations, half
+// of them logic and conversions, so decoding must be cheap: a conversion e2m1 ->
+// fp16 makes two weights, and one fp16 product scales them, two instructions per
+// two weights.  A lane loads whole blocks (16 bytes) of columns g, g + 8, g + 16
+// and g + 24, so each load has one scale 2^q.  fp16 holds 2^q times a code exactly
+// only near 1, so a column's weights are scaled by 2^(q - ref), ref being the scale
+// of the first block that the warp sees of that column, and the sums by 2^ref at
+// the end.  A step with a block outside 2^-14 .. 2^13 of its column's ref (or a NaN
+// scale) takes a path that multiplies the blocks one by one and scales sums.
 struct Mx {
   using Store = __nv_bfloat16;
   static constexpr int WF = 32, FG = 4, KG = 2, STEP = 128;
   static constexpr int PITCH = FG * WF + 1;   // of the results [row][column] in shared memory
-  static constexpr bool kRowPerLane = true;
+  static constexpr int kMaxTiles = 2;
+  static constexpr bool kRowPerLane = true, kHalfRows = true;
+
+  static __device__ __forceinline__ void mma(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+  // The eight codes of a word as fp16 pairs.
+  static __device__ __forceinline__ void decode(uint32_t w, uint32_t (&v)[4]) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+        : "r"(w));
+  }
   static __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
   }
-  // Codes j and j + 4 of a word as bf16 values times 2^-126.
-  template <int J>
-  static __device__ __forceinline__ uint32_t spread(uint32_t w) {
-    const uint32_t sign = J == 3 ? w : w << (12 - 4 * J);
-    const uint32_t mag = J < 2 ? w << (6 - 4 * J) : w >> (4 * J - 6);
-    return (sign & 0x80008000u) | (mag & 0x01c001c0u);
+  static __device__ __forceinline__ uint32_t word(const uint4& v, int q) {
+    return q == 0 ? v.x : (q == 1 ? v.y : (q == 2 ? v.z : v.w));
   }
-  template <int NT, bool X8>
+  // 2^d for d <= 0 in both halves of fp16, 0 below its range.
+  static __device__ __forceinline__ uint32_t pow2_down(int d) {
+    const uint32_t h = d >= -14 ? (d + 15) << 10 : (d >= -24 ? 1u << (d + 24) : 0u);
+    return h * 0x00010001u;
+  }
+
+  // A step of a warp: 4 blocks (one per lane t) of 4 x 8 columns.
+  struct Load {
+    uint4 v[4];
+    uint32_t byte[4];
+  };
+  // What brings the tokens' block b to the row's power of two; 0 past the end.
+  static __device__ __forceinline__ uint32_t row_factor(const Row& r, int b, int nb) {
+    if (b >= nb) return 0u;
+    if (!r.scale) return 0x3c003c00u;
+    const uint32_t p = ld_u8(r.scale + b);
+    return p == 255u ? 0x7e007e00u : pow2_down(static_cast<int>(p) - r.top);
+  }
+  static __device__ __forceinline__ uint4 row_vec(const Row& r, int b, int q) {
+    return ld_u128(static_cast<const __half*>(r.p) + 32 * b + 8 * q);
+  }
+
+  // A unit's first two steps of this warp: 64 bytes of 32 columns each.
+  static __device__ __forceinline__ void prefetch(const void* w, const uint8_t* scales, int64_t first, int64_t,
+                                                  int col, int ncol, int K, int kg) {
+    const int lane = threadIdx.x & 31;
+    if (lane >= ncol) return;
+    const int64_t c = col + lane;
+    const uint8_t* p = static_cast<const uint8_t*>(w) + first / 2 + c * (K >> 1);
+    prefetch_l2(scales + first / 32 + c * (K >> 5));
+    if (kg * 64 < K / 2) prefetch_l2(p + kg * 64);
+    if ((KG + kg) * 64 < K / 2) prefetch_l2(p + (KG + kg) * 64);
+  }
+  template <int NT>
   static __device__ __forceinline__ void run(const void* w, const uint8_t* scales, int64_t, int col,
                                              int ncol, int K, int s0, int s1, int kg,
-                                             const Row<X8>* rows, int, float* red) {
-    // the token rows' loads go ahead with the weights' where registers allow (16
-    // for a step's weights, 16 for a row tile's tokens, twice); two buffers take
-    // turns
+                                             const Row* rows, int nrows, float* red) {
+    // Two buffers take turns (16 registers for a step's weights); with one row tile
+    // the tokens' loads go ahead with the weights' (16 more), with two there are no
+    // registers for that.  Past the end the last block is loaded again and the
+    // tokens' factor is 0.
     constexpr bool EARLY = NT == 1;
+    const bool both = NT > 1 && nrows > 8;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int nb = K >> 5;
-    const int64_t cld = K >> 1;
+    const int64_t cld = 8ll * (K >> 1);         // from one eight columns to the next
     float acc[2][NT][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -520,97 +562,240 @@ struct Mx {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[m][n][q] = 0.f;
-    const uint8_t* cp = static_cast<const uint8_t*>(w) + (static_cast<int64_t>(col) + g) * cld;
+    const uint8_t* cp = static_cast<const uint8_t*>(w) + (static_cast<int64_t>(col) + g) * (K >> 1);
     const uint8_t* sp = scales + (static_cast<int64_t>(col) + g) * nb;
-    uint4 v[2][4];
-    uint32_t f[2][4];
-    RawBlock<X8> x[2][EARLY ? NT : 1];
-    auto load = [&](int buf, int s) {
-      const int b = (s * KG + kg) * 4 + t;
-      const bool ok = s < s1 && b < nb;
+    const int eights = min(4, ncol >> 3);       // inside
+    Load ld[2];
+    uint4 x[2][EARLY ? 4 : 1];
+    uint32_t xf[2] = {0, 0};
+    auto load_w = [&](int buf, int s) {
+      if (s >= s1) return;
+      const int b = min((s * KG + kg) * 4 + t, nb - 1);
+      const uint8_t* src = cp + 16 * b;
+      const uint8_t* byte = sp + b;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const bool in = ok && 8 * r < ncol;
-        v[buf][r] = in ? ldg_stream(cp + 8 * r * cld + 16 * b) : make_uint4(0, 0, 0, 0);
-        f[buf][r] = in ? __ldg(sp + static_cast<int64_t>(8 * r) * nb + b) : 0u;
+        const int rr = r < eights ? r : 0;
+        ld[buf].v[r] = ldg_stream(src + rr * cld);
+        ld[buf].byte[r] = __ldg(byte + rr * 8 * nb);
       }
-      if (EARLY)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) x[buf][n].load(rows[n], b, ok);
     };
-    auto multiply = [&](int buf, int s) {
+    auto load_x = [&](int buf, int s) {
+      if (!EARLY || s >= s1) return;
       const int b = (s * KG + kg) * 4 + t;
-      const bool ok = s < s1 && b < nb;
-      bool large = false;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) large = large || f[buf][r] > 128u;
-      if (__any_sync(0xffffffffu, large))
-        step<NT, X8, EARLY, true>(v[buf], f[buf], x[buf], b, ok, rows, acc);
-      else
-        step<NT, X8, EARLY, false>(v[buf], f[buf], x[buf], b, ok, rows, acc);
+      for (int q = 0; q < 4; ++q) x[buf][q % (EARLY ? 4 : 1)] = row_vec(rows[0], min(b, nb - 1), q);
+      xf[buf] = row_factor(rows[0], b, nb);
     };
-    load(0, s0);
-    for (int s = s0; s < s1; s += 2) {
-      load(1, s + 1);
-      multiply(0, s);
-      if (s + 1 >= s1) break;
-      load(0, s + 2);
-      multiply(1, s + 1);
-    }
+    load_w(0, s0);
+    load_w(1, s0 + 1);
+    wait_for_rows();
+    load_x(0, s0);
+    load_x(1, s0 + 1);
+    int ref[4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int r = 0; r < 4; ++r)
+      ref[r] = min(240, static_cast<int>(__shfl_sync(0xffffffffu, ld[0].byte[r], lane & 28)));
+    auto step = [&](int buf, int s) {
+      const int b = (s * KG + kg) * 4 + t;
+      // 2^(q - ref) in fp16, in range for -14 .. 13 (ref <= 240: a NaN's 255 is not)
+      uint32_t f[4];
+      bool far = false;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t d = ld[buf].byte[r] - ref[r] + 14;
+        far = far || d > 27u;
+        f[r] = d * 0x04000400u + 0x04000400u;
+      }
+      if (__any_sync(0xffffffffu, far)) {
+        far = false;   // a block of zeros needs no scale
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint4& v = ld[buf].v[r];
+          if (ld[buf].byte[r] - ref[r] + 14 > 27u) {
+            far = far || (v.x | v.y | v.z | v.w) != 0 || ld[buf].byte[r] == 255u;
+            f[r] = 0x3c003c00u;
+          }
+        }
+        far = __any_sync(0xffffffffu, far);
+      }
+      if (far) {
+        far_step<NT, EARLY>(ld[buf], x[buf], xf[buf], b, nb, ref, rows, acc);
+      } else {
+        uint32_t fxs[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) fxs[n] = EARLY ? 0u : row_factor(rows[n], b, nb);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t a[4][4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            decode(word(ld[buf].v[r], q), a[r]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[r][j] = mul2(a[r][j], f[r]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (n > 0 && !both) continue;
+            uint4 xv = EARLY ? x[buf][q % (EARLY ? 4 : 1)] : row_vec(rows[n], min(b, nb - 1), q);
+            const uint32_t fx = EARLY ? xf[buf] : fxs[n];
+            xv.x = mul2(xv.x, fx), xv.y = mul2(xv.y, fx), xv.z = mul2(xv.z, fx), xv.w = mul2(xv.w, fx);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              mma(acc[m][n], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], xv.x, xv.y);
+              mma(acc[m][n], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], xv.z, xv.w);
+            }
+          }
+        }
+      }
+      load_w(buf, s + 2);
+      load_x(buf, s + 2);
+    };
+    for (int s = s0; s < s1; s += 2) {
+      step(0, s);
+      if (s + 1 < s1) step(1, s + 1);
+    }
+    // the sums' powers of two: the columns' refs and the token rows' tops
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float t0 = mx_scale(__shfl_sync(0xffffffffu, rows[n].top, 8 * t));
+      const float t1 = mx_scale(__shfl_sync(0xffffffffu, rows[n].top, 8 * t + 4));
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
+        const float lo = mx_scale(ref[2 * m]), hi = mx_scale(ref[2 * m + 1]);
         float* d = red + (8 * n + 2 * t) * PITCH + 16 * m + g;
-        d[0] = acc[m][n][0], d[PITCH] = acc[m][n][1];
-        d[8] = acc[m][n][2], d[PITCH + 8] = acc[m][n][3];
+        d[0] = acc[m][n][0] * lo * t0, d[PITCH] = acc[m][n][1] * lo * t1;
+        d[8] = acc[m][n][2] * hi * t0, d[PITCH + 8] = acc[m][n][3] * hi * t1;
       }
-  }
-  template <int NT, bool X8, bool EARLY, bool LARGE>
-  static __device__ __forceinline__ void step(const uint4 (&v)[4], const uint32_t (&f)[4],
-                                              const RawBlock<X8>* x, int b, bool ok,
-                                              const Row<X8>* rows, float (&acc)[2][NT][4]) {
-    uint32_t f1[4], f2[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      f1[r] = ((LARGE ? min(f[r], 128u) : f[r]) + 126u) * 0x00800080u;
-      if (LARGE)
-        f2[r] = f[r] == 255u ? 0x7fc07fc0u : (f[r] > 128u ? (f[r] - 1u) * 0x00800080u : 0x3f803f80u);
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t xb[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint4 xv = EARLY ? x[n].bf16x8(q) : (ok ? rows[n].bf16x8(32 * b + 8 * q) : make_uint4(0, 0, 0, 0));
-        xb[n][0] = __byte_perm(xv.x, xv.z, 0x5410);   // values 0 and 4
-        xb[n][1] = __byte_perm(xv.x, xv.z, 0x7632);   // 1 and 5
-        xb[n][2] = __byte_perm(xv.y, xv.w, 0x5410);   // 2 and 6
-        xb[n][3] = __byte_perm(xv.y, xv.w, 0x7632);   // 3 and 7
-      }
-      uint32_t a[4][4];
+  }
+
+  // A step with far scales: the four lanes' blocks one after the other, codes as
+  // they are, each block's sums scaled by 2^(q - ref) in fp32.
+  template <int NT, bool EARLY>
+  static __device__ __forceinline__ void far_step(const Load& ld, const uint4* x, uint32_t xf, int b,
+                                                  int nb, const int (&ref)[4], const Row* rows,
+                                                  float (&acc)[2][NT][4]) {
+    const int lane = threadIdx.x & 31, t = lane & 3;
+#pragma unroll 1
+    for (int turn = 0; turn < 4; ++turn) {
+      float f[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const uint32_t wd = q == 0 ? v[r].x : (q == 1 ? v[r].y : (q == 2 ? v[r].z : v[r].w));
-        a[r][0] = mul2(spread<0>(wd), f1[r]);
-        a[r][1] = mul2(spread<1>(wd), f1[r]);
-        a[r][2] = mul2(spread<2>(wd), f1[r]);
-        a[r][3] = mul2(spread<3>(wd), f1[r]);
-        if (LARGE) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) a[r][j] = mul2(a[r][j], f2[r]);
-        }
+        const uint32_t byte = __shfl_sync(0xffffffffu, ld.byte[r], (lane & 28) | turn);
+        f[r] = byte == 255u ? __uint_as_float(0x7fc00000u) : ldexpf(1.f, static_cast<int>(byte) - ref[r]);
       }
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int n = 0; n < NT; ++n) {
+        float c[2][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma16816(acc[m][n], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], xb[n][0], xb[n][1]);
-          mma16816(acc[m][n], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], xb[n][2], xb[n][3]);
+        for (int m = 0; m < 2; ++m) c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
+        const uint32_t fx = EARLY ? xf : row_factor(rows[n], b, nb);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t a[4][4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) decode(t == turn ? word(ld.v[r], q) : 0u, a[r]);
+          uint4 xv = EARLY ? x[q] : row_vec(rows[n], min(b, nb - 1), q);
+          xv.x = mul2(xv.x, fx), xv.y = mul2(xv.y, fx), xv.z = mul2(xv.z, fx), xv.w = mul2(xv.w, fx);
+          if (t != turn) xv = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            mma(c[m], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], xv.x, xv.y);
+            mma(c[m], a[2 * m][2], a[2 * m + 1][2], a[2 * m][3], a[2 * m + 1][3], xv.z, xv.w);
+          }
         }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          acc[m][n][0] += c[m][0] * f[2 * m], acc[m][n][1] += c[m][1] * f[2 * m];
+          acc[m][n][2] += c[m][2] * f[2 * m + 1], acc[m][n][3] += c[m][3] * f[2 * m + 1];
+        }
+      }
     }
   }
 };
+
+// Values with a common scale of 2^p as fp16: p such that the largest magnitude (its
+// fp32 bits) lies in [2^14, 2^15).  Values down to 2^-29 of it keep bf16's bits;
+// smaller ones are rounded at 2^-39 of it.  Returns the scale's byte; 255 (NaN)
+// where one is an infinity or a NaN.
+__device__ __forceinline__ uint32_t half_block_byte(uint32_t amax_bits) {
+  if (amax_bits >= 0x7f800000u) return 255u;
+  return static_cast<uint32_t>(max(0, static_cast<int>(amax_bits >> 23) - 14));
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight values of e4m3 codes (times their block's scale) or bf16.
+template <bool X8>
+__device__ __forceinline__ void load_row8(const void* x, const uint8_t* x_scale, int64_t i, float (&v)[8]) {
+  if (!X8) {
+    load8(static_cast<const __nv_bfloat16*>(x) + 8 * i, v);
+    return;
+  }
+  const uint2 c = __ldg(static_cast<const uint2*>(x) + i);
+  const float f = mx_scale(__ldg(x_scale + (i >> 2)));
+  const uint32_t q[4] = {c.x, c.x >> 16, c.y, c.y >> 16};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 h = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>(q[j] & 0xffffu), __NV_E4M3)));
+    v[2 * j] = h.x * f, v[2 * j + 1] = h.y * f;
+  }
+}
+
+// e4m3 token rows in the storage type (bf16: exact but below its normal range).
+template <class S>
+__global__ void __launch_bounds__(256) few_rows_kernel(const void* __restrict__ x,
+                                                       const uint8_t* __restrict__ x_scale, int vecs,
+                                                       S* __restrict__ out) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= vecs) return;
+  float v[8];
+  load_row8<true>(x, x_scale, i, v);
+  store8(out + 8 * static_cast<int64_t>(i), v);
+}
+
+// Token rows, a block each, in fp16 with a power of two per row, for 4-bit weights.
+// Also clears what the gate_up kernel collects the activations' tops in.
+template <bool X8>
+__global__ void __launch_bounds__(256) few_half_rows_kernel(const void* __restrict__ x,
+                                                            const uint8_t* __restrict__ x_scale, int H,
+                                                            __half* __restrict__ out,
+                                                            int* __restrict__ top,
+                                                            int* __restrict__ act_top, int Tk) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ uint32_t part[8];
+  const int row = blockIdx.x, n = H / 8;
+  const int64_t base = static_cast<int64_t>(row) * n;
+  for (int i = row * 256 + threadIdx.x; i < Tk; i += gridDim.x * 256) act_top[i] = 0;
+  uint32_t amax = 0;
+  for (int i = threadIdx.x; i < n; i += 256) {
+    float v[8];
+    load_row8<X8>(x, x_scale, base + i, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
+  }
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) amax = max(amax, part[w]);
+  const uint32_t byte = half_block_byte(amax);
+  const float f = mx_inv_scale(byte);
+  for (int i = threadIdx.x; i < n; i += 256) {
+    float v[8];
+    load_row8<X8>(x, x_scale, base + i, v);
+    uint4 u;
+    u.x = pack_half(v[0] * f, v[1] * f), u.y = pack_half(v[2] * f, v[3] * f);
+    u.z = pack_half(v[4] * f, v[5] * f), u.w = pack_half(v[6] * f, v[7] * f);
+    reinterpret_cast<uint4*>(out)[base + i] = u;
+  }
+  if (threadIdx.x == 0) top[row] = static_cast<int>(byte);
+}
 
 // ------------------------------------------------------------------ kernels
 __device__ __forceinline__ float load_elem(const __nv_bfloat16* p, int64_t i) { return __bfloat162float(p[i]); }
@@ -642,27 +827,6 @@ struct Runs {
   }
 };
 
-// The products of one unit's share for `tiles` row tiles, in the smallest
-// instance that holds them.
-template <class W, int NT, bool X8>
-__device__ __forceinline__ void run_tiles(int tiles, const void* w, const uint8_t* scales, int64_t ld,
-                                          int col, int ncol, int K, int s0, int s1, int kg,
-                                          const Row<X8>* rows, int nrows, float* red) {
-  if constexpr (NT >= 4) {
-    if (tiles > 2) {
-      W::template run<4, X8>(w, scales, ld, col, ncol, K, s0, s1, kg, rows, nrows, red);
-      return;
-    }
-  }
-  if constexpr (NT >= 2) {
-    if (tiles > 1) {
-      W::template run<2, X8>(w, scales, ld, col, ncol, K, s0, s1, kg, rows, nrows, red);
-      return;
-    }
-  }
-  W::template run<1, X8>(w, scales, ld, col, ncol, K, s0, s1, kg, rows, nrows, red);
-}
-
 // Floats of `red`: the shares' results, or the 256 threads' sums of the combine.
 template <class W>
 __host__ __device__ __forceinline__ int red_floats(int rows) {
@@ -689,8 +853,20 @@ __device__ __forceinline__ void finish_gate_up(const FewArgs& a, const Plan& p, 
       gate += load_elem(b, a.interleaved ? 2 * feature : feature);
       up += load_elem(b, a.interleaved ? 2 * feature + 1 : a.I + feature);
     }
-    static_cast<S*>(a.act)[static_cast<int64_t>(p.slot[first + r]) * a.I + feature] =
-        static_cast<S>(activate(a, gate, up));
+    const float v = activate(a, gate, up);
+    const int64_t at = static_cast<int64_t>(p.slot[first + r]) * a.I + feature;
+    if constexpr (!W::kHalfRows) {
+      static_cast<S*>(a.act)[at] = static_cast<S>(v);
+    } else {
+      // a warp has the 32 values of one block (OUT and I are multiples of 32)
+      const uint32_t byte =
+          half_block_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu));
+      static_cast<__half*>(a.act)[at] = __float2half_rn(v * mx_inv_scale(byte));
+      if ((threadIdx.x & 31) == 0) {
+        a.act_scale[at >> 5] = static_cast<uint8_t>(byte);
+        if (byte != 255u) atomicMax(a.act_top + p.slot[first + r], static_cast<int>(byte));
+      }
+    }
   }
 }
 
@@ -786,15 +962,15 @@ __device__ __forceinline__ void combine_tile(const FewArgs& a, const Plan& p, co
 // experts with many rows and with few mix in every run.  A block counts itself in
 // at the end of its run, once, for the pieces at its two ends; the pieces between
 // are its own alone.
-template <class W, int PHASE, int NT, bool X8>
+template <class W, int PHASE, int NT>
 __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant__ FewArgs a) {
   using S = typename W::Store;
   constexpr int CW = W::FG * W::WF;            // weight columns of a unit
   const int UNIT = a.rows * CW;                // results of a unit, [row][column]
   const int SHARE = a.rows * W::PITCH;         // one share's results in shared memory
   constexpr int OUT = PHASE == 0 ? CW / 2 : CW;
-  extern __shared__ float4 red4[];
-  float* red = reinterpret_cast<float*>(red4);
+  extern __shared__ float4 dynamic[];          // results, plan
+  float* red = reinterpret_cast<float*>(dynamic);
   __shared__ PlanSmall ps;
   Plan p = plan_at(red + red_floats<W>(a.rows), a.T * a.k, a.E, a.rows);
 
@@ -811,8 +987,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   const int KS = (K + W::KG * W::STEP - 1) / (W::KG * W::STEP);
   const int chunks = p.chunks;
   const Runs runs(chunks * tiles * KS, gridDim.x);
-  if (PHASE == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (me >= runs.grid) {
+    wait_for_rows();
     // no row at all (every id out of range): y is still written
     if (PHASE == 1 && runs.grid == 0) {
       for (int64_t i = me * static_cast<int64_t>(kThreads) + tid; i < static_cast<int64_t>(a.T) * a.H;
@@ -826,6 +1002,18 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     return;
   }
   const int begin = runs.begin(me), end = runs.begin(me + 1);
+  // this warp's first weight column in a tile, and how many there are from it on
+  auto columns = [&](int tile, int* col, int* ncol) {
+    if (PHASE == 0 && !a.interleaved) {
+      constexpr int HALF = W::FG / 2;
+      const int o = tile * OUT + (fg % HALF) * W::WF;
+      *col = (fg / HALF) * a.I + o;
+      *ncol = a.I - o;
+    } else {
+      *col = tile * CW + fg * W::WF;
+      *ncol = N - *col;
+    }
+  };
 
   for (int s = begin; s < end;) {
     const int unit = s / KS;
@@ -835,42 +1023,39 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     const int chunk = unit % chunks, tile = unit / chunks;
     const int e = p.chunk_e[chunk], first = p.chunk_first[chunk], nrows = p.chunk_rows[chunk];
 
-    // this warp's columns
     int col, ncol;
-    if (PHASE == 0 && !a.interleaved) {
-      constexpr int HALF = W::FG / 2;
-      const int o = tile * OUT + (fg % HALF) * W::WF;
-      col = (fg / HALF) * a.I + o;
-      ncol = a.I - o;
-    } else {
-      col = tile * CW + fg * W::WF;
-      ncol = N - col;
+    columns(tile, &col, &ncol);
+    // the next unit's first steps, into L2: a unit starts with nothing in flight
+    if (u0 + ks1 < end) {
+      const int next = unit + 1;
+      int ncol_next, col_next;
+      columns(next / chunks, &col_next, &ncol_next);
+      W::prefetch(a.w, a.scales, static_cast<int64_t>(p.chunk_e[next % chunks]) * K * N, N, col_next,
+                  ncol_next, K, kg);
     }
     // the biases that the finishing block will want (128-byte lines)
     if (a.bias && lane == 0 && kg == 0 && ncol > 0)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const S*>(a.bias) + static_cast<int64_t>(e) * N + col));
-    Row<X8> rows[W::kRowPerLane ? NT : 8];
+      prefetch_l2(static_cast<const S*>(a.bias) + static_cast<int64_t>(e) * N + col);
+    Row rows[W::kRowPerLane ? NT : 8];
 #pragma unroll
     for (int i = 0; i < (W::kRowPerLane ? NT : 8); ++i) {
       const int r = W::kRowPerLane ? 8 * i + (lane >> 2) : i;
-      if (r < nrows) {
-        const int slot = p.slot[first + r];
-        const int64_t row = PHASE == 0 ? slot / a.k : slot;
-        if (X8) {
-          rows[i].p = static_cast<const uint8_t*>(a.x) + row * K;
-          rows[i].scale = a.x_scale + row * (K >> 5);
-        } else {
-          rows[i].p = static_cast<const S*>(a.x) + row * K;
-        }
+      const int slot = p.slot[first + (r < nrows ? r : 0)];
+      const int64_t row = PHASE == 0 ? slot / a.k : slot;
+      rows[i].p = static_cast<const S*>(a.x) + row * K;   // (fp16 rows: of the same size)
+      if (W::kHalfRows) {
+        if (PHASE == 1) rows[i].scale = a.x_scale + row * (K >> 5);
+        wait_for_rows();
+        rows[i].top = static_cast<int>(ld_u32(a.top + row));
       }
     }
     if (ncol > 0) {
       const int64_t we = static_cast<int64_t>(e) * K * N;   // weights of the experts before
       const void* w = sizeof(S) == 4 ? static_cast<const void*>(static_cast<const float*>(a.w) + we)
-                      : W::STEP == 128
+                      : W::kHalfRows
                           ? static_cast<const void*>(static_cast<const uint8_t*>(a.w) + we / 2)
                           : static_cast<const void*>(static_cast<const __nv_bfloat16*>(a.w) + we);
-      run_tiles<W, NT, X8>((nrows + 7) >> 3, w, W::STEP == 128 ? a.scales + we / 32 : nullptr, N, col,
+      W::template run<NT>(w, W::kHalfRows ? a.scales + we / 32 : nullptr, N, col,
                            ncol, K, ks0, ks1, kg, rows, nrows, red + kg * SHARE + fg * W::WF);
     }
     __syncthreads();
@@ -901,6 +1086,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       combine_tile<W>(a, p, runs, KS, tile, red);
     s = u0 + ks1;
   }
+
+  wait_for_rows();   // (warps without columns have not yet)
 
   // the pieces at the run's ends: piece 0 its first unit (tile), 1 its last
   const int per = PHASE == 0 ? KS : chunks * KS;       // steps of a unit (tile)
@@ -941,8 +1128,9 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   }
 }
 
-template <class W, int PHASE, int NT, bool X8>
-cudaError_t launch(const FewArgs& a, int grid, cudaStream_t st) {
+// `after`: may start while the kernel before it, which writes its rows, ends.
+template <class W, int PHASE, int NT>
+cudaError_t launch(const FewArgs& a, int grid, bool after, cudaStream_t st) {
   const int smem = red_floats<W>(a.rows) * 4 + plan_bytes(a.T * a.k, a.E, a.rows);
   const int most = red_floats<W>(8 * NT) * 4 + kMostPlanBytes;
   static std::atomic<uint64_t> ready{0};   // one bit per device
@@ -951,7 +1139,7 @@ cudaError_t launch(const FewArgs& a, int grid, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(few_kernel<W, PHASE, NT, X8>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    e = cudaFuncSetAttribute(few_kernel<W, PHASE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
@@ -964,27 +1152,45 @@ cudaError_t launch(const FewArgs& a, int grid, cudaStream_t st) {
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = PHASE == 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, few_kernel<W, PHASE, NT, X8>, a);
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, few_kernel<W, PHASE, NT>, a);
 }
 
-template <class W, int PHASE, bool X8>
-cudaError_t launch_nt(const FewArgs& a, int nt, int grid, cudaStream_t st) {
-  if constexpr (W::kRowPerLane) {
-    if (nt > 1) return launch<W, PHASE, 4, X8>(a, grid, st);
+template <class W, int PHASE>
+cudaError_t launch_nt(const FewArgs& a, int nt, int grid, bool after, cudaStream_t st) {
+  if constexpr (W::kMaxTiles > 1) {
+    if (nt > 1) return launch<W, PHASE, W::kMaxTiles>(a, grid, after, st);
   }
-  return launch<W, PHASE, 1, X8>(a, grid, st);
+  return launch<W, PHASE, 1>(a, grid, after, st);
 }
 
-// Row tiles of 8 tokens per unit, at most four (registers): as many as hold an
-// expert's rows when every token names it once, so its weights are read once.  A
-// unit runs only the tiles that its rows fill.
-int row_tiles(const moe_shape* s) {
-  return s->dtype == MOE_FP32 ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(4, (s->T + 7) / 8)));
+// x as the gate_up products want it; H % 32 == 0.
+cudaError_t launch_rows(const moe_shape* s, const void* x, const uint8_t* x_scale, bool half, void* out,
+                        int* top, int* act_top, cudaStream_t st) {
+  const int T = static_cast<int>(s->T), Tk = T * s->k;
+  const int vecs = T * (s->H / 8), grid = (vecs + 255) / 256;
+  if (half && x_scale)
+    few_half_rows_kernel<true><<<T, 256, 0, st>>>(x, x_scale, s->H, static_cast<__half*>(out), top, act_top, Tk);
+  else if (half)
+    few_half_rows_kernel<false><<<T, 256, 0, st>>>(x, x_scale, s->H, static_cast<__half*>(out), top, act_top, Tk);
+  else if (s->dtype == MOE_FP32)
+    few_rows_kernel<float><<<grid, 256, 0, st>>>(x, x_scale, vecs, static_cast<float*>(out));
+  else
+    few_rows_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(x, x_scale, vecs, static_cast<__nv_bfloat16*>(out));
+  return cudaGetLastError();
+}
+
+// Row tiles of 8 tokens per unit.  Two where an expert may have more than 8 rows,
+// so that its weights are read and decoded once for 16.  4-bit weights take two only
+// from 6 rows per expert on: the kernel for one tile has its tokens' loads ahead
+// and is the faster one where few experts have more than 8 rows.  fp32: one.
+int row_tiles(const moe_shape* s, bool mx) {
+  if (s->dtype == MOE_FP32 || s->T <= 8) return 1;
+  return mx && s->T * s->k < 6ll * s->E ? 1 : 2;
 }
 
 struct FewLayout {
-  size_t counters0, counters1, act, part, o, total;
+  size_t counters0, counters1, rows, top, act, act_scale, act_top, part, o, total;
 };
 FewLayout few_layout(const moe_shape* s) {
   FewLayout L;
@@ -997,8 +1203,12 @@ FewLayout few_layout(const moe_shape* s) {
   const size_t Tk = static_cast<size_t>(s->T) * s->k;
   L.counters0 = take(sizeof(unsigned) * kMaxGrid);
   L.counters1 = take(sizeof(unsigned) * ((s->H + 63) / 64));
+  L.rows = take((s->dtype == MOE_FP32 ? 4 : 2) * static_cast<size_t>(s->T) * s->H);
+  L.top = take(sizeof(int) * static_cast<size_t>(s->T));
+  L.act_top = take(sizeof(int) * Tk);
+  L.act_scale = take(Tk * (s->I / 32 + 1));
   L.act = take((s->dtype == MOE_FP32 ? 4 : 2) * Tk * s->I);
-  L.part = take(sizeof(float) * 2 * kMaxGrid * 128 * 8 * row_tiles(s));
+  L.part = take(sizeof(float) * 2 * kMaxGrid * 128 * 16);
   L.o = take(sizeof(float) * Tk * s->H);
   L.total = off;
   return L;
@@ -1062,6 +1272,9 @@ moe_status moe_ffn_few(const moe_shape* s, const void* x, const uint8_t* x_scale
   a.scales = mx ? mx->scales_gate_up : nullptr;
   a.bias = bias ? bias->b_gate_up : nullptr;
   a.act = base + L.act;
+  a.act_scale = reinterpret_cast<uint8_t*>(base + L.act_scale);
+  a.act_top = reinterpret_cast<int*>(base + L.act_top);
+  a.top = reinterpret_cast<const int*>(base + L.top);
   a.part = reinterpret_cast<float*>(base + L.part);
   a.o = reinterpret_cast<float*>(base + L.o);
   a.y = y;
@@ -1074,27 +1287,36 @@ moe_status moe_ffn_few(const moe_shape* s, const void* x, const uint8_t* x_scale
   a.out_fp32 = s->out_fp32;
   a.limit = s->clamp_limit;
   a.alpha = s->alpha;
-  const int nt = row_tiles(s);
+  const int nt = row_tiles(s, mx != nullptr);
   a.rows = 8 * nt;
 
-  cudaError_t e = abi_tracked(kAbiFewGateUp, 1, st, [&] {
-    if (s->dtype == MOE_FP32)
-      return x_scale ? launch_nt<F32, 0, true>(a, nt, grid, st) : launch_nt<F32, 0, false>(a, nt, grid, st);
-    if (mx)
-      return x_scale ? launch_nt<Mx, 0, true>(a, nt, grid, st) : launch_nt<Mx, 0, false>(a, nt, grid, st);
-    return x_scale ? launch_nt<Bf16, 0, true>(a, nt, grid, st) : launch_nt<Bf16, 0, false>(a, nt, grid, st);
+  cudaError_t e = cudaSuccess;
+  const bool convert = x_scale || mx;
+  if (convert) {
+    a.x = base + L.rows;
+    e = abi_tracked(kAbiFewRows, 1, st, [&] {
+      return launch_rows(s, x, x_scale, mx != nullptr, base + L.rows, reinterpret_cast<int*>(base + L.top),
+                         a.act_top, st);
+    });
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  e = abi_tracked(kAbiFewGateUp, 1, st, [&] {
+    if (s->dtype == MOE_FP32) return launch_nt<F32, 0>(a, nt, grid, convert, st);
+    if (mx) return launch_nt<Mx, 0>(a, nt, grid, convert, st);
+    return launch_nt<Bf16, 0>(a, nt, grid, convert, st);
   });
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   a.x = a.act;
-  a.x_scale = nullptr;
+  a.x_scale = a.act_scale;
+  a.top = a.act_top;
   a.w = mx ? mx->codes_down : w_down;
   a.scales = mx ? mx->scales_down : nullptr;
   a.bias = bias ? bias->b_down : nullptr;
   a.counters = reinterpret_cast<unsigned*>(base + L.counters1);
   e = abi_tracked(kAbiFewDown, 1, st, [&] {
-    if (s->dtype == MOE_FP32) return launch_nt<F32, 1, false>(a, nt, grid, st);
-    if (mx) return launch_nt<Mx, 1, false>(a, nt, grid, st);
-    return launch_nt<Bf16, 1, false>(a, nt, grid, st);
+    if (s->dtype == MOE_FP32) return launch_nt<F32, 1>(a, nt, grid, true, st);
+    if (mx) return launch_nt<Mx, 1>(a, nt, grid, true, st);
+    return launch_nt<Bf16, 1>(a, nt, grid, true, st);
   });
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
