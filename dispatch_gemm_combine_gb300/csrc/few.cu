@@ -313,9 +313,9 @@ struct Row {
 // bf16 weights [K, ld], columns innermost.  A lane loads 16 bytes (8 columns) of
 // four rows of the contraction; pairs along the contraction, as the instruction
 // wants them, come from two rows by byte permutes.  Columns 2 i and 2 i + 1 of
-// the lane are rows g and g + 8 of instruction i.  Past the contraction's end the
-// tokens are zero and the weights any valid ones; columns past the end and rows
-// that a unit does not have are computed from others' and never read.
+// the lane are rows g and g + 8 of instruction i.  Past the contraction's end both
+// are zero; columns past the end and rows that a unit does not have are computed
+// from others' and never read.
 struct Bf16 {
   using Store = __nv_bfloat16;
   static constexpr int WF = 64, FG = 2, KG = 4, STEP = 16;
@@ -323,12 +323,6 @@ struct Bf16 {
   static constexpr bool kHalfRows = false;
   static constexpr bool kRowPerLane = true;   // lane (g, t) reads rows g, g + 8, ...
   static constexpr int kMaxTiles = 2;
-  // A unit's first two steps of this warp: 16 rows of 128 bytes each.
-  static __device__ __forceinline__ void prefetch(const void* w, const uint8_t*, int64_t first, int64_t ld,
-                                                  int col, int ncol, int K, int kg) {
-    const int lane = threadIdx.x & 31, k = ((lane >> 4) * KG + kg) * STEP + (lane & 15);
-    if (ncol > 0 && k < K) prefetch_l2(static_cast<const __nv_bfloat16*>(w) + first + k * ld + col);
-  }
   template <int NT>
   static __device__ __forceinline__ void run(const void* w, const uint8_t*, int64_t ld, int col,
                                              int ncol, int K, int s0, int s1, int kg,
@@ -348,28 +342,28 @@ struct Bf16 {
     uint2 xb[2][U][NT];
     auto load_w = [&](int buf, int s) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (s + u < s1) {
-          const __nv_bfloat16* p = base + min(((s + u) * KG + kg) * STEP + 4 * t, K - 4) * ld;
+      for (int u = 0; u < U; ++u) {
+        const int k = ((s + u) * KG + kg) * STEP + 4 * t;
+        const bool ok = s + u < s1 && k < K;
+        const __nv_bfloat16* p = base + k * ld;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) v[buf][u][r] = ldg_stream(p + r * ld);
-        }
+        for (int r = 0; r < 4; ++r) v[buf][u][r] = ok ? ldg_stream(p + r * ld) : make_uint4(0, 0, 0, 0);
+      }
     };
     auto load_x = [&](int buf, int s) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (s + u < s1) {
-          const int k = ((s + u) * KG + kg) * STEP + 4 * t;
+      for (int u = 0; u < U; ++u) {
+        const int k = ((s + u) * KG + kg) * STEP + 4 * t;
+        const bool ok = s + u < s1 && k < K;
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            if (n == 0 || both)
-              xb[buf][u][n] = k < K ? ld_u64(static_cast<const __nv_bfloat16*>(rows[n].p) + k) : make_uint2(0, 0);
-        }
+        for (int n = 0; n < NT; ++n)
+          if (n == 0 || both)
+            xb[buf][u][n] = ok ? ld_u64(static_cast<const __nv_bfloat16*>(rows[n].p) + k) : make_uint2(0, 0);
+      }
     };
-    auto multiply = [&](int buf, int s) {
+    auto multiply = [&](int buf) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (s + u >= s1) continue;
         const uint32_t* w0 = &v[buf][u][0].x;
         const uint32_t* w1 = &v[buf][u][1].x;
         const uint32_t* w2 = &v[buf][u][2].x;
@@ -390,10 +384,10 @@ struct Bf16 {
     for (int s = s0; s < s1; s += 2 * U) {
       load_w(1, s + U);
       load_x(1, s + U);
-      multiply(0, s);
+      multiply(0);
       load_w(0, s + 2 * U);
       load_x(0, s + 2 * U);
-      multiply(1, s + U);
+      multiply(1);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -415,8 +409,6 @@ struct F32 {
   static constexpr bool kHalfRows = false;
   static constexpr bool kRowPerLane = false;   // every lane reads all rows
   static constexpr int kMaxTiles = 1;
-  static __device__ __forceinline__ void prefetch(const void*, const uint8_t*, int64_t, int64_t, int, int,
-                                                  int, int) {}
   template <int NT>
   static __device__ __forceinline__ void run(const void* w, const uint8_t*, int64_t ld, int col,
                                              int ncol, int K, int s0, int s1, int kg,
@@ -531,17 +523,6 @@ struct Mx {
     return ld_u128(static_cast<const __half*>(r.p) + 32 * b + 8 * q);
   }
 
-  // A unit's first two steps of this warp: 64 bytes of 32 columns each.
-  static __device__ __forceinline__ void prefetch(const void* w, const uint8_t* scales, int64_t first, int64_t,
-                                                  int col, int ncol, int K, int kg) {
-    const int lane = threadIdx.x & 31;
-    if (lane >= ncol) return;
-    const int64_t c = col + lane;
-    const uint8_t* p = static_cast<const uint8_t*>(w) + first / 2 + c * (K >> 1);
-    prefetch_l2(scales + first / 32 + c * (K >> 5));
-    if (kg * 64 < K / 2) prefetch_l2(p + kg * 64);
-    if ((KG + kg) * 64 < K / 2) prefetch_l2(p + (KG + kg) * 64);
-  }
   template <int NT>
   static __device__ __forceinline__ void run(const void* w, const uint8_t* scales, int64_t, int col,
                                              int ncol, int K, int s0, int s1, int kg,
@@ -1025,14 +1006,6 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
 
     int col, ncol;
     columns(tile, &col, &ncol);
-    // the next unit's first steps, into L2: a unit starts with nothing in flight
-    if (u0 + ks1 < end) {
-      const int next = unit + 1;
-      int ncol_next, col_next;
-      columns(next / chunks, &col_next, &ncol_next);
-      W::prefetch(a.w, a.scales, static_cast<int64_t>(p.chunk_e[next % chunks]) * K * N, N, col_next,
-                  ncol_next, K, kg);
-    }
     // the biases that the finishing block will want (128-byte lines)
     if (a.bias && lane == 0 && kg == 0 && ncol > 0)
       prefetch_l2(static_cast<const S*>(a.bias) + static_cast<int64_t>(e) * N + col);
