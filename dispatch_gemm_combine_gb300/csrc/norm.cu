@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kMaxVec = 4;                       // 8-column vectors per thread
 constexpr int kMaxH = 1024 * 8 * kMaxVec;
-constexpr int kBwdBlocksPerSm = 2;
+constexpr int kBwdThreadsPerSm = 1024;
 
 template <typename E, bool OUT8, int V>
 __global__ void __launch_bounds__(1024) norm_fwd_kernel(
@@ -65,6 +65,15 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(
       for (int j = 0; j < 8; ++j) ss = fmaf(r[i][j], r[i][j], ss);
     }
   }
+  // the weight before the barrier, where registers allow: one latency less
+  constexpr bool EARLY = V < 4;
+  float w[EARLY ? V : 1][8];
+  if (EARLY)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (threadIdx.x + i * blockDim.x) * 8;
+      if (c < H) load8(weight + c, w[i % (EARLY ? V : 1)]);
+    }
   ss = block_sum(ss, part);
   const float rstd = 1.f / sqrtf(ss / static_cast<float>(H) + eps);
   if (rstd_out && threadIdx.x == 0) rstd_out[row] = rstd;
@@ -74,10 +83,10 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(
     if (!OUT8 && c >= H) continue;
     float o[8];
     if (c < H) {
-      float w[8];
-      load8(weight + c, w);
+      float* wi = w[i % (EARLY ? V : 1)];
+      if (!EARLY) load8(weight + c, wi);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = r[i][j] * rstd * w[j];
+      for (int j = 0; j < 8; ++j) o[j] = r[i][j] * rstd * wi[j];
     }
     if (!OUT8) {
       store8(static_cast<E*>(y) + base + c, o);
@@ -111,44 +120,85 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(
   }
 }
 
-template <typename E, int V>
-__global__ void __launch_bounds__(1024) norm_bwd_kernel(
+// Eight elements as they lie in memory.
+template <typename E>
+struct Raw8 {
+  uint4 u[sizeof(E) / 2];
+  __device__ __forceinline__ void load(const E* p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(E) / 2); ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ float get(int j) const {
+    const uint32_t* w = &u[0].x;
+    if (sizeof(E) == 4) return __uint_as_float(w[j]);
+    return j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
+  }
+};
+
+// The next row's loads are issued before the current row's sum (AHEAD; not where a
+// thread has so many columns that the registers would not hold them).
+template <typename E, int V, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_bwd_kernel(
     const E* __restrict__ dy, const E* __restrict__ d_total, const E* __restrict__ total,
     const float* __restrict__ rstd_in, const E* __restrict__ weight, int64_t T, int H,
     E* __restrict__ dx, float* __restrict__ dw_part) {
+  constexpr bool AHEAD = V * sizeof(E) <= (THREADS <= 512 ? 4 : 2);
   __shared__ float part[2][32];
-  float dw[V][8], w[V][8];
+  float dw[V][8];
+  constexpr bool KEEP = V < 4;   // the weight in registers
+  Raw8<E> w[KEEP ? V : 1], g[V], r[V], e[V], g1[AHEAD ? V : 1], r1[AHEAD ? V : 1], e1[AHEAD ? V : 1];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = (threadIdx.x + i * blockDim.x) * 8;
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
-    if (c < H) load8(weight + c, w[i]);
+    if (KEEP && c < H) w[i % (KEEP ? V : 1)].load(weight + c);
   }
+  auto load = [&](int64_t row, Raw8<E>* gd, Raw8<E>* rd, Raw8<E>* ed) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (threadIdx.x + i * blockDim.x) * 8;
+      if (c < H) {
+        gd[i].load(dy + row * H + c);
+        rd[i].load(total + row * H + c);
+        if (d_total) ed[i].load(d_total + row * H + c);
+      }
+    }
+  };
   int flip = 0;   // a row's barrier also separates the reuse of the other buffer
+  float rstd1 = 0.f;
+  if (AHEAD) {
+    load(blockIdx.x, g1, r1, e1);
+    rstd1 = __ldg(rstd_in + blockIdx.x);
+  }
   for (int64_t row = blockIdx.x; row < T; row += gridDim.x, flip ^= 1) {
     const int64_t base = row * H;
-    const float rstd = __ldg(rstd_in + row);
-    float g[V][8], xh[V][8];
+    float rstd;
+    if (AHEAD) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) g[i] = g1[i % (AHEAD ? V : 1)], r[i] = r1[i % (AHEAD ? V : 1)], e[i] = e1[i % (AHEAD ? V : 1)];
+      rstd = rstd1;
+      const int64_t next = row + gridDim.x;
+      if (next < T) {
+        load(next, g1, r1, e1);
+        rstd1 = __ldg(rstd_in + next);
+      }
+    } else {
+      load(row, g, r, e);
+      rstd = __ldg(rstd_in + row);
+    }
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = (threadIdx.x + i * blockDim.x) * 8;
       if (c < H) {
-        load8(dy + base + c, g[i]);
-        load8(total + base + c, xh[i]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
-      if (c < H) {
+        Raw8<E>& wi = w[i % (KEEP ? V : 1)];
+        if (!KEEP) wi.load(weight + c);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          xh[i][j] *= rstd;
-          dw[i][j] = fmaf(g[i][j], xh[i][j], dw[i][j]);
-          g[i][j] *= w[i][j];
-          dot = fmaf(g[i][j], xh[i][j], dot);
+          const float gj = g[i].get(j), xh = r[i].get(j) * rstd;
+          dw[i][j] = fmaf(gj, xh, dw[i][j]);
+          dot = fmaf(gj * wi.get(j), xh, dot);
         }
       }
     }
@@ -158,13 +208,12 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(
       const int c = (threadIdx.x + i * blockDim.x) * 8;
       if (c < H) {
         float o[8];
+        Raw8<E>& wi = w[i % (KEEP ? V : 1)];
+        if (!KEEP) wi.load(weight + c);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = rstd * (g[i][j] - xh[i][j] * mean);
-        if (d_total) {
-          float b[8];
-          load8(d_total + base + c, b);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] += b[j];
+        for (int j = 0; j < 8; ++j) {
+          o[j] = rstd * (g[i].get(j) * wi.get(j) - r[i].get(j) * rstd * mean);
+          if (d_total) o[j] += e[i].get(j);
         }
         store8(dx + base + c, o);
       }
@@ -208,9 +257,9 @@ RowShape row_shape(int H) {
   return {((n + v - 1) / v + 31) / 32 * 32, v};
 }
 
+// As many blocks as stay resident: a block's sums are written and read once more.
 int bwd_blocks(int64_t T, int H, int sms) {
-  const int threads = row_shape(H).threads;
-  const int per_sm = std::max(1, std::min(8, 1024 * kBwdBlocksPerSm / threads));
+  const int per_sm = std::max(1, std::min(8, kBwdThreadsPerSm / row_shape(H).threads));
   return static_cast<int>(std::min<int64_t>(T, static_cast<int64_t>(sms) * per_sm));
 }
 
@@ -233,12 +282,14 @@ cudaError_t launch_bwd(const E* dy, const E* d_total, const E* total, const floa
                        const E* weight, int64_t T, int H, E* dx, float* part, int blocks,
                        cudaStream_t st) {
   const RowShape s = row_shape(H);
-  if (s.vecs == 1)
-    norm_bwd_kernel<E, 1><<<blocks, s.threads, 0, st>>>(dy, d_total, total, rstd, weight, T, H, dx, part);
+  if (s.threads <= 512)   // then one vector each
+    norm_bwd_kernel<E, 1, 512><<<blocks, s.threads, 0, st>>>(dy, d_total, total, rstd, weight, T, H, dx, part);
+  else if (s.vecs == 1)
+    norm_bwd_kernel<E, 1, 1024><<<blocks, s.threads, 0, st>>>(dy, d_total, total, rstd, weight, T, H, dx, part);
   else if (s.vecs == 2)
-    norm_bwd_kernel<E, 2><<<blocks, s.threads, 0, st>>>(dy, d_total, total, rstd, weight, T, H, dx, part);
+    norm_bwd_kernel<E, 2, 1024><<<blocks, s.threads, 0, st>>>(dy, d_total, total, rstd, weight, T, H, dx, part);
   else
-    norm_bwd_kernel<E, 4><<<blocks, s.threads, 0, st>>>(dy, d_total, total, rstd, weight, T, H, dx, part);
+    norm_bwd_kernel<E, 4, 1024><<<blocks, s.threads, 0, st>>>(dy, d_total, total, rstd, weight, T, H, dx, part);
   return cudaGetLastError();
 }
 
