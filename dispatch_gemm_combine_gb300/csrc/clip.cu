@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(
     ClipState* state, float* out) {
   __shared__ Sums part[kThreads / 32];
   __shared__ bool last;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Sums s{0, 0, 0};
   const int chunks = t.chunk0[t.count];
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
@@ -227,8 +228,9 @@ __device__ __forceinline__ void scale_chunk(const E* p, E* d, int n, bool vec, f
 }
 
 __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ GradTable t,
-                                                              const float* __restrict__ norm) {
-  const float c = __ldg(norm + 1);
+                                                              const float* norm) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the factor is there
+  const float c = __ldcg(norm + 1);
   const int chunks = t.chunk0[t.count];
   for (int r = blockIdx.x; r < chunks; r += gridDim.x) {
     const int ch = chunks - 1 - r;
@@ -354,12 +356,22 @@ moe_status moe_grad_clip(const moe_grad_t* grads, int64_t n, float max_norm, flo
     first += grid;
   }
   if (!scale) return MOE_OK;
+  int i_scaled = 0;
   for (int64_t i = 0; i < n;) {
     i = fill_table(grads, n, i, &t);
     if (!t.count) continue;
+    // (the first may start while the norm's last blocks end)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid_of(t, sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = i_scaled++ == 0 ? 1 : 0;
     const cudaError_t e = abi_tracked(kAbiGradScale, 1, st, [&] {
-      grad_scale_kernel<<<grid_of(t, sms), kThreads, 0, st>>>(t, norm_out);
-      return cudaGetLastError();
+      return cudaLaunchKernelEx(&cfg, grad_scale_kernel, t, static_cast<const float*>(norm_out));
     });
     if (e != cudaSuccess) return MOE_ERR_CUDA;
   }

@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(
     E* __restrict__ dx, float* __restrict__ dw_part) {
   extern __shared__ uint4 ring_mem[];
   __shared__ float part[2][32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   RowRing<E, 3, V, D> rows{ring_mem, {dy, total, d_total}, H};
 #pragma unroll
   for (int d = 0; d < D - 1; ++d) rows.issue(d, blockIdx.x + static_cast<int64_t>(d) * gridDim.x, T);
@@ -261,8 +262,10 @@ __global__ void __launch_bounds__(1024) norm_dweight_kernel(const float* __restr
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float a = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the sums are there
   if (c < H)
-    for (int b = grp; b < blocks; b += 32) a += part[static_cast<int64_t>(b) * H + c];
+#pragma unroll 8
+    for (int b = grp; b < blocks; b += 32) a += __ldcg(part + static_cast<int64_t>(b) * H + c);
   s[grp][lane] = a;
   __syncthreads();
   const float v = warp_sum(s[lane][grp]);
@@ -459,8 +462,17 @@ moe_status moe_rms_norm_bwd(int64_t T, int32_t H, int32_t dtype, const void* dy,
     cudaError_t r = dtype == MOE_FP32 ? go(static_cast<const float*>(dy))
                                       : go(static_cast<const __nv_bfloat16*>(dy));
     if (r == cudaSuccess && dweight) {
-      norm_dweight_kernel<<<(H + 31) / 32, 1024, 0, st>>>(part, blocks, H, dweight);
-      r = cudaGetLastError();
+      // (may start while the last rows are done)
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((H + 31) / 32);
+      cfg.blockDim = dim3(1024);
+      cfg.stream = st;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      at[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      r = cudaLaunchKernelEx(&cfg, norm_dweight_kernel, static_cast<const float*>(part), blocks, H, dweight);
     }
     return r;
   });
