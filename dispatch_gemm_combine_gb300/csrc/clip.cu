@@ -10,8 +10,9 @@
 // device memory and a captured graph holds its own copy.
 //
 // The sum: each thread squares and adds the few dozen values of one chunk in
-// fp32, then adds that to a double; blocks and the final sum stay in double, in
-// a fixed order (the last block to finish adds all blocks' sums by index).
+// fp32; from there on sums are pairs of fp32 values (the sum and what it rounded
+// off), in a fixed order: the last block to finish adds all blocks' sums by index.
+// (Doubles in their place take 2 us more on a short list: this GPU adds few a clock.)
 // Squares of fp32 values leave fp32's range beyond 2^64 and below 2^-63, so
 // three sums run side by side, of g^2, (2^-80 g)^2 and (2^80 g)^2, and the
 // final step takes the one in range; the arithmetic is a tenth of what the
@@ -47,20 +48,32 @@ struct ClipState {
   unsigned done;            // blocks that have stored their sums; 0 between calls
 };
 
-struct Sums {
-  double mid, big, small;
+// A sum as its rounded value and the rest.
+struct Pair {
+  float hi, lo;
 };
+__device__ __forceinline__ Pair operator+(const Pair& a, const Pair& b) {
+  const float s = a.hi + b.hi;
+  if (!isfinite(s)) return {s, 0.f};
+  const float v = s - a.hi;
+  const float e = ((a.hi - (s - v)) + (b.hi - v)) + (a.lo + b.lo);
+  const float hi = s + e;
+  return {hi, e - (hi - s)};
+}
+struct Sums {
+  Pair mid, big, small;
+};
+__device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) {
+  return {a.mid + b.mid, a.big + b.big, a.small + b.small};
+}
 
+// The whole warp asks for the same chunk; a lane looks at every 32nd tensor (one
+// round of loads in place of a search's seven, each waiting for the one before).
 __device__ __forceinline__ int tensor_of_chunk(const GradTable& t, int chunk) {
-  int lo = 0, hi = t.count - 1;
-  while (lo < hi) {
-    const int m = (lo + hi + 1) >> 1;
-    if (t.chunk0[m] <= chunk)
-      lo = m;
-    else
-      hi = m - 1;
-  }
-  return lo;
+  int k = 0;
+  for (int i = threadIdx.x & 31; i - static_cast<int>(threadIdx.x & 31) < t.count; i += 32)
+    k += __popc(__ballot_sync(0xffffffffu, i < t.count && t.chunk0[i + 1] <= chunk));
+  return k;
 }
 
 struct Acc {
@@ -123,24 +136,28 @@ __device__ __forceinline__ void sum_chunk(const E* p, int n, bool vec, Acc& acc)
   for (int i = done + threadIdx.x; i < n; i += kThreads) acc.add(elem(p, i));
 }
 
-__device__ __forceinline__ double warp_sum_d(double v) {
+__device__ __forceinline__ Pair warp_sum(Pair v) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  for (int d = 16; d > 0; d >>= 1)
+    v = v + Pair{__shfl_xor_sync(0xffffffffu, v.hi, d), __shfl_xor_sync(0xffffffffu, v.lo, d)};
   return v;
 }
 
 // Sum over the block in a fixed order; valid in thread 0.
 __device__ __forceinline__ Sums block_sums(Sums v, Sums* part) {
-  v.mid = warp_sum_d(v.mid), v.big = warp_sum_d(v.big), v.small = warp_sum_d(v.small);
-  const int lane = threadIdx.x & 31;
+  v = {warp_sum(v.mid), warp_sum(v.big), warp_sum(v.small)};
   __syncthreads();
-  if (lane == 0) part[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
-  Sums r{0, 0, 0};
   if (threadIdx.x == 0)
-    for (int w = 0; w < kThreads / 32; ++w)
-      r.mid += part[w].mid, r.big += part[w].big, r.small += part[w].small;
-  return r;
+    for (int w = 1; w < kThreads / 32; ++w) v = v + part[w];
+  return v;
+}
+
+// sqrt(v) with the rest taken in: one step of Newton's iteration on fp32's root.
+__device__ __forceinline__ float root(const Pair& v) {
+  const float s = sqrtf(v.hi);
+  return s > 0.f && isfinite(s) ? s + (fmaf(-s, s, v.hi) + v.lo) / (2.f * s) : s;
 }
 
 // `first`: this launch's place in the blocks' sums; `blocks_all`: the blocks of
@@ -151,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(
   __shared__ Sums part[kThreads / 32];
   __shared__ bool last;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Sums s{0, 0, 0};
+  Sums s{};
   const int chunks = t.chunk0[t.count];
   for (int c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int k = tensor_of_chunk(t, c);
@@ -162,36 +179,38 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(
       sum_chunk(static_cast<const __nv_bfloat16*>(t.src[k]) + i0, n, t.vec[k], a);
     else
       sum_chunk(static_cast<const float*>(t.src[k]) + i0, n, t.vec[k], a);
-    s.mid += a.mid, s.big += a.big, s.small += a.small;
+    s = s + Sums{{a.mid, 0.f}, {a.big, 0.f}, {a.small, 0.f}};
   }
   const Sums b = block_sums(s, part);
   if (threadIdx.x == 0) {
     sums[first + blockIdx.x] = b;
-    __threadfence();
-    last = atomicAdd(&state->done, 1u) == static_cast<unsigned>(blocks_all - 1);
+    unsigned old;   // after the sums' store, before the other blocks' are read
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(&state->done) : "memory");
+    last = old == static_cast<unsigned>(blocks_all - 1);
   }
   __syncthreads();
   if (!last) return;
-  __threadfence();
-  Sums v{0, 0, 0};
+  Sums v{};
   for (int i = threadIdx.x; i < blocks_all; i += kThreads) {
-    v.mid += __ldcg(&sums[i].mid), v.big += __ldcg(&sums[i].big), v.small += __ldcg(&sums[i].small);
+    const float2* q = reinterpret_cast<const float2*>(sums + i);
+    const float2 m = __ldcg(q), b2 = __ldcg(q + 1), s2 = __ldcg(q + 2);
+    v = v + Sums{{m.x, m.y}, {b2.x, b2.y}, {s2.x, s2.y}};
   }
   v = block_sums(v, part);
   if (threadIdx.x == 0) {
     state->done = 0;
     // |g| <= 2^-20 throughout where the middle sum is below 2^-40, so the
     // scaled-up squares stay in range there
-    double norm;
-    if (!isfinite(v.mid))
-      norm = sqrt(v.big) * 0x1p80;
-    else if (v.mid < 0x1p-40)
-      norm = sqrt(v.small) * 0x1p-80;
+    float norm;
+    if (!isfinite(v.mid.hi))
+      norm = root(v.big) * 0x1p80f;
+    else if (v.mid.hi < 0x1p-40f)
+      norm = root(v.small) * 0x1p-80f;
     else
-      norm = sqrt(v.mid);
-    const double c = static_cast<double>(max_norm) / (norm + 1e-6);
-    out[0] = static_cast<float>(norm);
-    out[1] = isfinite(norm) && c < 1.0 ? static_cast<float>(c) : 1.f;
+      norm = root(v.mid);
+    const float c = max_norm / (norm + 1e-6f);
+    out[0] = norm;
+    out[1] = isfinite(norm) && c < 1.f ? c : 1.f;
   }
 }
 
