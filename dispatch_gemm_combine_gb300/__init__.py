@@ -291,9 +291,11 @@ def _ptr(t):
 
 
 def _stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    # the raw handle of torch.cuda.current_stream(), without the Stream object
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check(status, where):
@@ -403,11 +405,11 @@ def _dense(where, name, t, shape, dtype):
     writes: this shape and dtype, dense and row-major, on the GPU.  None passes."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError("%s: %s must be a dense %s tensor of shape %s on the GPU, got %s %s%s" % (
-            where, name, dtype, tuple(shape), t.dtype, tuple(t.shape),
-            "" if t.is_contiguous() else " (strided)"))
-    return t.data_ptr()
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.shape == shape:
+        return t.data_ptr()
+    raise ValueError("%s: %s must be a dense %s tensor of shape %s on the GPU, got %s %s%s" % (
+        where, name, dtype, tuple(shape), t.dtype, tuple(t.shape),
+        "" if t.is_contiguous() else " (strided)"))
 
 
 def rms_norm_workspace(T, H, device="cuda"):
