@@ -9,8 +9,8 @@ library's kernels.
 import torch
 
 from . import (MOE_BF16, MOE_FP32, Shape, alloc_plan, bias_struct, check_device_error, ffn_bwd,
-               ffn_few, ffn_fwd, few_workspace, moe_saved_size, mx_alloc, mx_quantize, mx_struct,
-               plan, route, workspace)
+               ffn_few, ffn_fwd, few_workspace, grad_clip, grad_clip_workspace, grad_table,
+               moe_saved_size, mx_alloc, mx_quantize, mx_struct, plan, route, workspace)
 
 _TORCH_DTYPE = {MOE_BF16: torch.bfloat16, MOE_FP32: torch.float32}
 
@@ -106,6 +106,21 @@ class LayerRunner:
                 self.dx, self.d_topk_w, self.dw_gate_up, self.dw_down, ws, stream, bias)
         out = (self.dx, self.d_topk_w, self.dw_gate_up, self.dw_down)
         return out + (self.db_gate_up, self.db_down) if with_bias else out
+
+    def clip_grads(self, max_norm, extra=(), stream=None):
+        """Scale the last backward's weight gradients (and bias gradients, where it
+        gave them), with those of `extra` (tensors), so that their global norm is at
+        most max_norm, in place.  Returns (norm before, factor) as a tensor [2]."""
+        grads = [self.dw_gate_up, self.dw_down]
+        if getattr(self, "db_gate_up", None) is not None:
+            grads += [self.db_gate_up, self.db_down]
+        table = grad_table(grads + list(extra))
+        ws = getattr(self, "ws_clip", None)
+        if ws is None or self.clip_count < table.count:
+            self.ws_clip, self.clip_count = grad_clip_workspace(table, self.device), table.count
+            self.clip_norm = torch.empty(2, dtype=torch.float32, device=self.device)
+        grad_clip(table, max_norm, self.clip_norm, self.ws_clip, stream)
+        return self.clip_norm
 
     def check(self, stream=None):
         for ws in (self.ws_plan, self.ws_fwd, self.ws_bwd, getattr(self, "ws_bwd_recompute", None),
