@@ -45,6 +45,7 @@ constexpr int kMaxSlots = kMaxTokens * 32;   // k <= 32
 constexpr int kMaxE = 1024;
 constexpr int kMaxChunks = kMaxE + kMaxSlots / 8;
 constexpr int kMaxGrid = 512;
+constexpr int kPrefetchSteps = 6;
 constexpr int kNowhere = 0xffff;
 // the largest plan_bytes(): every chunk, slot and expert there can be
 constexpr int kMostPlanBytes = 4 * kMaxChunks + 4 * kMaxE + 6 * kMaxChunks + 4 * kMaxSlots + 64;
@@ -58,6 +59,9 @@ struct FewArgs {
   const void* w;           // this kernel's weights, or codes
   const uint8_t* scales;   // the codes' scale bytes
   const void* bias;        // this kernel's bias, or null
+  const void* w_next;      // gate_up: the down kernel's weights and bias
+  const uint8_t* scales_next;
+  const void* bias_next;
   void* act;               // [Tk, I]: storage type; fp16 with 4-bit weights, and
   uint8_t* act_scale;      // [Tk, I/32] its blocks' scale bytes, and
   int* act_top;            // [Tk] the largest of each row's
@@ -323,6 +327,13 @@ struct Bf16 {
   static constexpr bool kHalfRows = false;
   static constexpr bool kRowPerLane = true;   // lane (g, t) reads rows g, g + 8, ...
   static constexpr int kMaxTiles = 2;
+  // The weights of step s of a unit, all columns: 64 rows of two 128-byte lines.
+  static __device__ __forceinline__ void prefetch(const void* w, const uint8_t*, int64_t first, int64_t ld,
+                                                  int col, int K, int s) {
+    const int k = s * KG * STEP + (threadIdx.x >> 1), c = col + (threadIdx.x & 1) * 64;
+    if (threadIdx.x < 2 * KG * STEP && k < K && c < ld)
+      prefetch_l2(static_cast<const __nv_bfloat16*>(w) + first + k * ld + c);
+  }
   template <int NT>
   static __device__ __forceinline__ void run(const void* w, const uint8_t*, int64_t ld, int col,
                                              int ncol, int K, int s0, int s1, int kg,
@@ -409,6 +420,12 @@ struct F32 {
   static constexpr bool kHalfRows = false;
   static constexpr bool kRowPerLane = false;   // every lane reads all rows
   static constexpr int kMaxTiles = 1;
+  static __device__ __forceinline__ void prefetch(const void* w, const uint8_t*, int64_t first, int64_t ld,
+                                                  int col, int K, int s) {
+    const int k = s * KG * STEP + (threadIdx.x >> 1), c = col + (threadIdx.x & 1) * 32;
+    if (threadIdx.x < 2 * KG * STEP && k < K && c < ld)
+      prefetch_l2(static_cast<const float*>(w) + first + k * ld + c);
+  }
   template <int NT>
   static __device__ __forceinline__ void run(const void* w, const uint8_t*, int64_t ld, int col,
                                              int ncol, int K, int s0, int s1, int kg,
@@ -523,6 +540,16 @@ struct Mx {
     return ld_u128(static_cast<const __half*>(r.p) + 32 * b + 8 * q);
   }
 
+  // The codes of step s of a unit, 128 bytes of each of 128 columns, and the line
+  // of their scales.
+  static __device__ __forceinline__ void prefetch(const void* w, const uint8_t* scales, int64_t first,
+                                                  int64_t ld, int col, int K, int s) {
+    const int64_t c = col + threadIdx.x;
+    const int b = s * KG * STEP;
+    if (threadIdx.x >= FG * WF || c >= ld || b >= K) return;
+    prefetch_l2(static_cast<const uint8_t*>(w) + first / 2 + c * (K >> 1) + b / 2);
+    prefetch_l2(scales + first / 32 + c * (K >> 5) + b / 32);
+  }
   template <int NT>
   static __device__ __forceinline__ void run(const void* w, const uint8_t* scales, int64_t, int col,
                                              int ncol, int K, int s0, int s1, int kg,
@@ -1062,6 +1089,23 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
 
   wait_for_rows();   // (warps without columns have not yet)
 
+  // Until the last blocks are done HBM has little to do: the first steps of what
+  // this block's number does in the down kernel go to L2 meanwhile.
+  if (PHASE == 0) {
+    const int tiles2 = (a.H + CW - 1) / CW, KS2 = (a.I + W::KG * W::STEP - 1) / (W::KG * W::STEP);
+    const Runs next(chunks * tiles2 * KS2, gridDim.x);
+    const int from = next.begin(me), to = me < next.grid ? min(next.begin(me + 1), from + kPrefetchSteps) : 0;
+    for (int s = from; s < to; ++s) {
+      const int unit = s / KS2;
+      W::prefetch(a.w_next, a.scales_next, static_cast<int64_t>(p.chunk_e[unit % chunks]) * a.I * a.H, a.H,
+                  unit / chunks * CW, a.I, s - unit * KS2);
+    }
+    if (tid < a.T * a.k && me < 32) prefetch_l2(a.topk_w + tid);
+    if (a.bias_next && to > from && tid < CW / 32)
+      prefetch_l2(static_cast<const S*>(a.bias_next) + static_cast<int64_t>(p.chunk_e[from / KS2 % chunks]) * a.H +
+                  min(from / KS2 / chunks * CW + tid * 32, a.H - 1));
+  }
+
   // the pieces at the run's ends: piece 0 its first unit (tile), 1 its last
   const int per = PHASE == 0 ? KS : chunks * KS;       // steps of a unit (tile)
   const int p0 = begin / per, p1 = (end - 1) / per;
@@ -1244,6 +1288,9 @@ moe_status moe_ffn_few(const moe_shape* s, const void* x, const uint8_t* x_scale
   a.w = mx ? mx->codes_gate_up : w_gate_up;
   a.scales = mx ? mx->scales_gate_up : nullptr;
   a.bias = bias ? bias->b_gate_up : nullptr;
+  a.w_next = mx ? mx->codes_down : w_down;
+  a.scales_next = mx ? mx->scales_down : nullptr;
+  a.bias_next = bias ? bias->b_down : nullptr;
   a.act = base + L.act;
   a.act_scale = reinterpret_cast<uint8_t*>(base + L.act_scale);
   a.act_top = reinterpret_cast<int*>(base + L.act_top);
