@@ -46,6 +46,7 @@ constexpr int kMaxE = 1024;
 constexpr int kMaxChunks = kMaxE + kMaxSlots / 8;
 constexpr int kMaxGrid = 512;
 constexpr int kPrefetchSteps = 6;
+constexpr int kMaxCW = 256;       // weight columns of a unit, at most
 constexpr int kNowhere = 0xffff;
 // the largest plan_bytes(): every chunk, slot and expert there can be
 constexpr int kMostPlanBytes = 4 * kMaxChunks + 4 * kMaxE + 6 * kMaxChunks + 4 * kMaxSlots + 64;
@@ -320,18 +321,21 @@ struct Row {
 // the lane are rows g and g + 8 of instruction i.  Past the contraction's end both
 // are zero; columns past the end and rows that a unit does not have are computed
 // from others' and never read.
+//
+// Four groups of columns side by side make a block's rows 512 bytes (gate_up: two
+// times 256): with two, 16 tokens on 256 experts take 4% longer in gate_up.
 struct Bf16 {
   using Store = __nv_bfloat16;
-  static constexpr int WF = 64, FG = 2, KG = 4, STEP = 16;
+  static constexpr int WF = 64, FG = 4, KG = 2, STEP = 16;
   static constexpr int PITCH = FG * WF + 1;   // of the results [row][column] in shared memory
   static constexpr bool kHalfRows = false;
   static constexpr bool kRowPerLane = true;   // lane (g, t) reads rows g, g + 8, ...
   static constexpr int kMaxTiles = 2;
-  // The weights of step s of a unit, all columns: 64 rows of two 128-byte lines.
+  // The weights of step s of a unit, all columns: 32 rows of four 128-byte lines.
   static __device__ __forceinline__ void prefetch(const void* w, const uint8_t*, int64_t first, int64_t ld,
                                                   int col, int K, int s) {
-    const int k = s * KG * STEP + (threadIdx.x >> 1), c = col + (threadIdx.x & 1) * 64;
-    if (threadIdx.x < 2 * KG * STEP && k < K && c < ld)
+    const int k = s * KG * STEP + (threadIdx.x / FG), c = col + (threadIdx.x % FG) * 64;
+    if (threadIdx.x < FG * KG * STEP && k < K && c < ld)
       prefetch_l2(static_cast<const __nv_bfloat16*>(w) + first + k * ld + c);
   }
   template <int NT>
@@ -1225,7 +1229,7 @@ FewLayout few_layout(const moe_shape* s) {
   L.act_top = take(sizeof(int) * Tk);
   L.act_scale = take(Tk * (s->I / 32 + 1));
   L.act = take((s->dtype == MOE_FP32 ? 4 : 2) * Tk * s->I);
-  L.part = take(sizeof(float) * 2 * kMaxGrid * 128 * 16);
+  L.part = take(sizeof(float) * 2 * kMaxGrid * kMaxCW * (s->T <= 8 ? 8 : 16));
   L.o = take(sizeof(float) * Tk * s->H);
   L.total = off;
   return L;
