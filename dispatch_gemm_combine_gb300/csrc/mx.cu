@@ -3,10 +3,10 @@
 //
 // The codes are laid out with K innermost, [E, N, K/2], as a product that
 // streams them wants them, so both directions transpose.  A block of 256
-// threads owns 64 columns by 256 rows: warp w the rows [32 w, 32 w + 32) of
-// every column, lane l the columns 2 l and 2 l + 1.  A warp's access to w is 64
-// neighbouring columns of one row (128 bytes in bf16), 32 of them in flight per
-// lane; a lane then holds two whole blocks of 32, so the scale needs no
+// threads owns 32 C columns by 256 rows: warp w the rows [32 w, 32 w + 32) of
+// every column, lane l the columns C l .. C l + C - 1 (8 bytes: C = 4 in bf16, 2 in
+// fp32).  A warp's access to w is 256 bytes of one row, 32 of them in flight per
+// lane; a lane then holds C whole blocks of 32, so the scale needs no
 // exchange.  The codes pass through shared memory to reach global memory as
 // 128-byte rows.  Both directions are HBM-bound: 2 + 17/32 bytes per bf16 weight.
 #include "abi_internal.h"
@@ -16,7 +16,6 @@
 namespace moe {
 namespace {
 
-constexpr int kTileN = 64;
 constexpr int kTileK = 256;
 constexpr int kRowPad = kTileK / 2 + 16;   // bytes between the columns' codes in shared memory
 
@@ -25,67 +24,68 @@ struct MxDims {
   int tiles_k, tiles_n;
 };
 
-__device__ __forceinline__ float2 load_pair(const __nv_bfloat16* p) {
-  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p));
-  return make_float2(bf16_lo(w), bf16_hi(w));
+// C neighbouring values of a row, 8 bytes.
+template <typename E>
+struct Cols {
+  static constexpr int C = 8 / sizeof(E);
+  static constexpr int kTileN = 32 * C;
+  uint2 u;
+  __device__ __forceinline__ void load(const E* p) { u = __ldg(reinterpret_cast<const uint2*>(p)); }
+  __device__ __forceinline__ float get(int c) const {
+    if (sizeof(E) == 4) return __uint_as_float(c ? u.y : u.x);
+    const uint32_t w = c >> 1 ? u.y : u.x;
+    return c & 1 ? bf16_hi(w) : bf16_lo(w);
+  }
+};
+__device__ __forceinline__ void store_cols(__nv_bfloat16* p, const float* v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
-__device__ __forceinline__ float2 load_pair(const float* p) {
-  return __ldg(reinterpret_cast<const float2*>(p));
-}
-__device__ __forceinline__ void store_pair(__nv_bfloat16* p, float2 v) {
-  *reinterpret_cast<uint32_t*>(p) = pack_bf16(v.x, v.y);
-}
-__device__ __forceinline__ void store_pair(float* p, float2 v) {
-  *reinterpret_cast<float2*>(p) = v;
+__device__ __forceinline__ void store_cols(float* p, const float* v) {
+  *reinterpret_cast<float2*>(p) = make_float2(v[0], v[1]);
 }
 
 template <typename E>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(const E* __restrict__ w, MxDims d,
                                                           uint8_t* __restrict__ codes,
                                                           uint8_t* __restrict__ scales) {
-  __shared__ alignas(16) uint8_t sc[kTileN * kRowPad];
-  __shared__ uint8_t ss[kTileN][8];
+  constexpr int C = Cols<E>::C, TN = Cols<E>::kTileN;
+  __shared__ alignas(16) uint8_t sc[TN * kRowPad];
+  __shared__ uint8_t ss[TN][8];
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
   const int tn = blockIdx.x % d.tiles_n;
   const int64_t rest = blockIdx.x / d.tiles_n;
   const int tk = static_cast<int>(rest % d.tiles_k);
   const int64_t e = rest / d.tiles_k;
-  const int64_t n0 = static_cast<int64_t>(tn) * kTileN, n = n0 + 2 * lane;
+  const int64_t n0 = static_cast<int64_t>(tn) * TN, n = n0 + C * lane;
   const int64_t k0 = static_cast<int64_t>(tk) * kTileK, k = k0 + 32 * wp;
   if (k < d.K && n < d.N) {
     const E* p = w + (e * d.K + k) * d.N + n;
-    float2 v[32];
-    uint32_t ax = 0, ay = 0;
+    Cols<E> v[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = load_pair(p + i * d.N);
+    for (int i = 0; i < 32; ++i) v[i].load(p + i * d.N);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      ax = max(ax, __float_as_uint(v[i].x) & 0x7fffffffu);
-      ay = max(ay, __float_as_uint(v[i].y) & 0x7fffffffu);
-    }
-    const uint32_t bx = mx_scale_byte(ax, 0x400000u, 2), by = mx_scale_byte(ay, 0x400000u, 2);
-    const float ix = mx_inv_scale(bx), iy = mx_inv_scale(by);
-    uint32_t cx[4], cy[4];
+    for (int c = 0; c < C; ++c) {
+      uint32_t amax = 0;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      cx[q] = 0, cy[q] = 0;
+      for (int i = 0; i < 32; ++i) amax = max(amax, __float_as_uint(v[i].get(c)) & 0x7fffffffu);
+      const uint32_t byte = mx_scale_byte(amax, 0x400000u, 2);
+      const float inv = mx_inv_scale(byte);
+      uint32_t q[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 a = v[8 * q + 2 * j], b = v[8 * q + 2 * j + 1];
-        cx[q] |= e2m1_pair(a.x * ix, b.x * ix) << (8 * j);
-        cy[q] |= e2m1_pair(a.y * iy, b.y * iy) << (8 * j);
+        q[j] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          q[j] |= e2m1_pair(v[8 * j + 2 * i].get(c) * inv, v[8 * j + 2 * i + 1].get(c) * inv) << (8 * i);
+        if (byte == 255u) q[j] = 0;
       }
-      if (bx == 255u) cx[q] = 0;
-      if (by == 255u) cy[q] = 0;
+      *reinterpret_cast<uint4*>(sc + (C * lane + c) * kRowPad + 16 * wp) = make_uint4(q[0], q[1], q[2], q[3]);
+      ss[C * lane + c][wp] = static_cast<uint8_t>(byte);
     }
-    *reinterpret_cast<uint4*>(sc + (2 * lane) * kRowPad + 16 * wp) = make_uint4(cx[0], cx[1], cx[2], cx[3]);
-    *reinterpret_cast<uint4*>(sc + (2 * lane + 1) * kRowPad + 16 * wp) = make_uint4(cy[0], cy[1], cy[2], cy[3]);
-    ss[2 * lane][wp] = static_cast<uint8_t>(bx);
-    ss[2 * lane + 1][wp] = static_cast<uint8_t>(by);
   }
   __syncthreads();
 #pragma unroll
-  for (int i = threadIdx.x; i < kTileN * 8; i += 256) {
+  for (int i = threadIdx.x; i < TN * 8; i += 256) {
     const int c = i >> 3, b = i & 7;   // column, block of 32
     if (n0 + c < d.N && k0 + 32 * b < d.K) {
       const int64_t row = e * d.N + n0 + c;
@@ -100,17 +100,18 @@ template <typename E>
 __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __restrict__ codes,
                                                             const uint8_t* __restrict__ scales,
                                                             MxDims d, E* __restrict__ w) {
-  __shared__ alignas(16) uint8_t sc[kTileN * kRowPad];
-  __shared__ uint8_t ss[kTileN][8];
+  constexpr int C = Cols<E>::C, TN = Cols<E>::kTileN;
+  __shared__ alignas(16) uint8_t sc[TN * kRowPad];
+  __shared__ uint8_t ss[TN][8];
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
   const int tn = blockIdx.x % d.tiles_n;
   const int64_t rest = blockIdx.x / d.tiles_n;
   const int tk = static_cast<int>(rest % d.tiles_k);
   const int64_t e = rest / d.tiles_k;
-  const int64_t n0 = static_cast<int64_t>(tn) * kTileN, n = n0 + 2 * lane;
+  const int64_t n0 = static_cast<int64_t>(tn) * TN, n = n0 + C * lane;
   const int64_t k0 = static_cast<int64_t>(tk) * kTileK, k = k0 + 32 * wp;
 #pragma unroll
-  for (int i = threadIdx.x; i < kTileN * 8; i += 256) {
+  for (int i = threadIdx.x; i < TN * 8; i += 256) {
     const int c = i >> 3, b = i & 7;
     if (n0 + c < d.N && k0 + 32 * b < d.K) {
       const int64_t row = e * d.N + n0 + c;
@@ -121,25 +122,33 @@ __global__ void __launch_bounds__(256) mx_dequantize_kernel(const uint8_t* __res
   }
   __syncthreads();
   if (k >= d.K || n >= d.N) return;
-  const uint4 ux = *reinterpret_cast<const uint4*>(sc + (2 * lane) * kRowPad + 16 * wp);
-  const uint4 uy = *reinterpret_cast<const uint4*>(sc + (2 * lane + 1) * kRowPad + 16 * wp);
-  const float fx = mx_scale(ss[2 * lane][wp]), fy = mx_scale(ss[2 * lane + 1][wp]);
-  const uint32_t cx[4] = {ux.x, ux.y, ux.z, ux.w}, cy[4] = {uy.x, uy.y, uy.z, uy.w};
+  float f[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) f[c] = mx_scale(ss[C * lane + c][wp]);
   E* p = w + (e * d.K + k) * d.N + n;
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
+  for (int j = 0; j < 4; ++j) {
+    uint32_t q[C];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 a = e2m1_values((cx[q] >> (8 * j)) & 0xffu);
-      const float2 b = e2m1_values((cy[q] >> (8 * j)) & 0xffu);
-      const int i = 8 * q + 2 * j;
-      store_pair(p + i * d.N, make_float2(a.x * fx, b.x * fy));
-      store_pair(p + (i + 1) * d.N, make_float2(a.y * fx, b.y * fy));
+    for (int c = 0; c < C; ++c)
+      q[c] = *reinterpret_cast<const uint32_t*>(sc + (C * lane + c) * kRowPad + 16 * wp + 4 * j);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo[C], hi[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const float2 a = e2m1_values((q[c] >> (8 * i)) & 0xffu);
+        lo[c] = a.x * f[c], hi[c] = a.y * f[c];
+      }
+      store_cols(p + (8 * j + 2 * i) * d.N, lo);
+      store_cols(p + (8 * j + 2 * i + 1) * d.N, hi);
     }
+  }
 }
 
 // The tiles of a launch, or 0 for dimensions that the calls refuse.
-int64_t mx_tiles(int64_t E, int64_t K, int64_t N, MxDims* d) {
+int64_t mx_tiles(int64_t E, int64_t K, int64_t N, int32_t dtype, MxDims* d) {
+  const int kTileN = dtype == MOE_FP32 ? Cols<float>::kTileN : Cols<__nv_bfloat16>::kTileN;
   if (E < 0 || K < 32 || N < 8 || K % 32 || N % 8 || K > (1ll << 31) || N > (1ll << 31)) return 0;
   d->K = K, d->N = N;
   d->tiles_k = static_cast<int>((K + kTileK - 1) / kTileK);
@@ -159,8 +168,8 @@ extern "C" {
 moe_status moe_mx_quantize(const void* w, int32_t dtype, int64_t E, int64_t K, int64_t N,
                            uint8_t* codes, uint8_t* scales, moe_stream_t stream) {
   MxDims d;
-  const int64_t tiles = mx_tiles(E, K, N, &d);
-  if ((tiles == 0 && E != 0) || (E == 0 && mx_tiles(1, K, N, &d) == 0) ||
+  const int64_t tiles = mx_tiles(E, K, N, dtype, &d);
+  if ((tiles == 0 && E != 0) || (E == 0 && mx_tiles(1, K, N, dtype, &d) == 0) ||
       (dtype != MOE_BF16 && dtype != MOE_FP32))
     return MOE_ERR_INVALID_ARG;
   if (E == 0) return MOE_OK;
@@ -184,8 +193,8 @@ moe_status moe_mx_quantize(const void* w, int32_t dtype, int64_t E, int64_t K, i
 moe_status moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t E, int64_t K,
                              int64_t N, int32_t dtype, void* w, moe_stream_t stream) {
   MxDims d;
-  const int64_t tiles = mx_tiles(E, K, N, &d);
-  if ((tiles == 0 && E != 0) || (E == 0 && mx_tiles(1, K, N, &d) == 0) ||
+  const int64_t tiles = mx_tiles(E, K, N, dtype, &d);
+  if ((tiles == 0 && E != 0) || (E == 0 && mx_tiles(1, K, N, dtype, &d) == 0) ||
       (dtype != MOE_BF16 && dtype != MOE_FP32))
     return MOE_ERR_INVALID_ARG;
   if (E == 0) return MOE_OK;
