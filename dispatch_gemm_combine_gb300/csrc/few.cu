@@ -813,30 +813,38 @@ __global__ void __launch_bounds__(256) few_half_rows_kernel(const void* __restri
 __device__ __forceinline__ float load_elem(const __nv_bfloat16* p, int64_t i) { return __bfloat162float(p[i]); }
 __device__ __forceinline__ float load_elem(const float* p, int64_t i) { return p[i]; }
 
-__device__ __forceinline__ float sigmoid_exact(float v) { return 1.f / (1.f + expf(-v)); }
-
-// A NaN stays a NaN through the clamps.
+// A NaN stays a NaN through the clamps.  Both kinds share one sigmoid.
 __device__ __forceinline__ float activate(const FewArgs& a, float gate, float up) {
-  if (a.act_kind == MOE_ACT_SWIGLU) return gate * sigmoid_exact(gate) * up;
-  const float gc = gate > a.limit ? a.limit : gate;
-  const float uc = up > a.limit ? a.limit : (up < -a.limit ? -a.limit : up);
-  return (uc + 1.f) * gc * sigmoid_exact(a.alpha * gc);
+  float z = gate;
+  if (a.act_kind != MOE_ACT_SWIGLU) {
+    gate = gate > a.limit ? a.limit : gate;
+    up = (up > a.limit ? a.limit : (up < -a.limit ? -a.limit : up)) + 1.f;
+    z = a.alpha * gate;
+  }
+  return up * gate * (1.f / (1.f + expf(-z)));
 }
 
-// All units' steps cut into `grid` runs, the first `more` of them one step longer.
+// n / d for n >= 0 and quotients below 2^22, by the reciprocal (a handful of
+// instructions: what a block runs once it has to fetch first).
+__device__ __forceinline__ int quotient(int n, int d, float inv) {
+  int q = static_cast<int>(static_cast<float>(n) * inv);
+  const int r = n - q * d;
+  q += r >= d;
+  q -= r < 0;
+  return q;
+}
+
+// All units' steps cut into `grid` runs of `len` steps, the last one shorter.
 struct Runs {
-  int grid, len, more;
-  __device__ __forceinline__ Runs(int steps, int blocks) {
-    // no more runs than steps: a unit's blocks are consecutive and each has a share
-    grid = min(blocks, steps);
-    len = grid ? steps / grid : 0;
-    more = steps - len * grid;
+  int grid, len, steps;
+  float inv;
+  __device__ __forceinline__ Runs(int steps_, int blocks) : steps(steps_) {
+    len = max(1, (steps + blocks - 1) / blocks);
+    grid = (steps + len - 1) / len;
+    inv = 1.f / static_cast<float>(len);
   }
-  __device__ __forceinline__ int begin(int c) const { return c * len + min(c, more); }
-  __device__ __forceinline__ int block_of(int s) const {
-    const int head = more * (len + 1);
-    return s < head ? s / (len + 1) : more + (s - head) / len;
-  }
+  __device__ __forceinline__ int begin(int c) const { return min(c * len, steps); }
+  __device__ __forceinline__ int block_of(int s) const { return quotient(s, len, inv); }
 };
 
 // Floats of `red`: the shares' results, or the 256 threads' sums of the combine.
@@ -846,31 +854,39 @@ __host__ __device__ __forceinline__ int red_floats(int rows) {
   return n > 4 * kThreads ? n : 4 * kThreads;
 }
 
+// The biases of this thread's output in a unit: thread i has output i % OUT of every
+// kThreads / OUT-th row.
+template <class W>
+__device__ __forceinline__ float2 unit_bias(const FewArgs& a, int e, int tile) {
+  using S = typename W::Store;
+  constexpr int OUT = W::FG * W::WF / 2;
+  const int feature = tile * OUT + threadIdx.x % OUT;
+  if (!a.bias || feature >= a.I) return make_float2(0.f, 0.f);
+  const S* b = static_cast<const S*>(a.bias) + static_cast<int64_t>(e) * 2 * a.I;
+  return make_float2(load_elem(b, a.interleaved ? 2 * feature : feature),
+                     load_elem(b, a.interleaved ? 2 * feature + 1 : a.I + feature));
+}
+
 // The activation of a unit's results, red[row][column], into its rows of a.act.
 template <class W>
 __device__ __forceinline__ void finish_gate_up(const FewArgs& a, const Plan& p, const float* red,
-                                               int chunk, int tile) {
+                                               int chunk, int tile, float2 bias) {
   using S = typename W::Store;
   constexpr int OUT = W::FG * W::WF / 2;
+  static_assert(kThreads % OUT == 0 && OUT % 32 == 0, "a warp has 32 outputs of a row");
   const int first = p.chunk_first[chunk], nrows = p.chunk_rows[chunk];
-  const S* b = a.bias ? static_cast<const S*>(a.bias) + static_cast<int64_t>(p.chunk_e[chunk]) * 2 * a.I : nullptr;
-  for (int i = threadIdx.x; i < OUT * nrows; i += kThreads) {
-    const int f = i % OUT, r = i / OUT;
-    const int feature = tile * OUT + f;
-    if (feature >= a.I) continue;
+  const int f = threadIdx.x % OUT, feature = tile * OUT + f;
+  if (feature >= a.I) return;
+  for (int r = threadIdx.x / OUT; r < nrows; r += kThreads / OUT) {
     const float* q = red + r * W::PITCH;
-    float gate = q[a.interleaved ? 2 * f : f];
-    float up = q[a.interleaved ? 2 * f + 1 : f + OUT];
-    if (b) {
-      gate += load_elem(b, a.interleaved ? 2 * feature : feature);
-      up += load_elem(b, a.interleaved ? 2 * feature + 1 : a.I + feature);
-    }
+    const float gate = q[a.interleaved ? 2 * f : f] + bias.x;
+    const float up = q[a.interleaved ? 2 * f + 1 : f + OUT] + bias.y;
     const float v = activate(a, gate, up);
     const int64_t at = static_cast<int64_t>(p.slot[first + r]) * a.I + feature;
     if constexpr (!W::kHalfRows) {
       static_cast<S*>(a.act)[at] = static_cast<S>(v);
     } else {
-      // a warp has the 32 values of one block (OUT and I are multiples of 32)
+      // a warp has the 32 values of one block (I is a multiple of 32)
       const uint32_t byte =
           half_block_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu));
       static_cast<__half*>(a.act)[at] = __float2half_rn(v * mx_inv_scale(byte));
@@ -898,8 +914,16 @@ __device__ __forceinline__ void store_y(const FewArgs& a, int tok, int c, const 
         make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
 }
 
+// Four of a bias row's values.
+__device__ __forceinline__ float4 bias4(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+}
+__device__ __forceinline__ float4 bias4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
 // y of one column tile from every chunk's products: whole units' in a.o, cut
-// ones' in their blocks' parts.
+// ones' in their blocks' parts.  A block runs this once or twice, so most of its
+// time is the fetch of its instructions: it is kept small.
 template <class W>
 __device__ __forceinline__ void combine_tile(const FewArgs& a, const Plan& p, const Runs& runs, int KS,
                                              int tile, float* red) {
@@ -914,54 +938,56 @@ __device__ __forceinline__ void combine_tile(const FewArgs& a, const Plan& p, co
     p.span[c] = f0 | (f1 << 15) | (runs.begin(f0) < b0 ? 1u << 30 : 0u);
   }
   __syncthreads();
-  // With few tokens a token's choices are shared out over `groups` threads (every
-  // groups-th choice each) whose sums are added in order.
+  // With few tokens a token's choices are shared out over 2^shift threads (every
+  // 2^shift-th choice each) whose sums are added in order.
   const int items = a.T * V;
-  const int groups = max(1, min(a.k, kThreads / items));
+  int shift = 0;
+  while ((items << (shift + 1)) <= kThreads && (1 << shift) < a.k) ++shift;
   float4* sums = reinterpret_cast<float4*>(red);
-  for (int i = threadIdx.x; i < items * groups; i += kThreads) {
-    const int f = i % V * 4, tok = i / V % a.T, group = i / items;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < items << shift; i += kThreads) {
+    const int f = i % V * 4, tok = i / V >> shift, group = (i / V) & ((1 << shift) - 1);
     const int c = tile * CW + f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < a.H) {
-#pragma unroll 4
-      for (int j = group; j < a.k; j += groups) {
-        const int slot = tok * a.k + j;
-        const int at = p.where[slot];
-        if (at == kNowhere) continue;
-        const float w = __ldg(a.topk_w + slot);
-        const uint32_t sp = p.span[at >> 5];
-        const int f0 = sp & 0x7fff, n = static_cast<int>((sp >> 15) & 0x7fff) - f0;
-        const int q = (at & 31) * CW + f;
-        const float* head = n ? a.part + (2 * static_cast<int64_t>(f0) + (sp >> 30)) * UNIT + q
-                              : a.o + static_cast<int64_t>(slot) * a.H + c;
-        const float* next = a.part + 2 * static_cast<int64_t>(f0 + 1) * UNIT + q;
-        float4 v = ldcg4(head), o[3], bias = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int j = group; j < a.k && c < a.H; j += 1 << shift) {
+      const int slot = tok * a.k + j;
+      const int at = p.where[slot];
+      if (at == kNowhere) continue;
+      const float w = __ldg(a.topk_w + slot);
+      const uint32_t sp = p.span[at >> 5];
+      const int f0 = sp & 0x7fff;
+      int n = static_cast<int>((sp >> 15) & 0x7fff) - f0;
+      const float* next = a.part + 2 * static_cast<int64_t>(f0) * UNIT + (at & 31) * CW + f;
+      float4 v = ldcg4(n ? next + (sp >> 30) * UNIT : a.o + static_cast<int64_t>(slot) * a.H + c);
+      float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (a.bias) bias = bias4(static_cast<const S*>(a.bias) + static_cast<int64_t>(p.chunk_e[at >> 5]) * a.H + c);
+#pragma unroll 1
+      for (; n > 0; n -= 3) {   // three parts' loads at a time
+        float4 o[3];
 #pragma unroll
-        for (int b = 0; b < 3; ++b)
-          o[b] = b < n ? ldcg4(next + 2 * static_cast<int64_t>(b) * UNIT) : make_float4(0.f, 0.f, 0.f, 0.f);
-        if (a.bias) {
-          const S* b = static_cast<const S*>(a.bias) + static_cast<int64_t>(p.chunk_e[at >> 5]) * a.H + c;
-          bias = make_float4(load_elem(b, 0), load_elem(b, 1), load_elem(b, 2), load_elem(b, 3));
+        for (int b = 0; b < 3; ++b) {
+          next += 2 * UNIT;
+          o[b] = b < n ? ldcg4(next) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int b = 0; b < 3; ++b) add4(v, o[b]);
-        for (int b = 3; b < n; ++b) add4(v, ldcg4(next + 2 * static_cast<int64_t>(b) * UNIT));
-        add4(v, bias);
-        y.x = fmaf(w, v.x, y.x), y.y = fmaf(w, v.y, y.y);
-        y.z = fmaf(w, v.z, y.z), y.w = fmaf(w, v.w, y.w);
       }
+      add4(v, bias);
+      y.x = fmaf(w, v.x, y.x), y.y = fmaf(w, v.y, y.y);
+      y.z = fmaf(w, v.z, y.z), y.w = fmaf(w, v.w, y.w);
     }
-    if (groups == 1)
+    if (shift == 0)
       store_y<S>(a, tok, c, y);
     else
       sums[i] = y;
   }
-  if (groups > 1) {
+  if (shift > 0) {
     __syncthreads();
     for (int i = threadIdx.x; i < items; i += kThreads) {
-      float4 y = sums[i];
-      for (int g = 1; g < groups; ++g) add4(y, sums[g * items + i]);
+      const int at = (i / V << shift) * V + i % V;
+      float4 y = sums[at];
+      for (int g = 1; g < 1 << shift; ++g) add4(y, sums[at + g * V]);
       store_y<S>(a, i / V, tile * CW + i % V * 4, y);
     }
   }
@@ -999,6 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   const int KS = (K + W::KG * W::STEP - 1) / (W::KG * W::STEP);
   const int chunks = p.chunks;
   const Runs runs(chunks * tiles * KS, gridDim.x);
+  const float inv_KS = 1.f / static_cast<float>(KS), inv_chunks = 1.f / static_cast<float>(chunks);
   if (me >= runs.grid) {
     wait_for_rows();
     // no row at all (every id out of range): y is still written
@@ -1028,11 +1055,11 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   };
 
   for (int s = begin; s < end;) {
-    const int unit = s / KS;
+    const int unit = quotient(s, KS, inv_KS);
     const int u0 = unit * KS;
     const int ks0 = s - u0;
     const int ks1 = min(KS, end - u0);
-    const int chunk = unit % chunks, tile = unit / chunks;
+    const int tile = quotient(unit, chunks, inv_chunks), chunk = unit - tile * chunks;
     const int e = p.chunk_e[chunk], first = p.chunk_first[chunk], nrows = p.chunk_rows[chunk];
 
     int col, ncol;
@@ -1082,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     }
     __syncthreads();
     if (PHASE == 0 && whole) {
-      finish_gate_up<W>(a, p, red, chunk, tile);
+      finish_gate_up<W>(a, p, red, chunk, tile, unit_bias<W>(a, e, tile));
       __syncthreads();
     }
     // a tile that lies in this run alone
@@ -1137,14 +1164,17 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     const int nrows = p.chunk_rows[chunk];
     const int c0 = runs.block_of(piece * KS), c1 = runs.block_of(piece * KS + KS - 1);
     const float* head = a.part + (2 * static_cast<int64_t>(c0) + (runs.begin(c0) >= piece * KS ? 0 : 1)) * UNIT;
-    for (int j = tid; j < nrows * CW; j += kThreads) {
-      float v = __ldcg(head + j);
-#pragma unroll 4
-      for (int c = c0 + 1; c <= c1; ++c) v += __ldcg(a.part + 2 * static_cast<int64_t>(c) * UNIT + j);
-      red[j / CW * W::PITCH + j % CW] = v;
+    const float2 bias = unit_bias<W>(a, p.chunk_e[chunk], piece / chunks);
+#pragma unroll 1
+    for (int j = tid * 4; j < nrows * CW; j += kThreads * 4) {
+      float4 v = ldcg4(head + j);
+#pragma unroll 2
+      for (int c = c0 + 1; c <= c1; ++c) add4(v, ldcg4(a.part + 2 * static_cast<int64_t>(c) * UNIT + j));
+      float* d = red + j / CW * W::PITCH + j % CW;
+      d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
     }
     __syncthreads();
-    finish_gate_up<W>(a, p, red, chunk, piece / chunks);
+    finish_gate_up<W>(a, p, red, chunk, piece / chunks, bias);
     __syncthreads();
   }
 }
