@@ -1120,30 +1120,14 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
 
   wait_for_rows();   // (warps without columns have not yet)
 
-  // Until the last blocks are done HBM has little to do: the first steps of what
-  // this block's number does in the down kernel go to L2 meanwhile.
-  if (PHASE == 0) {
-    const int tiles2 = (a.H + CW - 1) / CW, KS2 = (a.I + W::KG * W::STEP - 1) / (W::KG * W::STEP);
-    const Runs next(chunks * tiles2 * KS2, gridDim.x);
-    const int from = next.begin(me), to = me < next.grid ? min(next.begin(me + 1), from + kPrefetchSteps) : 0;
-    for (int s = from; s < to; ++s) {
-      const int unit = s / KS2;
-      W::prefetch(a.w_next, a.scales_next, static_cast<int64_t>(p.chunk_e[unit % chunks]) * a.I * a.H, a.H,
-                  unit / chunks * CW, a.I, s - unit * KS2);
-    }
-    if (tid < a.T * a.k && me < 32) prefetch_l2(a.topk_w + tid);
-    if (a.bias_next && to > from && tid < CW / 32)
-      prefetch_l2(static_cast<const S*>(a.bias_next) + static_cast<int64_t>(p.chunk_e[from / KS2 % chunks]) * a.H +
-                  min(from / KS2 / chunks * CW + tid * 32, a.H - 1));
-  }
-
   // the pieces at the run's ends: piece 0 its first unit (tile), 1 its last
   const int per = PHASE == 0 ? KS : chunks * KS;       // steps of a unit (tile)
-  const int p0 = begin / per, p1 = (end - 1) / per;
+  const float inv_per = PHASE == 0 ? inv_KS : inv_KS * inv_chunks;
+  const int p0 = quotient(begin, per, inv_per), p1 = quotient(end - 1, per, inv_per);
+  int last = 0;
   if (tid < 2) {
     const int piece = tid ? p1 : p0;
     const int lo = max(begin, piece * per), hi = min(end, (piece + 1) * per);
-    int last = 0;
     if (hi - lo < per && (tid == 0 || p1 != p0)) {
       // a unit's counter is its first block's (a block is the first of at most one cut unit)
       unsigned* c = a.counters + (PHASE == 0 ? runs.block_of(piece * per) : piece);
@@ -1152,7 +1136,26 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     }
     ps.last[tid] = last;
   }
+  // Until the last blocks are done HBM has little to do: the first steps of what
+  // this block's number does in the down kernel go to L2 meanwhile.
+  if (PHASE == 0) {
+    const int tiles2 = (a.H + CW - 1) / CW, KS2 = (a.I + W::KG * W::STEP - 1) / (W::KG * W::STEP);
+    const Runs next(chunks * tiles2 * KS2, gridDim.x);
+    const int from = next.begin(me), to = me < next.grid ? min(next.begin(me + 1), from + kPrefetchSteps) : 0;
+    const float inv_KS2 = 1.f / static_cast<float>(KS2);
+#pragma unroll 1
+    for (int s = from; s < to; ++s) {
+      const int unit = quotient(s, KS2, inv_KS2), tile = quotient(unit, chunks, inv_chunks);
+      const int e = p.chunk_e[unit - tile * chunks];
+      W::prefetch(a.w_next, a.scales_next, static_cast<int64_t>(e) * a.I * a.H, a.H, tile * CW, a.I,
+                  s - unit * KS2);
+      if (a.bias_next && s == from && tid < CW / 32 && tile * CW + tid * 32 < a.H)
+        prefetch_l2(static_cast<const S*>(a.bias_next) + static_cast<int64_t>(e) * a.H + tile * CW + tid * 32);
+    }
+    if (tid < a.T * a.k && me < 32) prefetch_l2(a.topk_w + tid);
+  }
   __syncthreads();
+#pragma unroll 1
   for (int i = 0; i < 2; ++i) {
     if (!ps.last[i]) continue;
     const int piece = i ? p1 : p0;
@@ -1160,11 +1163,11 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       combine_tile<W>(a, p, runs, KS, piece, red);
       continue;
     }
-    const int chunk = piece % chunks;
+    const int tile = quotient(piece, chunks, inv_chunks), chunk = piece - tile * chunks;
     const int nrows = p.chunk_rows[chunk];
     const int c0 = runs.block_of(piece * KS), c1 = runs.block_of(piece * KS + KS - 1);
     const float* head = a.part + (2 * static_cast<int64_t>(c0) + (runs.begin(c0) >= piece * KS ? 0 : 1)) * UNIT;
-    const float2 bias = unit_bias<W>(a, p.chunk_e[chunk], piece / chunks);
+    const float2 bias = unit_bias<W>(a, p.chunk_e[chunk], tile);
 #pragma unroll 1
     for (int j = tid * 4; j < nrows * CW; j += kThreads * 4) {
       float4 v = ldcg4(head + j);
@@ -1174,7 +1177,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
     }
     __syncthreads();
-    finish_gate_up<W>(a, p, red, chunk, piece / chunks, bias);
+    finish_gate_up<W>(a, p, red, chunk, tile, bias);
     __syncthreads();
   }
 }
