@@ -4,6 +4,7 @@
 // the C ABI.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -17,6 +18,14 @@ bool abi_shape_ok(const moe_shape* s);
 // SM count of the current device, or MOE_ERR_UNSUPPORTED if it is not an
 // sm_103 part (cached per device).
 moe_status abi_device_sms(int* sms);
+
+// The limit of a kernel's wait for its own copies (moe_set_wait_timeout_ns).
+uint64_t abi_wait_timeout_ns();
+
+// A tensor map over bytes [d2, d1, d0], contiguous, d0 a multiple of 16; boxes of
+// [1, b1, b0].  False if it cannot be made.
+bool abi_map_bytes(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
+                   uint32_t b0, uint32_t b1);
 
 // The plan kernels (launch_plan) and a memset, counted by
 // moe_kernel_launch_count() and bracketed by the event timer when it is on.

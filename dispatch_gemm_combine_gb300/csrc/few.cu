@@ -28,6 +28,8 @@
 // kernels for bf16 storage, as the layer for many tokens does (it is an operand
 // of the bf16 product); it stays fp32 for fp32 storage, whose products run in
 // fp32 on the CUDA cores.
+#include <cuda.h>
+
 #include <algorithm>
 #include <atomic>
 
@@ -74,6 +76,8 @@ struct FewArgs {
   int* err;
   int T, H, I, E, k, rows, act_kind, interleaved, out_fp32;   // rows: of a chunk
   float limit, alpha;
+  uint64_t timeout_ns;
+  CUtensorMap codes;       // 4-bit weights: this kernel's [E, N, K/2]
 };
 
 // ------------------------------------------------------------------ plan
@@ -305,6 +309,15 @@ __device__ __forceinline__ uint4 ld_u128(const void* p) {
   return v;
 }
 
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // Waits for the kernel before (returns at once when it has ended).
 __device__ __forceinline__ void wait_for_rows() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -329,6 +342,7 @@ struct Bf16 {
   static constexpr int WF = 64, FG = 4, KG = 2, STEP = 16;
   static constexpr int PITCH = FG * WF + 1;   // of the results [row][column] in shared memory
   static constexpr bool kHalfRows = false;
+  static constexpr int kRing = 0;
   static constexpr bool kRowPerLane = true;   // lane (g, t) reads rows g, g + 8, ...
   static constexpr int kMaxTiles = 2;
   // The weights of step s of a unit, all columns: 32 rows of four 128-byte lines.
@@ -339,8 +353,7 @@ struct Bf16 {
       prefetch_l2(static_cast<const __nv_bfloat16*>(w) + first + k * ld + c);
   }
   template <int NT>
-  static __device__ __forceinline__ void run(const void* w, const uint8_t*, int64_t ld, int col,
-                                             int ncol, int K, int s0, int s1, int kg,
+  static __device__ __forceinline__ void run(const void* w, int64_t ld, int col, int ncol, int K, int s0, int s1, int kg,
                                              const Row* rows, int nrows, float* red) {
     constexpr int U = NT == 1 ? 2 : 1;   // steps per buffer; two buffers take turns
     const bool both = NT > 1 && nrows > 8;
@@ -422,6 +435,7 @@ struct F32 {
   static constexpr int WF = 32, FG = 2, KG = 4, STEP = 16;
   static constexpr int PITCH = FG * WF + 1;   // of the results [row][column] in shared memory
   static constexpr bool kHalfRows = false;
+  static constexpr int kRing = 0;
   static constexpr bool kRowPerLane = false;   // every lane reads all rows
   static constexpr int kMaxTiles = 1;
   static __device__ __forceinline__ void prefetch(const void* w, const uint8_t*, int64_t first, int64_t ld,
@@ -431,8 +445,7 @@ struct F32 {
       prefetch_l2(static_cast<const float*>(w) + first + k * ld + c);
   }
   template <int NT>
-  static __device__ __forceinline__ void run(const void* w, const uint8_t*, int64_t ld, int col,
-                                             int ncol, int K, int s0, int s1, int kg,
+  static __device__ __forceinline__ void run(const void* w, int64_t ld, int col, int ncol, int K, int s0, int s1, int kg,
                                              const Row* rows, int nrows, float* red) {
     wait_for_rows();
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -495,6 +508,8 @@ struct Mx {
   static constexpr int PITCH = FG * WF + 1;   // of the results [row][column] in shared memory
   static constexpr int kMaxTiles = 2;
   static constexpr bool kRowPerLane = true, kHalfRows = true;
+  // A warp's ring of steps in shared memory: 32 columns of 64 bytes each.
+  static constexpr int kRing = 4, kSlotBytes = WF * STEP / 2;
 
   static __device__ __forceinline__ void mma(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
                                              uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -528,15 +543,8 @@ struct Mx {
     return h * 0x00010001u;
   }
 
-  // A step of a warp: 4 blocks (one per lane t) of 4 x 8 columns.
-  struct Load {
-    uint4 v[4];
-    uint32_t byte[4];
-  };
-  // What brings the tokens' block b to the row's power of two; 0 past the end.
-  static __device__ __forceinline__ uint32_t row_factor(const Row& r, int b, int nb) {
-    if (b >= nb) return 0u;
-    if (!r.scale) return 0x3c003c00u;
+  // What brings the activations' block b to the row's power of two.
+  static __device__ __forceinline__ uint32_t row_factor(const Row& r, int b) {
     const uint32_t p = ld_u8(r.scale + b);
     return p == 255u ? 0x7e007e00u : pow2_down(static_cast<int>(p) - r.top);
   }
@@ -554,19 +562,24 @@ struct Mx {
     prefetch_l2(static_cast<const uint8_t*>(w) + first / 2 + c * (K >> 1) + b / 2);
     prefetch_l2(scales + first / 32 + c * (K >> 5) + b / 32);
   }
-  template <int NT>
-  static __device__ __forceinline__ void run(const void* w, const uint8_t* scales, int64_t, int col,
-                                             int ncol, int K, int s0, int s1, int kg,
-                                             const Row* rows, int nrows, float* red) {
-    // Two buffers take turns (16 registers for a step's weights); with one row tile
-    // the tokens' loads go ahead with the weights' (16 more), with two there are no
-    // registers for that.  Past the end the last block is loaded again and the
-    // tokens' factor is 0.
+  // Token rows times the row's factor for a block (gate_up's have one scale).
+  template <int PHASE>
+  static __device__ __forceinline__ uint4 scaled(uint4 x, uint32_t f) {
+    if (PHASE == 0) return x;
+    return make_uint4(mul2(x.x, f), mul2(x.y, f), mul2(x.z, f), mul2(x.w, f));
+  }
+  // `ring` has the codes: wait() returns the shared address of the next step's,
+  // release() gives their place to a later step's.
+  template <int NT, int PHASE, class Ring>
+  static __device__ __forceinline__ void run(Ring& ring, const uint8_t* scales, int col, int K, int s0,
+                                             int s1, int kg, const Row* rows, int nrows, float* red) {
+    // Scale bytes, and with one row tile the tokens, are loaded two steps ahead; with
+    // two there are no registers for that.  Codes past the end are zeros, whatever
+    // their scale and tokens (the last block's).
     constexpr bool EARLY = NT == 1;
     const bool both = NT > 1 && nrows > 8;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int nb = K >> 5;
-    const int64_t cld = 8ll * (K >> 1);         // from one eight columns to the next
     float acc[2][NT][4];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -574,48 +587,44 @@ struct Mx {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[m][n][q] = 0.f;
-    const uint8_t* cp = static_cast<const uint8_t*>(w) + (static_cast<int64_t>(col) + g) * (K >> 1);
     const uint8_t* sp = scales + (static_cast<int64_t>(col) + g) * nb;
-    const int eights = min(4, ncol >> 3);       // inside
-    Load ld[2];
+    uint32_t byte[2][4];
     uint4 x[2][EARLY ? 4 : 1];
     uint32_t xf[2] = {0, 0};
-    auto load_w = [&](int buf, int s) {
+    auto block = [&](int s) { return min((s * KG + kg) * 4 + t, nb - 1); };
+    auto load_bytes = [&](int buf, int s) {
       if (s >= s1) return;
-      const int b = min((s * KG + kg) * 4 + t, nb - 1);
-      const uint8_t* src = cp + 16 * b;
-      const uint8_t* byte = sp + b;
+      const uint8_t* p = sp + block(s);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int rr = r < eights ? r : 0;
-        ld[buf].v[r] = ldg_stream(src + rr * cld);
-        ld[buf].byte[r] = __ldg(byte + rr * 8 * nb);
-      }
+      for (int r = 0; r < 4; ++r) byte[buf][r] = __ldg(p + r * 8 * nb);
     };
     auto load_x = [&](int buf, int s) {
       if (!EARLY || s >= s1) return;
-      const int b = (s * KG + kg) * 4 + t;
+      const int b = block(s);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) x[buf][q % (EARLY ? 4 : 1)] = row_vec(rows[0], min(b, nb - 1), q);
-      xf[buf] = row_factor(rows[0], b, nb);
+      for (int q = 0; q < 4; ++q) x[buf][q % (EARLY ? 4 : 1)] = row_vec(rows[0], b, q);
+      if (PHASE == 1) xf[buf] = row_factor(rows[0], b);
     };
-    load_w(0, s0);
-    load_w(1, s0 + 1);
+    load_bytes(0, s0);
+    load_bytes(1, s0 + 1);
     wait_for_rows();
     load_x(0, s0);
     load_x(1, s0 + 1);
     int ref[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      ref[r] = min(240, static_cast<int>(__shfl_sync(0xffffffffu, ld[0].byte[r], lane & 28)));
+      ref[r] = min(240, static_cast<int>(__shfl_sync(0xffffffffu, byte[0][r], lane & 28)));
     auto step = [&](int buf, int s) {
-      const int b = (s * KG + kg) * 4 + t;
+      uint4 v[4];
+      const uint32_t at = ring.wait() + (g * 4 + t) * 16;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = ld_shared_v4(at + r * 8 * (STEP / 2));
       // 2^(q - ref) in fp16, in range for -14 .. 13 (ref <= 240: a NaN's 255 is not)
       uint32_t f[4];
       bool far = false;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const uint32_t d = ld[buf].byte[r] - ref[r] + 14;
+        const uint32_t d = byte[buf][r] - ref[r] + 14;
         far = far || d > 27u;
         f[r] = d * 0x04000400u + 0x04000400u;
       }
@@ -623,35 +632,33 @@ struct Mx {
         far = false;   // a block of zeros needs no scale
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const uint4& v = ld[buf].v[r];
-          if (ld[buf].byte[r] - ref[r] + 14 > 27u) {
-            far = far || (v.x | v.y | v.z | v.w) != 0 || ld[buf].byte[r] == 255u;
+          if (byte[buf][r] - ref[r] + 14 > 27u) {
+            far = far || (v[r].x | v[r].y | v[r].z | v[r].w) != 0 || byte[buf][r] == 255u;
             f[r] = 0x3c003c00u;
           }
         }
         far = __any_sync(0xffffffffu, far);
       }
       if (far) {
-        far_step<NT, EARLY>(ld[buf], x[buf], xf[buf], b, nb, ref, rows, acc);
+        far_step<NT, PHASE, EARLY>(v, byte[buf], x[buf], xf[buf], block(s), ref, rows, acc);
       } else {
         uint32_t fxs[NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) fxs[n] = EARLY ? 0u : row_factor(rows[n], b, nb);
+        for (int n = 0; n < NT; ++n) fxs[n] = EARLY || PHASE == 0 ? xf[buf] : row_factor(rows[n], block(s));
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t a[4][4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            decode(word(ld[buf].v[r], q), a[r]);
+            decode(word(v[r], q), a[r]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) a[r][j] = mul2(a[r][j], f[r]);
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             if (n > 0 && !both) continue;
-            uint4 xv = EARLY ? x[buf][q % (EARLY ? 4 : 1)] : row_vec(rows[n], min(b, nb - 1), q);
-            const uint32_t fx = EARLY ? xf[buf] : fxs[n];
-            xv.x = mul2(xv.x, fx), xv.y = mul2(xv.y, fx), xv.z = mul2(xv.z, fx), xv.w = mul2(xv.w, fx);
+            const uint4 xv =
+                scaled<PHASE>(EARLY ? x[buf][q % (EARLY ? 4 : 1)] : row_vec(rows[n], block(s), q), fxs[n]);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
               mma(acc[m][n], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], xv.x, xv.y);
@@ -660,8 +667,9 @@ struct Mx {
           }
         }
       }
-      load_w(buf, s + 2);
+      load_bytes(buf, s + 2);
       load_x(buf, s + 2);
+      ring.release();
     };
     for (int s = s0; s < s1; s += 2) {
       step(0, s);
@@ -684,17 +692,17 @@ struct Mx {
 
   // A step with far scales: the four lanes' blocks one after the other, codes as
   // they are, each block's sums scaled by 2^(q - ref) in fp32.
-  template <int NT, bool EARLY>
-  static __device__ __forceinline__ void far_step(const Load& ld, const uint4* x, uint32_t xf, int b,
-                                                  int nb, const int (&ref)[4], const Row* rows,
-                                                  float (&acc)[2][NT][4]) {
+  template <int NT, int PHASE, bool EARLY>
+  static __device__ __forceinline__ void far_step(const uint4 (&v)[4], const uint32_t (&bytes)[4],
+                                                  const uint4* x, uint32_t xf, int b, const int (&ref)[4],
+                                                  const Row* rows, float (&acc)[2][NT][4]) {
     const int lane = threadIdx.x & 31, t = lane & 3;
 #pragma unroll 1
     for (int turn = 0; turn < 4; ++turn) {
       float f[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const uint32_t byte = __shfl_sync(0xffffffffu, ld.byte[r], (lane & 28) | turn);
+        const uint32_t byte = __shfl_sync(0xffffffffu, bytes[r], (lane & 28) | turn);
         f[r] = byte == 255u ? __uint_as_float(0x7fc00000u) : ldexpf(1.f, static_cast<int>(byte) - ref[r]);
       }
 #pragma unroll
@@ -702,14 +710,13 @@ struct Mx {
         float c[2][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m) c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
-        const uint32_t fx = EARLY ? xf : row_factor(rows[n], b, nb);
+        const uint32_t fx = EARLY || PHASE == 0 ? xf : row_factor(rows[n], b);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t a[4][4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) decode(t == turn ? word(ld.v[r], q) : 0u, a[r]);
-          uint4 xv = EARLY ? x[q] : row_vec(rows[n], min(b, nb - 1), q);
-          xv.x = mul2(xv.x, fx), xv.y = mul2(xv.y, fx), xv.z = mul2(xv.z, fx), xv.w = mul2(xv.w, fx);
+          for (int r = 0; r < 4; ++r) decode(t == turn ? word(v[r], q) : 0u, a[r]);
+          uint4 xv = scaled<PHASE>(EARLY ? x[q] : row_vec(rows[n], b, q), fx);
           if (t != turn) xv = make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
@@ -852,6 +859,17 @@ template <class W>
 __host__ __device__ __forceinline__ int red_floats(int rows) {
   const int n = (W::KG * W::PITCH * rows + 3) & ~3;
   return n > 4 * kThreads ? n : 4 * kThreads;
+}
+
+template <class W>
+__host__ __device__ constexpr int ring_slot() {
+  if constexpr (W::kRing > 0) return W::kSlotBytes;
+  return 0;
+}
+// Bytes of the warps' rings, their barriers and the way to a multiple of 128.
+template <class W>
+__host__ __device__ constexpr int ring_bytes() {
+  return W::kRing ? kThreads / 32 * W::kRing * (ring_slot<W>() + 8) + 112 : 0;
 }
 
 // The biases of this thread's output in a unit: thread i has output i % OUT of every
@@ -1014,6 +1032,17 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int fg = warp % W::FG, kg = warp / W::FG;
+  uint32_t slots = 0, bars = 0;                // this warp's ring
+  if (W::kRing > 0) {
+    slots = (smem_u32(dynamic) + red_floats<W>(a.rows) * 4 + plan_bytes(a.T * a.k, a.E, a.rows) + 127) & ~127u;
+    bars = slots + kThreads / 32 * W::kRing * ring_slot<W>() + warp * W::kRing * 8;
+    slots += warp * W::kRing * ring_slot<W>();
+    if (lane == 0) {
+      for (int i = 0; i < W::kRing; ++i) mbar_init(bars + 8 * i, 1);
+      fence_barrier_init();
+    }
+    __syncwarp();
+  }
   const int me = blockIdx.x;
   if (PHASE == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -1054,6 +1083,56 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     }
   };
 
+  // The ring runs through all of the block's steps, whatever unit they are of.
+  struct Ring {
+    int next, left;            // the step to load next; steps left of its unit
+    int k, col, e;             // where its codes are
+    uint32_t put, got;
+  } at = {begin, 0, 0, 0, 0, 0, 0};
+  auto load_next = [&] {
+    while (at.left == 0) {
+      if (at.next >= end) return;
+      const int unit = quotient(at.next, KS, inv_KS), tile = quotient(unit, chunks, inv_chunks);
+      int ncol;
+      columns(tile, &at.col, &ncol);
+      const int stop = min(end, (unit + 1) * KS);
+      if (ncol <= 0) {
+        at.next = stop;
+        continue;
+      }
+      at.left = stop - at.next;
+      at.k = ((at.next - unit * KS) * W::KG + kg) * (W::STEP / 2);
+      at.e = p.chunk_e[unit - tile * chunks];
+    }
+    if (lane == 0) {
+      const uint32_t i = at.put % (W::kRing ? W::kRing : 1);
+      mbar_arrive_expect_tx(bars + 8 * i, ring_slot<W>());
+      tma_load_3d(slots + i * ring_slot<W>(), &a.codes, bars + 8 * i, at.k, at.col, at.e);
+    }
+    ++at.put, ++at.next, --at.left;
+    at.k += W::KG * W::STEP / 2;
+  };
+  struct {
+    decltype(load_next)& load;
+    Ring& at;
+    uint32_t slots, bars;
+    uint64_t timeout_ns;
+    int* err;
+    __device__ __forceinline__ uint32_t wait() {
+      constexpr uint32_t S = W::kRing ? W::kRing : 1;
+      const uint32_t i = at.got % S;
+      if (!mbar_wait(bars + 8 * i, at.got / S & 1, timeout_ns)) record_error(err, kErrTimeout);
+      return slots + i * ring_slot<W>();
+    }
+    __device__ __forceinline__ void release() {
+      ++at.got;
+      __syncwarp();
+      load();
+    }
+  } ring = {load_next, at, slots, bars, a.timeout_ns, a.err};
+  if (W::kRing > 0)
+    for (int i = 0; i < W::kRing; ++i) load_next();
+
   for (int s = begin; s < end;) {
     const int unit = quotient(s, KS, inv_KS);
     const int u0 = unit * KS;
@@ -1082,12 +1161,11 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     }
     if (ncol > 0) {
       const int64_t we = static_cast<int64_t>(e) * K * N;   // weights of the experts before
-      const void* w = sizeof(S) == 4 ? static_cast<const void*>(static_cast<const float*>(a.w) + we)
-                      : W::kHalfRows
-                          ? static_cast<const void*>(static_cast<const uint8_t*>(a.w) + we / 2)
-                          : static_cast<const void*>(static_cast<const __nv_bfloat16*>(a.w) + we);
-      W::template run<NT>(w, W::kHalfRows ? a.scales + we / 32 : nullptr, N, col,
-                           ncol, K, ks0, ks1, kg, rows, nrows, red + kg * SHARE + fg * W::WF);
+      float* out = red + kg * SHARE + fg * W::WF;
+      if constexpr (W::kRing > 0)
+        W::template run<NT, PHASE>(ring, a.scales + we / 32, col, K, ks0, ks1, kg, rows, nrows, out);
+      else
+        W::template run<NT>(static_cast<const S*>(a.w) + we, N, col, ncol, K, ks0, ks1, kg, rows, nrows, out);
     }
     __syncthreads();
 
@@ -1185,8 +1263,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
 // `after`: may start while the kernel before it, which writes its rows, ends.
 template <class W, int PHASE, int NT>
 cudaError_t launch(const FewArgs& a, int grid, bool after, cudaStream_t st) {
-  const int smem = red_floats<W>(a.rows) * 4 + plan_bytes(a.T * a.k, a.E, a.rows);
-  const int most = red_floats<W>(8 * NT) * 4 + kMostPlanBytes;
+  const int smem = red_floats<W>(a.rows) * 4 + plan_bytes(a.T * a.k, a.E, a.rows) + ring_bytes<W>();
+  const int most = red_floats<W>(8 * NT) * 4 + kMostPlanBytes + ring_bytes<W>();
   static std::atomic<uint64_t> ready{0};   // one bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1344,6 +1422,11 @@ moe_status moe_ffn_few(const moe_shape* s, const void* x, const uint8_t* x_scale
   a.out_fp32 = s->out_fp32;
   a.limit = s->clamp_limit;
   a.alpha = s->alpha;
+  a.timeout_ns = abi_wait_timeout_ns();
+  CUtensorMap down_codes;
+  if (mx && !(abi_map_bytes(&a.codes, mx->codes_gate_up, s->H / 2, 2 * static_cast<uint64_t>(s->I), s->E, Mx::STEP / 2, Mx::WF) &&
+              abi_map_bytes(&down_codes, mx->codes_down, s->I / 2, s->H, s->E, Mx::STEP / 2, Mx::WF)))
+    return MOE_ERR_CUDA;
   const int nt = row_tiles(s, mx != nullptr);
   a.rows = 8 * nt;
 
@@ -1366,6 +1449,7 @@ moe_status moe_ffn_few(const moe_shape* s, const void* x, const uint8_t* x_scale
   a.x = a.act;
   a.x_scale = a.act_scale;
   a.top = a.act_top;
+  if (mx) a.codes = down_codes;
   a.w = mx ? mx->codes_down : w_down;
   a.scales = mx ? mx->scales_down : nullptr;
   a.bias = bias ? bias->b_down : nullptr;
