@@ -25,7 +25,7 @@ uint64_t abi_wait_timeout_ns();
 // A tensor map over bytes [d2, d1, d0], contiguous, d0 a multiple of 16; boxes of
 // [1, b1, b0].  False if it cannot be made.
 bool abi_map_bytes(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
-                   uint32_t b0, uint32_t b1);
+                   uint32_t b0, uint32_t b1, CUtensorMapSwizzle sw);
 
 // The plan kernels (launch_plan) and a memset, counted by
 // moe_kernel_launch_count() and bracketed by the event timer when it is on.

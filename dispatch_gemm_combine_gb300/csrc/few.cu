@@ -290,6 +290,11 @@ __device__ __forceinline__ uint32_t ld_u8(const void* p) {
   asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
+__device__ __forceinline__ uint32_t ld_u16(const void* p) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .u16 h;\n\tld.global.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t ld_u32(const void* p) {
   uint32_t v;
   asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -324,8 +329,8 @@ __device__ __forceinline__ void wait_for_rows() { asm volatile("griddepcontrol.w
 // A token row (or a slot's activations) as the product reads it.
 struct Row {
   const void* p;
-  const uint8_t* scale = nullptr;   // of fp16 rows: null, or a byte per block of 32
-  int top = 127;                    // of fp16 rows: the row's byte, the largest of its blocks'
+  int row;    // of fp16 rows: which, and
+  int top;    // its byte, the largest of its blocks'
 };
 
 // bf16 weights [K, ld], columns innermost.  A lane loads 16 bytes (8 columns) of
@@ -504,12 +509,12 @@ struct F32 {
 // scale) takes a path that multiplies the blocks one by one and scales sums.
 struct Mx {
   using Store = __nv_bfloat16;
-  static constexpr int WF = 32, FG = 4, KG = 2, STEP = 128;
+  static constexpr int WF = 32, FG = 4, KG = 2, STEP = 256;
   static constexpr int PITCH = FG * WF + 1;   // of the results [row][column] in shared memory
   static constexpr int kMaxTiles = 2;
   static constexpr bool kRowPerLane = true, kHalfRows = true;
-  // A warp's ring of steps in shared memory: 32 columns of 64 bytes each.
-  static constexpr int kRing = 4, kSlotBytes = WF * STEP / 2;
+  // A warp's ring of steps in shared memory: 32 columns of 128 bytes each.
+  static constexpr int kRing = 2, kSlotBytes = WF * STEP / 2;
 
   static __device__ __forceinline__ void mma(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
                                              uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -543,24 +548,34 @@ struct Mx {
     return h * 0x00010001u;
   }
 
-  // What brings the activations' block b to the row's power of two.
-  static __device__ __forceinline__ uint32_t row_factor(const Row& r, int b) {
-    const uint32_t p = ld_u8(r.scale + b);
-    return p == 255u ? 0x7e007e00u : pow2_down(static_cast<int>(p) - r.top);
+  // fp16 rows lie as the lanes read them: of each 256 values (a step of a warp) the
+  // blocks 2 t of all lanes come before the blocks 2 t + 1, and the 16-byte chunks q
+  // of a half's four blocks side by side.
+  static __host__ __device__ __forceinline__ int pitch(int K) { return (K + STEP - 1) / STEP * STEP; }
+  static __host__ __device__ __forceinline__ int scale_pitch(int K) { return (K / 32 + 1) & ~1; }
+  // Where chunk i (values 8 i .. 8 i + 7) of a row is.
+  static __device__ __forceinline__ int chunk_at(int i) {
+    const int b = i >> 2;
+    return (i & ~31) | (b & 1) << 4 | (i & 3) << 2 | ((b >> 1) & 3);
   }
-  static __device__ __forceinline__ uint4 row_vec(const Row& r, int b, int q) {
-    return ld_u128(static_cast<const __half*>(r.p) + 32 * b + 8 * q);
+  static __device__ __forceinline__ uint4 row_vec(const void* p, int q) {
+    return ld_u128(static_cast<const char*>(p) + q * 64);
+  }
+  // What brings an activation block with this scale byte to the row's power of two.
+  static __device__ __forceinline__ uint32_t row_factor(uint32_t p, int top) {
+    return p == 255u ? 0x7e007e00u : pow2_down(static_cast<int>(p) - top);
   }
 
-  // The codes of step s of a unit, 128 bytes of each of 128 columns, and the line
-  // of their scales.
+  // The codes of step s of a unit, KG lines of each column, and the lines of their
+  // scales.
   static __device__ __forceinline__ void prefetch(const void* w, const uint8_t* scales, int64_t first,
                                                   int64_t ld, int col, int K, int s) {
-    const int64_t c = col + threadIdx.x;
-    const int b = s * KG * STEP;
-    if (threadIdx.x >= FG * WF || c >= ld || b >= K) return;
-    prefetch_l2(static_cast<const uint8_t*>(w) + first / 2 + c * (K >> 1) + b / 2);
-    prefetch_l2(scales + first / 32 + c * (K >> 5) + b / 32);
+    static_assert(FG * WF * KG == kThreads, "a line per thread");
+    const int64_t c = col + threadIdx.x / KG;
+    const int k = (s * KG + threadIdx.x % KG) * STEP;
+    if (c >= ld || k >= K) return;
+    prefetch_l2(static_cast<const uint8_t*>(w) + first / 2 + c * (K >> 1) + k / 2);
+    if (threadIdx.x % KG == 0) prefetch_l2(scales + first / 32 + c * (K >> 5) + k / 32);
   }
   // Token rows times the row's factor for a block (gate_up's have one scale).
   template <int PHASE>
@@ -572,10 +587,12 @@ struct Mx {
   // release() gives their place to a later step's.
   template <int NT, int PHASE, class Ring>
   static __device__ __forceinline__ void run(Ring& ring, const uint8_t* scales, int col, int K, int s0,
-                                             int s1, int kg, const Row* rows, int nrows, float* red) {
-    // Scale bytes, and with one row tile the tokens, are loaded two steps ahead; with
-    // two there are no registers for that.  Codes past the end are zeros, whatever
-    // their scale and tokens (the last block's).
+                                             int s1, int kg, const void* x_rows, const uint8_t* x_scales,
+                                             const Row* rows, int nrows, float* red) {
+    // A step is two halves: lane t takes the blocks 2 t and 2 t + 1 of a column's
+    // eight.  Scale bytes, and with one row tile the tokens, are loaded a step ahead;
+    // with two there are no registers for that.  Codes past the end are zeros,
+    // whatever their scale and tokens (the last step's).
     constexpr bool EARLY = NT == 1;
     const bool both = NT > 1 && nrows > 8;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -587,36 +604,52 @@ struct Mx {
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[m][n][q] = 0.f;
-    const uint8_t* sp = scales + (static_cast<int64_t>(col) + g) * nb;
-    uint32_t byte[2][4];
+    int b = (s0 * KG + kg) * 8 + 2 * t;         // the blocks whose loads are next: b, b + 1
+    const uint8_t* sp = scales + (static_cast<int64_t>(col) + g) * nb + b;
+    // two scale bytes in one load where every pair is aligned
+    const bool pairs = ((nb | static_cast<int>(reinterpret_cast<uintptr_t>(scales))) & 1) == 0;
+    const char* xp = static_cast<const char*>(x_rows) +
+                     2 * (static_cast<int64_t>(rows[0].row) * pitch(K) + (s0 * KG + kg) * STEP + 8 * t);
+    uint32_t bytes[4], bytes_next[4], xs = 0, xs_next = 0;
     uint4 x[2][EARLY ? 4 : 1];
-    uint32_t xf[2] = {0, 0};
-    auto block = [&](int s) { return min((s * KG + kg) * 4 + t, nb - 1); };
-    auto load_bytes = [&](int buf, int s) {
-      if (s >= s1) return;
-      const uint8_t* p = sp + block(s);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) byte[buf][r] = __ldg(p + r * 8 * nb);
-    };
-    auto load_x = [&](int buf, int s) {
-      if (!EARLY || s >= s1) return;
-      const int b = block(s);
+    for (int r = 0; r < 4; ++r) bytes_next[r] = 127 * 0x101, x[0][r % (EARLY ? 4 : 1)] = x[1][r % (EARLY ? 4 : 1)] = make_uint4(0, 0, 0, 0);
+    auto load_bytes = [&]() {
+      if (pairs) {
+        if (b < nb) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) x[buf][q % (EARLY ? 4 : 1)] = row_vec(rows[0], b, q);
-      if (PHASE == 1) xf[buf] = row_factor(rows[0], b);
+          for (int r = 0; r < 4; ++r) bytes_next[r] = ld_u16(sp + r * 8 * nb);
+        }
+      } else if (b < nb) {
+        const int d = b + 1 < nb;               // past the end: the last block's
+#pragma unroll
+        for (int r = 0; r < 4; ++r) bytes_next[r] = ld_u8(sp + r * 8 * nb) | ld_u8(sp + r * 8 * nb + d) << 8;
+      }
     };
-    load_bytes(0, s0);
-    load_bytes(1, s0 + 1);
+    auto load_x = [&](int u) {
+      if (EARLY && b + u < nb) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[u][q % (EARLY ? 4 : 1)] = row_vec(xp + u * 256, q);
+      }
+    };
+    auto load_xs = [&]() {
+      if (EARLY && PHASE == 1 && b < nb) {
+        xs_next = ld_u16(x_scales + rows[0].row * scale_pitch(K) + b);
+        if (b + 1 == nb) xs_next = (xs_next & 0xffu) * 0x101u;
+      }
+    };
+    load_bytes();
     wait_for_rows();
-    load_x(0, s0);
-    load_x(1, s0 + 1);
+    load_x(0);
+    load_x(1);
+    load_xs();
     int ref[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      ref[r] = min(240, static_cast<int>(__shfl_sync(0xffffffffu, byte[0][r], lane & 28)));
-    auto step = [&](int buf, int s) {
+      ref[r] = min(240, static_cast<int>(__shfl_sync(0xffffffffu, bytes_next[r] & 0xffu, lane & 28)));
+    // half u of a step, its codes at shared address `at`
+    auto half = [&](int u, int s, uint32_t at) {
       uint4 v[4];
-      const uint32_t at = ring.wait() + (g * 4 + t) * 16;
 #pragma unroll
       for (int r = 0; r < 4; ++r) v[r] = ld_shared_v4(at + r * 8 * (STEP / 2));
       // 2^(q - ref) in fp16, in range for -14 .. 13 (ref <= 240: a NaN's 255 is not)
@@ -624,7 +657,7 @@ struct Mx {
       bool far = false;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const uint32_t d = byte[buf][r] - ref[r] + 14;
+        const uint32_t d = (u ? bytes[r] >> 8 : bytes[r] & 0xffu) - ref[r] + 14;
         far = far || d > 27u;
         f[r] = d * 0x04000400u + 0x04000400u;
       }
@@ -632,19 +665,32 @@ struct Mx {
         far = false;   // a block of zeros needs no scale
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          if (byte[buf][r] - ref[r] + 14 > 27u) {
-            far = far || (v[r].x | v[r].y | v[r].z | v[r].w) != 0 || byte[buf][r] == 255u;
+          const uint32_t byte = u ? bytes[r] >> 8 : bytes[r] & 0xffu;
+          if (byte - ref[r] + 14 > 27u) {
+            far = far || (v[r].x | v[r].y | v[r].z | v[r].w) != 0 || byte == 255u;
             f[r] = 0x3c003c00u;
           }
         }
         far = __any_sync(0xffffffffu, far);
       }
-      if (far) {
-        far_step<NT, PHASE, EARLY>(v, byte[buf], x[buf], xf[buf], block(s), ref, rows, acc);
-      } else {
-        uint32_t fxs[NT];
+      uint32_t fx[NT];
+      const void* xp[NT];
+      const int here = (s * KG + kg) * 8 + 2 * t + u;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) fxs[n] = EARLY || PHASE == 0 ? xf[buf] : row_factor(rows[n], block(s));
+      for (int n = 0; n < NT; ++n) {
+        fx[n] = 0;
+        // past the end: block 0, which every row has
+        xp[n] = static_cast<const __half*>(x_rows) + rows[n].row * pitch(K) +
+                (here < nb ? (s * KG + kg) * STEP + u * (STEP / 2) + 8 * t : 0);
+        if (PHASE == 1) {
+          const uint32_t byte =
+              EARLY ? (u ? xs >> 8 : xs & 0xffu) : ld_u8(x_scales + rows[n].row * scale_pitch(K) + (here < nb ? here : 0));
+          fx[n] = row_factor(byte, rows[n].top);
+        }
+      }
+      if (far) {
+        far_step<NT, PHASE, EARLY>(v, bytes, u, x[u], xp, fx, ref, acc);
+      } else {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t a[4][4];
@@ -657,8 +703,7 @@ struct Mx {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             if (n > 0 && !both) continue;
-            const uint4 xv =
-                scaled<PHASE>(EARLY ? x[buf][q % (EARLY ? 4 : 1)] : row_vec(rows[n], block(s), q), fxs[n]);
+            const uint4 xv = scaled<PHASE>(EARLY ? x[u][q % (EARLY ? 4 : 1)] : row_vec(xp[n], q), fx[n]);
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
               mma(acc[m][n], a[2 * m][0], a[2 * m + 1][0], a[2 * m][1], a[2 * m + 1][1], xv.x, xv.y);
@@ -667,13 +712,23 @@ struct Mx {
           }
         }
       }
-      load_bytes(buf, s + 2);
-      load_x(buf, s + 2);
-      ring.release();
+      load_x(u);
     };
-    for (int s = s0; s < s1; s += 2) {
-      step(0, s);
-      if (s + 1 < s1) step(1, s + 1);
+    // the copies' swizzle has chunk j of row g at j ^ (g & 7): no bank conflicts
+    const uint32_t mine = g * (STEP / 2) + ((2 * t) ^ g) * 16;
+    for (int s = s0; s < s1; ++s) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) bytes[r] = bytes_next[r];
+      xs = xs_next;
+      b = s + 1 < s1 ? b + KG * 8 : nb;        // (no loads after the last)
+      sp += KG * 8;
+      xp += KG * 2 * STEP;
+      load_bytes();
+      load_xs();
+      const uint32_t at = ring.wait() + mine;
+      half(0, s, at);
+      half(1, s, at ^ 16u);
+      ring.release();
     }
     // the sums' powers of two: the columns' refs and the token rows' tops
 #pragma unroll
@@ -693,16 +748,17 @@ struct Mx {
   // A step with far scales: the four lanes' blocks one after the other, codes as
   // they are, each block's sums scaled by 2^(q - ref) in fp32.
   template <int NT, int PHASE, bool EARLY>
-  static __device__ __forceinline__ void far_step(const uint4 (&v)[4], const uint32_t (&bytes)[4],
-                                                  const uint4* x, uint32_t xf, int b, const int (&ref)[4],
-                                                  const Row* rows, float (&acc)[2][NT][4]) {
+  static __device__ __forceinline__ void far_step(const uint4 (&v)[4], const uint32_t (&bytes)[4], int u,
+                                                  const uint4* x, const void* const (&xp)[NT],
+                                                  const uint32_t (&fx)[NT], const int (&ref)[4],
+                                                  float (&acc)[2][NT][4]) {
     const int lane = threadIdx.x & 31, t = lane & 3;
 #pragma unroll 1
     for (int turn = 0; turn < 4; ++turn) {
       float f[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const uint32_t byte = __shfl_sync(0xffffffffu, bytes[r], (lane & 28) | turn);
+        const uint32_t byte = __shfl_sync(0xffffffffu, bytes[r], (lane & 28) | turn) >> 8 * u & 0xffu;
         f[r] = byte == 255u ? __uint_as_float(0x7fc00000u) : ldexpf(1.f, static_cast<int>(byte) - ref[r]);
       }
 #pragma unroll
@@ -710,13 +766,12 @@ struct Mx {
         float c[2][4];
 #pragma unroll
         for (int m = 0; m < 2; ++m) c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
-        const uint32_t fx = EARLY || PHASE == 0 ? xf : row_factor(rows[n], b);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t a[4][4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) decode(t == turn ? word(v[r], q) : 0u, a[r]);
-          uint4 xv = scaled<PHASE>(EARLY ? x[q] : row_vec(rows[n], b, q), fx);
+          uint4 xv = scaled<PHASE>(EARLY ? x[q] : row_vec(xp[n], q), fx[n]);
           if (t != turn) xv = make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
@@ -811,7 +866,7 @@ __global__ void __launch_bounds__(256) few_half_rows_kernel(const void* __restri
     uint4 u;
     u.x = pack_half(v[0] * f, v[1] * f), u.y = pack_half(v[2] * f, v[3] * f);
     u.z = pack_half(v[4] * f, v[5] * f), u.w = pack_half(v[6] * f, v[7] * f);
-    reinterpret_cast<uint4*>(out)[base + i] = u;
+    reinterpret_cast<uint4*>(out)[row * static_cast<int64_t>(Mx::pitch(H) / 8) + Mx::chunk_at(i)] = u;
   }
   if (threadIdx.x == 0) top[row] = static_cast<int>(byte);
 }
@@ -866,10 +921,10 @@ __host__ __device__ constexpr int ring_slot() {
   if constexpr (W::kRing > 0) return W::kSlotBytes;
   return 0;
 }
-// Bytes of the warps' rings, their barriers and the way to a multiple of 128.
+// Bytes of the warps' rings, their barriers and the way to a multiple of 1024.
 template <class W>
 __host__ __device__ constexpr int ring_bytes() {
-  return W::kRing ? kThreads / 32 * W::kRing * (ring_slot<W>() + 8) + 112 : 0;
+  return W::kRing ? kThreads / 32 * W::kRing * (ring_slot<W>() + 8) + 1008 : 0;
 }
 
 // The biases of this thread's output in a unit: thread i has output i % OUT of every
@@ -900,17 +955,18 @@ __device__ __forceinline__ void finish_gate_up(const FewArgs& a, const Plan& p, 
     const float gate = q[a.interleaved ? 2 * f : f] + bias.x;
     const float up = q[a.interleaved ? 2 * f + 1 : f + OUT] + bias.y;
     const float v = activate(a, gate, up);
-    const int64_t at = static_cast<int64_t>(p.slot[first + r]) * a.I + feature;
+    const int64_t slot = p.slot[first + r];
     if constexpr (!W::kHalfRows) {
-      static_cast<S*>(a.act)[at] = static_cast<S>(v);
+      static_cast<S*>(a.act)[slot * a.I + feature] = static_cast<S>(v);
     } else {
       // a warp has the 32 values of one block (I is a multiple of 32)
       const uint32_t byte =
           half_block_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu));
-      static_cast<__half*>(a.act)[at] = __float2half_rn(v * mx_inv_scale(byte));
+      static_cast<__half*>(a.act)[slot * W::pitch(a.I) + 8 * W::chunk_at(feature >> 3) + (feature & 7)] =
+          __float2half_rn(v * mx_inv_scale(byte));
       if ((threadIdx.x & 31) == 0) {
-        a.act_scale[at >> 5] = static_cast<uint8_t>(byte);
-        if (byte != 255u) atomicMax(a.act_top + p.slot[first + r], static_cast<int>(byte));
+        a.act_scale[slot * W::scale_pitch(a.I) + (feature >> 5)] = static_cast<uint8_t>(byte);
+        if (byte != 255u) atomicMax(a.act_top + slot, static_cast<int>(byte));
       }
     }
   }
@@ -1034,7 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   const int fg = warp % W::FG, kg = warp / W::FG;
   uint32_t slots = 0, bars = 0;                // this warp's ring
   if (W::kRing > 0) {
-    slots = (smem_u32(dynamic) + red_floats<W>(a.rows) * 4 + plan_bytes(a.T * a.k, a.E, a.rows) + 127) & ~127u;
+    slots = (smem_u32(dynamic) + red_floats<W>(a.rows) * 4 + plan_bytes(a.T * a.k, a.E, a.rows) + 1023) & ~1023u;
     bars = slots + kThreads / 32 * W::kRing * ring_slot<W>() + warp * W::kRing * 8;
     slots += warp * W::kRing * ring_slot<W>();
     if (lane == 0) {
@@ -1084,12 +1140,13 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   };
 
   // The ring runs through all of the block's steps, whatever unit they are of.
+  constexpr uint32_t kSlots = W::kRing ? W::kRing : 1;   // a power of two
   struct Ring {
     int next, left;            // the step to load next; steps left of its unit
     int k, col, e;             // where its codes are
-    uint32_t put, got;
-  } at = {begin, 0, 0, 0, 0, 0, 0};
-  auto load_next = [&] {
+    uint32_t used;             // steps taken out
+  } at = {begin, 0, 0, 0, 0, 0};
+  auto load_next = [&](uint32_t slot) {
     while (at.left == 0) {
       if (at.next >= end) return;
       const int unit = quotient(at.next, KS, inv_KS), tile = quotient(unit, chunks, inv_chunks);
@@ -1105,11 +1162,10 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       at.e = p.chunk_e[unit - tile * chunks];
     }
     if (lane == 0) {
-      const uint32_t i = at.put % (W::kRing ? W::kRing : 1);
-      mbar_arrive_expect_tx(bars + 8 * i, ring_slot<W>());
-      tma_load_3d(slots + i * ring_slot<W>(), &a.codes, bars + 8 * i, at.k, at.col, at.e);
+      mbar_arrive_expect_tx(bars + 8 * slot, ring_slot<W>());
+      tma_load_3d(slots + slot * ring_slot<W>(), &a.codes, bars + 8 * slot, at.k, at.col, at.e);
     }
-    ++at.put, ++at.next, --at.left;
+    ++at.next, --at.left;
     at.k += W::KG * W::STEP / 2;
   };
   struct {
@@ -1119,19 +1175,18 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     uint64_t timeout_ns;
     int* err;
     __device__ __forceinline__ uint32_t wait() {
-      constexpr uint32_t S = W::kRing ? W::kRing : 1;
-      const uint32_t i = at.got % S;
-      if (!mbar_wait(bars + 8 * i, at.got / S & 1, timeout_ns)) record_error(err, kErrTimeout);
-      return slots + i * ring_slot<W>();
+      const uint32_t slot = at.used % kSlots;
+      if (!mbar_wait(bars + 8 * slot, at.used / kSlots & 1, timeout_ns)) record_error(err, kErrTimeout);
+      return slots + slot * ring_slot<W>();
     }
     __device__ __forceinline__ void release() {
-      ++at.got;
       __syncwarp();
-      load();
+      load(at.used % kSlots);
+      ++at.used;
     }
   } ring = {load_next, at, slots, bars, a.timeout_ns, a.err};
   if (W::kRing > 0)
-    for (int i = 0; i < W::kRing; ++i) load_next();
+    for (int i = 0; i < W::kRing; ++i) load_next(i);
 
   for (int s = begin; s < end;) {
     const int unit = quotient(s, KS, inv_KS);
@@ -1152,9 +1207,10 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       const int r = W::kRowPerLane ? 8 * i + (lane >> 2) : i;
       const int slot = p.slot[first + (r < nrows ? r : 0)];
       const int64_t row = PHASE == 0 ? slot / a.k : slot;
-      rows[i].p = static_cast<const S*>(a.x) + row * K;   // (fp16 rows: of the same size)
-      if (W::kHalfRows) {
-        if (PHASE == 1) rows[i].scale = a.x_scale + row * (K >> 5);
+      if constexpr (!W::kHalfRows) {
+        rows[i].p = static_cast<const S*>(a.x) + row * K;
+      } else {
+        rows[i].row = static_cast<int>(row);
         wait_for_rows();
         rows[i].top = static_cast<int>(ld_u32(a.top + row));
       }
@@ -1163,7 +1219,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       const int64_t we = static_cast<int64_t>(e) * K * N;   // weights of the experts before
       float* out = red + kg * SHARE + fg * W::WF;
       if constexpr (W::kRing > 0)
-        W::template run<NT, PHASE>(ring, a.scales + we / 32, col, K, ks0, ks1, kg, rows, nrows, out);
+        W::template run<NT, PHASE>(ring, a.scales + we / 32, col, K, ks0, ks1, kg, a.x, a.x_scale, rows, nrows,
+                                    out);
       else
         W::template run<NT>(static_cast<const S*>(a.w) + we, N, col, ncol, K, ks0, ks1, kg, rows, nrows, out);
     }
@@ -1219,7 +1276,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   if (PHASE == 0) {
     const int tiles2 = (a.H + CW - 1) / CW, KS2 = (a.I + W::KG * W::STEP - 1) / (W::KG * W::STEP);
     const Runs next(chunks * tiles2 * KS2, gridDim.x);
-    const int from = next.begin(me), to = me < next.grid ? min(next.begin(me + 1), from + kPrefetchSteps) : 0;
+    const int from = next.begin(me), to = me < next.grid ? min(next.begin(me + 1), from + kPrefetchSteps / (W::kRing ? 2 : 1)) : 0;
     const float inv_KS2 = 1.f / static_cast<float>(KS2);
 #pragma unroll 1
     for (int s = from; s < to; ++s) {
@@ -1335,11 +1392,11 @@ FewLayout few_layout(const moe_shape* s) {
   const size_t Tk = static_cast<size_t>(s->T) * s->k;
   L.counters0 = take(sizeof(unsigned) * kMaxGrid);
   L.counters1 = take(sizeof(unsigned) * ((s->H + 63) / 64));
-  L.rows = take((s->dtype == MOE_FP32 ? 4 : 2) * static_cast<size_t>(s->T) * s->H);
+  L.rows = take((s->dtype == MOE_FP32 ? 4 : 2) * static_cast<size_t>(s->T) * Mx::pitch(s->H));
   L.top = take(sizeof(int) * static_cast<size_t>(s->T));
   L.act_top = take(sizeof(int) * Tk);
-  L.act_scale = take(Tk * (s->I / 32 + 1));
-  L.act = take((s->dtype == MOE_FP32 ? 4 : 2) * Tk * s->I);
+  L.act_scale = take(Tk * Mx::scale_pitch(s->I));
+  L.act = take((s->dtype == MOE_FP32 ? 4 : 2) * Tk * Mx::pitch(s->I));
   L.part = take(sizeof(float) * 2 * kMaxGrid * kMaxCW * (s->T <= 8 ? 8 : 16));
   L.o = take(sizeof(float) * Tk * s->H);
   L.total = off;
@@ -1424,8 +1481,10 @@ moe_status moe_ffn_few(const moe_shape* s, const void* x, const uint8_t* x_scale
   a.alpha = s->alpha;
   a.timeout_ns = abi_wait_timeout_ns();
   CUtensorMap down_codes;
-  if (mx && !(abi_map_bytes(&a.codes, mx->codes_gate_up, s->H / 2, 2 * static_cast<uint64_t>(s->I), s->E, Mx::STEP / 2, Mx::WF) &&
-              abi_map_bytes(&down_codes, mx->codes_down, s->I / 2, s->H, s->E, Mx::STEP / 2, Mx::WF)))
+  if (mx && !(abi_map_bytes(&a.codes, mx->codes_gate_up, s->H / 2, 2 * static_cast<uint64_t>(s->I), s->E,
+                            Mx::STEP / 2, Mx::WF, CU_TENSOR_MAP_SWIZZLE_128B) &&
+              abi_map_bytes(&down_codes, mx->codes_down, s->I / 2, s->H, s->E, Mx::STEP / 2, Mx::WF,
+                            CU_TENSOR_MAP_SWIZZLE_128B)))
     return MOE_ERR_CUDA;
   const int nt = row_tiles(s, mx != nullptr);
   a.rows = 8 * nt;
