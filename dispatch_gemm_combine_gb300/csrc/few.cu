@@ -940,8 +940,9 @@ __device__ __forceinline__ float2 unit_bias(const FewArgs& a, int e, int tile) {
                      load_elem(b, a.interleaved ? 2 * feature + 1 : a.I + feature));
 }
 
-// The activation of a unit's results, red[row][column], into its rows of a.act.
-template <class W>
+// The activation of a unit's results, the sums of `shares` of red[share][row][column],
+// into its rows of a.act.
+template <class W, int SHARES>
 __device__ __forceinline__ void finish_gate_up(const FewArgs& a, const Plan& p, const float* red,
                                                int chunk, int tile, float2 bias) {
   using S = typename W::Store;
@@ -952,8 +953,14 @@ __device__ __forceinline__ void finish_gate_up(const FewArgs& a, const Plan& p, 
   if (feature >= a.I) return;
   for (int r = threadIdx.x / OUT; r < nrows; r += kThreads / OUT) {
     const float* q = red + r * W::PITCH;
-    const float gate = q[a.interleaved ? 2 * f : f] + bias.x;
-    const float up = q[a.interleaved ? 2 * f + 1 : f + OUT] + bias.y;
+    const int at_gate = a.interleaved ? 2 * f : f, at_up = a.interleaved ? 2 * f + 1 : f + OUT;
+    float gate = q[at_gate], up = q[at_up];
+#pragma unroll
+    for (int j = 1; j < SHARES; ++j) {
+      q += a.rows * W::PITCH;
+      gate += q[at_gate], up += q[at_up];
+    }
+    gate += bias.x, up += bias.y;
     const float v = activate(a, gate, up);
     const int64_t slot = p.slot[first + r];
     if constexpr (!W::kHalfRows) {
@@ -1082,15 +1089,16 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   const int SHARE = a.rows * W::PITCH;         // one share's results in shared memory
   constexpr int OUT = PHASE == 0 ? CW / 2 : CW;
   extern __shared__ float4 dynamic[];          // results, plan
-  float* red = reinterpret_cast<float*>(dynamic);
+  float* const reds = reinterpret_cast<float*>(dynamic);
+  float* red = reds;
   __shared__ PlanSmall ps;
-  Plan p = plan_at(red + red_floats<W>(a.rows), a.T * a.k, a.E, a.rows);
+  Plan p = plan_at(reds + 2 * red_floats<W>(a.rows), a.T * a.k, a.E, a.rows);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int fg = warp % W::FG, kg = warp / W::FG;
   uint32_t slots = 0, bars = 0;                // this warp's ring
   if (W::kRing > 0) {
-    slots = (smem_u32(dynamic) + red_floats<W>(a.rows) * 4 + plan_bytes(a.T * a.k, a.E, a.rows) + 1023) & ~1023u;
+    slots = (smem_u32(dynamic) + red_floats<W>(a.rows) * 8 + plan_bytes(a.T * a.k, a.E, a.rows) + 1023) & ~1023u;
     bars = slots + kThreads / 32 * W::kRing * ring_slot<W>() + warp * W::kRing * 8;
     slots += warp * W::kRing * ring_slot<W>();
     if (lane == 0) {
@@ -1160,6 +1168,9 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       at.left = stop - at.next;
       at.k = ((at.next - unit * KS) * W::KG + kg) * (W::STEP / 2);
       at.e = p.chunk_e[unit - tile * chunks];
+      // the first of the unit's scale bytes, a column per lane
+      prefetch_l2(a.scales + (static_cast<int64_t>(at.e) * N + min(at.col + lane, N - 1)) * (K >> 5) +
+                  min(at.k >> 4, (K >> 5) - 1));
     }
     if (lane == 0) {
       mbar_arrive_expect_tx(bars + 8 * slot, ring_slot<W>());
@@ -1224,34 +1235,39 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       else
         W::template run<NT>(static_cast<const S*>(a.w) + we, N, col, ncol, K, ks0, ks1, kg, rows, nrows, out);
     }
+    const bool whole = ks1 - ks0 == KS;
+    float2 bias = make_float2(0.f, 0.f);
+    if (PHASE == 0 && whole) bias = unit_bias<W>(a, e, tile);
     __syncthreads();
 
-    // add the shares of the contraction; a cut unit's sum goes to its part, a
-    // whole one stays (gate_up) or goes to its rows (down)
-    const bool whole = ks1 - ks0 == KS;
-    float* part = a.part + (2 * static_cast<int64_t>(me) + (begin >= u0 ? 0 : 1)) * UNIT;
-    for (int i = tid; i < nrows * CW; i += kThreads) {
-      const int f = i % CW, r = i / CW, q = r * W::PITCH + f;
-      float v = red[q];
-#pragma unroll
-      for (int j = 1; j < W::KG; ++j) v += red[j * SHARE + q];
-      if (!whole)
-        part[i] = v;
-      else if (PHASE == 0)
-        red[q] = v;
-      else if (tile * OUT + f < a.H)
-        a.o[static_cast<int64_t>(p.slot[first + r]) * a.H + tile * OUT + f] = v;
-    }
-    __syncthreads();
+    // A whole unit of gate_up is finished here; else the shares of the contraction
+    // are added, a cut unit's into its part, a whole one's into its rows of o.
     if (PHASE == 0 && whole) {
-      finish_gate_up<W>(a, p, red, chunk, tile, unit_bias<W>(a, e, tile));
-      __syncthreads();
+      finish_gate_up<W, W::KG>(a, p, red, chunk, tile, bias);
+    } else {
+      float* part = a.part + (2 * static_cast<int64_t>(me) + (begin >= u0 ? 0 : 1)) * UNIT;
+      for (int i = tid; i < nrows * CW; i += kThreads) {
+        const int f = i % CW, r = i / CW, q = r * W::PITCH + f;
+        float v = red[q];
+#pragma unroll
+        for (int j = 1; j < W::KG; ++j) v += red[j * SHARE + q];
+        if (!whole)
+          part[i] = v;
+        else if (tile * OUT + f < a.H)
+          a.o[static_cast<int64_t>(p.slot[first + r]) * a.H + tile * OUT + f] = v;
+      }
     }
+    // the next unit's results go to the other half of `red`, so that they need not
+    // wait for these to be read
+    red = red == reds ? reds + red_floats<W>(a.rows) : reds;
     // a tile that lies in this run alone
-    if (PHASE == 1 && chunk == chunks - 1 && ks1 == KS && begin <= tile * chunks * KS)
+    if (PHASE == 1 && chunk == chunks - 1 && ks1 == KS && begin <= tile * chunks * KS) {
+      __syncthreads();
       combine_tile<W>(a, p, runs, KS, tile, red);
+    }
     s = u0 + ks1;
   }
+  __syncthreads();
 
   wait_for_rows();   // (warps without columns have not yet)
 
@@ -1312,7 +1328,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
     }
     __syncthreads();
-    finish_gate_up<W>(a, p, red, chunk, tile, bias);
+    finish_gate_up<W, 1>(a, p, red, chunk, tile, bias);
     __syncthreads();
   }
 }
@@ -1320,8 +1336,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
 // `after`: may start while the kernel before it, which writes its rows, ends.
 template <class W, int PHASE, int NT>
 cudaError_t launch(const FewArgs& a, int grid, bool after, cudaStream_t st) {
-  const int smem = red_floats<W>(a.rows) * 4 + plan_bytes(a.T * a.k, a.E, a.rows) + ring_bytes<W>();
-  const int most = red_floats<W>(8 * NT) * 4 + kMostPlanBytes + ring_bytes<W>();
+  const int smem = red_floats<W>(a.rows) * 8 + plan_bytes(a.T * a.k, a.E, a.rows) + ring_bytes<W>();
+  const int most = red_floats<W>(8 * NT) * 8 + kMostPlanBytes + ring_bytes<W>();
   static std::atomic<uint64_t> ready{0};   // one bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
