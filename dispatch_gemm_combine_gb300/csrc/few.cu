@@ -292,7 +292,7 @@ __device__ __forceinline__ uint32_t ld_u8(const void* p) {
 }
 __device__ __forceinline__ uint32_t ld_u16(const void* p) {
   uint32_t v;
-  asm volatile("{\n\t.reg .u16 h;\n\tld.global.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "l"(p) : "memory");
+  asm volatile("ld.global.u16 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t ld_u32(const void* p) {
@@ -661,7 +661,7 @@ struct Mx {
         far = far || d > 27u;
         f[r] = d * 0x04000400u + 0x04000400u;
       }
-      if (__any_sync(0xffffffffu, far)) {
+      if (__builtin_expect(__any_sync(0xffffffffu, far), 0)) {
         far = false;   // a block of zeros needs no scale
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -688,7 +688,7 @@ struct Mx {
           fx[n] = row_factor(byte, rows[n].top);
         }
       }
-      if (far) {
+      if (__builtin_expect(far, 0)) {
         far_step<NT, PHASE, EARLY>(v, bytes, u, x[u], xp, fx, ref, acc);
       } else {
 #pragma unroll
