@@ -211,6 +211,78 @@ def test_non_finite_tokens_stay_apart():
     assert torch.isnan(y[2]).all() and torch.isfinite(y[[0, 1, 3, 4, 5]]).all()
 
 
+@pytest.mark.parametrize("T,H,I,E,k", [(5, 96, 352, 6, 2), (30, 1056, 288, 4, 2), (24, 416, 544, 3, 2),
+                                       (2, 2080, 736, 12, 4)])
+def test_microscaled_odd_blocks_and_wide_scales(T, H, I, E, k):
+    """Contractions that end inside a step, odd counts of blocks, and scales far from
+    their column's first one."""
+    check(make(T, H, I, E, k, SWIGLU, "mx", bias=True))
+    c = make(T, H, I, E, k, CLAMPED, "mx", x8=True, seed=1)
+    g = torch.Generator().manual_seed(2)
+    for s in (c["mx"][1], c["mx"][3]):
+        s.copy_(torch.randint(100, 128, s.shape, generator=g))
+    c["wgu"], c["wd"] = mx_values(*c["mx"][:2]), mx_values(*c["mx"][2:])
+    check(c)
+
+
+def test_microscaled_scales_at_odd_addresses():
+    c = make(20, 128, 320, 6, 2, SWIGLU, "mx")
+    a, _ = run(c)
+    s = moe.Shape(20, 128, 320, 6, 2, SWIGLU, moe.MOE_BF16, 7.0, 1.702, 0, 0)
+    d = [v.cuda() for v in c["mx"]]
+    for i in (1, 3):
+        odd = torch.empty(d[i].numel() + 1, dtype=torch.uint8, device="cuda")[1:]
+        odd.copy_(d[i].flatten())
+        d[i] = odd.view(d[i].shape)
+        assert d[i].data_ptr() % 2 == 1
+    y = torch.empty(20, 128, device="cuda", dtype=torch.bfloat16)
+    moe.ffn_few(s, c["x"].cuda(), c["idx"].cuda(), c["w"].cuda(), None, None, y, moe.few_workspace(s),
+                mx=moe.mx_struct(*d))
+    assert torch.equal(y.cpu(), a)
+
+
+@pytest.mark.parametrize("T,H,I", [(6, 64, 64), (6, 352, 96), (20, 96, 288)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_non_finite_tokens_stay_apart_on_4_bits(T, H, I, bad):
+    c = make(T, H, I, 3, 2, SWIGLU, "mx")
+    c["x"][2, 7] = bad
+    y, _ = run(c)
+    others = [t for t in range(T) if t != 2]
+    assert torch.isnan(y[2]).all() and torch.isfinite(y[others]).all()
+
+
+@pytest.mark.parametrize("mx", [True, False])
+def test_experts_past_32_bits(mx):
+    """The last of many experts gives the bits that it gives alone."""
+    H, I, E = (4096, 4096, 300) if mx else (2048, 2048, 300)
+    g = torch.Generator("cuda").manual_seed(3)
+    if mx:
+        one = [torch.randint(0, 256, (1, n, k // 2), generator=g, device="cuda", dtype=torch.uint8)
+               for n, k in ((2 * I, H), (H, I))]
+        one = [one[0], torch.randint(118, 122, (1, 2 * I, H // 32), generator=g, device="cuda", dtype=torch.uint8),
+               one[1], torch.randint(118, 122, (1, H, I // 32), generator=g, device="cuda", dtype=torch.uint8)]
+    else:
+        one = [0.02 * torch.randn(s, generator=g, device="cuda", dtype=torch.bfloat16)
+               for s in ((1, H, 2 * I), (1, I, H))]
+    x = torch.randn((3, H), generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.ones((3, 1), device="cuda")
+    out = []
+    for n in (1, E):
+        ts = []
+        for t in one:
+            big = torch.empty((n,) + t.shape[1:], dtype=t.dtype, device="cuda")
+            big[n - 1] = t[0]
+            ts.append(big)
+        s = moe.Shape(3, H, I, n, 1, SWIGLU)
+        idx = torch.full((3, 1), n - 1, dtype=torch.int32, device="cuda")
+        y = torch.empty((3, H), dtype=torch.bfloat16, device="cuda")
+        moe.ffn_few(s, x, idx, w, None if mx else ts[0], None if mx else ts[1], y, moe.few_workspace(s),
+                    mx=moe.mx_struct(*ts) if mx else None)
+        out.append(y.cpu())
+    assert max(t.numel() * t.element_size() for t in ts) > 2 ** 32
+    assert torch.isfinite(out[0]).all() and torch.equal(*out)
+
+
 def test_bad_ids_are_reported_and_left_out():
     idx = torch.tensor([[0, 9], [-1, 1], [2, 3]])
     c = make(3, 64, 64, 4, 2, SWIGLU, idx=idx)
