@@ -50,6 +50,7 @@ constexpr int kMaxGrid = 512;
 constexpr int kPrefetchSteps = 6;
 constexpr int kMaxCW = 256;       // weight columns of a unit, at most
 constexpr int kNowhere = 0xffff;
+constexpr uint64_t kDrainNs = 200000000ull;   // for copies in flight after a wait ran out
 // the largest plan_bytes(): every chunk, slot and expert there can be
 constexpr int kMostPlanBytes = 4 * kMaxChunks + 4 * kMaxE + 6 * kMaxChunks + 4 * kMaxSlots + 64;
 static_assert(kMaxChunks * 32 < kNowhere, "a slot's place fits 16 bits");
@@ -1150,7 +1151,8 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   // The ring runs through all of the block's steps, whatever unit they are of.
   constexpr uint32_t kSlots = W::kRing ? W::kRing : 1;   // a power of two
   struct Ring {
-    int next, left;            // the step to load next; steps left of its unit
+    int next, left;            // the step to load next; steps left of its unit, or -1:
+                               // a copy did not come in time, no more are made
     int k, col, e;             // where its codes are
     uint32_t used;             // steps taken out
   } at = {begin, 0, 0, 0, 0, 0};
@@ -1186,12 +1188,18 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     uint64_t timeout_ns;
     int* err;
     __device__ __forceinline__ uint32_t wait() {
-      const uint32_t slot = at.used % kSlots;
-      if (!mbar_wait(bars + 8 * slot, at.used / kSlots & 1, timeout_ns)) record_error(err, kErrTimeout);
+      const uint32_t slot = at.used % kSlots, phase = at.used / kSlots & 1;
+      if (__builtin_expect(!__all_sync(0xffffffffu, mbar_try_wait(bars + 8 * slot, phase)), 0)) {
+        if (!__all_sync(0xffffffffu, at.left >= 0 && mbar_wait(bars + 8 * slot, phase, timeout_ns))) {
+          record_error(err, kErrTimeout);
+          at.left = -1;
+        }
+      }
       return slots + slot * ring_slot<W>();
     }
     __device__ __forceinline__ void release() {
       __syncwarp();
+      if (at.left < 0) return;
       load(at.used % kSlots);
       ++at.used;
     }
@@ -1267,6 +1275,9 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
     }
     s = u0 + ks1;
   }
+  if (W::kRing > 0 && at.left < 0)   // no copy is in flight when the block ends
+    for (uint32_t i = at.used; i < at.used + kSlots; ++i)
+      mbar_wait(bars + 8 * (i % kSlots), i / kSlots & 1, kDrainNs);
   __syncthreads();
 
   wait_for_rows();   // (warps without columns have not yet)

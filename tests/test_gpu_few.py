@@ -296,6 +296,35 @@ def test_bad_ids_are_reported_and_left_out():
     assert torch.all(run(c)[0] == 0)
 
 
+def test_wait_limit_unwinds():
+    """A limit of 1 ns on the waits for the codes' copies suffices or is reported, and
+    the next call on the same workspace with the usual limit is right."""
+    c = make(24, 1056, 736, 12, 2, SWIGLU, "mx")
+    s = moe.Shape(24, 1056, 736, 12, 2, SWIGLU, moe.MOE_BF16, 7.0, 1.702, 0, 0)
+    right, ws = run(c)
+    d = [c[n].cuda() for n in ("x", "idx", "w")]
+    mx = [t.cuda() for t in c["mx"]]
+    y = torch.empty(24, 1056, device="cuda", dtype=torch.bfloat16)
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    flush.zero_()             # the codes are not in the L2 cache
+    torch.cuda.synchronize()
+    old = moe.moe_set_wait_timeout_ns(1)
+    try:
+        moe.ffn_few(s, *d, None, None, y, ws, mx=moe.mx_struct(*mx))
+        torch.cuda.synchronize()
+    finally:
+        moe.moe_set_wait_timeout_ns(old)
+    try:                      # (the hardware's own wait may be long enough)
+        moe.check_device_error(ws)
+        assert torch.equal(y.cpu(), right)
+    except moe.MoeError as e:
+        assert e.status == moe.MOE_ERR_TIMEOUT
+    ws[:4] = 0
+    moe.ffn_few(s, *d, None, None, y, ws, mx=moe.mx_struct(*mx))
+    moe.check_device_error(ws)
+    assert torch.equal(y.cpu(), right)
+
+
 def test_agrees_with_the_layer_for_many_tokens():
     from dispatch_gemm_combine_gb300.runner import LayerRunner
     c = make(16, 256, 128, 8, 2, SWIGLU)
