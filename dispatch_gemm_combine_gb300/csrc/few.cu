@@ -3,13 +3,14 @@
 //   gate_up:  a[s]  = act(x[s / k] Wgu[e_s] (+ b_gate_up))      for every slot s
 //   down:     y[t]  = sum_j w[t,j] (a[t k + j] Wd[e] (+ b_down))
 //
+// (A small one before them rewrites e4m3 tokens, or any tokens for 4-bit weights.)
 // With a few rows per expert the layer reads each touched expert's weights once
 // and does next to nothing with them: it is bound by HBM, not by the tensor
-// cores.  So the weights go from global memory straight into registers, as
-// operands of warp-level matrix instructions (weights on the 16-row side, up to
-// 8 tokens per instruction on the other), with no shared-memory ring between,
-// and everything else is arranged to keep loads in flight and every SM busy to
-// the end:
+// cores.  So the weights are operands of warp-level matrix instructions (weights on
+// the 16-row side, up to 8 tokens per instruction on the other): bf16 and fp32 ones
+// go from global memory straight into registers, 4-bit ones through a ring of TMA
+// copies per warp, and everything else is arranged to keep loads in flight and every
+// SM busy to the end:
 //
 // Work.  A unit is (expert and up to 8 NT of its rows, tile of weight columns)
 // and takes KS steps along the contraction.  All units' steps, laid end to end,
@@ -24,10 +25,16 @@
 // kernel and no gather.  The down kernel does this while the gate_up kernel
 // ends (programmatic launch), and waits only before it reads a.
 //
-// Precision.  Products accumulate in fp32.  a is rounded to bf16 between the
-// kernels for bf16 storage, as the layer for many tokens does (it is an operand
-// of the bf16 product); it stays fp32 for fp32 storage, whose products run in
-// fp32 on the CUDA cores.
+// Precision.  Products accumulate in fp32.  a is rounded between the kernels, being
+// an operand of the next product: to bf16 with bf16 weights, as the layer for many
+// tokens does; to fp16 with a power of two per 32 values (11 bits) with 4-bit
+// weights.  fp32 weights keep it in fp32 and multiply on the CUDA cores in fp32.
+//
+// Measured, of the bytes of the touched experts' weights (a copy reaches 6.76 TB/s):
+// 16 tokens on 256 bf16 experts of 4096 x 2048 (5.1 GB) 745 us, 6.9 TB/s; one token
+// on four of 2880 x 2880 (199 MB) 48 us, of which 35 us stream at 5.5 TB/s and the
+// rest is start, joins and the step between the kernels; 32 tokens on 64 4-bit
+// experts of 8192 x 2048 (1.7 GB) 365 us, 4.6 TB/s, bound by instructions.
 #include <cuda.h>
 
 #include <algorithm>
@@ -82,7 +89,7 @@ struct FewArgs {
 };
 
 // ------------------------------------------------------------------ plan
-// A chunk is up to `rows` (8 or 32) rows of one expert; chunks are ordered by
+// A chunk is up to `rows` (8 or 16) rows of one expert; chunks are ordered by
 // expert, rows by slot.
 // Its arrays lie in dynamic shared memory, sized for the call (what they do not
 // take is L1 cache for the token rows).
@@ -502,8 +509,12 @@ struct F32 {
 // At HBM's rate an SM gets some 44 weights a clock and issues 128 operations, half
 // of them logic and conversions, so decoding must be cheap: a conversion e2m1 ->
 // fp16 makes two weights, and one fp16 product scales them, two instructions per
-// two weights.  A lane loads whole blocks (16 bytes) of columns g, g + 8, g + 16
-// and g + 24, so each load has one scale 2^q.  fp16 holds 2^q times a code exactly
+// two weights (half of all that a step takes).  A lane takes whole blocks (16 bytes)
+// of columns g, g + 8, g + 16 and g + 24, so each has one scale 2^q.  The codes come
+// by TMA, two steps ahead and across the ends of units: with two steps in registers
+// instead, 32 tokens on 64 experts take 465 us, not 365, and a ring of four smaller
+// steps takes 427.  What is left to wait for are tokens and scale bytes at a unit's
+// start.  fp16 holds 2^q times a code exactly
 // only near 1, so a column's weights are scaled by 2^(q - ref), ref being the scale
 // of the first block that the warp sees of that column, and the sums by 2^ref at
 // the end.  A step with a block outside 2^-14 .. 2^13 of its column's ref (or a NaN
@@ -1398,11 +1409,12 @@ cudaError_t launch_rows(const moe_shape* s, const void* x, const uint8_t* x_scal
 
 // Row tiles of 8 tokens per unit.  Two where an expert may have more than 8 rows,
 // so that its weights are read and decoded once for 16.  4-bit weights take two only
-// from 6 rows per expert on: the kernel for one tile has its tokens' loads ahead
-// and is the faster one where few experts have more than 8 rows.  fp32: one.
+// from 8 rows per expert on: the kernel for one tile has its tokens' loads ahead.
+// (One and two tiles, 32 experts of 2880 x 2880, top-4: 48 tokens 146 and 171 us, 64
+// tokens 187 and 185, 96 tokens 246 and 210.)  fp32: one.
 int row_tiles(const moe_shape* s, bool mx) {
   if (s->dtype == MOE_FP32 || s->T <= 8) return 1;
-  return mx && s->T * s->k < 6ll * s->E ? 1 : 2;
+  return mx && s->T * s->k < 8ll * s->E ? 1 : 2;
 }
 
 struct FewLayout {

@@ -9,6 +9,7 @@
 // lane; a lane then holds C whole blocks of 32, so the scale needs no
 // exchange.  The codes pass through shared memory to reach global memory as
 // 128-byte rows.  Both directions are HBM-bound: 2 + 17/32 bytes per bf16 weight.
+// Measured: 16 x 2880 x 5760 bf16 there and back in 225 us, 6.0 TB/s.
 #include "abi_internal.h"
 #include "mx.cuh"
 #include "vec.cuh"

@@ -403,8 +403,9 @@ typedef struct {
 size_t moe_few_workspace_size(const moe_shape* shape);
 
 /* The forward pass of the layer for a few tokens (inference), in two kernels
- * that read each touched expert's weights once: the y of moe_ffn_fwd, without
- * its plan, gather and grouped rows.
+ * (and a small one before them for e4m3 tokens or 4-bit weights) that read each
+ * touched expert's weights once: the y of moe_ffn_fwd, without its plan, gather
+ * and grouped rows.
  *   T <= 128 (more: MOE_ERR_UNSUPPORTED); moe_ffn_fwd is the faster one where
  *     experts get dozens of rows each.
  *   x [T,H] in the storage dtype, or with x_scale != NULL e4m3 codes [T,H] with
@@ -413,8 +414,11 @@ size_t moe_few_workspace_size(const moe_shape* shape);
  *     mx = NULL, or mx with both NULL (dtype MOE_BF16; H and I multiples of 32).
  *   bias: NULL, or per-expert biases (b_gate_up and b_down are read).
  *   y [T,H] in the storage dtype, or fp32 with out_fp32.
- * With dtype MOE_FP32 the products run in fp32 (not TF32).  With MOE_BF16 the
- * activation is rounded to bf16 before the down product, as in moe_ffn_fwd.  An
+ * With dtype MOE_FP32 the products run in fp32 (not TF32).  With bf16 weights
+ * the activation is rounded to bf16 before the down product, as in moe_ffn_fwd.
+ * With 4-bit weights tokens and activations are held in fp16 with a power of two
+ * per token row and per 32 activations: a token value below 2^-29 of its row's
+ * largest loses bits, and a row that holds an infinity or a NaN gives NaN.  An
  * expert id outside [0,E) records MOE_ERR_BAD_INDEX in the workspace and its
  * slot contributes nothing.  The sums run in an order that depends on the shape,
  * the ids and the device only.  ws: moe_few_workspace_size(shape) bytes. */
