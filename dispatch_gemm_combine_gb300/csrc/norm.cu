@@ -48,6 +48,7 @@ struct Raw8 {
     if (sizeof(E) == 4) return __uint_as_float(w[j]);
     return j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
   }
+  __device__ __forceinline__ float2 pair(int j) const { return make_float2(get(2 * j), get(2 * j + 1)); }
 };
 
 // The rows that a block walks, N arrays of them, D - 1 rows ahead of their use: each
@@ -192,13 +193,15 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(
 #pragma unroll
   for (int d = 0; d < D - 1; ++d) rows.issue(d, blockIdx.x + static_cast<int64_t>(d) * gridDim.x, T);
   constexpr bool KEEP = V < 4;   // the weight in registers
-  float dw[V][8];
+  // n and xhat stay in fp32 between the two passes over a row where registers allow
+  constexpr bool HOLD = V == 1;
+  float2 dw[V][4], n[4], xh[4];
   Raw8<E> w[KEEP ? V : 1], g[V], r[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = (threadIdx.x + i * blockDim.x) * 8;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) dw[i][j] = make_float2(0.f, 0.f);
     if (KEEP && c < H) w[i % (KEEP ? V : 1)].load(weight + c);
   }
   int stage = 0, flip = 0;   // a row's barrier also separates the reuse of the other sums
@@ -211,7 +214,8 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(
       cp_async_wait<D >= 2 ? D - 2 : 0>();
       rows.issue(stage == 0 ? D - 1 : stage - 1, row + static_cast<int64_t>(D - 1) * gridDim.x, T);
     }
-    float dot = 0.f;
+    float2 dot2 = make_float2(0.f, 0.f);
+    const float2 rstd2 = make_float2(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = (threadIdx.x + i * blockDim.x) * 8;
@@ -221,14 +225,17 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(
         Raw8<E>& wi = w[i % (KEEP ? V : 1)];
         if (!KEEP) wi.load(weight + c);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float gj = g[i].get(j), xh = r[i].get(j) * rstd;
-          dw[i][j] = fmaf(gj, xh, dw[i][j]);
-          dot = fmaf(gj * wi.get(j), xh, dot);
+        for (int j = 0; j < 4; ++j) {
+          const float2 gj = g[i].pair(j);
+          n[j] = mul2(gj, wi.pair(j));
+          xh[j] = mul2(r[i].pair(j), rstd2);
+          dw[i][j] = fma2(gj, xh[j], dw[i][j]);
+          dot2 = fma2(n[j], xh[j], dot2);
         }
       }
     }
-    const float mean = block_sum(dot, part[flip]) / static_cast<float>(H);
+    const float mean = block_sum(dot2.x + dot2.y, part[flip]) / static_cast<float>(H);
+    const float2 mean2 = make_float2(-mean, -mean);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = (threadIdx.x + i * blockDim.x) * 8;
@@ -239,9 +246,11 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(
         Raw8<E> e;
         if (d_total) rows.take(stage, 2, i, row, c, e);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          o[j] = rstd * (g[i].get(j) * wi.get(j) - r[i].get(j) * rstd * mean);
-          if (d_total) o[j] += e.get(j);
+        for (int j = 0; j < 4; ++j) {
+          const float2 nj = HOLD ? n[j] : mul2(g[i].pair(j), wi.pair(j));
+          const float2 d = fma2(HOLD ? xh[j] : mul2(r[i].pair(j), rstd2), mean2, nj);
+          const float2 v = d_total ? fma2(rstd2, d, e.pair(j)) : mul2(rstd2, d);
+          o[2 * j] = v.x, o[2 * j + 1] = v.y;
         }
         store8(dx + base + c, o);
       }
@@ -252,7 +261,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_kernel(
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = (threadIdx.x + i * blockDim.x) * 8;
-      if (c < H) store8(dw_part + static_cast<int64_t>(blockIdx.x) * H + c, dw[i]);
+      if (c < H) store8(dw_part + static_cast<int64_t>(blockIdx.x) * H + c, &dw[i][0].x);
     }
   }
 }
