@@ -479,17 +479,28 @@ struct F32 {
         v[r][0] = __uint_as_float(q.x), v[r][1] = __uint_as_float(q.y);
         v[r][2] = __uint_as_float(q.z), v[r][3] = __uint_as_float(q.w);
       }
+      // four rows' loads at a time (rows that are not there repeat the first)
 #pragma unroll
-      for (int n = 0; n < 8; ++n)
-        if (n < nrows && ok) {
-          const uint4 q = ld_u128(static_cast<const float*>(rows[n].p) + k);
-          const float x[4] = {__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z),
-                              __uint_as_float(q.w)};
+      for (int half = 0; half < 2; ++half) {
+        if (!ok || 4 * half >= nrows) break;
+        uint4 x[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
+        for (int n = 0; n < 4; ++n) x[n] = ld_u128(static_cast<const float*>(rows[4 * half + n].p) + k);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[n][c] = fmaf(x[r], v[r][c], acc[n][c]);
+        for (int n = 0; n < 4; ++n) {
+          float* s = acc[4 * half + n];
+          const uint32_t* q = &x[n].x;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float2 xx = make_float2(__uint_as_float(q[r]), __uint_as_float(q[r]));
+#pragma unroll
+            for (int c = 0; c < 4; c += 2) {
+              const float2 d = fma2(xx, make_float2(v[r][c], v[r][c + 1]), make_float2(s[c], s[c + 1]));
+              s[c] = d.x, s[c + 1] = d.y;
+            }
+          }
         }
+      }
     }
 #pragma unroll
     for (int n = 0; n < 8; ++n)
