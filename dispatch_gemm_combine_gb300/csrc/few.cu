@@ -460,7 +460,6 @@ struct F32 {
   template <int NT>
   static __device__ __forceinline__ void run(const void* w, int64_t ld, int col, int ncol, int K, int s0, int s1, int kg,
                                              const Row* rows, int nrows, float* red) {
-    wait_for_rows();
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const bool col_ok = 4 * g < ncol;
     float acc[8][4];
@@ -469,38 +468,48 @@ struct F32 {
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[n][c] = 0.f;
     const float* base = static_cast<const float*>(w) + col + 4 * g;
-    for (int s = s0; s < s1; ++s) {
+    uint4 v[2][4];   // two buffers take turns
+    auto load = [&](int buf, int s) {
       const int k = (s * KG + kg) * STEP + 4 * t;
-      const bool ok = k < K;
-      float v[4][4];
+      const bool ok = s < s1 && k < K && col_ok;
+      const float* p = base + k * ld;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint4 q = ok && col_ok ? ldg_stream(base + (k + r) * ld) : make_uint4(0, 0, 0, 0);
-        v[r][0] = __uint_as_float(q.x), v[r][1] = __uint_as_float(q.y);
-        v[r][2] = __uint_as_float(q.z), v[r][3] = __uint_as_float(q.w);
-      }
+      for (int r = 0; r < 4; ++r) v[buf][r] = ok ? ldg_stream(p + r * ld) : make_uint4(0, 0, 0, 0);
+    };
+    auto multiply = [&](int buf, int s) {
+      const int k = (s * KG + kg) * STEP + 4 * t;
+      if (s >= s1 || k >= K) return;
       // four rows' loads at a time (rows that are not there repeat the first)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        if (!ok || 4 * half >= nrows) break;
+        if (4 * half >= nrows) break;
         uint4 x[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) x[n] = ld_u128(static_cast<const float*>(rows[4 * half + n].p) + k);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          float* s = acc[4 * half + n];
+          float* s4 = acc[4 * half + n];
           const uint32_t* q = &x[n].x;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float2 xx = make_float2(__uint_as_float(q[r]), __uint_as_float(q[r]));
-#pragma unroll
-            for (int c = 0; c < 4; c += 2) {
-              const float2 d = fma2(xx, make_float2(v[r][c], v[r][c + 1]), make_float2(s[c], s[c + 1]));
-              s[c] = d.x, s[c + 1] = d.y;
-            }
+            const float xr = __uint_as_float(q[r]);
+            const uint4& wr = v[buf][r];
+            const float2 lo = fma2(make_float2(xr, xr), make_float2(__uint_as_float(wr.x), __uint_as_float(wr.y)),
+                                   make_float2(s4[0], s4[1]));
+            const float2 hi = fma2(make_float2(xr, xr), make_float2(__uint_as_float(wr.z), __uint_as_float(wr.w)),
+                                   make_float2(s4[2], s4[3]));
+            s4[0] = lo.x, s4[1] = lo.y, s4[2] = hi.x, s4[3] = hi.y;
           }
         }
       }
+    };
+    load(0, s0);
+    wait_for_rows();
+    for (int s = s0; s < s1; s += 2) {
+      load(1, s + 1);
+      multiply(0, s);
+      load(0, s + 2);
+      multiply(1, s + 1);
     }
 #pragma unroll
     for (int n = 0; n < 8; ++n)
