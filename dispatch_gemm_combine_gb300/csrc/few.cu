@@ -443,6 +443,8 @@ struct Bf16 {
 
 // fp32 weights [K, ld]: the same loads (4 columns per lane), products on the
 // CUDA cores in fp32; the four lanes of a group hold shares of the contraction.
+// Bound by HBM up to a row or two per expert (one token on 4 experts of 2880 x 2880:
+// 88 us, 4.5 TB/s), by instructions beyond (16 tokens on 16: 381 us, 4.2 TB/s).
 struct F32 {
   using Store = float;
   static constexpr int WF = 32, FG = 2, KG = 4, STEP = 16;
