@@ -880,8 +880,21 @@ __global__ void __launch_bounds__(256) few_half_rows_kernel(const void* __restri
   const int row = blockIdx.x, n = H / 8;
   const int64_t base = static_cast<int64_t>(row) * n;
   for (int i = row * 256 + threadIdx.x; i < Tk; i += gridDim.x * 256) act_top[i] = 0;
+  constexpr int kHeld = 4;   // of a thread's vectors, loaded once
+  float held[kHeld][8];
   uint32_t amax = 0;
-  for (int i = threadIdx.x; i < n; i += 256) {
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) held[h][j] = 0.f;
+    const int i = threadIdx.x + h * 256;
+    if (i < n) load_row8<X8>(x, x_scale, base + i, held[h]);
+  }
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(held[h][j]) & 0x7fffffffu);
+  for (int i = threadIdx.x + kHeld * 256; i < n; i += 256) {
     float v[8];
     load_row8<X8>(x, x_scale, base + i, v);
 #pragma unroll
@@ -894,13 +907,20 @@ __global__ void __launch_bounds__(256) few_half_rows_kernel(const void* __restri
   for (int w = 0; w < 8; ++w) amax = max(amax, part[w]);
   const uint32_t byte = half_block_byte(amax);
   const float f = mx_inv_scale(byte);
-  for (int i = threadIdx.x; i < n; i += 256) {
-    float v[8];
-    load_row8<X8>(x, x_scale, base + i, v);
+  uint4* row_out = reinterpret_cast<uint4*>(out) + row * static_cast<int64_t>(Mx::pitch(H) / 8);
+  auto put = [&](int i, const float (&v)[8]) {
     uint4 u;
     u.x = pack_half(v[0] * f, v[1] * f), u.y = pack_half(v[2] * f, v[3] * f);
     u.z = pack_half(v[4] * f, v[5] * f), u.w = pack_half(v[6] * f, v[7] * f);
-    reinterpret_cast<uint4*>(out)[row * static_cast<int64_t>(Mx::pitch(H) / 8) + Mx::chunk_at(i)] = u;
+    row_out[Mx::chunk_at(i)] = u;
+  };
+#pragma unroll
+  for (int h = 0; h < kHeld; ++h)
+    if (threadIdx.x + h * 256 < n) put(threadIdx.x + h * 256, held[h]);
+  for (int i = threadIdx.x + kHeld * 256; i < n; i += 256) {
+    float v[8];
+    load_row8<X8>(x, x_scale, base + i, v);
+    put(i, v);
   }
   if (threadIdx.x == 0) top[row] = static_cast<int>(byte);
 }
