@@ -362,7 +362,11 @@ cudaError_t launch_fwd_v(const E* x, const E* residual, const E* weight, int64_t
                          void* y, uint8_t* y_scale, E* total, float* rstd, int threads, int sms,
                          cudaStream_t st) {
   const NormLaunch l = norm_launch(T, threads, RowRing<E, 2, V, kAhead>::bytes(threads), kThreadsPerSm, sms);
-  if (l.ring) {
+  // Without the 8-bit output there is little to compute, and where several rows fit an
+  // SM a block for each is the faster form: 16384 x 4096 bf16 84 us instead of 94,
+  // 32768 x 1024 43 and 50, 8192 x 4096 fp32 82 and 96.  (8192 x 7168 bf16: 83 and 81;
+  // with 8-bit output 16384 x 4096 takes 123 and 80.)
+  if (l.ring && (OUT8 || threads > 512)) {
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = allow_smem(norm_fwd_kernel<E, OUT8, V, kAhead>, ready);
     if (e != cudaSuccess) return e;
