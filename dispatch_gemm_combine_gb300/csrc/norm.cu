@@ -3,12 +3,13 @@
 //
 //   r = x + residual,  rstd = (mean_h r^2 + eps)^-1/2,  y = r * rstd * weight
 //
-// Forward: a block walks rows, each thread holds 8 * V columns of r in registers,
-// so x and the residual are read once and the outputs written once: HBM-bound.
-// Later rows' loads are in flight while a row is summed (RowRing).  r^2 is summed
-// in fp32 (eight values per thread, then a warp butterfly, then the warps).  r itself
-// is not rounded before the norm; `total` is r rounded once to the storage type.  The 8-bit output takes the
-// block's scale from four neighbouring threads (32 columns) by two shuffles.
+// Forward: a block walks rows (or has one), each thread holds 8 * V columns of r in
+// registers, so x and the residual are read once and the outputs written once:
+// HBM-bound.  Later rows' loads are in flight while a row is summed (RowRing).  r^2
+// is summed in fp32 (eight values per thread, then a warp butterfly, then the warps).
+// r itself is not rounded before the norm; `total` is r rounded once to the storage
+// type.  The 8-bit output takes the block's scale from four neighbouring threads (32
+// columns) by two shuffles.
 //
 // Backward, with xhat = r * rstd and n = dy * weight:
 //   dx = rstd * (n - xhat * mean_h(n * xhat)) + d_total,
@@ -380,7 +381,12 @@ cudaError_t launch_fwd_v(const E* x, const E* residual, const E* weight, int64_t
 template <typename E, bool OUT8>
 cudaError_t launch_fwd(const E* x, const E* residual, const E* weight, int64_t T, int H, float eps,
                        void* y, uint8_t* y_scale, E* total, float* rstd, int sms, cudaStream_t st) {
-  const RowShape s = row_shape(H);
+  RowShape s = row_shape(H);
+  // bf16 with 8-bit output: of 513 to 1023 threads one block fits an SM, so two
+  // vectors per thread (8192 x 5120 53 us instead of 59, 8192 x 7168 70 and 72; the
+  // other outputs lose: 8192 x 5120 65 and 56).
+  if (OUT8 && sizeof(E) == 2 && s.threads > 512 && s.threads < 1024)
+    s = {((H + 15) / 16 + 31) / 32 * 32, 2};
   if (s.vecs == 1) return launch_fwd_v<E, OUT8, 1>(x, residual, weight, T, H, eps, y, y_scale, total, rstd, s.threads, sms, st);
   if (s.vecs == 2) return launch_fwd_v<E, OUT8, 2>(x, residual, weight, T, H, eps, y, y_scale, total, rstd, s.threads, sms, st);
   return launch_fwd_v<E, OUT8, 4>(x, residual, weight, T, H, eps, y, y_scale, total, rstd, s.threads, sms, st);

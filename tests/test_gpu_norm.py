@@ -84,6 +84,15 @@ def test_forward_8bit(T, H, dtype):
     check_fwd(T, H, DT[dtype], False, True)
 
 
+@pytest.mark.parametrize("T,H,out8", [(1400, 288, True), (700, 2912, True), (400, 5152, True), (320, 8224, True),
+                                      (400, 5128, False), (320, 8200, False), (1400, 264, False)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_forward_several_rows_per_block(T, H, out8, dtype):
+    """More rows than resident blocks, and warps that a row's end cuts."""
+    check_fwd(T, H, DT[dtype], True, out8)
+    check_fwd(T, H, DT[dtype], False, out8)
+
+
 def test_small_and_large_rows():
     check_fwd(4, 256, torch.float32, False, False, std=1e-12)
     check_fwd(4, 256, torch.float32, False, False, std=1e15)
@@ -145,6 +154,12 @@ def test_backward(T, H, dtype, d_total):
     # fp32 sums of T terms: at most rows per block + 64 additions, each u32 of the partial sum
     rows = -(-T // 152) + 64
     assert torch.all((dw.double() - terms.sum(0)).abs() <= (rows + 4) * U32 * terms.abs().sum(0) + 1e-40)
+
+
+@pytest.mark.parametrize("T,H", [(2600, 264), (1400, 2888), (400, 5128), (320, 8200)])
+@pytest.mark.parametrize("dtype,d_total", [("bf16", True), ("fp32", False), ("fp32", True)])
+def test_backward_several_rows_per_block(T, H, dtype, d_total):
+    test_backward(T, H, dtype, d_total)
 
 
 def test_backward_against_differences():
