@@ -536,11 +536,12 @@ struct F32 {
 // by TMA, two steps ahead and across the ends of units: with two steps in registers
 // instead, 32 tokens on 64 experts take 465 us, not 365, and a ring of four smaller
 // steps takes 427.  What is left to wait for are tokens and scale bytes at a unit's
-// start.  fp16 holds 2^q times a code exactly
-// only near 1, so a column's weights are scaled by 2^(q - ref), ref being the scale
-// of the first block that the warp sees of that column, and the sums by 2^ref at
-// the end.  A step with a block outside 2^-14 .. 2^13 of its column's ref (or a NaN
-// scale) takes a path that multiplies the blocks one by one and scales sums.
+// start.  fp16 holds 2^q times a code exactly only near 1, so a column's weights are
+// scaled by 2^(q - ref), ref being the scale of the first block that the warp sees of
+// that column (or, where that holds zeros, of the first that does not: new_ref), and
+// the sums by 2^ref at the end.  A step with a block outside 2^-14 .. 2^13 of its
+// column's ref (or a NaN scale) takes a path that multiplies the blocks one by one and
+// scales sums.
 struct Mx {
   using Store = __nv_bfloat16;
   static constexpr int WF = 32, FG = 4, KG = 2, STEP = 256;
@@ -688,24 +689,37 @@ struct Mx {
       for (int r = 0; r < 4; ++r) v[r] = ld_shared_v4(at + r * 8 * (STEP / 2));
       // 2^(q - ref) in fp16, in range for -14 .. 13 (ref <= 240: a NaN's 255 is not)
       uint32_t f[4];
-      bool far = false;
+      auto factors = [&]() {
+        bool out = false;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint32_t d = (u ? bytes[r] >> 8 : bytes[r] & 0xffu) - ref[r] + 14;
-        far = far || d > 27u;
-        f[r] = d * 0x04000400u + 0x04000400u;
-      }
-      if (__builtin_expect(__any_sync(0xffffffffu, far), 0)) {
-        far = false;   // a block of zeros needs no scale
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t d = (u ? bytes[r] >> 8 : bytes[r] & 0xffu) - ref[r] + 14;
+          out = out || d > 27u;
+          f[r] = d * 0x04000400u + 0x04000400u;
+        }
+        return out;
+      };
+      // the same, with any finite factor for a block of zeros, which needs none
+      auto factors_but_zeros = [&]() {
+        factors();
+        bool out = false;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const uint32_t byte = u ? bytes[r] >> 8 : bytes[r] & 0xffu;
           if (byte - ref[r] + 14 > 27u) {
-            far = far || (v[r].x | v[r].y | v[r].z | v[r].w) != 0 || byte == 255u;
+            out = out || !zeros(v[r]) || byte == 255u;
             f[r] = 0x3c003c00u;
           }
         }
-        far = __any_sync(0xffffffffu, far);
+        return __any_sync(0xffffffffu, out);
+      };
+      bool far = false;
+      if (__builtin_expect(__any_sync(0xffffffffu, factors()), 0)) {
+        far = factors_but_zeros();
+        if (far) {
+          new_ref<NT>(v, bytes, u, ref, acc);
+          far = factors_but_zeros();
+        }
       }
       uint32_t fx[NT];
       const void* xp[NT];
@@ -779,6 +793,53 @@ struct Mx {
     }
   }
 
+  static __device__ __forceinline__ bool zeros(const uint4& codes) {
+    return ((codes.x | codes.y | codes.z | codes.w) & 0x77777777u) == 0;
+  }
+  // A step with far scales first moves the columns' refs where they do not serve.  A
+  // column whose sums are still 0 (its blocks so far were zeros, to which the quantiser
+  // gives the byte 0, or met zeros) takes the largest scale of the blocks here that hold
+  // something.  One that has sums rises only as far as far_step needs: with
+  // 2^(q - ref) <= 2^90 the sums of 2^13 blocks (below 2^23 each) are inside fp32.  The
+  // sums lose bits by that only where a column's scales lie more than 2^150 apart.
+  template <int NT>
+  static __device__ __forceinline__ void new_ref(const uint4 (&v)[4], const uint32_t (&bytes)[4], int u,
+                                                 int (&ref)[4], float (&acc)[2][NT][4]) {
+    constexpr int kMost = 90;
+    // a byte per column: the largest scale byte of the group's blocks, plus one; and a
+    // bit per column: whether the group has sums
+    uint32_t tops = 0, held = 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int m = r >> 1, q = 2 * (r & 1);
+      const uint32_t byte = bytes[r] >> 8 * u & 0xffu;
+      if (!zeros(v[r]) && byte != 255u) tops |= (byte + 1) << 8 * r;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (acc[m][n][q] != 0.f || acc[m][n][q + 1] != 0.f) held |= 1u << r;
+    }
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+      tops = __vmaxu4(tops, __shfl_xor_sync(0xffffffffu, tops, d));
+      held |= __shfl_xor_sync(0xffffffffu, held, d);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int m = r >> 1, q = 2 * (r & 1);
+      const int top = static_cast<int>(tops >> 8 * r & 0xffu) - 1;
+      int to = ref[r];
+      if (top >= 0) to = held >> r & 1 ? max(to, top - kMost) : min(top, 240);
+      const float down = pow2(min(0, ref[r] - to));
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[m][n][q] *= down, acc[m][n][q + 1] *= down;
+      ref[r] = to;
+    }
+  }
+  // 2^e for e <= 127, 0 below fp32's range.
+  static __device__ __forceinline__ float pow2(int e) {
+    return __uint_as_float(e >= -126 ? static_cast<uint32_t>(e + 127) << 23 : (e >= -149 ? 1u << (e + 149) : 0u));
+  }
+
   // A step with far scales: the four lanes' blocks one after the other, codes as
   // they are, each block's sums scaled by 2^(q - ref) in fp32.
   template <int NT, int PHASE, bool EARLY>
@@ -793,7 +854,7 @@ struct Mx {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const uint32_t byte = __shfl_sync(0xffffffffu, bytes[r], (lane & 28) | turn) >> 8 * u & 0xffu;
-        f[r] = byte == 255u ? __uint_as_float(0x7fc00000u) : ldexpf(1.f, static_cast<int>(byte) - ref[r]);
+        f[r] = byte == 255u ? __uint_as_float(0x7fc00000u) : pow2(static_cast<int>(byte) - ref[r]);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
