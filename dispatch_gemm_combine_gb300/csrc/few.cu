@@ -781,16 +781,25 @@ struct Mx {
     // the sums' powers of two: the columns' refs and the token rows' tops
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float t0 = mx_scale(__shfl_sync(0xffffffffu, rows[n].top, 8 * t));
-      const float t1 = mx_scale(__shfl_sync(0xffffffffu, rows[n].top, 8 * t + 4));
+      const int t0 = __shfl_sync(0xffffffffu, rows[n].top, 8 * t);
+      const int t1 = __shfl_sync(0xffffffffu, rows[n].top, 8 * t + 4);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        const float lo = mx_scale(ref[2 * m]), hi = mx_scale(ref[2 * m + 1]);
+        const int lo = ref[2 * m], hi = ref[2 * m + 1];
         float* d = red + (8 * n + 2 * t) * PITCH + 16 * m + g;
-        d[0] = acc[m][n][0] * lo * t0, d[PITCH] = acc[m][n][1] * lo * t1;
-        d[8] = acc[m][n][2] * hi * t0, d[PITCH + 8] = acc[m][n][3] * hi * t1;
+        d[0] = times_scales(acc[m][n][0], lo, t0), d[PITCH] = times_scales(acc[m][n][1], lo, t1);
+        d[8] = times_scales(acc[m][n][2], hi, t0), d[PITCH + 8] = times_scales(acc[m][n][3], hi, t1);
       }
     }
+  }
+  // v * 2^(a - 127) * 2^(b - 127); b = 255: NaN.  One scale after the other could leave
+  // fp32's range on the way to a result inside it, so each factor has half of the
+  // exponent (2^-126 at the least: below 2^-252 no sum leaves anything).
+  static __device__ __forceinline__ float times_scales(float v, int a, int b) {
+    const int e = a + b, half = e >> 1;
+    const float f = __uint_as_float(static_cast<uint32_t>(max(half, 1)) << 23);
+    const float g = __uint_as_float(b == 255 ? 0x7fc00000u : static_cast<uint32_t>(max(e - half, 1)) << 23);
+    return v * f * g;
   }
 
   static __device__ __forceinline__ bool zeros(const uint4& codes) {

@@ -122,3 +122,24 @@ def test_tokens_of_zeros_under_the_large_blocks():
     c["x"] *= 2.0 ** 60
     c["xv"] *= 2.0 ** 60
     check(c)
+
+
+@pytest.mark.parametrize("byte,power", [(238, -108), (250, -125), (254, -126), (30, 95), (10, 110), (120, 0)])
+def test_large_scales_by_small_tokens(byte, power):
+    """Scales near the ends of their range with tokens that bring the result back."""
+    c = make(4, 320, 64, 2, 1, SWIGLU, "mx")
+    c["mx"][1].fill_(byte)
+    c["x"] = c["xv"].mul(2.0 ** power).to(torch.bfloat16)
+    c["xv"] = c["x"].double()
+    check(c)
+
+
+def test_largest_scales():
+    """Codes of one half on scales of 2^127, products in range."""
+    c = make(1, 64, 32, 1, 1, SWIGLU, "mx")
+    c["mx"][1].fill_(112)
+    c["mx"][2].fill_(0x11)
+    c["mx"][3].fill_(254)
+    c["wgu"] = mx_values(*c["mx"][:2])
+    check(c)
+    assert run(c)[0].abs().max() > 2.0 ** 100
