@@ -27,8 +27,8 @@
 //
 // Precision.  Products accumulate in fp32.  a is rounded between the kernels, being
 // an operand of the next product: to bf16 with bf16 weights, as the layer for many
-// tokens does; to fp16 with a power of two per 32 values (11 bits) with 4-bit
-// weights.  fp32 weights keep it in fp32 and multiply on the CUDA cores in fp32.
+// tokens does; to fp16 with a power of two per 32 values (11 bits, see kTokenTop) with
+// 4-bit weights.  fp32 weights keep it in fp32 and multiply on the CUDA cores in fp32.
 //
 // Measured, of the bytes of the touched experts' weights (a copy reaches 6.76 TB/s):
 // 16 tokens on 256 bf16 experts of 4096 x 2048 (5.1 GB) 745 us, 6.9 TB/s; one token
@@ -524,6 +524,16 @@ struct F32 {
   }
 };
 
+// Where fp16 holds the largest of a token row's values and of a block of 32
+// activations, as a power of two.  A token row has one scale: its values down to 2^-29
+// of the largest keep bf16's bits, and smaller ones are rounded at 2^-39 of it.  Blocks
+// of activations are brought to their row's power of two by a factor in fp16, whose own
+// range ends at 2^-24, so a block with its largest at 2^7 may lie 2^31 below the row's
+// largest before it is lost, and its values are rounded at 2^-32 of the block's
+// largest: an activation has fp16's 11 bits or an error of at most 2^-31 of its row's
+// largest.  (With 2^14 for both, blocks more than 2^24 below were lost.)
+constexpr int kTokenTop = 14, kActTop = 7;
+
 // Microscaled e2m1 weights: codes [N, K/2] and scale bytes [N, K/32], the
 // contraction innermost; token rows in fp16 with a power of two per row (and
 // possibly per block of 32).
@@ -577,8 +587,8 @@ struct Mx {
   static __device__ __forceinline__ uint32_t word(const uint4& v, int q) {
     return q == 0 ? v.x : (q == 1 ? v.y : (q == 2 ? v.z : v.w));
   }
-  // 2^d for d <= 0 in both halves of fp16, 0 below its range.
-  static __device__ __forceinline__ uint32_t pow2_down(int d) {
+  // 2^d for d <= 15 in both halves of fp16, 0 below its range.
+  static __device__ __forceinline__ uint32_t pow2_half(int d) {
     const uint32_t h = d >= -14 ? (d + 15) << 10 : (d >= -24 ? 1u << (d + 24) : 0u);
     return h * 0x00010001u;
   }
@@ -596,9 +606,11 @@ struct Mx {
   static __device__ __forceinline__ uint4 row_vec(const void* p, int q) {
     return ld_u128(static_cast<const char*>(p) + q * 64);
   }
-  // What brings an activation block with this scale byte to the row's power of two.
+  // What brings an activation block with this scale byte to the row's power of two,
+  // which has the largest block where fp16's tokens are too.
+  static constexpr int kActUp = kTokenTop - kActTop;
   static __device__ __forceinline__ uint32_t row_factor(uint32_t p, int top) {
-    return p == 255u ? 0x7e007e00u : pow2_down(static_cast<int>(p) - top);
+    return p == 255u ? 0x7e007e00u : pow2_half(static_cast<int>(p) - top + kActUp);
   }
 
   // The codes of step s of a unit, KG lines of each column, and the lines of their
@@ -781,8 +793,8 @@ struct Mx {
     // the sums' powers of two: the columns' refs and the token rows' tops
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int t0 = __shfl_sync(0xffffffffu, rows[n].top, 8 * t);
-      const int t1 = __shfl_sync(0xffffffffu, rows[n].top, 8 * t + 4);
+      const int t0 = __shfl_sync(0xffffffffu, rows[n].top, 8 * t) - (PHASE == 1 ? kActUp : 0);
+      const int t1 = __shfl_sync(0xffffffffu, rows[n].top, 8 * t + 4) - (PHASE == 1 ? kActUp : 0);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         const int lo = ref[2 * m], hi = ref[2 * m + 1];
@@ -894,12 +906,11 @@ struct Mx {
 };
 
 // Values with a common scale of 2^p as fp16: p such that the largest magnitude (its
-// fp32 bits) lies in [2^14, 2^15).  Values down to 2^-29 of it keep bf16's bits;
-// smaller ones are rounded at 2^-39 of it.  Returns the scale's byte; 255 (NaN)
-// where one is an infinity or a NaN.
-__device__ __forceinline__ uint32_t half_block_byte(uint32_t amax_bits) {
+// fp32 bits) lies in [2^top, 2^(top + 1)), see kTokenTop.  Returns the scale's byte; 255
+// (NaN) where one is an infinity or a NaN.
+__device__ __forceinline__ uint32_t half_block_byte(uint32_t amax_bits, int top) {
   if (amax_bits >= 0x7f800000u) return 255u;
-  return static_cast<uint32_t>(max(0, static_cast<int>(amax_bits >> 23) - 14));
+  return static_cast<uint32_t>(max(0, static_cast<int>(amax_bits >> 23) - top));
 }
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -975,7 +986,7 @@ __global__ void __launch_bounds__(256) few_half_rows_kernel(const void* __restri
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < 8; ++w) amax = max(amax, part[w]);
-  const uint32_t byte = half_block_byte(amax);
+  const uint32_t byte = half_block_byte(amax, kTokenTop);
   const float f = mx_inv_scale(byte);
   uint4* row_out = reinterpret_cast<uint4*>(out) + row * static_cast<int64_t>(Mx::pitch(H) / 8);
   auto put = [&](int i, const float (&v)[8]) {
@@ -1092,7 +1103,7 @@ __device__ __forceinline__ void finish_gate_up(const FewArgs& a, const Plan& p, 
     } else {
       // a warp has the 32 values of one block (I is a multiple of 32)
       const uint32_t byte =
-          half_block_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu));
+          half_block_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu), kActTop);
       static_cast<__half*>(a.act)[slot * W::pitch(a.I) + 8 * W::chunk_at(feature >> 3) + (feature & 7)] =
           __float2half_rn(v * mx_inv_scale(byte));
       if ((threadIdx.x & 31) == 0) {

@@ -418,7 +418,8 @@ size_t moe_few_workspace_size(const moe_shape* shape);
  * the activation is rounded to bf16 before the down product, as in moe_ffn_fwd.
  * With 4-bit weights tokens and activations are held in fp16 with a power of two
  * per token row and per 32 activations: a token value below 2^-29 of its row's
- * largest loses bits, and a row that holds an infinity or a NaN gives NaN.  An
+ * largest loses bits, an activation keeps 11 bits or has an error of at most 2^-31
+ * of its row's largest, and a row that holds an infinity or a NaN gives NaN.  An
  * expert id outside [0,E) records MOE_ERR_BAD_INDEX in the workspace and its
  * slot contributes nothing.  The sums run in an order that depends on the shape,
  * the ids and the device only.  ws: moe_few_workspace_size(shape) bytes. */

@@ -143,3 +143,29 @@ def test_largest_scales():
     c["wgu"] = mx_values(*c["mx"][:2])
     check(c)
     assert run(c)[0].abs().max() > 2.0 ** 100
+
+
+@pytest.mark.parametrize("T", [2, 20])
+def test_activation_keeps_11_bits_in_every_block(T):
+    """Blocks of activations up to 2^27 below their row's largest: each column of y
+    sees one block alone."""
+    H, I = 320, 320
+    c = make(T, H, I, 1, 1, SWIGLU, "mx", out_fp32=True)
+    x = 1.7109375                            # all of bf16's bits
+    c["x"].zero_()
+    c["x"][:, 0] = x
+    c["xv"] = c["x"].double()
+    for t in c["mx"][::2]:
+        t.zero_()
+    c["mx"][0][:, :, 0] = 7                  # 6 for the first value of a token
+    c["mx"][1][:, :I] = 130                  # gate: 48 x, where the sigmoid is 1
+    c["mx"][3].fill_(127)
+    for b in range(I // 32):
+        c["mx"][1][:, I + 32 * b:I + 32 * b + 32] = 120 - 3 * b
+        c["mx"][2][:, 32 * b:32 * b + 32, 16 * b:16 * b + 16] = 0x52
+    c["wgu"], c["wd"] = mx_values(*c["mx"][:2]), mx_values(*c["mx"][2:])
+    y, _ = run(c)
+    h = c["xv"] @ c["wgu"][0]
+    ref = act_and_slopes(h[:, :I], h[:, I:], SWIGLU)[0] @ c["wd"][0]
+    # 32 products of one sign, each within 2^-11; sums and the activation within 100 steps
+    assert torch.all((y.double() - ref).abs() <= (U11 + 100 * EPS) * ref.abs())
