@@ -3,7 +3,8 @@
 //   gate_up:  a[s]  = act(x[s / k] Wgu[e_s] (+ b_gate_up))      for every slot s
 //   down:     y[t]  = sum_j w[t,j] (a[t k + j] Wd[e] (+ b_down))
 //
-// (A small one before them rewrites e4m3 tokens, or any tokens for 4-bit weights.)
+// (A small one before them clears the joins' counters and rewrites e4m3 tokens, or any
+// tokens for 4-bit weights.)
 // With a few rows per expert the layer reads each touched expert's weights once
 // and does next to nothing with them: it is bound by HBM, not by the tensor
 // cores.  So the weights are operands of warp-level matrix instructions (weights on
@@ -80,7 +81,7 @@ struct FewArgs {
   float* part;             // parts of cut units: 2 per block
   float* o;                // [Tk, H] products of whole units
   void* y;
-  unsigned* counters;      // this kernel's; 0 between calls
+  unsigned* counters;      // this kernel's, cleared by the kernel before both
   int* err;
   int T, H, I, E, k, rows, act_kind, interleaved, out_fp32;   // rows: of a chunk
   float limit, alpha;
@@ -935,12 +936,26 @@ __device__ __forceinline__ void load_row8(const void* x, const uint8_t* x_scale,
   }
 }
 
+// The counters of both products' joins are cleared by the call itself: a workspace may
+// hold anything that earlier calls of other shapes and kinds left in it.
+__device__ __forceinline__ void clear_counters(unsigned* counters, int n) {
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) counters[i] = 0;
+}
+
+// What is left to do before the products where tokens are taken as they are.
+__global__ void __launch_bounds__(256) few_clear_kernel(unsigned* counters, int n) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  clear_counters(counters, n);
+}
+
 // e4m3 token rows in the storage type (bf16: exact but below its normal range).
 template <class S>
 __global__ void __launch_bounds__(256) few_rows_kernel(const void* __restrict__ x,
                                                        const uint8_t* __restrict__ x_scale, int vecs,
-                                                       S* __restrict__ out) {
+                                                       S* __restrict__ out, unsigned* counters,
+                                                       int ncounters) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  clear_counters(counters, ncounters);
   const int i = blockIdx.x * 256 + threadIdx.x;
   if (i >= vecs) return;
   float v[8];
@@ -955,8 +970,10 @@ __global__ void __launch_bounds__(256) few_half_rows_kernel(const void* __restri
                                                             const uint8_t* __restrict__ x_scale, int H,
                                                             __half* __restrict__ out,
                                                             int* __restrict__ top,
-                                                            int* __restrict__ act_top, int Tk) {
+                                                            int* __restrict__ act_top, int Tk,
+                                                            unsigned* counters, int ncounters) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  clear_counters(counters, ncounters);
   __shared__ uint32_t part[8];
   const int row = blockIdx.x, n = H / 8;
   const int64_t base = static_cast<int64_t>(row) * n;
@@ -1428,7 +1445,6 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
       // a unit's counter is its first block's (a block is the first of at most one cut unit)
       unsigned* c = a.counters + (PHASE == 0 ? runs.block_of(piece * per) : piece);
       last = join_add(c, hi - lo) + (hi - lo) == static_cast<unsigned>(per);
-      if (last) *c = 0;
     }
     ps.last[tid] = last;
   }
@@ -1478,9 +1494,9 @@ __global__ void __launch_bounds__(kThreads, 2) few_kernel(const __grid_constant_
   }
 }
 
-// `after`: may start while the kernel before it, which writes its rows, ends.
+// May start while the kernel before it, which writes its rows, ends.
 template <class W, int PHASE, int NT>
-cudaError_t launch(const FewArgs& a, int grid, bool after, cudaStream_t st) {
+cudaError_t launch(const FewArgs& a, int grid, cudaStream_t st) {
   const int smem = red_floats<W>(a.rows) * 8 + plan_bytes(a.T * a.k, a.E, a.rows) + ring_bytes<W>();
   const int most = red_floats<W>(8 * NT) * 8 + kMostPlanBytes + ring_bytes<W>();
   static std::atomic<uint64_t> ready{0};   // one bit per device
@@ -1502,31 +1518,34 @@ cudaError_t launch(const FewArgs& a, int grid, bool after, cudaStream_t st) {
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = after ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, few_kernel<W, PHASE, NT>, a);
 }
 
 template <class W, int PHASE>
-cudaError_t launch_nt(const FewArgs& a, int nt, int grid, bool after, cudaStream_t st) {
+cudaError_t launch_nt(const FewArgs& a, int nt, int grid, cudaStream_t st) {
   if constexpr (W::kMaxTiles > 1) {
-    if (nt > 1) return launch<W, PHASE, W::kMaxTiles>(a, grid, after, st);
+    if (nt > 1) return launch<W, PHASE, W::kMaxTiles>(a, grid, st);
   }
-  return launch<W, PHASE, 1>(a, grid, after, st);
+  return launch<W, PHASE, 1>(a, grid, st);
 }
 
-// x as the gate_up products want it; H % 32 == 0.
+// The kernel before the products: x as gate_up wants it (x_scale: e4m3, half: fp16;
+// H % 32 == 0), counters cleared.
 cudaError_t launch_rows(const moe_shape* s, const void* x, const uint8_t* x_scale, bool half, void* out,
-                        int* top, int* act_top, cudaStream_t st) {
+                        int* top, int* act_top, unsigned* counters, int ncounters, cudaStream_t st) {
   const int T = static_cast<int>(s->T), Tk = T * s->k;
   const int vecs = T * (s->H / 8), grid = (vecs + 255) / 256;
   if (half && x_scale)
-    few_half_rows_kernel<true><<<T, 256, 0, st>>>(x, x_scale, s->H, static_cast<__half*>(out), top, act_top, Tk);
+    few_half_rows_kernel<true><<<T, 256, 0, st>>>(x, x_scale, s->H, static_cast<__half*>(out), top, act_top, Tk, counters, ncounters);
   else if (half)
-    few_half_rows_kernel<false><<<T, 256, 0, st>>>(x, x_scale, s->H, static_cast<__half*>(out), top, act_top, Tk);
+    few_half_rows_kernel<false><<<T, 256, 0, st>>>(x, x_scale, s->H, static_cast<__half*>(out), top, act_top, Tk, counters, ncounters);
+  else if (!x_scale)
+    few_clear_kernel<<<1, 256, 0, st>>>(counters, ncounters);
   else if (s->dtype == MOE_FP32)
-    few_rows_kernel<float><<<grid, 256, 0, st>>>(x, x_scale, vecs, static_cast<float*>(out));
+    few_rows_kernel<float><<<grid, 256, 0, st>>>(x, x_scale, vecs, static_cast<float*>(out), counters, ncounters);
   else
-    few_rows_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(x, x_scale, vecs, static_cast<__nv_bfloat16*>(out));
+    few_rows_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(x, x_scale, vecs, static_cast<__nv_bfloat16*>(out), counters, ncounters);
   return cudaGetLastError();
 }
 
@@ -1651,20 +1670,16 @@ moe_status moe_ffn_few(const moe_shape* s, const void* x, const uint8_t* x_scale
   const int nt = row_tiles(s, mx != nullptr);
   a.rows = 8 * nt;
 
-  cudaError_t e = cudaSuccess;
-  const bool convert = x_scale || mx;
-  if (convert) {
-    a.x = base + L.rows;
-    e = abi_tracked(kAbiFewRows, 1, st, [&] {
-      return launch_rows(s, x, x_scale, mx != nullptr, base + L.rows, reinterpret_cast<int*>(base + L.top),
-                         a.act_top, st);
-    });
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
-  }
+  if (x_scale || mx) a.x = base + L.rows;
+  cudaError_t e = abi_tracked(kAbiFewRows, 1, st, [&] {
+    return launch_rows(s, x, x_scale, mx != nullptr, base + L.rows, reinterpret_cast<int*>(base + L.top), a.act_top,
+                       a.counters, static_cast<int>((L.rows - L.counters0) / sizeof(unsigned)), st);
+  });
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
   e = abi_tracked(kAbiFewGateUp, 1, st, [&] {
-    if (s->dtype == MOE_FP32) return launch_nt<F32, 0>(a, nt, grid, convert, st);
-    if (mx) return launch_nt<Mx, 0>(a, nt, grid, convert, st);
-    return launch_nt<Bf16, 0>(a, nt, grid, convert, st);
+    if (s->dtype == MOE_FP32) return launch_nt<F32, 0>(a, nt, grid, st);
+    if (mx) return launch_nt<Mx, 0>(a, nt, grid, st);
+    return launch_nt<Bf16, 0>(a, nt, grid, st);
   });
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   a.x = a.act;
@@ -1676,9 +1691,9 @@ moe_status moe_ffn_few(const moe_shape* s, const void* x, const uint8_t* x_scale
   a.bias = bias ? bias->b_down : nullptr;
   a.counters = reinterpret_cast<unsigned*>(base + L.counters1);
   e = abi_tracked(kAbiFewDown, 1, st, [&] {
-    if (s->dtype == MOE_FP32) return launch_nt<F32, 1>(a, nt, grid, true, st);
-    if (mx) return launch_nt<Mx, 1>(a, nt, grid, true, st);
-    return launch_nt<Bf16, 1>(a, nt, grid, true, st);
+    if (s->dtype == MOE_FP32) return launch_nt<F32, 1>(a, nt, grid, st);
+    if (mx) return launch_nt<Mx, 1>(a, nt, grid, st);
+    return launch_nt<Bf16, 1>(a, nt, grid, st);
   });
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -403,9 +403,8 @@ typedef struct {
 size_t moe_few_workspace_size(const moe_shape* shape);
 
 /* The forward pass of the layer for a few tokens (inference), in two kernels
- * (and a small one before them for e4m3 tokens or 4-bit weights) that read each
- * touched expert's weights once: the y of moe_ffn_fwd, without its plan, gather
- * and grouped rows.
+ * (and a small one before them) that read each touched expert's weights once: the
+ * y of moe_ffn_fwd, without its plan, gather and grouped rows.
  *   T <= 128 (more: MOE_ERR_UNSUPPORTED); moe_ffn_fwd is the faster one where
  *     experts get dozens of rows each.
  *   x [T,H] in the storage dtype, or with x_scale != NULL e4m3 codes [T,H] with

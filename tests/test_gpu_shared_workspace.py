@@ -1,0 +1,64 @@
+"""Workspaces that other calls have used: a call's result does not depend on what
+its workspace holds (but for the error word, which the first zero-fill clears)."""
+
+import pytest
+import torch
+
+import dispatch_gemm_combine_gb300 as moe
+from test_gpu_few import CLAMPED, SWIGLU, make, run
+
+pytestmark = pytest.mark.gpu
+
+KINDS = [("bf16", False), ("bf16", True), ("fp32", False), ("mx", False), ("mx", True)]
+
+
+def used(n):
+    ws = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+    ws[:256] = 0
+    return ws
+
+
+def shape_of(c):
+    return moe.Shape(c["T"], c["H"], c["I"], c["E"], c["k"], c["act"],
+                     moe.MOE_FP32 if c["weights"] == "fp32" else moe.MOE_BF16, 7.0, 1.702, 0, 0)
+
+
+@pytest.mark.parametrize("weights,x8", KINDS)
+@pytest.mark.parametrize("T,H,I", [(1, 1088, 544), (5, 4160, 96), (20, 288, 320)])
+def test_few_on_a_used_workspace(weights, x8, T, H, I):
+    c = make(T, H, I, 6, 3, SWIGLU, weights, x8=x8, bias=True)
+    right, _ = run(c)
+    y, ws = run(c, ws=used(moe.moe_few_workspace_size(shape_of(c))))
+    moe.check_device_error(ws)
+    assert torch.equal(y, right)
+
+
+@pytest.mark.parametrize("weights,x8", KINDS)
+def test_few_of_two_shapes_in_turn(weights, x8):
+    small = make(6, 64, 1056, 4, 2, SWIGLU, weights, x8=x8)
+    large = make(3, 8224, 64, 4, 2, CLAMPED, weights, x8=x8, seed=1)
+    right = [run(c)[0] for c in (small, large)]
+    ws = torch.zeros(max(moe.moe_few_workspace_size(shape_of(c)) for c in (small, large)),
+                     dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        for c, r in zip((small, large), right):
+            assert torch.equal(run(c, ws=ws)[0], r)
+    moe.check_device_error(ws)
+
+
+def test_prompt_and_decode_on_one_workspace():
+    few = make(9, 264, 136, 8, 2, SWIGLU)
+    many = make(300, 264, 136, 8, 2, SWIGLU, seed=1)
+    s_few, s_many = shape_of(few), shape_of(many)
+    ws = torch.zeros(max(moe.moe_few_workspace_size(s_few), moe.moe_workspace_size(s_many, 1)),
+                     dtype=torch.uint8, device="cuda")
+    right, _ = run(few)
+    d = [many[n].cuda() for n in ("x", "idx", "w", "w_gate_up", "w_down")]
+    first = None
+    for _ in range(2):
+        y = torch.full((300, 264), 77.0, dtype=torch.bfloat16, device="cuda")
+        moe.ffn_fwd(s_many, *d, y, ws)
+        first = y if first is None else first
+        assert torch.equal(y, first)
+        assert torch.equal(run(few, ws=ws)[0], right)
+    moe.check_device_error(ws)
