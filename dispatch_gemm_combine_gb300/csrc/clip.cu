@@ -11,15 +11,16 @@
 //
 // The sum: each thread squares and adds the few dozen values of one chunk in
 // fp32; from there on sums are pairs of fp32 values (the sum and what it rounded
-// off), in a fixed order: the last block to finish adds all blocks' sums by index.
-// (Doubles in their place take 2 us more on a short list: this GPU adds few a clock.)
+// off), in a fixed order: every block of the second pass adds all blocks' sums by
+// index, so nothing but those sums goes from one kernel to the other.  (Doubles in
+// their place take 2 us more on a short list: this GPU adds few a clock.)
 // Squares of fp32 values leave fp32's range beyond 2^64 and below 2^-63, so
 // three sums run side by side, of g^2, (2^-80 g)^2 and (2^80 g)^2, and the
 // final step takes the one in range; the arithmetic is a tenth of what the
 // loads leave room for.
 //
-// Measured: 796 M fp32 values in 1.40 ms, 6.8 TB/s of what two reads and a write
-// move; a dozen small tensors in 14 us, two launches.
+// Measured: 796 M fp32 values in 1.41 ms, 6.8 TB/s of what two reads and a write
+// move; a dozen small tensors in 13 us, two launches.
 #include <algorithm>
 #include <cmath>
 
@@ -45,10 +46,6 @@ struct GradTable {
   uint8_t bf16[kBatch];
   uint8_t vec[kBatch];      // 16-byte accesses: src and dst are aligned for them
   int count;
-};
-
-struct ClipState {
-  unsigned done;            // blocks that have stored their sums; 0 between calls
 };
 
 // A sum as its rounded value and the rest.
@@ -163,13 +160,10 @@ __device__ __forceinline__ float root(const Pair& v) {
   return s > 0.f && isfinite(s) ? s + (fmaf(-s, s, v.hi) + v.lo) / (2.f * s) : s;
 }
 
-// `first`: this launch's place in the blocks' sums; `blocks_all`: the blocks of
-// all launches of the call, the last of which to finish writes the result.
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(
-    const __grid_constant__ GradTable t, int first, int blocks_all, float max_norm, Sums* sums,
-    ClipState* state, float* out) {
+// `first`: this launch's place in the blocks' sums.
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ GradTable t,
+                                                             int first, Sums* sums) {
   __shared__ Sums part[kThreads / 32];
-  __shared__ bool last;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Sums s{};
   const int chunks = t.chunk0[t.count];
@@ -185,23 +179,21 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(
     s = s + Sums{{a.mid, 0.f}, {a.big, 0.f}, {a.small, 0.f}};
   }
   const Sums b = block_sums(s, part);
-  if (threadIdx.x == 0) {
-    sums[first + blockIdx.x] = b;
-    unsigned old;   // after the sums' store, before the other blocks' are read
-    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(&state->done) : "memory");
-    last = old == static_cast<unsigned>(blocks_all - 1);
-  }
-  __syncthreads();
-  if (!last) return;
+  if (threadIdx.x == 0) sums[first + blockIdx.x] = b;
+}
+
+// (norm, coef) of all blocks' sums, the same in every thread of every block.
+__device__ __forceinline__ float2 norm_and_coef(const Sums* sums, int blocks, float max_norm) {
+  __shared__ Sums part[kThreads / 32];
+  __shared__ float2 result;
   Sums v{};
-  for (int i = threadIdx.x; i < blocks_all; i += kThreads) {
+  for (int i = threadIdx.x; i < blocks; i += kThreads) {
     const float2* q = reinterpret_cast<const float2*>(sums + i);
-    const float2 m = __ldcg(q), b2 = __ldcg(q + 1), s2 = __ldcg(q + 2);
-    v = v + Sums{{m.x, m.y}, {b2.x, b2.y}, {s2.x, s2.y}};
+    const float2 m = __ldcg(q), b = __ldcg(q + 1), s = __ldcg(q + 2);
+    v = v + Sums{{m.x, m.y}, {b.x, b.y}, {s.x, s.y}};
   }
   v = block_sums(v, part);
   if (threadIdx.x == 0) {
-    state->done = 0;
     // |g| <= 2^-20 throughout where the middle sum is below 2^-40, so the
     // scaled-up squares stay in range there
     float norm;
@@ -212,9 +204,10 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(
     else
       norm = root(v.mid);
     const float c = max_norm / (norm + 1e-6f);
-    out[0] = norm;
-    out[1] = isfinite(norm) && c < 1.f ? c : 1.f;
+    result = make_float2(norm, isfinite(norm) && c < 1.f ? c : 1.f);
   }
+  __syncthreads();
+  return result;
 }
 
 template <typename E>
@@ -249,10 +242,16 @@ __device__ __forceinline__ void scale_chunk(const E* p, E* d, int n, bool vec, f
     d[i] = copy ? p[i] : static_cast<E>(static_cast<float>(p[i]) * c);
 }
 
-__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ GradTable t,
-                                                              const float* norm) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the factor is there
-  const float c = __ldcg(norm + 1);
+// `out`: where the norm and the factor go, or null.  Five blocks per SM: with the 54
+// registers that the compiler would take four fit (796 M values: 28 us more); with six
+// or eight, those for the loads in flight are short (97 and 430 us more).
+__global__ void __launch_bounds__(kThreads, 5) grad_scale_kernel(const __grid_constant__ GradTable t,
+                                                              const Sums* sums, int blocks,
+                                                              float max_norm, float* out) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the sums are there
+  const float2 result = norm_and_coef(sums, blocks, max_norm);
+  const float c = result.y;
+  if (out && blockIdx.x == 0 && threadIdx.x == 0) out[0] = result.x, out[1] = c;
   const int chunks = t.chunk0[t.count];
   for (int r = blockIdx.x; r < chunks; r += gridDim.x) {
     const int ch = chunks - 1 - r;
@@ -326,12 +325,12 @@ extern "C" {
 
 size_t moe_grad_clip_workspace_size(const moe_grad_t* grads, int64_t n) {
   if (!grads_ok(grads, n)) return 0;
-  // the error word's place, the block counter, the blocks' sums; a launch that
-  // ends early for its chunks leaves the next one its tensors
+  // the error word's place, the blocks' sums; a launch that ends early for its
+  // chunks leaves the next one its tensors
   int64_t launches = 0;
   GradTable t;
   for (int64_t i = 0; i < n; ++launches) i = fill_table(grads, n, i, &t);
-  return 512 + sums_bytes(std::max<int64_t>(1, launches) * kBatch);
+  return 256 + sums_bytes(std::max<int64_t>(1, launches) * kBatch);
 }
 
 moe_status moe_grad_clip(const moe_grad_t* grads, int64_t n, float max_norm, float* norm_out,
@@ -344,58 +343,45 @@ moe_status moe_grad_clip(const moe_grad_t* grads, int64_t n, float max_norm, flo
   const moe_status ds = abi_device_sms(&sms);
   if (ds != MOE_OK) return ds;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  ClipState* state = reinterpret_cast<ClipState*>(static_cast<char*>(ws) + 256);
-  Sums* sums = reinterpret_cast<Sums*>(static_cast<char*>(ws) + 512);
+  Sums* sums = reinterpret_cast<Sums*>(static_cast<char*>(ws) + 256);
   GradTable t;
-  int64_t blocks_all = 0;
-  bool scale = false;
-  for (int64_t i = 0; i < n;) {
-    i = fill_table(grads, n, i, &t);
-    if (t.count) blocks_all += grid_of(t, sms);
-  }
-  for (int64_t i = 0; i < n; ++i) scale = scale || (grads[i].n > 0 && grads[i].dst);
-  if (blocks_all == 0) {   // no element: the norm is 0 and nothing is scaled
-    t.count = 0;
-    t.chunk0[0] = 0;
-    const cudaError_t e = abi_tracked(kAbiGradNorm, 1, st, [&] {
-      grad_norm_kernel<<<1, kThreads, 0, st>>>(t, 0, 1, max_norm, sums, state, norm_out);
-      return cudaGetLastError();
-    });
-    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-  }
-  int64_t first = 0;
+  int blocks = 0;
   for (int64_t i = 0; i < n;) {
     i = fill_table(grads, n, i, &t);
     if (!t.count) continue;
     const int grid = grid_of(t, sms);
     const cudaError_t e = abi_tracked(kAbiGradNorm, 1, st, [&] {
-      grad_norm_kernel<<<grid, kThreads, 0, st>>>(t, static_cast<int>(first),
-                                                  static_cast<int>(blocks_all), max_norm, sums,
-                                                  state, norm_out);
+      grad_norm_kernel<<<grid, kThreads, 0, st>>>(t, blocks, sums);
       return cudaGetLastError();
     });
     if (e != cudaSuccess) return MOE_ERR_CUDA;
-    first += grid;
+    blocks += grid;
   }
-  if (!scale) return MOE_OK;
-  int i_scaled = 0;
-  for (int64_t i = 0; i < n;) {
+  bool scale = false;
+  for (int64_t i = 0; i < n; ++i) scale = scale || (grads[i].n > 0 && grads[i].dst);
+  // Where there is nothing to scale, one block for the norm (0 of no element).
+  bool first = true;
+  for (int64_t i = scale ? 0 : n; i < n || first;) {
+    t.count = 0;
+    t.chunk0[0] = 0;
     i = fill_table(grads, n, i, &t);
-    if (!t.count) continue;
+    if (scale && !t.count) continue;
     // (the first may start while the norm's last blocks end)
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid_of(t, sms));
+    cfg.gridDim = dim3(std::max(1, grid_of(t, sms)));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = i_scaled++ == 0 ? 1 : 0;
+    cfg.numAttrs = first && blocks > 0 ? 1 : 0;
+    float* out = first ? norm_out : nullptr;
     const cudaError_t e = abi_tracked(kAbiGradScale, 1, st, [&] {
-      return cudaLaunchKernelEx(&cfg, grad_scale_kernel, t, static_cast<const float*>(norm_out));
+      return cudaLaunchKernelEx(&cfg, grad_scale_kernel, t, static_cast<const Sums*>(sums), blocks, max_norm, out);
     });
     if (e != cudaSuccess) return MOE_ERR_CUDA;
+    first = false;
   }
   return MOE_OK;
 }

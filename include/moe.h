@@ -359,18 +359,18 @@ typedef struct {
   int32_t dtype;
 } moe_grad_t;
 
-/* Bytes of workspace of moe_grad_clip for this list (0 for a bad list).  It is
- * zero-filled by the caller before its first use and 256-byte aligned. */
+/* Bytes of workspace of moe_grad_clip for this list (0 for a bad list). */
 size_t moe_grad_clip_workspace_size(const moe_grad_t* grads, int64_t n);
 
 /* Global norm of a list of gradients, and clipping by it:
  *   norm = sqrt(sum over all elements of all tensors of g^2),
  *   coef = min(1, max_norm / (norm + 1e-6)),  dst = coef * src.
  *   norm_out [2] fp32 (device): norm, coef.
- * The squares are summed in fp32 and double in a fixed order, in range for every
- * finite fp32 gradient.  A norm that is not finite (a gradient holds an
- * infinity or a NaN) gives coef = 1: the gradients come through unscaled and
- * norm_out tells the caller to skip the step.  max_norm >= 0 (infinity: never
+ * The squares are summed in fp32 and in pairs of fp32 values (a sum and what it
+ * rounded off) in a fixed order, in range for every finite fp32 gradient.  A norm
+ * that is not finite (a gradient holds an infinity or a NaN, or the norm itself is
+ * outside fp32) gives coef = 1: the gradients come through unscaled and norm_out
+ * tells the caller to skip the step.  max_norm >= 0 (infinity: never
  * clips).  dst is src or does not overlap any src.  The list is read before the
  * call returns.  An empty list has the norm 0. */
 moe_status moe_grad_clip(const moe_grad_t* grads, int64_t n, float max_norm, float* norm_out,

@@ -6,6 +6,7 @@ import torch
 
 import dispatch_gemm_combine_gb300 as moe
 from test_gpu_few import CLAMPED, SWIGLU, make, run
+from test_gpu_grad_clip import tensors
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +63,36 @@ def test_prompt_and_decode_on_one_workspace():
         assert torch.equal(y, first)
         assert torch.equal(run(few, ws=ws)[0], right)
     moe.check_device_error(ws)
+
+
+@pytest.mark.parametrize("sizes", [[5], [1000, 3, 70000], [333] * 250, [4 << 20]])
+@pytest.mark.parametrize("scaled", [True, False])
+def test_grad_clip_on_a_used_workspace(sizes, scaled):
+    dev = [t.cuda() for t in tensors(sizes, [torch.float32, torch.bfloat16])]
+    out = []
+    for fill in (False, True):
+        dst = [torch.full_like(t, 9.0) for t in dev]
+        t = moe.grad_table(dev, dst if scaled else False)
+        ws = moe.grad_clip_workspace(t)
+        if fill:
+            ws = used(ws.numel())
+        norm = torch.full((2,), -1.0, device="cuda")
+        moe.grad_clip(t, 0.01, norm, ws)
+        out.append([norm] + dst)
+    assert out[0][0][0] > 0
+    assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+def test_clip_and_few_on_one_workspace():
+    c = make(4, 320, 96, 6, 2, SWIGLU, "mx")
+    right, _ = run(c)
+    dev = [t.cuda() for t in tensors([5000, 70000], [torch.float32])]
+    t = moe.grad_table(dev, False)
+    ws = torch.zeros(max(moe.moe_few_workspace_size(shape_of(c)), moe.grad_clip_workspace(t).numel()),
+                     dtype=torch.uint8, device="cuda")
+    norm, first = torch.empty(2, device="cuda"), None
+    for _ in range(2):
+        moe.grad_clip(t, 1.0, norm, ws)
+        first = norm.clone() if first is None else first
+        assert torch.equal(norm, first)
+        assert torch.equal(run(c, ws=ws)[0], right)
