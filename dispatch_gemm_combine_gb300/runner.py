@@ -89,6 +89,7 @@ class LayerRunner:
         the forward.  With recompute the saved context is not used: the
         backward recomputes it in a larger workspace (allocated on first use)."""
         with_bias = b_gate_up is not None or b_down is not None
+        self.gave_bias = with_bias      # what clip_grads takes
         bias = None
         if with_bias:
             if getattr(self, "db_gate_up", None) is None:
@@ -112,7 +113,7 @@ class LayerRunner:
         gave them), with those of `extra` (tensors), so that their global norm is at
         most max_norm, in place.  Returns (norm before, factor) as a tensor [2]."""
         grads = [self.dw_gate_up, self.dw_down]
-        if getattr(self, "db_gate_up", None) is not None:
+        if getattr(self, "gave_bias", False):
             grads += [self.db_gate_up, self.db_down]
         table = grad_table(grads + list(extra))
         ws = getattr(self, "ws_clip", None)

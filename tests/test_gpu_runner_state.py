@@ -1,0 +1,49 @@
+"""What LayerRunner keeps between calls: bias gradients of an earlier backward."""
+
+import pytest
+import torch
+
+import dispatch_gemm_combine_gb300 as moe
+from dispatch_gemm_combine_gb300.runner import LayerRunner
+
+pytestmark = pytest.mark.gpu
+
+H, I, E, K = 96, 64, 4, 2
+
+
+def inputs(T, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def bf16(*shape, std=1.0):
+        return (std * torch.randn(shape, generator=g, device="cuda")).to(torch.bfloat16)
+
+    idx = torch.topk(torch.randn((T, E), generator=g, device="cuda"), K, dim=-1).indices.to(torch.int32)
+    w = torch.full((T, K), 0.5, device="cuda")
+    return dict(x=bf16(T, H), idx=idx.contiguous(), w=w, wgu=bf16(E, H, 2 * I, std=0.1),
+                wd=bf16(E, I, H, std=0.1), dy=bf16(T, H), bgu=bf16(E, 2 * I, std=0.1), bd=bf16(E, H, std=0.1))
+
+
+def train(r, d, bias):
+    a = [d[n] for n in ("x", "idx", "w", "wgu", "wd")]
+    b = dict(b_gate_up=d["bgu"], b_down=d["bd"]) if bias else {}
+    r.plan(d["idx"])
+    r.forward(*a, **b)
+    r.backward(d["dy"], *a, **b)
+
+
+def test_clip_grads_takes_the_last_backwards_gradients():
+    d = inputs(40)
+    r = LayerRunner(40, H, I, E, K, moe.MOE_ACT_SWIGLU)
+    train(r, d, True)
+    norm = r.clip_grads(float("inf"))[0].item()
+    ref = sum(float(t.double().square().sum()) for t in (r.dw_gate_up, r.dw_down, r.db_gate_up, r.db_down)) ** 0.5
+    assert abs(norm - ref) <= 1e-6 * ref
+    stale = r.db_gate_up.clone(), r.db_down.clone()
+    train(r, d, False)
+    ref = sum(float(t.double().square().sum()) for t in (r.dw_gate_up, r.dw_down)) ** 0.5
+    norm = r.clip_grads(0.25 * ref)
+    assert abs(norm[0].item() - ref) <= 1e-6 * ref
+    assert torch.equal(r.db_gate_up, stale[0]) and torch.equal(r.db_down, stale[1])
+    train(r, d, True)
+    ref = sum(float(t.double().square().sum()) for t in (r.dw_gate_up, r.dw_down, r.db_gate_up, r.db_down)) ** 0.5
+    assert abs(r.clip_grads(float("inf"))[0].item() - ref) <= 1e-6 * ref
