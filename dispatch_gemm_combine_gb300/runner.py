@@ -4,6 +4,10 @@
 saved context and the outputs for a fixed shape once, then runs
 moe_plan / moe_ffn_fwd / moe_ffn_bwd on them.  All arithmetic happens in the
 library's kernels.
+
+What only some calls need is made at the first of them, with that call's stream
+current: a zero-fill comes before the kernels that use the buffer, and the allocator
+gives no memory that another stream still has work for.
 """
 
 import torch
@@ -30,6 +34,7 @@ class LayerRunner:
         self.saved = (torch.empty(moe_saved_size(self.shape), dtype=torch.uint8, device=device)
                       if training else None)
         self.y = torch.empty((T, H), dtype=odt, device=device)
+        self.gave_bias = False
         if backward:
             self.dx = torch.empty((T, H), dtype=odt, device=device)
             self.d_topk_w = torch.empty((T, k), dtype=torch.float32, device=device)
@@ -60,7 +65,8 @@ class LayerRunner:
         """Keep both weights in microscaled 4-bit for few(): (codes, scales) of
         w_gate_up and of w_down.  Call it again when the weights change."""
         E, H, I = self.shape.E, self.shape.H, self.shape.I
-        self.mx_t = mx_alloc(E, H, 2 * I, self.device) + mx_alloc(E, I, H, self.device)
+        with torch.cuda.stream(stream):
+            self.mx_t = mx_alloc(E, H, 2 * I, self.device) + mx_alloc(E, I, H, self.device)
         mx_quantize(w_gate_up, *self.mx_t[:2], stream=stream)
         mx_quantize(w_down, *self.mx_t[2:], stream=stream)
         self.mx_s = mx_struct(*self.mx_t)
@@ -72,7 +78,8 @@ class LayerRunner:
         Without weights, on the 4-bit ones that quantize() keeps.  x may be e4m3
         codes with x_scale, as rms_norm_fwd gives them."""
         if getattr(self, "ws_few", None) is None:
-            self.ws_few = few_workspace(self.shape, self.device)
+            with torch.cuda.stream(stream):
+                self.ws_few = few_workspace(self.shape, self.device)
         mx = None
         if w_gate_up is None and w_down is None:
             mx = getattr(self, "mx_s", None)
@@ -94,12 +101,14 @@ class LayerRunner:
         if with_bias:
             if getattr(self, "db_gate_up", None) is None:
                 E, H, I = self.shape.E, self.shape.H, self.shape.I
-                self.db_gate_up = torch.empty((E, 2 * I), dtype=torch.float32, device=self.device)
-                self.db_down = torch.empty((E, H), dtype=torch.float32, device=self.device)
+                with torch.cuda.stream(stream):
+                    self.db_gate_up = torch.empty((E, 2 * I), dtype=torch.float32, device=self.device)
+                    self.db_down = torch.empty((E, H), dtype=torch.float32, device=self.device)
             bias = bias_struct(b_gate_up, b_down, self.db_gate_up, self.db_down)
         if recompute:
             if getattr(self, "ws_bwd_recompute", None) is None:
-                self.ws_bwd_recompute = workspace(self.shape, 3, self.device)
+                with torch.cuda.stream(stream):
+                    self.ws_bwd_recompute = workspace(self.shape, 3, self.device)
             ws, saved = self.ws_bwd_recompute, None
         else:
             ws, saved = self.ws_bwd, self.saved
@@ -113,13 +122,14 @@ class LayerRunner:
         gave them), with those of `extra` (tensors), so that their global norm is at
         most max_norm, in place.  Returns (norm before, factor) as a tensor [2]."""
         grads = [self.dw_gate_up, self.dw_down]
-        if getattr(self, "gave_bias", False):
+        if self.gave_bias:
             grads += [self.db_gate_up, self.db_down]
         table = grad_table(grads + list(extra))
         ws = getattr(self, "ws_clip", None)
         if ws is None or self.clip_count < table.count:
-            self.ws_clip, self.clip_count = grad_clip_workspace(table, self.device), table.count
-            self.clip_norm = torch.empty(2, dtype=torch.float32, device=self.device)
+            with torch.cuda.stream(stream):
+                self.ws_clip, self.clip_count = grad_clip_workspace(table, self.device), table.count
+                self.clip_norm = torch.empty(2, dtype=torch.float32, device=self.device)
         grad_clip(table, max_norm, self.clip_norm, self.ws_clip, stream)
         return self.clip_norm
 

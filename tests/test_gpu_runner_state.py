@@ -1,4 +1,5 @@
-"""What LayerRunner keeps between calls: bias gradients of an earlier backward."""
+"""What LayerRunner keeps between calls: bias gradients of an earlier backward, and
+buffers made at a call on another stream."""
 
 import pytest
 import torch
@@ -47,3 +48,39 @@ def test_clip_grads_takes_the_last_backwards_gradients():
     train(r, d, True)
     ref = sum(float(t.double().square().sum()) for t in (r.dw_gate_up, r.dw_down, r.db_gate_up, r.db_down)) ** 0.5
     assert abs(r.clip_grads(float("inf"))[0].item() - ref) <= 1e-6 * ref
+
+
+def test_first_few_on_another_stream_keeps_its_error():
+    d = inputs(3)
+    r = LayerRunner(3, H, I, E, K, moe.MOE_ACT_SWIGLU, training=False, backward=False)
+    d["idx"][1, 1] = E
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)         # what the current stream still has to do
+    r.few(*[d[n] for n in ("x", "idx", "w", "wgu", "wd")], stream=s)
+    torch.cuda.synchronize()
+    with pytest.raises(moe.MoeError) as e:
+        r.check()
+    assert e.value.status == moe.MOE_ERR_BAD_INDEX
+
+
+def test_buffers_made_at_a_call_are_its_streams():
+    """... so that what the allocator hands out has no work of another stream pending."""
+    d = inputs(40)
+    r = LayerRunner(40, H, I, E, K, moe.MOE_ACT_SWIGLU)
+    s = torch.cuda.Stream()
+    many = [torch.ones(3, device="cuda") for _ in range(300)]
+    torch.cuda.synchronize()
+    a = [d[n] for n in ("x", "idx", "w", "wgu", "wd")]
+    bias = dict(b_gate_up=d["bgu"], b_down=d["bd"])
+    r.plan(d["idx"], stream=s)
+    r.forward(*a, stream=s, **bias)
+    r.backward(d["dy"], *a, recompute=True, stream=s, **bias)
+    r.clip_grads(1.0, extra=many, stream=s)
+    r.quantize(d["wgu"], d["wd"], stream=s)
+    torch.cuda.synchronize()
+    made = [r.ws_bwd_recompute, r.db_gate_up, r.db_down, r.ws_clip, *r.mx_t]
+    for t in made:
+        at = [g for g in torch.cuda.memory_snapshot()
+              if g["address"] <= t.data_ptr() < g["address"] + g["total_size"]]
+        assert len(at) == 1 and at[0]["stream"] == s.cuda_stream
