@@ -14,7 +14,8 @@ import torch
 
 from . import (MOE_BF16, MOE_FP32, Shape, alloc_plan, bias_struct, check_device_error, ffn_bwd,
                ffn_few, ffn_fwd, few_workspace, grad_clip, grad_clip_workspace, grad_table,
-               moe_saved_size, mx_alloc, mx_quantize, mx_struct, plan, route, workspace)
+               moe_grad_clip_workspace_size, moe_saved_size, mx_alloc, mx_quantize, mx_struct,
+               plan, route, workspace)
 
 _TORCH_DTYPE = {MOE_BF16: torch.bfloat16, MOE_FP32: torch.float32}
 
@@ -35,6 +36,7 @@ class LayerRunner:
                       if training else None)
         self.y = torch.empty((T, H), dtype=odt, device=device)
         self.gave_bias = False
+        self.ws_clip, self.ws_clips = None, []
         if backward:
             self.dx = torch.empty((T, H), dtype=odt, device=device)
             self.d_topk_w = torch.empty((T, k), dtype=torch.float32, device=device)
@@ -63,10 +65,12 @@ class LayerRunner:
 
     def quantize(self, w_gate_up, w_down, stream=None):
         """Keep both weights in microscaled 4-bit for few(): (codes, scales) of
-        w_gate_up and of w_down.  Call it again when the weights change."""
-        E, H, I = self.shape.E, self.shape.H, self.shape.I
-        with torch.cuda.stream(stream):
-            self.mx_t = mx_alloc(E, H, 2 * I, self.device) + mx_alloc(E, I, H, self.device)
+        w_gate_up and of w_down.  Call it again when the weights change: the same
+        tensors then hold the new ones, for captured graphs too."""
+        if getattr(self, "mx_t", None) is None:
+            E, H, I = self.shape.E, self.shape.H, self.shape.I
+            with torch.cuda.stream(stream):
+                self.mx_t = mx_alloc(E, H, 2 * I, self.device) + mx_alloc(E, I, H, self.device)
         mx_quantize(w_gate_up, *self.mx_t[:2], stream=stream)
         mx_quantize(w_down, *self.mx_t[2:], stream=stream)
         self.mx_s = mx_struct(*self.mx_t)
@@ -125,11 +129,13 @@ class LayerRunner:
         if self.gave_bias:
             grads += [self.db_gate_up, self.db_down]
         table = grad_table(grads + list(extra))
-        ws = getattr(self, "ws_clip", None)
-        if ws is None or self.clip_count < table.count:
+        if self.ws_clip is None or self.ws_clip.numel() < moe_grad_clip_workspace_size(table, table.count):
             with torch.cuda.stream(stream):
-                self.ws_clip, self.clip_count = grad_clip_workspace(table, self.device), table.count
-                self.clip_norm = torch.empty(2, dtype=torch.float32, device=self.device)
+                if self.ws_clip is None:
+                    self.clip_norm = torch.empty(2, dtype=torch.float32, device=self.device)
+                self.ws_clip = grad_clip_workspace(table, self.device)
+            # those of shorter lists stay for the graphs that may have been captured with them
+            self.ws_clips.append(self.ws_clip)
         grad_clip(table, max_norm, self.clip_norm, self.ws_clip, stream)
         return self.clip_norm
 

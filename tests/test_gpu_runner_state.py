@@ -1,5 +1,6 @@
-"""What LayerRunner keeps between calls: bias gradients of an earlier backward, and
-buffers made at a call on another stream."""
+"""What LayerRunner keeps between calls: bias gradients of an earlier backward,
+buffers made at a call on another stream, 4-bit weights and clipping workspaces
+that a captured graph still uses."""
 
 import pytest
 import torch
@@ -84,3 +85,53 @@ def test_buffers_made_at_a_call_are_its_streams():
         at = [g for g in torch.cuda.memory_snapshot()
               if g["address"] <= t.data_ptr() < g["address"] + g["total_size"]]
         assert len(at) == 1 and at[0]["stream"] == s.cuda_stream
+
+
+def test_quantizing_again_serves_the_new_weights_in_a_captured_graph():
+    d, new = inputs(5), inputs(5, seed=1)
+    r = LayerRunner(5, H, I, E, K, moe.MOE_ACT_SWIGLU, training=False, backward=False)
+    first = r.quantize(d["wgu"], d["wd"])
+    at = [t.data_ptr() for t in first]
+    a = [d[n] for n in ("x", "idx", "w")]
+    r.few(*a)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r.few(*a)
+    second = r.quantize(new["wgu"], new["wd"])
+    assert [t.data_ptr() for t in second] == at
+    fresh = LayerRunner(5, H, I, E, K, moe.MOE_ACT_SWIGLU, training=False, backward=False)
+    fresh.quantize(new["wgu"], new["wd"])
+    right = fresh.few(*a)
+    r.y.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(r.y, right)
+
+
+def test_clip_grads_with_lists_that_grow():
+    d = inputs(40)
+    r = LayerRunner(40, H, I, E, K, moe.MOE_ACT_SWIGLU)
+    train(r, d, False)
+    kept = r.dw_gate_up.clone(), r.dw_down.clone()
+    norm = r.clip_grads(1e-3)
+    right = norm.clone()
+    scaled = r.dw_gate_up.clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r.clip_grads(1e-3)
+    for n in (90, 250, 400):      # one launch's tensors, several, more
+        extra = [torch.full((5,), 2.0, device="cuda") for _ in range(n)]
+        r.dw_gate_up.copy_(kept[0]), r.dw_down.copy_(kept[1])
+        out = r.clip_grads(float("inf"), extra=extra)
+        ref = (float(kept[0].double().square().sum()) + float(kept[1].double().square().sum()) + 20.0 * n) ** 0.5
+        assert abs(out[0].item() - ref) <= 1e-6 * ref
+        assert out.data_ptr() == norm.data_ptr()
+    # a list with empty entries, then a shorter one without
+    r.clip_grads(1.0, extra=[torch.empty(0, device="cuda")] * 900)
+    r.clip_grads(1.0, extra=[torch.ones(1, device="cuda")] * 500)
+    r.dw_gate_up.copy_(kept[0]), r.dw_down.copy_(kept[1])
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(norm, right) and torch.equal(r.dw_gate_up, scaled)
