@@ -341,9 +341,12 @@ def route(shape, logits, topk_idx, topk_w, plan_struct=None, ws=None, stream=Non
 
 def bias_struct(b_gate_up=None, b_down=None, db_gate_up=None, db_down=None):
     """MoeBias over torch tensors (None = absent), or None when all are absent."""
-    if all(t is None for t in (b_gate_up, b_down, db_gate_up, db_down)):
+    ts = (b_gate_up, b_down, db_gate_up, db_down)
+    if all(t is None for t in ts):
         return None
-    return MoeBias(_ptr(b_gate_up), _ptr(b_down), _ptr(db_gate_up), _ptr(db_down))
+    s = MoeBias(*[_ptr(t) for t in ts])
+    s.tensors = ts                   # they live as long as the struct
+    return s
 
 
 def plan(shape, topk_idx, plan_struct, ws, stream=None):
@@ -539,9 +542,18 @@ def mx_struct(codes_gate_up, scales_gate_up, codes_down, scales_down):
     """MoeMxWeights over the tensors mx_quantize filled for w_gate_up and w_down."""
     import torch
     ts = (codes_gate_up, scales_gate_up, codes_down, scales_down)
-    for name, t in zip(("codes_gate_up", "scales_gate_up", "codes_down", "scales_down"), ts):
-        _dense("mx_struct", name, t, t.shape, torch.uint8)
-    return MoeMxWeights(*[t.data_ptr() for t in ts])
+    s = MoeMxWeights(*[_dense("mx_struct", f[0], t, t.shape, torch.uint8)
+                       for f, t in zip(MoeMxWeights._fields_, ts)])
+    s.tensors = ts                   # they live as long as the struct
+    s.shapes = tuple(t.shape for t in ts)
+    return s
+
+
+def _check_mx(where, mx, E, H, I):
+    """The shapes of mx_struct's tensors are those of a layer with these sizes."""
+    if mx.shapes != ((E, 2 * I, H // 2), (E, 2 * I, H // 32), (E, H, I // 2), (E, H, I // 32)):
+        raise ValueError("%s: 4-bit weights of shapes %s are not those of a layer with %d experts, H = %d, I = %d"
+                         % (where, [tuple(s) for s in mx.shapes], E, H, I))
 
 
 def ffn_few(shape, x, topk_idx, topk_w, w_gate_up, w_down, y, ws, stream=None, bias=None,
@@ -556,6 +568,11 @@ def ffn_few(shape, x, topk_idx, topk_w, w_gate_up, w_down, y, ws, stream=None, b
     xdt = dt
     if x_scale is not None:
         xdt = torch.float8_e4m3fn if x.dtype is torch.float8_e4m3fn else torch.uint8
+    if hasattr(mx, "shapes"):        # (a struct filled by hand names no tensors)
+        _check_mx(f, mx, E, H, I)
+    if hasattr(bias, "tensors"):
+        _dense(f, "b_gate_up", bias.tensors[0], (E, 2 * I), dt)
+        _dense(f, "b_down", bias.tensors[1], (E, H), dt)
     _check(lib().moe_ffn_few(
         ctypes.byref(shape), _dense(f, "x", x, (T, H), xdt),
         _dense(f, "x_scale", x_scale, (T, H // 32), torch.uint8),
