@@ -415,6 +415,15 @@ def _dense(where, name, t, shape, dtype):
         "" if t.is_contiguous() else " (strided)"))
 
 
+def _ws(where, ws):
+    """(address, bytes) of a workspace, after a check that it is on the GPU and dense."""
+    if ws is None:
+        return None, 0
+    if ws.is_cuda and ws.is_contiguous():
+        return ws.data_ptr(), ws.numel() * ws.element_size()
+    raise ValueError("%s: the workspace must be a dense tensor on the GPU" % where)
+
+
 def rms_norm_workspace(T, H, device="cuda"):
     """Zero-filled workspace of rms_norm_bwd for at most T rows of H columns."""
     import torch
@@ -458,8 +467,8 @@ def rms_norm_bwd(dy, total, rstd, weight, dx, dweight=None, d_total=None, ws=Non
         T, H, code, _dense(w, "dy", dy, shape, dt), _dense(w, "d_total", d_total, shape, dt),
         _dense(w, "total", total, shape, dt), _dense(w, "rstd", rstd, (T,), torch.float32),
         _dense(w, "weight", weight, (H,), dt), _dense(w, "dx", dx, shape, dt),
-        _dense(w, "dweight", dweight, (H,), torch.float32), _ptr(ws),
-        0 if ws is None else ws.numel(), _stream(stream)), "moe_rms_norm_bwd")
+        _dense(w, "dweight", dweight, (H,), torch.float32), *_ws(w, ws), _stream(stream)),
+        "moe_rms_norm_bwd")
 
 
 def grad_table(grads, out=None):
@@ -495,8 +504,8 @@ def grad_clip(table, max_norm, norm, ws, stream=None):
     (1 where nothing is clipped, or where the norm is not finite)."""
     import torch
     _check(lib().moe_grad_clip(table, table.count, max_norm,
-                               _dense("grad_clip", "norm", norm, (2,), torch.float32), _ptr(ws),
-                               ws.numel(), _stream(stream)), "moe_grad_clip")
+                               _dense("grad_clip", "norm", norm, (2,), torch.float32),
+                               *_ws("grad_clip", ws), _stream(stream)), "moe_grad_clip")
 
 
 def mx_alloc(E, K, N, device="cuda"):
@@ -580,7 +589,7 @@ def ffn_few(shape, x, topk_idx, topk_w, w_gate_up, w_down, y, ws, stream=None, b
         _dense(f, "topk_w", topk_w, (T, k), torch.float32),
         _dense(f, "w_gate_up", w_gate_up, (E, H, 2 * I), dt),
         _dense(f, "w_down", w_down, (E, I, H), dt), _byref(mx), _byref(bias),
-        _dense(f, "y", y, (T, H), torch.float32 if shape.out_fp32 else dt), _ptr(ws), ws.numel(),
+        _dense(f, "y", y, (T, H), torch.float32 if shape.out_fp32 else dt), *_ws(f, ws),
         _stream(stream)), "moe_ffn_few")
 
 

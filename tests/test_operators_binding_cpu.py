@@ -116,3 +116,19 @@ def test_biases_of_another_kind_are_refused(library, b_gate_up, b_down):
     with pytest.raises(ValueError):
         few(library, bias=moe.bias_struct(b_gate_up, b_down))
     assert library.calls == []
+
+
+def test_workspaces_on_the_host_are_refused(library):
+    host = torch.zeros(1 << 20, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        few(library, ws=host)
+    table = (moe.MoeGrad * 1)()
+    table.count = 0
+    with pytest.raises(ValueError):
+        moe.grad_clip(table, 1.0, Fake((2,), torch.float32), host)
+    with pytest.raises(ValueError):
+        moe.rms_norm_bwd(bf16(T, H), bf16(T, H), Fake((T,), torch.float32), bf16(H), bf16(T, H),
+                         Fake((H,), torch.float32), ws=host)
+    assert library.calls == []
+    moe.rms_norm_bwd(bf16(T, H), bf16(T, H), Fake((T,), torch.float32), bf16(H), bf16(T, H))
+    assert library.calls == ["moe_rms_norm_bwd"]
