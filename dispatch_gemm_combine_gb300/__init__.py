@@ -548,7 +548,8 @@ def few_workspace(shape, device="cuda"):
 
 
 def mx_struct(codes_gate_up, scales_gate_up, codes_down, scales_down):
-    """MoeMxWeights over the tensors mx_quantize filled for w_gate_up and w_down."""
+    """MoeMxWeights over the tensors mx_quantize filled for w_gate_up and w_down
+    (ffn_few checks their shapes)."""
     import torch
     ts = (codes_gate_up, scales_gate_up, codes_down, scales_down)
     s = MoeMxWeights(*[_dense("mx_struct", f[0], t, t.shape, torch.uint8)

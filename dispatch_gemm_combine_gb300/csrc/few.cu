@@ -32,10 +32,11 @@
 // 4-bit weights.  fp32 weights keep it in fp32 and multiply on the CUDA cores in fp32.
 //
 // Measured, of the bytes of the touched experts' weights (a copy reaches 6.76 TB/s):
-// 16 tokens on 256 bf16 experts of 4096 x 2048 (5.1 GB) 745 us, 6.9 TB/s; one token
-// on four of 2880 x 2880 (199 MB) 48 us, of which 35 us stream at 5.5 TB/s and the
-// rest is start, joins and the step between the kernels; 32 tokens on 64 4-bit
-// experts of 8192 x 2048 (1.7 GB) 365 us, 4.6 TB/s, bound by instructions.
+// 16 tokens on 256 bf16 experts of 4096 x 2048 (5.1 GB) 745 to 847 us by machine and
+// pass, 6.1 to 6.9 TB/s; one token on four of 2880 x 2880 (199 MB) 47 us, of which 36 us
+// stream at 5.5 TB/s and the rest is start, joins and the step between the kernels; 32
+// tokens on 64 4-bit experts of 8192 x 2048 (1.7 GB) 366 to 380 us, 4.5 TB/s, bound by
+// instructions.
 #include <cuda.h>
 
 #include <algorithm>
@@ -545,7 +546,7 @@ constexpr int kTokenTop = 14, kActTop = 7;
 // two weights (half of all that a step takes).  A lane takes whole blocks (16 bytes)
 // of columns g, g + 8, g + 16 and g + 24, so each has one scale 2^q.  The codes come
 // by TMA, two steps ahead and across the ends of units: with two steps in registers
-// instead, 32 tokens on 64 experts take 465 us, not 365, and a ring of four smaller
+// instead, 32 tokens on 64 experts took 465 us, not 365, and a ring of four smaller
 // steps takes 427.  What is left to wait for are tokens and scale bytes at a unit's
 // start.  fp16 holds 2^q times a code exactly only near 1, so a column's weights are
 // scaled by 2^(q - ref), ref being the scale of the first block that the warp sees of

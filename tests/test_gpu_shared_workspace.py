@@ -96,3 +96,23 @@ def test_clip_and_few_on_one_workspace():
         first = norm.clone() if first is None else first
         assert torch.equal(norm, first)
         assert torch.equal(run(c, ws=ws)[0], right)
+
+
+@pytest.mark.parametrize("dtype", [moe.MOE_BF16, moe.MOE_FP32])
+@pytest.mark.parametrize("recompute", [False, True])
+def test_the_layer_on_used_workspaces(dtype, recompute):
+    from dispatch_gemm_combine_gb300.runner import LayerRunner
+    c = make(70, 264, 136, 8, 2, SWIGLU, "fp32" if dtype == moe.MOE_FP32 else "bf16")
+    a = [c[n].cuda() for n in ("x", "idx", "w", "w_gate_up", "w_down")]
+    out = []
+    for fill in (False, True):
+        r = LayerRunner(70, 264, 136, 8, 2, SWIGLU, dtype)
+        r.ws_bwd_recompute = moe.workspace(r.shape, 3)
+        if fill:
+            for ws in (r.ws_plan, r.ws_fwd, r.ws_bwd, r.ws_bwd_recompute):
+                ws[256:] = 0xA5
+        r.plan(a[1])
+        y = r.forward(*a).clone()
+        out.append((y,) + tuple(t.clone() for t in r.backward(a[0], *a, recompute=recompute)))
+        r.check()
+    assert all(torch.equal(p, q) for p, q in zip(*out))
