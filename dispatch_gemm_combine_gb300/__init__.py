@@ -26,7 +26,11 @@ __all__ = [
     "moe_grad_clip_workspace_size", "moe_grad_clip", "grad_table", "grad_clip_workspace",
     "grad_clip", "moe_mx_quantize", "moe_mx_dequantize", "mx_alloc", "mx_quantize",
     "mx_dequantize", "MoeMxWeights", "moe_few_workspace_size", "moe_ffn_few", "few_workspace",
-    "mx_struct", "ffn_few",
+    "mx_struct", "ffn_few", "moe_join_norm_workspace_size", "moe_join_norm_fwd",
+    "moe_join_norm_bwd", "join_norm_workspace", "join_norm_fwd", "join_norm_bwd",
+    "moe_route_bwd_workspace_size", "moe_route_bwd", "route_bwd_workspace", "route_bwd",
+    "moe_orthogonalize_workspace_size", "moe_orthogonalize", "orthogonalize_workspace",
+    "orthogonalize",
 ]
 
 MOE_OK = 0
@@ -150,6 +154,21 @@ def lib():
     L.moe_few_workspace_size.restype = SZ
     L.moe_ffn_few.argtypes = [S, P, P, P, P, P, P, ctypes.POINTER(MoeMxWeights), B, P, P, SZ, P]
     L.moe_ffn_few.restype = ctypes.c_int
+    L.moe_join_norm_fwd.argtypes = [I64, I32, I32, P, P, I32, P, P, F32, P, F32, P, P, P, P, P, P]
+    L.moe_join_norm_fwd.restype = ctypes.c_int
+    L.moe_join_norm_workspace_size.argtypes = [I64, I32]
+    L.moe_join_norm_workspace_size.restype = SZ
+    L.moe_join_norm_bwd.argtypes = ([I64, I32, I32] + [P] * 9 + [F32] + [P] * 6 + [SZ, P])
+    L.moe_join_norm_bwd.restype = ctypes.c_int
+    L.moe_route_bwd_workspace_size.argtypes = [S]
+    L.moe_route_bwd_workspace_size.restype = SZ
+    L.moe_route_bwd.argtypes = [S, P, P, P, P, P, F32, F32, P, P, P, SZ, P]
+    L.moe_route_bwd.restype = ctypes.c_int
+    L.moe_orthogonalize_workspace_size.argtypes = [I64, I64, I64]
+    L.moe_orthogonalize_workspace_size.restype = SZ
+    L.moe_orthogonalize.argtypes = [I64, I64, I64, I32, P, I64, I64, I32, P, F32, F32, P, I64, I64, P,
+                                    SZ, P]
+    L.moe_orthogonalize.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -211,7 +230,7 @@ def moe_profile_kernel_name(kind):
 
 def moe_profile_read():
     """{kernel kind name: (total ms, launches)} since the last read."""
-    n = 32
+    n = 64
     ms = (ctypes.c_double * n)()
     cnt = (ctypes.c_uint64 * n)()
     k = lib().moe_profile_read(ms, cnt, n)
@@ -277,6 +296,46 @@ def moe_ffn_few(shape, x, x_scale, topk_idx, topk_w, w_gate_up, w_down, mx, bias
                 stream):
     return lib().moe_ffn_few(ctypes.byref(shape), x, x_scale, topk_idx, topk_w, w_gate_up, w_down,
                              _byref(mx), _byref(bias), y, ws, ws_bytes, stream)
+
+
+def moe_join_norm_fwd(T, H, dtype, y, residual, post_norm, post_weight, gate, residual_scale,
+                      weight, eps, total, n, n_scale, rstd_post, rstd, stream):
+    return lib().moe_join_norm_fwd(T, H, dtype, y, residual, post_norm, post_weight, gate,
+                                   residual_scale, weight, eps, total, n, n_scale, rstd_post, rstd,
+                                   stream)
+
+
+def moe_join_norm_workspace_size(T, H):
+    return lib().moe_join_norm_workspace_size(T, H)
+
+
+def moe_join_norm_bwd(T, H, dtype, dn, d_total, total, rstd, weight, y, rstd_post, post_weight, gate,
+                      residual_scale, dy, d_residual, d_gate, d_post_weight, d_weight, ws, ws_bytes,
+                      stream):
+    return lib().moe_join_norm_bwd(T, H, dtype, dn, d_total, total, rstd, weight, y, rstd_post,
+                                   post_weight, gate, residual_scale, dy, d_residual, d_gate,
+                                   d_post_weight, d_weight, ws, ws_bytes, stream)
+
+
+def moe_route_bwd_workspace_size(shape):
+    return lib().moe_route_bwd_workspace_size(ctypes.byref(shape))
+
+
+def moe_route_bwd(shape, logits, topk_idx, topk_w, counts, d_topk_w, balance, z, d_logits, losses,
+                  ws, ws_bytes, stream):
+    return lib().moe_route_bwd(ctypes.byref(shape), logits, topk_idx, topk_w, counts, d_topk_w,
+                               balance, z, d_logits, losses, ws, ws_bytes, stream)
+
+
+def moe_orthogonalize_workspace_size(E, M, N):
+    return lib().moe_orthogonalize_workspace_size(E, M, N)
+
+
+def moe_orthogonalize(E, M, N, dtype, g, g_ld, g_stride, steps, coefs, eps, scale, out, out_ld,
+                      out_stride, ws, ws_bytes, stream):
+    """coefs: None, or a ctypes array of 3 * steps floats."""
+    return lib().moe_orthogonalize(E, M, N, dtype, g, g_ld, g_stride, steps, coefs, eps, scale, out,
+                                   out_ld, out_stride, ws, ws_bytes, stream)
 
 
 # ---------------------------------------------------------------- torch helpers
@@ -592,6 +651,141 @@ def ffn_few(shape, x, topk_idx, topk_w, w_gate_up, w_down, y, ws, stream=None, b
         _dense(f, "w_down", w_down, (E, I, H), dt), _byref(mx), _byref(bias),
         _dense(f, "y", y, (T, H), torch.float32 if shape.out_fp32 else dt), *_ws(f, ws),
         _stream(stream)), "moe_ffn_few")
+
+
+def join_norm_workspace(T, H, device="cuda"):
+    """Zero-filled workspace of join_norm_bwd for at most T rows of H columns."""
+    import torch
+    n = moe_join_norm_workspace_size(T, H)
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_join_norm_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def join_norm_fwd(y, residual, total, post_norm=True, post_weight=None, gate=None, residual_scale=1.0,
+                  weight=None, n=None, n_scale=None, eps=1e-6, rstd_post=None, rstd=None, stream=None):
+    """A block's output y [T,H] joins the residual stream:
+        total = residual_scale * residual + gate * (rms_norm(y) * post_weight)
+    (post_norm=False: y * post_weight without the norm; gate [T] fp32, one factor per
+    token; either may be None), and the norm before the next block:
+        n = rms_norm(total) * weight
+    (both None where none follows), in y's dtype, or with n_scale [T,H/32] (uint8) as
+    e4m3 codes (uint8 or float8_e4m3fn).  rstd_post and rstd [T] (fp32) receive both
+    norms' 1 / rms for the backward."""
+    import torch
+    T, H = y.shape
+    f, dt, shape = "join_norm_fwd", y.dtype, y.shape
+    code = _storage_dtype(f, y)
+    ndt = dt
+    if n_scale is not None and n is not None:
+        ndt = torch.float8_e4m3fn if n.dtype is torch.float8_e4m3fn else torch.uint8
+    _check(lib().moe_join_norm_fwd(
+        T, H, code, _dense(f, "y", y, shape, dt), _dense(f, "residual", residual, shape, dt),
+        1 if post_norm else 0, _dense(f, "post_weight", post_weight, (H,), dt),
+        _dense(f, "gate", gate, (T,), torch.float32), residual_scale,
+        _dense(f, "weight", weight, (H,), dt), eps, _dense(f, "total", total, shape, dt),
+        _dense(f, "n", n, shape, ndt), _dense(f, "n_scale", n_scale, (T, H // 32), torch.uint8),
+        _dense(f, "rstd_post", rstd_post, (T,), torch.float32),
+        _dense(f, "rstd", rstd, (T,), torch.float32), _stream(stream)), "moe_join_norm_fwd")
+
+
+def join_norm_bwd(y, dy, d_residual, d_total=None, dn=None, total=None, weight=None, rstd=None,
+                  post_norm=True, post_weight=None, rstd_post=None, gate=None, residual_scale=1.0,
+                  d_gate=None, d_post_weight=None, d_weight=None, ws=None, stream=None):
+    """Gradient of join_norm_fwd: dy and d_residual [T,H] from dn (the gradient of n;
+    None where no norm followed) and d_total (the gradient that reaches total from
+    elsewhere, or None), with what the forward had and gave.  d_gate [T],
+    d_post_weight [H] and d_weight [H] (fp32) are optional; ws: join_norm_workspace(T, H),
+    needed with either weight's gradient."""
+    import torch
+    T, H = y.shape
+    f, dt, shape = "join_norm_bwd", y.dtype, y.shape
+    code = _storage_dtype(f, y)
+    if bool(post_norm) != (rstd_post is not None):
+        raise ValueError("join_norm_bwd: rstd_post is given with a post norm, and only then")
+    _check(lib().moe_join_norm_bwd(
+        T, H, code, _dense(f, "dn", dn, shape, dt), _dense(f, "d_total", d_total, shape, dt),
+        _dense(f, "total", total, shape, dt), _dense(f, "rstd", rstd, (T,), torch.float32),
+        _dense(f, "weight", weight, (H,), dt), _dense(f, "y", y, shape, dt),
+        _dense(f, "rstd_post", rstd_post, (T,), torch.float32),
+        _dense(f, "post_weight", post_weight, (H,), dt), _dense(f, "gate", gate, (T,), torch.float32),
+        residual_scale, _dense(f, "dy", dy, shape, dt),
+        _dense(f, "d_residual", d_residual, shape, dt),
+        _dense(f, "d_gate", d_gate, (T,), torch.float32),
+        _dense(f, "d_post_weight", d_post_weight, (H,), torch.float32),
+        _dense(f, "d_weight", d_weight, (H,), torch.float32), *_ws(f, ws), _stream(stream)),
+        "moe_join_norm_bwd")
+
+
+def route_bwd_workspace(shape, device="cuda"):
+    """Zero-filled workspace of route_bwd for this shape (T, E and k count)."""
+    import torch
+    n = moe_route_bwd_workspace_size(shape)
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_route_bwd_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def route_bwd(shape, logits, d_logits, ws, topk_idx=None, topk_w=None, d_topk_w=None, counts=None,
+              balance=0.0, z=0.0, losses=None, stream=None):
+    """d_logits [T,E] (fp32): the gradient of <d_topk_w, topk_w> with respect to the
+    logits that route() took, plus balance times that of the load-balancing loss and z
+    times that of the z-loss (include/moe.h); losses [2] (fp32) receives both.  counts:
+    the plan's."""
+    import torch
+    f, T, E, k, f32 = "route_bwd", shape.T, shape.E, shape.k, torch.float32
+    _check(lib().moe_route_bwd(
+        ctypes.byref(shape), _dense(f, "logits", logits, (T, E), f32),
+        _dense(f, "topk_idx", topk_idx, (T, k), torch.int32), _dense(f, "topk_w", topk_w, (T, k), f32),
+        _dense(f, "counts", counts, (E,), torch.int32), _dense(f, "d_topk_w", d_topk_w, (T, k), f32),
+        balance, z, _dense(f, "d_logits", d_logits, (T, E), f32), _dense(f, "losses", losses, (2,), f32),
+        *_ws(f, ws), _stream(stream)), "moe_route_bwd")
+
+
+def _matrices(where, name, t, dtype):
+    """(address, row stride, matrix stride) of [M,N] or [E,M,N], after a check that it
+    is of this dtype, on the GPU, with its rows' elements side by side."""
+    if t.dtype is not dtype or not t.is_cuda or t.dim() not in (2, 3):
+        raise ValueError("%s: %s must be a %s tensor [M,N] or [E,M,N] on the GPU, got %s %s" % (
+            where, name, dtype, t.dtype, tuple(t.shape)))
+    M, N = t.shape[-2:]
+    ld = t.stride(-2) if M > 1 else N
+    if (N > 1 and t.stride(-1) != 1) or ld < N:
+        raise ValueError("%s: %s's rows must be contiguous and apart, got strides %s" % (
+            where, name, tuple(t.stride())))
+    return t.data_ptr(), ld, t.stride(0) if t.dim() == 3 and t.shape[0] > 1 else M * ld
+
+
+def orthogonalize_workspace(g, device=None):
+    """Zero-filled workspace of orthogonalize for g [M,N] or [E,M,N] (fewer matrices
+    of that size take no more)."""
+    import torch
+    E = g.shape[0] if g.dim() == 3 else 1
+    n = moe_orthogonalize_workspace_size(E, *g.shape[-2:])
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_orthogonalize_workspace_size")
+    return torch.zeros(n, dtype=torch.uint8, device=g.device if device is None else device)
+
+
+def orthogonalize(g, out, ws, steps=5, coefs=None, eps=1e-7, scale=1.0, stream=None):
+    """out = scale * (g made orthogonal by `steps` Newton-Schulz products), for each
+    matrix of g [M,N] or [E,M,N] (bf16 or fp32); out of the same shape, bf16.  Rows may
+    lie apart: the gate half of dw_gate_up is dw_gate_up[:, :, :I].  coefs: (c0, c1, c2)
+    for every step, or a list of `steps` of them; ws: orthogonalize_workspace(g)."""
+    import torch
+    f = "orthogonalize"
+    code = _storage_dtype(f, g)
+    if out.shape != g.shape:
+        raise ValueError("orthogonalize: out has shape %s for %s" % (tuple(out.shape), tuple(g.shape)))
+    if coefs is not None:
+        rows = [tuple(c) for c in coefs] if hasattr(coefs[0], "__len__") else [tuple(coefs)] * steps
+        if len(rows) != steps or any(len(c) != 3 for c in rows):
+            raise ValueError("orthogonalize: three coefficients, or %d times three" % steps)
+        coefs = (ctypes.c_float * (3 * steps))(*[v for c in rows for v in c])
+    _check(lib().moe_orthogonalize(
+        g.shape[0] if g.dim() == 3 else 1, g.shape[-2], g.shape[-1], code,
+        *_matrices(f, "g", g, g.dtype), steps, coefs, eps, scale,
+        *_matrices(f, "out", out, torch.bfloat16), *_ws(f, ws), _stream(stream)), "moe_orthogonalize")
 
 
 def check_device_error(ws, stream=None):

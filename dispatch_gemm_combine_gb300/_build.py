@@ -20,8 +20,8 @@ LIB = os.path.join(PKG, "libmoe_gb300.so")
 
 SOURCES = ["api.cu", "plan.cu", "permute.cu", "gemm_bf16_fwd.cu", "gemm_bf16_dgrad.cu",
            "gemm_bf16_wgrad.cu", "gemm_f32.cu", "plan_noalloc.cu", "route.cu", "norm.cu", "clip.cu",
-           "mx.cu", "few.cu"]
-HEADERS = ["common.cuh", "kernels.h", "gemm.cuh", "abi_internal.h", "vec.cuh", "mx.cuh"]
+           "mx.cu", "few.cu", "join.cu", "route_bwd.cu", "orth.cu"]
+HEADERS = ["common.cuh", "kernels.h", "gemm.cuh", "abi_internal.h", "vec.cuh", "mx.cuh", "rows.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

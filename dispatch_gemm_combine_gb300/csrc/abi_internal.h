@@ -27,6 +27,11 @@ uint64_t abi_wait_timeout_ns();
 bool abi_map_bytes(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2,
                    uint32_t b0, uint32_t b1, CUtensorMapSwizzle sw);
 
+// A tensor map over fp16 matrices [d2][d1][d0] with rows of ld elements (a multiple
+// of 8), matrices d1 * ld apart; boxes of [1, b1, b0].  False if it cannot be made.
+bool abi_map_half(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t ld,
+                  uint32_t b0, uint32_t b1, CUtensorMapSwizzle sw);
+
 // The plan kernels (launch_plan) and a memset, counted by
 // moe_kernel_launch_count() and bracketed by the event timer when it is on.
 cudaError_t abi_tracked_plan(const int* idx, int64_t Tk, int E, int* counts, int* offsets,
@@ -38,7 +43,8 @@ cudaError_t abi_tracked_memset(void* p, int value, size_t bytes, cudaStream_t st
 // event timer (their names: api.cu).
 enum AbiKind : int {
   kAbiNormFwd = 0, kAbiNormBwd, kAbiGradNorm, kAbiGradScale, kAbiMxQuantize, kAbiMxDequantize,
-  kAbiFewGateUp, kAbiFewDown, kAbiFewRows, kNumAbiKinds
+  kAbiFewGateUp, kAbiFewDown, kAbiFewRows, kAbiJoinFwd, kAbiJoinBwd, kAbiRouteBwd, kAbiOrthLoad,
+  kAbiOrthGram, kAbiOrthPoly, kAbiOrthUpdate, kNumAbiKinds
 };
 
 // Launch accounting around a launcher of `nkernels` kernels, as moe.h

@@ -95,7 +95,8 @@ const char* const kKindNames[kNumKinds] = {
     "gemm_wgrad_gate_up", "memset", "transpose_f32", "route", "bias_slot_dot", "bias_colsum",
     "split_select", "gather_index", "combine_dense", "norm_fwd", "norm_bwd",
     "grad_norm", "grad_scale", "mx_quantize", "mx_dequantize", "few_gate_up", "few_down",
-    "few_rows"};
+    "few_rows", "join_fwd", "join_bwd", "route_bwd", "orth_load", "orth_gram", "orth_poly",
+    "orth_update"};
 
 std::atomic<uint64_t> g_launches{0};
 std::atomic<int> g_profile{0};
@@ -482,6 +483,19 @@ bool abi_map_bytes(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, u
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool abi_map_half(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t ld,
+                  uint32_t b0, uint32_t b1, CUtensorMapSwizzle sw) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {d0, d1, d2};
+  cuuint64_t strides[2] = {2 * ld, 2 * ld * d1};
+  cuuint32_t box[3] = {b0, b1, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -27,81 +27,11 @@
 
 #include "abi_internal.h"
 #include "common.cuh"
+#include "rows.cuh"
 #include "vec.cuh"
 
 namespace moe {
 namespace {
-
-constexpr int kMaxVec = 4;                       // 8-column vectors per thread
-constexpr int kMaxH = 1024 * 8 * kMaxVec;
-
-// Eight elements as they lie in memory.
-template <typename E>
-struct Raw8 {
-  static constexpr int W = sizeof(E) / 2;   // 16-byte pieces
-  uint4 u[W];
-  __device__ __forceinline__ void load(const E* p) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
-  }
-  __device__ __forceinline__ float get(int j) const {
-    const uint32_t* w = &u[0].x;
-    if (sizeof(E) == 4) return __uint_as_float(w[j]);
-    return j & 1 ? bf16_hi(w[j >> 1]) : bf16_lo(w[j >> 1]);
-  }
-  __device__ __forceinline__ float2 pair(int j) const { return make_float2(get(2 * j), get(2 * j + 1)); }
-};
-
-// The rows that a block walks, N arrays of them, D - 1 rows ahead of their use: each
-// warp copies its own columns asynchronously into its own part of shared memory and
-// reads them back itself, so no barrier of the block is needed.  A copy instruction
-// covers 512 contiguous bytes (in fp32 a lane copies other pieces than it reads: with
-// its own, 32 bytes apart, the backward at 8192 x 2880 takes 100 us instead of 74).
-// D = 0: loads at their use.
-template <typename E, int N, int V, int D>
-struct RowRing {
-  static constexpr int W = Raw8<E>::W;
-  static constexpr int bytes(int threads) { return D * N * V * W * 16 * threads; }
-  uint4* ring;
-  const E* src[N];   // null: absent
-  int H;
-  // Piece p of the warp's 32 W in vector i of array n.
-  __device__ __forceinline__ uint4* slot(int stage, int n, int i, int p) const {
-    if (W == 1) return ring + ((stage * N + n) * V + i) * blockDim.x + threadIdx.x;
-    return ring + ((stage * N + n) * V + i) * W * blockDim.x + (threadIdx.x & ~31u) * W + p;
-  }
-  __device__ __forceinline__ void issue(int stage, int64_t row, int64_t T) {
-    if (D == 0) return;
-    if (row < T) {
-      const int lane = threadIdx.x & 31;
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int c0 = ((threadIdx.x & ~31u) + i * blockDim.x) * 8;   // the warp's first column
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            const int p = w * 32 + lane, c = W == 1 ? (threadIdx.x + i * blockDim.x) * 8 : c0 + p * (8 / W);
-            if (src[n] && c < H) cp_async16(smem_u32(slot(stage, n, i, p)), src[n] + row * H + c, 16);
-          }
-        }
-    }
-    cp_async_commit();
-  }
-  // The oldest row's copies are there, and may be read.
-  __device__ __forceinline__ void wait() const {
-    cp_async_wait<D >= 2 ? D - 2 : 0>();
-    if (W > 1) __syncwarp();
-  }
-  __device__ __forceinline__ void take(int stage, int n, int i, int64_t row, int c, Raw8<E>& r) const {
-    if (D == 0) {
-      r.load(src[n] + row * H + c);
-      return;
-    }
-#pragma unroll
-    for (int w = 0; w < W; ++w) r.u[w] = *slot(stage, n, i, (threadIdx.x & 31) * W + w);
-  }
-};
 
 template <typename E, bool OUT8, int V, int D>
 __global__ void __launch_bounds__(1024) norm_fwd_kernel(
@@ -164,31 +94,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(
       if (!OUT8) {
         store8(static_cast<E*>(y) + base + c, o);
       } else {
-        // the four threads of a block of 32 columns are inside or outside the row
-        // together (H is a multiple of 32); all lanes take part in the shuffles
-        uint32_t amax = 0;
-        if (c < H) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(o[j]) & 0x7fffffffu);
-        }
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        if (c < H) {
-          const uint32_t sb = mx_scale_byte(amax, 0x600000u, 8);
-          const float inv = mx_inv_scale(sb);
-          uint2 code;
-          uint32_t h[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float2 p = make_float2(o[2 * j] * inv, o[2 * j + 1] * inv);
-            if (sb == 255u) p = make_float2(0.f, 0.f);
-            h[j] = __nv_cvt_float2_to_fp8x2(p, __NV_SATFINITE, __NV_E4M3);
-          }
-          code.x = h[0] | (h[1] << 16);
-          code.y = h[2] | (h[3] << 16);
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(y) + base + c) = code;
-          if ((threadIdx.x & 3) == 0) y_scale[row * (H / 32) + c / 32] = static_cast<uint8_t>(sb);
-        }
+        store_e4m3(o, c < H, static_cast<uint8_t*>(y) + base + c, y_scale + row * (H / 32) + c / 32);
       }
     }
   }
@@ -306,58 +212,6 @@ __global__ void __launch_bounds__(1024) norm_dweight_kernel(const float* __restr
   if (lane == 0 && blockIdx.x * 32 + grp < H) dweight[blockIdx.x * 32 + grp] = v;
 }
 
-// Threads and vectors per thread for a row of H columns: one vector per thread
-// up to 1024 threads.  (Two vectors share a row's sum, but the backward at
-// 8192 x 2880 then takes 66 us instead of 41.)
-struct RowShape {
-  int threads, vecs;
-};
-RowShape row_shape(int H) {
-  const int n = (H + 7) / 8;
-  int v = 1;
-  while (n > 1024 * v) v *= 2;
-  return {((n + v - 1) / v + 31) / 32 * 32, v};
-}
-
-// Resident blocks per SM of the kernels that walk rows: as many as hold
-// kThreadsPerSm threads of up to 64 registers and kRingPerSm of shared memory.
-// (1536 threads of 40 registers: 88 us instead of 80 for the forward at 16384 x
-// 4096, 61 instead of 41 for the backward at 8192 x 2880.)
-constexpr int kThreadsPerSm = 1024;
-constexpr int kRingPerSm = 210 * 1024;
-constexpr int kAhead = 3;   // the ring's rows
-
-// A launch of K<..., D> with the ring where it fits, or without.  The ring needs a
-// few rows per block to pay: with no more rows than blocks, loads go at their use.
-struct NormLaunch {
-  int blocks, threads, smem;
-  bool ring;
-};
-NormLaunch norm_launch(int64_t T, int threads, int ring_bytes, int threads_per_sm, int sms) {
-  const int fit = ring_bytes <= kRingPerSm ? kRingPerSm / ring_bytes : 0;
-  const int by_threads = std::max(1, std::min(8, threads_per_sm / threads));
-  const int64_t most = static_cast<int64_t>(sms) * (fit ? std::min(fit, by_threads) : by_threads);
-  NormLaunch l;
-  l.ring = fit > 0 && T > most;
-  l.blocks = static_cast<int>(std::min<int64_t>(T, most));
-  l.threads = threads;
-  l.smem = l.ring ? ring_bytes : 0;
-  return l;
-}
-
-// More than 48 KB of dynamic shared memory has to be asked for, once per device.
-template <typename K>
-cudaError_t allow_smem(K kernel, std::atomic<uint64_t>& ready) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingPerSm);
-  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
-
 template <typename E, bool OUT8, int V>
 cudaError_t launch_fwd_v(const E* x, const E* residual, const E* weight, int64_t T, int H, float eps,
                          void* y, uint8_t* y_scale, E* total, float* rstd, int threads, int sms,
@@ -419,10 +273,6 @@ cudaError_t launch_bwd(const E* dy, const E* d_total, const E* total, const floa
   if (s.vecs == 2) return launch_bwd_v<E, 2>(dy, d_total, total, rstd, weight, T, H, dx, part, s.threads, sms, blocks, st);
   return launch_bwd_v<E, 4>(dy, d_total, total, rstd, weight, T, H, dx, part, s.threads, sms, blocks, st);
 }
-
-// An upper bound on the backward's blocks that needs no device.
-constexpr int kMaxSms = 256;
-constexpr int kMaxBwdBlocks = 8 * kMaxSms;
 
 bool norm_dims_ok(int64_t T, int32_t H, int32_t dtype) {
   return T >= 0 && T < (1ll << 31) && H >= 8 && H % 8 == 0 && H <= kMaxH &&

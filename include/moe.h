@@ -427,6 +427,116 @@ moe_status moe_ffn_few(const moe_shape* shape, const void* x, const uint8_t* x_s
                        const void* w_down, const moe_mx_weights_t* mx, const moe_bias_t* bias,
                        void* y, void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/* ---- a training step around the layer: the block's output joins the residual
+ * stream, the router's gradient, and orthogonal updates ---- */
+
+/* A block's output y joins the residual stream, with the norms on either side:
+ *   p = y * rs_y * post_weight  (post_norm = 1)  or  y * post_weight  (0),
+ *   total = residual_scale * residual + gate * p,
+ *   n = total * rs * weight,
+ *   rs = 1 / sqrt(mean over the row of total^2 + eps), rs_y likewise of y.
+ *   y, residual [T,H], post_weight [H] (NULL: ones) and weight [H] in `dtype`
+ *     (moe_dtype); gate [T] fp32, one factor per token (NULL: ones).
+ *   total [T,H] in `dtype`, rounded once; n is of the sum before that rounding:
+ *     [T,H] in `dtype`, or with n_scale != NULL e4m3 codes [T,H] with their scale
+ *     bytes n_scale [T,H/32].  weight and n both NULL: no norm follows.
+ *   rstd_post [T] (with post_norm) and rstd [T] (with n), fp32: rs_y and rs, which
+ *     the backward wants; each may be NULL.
+ * Requirements: as moe_rms_norm_fwd (H a multiple of 32 with n_scale);
+ * residual_scale finite.  total and n may each be y or residual where the types
+ * agree, not one another; no other overlap.  T = 0 is a no-op. */
+moe_status moe_join_norm_fwd(int64_t T, int32_t H, int32_t dtype, const void* y,
+                             const void* residual, int32_t post_norm, const void* post_weight,
+                             const float* gate, float residual_scale, const void* weight,
+                             float eps, void* total, void* n, uint8_t* n_scale,
+                             float* rstd_post, float* rstd, moe_stream_t stream);
+
+/* Bytes of workspace for the weights' gradients (0 for bad dimensions). */
+size_t moe_join_norm_workspace_size(int64_t T, int32_t H);
+
+/* Gradient of moe_join_norm_fwd.  With rhat = total * rstd, v = dn * weight,
+ * yhat = y * rstd_post (y itself without a post norm):
+ *   dr = d_total + rstd * (v - rhat * mean over the row of (v * rhat)),
+ *   d_residual = residual_scale * dr,
+ *   d_gate = sum over the row of dr * yhat * post_weight,
+ *   dy = rstd_post * (gate * dr * post_weight - yhat * gate * d_gate / H)
+ *        (gate * dr * post_weight without a post norm),
+ *   d_post_weight[h] = sum over the rows of gate * dr * yhat,
+ *   d_weight[h] = sum over the rows of dn * rhat.
+ *   dn (the gradient of n) NULL: no norm followed; total, rstd and weight are then
+ *     not read.  d_total (the gradient that reaches total from elsewhere) may be
+ *     NULL where dn is given.  rstd_post NULL: no post norm.  post_weight, gate and
+ *     residual_scale as the forward had them; total, rstd, rstd_post as it gave them.
+ *   dy, d_residual [T,H] in `dtype`: each may be any of the [T,H] inputs, not one
+ *     another.  d_gate [T], d_post_weight [H], d_weight [H]: fp32, each may be NULL.
+ *   ws: moe_join_norm_workspace_size(T, H) bytes where a weight's gradient is wanted.
+ * The sums over the rows run in a fixed order that depends on T, H and the device
+ * only.  T = 0 zero-fills the weights' gradients. */
+moe_status moe_join_norm_bwd(int64_t T, int32_t H, int32_t dtype, const void* dn,
+                             const void* d_total, const void* total, const float* rstd,
+                             const void* weight, const void* y, const float* rstd_post,
+                             const void* post_weight, const float* gate, float residual_scale,
+                             void* dy, void* d_residual, float* d_gate, float* d_post_weight,
+                             float* d_weight, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Bytes of workspace of moe_route_bwd (0 for an invalid shape). */
+size_t moe_route_bwd_workspace_size(const moe_shape* shape);
+
+/* Gradient of the router's logits: of <d_topk_w, topk_w> through the softmax over
+ * the chosen logits (moe_route), and of two losses that keep a router in balance,
+ *   f_e = counts[e] * E / (T * k)   (taken as a constant),
+ *   L_balance = sum_e f_e * mean over t of softmax(logits[t])_e   (1 when uniform),
+ *   L_z = mean over t of (log sum_e exp logits[t,e])^2:
+ *   d_logits = that of the weights + balance * dL_balance + z * dL_z.
+ *   logits [T,E] fp32 as given to moe_route; -inf is an expert that the row cannot
+ *     choose (a row of them alone adds nothing).
+ *   topk_idx, topk_w [T,k] as moe_route gave them; d_topk_w [T,k] fp32 as
+ *     moe_ffn_bwd gives it, or NULL (topk_idx and topk_w are then not read).  An id
+ *     outside [0,E) records MOE_ERR_BAD_INDEX in the workspace and adds nothing; an
+ *     id that a row names twice adds both terms.
+ *   counts [E] int32: the plan's.  logits and counts may be NULL where losses is
+ *     NULL and balance and z are 0.
+ *   losses [2] fp32: L_balance, L_z; or NULL.
+ *   d_logits [T,E] fp32; it may not overlap logits.
+ * E <= 1024, k <= 32; 16-byte aligned logits and d_logits.  The sums over the rows
+ * run in a fixed order.  T = 0 zero-fills losses. */
+moe_status moe_route_bwd(const moe_shape* shape, const float* logits, const int32_t* topk_idx,
+                         const float* topk_w, const int32_t* counts, const float* d_topk_w,
+                         float balance, float z, float* d_logits, float* losses, void* ws,
+                         size_t ws_bytes, moe_stream_t stream);
+
+/* Bytes of workspace of moe_orthogonalize (0 for bad dimensions).  It does not grow
+ * with E beyond a few hundred MB or one matrix's need (8 bytes an element). */
+size_t moe_orthogonalize_workspace_size(int64_t E, int64_t M, int64_t N);
+
+/* Orthogonal updates by Newton-Schulz products, for each matrix g [M,N] of a batch
+ * (gradients or momenta of expert weights):
+ *   x_0 = g / (|g|_F + eps);   `steps` times:  a = x x^T,
+ *   x <- (c0 + c1 a + c2 a a) x;   out = scale * x.
+ * With the default coefficients (3.4445, -4.7750, 2.0315) and five steps the
+ * singular values of x end up near 1 and its singular vectors are g's.
+ *   g: E matrices of `dtype` (moe_dtype), element (e,r,c) at e*g_stride + r*g_ld + c
+ *     elements: columns of a wider tensor (the gate half of dw_gate_up, say) are
+ *     taken as they lie.  Read once for the norm and once more.
+ *   coefs: NULL for the default ones, or host memory [steps][3].  Coefficients that
+ *     lead beyond fp16's range (from singular values in [0,1]) are refused.
+ *   out: bf16, laid out by out_stride and out_ld; it may be g itself (bf16, the same
+ *     strides), otherwise no overlap.
+ * The norm is in range for every finite fp32 g.  A matrix of zeros gives zeros; one
+ * that holds an infinity or a NaN gives NaN.  The products run in fp16 (11 bits) with
+ * fp32 accumulation: against exact arithmetic the result is 1e-3 off where g's
+ * singular values are within a factor of about 500 of one another; what lies farther
+ * below the largest is amplified with the roundings in it.
+ * Requirements: 1 <= M, N <= 65536, 1 <= steps <= 32, g_ld and out_ld >= N,
+ * out_stride >= (M-1)*out_ld + N (E > 1), eps >= 0, scale finite; g and out aligned
+ * to their elements (rows on 16 bytes are faster).  E = 0 is a no-op.
+ * ws: moe_orthogonalize_workspace_size(E, M, N) bytes. */
+moe_status moe_orthogonalize(int64_t E, int64_t M, int64_t N, int32_t dtype, const void* g,
+                             int64_t g_ld, int64_t g_stride, int32_t steps, const float* coefs,
+                             float eps, float scale, void* out, int64_t out_ld,
+                             int64_t out_stride, void* ws, size_t ws_bytes,
+                             moe_stream_t stream);
+
 /* ---- measurement helpers (no counterpart in the pages; they serve the
  * roofline accounting of the benchmark) ---- */
 

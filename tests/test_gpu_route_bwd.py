@@ -1,0 +1,198 @@
+"""The router's gradient (chosen weights, load-balancing loss, z-loss) against the
+definitions in 64 bits.
+
+Tolerances: an exponential's argument v - max carries |v - max| u32, so a probability
+is off by that and a handful of roundings relative to itself; sums over a row below 48
+roundings.  The bound adds the terms' magnitudes with (64 + |v - max|) u32."""
+
+import pytest
+import torch
+
+import dispatch_gemm_combine_gb300 as moe
+
+pytestmark = pytest.mark.gpu
+
+U32 = torch.finfo(torch.float32).eps / 2
+
+
+class Case:
+    def __init__(self, T, E, k, balance=0.02, z=0.001, weights=True, seed=1, std=2.0):
+        g = torch.Generator().manual_seed(seed)
+        self.T, self.E, self.k, self.balance, self.z = T, E, k, balance, z
+        self.logits = torch.randn((T, E), generator=g) * std
+        top = torch.topk(self.logits, k, dim=-1)
+        self.idx, self.w = top.indices.to(torch.int32), torch.softmax(top.values, dim=-1)
+        self.counts = torch.bincount(self.idx.flatten().long(), minlength=E).to(torch.int32)
+        self.dw = torch.randn((T, k), generator=g) * 0.1 if weights else None
+
+    def exact(self):
+        v = self.logits.double()
+        top = v.amax(-1, keepdim=True)
+        alive = torch.isfinite(top)
+        p = torch.where(alive, torch.softmax(v, -1), torch.zeros_like(v))
+        lse = torch.where(alive, torch.logsumexp(v, -1, keepdim=True), torch.zeros_like(top))
+        f = self.counts.double() * self.E / (self.T * self.k)
+        F = (f * p).sum(-1, keepdim=True)
+        a, b = self.balance / self.T, 2 * self.z / self.T
+        d = a * p * (f - F) + b * lse * p
+        reach = torch.where(p > 0, (v - top).abs(), torch.zeros_like(v))
+        size = (a * p * (f + F) + b * (lse.abs() + top.nan_to_num(0, 0, 0).abs()) * p) * (64 + reach)
+        if self.dw is not None:
+            w, dw = self.w.double(), self.dw.double()
+            ok = (self.idx >= 0) & (self.idx < self.E)
+            c = w * (dw - (w * dw).sum(-1, keepdim=True))
+            at = self.idx.long().clamp(0, self.E - 1)
+            d.scatter_add_(1, at, c * ok)
+            size.scatter_add_(1, at, 64 * w * (dw.abs() + (w * dw).abs().sum(-1, keepdim=True)) * ok)
+        return d, U32 * size, torch.stack((F.mean(), lse.square().mean()))
+
+    def run(self, losses=True, stream=None, counts=True, logits=True):
+        shape = moe.Shape(self.T, 8, 8, self.E, self.k)
+        ws = moe.route_bwd_workspace(shape)
+        d = torch.full((self.T, self.E), 7.0, device="cuda")
+        out = torch.full((2,), 7.0, device="cuda") if losses else None
+        moe.route_bwd(shape, self.logits.cuda() if logits else None, d, ws, topk_idx=self.idx.cuda(), topk_w=self.w.cuda(),
+                      d_topk_w=None if self.dw is None else self.dw.cuda(), counts=self.counts.cuda() if counts else None,
+                      balance=self.balance, z=self.z, losses=out)
+        torch.cuda.synchronize()
+        return d.cpu(), None if out is None else out.cpu(), ws
+
+    def check(self, **kw):
+        d, losses, ws = self.run(**kw)
+        ref, bound, ref_losses = self.exact()
+        assert torch.all((d.double() - ref).abs() <= U32 * ref.abs() + bound + 1e-44)
+        if losses is not None:
+            # F and the square of log sum exp: below 64 + |v| roundings each, all of one
+            # sign; a loss beyond fp32's range (logits past 1e19) rounds to infinity
+            far = torch.isinf(ref_losses.float())
+            assert torch.all(torch.isposinf(losses[far]))
+            losses, ref_losses = losses[~far], ref_losses[~far]
+            assert torch.all((losses.double() - ref_losses).abs() <= (80 + 2 * float(self.logits.nan_to_num(0, 0, 0).abs().max())) * U32 * ref_losses + 1e-44)
+        return ws
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 4, 4), (3, 5, 2), (37, 61, 6), (8, 128, 4), (1000, 128, 4), (5, 129, 8), (64, 256, 8),
+                                   (33, 255, 3), (9, 512, 8), (6, 511, 32), (4, 1024, 32), (7, 1023, 8), (20000, 32, 2), (12000, 60, 5), (2, 40, 32)])
+def test_gradient(T, E, k):
+    Case(T, E, k).check()
+    Case(T, E, k, weights=False).check()
+    Case(T, E, k, balance=0.0, z=0.0).check()
+    Case(T, E, k, balance=0.0, z=0.0).check(losses=False, counts=False, logits=False)
+    Case(T, E, k, balance=0.5, z=0.0).check(losses=False)
+
+
+def test_against_differences():
+    """Of the losses and the weights that the framework's own forward gives."""
+    c = Case(6, 24, 3, std=1.0)
+    d, _, _ = c.run()
+    g = torch.Generator().manual_seed(9)
+    direction = torch.randn(c.logits.shape, generator=g, dtype=torch.float64)
+    direction /= direction.norm()
+
+    def loss(v):
+        chosen = torch.softmax(v.gather(1, c.idx.long()), -1)
+        f = c.counts.double() * c.E / (c.T * c.k)
+        return float((chosen * c.dw.double()).sum() + c.balance * (torch.softmax(v, -1).mean(0) * f).sum()
+                     + c.z * torch.logsumexp(v, -1).square().mean())
+
+    h = 2.0 ** -12
+    slope = (loss(c.logits.double() + h * direction) - loss(c.logits.double() - h * direction)) / (2 * h)
+    assert abs(slope - float((d.double() * direction).sum())) <= 64 * U32 * float(d.double().norm()) + h * h
+
+
+def test_masked_experts_and_rows():
+    c = Case(6, 40, 4)
+    c.logits[:, 7] = float("-inf")
+    c.logits[2, 3:] = float("-inf")
+    c.logits[4] = float("-inf")
+    c.logits[5] = -3.0e38
+    c.idx[:, :] = torch.tensor([0, 1, 2, 3], dtype=torch.int32)
+    c.check()
+    c.dw = None
+    d, _, _ = c.run()
+    assert torch.isfinite(d).all() and not d[4].any() and not d[:5, 7].any()      # (row 5 masks none)
+
+
+def test_non_finite_rows_stay_apart():
+    c = Case(5, 40, 4)
+    c.logits[1, 5] = float("nan")
+    c.logits[3, 5] = float("inf")
+    d, losses, _ = c.run()
+    assert torch.isnan(d[1]).all() and torch.isnan(losses).all()
+    assert torch.isfinite(d[[0, 2, 4]]).all()
+
+
+def test_large_logits():
+    Case(9, 100, 4, std=1e4).check()
+    Case(9, 100, 4, std=1e-20).check()
+
+
+def test_the_same_expert_twice():
+    c = Case(5, 128, 6)
+    c.idx[1] = 3
+    c.idx[2, :2] = c.idx[2, 2]
+    c.check()
+    c = Case(5, 33, 32)
+    c.idx[0] = 32
+    c.check()
+
+
+def test_bad_ids_are_reported_and_add_nothing():
+    c = Case(5, 128, 4)
+    c.idx[1, 2], c.idx[3, 0] = 128, -1
+    ws = c.check()
+    with pytest.raises(moe.MoeError):
+        moe.check_device_error(ws)
+    moe.check_device_error(ws)        # read and cleared
+
+
+def test_no_rows():
+    shape = moe.Shape(0, 8, 8, 16, 2)
+    losses = torch.full((2,), 7.0, device="cuda")
+    moe.route_bwd(shape, torch.empty((0, 16), device="cuda"), torch.empty((0, 16), device="cuda"),
+                  moe.route_bwd_workspace(shape), balance=1.0, counts=torch.zeros(16, dtype=torch.int32, device="cuda"), losses=losses)
+    assert not losses.any()
+
+
+def test_repeats_bit_for_bit_and_in_a_graph():
+    c = Case(5000, 100, 4)
+    d0, l0, _ = c.run()
+    shape = moe.Shape(c.T, 8, 8, c.E, c.k)
+    t = [v.cuda() for v in (c.logits, c.idx, c.w, c.dw, c.counts)]
+    ws, d, losses = moe.route_bwd_workspace(shape), torch.zeros((c.T, c.E), device="cuda"), torch.zeros(2, device="cuda")
+
+    def go(stream=None):
+        moe.route_bwd(shape, t[0], d, ws, t[1], t[2], t[3], t[4], c.balance, c.z, losses, stream)
+
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    go(s)
+    torch.cuda.synchronize()
+    assert torch.equal(d.cpu(), d0) and torch.equal(losses.cpu(), l0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go()
+    d.zero_(), losses.zero_()
+    ws[256:].fill_(0xff)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(d.cpu(), d0) and torch.equal(losses.cpu(), l0)
+
+
+def test_refusals():
+    c = Case(4, 16, 2)
+    shape = moe.Shape(4, 8, 8, 16, 2)
+    ws, d = moe.route_bwd_workspace(shape), torch.empty((4, 16), device="cuda")
+    v, idx, w, dw, counts = [t.cuda() for t in (c.logits, c.idx, c.w, c.dw, c.counts)]
+    for bad in (dict(counts=None, balance=1.0), dict(topk_idx=None), dict(topk_w=None), dict(z=float("inf"))):
+        args = dict(topk_idx=idx, topk_w=w, d_topk_w=dw, counts=counts)
+        args.update(bad)
+        with pytest.raises(moe.MoeError):
+            moe.route_bwd(shape, v, d, ws, **args)
+    with pytest.raises(ValueError):
+        moe.route_bwd(shape, v[:, :8], d, ws, z=1.0, counts=counts)
+    with pytest.raises(ValueError):
+        moe.route_bwd(shape, v, d, ws, topk_idx=idx.long(), topk_w=w, d_topk_w=dw)
+    with pytest.raises(moe.MoeError):
+        moe.route_bwd(shape, v, d, ws[:256], z=1.0, counts=counts)
