@@ -44,7 +44,7 @@ cudaError_t abi_tracked_memset(void* p, int value, size_t bytes, cudaStream_t st
 enum AbiKind : int {
   kAbiNormFwd = 0, kAbiNormBwd, kAbiGradNorm, kAbiGradScale, kAbiMxQuantize, kAbiMxDequantize,
   kAbiFewGateUp, kAbiFewDown, kAbiFewRows, kAbiJoinFwd, kAbiJoinBwd, kAbiRouteBwd, kAbiOrthLoad,
-  kAbiOrthGram, kAbiOrthPoly, kAbiOrthUpdate, kNumAbiKinds
+  kAbiOrthSteps, kAbiOrthSmall, kNumAbiKinds
 };
 
 // Launch accounting around a launcher of `nkernels` kernels, as moe.h

@@ -95,8 +95,7 @@ const char* const kKindNames[kNumKinds] = {
     "gemm_wgrad_gate_up", "memset", "transpose_f32", "route", "bias_slot_dot", "bias_colsum",
     "split_select", "gather_index", "combine_dense", "norm_fwd", "norm_bwd",
     "grad_norm", "grad_scale", "mx_quantize", "mx_dequantize", "few_gate_up", "few_down",
-    "few_rows", "join_fwd", "join_bwd", "route_bwd", "orth_load", "orth_gram", "orth_poly",
-    "orth_update"};
+    "few_rows", "join_fwd", "join_bwd", "route_bwd", "orth_load", "orth_steps", "orth_small"};
 
 std::atomic<uint64_t> g_launches{0};
 std::atomic<int> g_profile{0};

@@ -35,8 +35,9 @@ namespace {
 
 // ------------------------------------------------------------ norm and load
 constexpr int kNormThreads = 256;
-constexpr int kNormElems = 32768;      // of a matrix per block of the norm
-constexpr int kMaxParts = 1024;         // blocks per matrix
+constexpr int kNormElems = 8192;       // of a matrix per block of the norm, at least
+constexpr int kNormBlocks = 1216;      // about, of a launch
+constexpr int kMaxParts = 1024;        // blocks per matrix
 
 // Squares of fp32 values leave fp32's range beyond 2^64 and below 2^-63: sums of
 // g^2, (2^-80 g)^2 and (2^80 g)^2 side by side, of which the one in range is taken.
@@ -54,72 +55,58 @@ struct OrthIn {
   const void* g;
   int64_t ld, stride;   // of rows and matrices
   int M, N;
-  int bf16;
   int vec;              // rows start on 16 bytes
 };
 
+// Elements [c, c + 8) of a row, 0 past its end.
 template <typename E>
-__device__ __forceinline__ float elem(const void* g, int64_t i) {
-  return to_f32(static_cast<const E*>(g)[i]);
-}
-
-// Sums of squares of rows [r0, r1) of matrix blockIdx.y.
-template <typename E>
-__device__ __forceinline__ void add_rows(const OrthIn& in, int64_t base, int r0, int r1, Squares& s) {
-  constexpr int W = 16 / sizeof(E);
-  const int nv = in.vec ? in.N / W : 0;   // whole vectors of a row
-  const int tail = in.N - nv * W;
-  const E* g = static_cast<const E*>(in.g);
-  const int64_t vecs = static_cast<int64_t>(r1 - r0) * nv;
-  for (int64_t i = threadIdx.x; i < vecs; i += kNormThreads) {
-    const int r = static_cast<int>(i / nv), c = static_cast<int>(i - static_cast<int64_t>(r) * nv);
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(g + base + (r0 + r) * in.ld) + c);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void load_row8(const OrthIn& in, const E* row, int c, float (&v)[8]) {
+  if (in.vec && c + 8 <= in.N) {
+    load8(row + c, v);
+  } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (sizeof(E) == 4) {
-        s.add(__uint_as_float(w[k]));
-      } else {
-        s.add(bf16_lo(w[k]));
-        s.add(bf16_hi(w[k]));
-      }
-    }
-  }
-  const int64_t rest = static_cast<int64_t>(r1 - r0) * tail;
-  for (int64_t i = threadIdx.x; i < rest; i += kNormThreads) {
-    const int r = static_cast<int>(i / tail), c = nv * W + static_cast<int>(i - static_cast<int64_t>(r) * tail);
-    s.add(elem<E>(in.g, base + (r0 + r) * in.ld + c));
+    for (int k = 0; k < 8; ++k) v[k] = c + k < in.N ? to_f32(row[c + k]) : 0.f;
   }
 }
 
+// Sum of squares of rows [blockIdx.x * rows, ...) of matrix blockIdx.y: the block's
+// threads walk the rows' groups of eight columns, four at a time.
+template <typename E>
 __global__ void __launch_bounds__(kNormThreads) orth_norm_kernel(const OrthIn in, int rows, Squares* parts) {
   __shared__ float part[3][32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t base = static_cast<int64_t>(blockIdx.y) * in.stride;
-  const int r0 = blockIdx.x * rows, r1 = min(in.M, r0 + rows);
+  const int r1 = min(in.M, static_cast<int>(blockIdx.x + 1) * rows);
+  const E* g = static_cast<const E*>(in.g) + static_cast<int64_t>(blockIdx.y) * in.stride;
+  const int nv = (in.N + 7) / 8;
+  const int dr = kNormThreads / nv, dc = kNormThreads - dr * nv;   // a step of all threads
+  int r = blockIdx.x * rows + static_cast<int>(threadIdx.x) / nv, c = static_cast<int>(threadIdx.x) % nv;
   Squares s;
-  if (in.bf16)
-    add_rows<__nv_bfloat16>(in, base, r0, r1, s);
-  else
-    add_rows<float>(in, base, r0, r1, s);
+  while (r < r1) {
+    float v[4][8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (r < r1) {
+        load_row8(in, g + r * in.ld, 8 * c, v[u]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[u][k] = 0.f;
+      }
+      r += dr, c += dc;
+      if (c >= nv) c -= nv, ++r;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s.add(v[u][k]);
+  }
   s.mid = block_sum(s.mid, part[0]);
   s.big = block_sum(s.big, part[1]);
   s.small = block_sum(s.small, part[2]);
   if (threadIdx.x == 0) parts[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = s;
 }
 
-// The factors (pre, f) with x_0 S = (g pre) f, of the matrix's parts: the same in
-// every thread.
-__device__ __forceinline__ float2 orth_factor(const Squares* parts, int n, float eps, float S) {
-  __shared__ float part[3][32];
-  Squares v;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const float* p = &parts[i].mid;
-    v.mid += __ldcg(p), v.big += __ldcg(p + 1), v.small += __ldcg(p + 2);
-  }
-  v.mid = block_sum(v.mid, part[0]);
-  v.big = block_sum(v.big, part[1]);
-  v.small = block_sum(v.small, part[2]);
+// The factors (pre, f) with x_0 S = (g pre) f, of the matrix's sums of squares.
+__device__ __forceinline__ float2 orth_factor_of(const Squares& v, float eps, float S) {
   float pre = 1.f, ss = v.mid;
   if (!isfinite(v.mid))
     pre = 0x1p-80f, ss = v.big;
@@ -132,123 +119,275 @@ __device__ __forceinline__ float2 orth_factor(const Squares* parts, int n, float
   return make_float2(pre, f);
 }
 
-// X [m, ldx] fp16 from g: a block takes a tile of 64 x 64 (64 rows of the result).
+// The same of its blocks' sums, in every thread.
+__device__ __forceinline__ float2 orth_factor(const Squares* parts, int n, float eps, float S) {
+  __shared__ float part[3][32];
+  Squares v;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const float* p = &parts[i].mid;
+    v.mid += __ldcg(p), v.big += __ldcg(p + 1), v.small += __ldcg(p + 2);
+  }
+  v.mid = block_sum(v.mid, part[0]);
+  v.big = block_sum(v.big, part[1]);
+  v.small = block_sum(v.small, part[2]);
+  return orth_factor_of(v, eps, S);
+}
+
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// X [m, ldx] fp16 from g, tiles of 64 x 64 of matrix blockIdx.y in turn; the columns
+// from n to ldx hold 0.  Also clears the counters of the products.
 template <typename E, bool FLIP>
 __global__ void __launch_bounds__(256) orth_load_kernel(const OrthIn in, const Squares* parts, int nparts, float eps,
-                                                        float S, __half* X, int ldx, int64_t xstride) {
-  __shared__ float tile[64][65];
+                                                        float S, __half* X, int ldx, int64_t xstride, int* counters,
+                                                        int ncounters) {
+  __shared__ float tile[FLIP ? 64 : 1][FLIP ? 65 : 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the sums are there
-  const int e = blockIdx.z;
+  const int e = blockIdx.y;
+  if (blockIdx.x == 0 && e == 0)
+    for (int i = threadIdx.x; i < ncounters; i += 256) counters[i] = 0;
   const float2 f = orth_factor(parts + static_cast<int64_t>(e) * nparts, nparts, eps, S);
-  const int64_t base = static_cast<int64_t>(e) * in.stride;
-  const int c0 = blockIdx.x * 64, r0 = blockIdx.y * 64;   // of g
-  const int lc = threadIdx.x & 63, lr = threadIdx.x >> 6;
-  for (int i = lr; i < 64; i += 4) {
-    const int r = r0 + i, c = c0 + lc;
-    float v = 0.f;
-    if (r < in.M && c < in.N) v = elem<E>(in.g, base + r * in.ld + c) * f.x * f.y;
-    tile[i][lc] = v;
-  }
-  __syncthreads();
+  const E* g = static_cast<const E*>(in.g) + static_cast<int64_t>(e) * in.stride;
   __half* x = X + static_cast<int64_t>(e) * xstride;
-  const int rows = FLIP ? in.N : in.M;
-  const int xr0 = FLIP ? c0 : r0, xc0 = FLIP ? r0 : c0;
-  const int xc = (threadIdx.x & 31) * 2;
-  for (int i = threadIdx.x >> 5; i < 64; i += 8) {
-    const float a = FLIP ? tile[xc][i] : tile[i][xc];
-    const float b = FLIP ? tile[xc + 1][i] : tile[i][xc + 1];
-    // columns up to ldx (a multiple of 8) are in the buffer; those past the matrix hold 0
-    if (xr0 + i < rows && xc0 + xc < ldx)
-      *reinterpret_cast<__half2*>(x + static_cast<int64_t>(xr0 + i) * ldx + xc0 + xc) = __floats2half2_rn(a, b);
+  const int tc = (in.N + 63) / 64, tiles = tc * ((in.M + 63) / 64);
+  const int c8 = (threadIdx.x & 7) * 8, i0 = threadIdx.x >> 3;   // 32 rows of eight groups of eight
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int r0 = t / tc * 64, c0 = t % tc * 64;   // of g
+    float v[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = r0 + i0 + 32 * h;
+      if (r < in.M && c0 + c8 < in.N) {
+        load_row8(in, g + r * in.ld, c0 + c8, v[h]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[h][k] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = i0 + 32 * h;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[h][k] = v[h][k] * f.x * f.y;
+      if (FLIP) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) tile[c8 + k][i] = v[h][k];
+      }
+    }
+    if (FLIP) {
+      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[h][k] = tile[i0 + 32 * h][c8 + k];
+      __syncthreads();
+    }
+    const int rows = FLIP ? in.N : in.M, xr0 = FLIP ? c0 : r0, xc = (FLIP ? r0 : c0) + c8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (xr0 + i0 + 32 * h < rows && xc < ldx)
+        *reinterpret_cast<uint4*>(x + static_cast<int64_t>(xr0 + i0 + 32 * h) * ldx + xc) =
+            make_uint4(pack_half(v[h][0], v[h][1]), pack_half(v[h][2], v[h][3]), pack_half(v[h][4], v[h][5]),
+                       pack_half(v[h][6], v[h][7]));
   }
 }
 
 // ------------------------------------------------------------ products
-// A persistent batched product D = A B^T on CTA pairs (2-SM MMA, M = 256, N = 256):
-// each CTA loads 128 rows of A and 128 of B per 64 columns of K into a ring, one
-// thread of the even CTA issues the MMAs, the accumulators are double-buffered in
-// tensor memory and four warps per CTA store them.  Warp roles and unwinding as in
-// the expert layer's grouped products.
-enum OrthMode : int { kGram = 0, kPoly = 1, kUpdate = 2 };
+// All steps of a batch in one persistent kernel on CTA pairs (2-SM MMA, M = 256,
+// N <= 256): the phases gram, poly, update of every step, in each phase the tiles of
+// every matrix, make one list of units that the pairs take in turn.  A unit waits for
+// the phase before it of its own matrix only (a counter per matrix and phase), so
+// with a few matrices no pair waits for the end of a phase, and a step costs no
+// launches.  The launch is cooperative: pairs wait for one another, so all of them
+// have to be resident (one CTA per SM).
+//
+// Within a unit each CTA loads 128 rows of A and half of B's columns per 64 columns
+// of K into a ring, one thread of the even CTA issues the MMAs, the accumulators are
+// double-buffered in tensor memory and four warps per CTA store them.  Warp roles and
+// unwinding as in the expert layer's grouped products.
+enum OrthPhase : int { kGram = 0, kPoly = 1, kUpdate = 2 };
 
 constexpr int kOrthStages = 6;
 constexpr int kStageBytes = 2 * 128 * 128;
 constexpr int kEpiWarpBytes = 2 * 4096;
 constexpr int kOrthBars = (2 * kOrthStages + 5) * 8 + 16;
 constexpr int kOrthSmem = 1024 + kOrthStages * kStageBytes + 4 * kEpiWarpBytes + kOrthBars;
+constexpr int kMaxOrthSteps = 32;
+constexpr int kUnitArrivals = 8;         // epilogue warps of a pair
 static_assert(kOrthSmem <= 232448, "shared memory budget");
 
 struct OrthMaps {
-  CUtensorMap a, b;        // operands
-  CUtensorMap out, out_t;  // fp16 result: boxes {64 columns, 32 rows}, mirrored {32, 64}
+  CUtensorMap xk[2];   // X as a K-major operand, rows of A: box {64, 128}
+  CUtensorMap xs[2];   //   rows of B: box {64, bn_sym / 2}
+  CUtensorMap xn[2];   // X as the MN-major operand of the update: box {64, 64}
+  CUtensorMap xo[2];   // X as a result: box {64, 32}
+  CUtensorMap ak, as, ao, at;   // A likewise; at: mirrored, box {32, 64}
+  CUtensorMap bk, bo, bt;       // B
 };
 
 struct OrthArgs {
-  int m, n;              // of the result
-  int num_kb;            // blocks of 64 of the contraction
-  int batch;
-  int mt, nt;            // tiles of 256
-  float ds;              // factor on the accumulator
-  float cA, cI;          // poly: factor on A, addend on the diagonal
-  const __half* A;       // poly: A [batch][m][lda]
+  int m, n;              // of X
+  int batch, steps;
+  int mt;                // row tiles of 256
+  int bn_sym, nt_sym;    // column tiles of the symmetric products: width and number
+  int bn_upd, nt_upd;    // of the update
+  int units_sym, units_upd;   // per matrix
+  float S2;              // A and B hold S2 times theirs
+  float out_scale;       // scale / S
+  const __half* A;       // [batch][m][lda]
   int lda;
   int64_t astride;
-  // the last update: bf16 out[e][r][c], transposed when `flip`
-  __nv_bfloat16* out;
+  __nv_bfloat16* out;    // the last update: out[e][r][c], transposed when `flip`
   int64_t out_ld, out_stride;
   int flip, vec;         // vec: rows of out start on 16 bytes
+  int* counters;         // [3 steps][batch], cleared before the launch
   int* err;
   uint64_t timeout_ns;
+  float coefs[kMaxOrthSteps][3];
 };
 
-struct OrthTile {
-  int e, i, j;
+struct OrthUnit {
+  int phase;       // 3 * step + OrthPhase
+  int kind, step;
+  int e, i, c0;    // matrix, row tile, first column
+  int nn;          // columns: a multiple of 16
+  bool mirror;     // the tile lies above the diagonal
 };
 
-// Unit t: matrix, row tile, column tile; symmetric results have the column tiles
-// from the diagonal on only.
-template <int MODE>
-__device__ __forceinline__ OrthTile orth_tile(const OrthArgs& a, int t) {
-  OrthTile r;
-  if (MODE == kUpdate) {
-    const int per = a.mt * a.nt;
-    r.e = t / per;
-    const int u = t - r.e * per;
-    r.j = u / a.mt;
-    r.i = u - r.j * a.mt;
-  } else {
-    const int per = a.mt * (a.mt + 1) / 2;
-    r.e = t / per;
-    int u = t - r.e * per;
-    // row i has mt - i tiles
+// Unit t.  A symmetric result has the column tiles from the diagonal tile's first
+// column on: those inside the diagonal 256 x 256 block are stored as they are, those
+// beyond it mirrored too.
+__device__ __forceinline__ OrthUnit orth_unit(const OrthArgs& a, int t) {
+  OrthUnit u;
+  const int us = a.units_sym * a.batch, per_step = 2 * us + a.units_upd * a.batch;
+  u.step = t / per_step;
+  int r = t - u.step * per_step;
+  int cols, bn;
+  if (r < 2 * us) {
+    u.kind = r < us ? kGram : kPoly;
+    if (u.kind == kPoly) r -= us;
+    u.e = r / a.units_sym;
+    r -= u.e * a.units_sym;
+    const int f = 256 / a.bn_sym;   // column tiles in a diagonal block
     int i = 0;
-    while (u >= a.mt - i) {
-      u -= a.mt - i;
+    while (r >= a.nt_sym - i * f) {
+      r -= a.nt_sym - i * f;
       ++i;
     }
-    r.i = i;
-    r.j = i + u;
+    u.i = i;
+    bn = a.bn_sym, cols = a.m;
+    u.c0 = (i * f + r) * bn;
+    u.mirror = r >= f;
+  } else {
+    r -= 2 * us;
+    u.kind = kUpdate;
+    u.e = r / a.units_upd;
+    r -= u.e * a.units_upd;
+    const int j = r / a.mt;
+    u.i = r - j * a.mt;
+    bn = a.bn_upd, cols = a.n;
+    u.c0 = j * bn;
+    u.mirror = false;
   }
-  return r;
+  u.phase = 3 * u.step + u.kind;
+  u.nn = (min(bn, cols - u.c0) + 15) & ~15;
+  return u;
 }
 
-// Instruction descriptor: fp16 operands, fp32 accumulator, M = 256, N = 256.
-__host__ __device__ constexpr uint32_t orth_idesc(bool b_mn) {
-  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((256u >> 3) << 17) | ((256u >> 4) << 24);
+// Instruction descriptor: fp16 operands, fp32 accumulator, M = 256.
+__device__ __forceinline__ uint32_t orth_idesc(bool b_mn, int n) {
+  return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | ((256u >> 4) << 24);
 }
 
 __device__ __forceinline__ void st_shared_v4u(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-__device__ __forceinline__ uint32_t pack_half(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
+
+__device__ __forceinline__ int load_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
 }
 
-template <int MODE, bool LAST>
+__device__ __forceinline__ void add_release(int* p, int v) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// Wait until the unit's matrix has finished the phase before: false when that takes
+// longer than the limit.
+__device__ __forceinline__ bool orth_wait(const OrthArgs& a, const OrthUnit& u, uint64_t timeout_ns) {
+  if (u.phase == 0) return true;      // X is the load kernel's
+  const int* c = a.counters + (u.phase - 1) * a.batch + u.e;
+  const int target = kUnitArrivals * (u.kind == kGram ? a.units_upd : a.units_sym);
+  if (load_acquire(c) >= target) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (load_acquire(c) < target) {
+    if (global_timer_ns() - t0 > timeout_ns) return false;
+    __nanosleep(32);
+  }
+  return true;
+}
+
+// Sixteen-bit values of a 32 x 64 tile (lane: row) to out[r0 + row][col + ...] or, with
+// `flip`, to its transpose, through the warp's stage of 4 KB.
+__device__ __forceinline__ void store_out(const OrthArgs& a, __nv_bfloat16* out, int r0, int col, int rows, int cols,
+                                          const float (&v)[64], uint8_t* stage_g, uint32_t stage_s, int lane) {
+  __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(stage_g);
+  if (!a.flip) {
+    // 32 rows of 64, 16-byte pieces at piece ^ (row & 7)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      st_shared_v4u(stage_s + lane * 128 + ((j ^ (lane & 7)) << 4), pack_bf16(v[8 * j], v[8 * j + 1]),
+                    pack_bf16(v[8 * j + 2], v[8 * j + 3]), pack_bf16(v[8 * j + 4], v[8 * j + 5]),
+                    pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+    __syncwarp();
+    if (a.vec) {
+      for (int r = lane >> 3; r < rows; r += 4) {
+        const int p = lane & 7;
+        const uint4 u = *reinterpret_cast<const uint4*>(stage_g + r * 128 + ((p ^ (r & 7)) << 4));
+        __nv_bfloat16* d = out + static_cast<int64_t>(r0 + r) * a.out_ld + col + 8 * p;
+        if (8 * p + 8 <= cols) {
+          *reinterpret_cast<uint4*>(d) = u;
+        } else {
+          const __nv_bfloat16* s = reinterpret_cast<const __nv_bfloat16*>(&u);
+          for (int k = 0; 8 * p + k < cols; ++k) d[k] = s[k];
+        }
+      }
+    } else {
+      for (int r = 0; r < rows; ++r)
+        for (int k = lane; k < cols; k += 32)
+          out[static_cast<int64_t>(r0 + r) * a.out_ld + col + k] = h[r * 64 + (((k >> 3) ^ (r & 7)) << 3) + (k & 7)];
+    }
+  } else {
+    // the tile's columns are rows of out: 64 rows of 32
+#pragma unroll
+    for (int j = 0; j < 64; ++j) h[j * 32 + lane] = __float2bfloat16_rn(v[j]);
+    __syncwarp();
+    if (a.vec) {
+      for (int r = lane >> 2; r < cols; r += 8) {
+        const int p = lane & 3;
+        const uint4 u = *reinterpret_cast<const uint4*>(stage_g + r * 64 + p * 16);
+        __nv_bfloat16* d = out + static_cast<int64_t>(col + r) * a.out_ld + r0 + 8 * p;
+        if (8 * p + 8 <= rows) {
+          *reinterpret_cast<uint4*>(d) = u;
+        } else {
+          const __nv_bfloat16* s = reinterpret_cast<const __nv_bfloat16*>(&u);
+          for (int k = 0; 8 * p + k < rows; ++k) d[k] = s[k];
+        }
+      }
+    } else {
+      for (int r = 0; r < cols; ++r)
+        if (lane < rows) out[static_cast<int64_t>(col + r) * a.out_ld + r0 + lane] = h[r * 32 + lane];
+    }
+  }
+  __syncwarp();
+}
+
 __global__ void __launch_bounds__(192, 1)
-    orth_gemm_kernel(const __grid_constant__ OrthMaps maps, const __grid_constant__ OrthArgs args) {
-  constexpr bool B_MN = MODE == kUpdate;
+    orth_steps_kernel(const __grid_constant__ OrthMaps maps, const __grid_constant__ OrthArgs args) {
   constexpr int STAGES = kOrthStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -269,6 +408,7 @@ __global__ void __launch_bounds__(192, 1)
   const int crank = static_cast<int>(cluster_ctarank());
   const bool leader = crank == 0;
   constexpr uint16_t kPairMask = 0x3;
+  constexpr uint64_t kDrain = 1000000000ull;
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -281,8 +421,6 @@ __global__ void __launch_bounds__(192, 1)
     }
     mbar_init(drain_bar, 1);
     fence_barrier_init();
-    prefetch_tmap(&maps.a);
-    prefetch_tmap(&maps.b);
   }
   if (warp == 1) {
     tmem_alloc2(tmem_slot, 512);
@@ -293,8 +431,7 @@ __global__ void __launch_bounds__(192, 1)
   cluster_sync();   // both CTAs' barriers exist before any remote use
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot_g;
-  const int per = MODE == kUpdate ? args.mt * args.nt : args.mt * (args.mt + 1) / 2;
-  const int total = args.batch * per;
+  const int total = args.steps * args.batch * (2 * args.units_sym + args.units_upd);
   const int unit0 = blockIdx.x / 2, ustride = gridDim.x / 2;
   const uint64_t tmo = args.timeout_ns;
   auto ring_next = [](int& s, uint32_t& p) {
@@ -303,6 +440,7 @@ __global__ void __launch_bounds__(192, 1)
       p ^= 1u;
     }
   };
+  auto num_kb = [&](const OrthUnit& u) { return ((u.kind == kGram ? args.n : args.m) + 63) >> 6; };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -313,9 +451,20 @@ __global__ void __launch_bounds__(192, 1)
       int64_t issued = 0;
       bool ok = true;
       for (int t = unit0; t < total && ok; t += ustride) {
-        const OrthTile ti = orth_tile<MODE>(args, t);
-        const int ra = ti.i * 256 + crank * 128, rb = ti.j * 256 + crank * 128;
-        for (int kb = 0; kb < args.num_kb; ++kb) {
+        const OrthUnit u = orth_unit(args, t);
+        if (!orth_wait(args, u, tmo)) {
+          record_error(args.err, kErrTimeout);
+          break;
+        }
+        asm volatile("fence.proxy.async;" ::: "memory");   // the loads see what the wait saw
+        const int x = u.step & 1;
+        const CUtensorMap* am = u.kind == kGram ? &maps.xk[x] : (u.kind == kPoly ? &maps.ak : &maps.bk);
+        const CUtensorMap* bm = u.kind == kGram ? &maps.xs[x] : (u.kind == kPoly ? &maps.as : &maps.xn[x]);
+        const int chunks = args.bn_upd == 256 ? 2 : 1;
+        const uint32_t bytes = 128 * 128 + (u.kind == kUpdate ? chunks * 64 * 128 : args.bn_sym / 2 * 128);
+        const int ra = u.i * 256 + crank * 128, rb = u.c0 + crank * (u.nn >> 1);
+        const int nkb = num_kb(u);
+        for (int kb = 0; kb < nkb; ++kb) {
           if (!mbar_wait(empty_bar + 8 * stage, phase ^ 1u, tmo)) {
             record_error(args.err, kErrTimeout);
             ok = false;
@@ -323,13 +472,13 @@ __global__ void __launch_bounds__(192, 1)
           }
           const uint32_t sA = sbase + stage * kStageBytes, sB = sA + 128 * 128;
           const uint32_t fb = full_l + 8 * stage;
-          if (leader) mbar_arrive_expect_tx(full_bar + 8 * stage, 2 * kStageBytes);
-          tma_load_3d_g2(sA, &maps.a, fb, kb * 64, ra, ti.e);
-          if constexpr (B_MN) {
-            tma_load_3d_g2(sB, &maps.b, fb, rb, kb * 64, ti.e);
-            tma_load_3d_g2(sB + 64 * 128, &maps.b, fb, rb + 64, kb * 64, ti.e);
+          if (leader) mbar_arrive_expect_tx(full_bar + 8 * stage, 2 * bytes);
+          tma_load_3d_g2(sA, am, fb, kb * 64, ra, u.e);
+          if (u.kind == kUpdate) {
+            tma_load_3d_g2(sB, bm, fb, rb, kb * 64, u.e);
+            if (chunks == 2) tma_load_3d_g2(sB + 64 * 128, bm, fb, rb + 64, kb * 64, u.e);
           } else {
-            tma_load_3d_g2(sB, &maps.b, fb, kb * 64, rb, ti.e);
+            tma_load_3d_g2(sB, bm, fb, kb * 64, rb, u.e);
           }
           ++issued;
           ring_next(stage, phase);
@@ -340,7 +489,7 @@ __global__ void __launch_bounds__(192, 1)
       if (leader) {
         for (int s = 0; s < STAGES; ++s) {
           const int64_t n_s = issued > s ? (issued - 1 - s) / STAGES + 1 : 0;
-          if (n_s > 0 && !mbar_wait(full_bar + 8 * s, static_cast<uint32_t>((n_s - 1) & 1), 1000000000ull))
+          if (n_s > 0 && !mbar_wait(full_bar + 8 * s, static_cast<uint32_t>((n_s - 1) & 1), kDrain))
             record_error(args.err, kErrTimeout);
         }
       }
@@ -349,19 +498,24 @@ __global__ void __launch_bounds__(192, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (leader && lane == 0) {
-      constexpr uint32_t idesc = orth_idesc(B_MN);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int t = unit0; t < total && ok; t += ustride) {
+        const OrthUnit u = orth_unit(args, t);
+        const bool b_mn = u.kind == kUpdate;
+        const uint32_t idesc = orth_idesc(b_mn, u.nn);
+        const int nkb = num_kb(u);
+        // (the producer has waited for this unit's matrix before; its wait and the
+        // loads may take two limits)
         if (!mbar_wait(tempty_bar + 8 * acc, acc_phase ^ 1u, tmo)) {
           record_error(args.err, kErrTimeout);
           break;
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
-        for (int kb = 0; kb < args.num_kb; ++kb) {
-          if (!mbar_wait(full_bar + 8 * stage, phase, tmo)) {
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait(full_bar + 8 * stage, phase, kb == 0 ? 2 * tmo : tmo)) {
             record_error(args.err, kErrTimeout);
             ok = false;
             break;
@@ -371,7 +525,7 @@ __global__ void __launch_bounds__(192, 1)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const uint64_t ad = smem_desc_sw128(sA + kk * 32, 16, 1024);
-            const uint64_t bd = B_MN ? smem_desc_sw128(sB + kk * 16 * 128, 64 * 128, 1024)
+            const uint64_t bd = b_mn ? smem_desc_sw128(sB + kk * 16 * 128, 64 * 128, 1024)
                                      : smem_desc_sw128(sB + kk * 32, 16, 1024);
             tc_mma2(d_tmem, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
           }
@@ -399,135 +553,101 @@ __global__ void __launch_bounds__(192, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = unit0; t < total; t += ustride) {
-      const OrthTile ti = orth_tile<MODE>(args, t);
+      const OrthUnit u = orth_unit(args, t);
+      const int r0 = u.i * 256 + crank * 128 + q * 32;
       int good = 1;
-      if (lane == 0) good = mbar_wait(tfull_bar + 8 * acc, acc_phase, tmo);
+      uint4 ax[8];      // poly: A's values of the chunk, ahead of the products
+      auto fetch_a = [&](int col) {
+        const __half* p = args.A + u.e * args.astride + static_cast<int64_t>(r0 + lane) * args.lda + col;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)      // lda: a multiple of 8, as col is
+          ax[j] = r0 + lane < args.m && col + 8 * j < args.lda ? __ldcg(reinterpret_cast<const uint4*>(p) + j)
+                                                               : make_uint4(0u, 0u, 0u, 0u);
+      };
+      if (u.kind == kPoly) {
+        if (lane == 0) good = orth_wait(args, u, 2 * tmo);
+        good = __shfl_sync(0xffffffffu, good, 0);
+        if (good) fetch_a(u.c0);
+      }
+      if (lane == 0 && good) good = mbar_wait(tfull_bar + 8 * acc, acc_phase, 3 * tmo);
       good = __shfl_sync(0xffffffffu, good, 0);
       if (!good) {
         if (lane == 0) record_error(args.err, kErrTimeout);
         break;
       }
       tc_fence_after();
-      const int r0 = ti.i * 256 + crank * 128 + q * 32, c0 = ti.j * 256;
+      const bool last = u.kind == kUpdate && u.step + 1 == args.steps;
+      const int cols = u.kind == kUpdate ? args.n : args.m;
       const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
+      const float cI = args.coefs[u.step][0] * args.S2, cA = args.coefs[u.step][1];
+      const float ds = u.kind == kGram ? 1.f
+                       : u.kind == kPoly ? args.coefs[u.step][2] / args.S2
+                                         : (last ? args.out_scale : 1.f) / args.S2;
+      const CUtensorMap* om = u.kind == kGram ? &maps.ao : (u.kind == kPoly ? &maps.bo : &maps.xo[1 - (u.step & 1)]);
+      const CUtensorMap* tm = u.kind == kGram ? &maps.at : &maps.bt;
       if (r0 < args.m) {
-        const bool mirror = MODE != kUpdate && ti.i != ti.j;
 #pragma unroll 1
-        for (int c = 0; c < 256 && c0 + c < args.n; c += 64) {
+        for (int c = 0; c < u.nn; c += 64) {
           float v[64];
           tmem_ld64(tacc + c, v);
-          const int row = r0 + lane, col = c0 + c;
-          if constexpr (MODE == kPoly) {
+          const int row = r0 + lane, col = u.c0 + c;
+          if (u.kind == kPoly) {
 #pragma unroll
             for (int j = 0; j < 64; j += 8) {
-              float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-              if (row < args.m && col + j < args.lda) {   // lda: a multiple of 8, as col is
-                const uint4 u = __ldg(reinterpret_cast<const uint4*>(
-                    args.A + ti.e * args.astride + static_cast<int64_t>(row) * args.lda + col + j));
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+              float x[8];
+              const uint32_t w[4] = {ax[j / 8].x, ax[j / 8].y, ax[j / 8].z, ax[j / 8].w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-                  x[2 * k] = f.x, x[2 * k + 1] = f.y;
-                }
+              for (int k = 0; k < 4; ++k) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                x[2 * k] = f.x, x[2 * k + 1] = f.y;
               }
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
-                v[j + k] = fmaf(args.cA, x[k], args.ds * v[j + k]);
-                if (row == col + j + k) v[j + k] += args.cI;
+                v[j + k] = fmaf(cA, x[k], ds * v[j + k]);
+                if (row == col + j + k) v[j + k] += cI;
               }
             }
+            if (c + 64 < u.nn) fetch_a(col + 64);
           } else {
 #pragma unroll
-            for (int j = 0; j < 64; ++j) v[j] *= args.ds;
+            for (int j = 0; j < 64; ++j) v[j] *= ds;
           }
-          if constexpr (!LAST) {
-            // 32 rows of 64 values, in the 128-byte swizzle, stored by one lane
-            const uint32_t st = stage_s + buf * 4096;
+          if (last) {
+            store_out(args, args.out + u.e * args.out_stride, r0, col, min(32, args.m - r0), min(64, cols - col), v,
+                      stage_g, stage_s, lane);
+            continue;
+          }
+          // 32 rows of 64 values, in the 128-byte swizzle, stored by one lane
+          const uint32_t st = stage_s + buf * 4096;
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            st_shared_v4u(st + lane * 128 + ((j ^ (lane & 7)) << 4), pack_half(v[8 * j], v[8 * j + 1]),
+                          pack_half(v[8 * j + 2], v[8 * j + 3]), pack_half(v[8 * j + 4], v[8 * j + 5]),
+                          pack_half(v[8 * j + 6], v[8 * j + 7]));
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(om, st, col, r0, u.e);
+            bulk_commit();
+          }
+          buf ^= 1;
+          if (u.mirror) {
+            // 64 rows (the tile's columns) of 32 values
+            const uint32_t tt = stage_s + buf * 4096;
             if (lane == 0) bulk_wait_read<1>();
             __syncwarp();
+            __half* h = reinterpret_cast<__half*>(stage_g + buf * 4096);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              st_shared_v4u(st + lane * 128 + ((j ^ (lane & 7)) << 4), pack_half(v[8 * j], v[8 * j + 1]),
-                            pack_half(v[8 * j + 2], v[8 * j + 3]), pack_half(v[8 * j + 4], v[8 * j + 5]),
-                            pack_half(v[8 * j + 6], v[8 * j + 7]));
+            for (int j = 0; j < 64; ++j) h[j * 32 + lane] = __float2half_rn(v[j]);
             fence_async_shared();
             __syncwarp();
             if (lane == 0) {
-              tma_store_3d(&maps.out, st, col, r0, ti.e);
+              tma_store_3d(tm, tt, r0, col, u.e);
               bulk_commit();
             }
             buf ^= 1;
-            if (mirror) {
-              // 64 rows (the tile's columns) of 32 values
-              const uint32_t tt = stage_s + buf * 4096;
-              if (lane == 0) bulk_wait_read<1>();
-              __syncwarp();
-              __half* h = reinterpret_cast<__half*>(stage_g + buf * 4096);
-#pragma unroll
-              for (int j = 0; j < 64; ++j) h[j * 32 + lane] = __float2half_rn(v[j]);
-              fence_async_shared();
-              __syncwarp();
-              if (lane == 0) {
-                tma_store_3d(&maps.out_t, tt, r0, col, ti.e);
-                bulk_commit();
-              }
-              buf ^= 1;
-            }
-          } else {
-            // bf16, through the warp's stage, in rows of the result
-            __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(stage_g);
-            __nv_bfloat16* out = args.out + ti.e * args.out_stride;
-            const int rows = min(32, args.m - r0), cols = min(64, args.n - col);
-            if (!args.flip) {
-              // 32 rows of 64 (16-byte pieces at piece ^ (row & 7))
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                st_shared_v4u(stage_s + lane * 128 + ((j ^ (lane & 7)) << 4), pack_bf16(v[8 * j], v[8 * j + 1]),
-                              pack_bf16(v[8 * j + 2], v[8 * j + 3]), pack_bf16(v[8 * j + 4], v[8 * j + 5]),
-                              pack_bf16(v[8 * j + 6], v[8 * j + 7]));
-              __syncwarp();
-              if (args.vec) {
-                for (int r = lane >> 3; r < rows; r += 4) {
-                  const int p = lane & 7;
-                  const uint4 u = *reinterpret_cast<const uint4*>(stage_g + r * 128 + ((p ^ (r & 7)) << 4));
-                  __nv_bfloat16* d = out + static_cast<int64_t>(r0 + r) * args.out_ld + col + 8 * p;
-                  if (8 * p + 8 <= cols) {
-                    *reinterpret_cast<uint4*>(d) = u;
-                  } else {
-                    const __nv_bfloat16* s = reinterpret_cast<const __nv_bfloat16*>(&u);
-                    for (int k = 0; 8 * p + k < cols; ++k) d[k] = s[k];
-                  }
-                }
-              } else {
-                for (int r = 0; r < rows; ++r)
-                  for (int k = lane; k < cols; k += 32)
-                    out[static_cast<int64_t>(r0 + r) * args.out_ld + col + k] =
-                        h[r * 64 + (((k >> 3) ^ (r & 7)) << 3) + (k & 7)];
-              }
-            } else {
-              // the tile's columns are rows of out: 64 rows of 32
-#pragma unroll
-              for (int j = 0; j < 64; ++j) h[j * 32 + lane] = __float2bfloat16_rn(v[j]);
-              __syncwarp();
-              if (args.vec) {
-                for (int r = lane >> 2; r < cols; r += 8) {
-                  const int p = lane & 3;
-                  const uint4 u = *reinterpret_cast<const uint4*>(stage_g + r * 64 + p * 16);
-                  __nv_bfloat16* d = out + static_cast<int64_t>(col + r) * args.out_ld + r0 + 8 * p;
-                  if (8 * p + 8 <= rows) {
-                    *reinterpret_cast<uint4*>(d) = u;
-                  } else {
-                    const __nv_bfloat16* s = reinterpret_cast<const __nv_bfloat16*>(&u);
-                    for (int k = 0; 8 * p + k < rows; ++k) d[k] = s[k];
-                  }
-                }
-              } else {
-                for (int r = 0; r < cols; ++r)
-                  if (lane < rows) out[static_cast<int64_t>(col + r) * args.out_ld + r0 + lane] = h[r * 32 + lane];
-              }
-            }
-            __syncwarp();
           }
         }
       }
@@ -539,62 +659,477 @@ __global__ void __launch_bounds__(192, 1)
           mbar_arrive(tempty_bar + 8 * acc);
         else
           mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar + 8 * acc, 0));
+        // and, once the stores have landed, the tile to the next phase
+        if (!last) {
+          bulk_wait_all();
+          asm volatile("fence.proxy.async;" ::: "memory");
+          add_release(args.counters + u.phase * args.batch + u.e, 1);
+        }
       }
+      __syncwarp();
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
       }
     }
-    if (!LAST) {
-      if (lane == 0) bulk_wait_all();
-      __syncwarp();
-    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
 
   tc_fence_before();
   __syncthreads();
   // Every MMA of the pair has completed once the drain barrier has seen the leader's
   // final commit; only then may tensor memory be freed and the CTAs exit.
-  if (warp == 1 && lane == 0 && !mbar_wait(drain_bar, 0, 1000000000ull)) record_error(args.err, kErrTimeout);
+  if (warp == 1 && lane == 0 && !mbar_wait(drain_bar, 0, 4 * tmo + kDrain)) record_error(args.err, kErrTimeout);
   __syncthreads();
   cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc2(tmem_base, 512);
 }
 
-template <int MODE, bool LAST>
-cudaError_t launch_orth(const OrthMaps& maps, const OrthArgs& args, int sms, cudaStream_t st) {
-  auto kern = orth_gemm_kernel<MODE, LAST>;
+// The pairs that fit the device at once, asked for once per device; also allows the
+// kernel its shared memory.
+cudaError_t orth_pairs(int sms, int* pairs) {
+  static std::atomic<int> known[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  static std::atomic<uint64_t> ready{0};
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthSmem);
-    if (e != cudaSuccess) return e;
-    ready.fetch_or(bit, std::memory_order_relaxed);
-  }
-  const int64_t units = static_cast<int64_t>(args.batch) *
-                        (MODE == kUpdate ? args.mt * args.nt : args.mt * (args.mt + 1) / 2);
+  if ((*pairs = known[dev & 63].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(orth_steps_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOrthSmem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(units, sms / 2)));
+  cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = kOrthSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, orth_steps_kernel, &cfg);
+  if (e != cudaSuccess) return e;
+  if (n < 1) return cudaErrorLaunchOutOfResources;
+  *pairs = std::min(n, sms / 2);
+  known[dev & 63].store(*pairs, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
+cudaError_t launch_orth_steps(const OrthMaps& maps, const OrthArgs& args, int sms, cudaStream_t st) {
+  int pairs = 0;
+  const cudaError_t e = orth_pairs(sms, &pairs);
+  if (e != cudaSuccess) return e;
+  const int64_t units = static_cast<int64_t>(args.steps) * args.batch * (2 * args.units_sym + args.units_upd);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(units, pairs)));
   cfg.blockDim = dim3(192);
   cfg.dynamicSmemBytes = kOrthSmem;
   cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeCooperative;
+  attr[1].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, orth_steps_kernel, maps, args);
+}
+
+// ------------------------------------------------------------ narrow matrices
+// m <= 128: a matrix stays in shared memory from its first read to the result, in one
+// kernel.  A cluster of `ranks` CTAs takes a matrix, each CTA `chunks` blocks of 64
+// columns of X [128 rows, zeros past m], in the 128-byte swizzle: one layout serves as
+// the K-major operand of the gram and as the MN-major one of the update.
+//   norm and load   from g, the squares joined over the cluster
+//   gram            each CTA's columns; the CTAs' sums are added in rank order, a share
+//                   of the rows by each, which hands it to all
+//   poly            128 x 128 in every CTA
+//   update          in place: a group of 256 columns is overwritten when its product
+//                   is done
+// What bounds it is the chain of dependent steps, not the products.  At most one CTA
+// fits an SM (kSmallSmemMin): tensor memory of two clusters on shared SMs could each
+// wait for the other's.
+constexpr int kSmallThreads = 512;
+constexpr int kChunkBytes = 128 * 128;            // 128 rows of 64 columns
+constexpr int kMaxSmallChunks = 8;                // per CTA
+constexpr int kMaxSmallRanks = 16;             // (more than 8 where the device can)
+constexpr int kSmallTail = 2 * kChunkBytes + 4 * kChunkBytes + 1024 + 512;   // A, P (B in its first half), alignment, rest
+constexpr int kSmallSmemMin = 120 * 1024;
+constexpr int kSmallM = 128;
+constexpr int kSmallN = 8 * kMaxSmallChunks * 64;   // on 8 CTAs
+static_assert(kMaxSmallChunks * kChunkBytes + kSmallTail <= 232448, "shared memory budget");
+
+struct OrthSmall {
+  OrthIn in;
+  int m, n, chunks, ranks, steps;
+  float eps, S, out_scale;
+  __nv_bfloat16* out;
+  int64_t out_ld, out_stride;
+  int vec;               // rows of out start on 16 bytes
+  int* err;
+  uint64_t timeout_ns;
+  float coefs[kMaxOrthSteps][3];
+};
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void st_cluster1(uint32_t addr, float a) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(a) : "memory");
+}
+
+// Byte of element (row, column) in blocks of 64 columns in the 128-byte swizzle.
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  return (c >> 6) * kChunkBytes + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4) + (c & 7) * 2;
+}
+
+// Eight of g's elements as X sees them: row r, columns c .. c + 7 (not FLIP), or rows
+// r .. r + 7, column c (FLIP); 0 outside.
+template <typename E, bool FLIP>
+__device__ __forceinline__ void small_load8(const OrthIn& in, const E* g, int r, int c, float (&v)[8]) {
+  const int gr = FLIP ? c : r, gc = FLIP ? r : c;
+  if (gr < in.M && gc < in.N) {
+    load_row8(in, g + gr * in.ld, gc, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = 0.f;
+  }
+}
+
+template <typename E, bool FLIP>
+__global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __grid_constant__ OrthSmall a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ float part[3][32];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (sbase - raw);
+  const uint32_t sX = sbase, sA = sX + a.chunks * kChunkBytes, sP = sA + 2 * kChunkBytes, sB = sP;
+  const uint32_t bars = sP + 4 * kChunkBytes, slots = bars + 32, tmem_slot = bars + 24;
+  uint8_t *gX = gbase, *gA = gbase + (sA - sbase);
+  const float* gslots = reinterpret_cast<const float*>(gbase + (slots - sbase));   // [ranks][3]
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = a.ranks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int e = blockIdx.x / a.ranks;
+  const int width = a.chunks * 64, first = rank * width;   // this CTA's columns of X
+  const E* g = static_cast<const E*>(a.in.g) + static_cast<int64_t>(e) * a.in.stride;
+
+  if (tid == 0) {
+    mbar_init(bars, 1);
+    mbar_init(bars + 8, 1);
+    mbar_init(bars + 16, 1);
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+
+  // ---- norm and load: eight elements a thread; without FLIP neighbours along a row
+  // of X, with it along g's rows, which are X's columns
+  const int groups = FLIP ? 16 * width : 128 * (width / 8);
+  auto at = [&](int i, int& r, int& c) {
+    if (FLIP) {
+      r = i / width * 8;
+      c = i % width;
+    } else {
+      r = i / (width / 8);
+      c = i % (width / 8) * 8;
+    }
+  };
+  // (groups is a multiple of 2 kSmallThreads: 128 rows of a multiple of 64 columns)
+  constexpr int U = 2;
+  auto fetch = [&](int i0, float (&v)[U][8]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      int r, c;
+      at(i0 + u * kSmallThreads, r, c);
+      small_load8<E, FLIP>(a.in, g, r, first + c, v[u]);
+    }
+  };
+  Squares s;
+  for (int i = tid; i < groups; i += U * kSmallThreads) {
+    float v[U][8];
+    fetch(i, v);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s.add(v[u][k]);
+  }
+  s.mid = block_sum(s.mid, part[0]);
+  s.big = block_sum(s.big, part[1]);
+  s.small = block_sum(s.small, part[2]);
+  if (a.ranks > 1) {
+    // (a CTA of the cluster may be written to once all have started)
+    cluster_sync();
+    if (tid < a.ranks) {
+      const uint32_t p = mapa_shared(slots + rank * 12, tid);
+      st_cluster1(p, s.mid), st_cluster1(p + 4, s.big), st_cluster1(p + 8, s.small);
+    }
+    __syncwarp();
+    cluster_sync();
+    s = Squares{0.f, 0.f, 0.f};
+    for (int k = 0; k < a.ranks; ++k)
+      s.mid += gslots[3 * k], s.big += gslots[3 * k + 1], s.small += gslots[3 * k + 2];
+  }
+  const float2 f = orth_factor_of(s, a.eps, a.S);
+  for (int i = tid; i < groups; i += U * kSmallThreads) {
+    float v[U][8];
+    fetch(i, v);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      int r, c;
+      at(i + u * kSmallThreads, r, c);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[u][k] = v[u][k] * f.x * f.y;
+      if (FLIP) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) *reinterpret_cast<__half*>(gX + swz(r + k, c)) = __float2half_rn(v[u][k]);
+      } else {
+        st_shared_v4u(sX + swz(r, c), pack_half(v[u][0], v[u][1]), pack_half(v[u][2], v[u][3]),
+                      pack_half(v[u][4], v[u][5]), pack_half(v[u][6], v[u][7]));
+      }
+    }
+  }
+  fence_async_shared();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gbase + (tmem_slot - sbase));
+
+  const int q = warp & 3, part_c = (warp >> 2) * 32;      // rows of this warp, and its columns of 128
+  const int row = q * 32 + lane;
+  const uint32_t tq = tmem + (static_cast<uint32_t>(q * 32) << 16);
+  const int mc = (a.m + 15) & ~15;               // columns of A and B
+  const uint32_t idesc_sym = (1u << 4) | (static_cast<uint32_t>(mc >> 3) << 17) | ((128u >> 4) << 24);
+  const float S2 = a.S * a.S;
+  uint32_t phase[2] = {0, 0};
+  auto wait = [&](int b) {
+    if (!mbar_wait(bars + 8 * b, phase[b], a.timeout_ns)) record_error(a.err, kErrTimeout);
+    phase[b] ^= 1u;
+    tc_fence_after();
+  };
+
+  for (int step = 0; step < a.steps; ++step) {
+    // ---- gram
+    if (tid == 0) {
+      for (int k = 0; k < a.chunks * 4; ++k) {
+        const uint64_t d = smem_desc_sw128(sX + (k >> 2) * kChunkBytes + (k & 3) * 32, 16, 1024);
+        tc_mma<false>(tmem, d, d, idesc_sym, k != 0 ? 1u : 0u);
+      }
+      tc_commit(bars);
+    }
+    wait(0);
+    if (part_c < mc) {
+      const int c = part_c;
+      float v[32];
+      tmem_ld32(tq + c, v);
+      if (a.ranks == 1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          st_shared_v4u(sA + swz(row, c + 8 * j), pack_half(v[8 * j], v[8 * j + 1]), pack_half(v[8 * j + 2], v[8 * j + 3]),
+                        pack_half(v[8 * j + 4], v[8 * j + 5]), pack_half(v[8 * j + 6], v[8 * j + 7]));
+      } else {
+        // rows of 512 bytes, 16-byte pieces at piece ^ (row & 7)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          st_shared_v4(sP + row * 512 + (((c >> 2) + j) ^ (row & 7)) * 16, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+      }
+    }
+    if (a.ranks > 1) {
+      __syncwarp();
+      cluster_sync();
+      const int rows = 128 / a.ranks;
+      for (int i = tid; i < rows * 32; i += kSmallThreads) {
+        const int r = rank * rows + (i >> 5), p = i & 31;
+        if (4 * p >= mc) continue;      // (rows past m are zeros, and wanted as such)
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+        const uint32_t at_p = sP + r * 512 + (p ^ (r & 7)) * 16;
+        for (int k = 0; k < a.ranks; k += 4) {      // four loads at a time, added in order
+          float4 v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            v[j] = k + j < a.ranks ? ld_cluster4(mapa_shared(at_p, k + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t.x += v[j].x, t.y += v[j].y, t.z += v[j].z, t.w += v[j].w;
+        }
+        const uint32_t lo = pack_half(t.x, t.y), hi = pack_half(t.z, t.w), at_a = sA + swz(r, 4 * p);
+        for (int k = 0; k < a.ranks; ++k) st_cluster2(mapa_shared(at_a, k), lo, hi);
+      }
+      asm volatile("fence.proxy.async;" ::: "memory");
+      tc_fence_before();
+      __syncwarp();
+      cluster_sync();
+    } else {
+      fence_async_shared();
+      tc_fence_before();
+      __syncthreads();
+    }
+    // ---- poly
+    if (tid == 0) {
+      tc_fence_after();
+      asm volatile("fence.proxy.async;" ::: "memory");
+      for (int k = 0; k < mc / 16; ++k) {
+        const uint64_t d = smem_desc_sw128(sA + (k >> 2) * kChunkBytes + (k & 3) * 32, 16, 1024);
+        tc_mma<false>(tmem + 128, d, d, idesc_sym, k != 0 ? 1u : 0u);
+      }
+      tc_commit(bars);
+    }
+    wait(0);
+    const float cI = a.coefs[step][0] * S2, cA = a.coefs[step][1], cP = a.coefs[step][2] / S2;
+    if (part_c < mc) {
+      const int c = part_c;
+      float v[32];
+      tmem_ld32(tq + 128 + c, v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 u = *reinterpret_cast<const uint4*>(gA + swz(row, c + 8 * j));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+          float lo = fmaf(cA, x.x, cP * v[8 * j + 2 * k]), hi = fmaf(cA, x.y, cP * v[8 * j + 2 * k + 1]);
+          if (row == c + 8 * j + 2 * k) lo += cI;
+          if (row == c + 8 * j + 2 * k + 1) hi += cI;
+          o[k] = pack_half(lo, hi);
+        }
+        st_shared_v4u(sB + swz(row, c + 8 * j), o[0], o[1], o[2], o[3]);
+      }
+    }
+    fence_async_shared();
+    tc_fence_before();
+    __syncthreads();
+    // ---- update: groups of 256 columns, the first into columns 256.. of the tensor
+    // memory, the second into 0..255, where gram and poly are done with
+    const int ngroups = (a.chunks + 3) >> 2;
+    if (tid == 0) {
+      tc_fence_after();
+      for (int b = 0; b < ngroups; ++b) {
+        const int cols = min(256, width - 256 * b);
+        const uint32_t idesc = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(cols >> 3) << 17) | ((128u >> 4) << 24);
+        for (int k = 0; k < mc / 16; ++k)
+          tc_mma<false>(tmem + 256 * (1 - b), smem_desc_sw128(sB + (k >> 2) * kChunkBytes + (k & 3) * 32, 16, 1024),
+                        smem_desc_sw128(sX + 4 * b * kChunkBytes + k * 16 * 128, kChunkBytes, 1024), idesc, k != 0 ? 1u : 0u);
+        tc_commit(bars + 8 * b);
+      }
+    }
+    const bool last = step + 1 == a.steps;
+    const float ds = (last ? a.out_scale : 1.f) / S2;
+#pragma unroll 1
+    for (int b = 0; b < ngroups; ++b) {
+      wait(b);
+      const int cols = min(256, width - 256 * b);
+#pragma unroll 1
+      for (int c = part_c; c < cols; c += 128) {
+        float v[32];
+        tmem_ld32(tq + 256 * (1 - b) + c, v);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] *= ds;
+        const int xc = 256 * b + c;
+        if (!last) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            st_shared_v4u(sX + swz(row, xc + 8 * j), pack_half(v[8 * j], v[8 * j + 1]), pack_half(v[8 * j + 2], v[8 * j + 3]),
+                          pack_half(v[8 * j + 4], v[8 * j + 5]), pack_half(v[8 * j + 6], v[8 * j + 7]));
+        } else if (row < a.m) {
+          const int col = first + xc, live = a.n - col;    // columns that exist, from here
+          __nv_bfloat16* out = a.out + e * a.out_stride;
+          if (FLIP) {
+            // a warp's rows lie side by side
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j < live) out[static_cast<int64_t>(col + j) * a.out_ld + row] = __float2bfloat16_rn(v[j]);
+          } else {
+            __nv_bfloat16* o = out + static_cast<int64_t>(row) * a.out_ld + col;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              if (a.vec && j + 8 <= live) {
+                store8(o + j, v + j);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  if (j + k < live) o[j + k] = __float2bfloat16_rn(v[j + k]);
+              }
+            }
+          }
+        }
+      }
+    }
+    fence_async_shared();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
+  // every product has completed before the tensor memory is given back
+  if (tid == 0) {
+    tc_commit(bars + 16);
+    if (!mbar_wait(bars + 16, 0, 1000000000ull)) record_error(a.err, kErrTimeout);
+  }
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// CTAs per matrix: the number with the least time.  Measured, five steps at m = 128: 16
+// us, 3.3 for each block of 64 columns of a CTA, and 9 + 4 log2(r) for the exchanges in a
+// cluster of r (512 columns: 43.9 us on one CTA, 41.4 on 4; 2048: 61.9 on 4, 49.6 on
+// 16).  Matrices that do not fit at once go in waves, with whole clusters in each of the
+// eight groups of SMs (32 of 64 x 512: 31 us on 4, 88 on 8).
+void orth_small_ranks(OrthSmall* a, int batch, int most, int sms) {
+  double least = 1e300;
+  for (int r = 1, log = 0; r <= most; r *= 2, ++log) {
+    const int chunks = (a->n + 64 * r - 1) / (64 * r);
+    if (chunks > kMaxSmallChunks) continue;
+    const int slots = r == 1 ? sms : std::max(1, sms / 8 / r) * 8;
+    const double t = std::ceil(static_cast<double>(batch) / slots) * (16 + 3.3 * chunks + (r > 1 ? 9 + 4 * log : 0));
+    if (t < least) least = t, a->ranks = r, a->chunks = chunks;
+  }
+}
+
+template <typename E, bool FLIP>
+cudaError_t launch_orth_small(OrthSmall& a, int batch, int sms, cudaStream_t st) {
+  auto kern = orth_small_kernel<E, FLIP>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  constexpr int kMost = kMaxSmallChunks * kChunkBytes + kSmallTail;
+  cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, maps, args);
+  cfg.blockDim = dim3(kSmallThreads);
+  static std::atomic<int> known[64];      // the largest cluster, once per device
+  int most = known[dev & 63].load(std::memory_order_relaxed);
+  if (most == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(kMaxSmallRanks);
+    cfg.dynamicSmemBytes = kMost;
+    attr[0].val.clusterDim.x = kMaxSmallRanks;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    if (e != cudaSuccess) (void)cudaGetLastError(), n = 0;
+    most = n > 0 ? kMaxSmallRanks : 8;
+    known[dev & 63].store(most, std::memory_order_relaxed);
+  }
+  orth_small_ranks(&a, batch, most, sms);
+  cfg.gridDim = dim3(static_cast<unsigned>(batch * a.ranks));
+  cfg.dynamicSmemBytes = std::max(kSmallSmemMin, a.chunks * kChunkBytes + kSmallTail);
+  cfg.stream = st;
+  attr[0].val.clusterDim.x = a.ranks;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 // ------------------------------------------------------------ host
 constexpr int kMaxOrthSide = 65536;
-constexpr int kMaxOrthSteps = 32;
 const float kDefaultCoefs[3] = {3.4445f, -4.7750f, 2.0315f};
 
 struct OrthPlan {
@@ -603,13 +1138,21 @@ struct OrthPlan {
   int ldx, lda;
   int nparts, part_rows;
   int chunk;           // matrices per launch
-  size_t parts, x[2], a, b, total;
+  int small;           // narrow matrices: orth_small_kernel
+  size_t counters, parts, x[2], a, b, total;
 };
 
 int64_t round8(int64_t v) { return (v + 7) & ~static_cast<int64_t>(7); }
 
-// Matrices go through in chunks of about kChunkUnits tiles, enough to fill the last
-// wave of the 76 CTA pairs well, so the workspace does not grow with E.
+// Tiles of a symmetric m x m result with column tiles of bn: those from the diagonal
+// 256 x 256 block on.
+int64_t sym_units(int64_t m, int bn) {
+  const int64_t mt = (m + 255) / 256, nt = (m + bn - 1) / bn, f = 256 / bn;
+  return mt * nt - f * mt * (mt - 1) / 2;
+}
+
+// Matrices go through in chunks of about kChunkUnits tiles of a product, so the
+// workspace does not grow with E.
 constexpr int kChunkUnits = 1200;
 
 bool orth_plan(int64_t E, int64_t M, int64_t N, OrthPlan* p) {
@@ -619,12 +1162,19 @@ bool orth_plan(int64_t E, int64_t M, int64_t N, OrthPlan* p) {
   p->n = static_cast<int>(std::max(M, N));
   p->ldx = static_cast<int>(round8(p->n));
   p->lda = static_cast<int>(round8(p->m));
-  p->nparts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(M * N + kNormElems - 1) / kNormElems, M, kMaxParts})));
+  p->small = 0;
+  if (p->m <= kSmallM && p->n <= kSmallN) {
+    p->small = 1;
+    p->chunk = 1 << 24;
+    p->total = 256;
+    return true;
+  }
+  const int64_t units = sym_units(p->m, 256);
+  p->chunk = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({E, (kChunkUnits + units - 1) / units, 4096})));
+  const int64_t want = std::min<int64_t>((M * N + kNormElems - 1) / kNormElems, kNormBlocks / p->chunk);
+  p->nparts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, M, kMaxParts})));
   p->part_rows = static_cast<int>((M + p->nparts - 1) / p->nparts);
   p->nparts = static_cast<int>((M + p->part_rows - 1) / p->part_rows);
-  const int64_t mt = (p->m + 255) / 256;
-  const int64_t units = mt * (mt + 1) / 2;
-  p->chunk = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({E, (kChunkUnits + units - 1) / units, 4096})));
   size_t at = 256;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -632,6 +1182,7 @@ bool orth_plan(int64_t E, int64_t M, int64_t N, OrthPlan* p) {
     return o;
   };
   const size_t C = p->chunk;
+  p->counters = take(sizeof(int) * 3 * kMaxOrthSteps * C);
   p->parts = take(sizeof(Squares) * C * p->nparts);
   p->x[0] = take(2 * C * p->m * static_cast<size_t>(p->ldx));
   p->x[1] = take(2 * C * p->m * static_cast<size_t>(p->ldx));
@@ -685,6 +1236,61 @@ float orth_scale(const float* coefs, int steps, int n) {
   return std::ldexp(top, 2 * s) <= 60000.0 ? std::ldexp(1.f, s) : 0.f;
 }
 
+bool rows_on_16(const void* p, int es, int64_t ld, int64_t stride, int batch) {
+  const int W = 16 / es;
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % W == 0 && (batch == 1 || stride % W == 0);
+}
+
+OrthIn orth_in(const void* g, int32_t dtype, int64_t e0, int batch, int64_t M, int64_t N, int64_t ld, int64_t stride) {
+  const int es = dtype == MOE_FP32 ? 4 : 2;
+  const char* p = static_cast<const char*>(g) + e0 * stride * es;
+  return OrthIn{p, ld, stride, static_cast<int>(M), static_cast<int>(N), rows_on_16(p, es, ld, stride, batch)};
+}
+
+// Width of the column tiles: the one with the least time.  Full tiles are bound by the
+// products, narrower ones by their loads (16 KB for the rows of A whatever their width):
+// in units of a full tile's 256 they take 183 and 152, and each about 32 for its start
+// and end.  One matrix alone waits for each phase's last tiles, several fill one
+// another's.
+template <typename F>
+int orth_width(const F& units, int batch, int pairs) {
+  int best = 256;
+  double least = 1e300;
+  for (int bn = 256; bn >= 64; bn /= 2) {
+    const double waves = static_cast<double>(units(bn)) * batch / pairs;
+    const double each = 32 + (bn == 256 ? 256 : bn == 128 ? 183 : 152);
+    const double t = (batch == 1 ? std::ceil(waves) : std::max(1.0, waves)) * each;
+    if (t < least) least = t, best = bn;
+  }
+  return best;
+}
+
+void orth_tiles(OrthArgs* a, int pairs) {
+  const auto upd = [&](int bn) { return static_cast<int64_t>(a->mt) * ((a->n + bn - 1) / bn); };
+  int bn = orth_width([&](int w) { return sym_units(a->m, w); }, a->batch, pairs);
+  a->bn_sym = bn, a->nt_sym = (a->m + bn - 1) / bn;
+  a->units_sym = static_cast<int>(sym_units(a->m, bn));
+  bn = orth_width(upd, a->batch, pairs);
+  a->bn_upd = bn, a->nt_upd = (a->n + bn - 1) / bn;
+  a->units_upd = static_cast<int>(upd(bn));
+}
+
+bool orth_maps(OrthMaps* t, const OrthPlan& p, const OrthArgs& a, __half* const* x, const __half* A, const __half* B) {
+  const auto SW = CU_TENSOR_MAP_SWIZZLE_128B, NOSW = CU_TENSOR_MAP_SWIZZLE_NONE;
+  const uint64_t m = p.m, n = p.n, C = a.batch, lda = p.lda;
+  const uint32_t bs = a.bn_sym / 2;
+  bool ok = true;
+  for (int i = 0; i < 2; ++i)
+    ok = ok && abi_map_half(&t->xk[i], x[i], n, m, C, p.ldx, 64, 128, SW) &&
+         abi_map_half(&t->xs[i], x[i], n, m, C, p.ldx, 64, bs, SW) &&
+         abi_map_half(&t->xn[i], x[i], n, m, C, p.ldx, 64, 64, SW) &&
+         abi_map_half(&t->xo[i], x[i], n, m, C, p.ldx, 64, 32, SW);
+  return ok && abi_map_half(&t->ak, A, m, m, C, lda, 64, 128, SW) && abi_map_half(&t->as, A, m, m, C, lda, 64, bs, SW) &&
+         abi_map_half(&t->ao, A, m, m, C, lda, 64, 32, SW) && abi_map_half(&t->at, A, m, m, C, lda, 32, 64, NOSW) &&
+         abi_map_half(&t->bk, B, m, m, C, lda, 64, 128, SW) && abi_map_half(&t->bo, B, m, m, C, lda, 64, 32, SW) &&
+         abi_map_half(&t->bt, B, m, m, C, lda, 32, 64, NOSW);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -719,49 +1325,60 @@ moe_status moe_orthogonalize(int64_t E, int64_t M, int64_t N, int32_t dtype, con
   const moe_status ds = abi_device_sms(&sms);
   if (ds != MOE_OK) return ds;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (p.small) {
+    OrthSmall a = {};
+    a.m = p.m, a.n = p.n, a.steps = steps;
+    a.eps = eps, a.S = S, a.out_scale = scale / S;
+    a.out_ld = out_ld, a.out_stride = out_stride;
+    a.err = static_cast<int*>(ws);
+    a.timeout_ns = abi_wait_timeout_ns();
+    for (int i = 0; i < steps; ++i)
+      for (int k = 0; k < 3; ++k) a.coefs[i][k] = coefs ? coefs[3 * i + k] : kDefaultCoefs[k];
+    for (int64_t e0 = 0; e0 < E; e0 += p.chunk) {
+      const int batch = static_cast<int>(std::min<int64_t>(p.chunk, E - e0));
+      a.in = orth_in(g, dtype, e0, batch, M, N, g_ld, g_stride);
+      a.out = static_cast<__nv_bfloat16*>(out) + e0 * out_stride;
+      a.vec = rows_on_16(a.out, 2, out_ld, out_stride, batch);
+      const cudaError_t e = abi_tracked(kAbiOrthSmall, 1, st, [&] {
+        if (dtype == MOE_FP32)
+          return p.flip ? launch_orth_small<float, true>(a, batch, sms, st) : launch_orth_small<float, false>(a, batch, sms, st);
+        return p.flip ? launch_orth_small<__nv_bfloat16, true>(a, batch, sms, st)
+                      : launch_orth_small<__nv_bfloat16, false>(a, batch, sms, st);
+      });
+      if (e != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
+  }
   char* w = static_cast<char*>(ws);
   Squares* parts = reinterpret_cast<Squares*>(w + p.parts);
+  int* counters = reinterpret_cast<int*>(w + p.counters);
   __half* x[2] = {reinterpret_cast<__half*>(w + p.x[0]), reinterpret_cast<__half*>(w + p.x[1])};
   __half* a = reinterpret_cast<__half*>(w + p.a);
   __half* b = reinterpret_cast<__half*>(w + p.b);
-  const uint64_t C = p.chunk;
-  const auto SW = CU_TENSOR_MAP_SWIZZLE_128B, NOSW = CU_TENSOR_MAP_SWIZZLE_NONE;
-  OrthMaps gram[2], poly, update[2];
-  bool ok = true;
-  for (int i = 0; i < 2; ++i) {
-    ok = ok && abi_map_half(&gram[i].a, x[i], p.n, p.m, C, p.ldx, 64, 128, SW) &&
-         abi_map_half(&gram[i].out, a, p.m, p.m, C, p.lda, 64, 32, SW) &&
-         abi_map_half(&gram[i].out_t, a, p.m, p.m, C, p.lda, 32, 64, NOSW) &&
-         abi_map_half(&update[i].a, b, p.m, p.m, C, p.lda, 64, 128, SW) &&
-         abi_map_half(&update[i].b, x[i], p.n, p.m, C, p.ldx, 64, 64, SW) &&
-         abi_map_half(&update[i].out, x[1 - i], p.n, p.m, C, p.ldx, 64, 32, SW);
-    gram[i].b = gram[i].a;
-    update[i].out_t = update[i].out;
-  }
-  ok = ok && abi_map_half(&poly.a, a, p.m, p.m, C, p.lda, 64, 128, SW) &&
-       abi_map_half(&poly.out, b, p.m, p.m, C, p.lda, 64, 32, SW) &&
-       abi_map_half(&poly.out_t, b, p.m, p.m, C, p.lda, 32, 64, NOSW);
-  if (!ok) return MOE_ERR_CUDA;
-  poly.b = poly.a;
-  const float S2 = S * S;
-  OrthArgs base = {};
-  base.mt = (p.m + 255) / 256;
-  base.err = static_cast<int*>(ws);
-  base.timeout_ns = abi_wait_timeout_ns();
-  base.m = p.m;
-  base.A = a, base.lda = p.lda, base.astride = static_cast<int64_t>(p.m) * p.lda;
+  OrthArgs args = {};
+  args.m = p.m, args.n = p.n, args.steps = steps;
+  args.mt = (p.m + 255) / 256;
+  args.S2 = S * S, args.out_scale = scale / S;
+  args.A = a, args.lda = p.lda, args.astride = static_cast<int64_t>(p.m) * p.lda;
+  args.out_ld = out_ld, args.out_stride = out_stride, args.flip = p.flip;
+  args.counters = counters;
+  args.err = static_cast<int*>(ws);
+  args.timeout_ns = abi_wait_timeout_ns();
+  for (int i = 0; i < steps; ++i)
+    for (int k = 0; k < 3; ++k) args.coefs[i][k] = coefs ? coefs[3 * i + k] : kDefaultCoefs[k];
   for (int64_t e0 = 0; e0 < E; e0 += p.chunk) {
     const int batch = static_cast<int>(std::min<int64_t>(p.chunk, E - e0));
-    const char* gp = static_cast<const char*>(g) + e0 * g_stride * es;
-    const int W = 16 / es;
-    OrthIn in{gp, g_ld, g_stride, static_cast<int>(M), static_cast<int>(N), dtype == MOE_BF16,
-              (reinterpret_cast<uintptr_t>(gp) & 15) == 0 && g_ld % W == 0 && (batch == 1 || g_stride % W == 0)};
+    const OrthIn in = orth_in(g, dtype, e0, batch, M, N, g_ld, g_stride);
     cudaError_t e = abi_tracked(kAbiOrthLoad, 2, st, [&] {
-      orth_norm_kernel<<<dim3(p.nparts, batch), kNormThreads, 0, st>>>(in, p.part_rows, parts);
+      if (dtype == MOE_FP32)
+        orth_norm_kernel<float><<<dim3(p.nparts, batch), kNormThreads, 0, st>>>(in, p.part_rows, parts);
+      else
+        orth_norm_kernel<__nv_bfloat16><<<dim3(p.nparts, batch), kNormThreads, 0, st>>>(in, p.part_rows, parts);
       cudaError_t r = cudaGetLastError();
       if (r != cudaSuccess) return r;
+      const int64_t tiles = ((M + 63) / 64) * ((N + 63) / 64);
       cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(static_cast<unsigned>((N + 63) / 64), static_cast<unsigned>((M + 63) / 64), batch);
+      cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(tiles, (sms * 8 + batch - 1) / batch)), batch);
       cfg.blockDim = dim3(256);
       cfg.stream = st;
       cudaLaunchAttribute at[1];
@@ -771,37 +1388,20 @@ moe_status moe_orthogonalize(int64_t E, int64_t M, int64_t N, int32_t dtype, con
       cfg.numAttrs = 1;
       auto go = [&](auto kern) {
         return cudaLaunchKernelEx(&cfg, kern, in, static_cast<const Squares*>(parts), p.nparts, eps, S, x[0], p.ldx,
-                                  static_cast<int64_t>(p.m) * p.ldx);
+                                  static_cast<int64_t>(p.m) * p.ldx, counters, 3 * steps * batch);
       };
       if (dtype == MOE_FP32) return p.flip ? go(orth_load_kernel<float, true>) : go(orth_load_kernel<float, false>);
       return p.flip ? go(orth_load_kernel<__nv_bfloat16, true>) : go(orth_load_kernel<__nv_bfloat16, false>);
     });
     if (e != cudaSuccess) return MOE_ERR_CUDA;
-    base.batch = batch;
-    for (int i = 0; i < steps; ++i) {
-      const float* c = coefs ? coefs + 3 * i : kDefaultCoefs;
-      OrthArgs args = base;
-      args.n = p.m, args.nt = args.mt, args.num_kb = (p.n + 63) / 64, args.ds = 1.f;
-      e = abi_tracked(kAbiOrthGram, 1, st, [&] { return launch_orth<kGram, false>(gram[i & 1], args, sms, st); });
-      if (e != cudaSuccess) return MOE_ERR_CUDA;
-      args.num_kb = (p.m + 63) / 64, args.ds = c[2] / S2, args.cA = c[1], args.cI = c[0] * S2;
-      e = abi_tracked(kAbiOrthPoly, 1, st, [&] { return launch_orth<kPoly, false>(poly, args, sms, st); });
-      if (e != cudaSuccess) return MOE_ERR_CUDA;
-      args.n = p.n, args.nt = (p.n + 255) / 256, args.ds = 1.f / S2;
-      const bool last = i + 1 == steps;
-      if (last) {
-        args.ds = scale / (S2 * S);
-        args.out = static_cast<__nv_bfloat16*>(out) + e0 * out_stride;
-        args.out_ld = out_ld, args.out_stride = out_stride, args.flip = p.flip;
-        args.vec = (reinterpret_cast<uintptr_t>(args.out) & 15) == 0 && out_ld % 8 == 0 &&
-                   (batch == 1 || out_stride % 8 == 0);
-      }
-      e = abi_tracked(kAbiOrthUpdate, 1, st, [&] {
-        return last ? launch_orth<kUpdate, true>(update[i & 1], args, sms, st)
-                    : launch_orth<kUpdate, false>(update[i & 1], args, sms, st);
-      });
-      if (e != cudaSuccess) return MOE_ERR_CUDA;
-    }
+    args.batch = batch;
+    orth_tiles(&args, sms / 2);
+    args.out = static_cast<__nv_bfloat16*>(out) + e0 * out_stride;
+    args.vec = rows_on_16(args.out, 2, out_ld, out_stride, batch);
+    OrthMaps maps;
+    if (!orth_maps(&maps, p, args, x, a, b)) return MOE_ERR_CUDA;
+    e = abi_tracked(kAbiOrthSteps, 1, st, [&] { return launch_orth_steps(maps, args, sms, st); });
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
   }
   return MOE_OK;
 }

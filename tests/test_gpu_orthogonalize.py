@@ -89,7 +89,7 @@ def check(g, **kw):
 
 
 SHAPES = [(1, 1), (1, 7), (7, 1), (3, 5), (16, 16), (8, 200), (64, 64), (65, 63), (128, 128), (129, 127), (128, 300), (300, 128),
-          (257, 255), (255, 513), (256, 256), (512, 512), (640, 384), (1000, 40), (40, 1001), (511, 1029), (2880, 128)]
+          (257, 255), (255, 513), (256, 256), (512, 512), (640, 384), (1000, 40), (40, 1001), (511, 1029), (2880, 128), (100, 512), (513, 33), (128, 2049), (4096, 72), (24, 4097)]
 
 
 @pytest.mark.parametrize("M,N", SHAPES)
@@ -261,7 +261,7 @@ def test_empty_and_refused():
     with pytest.raises(ValueError):
         moe.orthogonalize(g, out, ws, coefs=[COEFS] * 3)
     with pytest.raises(moe.MoeError):
-        moe.orthogonalize(g, out, ws[:512])
+        moe.orthogonalize(g, out, ws[:128])
     with pytest.raises(moe.MoeError):
         moe.orthogonalize(g, out[:1].expand(2, 16, 24), ws)        # results over one another
 

@@ -57,7 +57,9 @@ def test_route_bwd_refusals(L):
 
 def test_orthogonalize_refusals(L):
     size = L.moe_orthogonalize_workspace_size(2, 16, 24)
-    assert size >= 256 + 2 * 2 * 16 * (24 + 24 + 16 + 16)
+    assert size >= 256
+    # two copies of x, a and b in fp16
+    assert L.moe_orthogonalize_workspace_size(2, 300, 500) >= 2 * 2 * 300 * (500 + 500 + 300 + 300)
     for bad in ((-1, 16, 24), (2, 0, 24), (2, 16, 0), (2, 65537, 4), (2, 4, 65537)):
         assert L.moe_orthogonalize_workspace_size(*bad) == 0
     # the workspace is that of the matrices that go through at once
@@ -94,4 +96,4 @@ def test_kernel_kinds_have_names(L):
     names = [L.moe_profile_kernel_name(i) for i in range(64)]
     known = [n for n in names if n]
     assert len(set(known)) == len(known) and names[len(known):] == [None] * (64 - len(known))
-    assert {"join_fwd", "join_bwd", "route_bwd", "orth_load", "orth_gram", "orth_poly", "orth_update"} <= set(known)
+    assert {"join_fwd", "join_bwd", "route_bwd", "orth_load", "orth_steps", "orth_small"} <= set(known)
