@@ -25,8 +25,118 @@
 #include "rows.cuh"
 #include "vec.cuh"
 
+#ifndef JTH
+#define JTH 512
+#define JTB 1024
+#endif
 namespace moe {
 namespace {
+
+// The rows that a block walks (blockIdx.x, + gridDim.x, ..), N arrays of them, D - 1 rows
+// ahead of their use.  A warp owns 256 V neighbouring columns, vector i of a lane is
+// columns 256 i + 8 lane of them: each warp copies its columns asynchronously into its
+// own part of shared memory and reads them back itself, so no barrier of the block is
+// needed, and all addresses within a row are one register and constants.  Places whose
+// columns or array do not exist hold zeros, which add nothing to a sum: the arithmetic
+// has no branches.  In fp32 a copy instruction covers 512 contiguous bytes, so a lane
+// copies other pieces than it reads.  D = 0: loads at their use.
+template <typename E, int N, int V, int D>
+struct RowStream {
+  static constexpr int W = Raw8<E>::W;
+  static constexpr int WARP_BYTES = N * V * W * 512;       // of a row
+  static constexpr int bytes(int threads) { return D * WARP_BYTES * (threads / 32); }
+  const char* src[N];   // this warp's columns of the next row to be copied; null: absent
+  int64_t step;         // from one of the block's rows to the next
+  uint32_t ring;        // this warp's part
+  int put, get;         // stages
+  uint32_t copies;      // a bit for each piece of a row that exists
+  bool in[V];           // the lane's vectors exist
+
+  __device__ __forceinline__ void init(uint4* smem, const E* const (&p)[N], int H) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int first = warp * 256 * V;
+    copies = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      in[i] = first + i * 256 + lane * 8 < H;
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        if (first + i * 256 + (w * 32 + lane) * (8 / W) < H) copies |= 1u << (i * W + w);
+    }
+    const int own = D > 0 ? lane * 16 : lane * 16 * W;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      src[n] = p[n] ? reinterpret_cast<const char*>(p[n] + static_cast<int64_t>(blockIdx.x) * H + first) + own : nullptr;
+    step = static_cast<int64_t>(gridDim.x) * H * sizeof(E);
+    put = get = 0;
+    if (D > 0) {
+      ring = smem_u32(smem) + warp * (D * WARP_BYTES);
+      for (int i = lane * 16; i < D * WARP_BYTES; i += 512) st_shared_v4(ring + i, 0.f, 0.f, 0.f, 0.f);
+      __syncwarp();
+    }
+  }
+  // Copies of the block's next row, where there is one.
+  __device__ __forceinline__ void issue(bool more) {
+    if (D == 0) return;
+    if (more) {
+      const uint32_t dst = ring + put * WARP_BYTES + (threadIdx.x & 31) * 16;
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        if (!src[n]) continue;
+#pragma unroll
+        for (int i = 0; i < V * W; ++i)
+          if (copies & (1u << i)) cp_async16(dst + (n * V * W + i) * 512, src[n] + i * 512, 16);
+        src[n] += step;
+      }
+      put = put + 1 == D ? 0 : put + 1;
+    }
+    cp_async_commit();
+  }
+  // The oldest row's copies are there, and may be read.
+  __device__ __forceinline__ void wait() const {
+    if (D == 0) return;
+    cp_async_wait<D >= 2 ? D - 2 : 0>();
+    if (W > 1) __syncwarp();
+  }
+  __device__ __forceinline__ void take(int n, int i, Raw8<E>& r) const {
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (D > 0) {
+        const uint32_t at = ring + get * WARP_BYTES + (n * V + i) * W * 512 + (threadIdx.x & 31) * (16 * W) + w * 16;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.u[w].x), "=r"(r.u[w].y), "=r"(r.u[w].z), "=r"(r.u[w].w) : "r"(at) : "memory");
+      } else {
+        r.u[w] = make_uint4(0u, 0u, 0u, 0u);
+        if (src[n] && in[i]) r.u[w] = *reinterpret_cast<const uint4*>(src[n] + i * 512 * W + w * 16);
+      }
+    }
+  }
+  // The row's arrays have been taken.
+  __device__ __forceinline__ void next() {
+    if (D > 0) {
+      get = get + 1 == D ? 0 : get + 1;
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        if (src[n]) src[n] += step;
+    }
+  }
+};
+
+// Rows of a block: k-th is blockIdx.x + k gridDim.x.
+__device__ __forceinline__ int block_rows(int64_t T) {
+  return static_cast<int>((T - blockIdx.x + gridDim.x - 1) / gridDim.x);
+}
+
+// A column's weights as fp32 pairs, ones where there are none.
+template <typename E>
+__device__ __forceinline__ void load_weights(const E* p, bool in, float2 (&w)[4]) {
+  Raw8<E> r;
+  r.ones();
+  if (p && in) r.load(p);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = r.pair(j);
+}
 
 struct JoinFwd {
   const void *y, *residual, *post_weight, *weight;
@@ -42,86 +152,129 @@ struct JoinFwd {
 
 enum JoinOut : int { kNoNorm = 0, kSameType = 1, kE4m3 = 2 };
 
-template <typename E, int OUT, int V, int D>
-__global__ void __launch_bounds__(1024) join_fwd_kernel(const JoinFwd a) {
+template <typename E, int OUT, int V, int D, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) join_fwd_kernel(const JoinFwd a) {
   extern __shared__ uint4 ring_mem[];
-  __shared__ float part[4][32];
-  const int H = a.H;
-  const int64_t T = a.T;
-  const E* post_weight = static_cast<const E*>(a.post_weight);
-  const E* weight = static_cast<const E*>(a.weight);
-  E* total = static_cast<E*>(a.total);
-  RowRing<E, 2, V, D> rows{ring_mem, {static_cast<const E*>(a.y), static_cast<const E*>(a.residual)}, H};
+  __shared__ float part[2][128];
+  const int H = a.H, count = block_rows(a.T);
+  RowStream<E, 2, V, D> rows;
+  rows.init(ring_mem, {static_cast<const E*>(a.y), static_cast<const E*>(a.residual)}, H);
 #pragma unroll
-  for (int d = 0; d < D - 1; ++d) rows.issue(d, blockIdx.x + static_cast<int64_t>(d) * gridDim.x, T);
-  int stage = 0, flip = 0;   // a row's barriers also separate the reuse of the other sums
-  for (int64_t row = blockIdx.x; row < T; row += gridDim.x, flip ^= 2) {
-    const int64_t base = row * H;
-    if (D > 0) {
-      rows.wait();
-      rows.issue(stage == 0 ? D - 1 : stage - 1, row + static_cast<int64_t>(D - 1) * gridDim.x, T);
-    }
+  for (int d = 0; d < D - 1; ++d) rows.issue(d < count);
+  const int lane = threadIdx.x & 31;
+  const int c0 = (threadIdx.x >> 5) * 256 * V + lane * 8;     // of vector 0
+  // the weights, and a row's terms between its two passes, in registers where these
+  // allow (twice unpacked, a vector takes a third more instructions)
+  constexpr bool KEEP = V == 1 || MAXT <= 256;
+  constexpr int K = KEEP ? V : 1;
+  float2 wp[K][4], w[K][4];
+  auto weights = [&](int i) {
+    const E* pw = static_cast<const E*>(a.post_weight);
+    load_weights(pw ? pw + c0 + i * 256 : pw, rows.in[i], wp[KEEP ? i : 0]);
+    if (OUT != kNoNorm) load_weights(static_cast<const E*>(a.weight) + c0 + i * 256, rows.in[i], w[KEEP ? i : 0]);
+  };
+  if (KEEP)
+#pragma unroll
+    for (int i = 0; i < V; ++i) weights(i);
+  const float inv_H = 1.f / static_cast<float>(H);
+  const float2 scale2 = make_float2(a.scale, a.scale);
+  const int64_t at0 = static_cast<int64_t>(blockIdx.x) * H + c0;
+  E* total = static_cast<E*>(a.total) + at0;
+  char* n_out = OUT == kNoNorm ? nullptr : static_cast<char*>(a.n) + at0 * (OUT == kE4m3 ? 1 : sizeof(E));
+  uint8_t* s_out = OUT == kE4m3 ? a.n_scale + at0 / 32 : nullptr;
+  float gates = 1.f;      // of 32 rows, one per lane (a load per row would wait for the rows' copies)
+  for (int row = 0; row < count; ++row) {
+    const int flip = row & 1;      // a row's barrier also separates the reuse of the other sums
+    if (a.gate && (row & 31) == 0 && row + lane < count)
+      gates = __ldg(a.gate + blockIdx.x + static_cast<int64_t>(row + lane) * gridDim.x);
+    const float gate = __shfl_sync(0xffffffffu, gates, row & 31);
+    rows.wait();
+    rows.issue(row + D - 1 < count);
+    // total = t + f q with t = scale * residual, q = y * post_weight, f = gate * rs_y
     Raw8<E> ry[V], rr[V];
+    float2 t[K][4], q[K][4];
+    auto terms = [&](int i) {
+      const int k = KEEP ? i : 0;
+      if (!KEEP) weights(i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        t[k][j] = mul2(scale2, rr[i].pair(j));
+        q[k][j] = mul2(ry[i].pair(j), wp[k][j]);
+      }
+    };
+    float2 yy = make_float2(0.f, 0.f), tt = yy, tq = yy, qq = yy;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int k = KEEP ? i : 0;
+      rows.take(0, i, ry[i]);
+      rows.take(1, i, rr[i]);
+      terms(i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 y = ry[i].pair(j);
+        yy = fma2(y, y, yy);
+        if (OUT != kNoNorm) {
+          tt = fma2(t[k][j], t[k][j], tt);
+          tq = fma2(t[k][j], q[k][j], tq);
+          qq = fma2(q[k][j], q[k][j], qq);
+        }
+      }
+    }
+    rows.next();
+    float4 s = make_float4(yy.x + yy.y, tt.x + tt.y, tq.x + tq.y, qq.x + qq.y);
+    if (OUT != kNoNorm)
+      s = block_sum4(s, part[flip]);
+    else if (a.post_norm)
+      s.x = block_sum(s.x, part[flip]);
+    const float rs_y = a.post_norm ? rsqrtf(s.x * inv_H + a.eps) : 1.f;
+    const float f = gate * rs_y;
+    const float2 f2 = make_float2(f, f);
+    // the sum of total^2 from those of its terms, unless they cancel (or leave fp32's
+    // range): then once more from total
     float ss = 0.f;
+    if (OUT != kNoNorm) {
+      const float terms2 = s.y + f * f * s.w;
+      ss = terms2 + 2.f * f * s.z;
+      if (!(ss >= 0.25f * terms2 && ss < INFINITY)) {
+        ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
-      if (c < H) {
-        rows.take(stage, 0, i, row, c, ry[i]);
-        rows.take(stage, 1, i, row, c, rr[i]);
-        if (a.post_norm) {
+        for (int i = 0; i < V; ++i) {
+          if (!KEEP) terms(i);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss = fmaf(ry[i].get(j), ry[i].get(j), ss);
+          for (int j = 0; j < 4; ++j) {
+            const float2 r = fma2(f2, q[KEEP ? i : 0][j], t[KEEP ? i : 0][j]);
+            if (rows.in[i]) ss = fmaf(r.x, r.x, fmaf(r.y, r.y, ss));     // (an infinite f makes NaN of zeros)
+          }
         }
+        __syncthreads();      // all have read `part`
+        ss = block_sum(ss, part[flip]);
       }
     }
-    if (D > 0) stage = stage + 1 == D ? 0 : stage + 1;
-    float rs_y = 1.f;
-    if (a.post_norm) {
-      ss = block_sum(ss, part[flip]);
-      rs_y = 1.f / sqrtf(ss / static_cast<float>(H) + a.eps);
-      if (a.rstd_post && threadIdx.x == 0) a.rstd_post[row] = rs_y;
+    const float rs = rsqrtf(ss * inv_H + a.eps);
+    if (threadIdx.x == 0) {
+      const int64_t r = blockIdx.x + static_cast<int64_t>(row) * gridDim.x;
+      if (a.rstd_post) a.rstd_post[r] = rs_y;
+      if (OUT != kNoNorm && a.rstd) a.rstd[r] = rs;
     }
-    const float gate = a.gate ? __ldg(a.gate + row) : 1.f;
-    float r[V][8];
-    ss = 0.f;
+    const float2 rs2 = make_float2(rs, rs);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
-      if (c < H) {
-        Raw8<E> w;
-        if (post_weight) w.load(post_weight + c);
+      const int k = KEEP ? i : 0;
+      if (!KEEP) terms(i);
+      float2 r[4], n[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float p = ry[i].get(j) * rs_y;
-          if (post_weight) p *= w.get(j);
-          r[i][j] = fmaf(a.scale, rr[i].get(j), gate * p);
-          if (OUT != kNoNorm) ss = fmaf(r[i][j], r[i][j], ss);
-        }
-        store8(total + base + c, r[i]);
+      for (int j = 0; j < 4; ++j) {
+        r[j] = fma2(f2, q[k][j], t[k][j]);
+        if (OUT != kNoNorm) n[j] = mul2(mul2(r[j], rs2), w[k][j]);
       }
+      if (rows.in[i]) store8(total + i * 256, &r[0].x);
+      if (OUT == kSameType && rows.in[i]) store8(reinterpret_cast<E*>(n_out) + i * 256, &n[0].x);
+      if (OUT == kE4m3) store_e4m3(n, rows.in[i], reinterpret_cast<uint8_t*>(n_out) + i * 256, s_out + i * 8);
     }
-    if (OUT == kNoNorm) continue;
-    ss = block_sum(ss, part[flip + 1]);
-    const float rs = 1.f / sqrtf(ss / static_cast<float>(H) + a.eps);
-    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rs;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
-      if (OUT == kSameType && c >= H) continue;
-      float o[8];
-      if (c < H) {
-        Raw8<E> w;
-        w.load(weight + c);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = r[i][j] * rs * w.get(j);
-      }
-      if (OUT == kSameType) {
-        store8(static_cast<E*>(a.n) + base + c, o);
-      } else {
-        store_e4m3(o, c < H, static_cast<uint8_t*>(a.n) + base + c, a.n_scale + row * (H / 32) + c / 32);
-      }
-    }
+    const int64_t step = static_cast<int64_t>(gridDim.x) * H;
+    total += step;
+    if (OUT != kNoNorm) n_out += step * (OUT == kE4m3 ? 1 : sizeof(E));
+    if (OUT == kE4m3) s_out += step / 32;
   }
 }
 
@@ -136,132 +289,138 @@ struct JoinBwd {
 };
 
 // NEXT: a norm follows (dn, total, weight and rstd are there).
-template <typename E, bool NEXT, int V, int D>
-__global__ void __launch_bounds__(1024) join_bwd_kernel(const JoinBwd a) {
+template <typename E, bool NEXT, int V, int D, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 1) join_bwd_kernel(const JoinBwd a) {
   extern __shared__ uint4 ring_mem[];
-  __shared__ float part[2][3][32];
+  __shared__ float part[2][128];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int N = NEXT ? 4 : 2;
-  const int H = a.H;
-  const int64_t T = a.T;
-  RowRing<E, N, V, D> rows{ring_mem, {}, H};
-  rows.src[0] = static_cast<const E*>(a.y);
-  rows.src[1] = static_cast<const E*>(a.d_total);
-  if (NEXT) {
-    rows.src[N - 2] = static_cast<const E*>(a.dn);
-    rows.src[N - 1] = static_cast<const E*>(a.total);
+  const int H = a.H, count = block_rows(a.T);
+  RowStream<E, N, V, D> rows;
+  {
+    const E* p[N] = {static_cast<const E*>(a.y), static_cast<const E*>(a.d_total)};
+    if (NEXT) p[N - 2] = static_cast<const E*>(a.dn), p[N - 1] = static_cast<const E*>(a.total);
+    rows.init(ring_mem, p, H);
   }
 #pragma unroll
-  for (int d = 0; d < D - 1; ++d) rows.issue(d, blockIdx.x + static_cast<int64_t>(d) * gridDim.x, T);
-  const E* weight = static_cast<const E*>(a.weight);
-  const E* post_weight = static_cast<const E*>(a.post_weight);
+  for (int d = 0; d < D - 1; ++d) rows.issue(d < count);
+  const int lane = threadIdx.x & 31;
+  const int c0 = (threadIdx.x >> 5) * 256 * V + lane * 8;     // of vector 0
+  // the weights, and a row's terms between its two passes, in registers where these allow
+  constexpr bool KEEP = V == 1;
+  constexpr int K = KEEP ? V : 1;
+  float2 wp[K][4], w[K][4];
+  auto weights = [&](int i) {
+    const E* pw = static_cast<const E*>(a.post_weight);
+    load_weights(pw ? pw + c0 + i * 256 : pw, rows.in[i], wp[KEEP ? i : 0]);
+    if (NEXT) load_weights(static_cast<const E*>(a.weight) + c0 + i * 256, rows.in[i], w[KEEP ? i : 0]);
+  };
+  if (KEEP) weights(0);
   float2 dw[NEXT ? V : 1][4], dwp[V][4];
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dwp[i][j] = dw[NEXT ? i : 0][j] = make_float2(0.f, 0.f);
   const float inv_H = 1.f / static_cast<float>(H);
-  const int lane = threadIdx.x & 31;
+  const int64_t at0 = static_cast<int64_t>(blockIdx.x) * H + c0;
+  E *dy = static_cast<E*>(a.dy) + at0, *d_residual = static_cast<E*>(a.d_residual) + at0;
+  const float2 scale2 = make_float2(a.scale, a.scale);
   // 1 / rms and gate of 32 rows, one per lane (a load per row would wait for the
   // rows' copies)
   float rstds = 0.f, posts = 1.f, gates = 1.f;
-  int stage = 0, flip = 0, turn = 0;
-  for (int64_t row = blockIdx.x; row < T; row += gridDim.x, flip ^= 1) {
-    const int64_t base = row * H;
-    if ((turn & 31) == 0) {
-      const int64_t mine = row + static_cast<int64_t>(lane) * gridDim.x;
-      if (mine < T) {
-        if (NEXT) rstds = __ldg(a.rstd + mine);
-        if (a.rstd_post) posts = __ldg(a.rstd_post + mine);
-        if (a.gate) gates = __ldg(a.gate + mine);
-      }
+  for (int row = 0; row < count; ++row) {
+    const int flip = row & 1;
+    if ((row & 31) == 0 && row + lane < count) {
+      const int64_t mine = blockIdx.x + static_cast<int64_t>(row + lane) * gridDim.x;
+      if (NEXT) rstds = __ldg(a.rstd + mine);
+      if (a.rstd_post) posts = __ldg(a.rstd_post + mine);
+      if (a.gate) gates = __ldg(a.gate + mine);
     }
-    const float rs = NEXT ? __shfl_sync(0xffffffffu, rstds, turn & 31) : 0.f;
-    const float rs_y = __shfl_sync(0xffffffffu, posts, turn & 31);
-    const float gate = __shfl_sync(0xffffffffu, gates, turn & 31);
-    ++turn;
-    if (D > 0) {
-      rows.wait();
-      rows.issue(stage == 0 ? D - 1 : stage - 1, row + static_cast<int64_t>(D - 1) * gridDim.x, T);
-    }
+    const float rs = NEXT ? __shfl_sync(0xffffffffu, rstds, row & 31) : 0.f;
+    const float rs_y = __shfl_sync(0xffffffffu, posts, row & 31);
+    const float gate = __shfl_sync(0xffffffffu, gates, row & 31);
+    rows.wait();
+    rows.issue(row + D - 1 < count);
     const float2 rs2 = make_float2(rs, rs), rs_y2 = make_float2(rs_y, rs_y);
-    float2 u[V][4], rhat[NEXT ? V : 1][4], yhat[V][4];
+    Raw8<E> ry[V], rt[V], rn[NEXT ? V : 1], rr[NEXT ? V : 1];
+    float2 u[4], rhat[4], yhat[4];
+    // u = d_total + rs dn weight, rhat, yhat of vector i
+    auto terms = [&](int i) {
+      const int k = NEXT ? i : 0;
+      if (!KEEP) weights(i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        yhat[j] = mul2(ry[i].pair(j), rs_y2);
+        u[j] = rt[i].pair(j);
+        if (NEXT) {
+          rhat[j] = mul2(rr[k].pair(j), rs2);
+          u[j] = fma2(rs2, mul2(rn[k].pair(j), w[0][j]), u[j]);
+        }
+      }
+    };
     float2 s1 = make_float2(0.f, 0.f), s2 = s1, s3 = s1;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
-      if (c < H) {
-        Raw8<E> ry, rt, rn, rr, w, wp;
-        rows.take(stage, 0, i, row, c, ry);
-        if (a.d_total) rows.take(stage, 1, i, row, c, rt);
-        if (NEXT) {
-          rows.take(stage, N - 2, i, row, c, rn);
-          rows.take(stage, N - 1, i, row, c, rr);
-          w.load(weight + c);
-        }
-        if (post_weight) wp.load(post_weight + c);
+      const int k = NEXT ? i : 0;
+      rows.take(0, i, ry[i]);
+      rows.take(1, i, rt[i]);
+      if (NEXT) {
+        rows.take(N - 2, i, rn[k]);
+        rows.take(N - 1, i, rr[k]);
+      }
+      terms(i);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          yhat[i][j] = mul2(ry.pair(j), rs_y2);
-          const float2 q = post_weight ? mul2(yhat[i][j], wp.pair(j)) : yhat[i][j];
-          float2 uj = a.d_total ? rt.pair(j) : make_float2(0.f, 0.f);
-          if (NEXT) {
-            const float2 dn = rn.pair(j);
-            const float2 v = mul2(dn, w.pair(j));
-            const float2 rh = mul2(rr.pair(j), rs2);
-            rhat[NEXT ? i : 0][j] = rh;
-            uj = fma2(rs2, v, uj);
-            s1 = fma2(v, rh, s1);
-            s3 = fma2(rh, q, s3);
-            dw[NEXT ? i : 0][j] = fma2(dn, rh, dw[NEXT ? i : 0][j]);
-          }
-          s2 = fma2(uj, q, s2);
-          u[i][j] = uj;
+      for (int j = 0; j < 4; ++j) {
+        const float2 q = mul2(yhat[j], wp[0][j]);
+        if (NEXT) {
+          const float2 g = mul2(rn[k].pair(j), rhat[j]);
+          s1 = fma2(g, w[0][j], s1);
+          s3 = fma2(rhat[j], q, s3);
+          dw[k][j].x += g.x, dw[k][j].y += g.y;
         }
+        s2 = fma2(u[j], q, s2);
       }
     }
-    if (D > 0) stage = stage + 1 == D ? 0 : stage + 1;
-    float sums[3] = {s2.x + s2.y, s1.x + s1.y, s3.x + s3.y};
-    block_sums<NEXT ? 3 : 1>(sums, part[flip]);
-    const float rsm = NEXT ? rs * sums[1] * inv_H : 0.f;
-    const float dot = NEXT ? fmaf(-rsm, sums[2], sums[0]) : sums[0];
-    if (a.d_gate && threadIdx.x == 0) a.d_gate[row] = dot;
+    rows.next();
+    float m = 0.f, dot;
+    if (NEXT) {
+      const float4 s = block_sum4(make_float4(s1.x + s1.y, s2.x + s2.y, s3.x + s3.y, 0.f), part[flip]);
+      m = rs * s.x * inv_H;
+      dot = fmaf(-m, s.z, s.y);
+    } else {
+      dot = block_sum(s2.x + s2.y, part[flip]);
+    }
+    if (a.d_gate && threadIdx.x == 0) a.d_gate[blockIdx.x + static_cast<int64_t>(row) * gridDim.x] = dot;
     const float back = a.rstd_post ? -gate * dot * inv_H : 0.f;
-    const float2 rsm2 = make_float2(-rsm, -rsm), gate2 = make_float2(gate, gate), back2 = make_float2(back, back);
-    const float2 scale2 = make_float2(a.scale, a.scale);
+    const float2 m2 = make_float2(-m, -m), gate2 = make_float2(gate, gate), back2 = make_float2(back, back);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
-      if (c < H) {
-        Raw8<E> wp;
-        if (post_weight) wp.load(post_weight + c);
-        float oy[8], orr[8];
+      if (!KEEP) terms(i);
+      float2 oy[4], od[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 dr = NEXT ? fma2(rsm2, rhat[NEXT ? i : 0][j], u[i][j]) : u[i][j];
-          const float2 dres = mul2(scale2, dr);
-          const float2 dp = mul2(gate2, dr);
-          dwp[i][j] = fma2(dp, yhat[i][j], dwp[i][j]);
-          const float2 dpw = post_weight ? mul2(dp, wp.pair(j)) : dp;
-          const float2 dy = mul2(rs_y2, fma2(back2, yhat[i][j], dpw));
-          oy[2 * j] = dy.x, oy[2 * j + 1] = dy.y;
-          orr[2 * j] = dres.x, orr[2 * j + 1] = dres.y;
-        }
-        store8(static_cast<E*>(a.dy) + base + c, oy);
-        store8(static_cast<E*>(a.d_residual) + base + c, orr);
+      for (int j = 0; j < 4; ++j) {
+        const float2 dr = NEXT ? fma2(m2, rhat[j], u[j]) : u[j];
+        od[j] = mul2(scale2, dr);
+        const float2 dp = mul2(gate2, dr);
+        dwp[i][j] = fma2(dp, yhat[j], dwp[i][j]);
+        oy[j] = mul2(rs_y2, fma2(back2, yhat[j], mul2(dp, wp[0][j])));
+      }
+      if (rows.in[i]) {
+        store8(dy + i * 256, &oy[0].x);
+        store8(d_residual + i * 256, &od[0].x);
       }
     }
+    const int64_t step = static_cast<int64_t>(gridDim.x) * H;
+    dy += step, d_residual += step;
   }
   if (a.part) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (threadIdx.x + i * blockDim.x) * 8;
-      if (c < H) {
-        const int64_t at = static_cast<int64_t>(blockIdx.x) * H + c;
+    for (int i = 0; i < V; ++i)
+      if (rows.in[i]) {
+        const int64_t at = static_cast<int64_t>(blockIdx.x) * H + c0 + i * 256;
         if (NEXT) store8(a.part + at, &dw[NEXT ? i : 0][0].x);
         store8(a.part + static_cast<int64_t>(gridDim.x) * H + at, &dwp[i][0].x);
       }
-    }
   }
 }
 
@@ -287,50 +446,77 @@ __global__ void __launch_bounds__(1024) join_dweight_kernel(const float* __restr
   if (lane == 0 && blockIdx.x * 32 + grp < H) out[blockIdx.x * 32 + grp] = t;
 }
 
-template <typename E, int OUT, int V>
-cudaError_t launch_join_fwd_v(const JoinFwd& a, int threads, int sms, cudaStream_t st) {
-  const NormLaunch l = norm_launch(a.T, threads, RowRing<E, 2, V, kAhead>::bytes(threads), kThreadsPerSm, sms);
-  if (l.ring) {
-    static std::atomic<uint64_t> ready{0};
-    const cudaError_t e = allow_smem(join_fwd_kernel<E, OUT, V, kAhead>, ready);
-    if (e != cudaSuccess) return e;
-    join_fwd_kernel<E, OUT, V, kAhead><<<l.blocks, l.threads, l.smem, st>>>(a);
-  } else {
-    join_fwd_kernel<E, OUT, V, 0><<<l.blocks, l.threads, 0, st>>>(a);
-  }
+// A launch: threads of V vectors each, and blocks.  The ring needs a few rows per block
+// to pay.
+struct JoinLaunch {
+  int threads, blocks, smem;
+};
+JoinLaunch join_launch(int64_t T, int H, int v, int ring_per_warp, int threads_per_sm, int most, int sms) {
+  JoinLaunch l;
+  const int warps = (H + 256 * v - 1) / (256 * v);
+  l.threads = 32 * warps;
+  l.smem = ring_per_warp * warps;
+  const int per_sm = std::min({l.smem <= kRingPerSm ? kRingPerSm / l.smem : 0, std::max(1, threads_per_sm / l.threads), most});
+  l.blocks = l.threads > 1024 ? 0 : static_cast<int>(std::min<int64_t>(T, static_cast<int64_t>(sms) * per_sm));
+  return l;
+}
+
+template <typename E, int OUT, int V, int MAXT>
+cudaError_t launch_join_ring(const JoinFwd& a, const JoinLaunch& l, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(join_fwd_kernel<E, OUT, V, kAhead, MAXT>, ready);
+  if (e != cudaSuccess) return e;
+  join_fwd_kernel<E, OUT, V, kAhead, MAXT><<<l.blocks, l.threads, l.smem, st>>>(a);
   return cudaGetLastError();
 }
 
 template <typename E, int OUT>
 cudaError_t launch_join_fwd(const JoinFwd& a, int sms, cudaStream_t st) {
-  const RowShape s = row_shape(a.H);
-  if (s.vecs == 1) return launch_join_fwd_v<E, OUT, 1>(a, s.threads, sms, st);
-  if (s.vecs == 2) return launch_join_fwd_v<E, OUT, 2>(a, s.threads, sms, st);
-  return launch_join_fwd_v<E, OUT, 4>(a, s.threads, sms, st);
-}
-
-template <typename E, bool NEXT, int V>
-cudaError_t launch_join_bwd_v(const JoinBwd& a, int threads, int sms, int* blocks, cudaStream_t st) {
-  const NormLaunch l = norm_launch(a.T, threads, RowRing<E, NEXT ? 4 : 2, V, kAhead>::bytes(threads), kThreadsPerSm, sms);
-  *blocks = l.blocks;
-  if (l.ring) {
-    static std::atomic<uint64_t> ready{0};
-    const cudaError_t e = allow_smem(join_bwd_kernel<E, NEXT, V, kAhead>, ready);
-    if (e != cudaSuccess) return e;
-    join_bwd_kernel<E, NEXT, V, kAhead><<<l.blocks, l.threads, l.smem, st>>>(a);
-  } else {
-    join_bwd_kernel<E, NEXT, V, 0><<<l.blocks, l.threads, 0, st>>>(a);
+  const int v = a.H <= 512 ? 1 : 2;
+  const bool small = a.H <= 256 * 8 * v;      // at most 256 threads, more registers for each
+  const JoinLaunch l = join_launch(a.T, a.H, v, RowStream<E, 2, 1, kAhead>::bytes(32) * v, small ? JTH : 1024, 24, sms);
+  if (l.blocks > 0 && a.T > l.blocks) {
+    if (v == 1) return launch_join_ring<E, OUT, 1, 256>(a, l, st);
+    if (small) return launch_join_ring<E, OUT, 2, 256>(a, l, st);
+    return launch_join_ring<E, OUT, 2, 1024>(a, l, st);
   }
+  // few rows: a block for each, as many threads as there are
+  const unsigned T = static_cast<unsigned>(a.T);
+  const int warps = (a.H + 255) / 256;
+  if (warps <= 32)
+    join_fwd_kernel<E, OUT, 1, 0, 1024><<<T, 32 * warps, 0, st>>>(a);
+  else if (warps <= 64)
+    join_fwd_kernel<E, OUT, 2, 0, 1024><<<T, 32 * ((warps + 1) / 2), 0, st>>>(a);
+  else
+    join_fwd_kernel<E, OUT, 4, 0, 1024><<<T, 32 * ((warps + 3) / 4), 0, st>>>(a);
   return cudaGetLastError();
 }
 
 // *blocks: of the launch, each of which leaves its sums in a.part.
+template <typename E, bool NEXT, int V, int MAXT>
+cudaError_t launch_join_bwd_v(const JoinBwd& a, int sms, int* blocks, cudaStream_t st) {
+  JoinLaunch l = join_launch(a.T, a.H, V, RowStream<E, NEXT ? 4 : 2, V, kAhead>::bytes(32), JTB, 8, sms);
+  if (l.blocks > 0 && a.T > l.blocks) {
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = allow_smem(join_bwd_kernel<E, NEXT, V, kAhead, MAXT>, ready);
+    if (e != cudaSuccess) return e;
+    join_bwd_kernel<E, NEXT, V, kAhead, MAXT><<<l.blocks, l.threads, l.smem, st>>>(a);
+  } else {
+    const int per_sm = std::max(1, std::min(8, 1024 / l.threads));
+    l.blocks = static_cast<int>(std::min<int64_t>(a.T, static_cast<int64_t>(sms) * per_sm));
+    join_bwd_kernel<E, NEXT, V, 0, MAXT><<<l.blocks, l.threads, 0, st>>>(a);
+  }
+  *blocks = l.blocks;
+  return cudaGetLastError();
+}
+
 template <typename E, bool NEXT>
 cudaError_t launch_join_bwd(const JoinBwd& a, int sms, int* blocks, cudaStream_t st) {
-  const RowShape s = row_shape(a.H);
-  if (s.vecs == 1) return launch_join_bwd_v<E, NEXT, 1>(a, s.threads, sms, blocks, st);
-  if (s.vecs == 2) return launch_join_bwd_v<E, NEXT, 2>(a, s.threads, sms, blocks, st);
-  return launch_join_bwd_v<E, NEXT, 4>(a, s.threads, sms, blocks, st);
+  const int warps = (a.H + 255) / 256;
+  if (warps <= 12) return launch_join_bwd_v<E, NEXT, 1, 384>(a, sms, blocks, st);
+  if (warps <= 32) return launch_join_bwd_v<E, NEXT, 1, 1024>(a, sms, blocks, st);
+  if (warps <= 64) return launch_join_bwd_v<E, NEXT, 2, 1024>(a, sms, blocks, st);
+  return launch_join_bwd_v<E, NEXT, 4, 1024>(a, sms, blocks, st);
 }
 
 bool join_dims_ok(int64_t T, int32_t H, int32_t dtype) {

@@ -23,6 +23,11 @@ struct Raw8 {
 #pragma unroll
     for (int i = 0; i < W; ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
   }
+  __device__ __forceinline__ void ones() {
+    const uint32_t w = sizeof(E) == 4 ? 0x3f800000u : 0x3f803f80u;
+#pragma unroll
+    for (int i = 0; i < W; ++i) u[i] = make_uint4(w, w, w, w);
+  }
   __device__ __forceinline__ float get(int j) const {
     const uint32_t* w = &u[0].x;
     if (sizeof(E) == 4) return __uint_as_float(w[j]);
@@ -31,98 +36,65 @@ struct Raw8 {
   __device__ __forceinline__ float2 pair(int j) const { return make_float2(get(2 * j), get(2 * j + 1)); }
 };
 
-// The rows that a block walks, N arrays of them, D - 1 rows ahead of their use: each
-// warp copies its own columns asynchronously into its own part of shared memory and
-// reads them back itself, so no barrier of the block is needed.  A copy instruction
-// covers 512 contiguous bytes (in fp32 a lane copies other pieces than it reads: with
-// its own, 32 bytes apart, the backward at 8192 x 2880 takes 100 us instead of 74).
-// D = 0: loads at their use.
-template <typename E, int N, int V, int D>
-struct RowRing {
-  static constexpr int W = Raw8<E>::W;
-  static constexpr int bytes(int threads) { return D * N * V * W * 16 * threads; }
-  uint4* ring;
-  const E* src[N];   // null: absent
-  int H;
-  // Piece p of the warp's 32 W in vector i of array n.
-  __device__ __forceinline__ uint4* slot(int stage, int n, int i, int p) const {
-    if (W == 1) return ring + ((stage * N + n) * V + i) * blockDim.x + threadIdx.x;
-    return ring + ((stage * N + n) * V + i) * W * blockDim.x + (threadIdx.x & ~31u) * W + p;
-  }
-  __device__ __forceinline__ void issue(int stage, int64_t row, int64_t T) {
-    if (D == 0) return;
-    if (row < T) {
-      const int lane = threadIdx.x & 31;
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int c0 = ((threadIdx.x & ~31u) + i * blockDim.x) * 8;   // the warp's first column
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            const int p = w * 32 + lane, c = W == 1 ? (threadIdx.x + i * blockDim.x) * 8 : c0 + p * (8 / W);
-            if (src[n] && c < H) cp_async16(smem_u32(slot(stage, n, i, p)), src[n] + row * H + c, 16);
-          }
-        }
-    }
-    cp_async_commit();
-  }
-  // The oldest row's copies are there, and may be read.
-  __device__ __forceinline__ void wait() const {
-    cp_async_wait<D >= 2 ? D - 2 : 0>();
-    if (W > 1) __syncwarp();
-  }
-  __device__ __forceinline__ void take(int stage, int n, int i, int64_t row, int c, Raw8<E>& r) const {
-    if (D == 0) {
-      r.load(src[n] + row * H + c);
-      return;
-    }
-#pragma unroll
-    for (int w = 0; w < W; ++w) r.u[w] = *slot(stage, n, i, (threadIdx.x & 31) * W + w);
-  }
-};
-
-// Sums of K values over the block, the same in every thread, in a fixed order.
-// `part` may be reused after the next barrier.
-template <int K>
-__device__ __forceinline__ void block_sums(float (&v)[3], float (*part)[32]) {
-#pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
-  const int warps = blockDim.x >> 5;
-  if (warps == 1) return;
+// Four sums over the warp at once: two exchanges leave each lane one of the four
+// (lane & 3: x, z, y, w), three butterflies add it up, six shuffles in place of twenty.
+__device__ __forceinline__ float warp_sum4(const float4& v) {
   const int lane = threadIdx.x & 31;
-  if (lane == 0)
+  const bool odd = lane & 1, high = lane & 2;
+  float a = odd ? v.z : v.x, b = odd ? v.w : v.y;
+  a += __shfl_xor_sync(0xffffffffu, odd ? v.x : v.z, 1);
+  b += __shfl_xor_sync(0xffffffffu, odd ? v.y : v.w, 1);
+  float s = high ? b : a;
+  s += __shfl_xor_sync(0xffffffffu, high ? a : b, 2);
 #pragma unroll
-    for (int k = 0; k < K; ++k) part[k][threadIdx.x >> 5] = v[k];
-  __syncthreads();
+  for (int d = 4; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  return s;
+}
+
+// Four sums over the block, the same in every thread, in a fixed order.  `part` holds
+// 128 floats and may be reused after the next barrier.
+__device__ __forceinline__ float4 block_sum4(const float4& v, float* part) {
+  float s = warp_sum4(v);
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  if (warps > 1) {
+    if (lane < 4) part[(threadIdx.x >> 5) * 4 + lane] = s;
+    __syncthreads();
+    s = 0.f;
+    for (int i = lane; i < warps * 4; i += 32) s += part[i];
 #pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = warp_sum(lane < warps ? part[k][lane] : 0.f);
+    for (int d = 4; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  }
+  return make_float4(__shfl_sync(0xffffffffu, s, 0), __shfl_sync(0xffffffffu, s, 2),
+                     __shfl_sync(0xffffffffu, s, 1), __shfl_sync(0xffffffffu, s, 3));
+}
+
+// The largest of three, NaN if one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // Eight of a row's values as e4m3 codes with their block's scale byte, which four
 // neighbouring threads (32 columns, inside or outside the row together) find by two
-// shuffles: all lanes of the warp call it, `in` where the columns exist.
-__device__ __forceinline__ void store_e4m3(const float (&o)[8], bool in, uint8_t* codes, uint8_t* scale) {
-  uint32_t amax = 0;
-  if (in) {
+// shuffles: all lanes of the warp call it, with zeros where the columns do not exist
+// (`in` is false).
+__device__ __forceinline__ void store_e4m3(const float2 (&o)[4], bool in, uint8_t* codes, uint8_t* scale) {
+  float top = max3_nan(fabsf(o[0].x), fabsf(o[0].y), 0.f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(o[j]) & 0x7fffffffu);
-  }
+  for (int j = 1; j < 4; ++j) top = max3_nan(top, fabsf(o[j].x), fabsf(o[j].y));
+  uint32_t amax = __float_as_uint(top) & 0x7fffffffu;
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  if (!in) return;
   const uint32_t sb = mx_scale_byte(amax, 0x600000u, 8);
   const float inv = mx_inv_scale(sb);
-  uint2 code;
+  const float2 inv2 = make_float2(inv, inv);
   uint32_t h[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float2 p = make_float2(o[2 * j] * inv, o[2 * j + 1] * inv);
-    if (sb == 255u) p = make_float2(0.f, 0.f);
-    h[j] = __nv_cvt_float2_to_fp8x2(p, __NV_SATFINITE, __NV_E4M3);
-  }
-  code.x = h[0] | (h[1] << 16);
-  code.y = h[2] | (h[3] << 16);
+  for (int j = 0; j < 4; ++j) h[j] = __nv_cvt_float2_to_fp8x2(mul2(o[j], inv2), __NV_SATFINITE, __NV_E4M3);
+  uint2 code = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  if (sb == 255u) code = make_uint2(0u, 0u);      // a block that is NaN
+  if (!in) return;
   *reinterpret_cast<uint2*>(codes) = code;
   if ((threadIdx.x & 3) == 0) *scale = static_cast<uint8_t>(sb);
 }
