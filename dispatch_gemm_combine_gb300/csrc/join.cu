@@ -25,12 +25,14 @@
 #include "rows.cuh"
 #include "vec.cuh"
 
-#ifndef JTH
-#define JTH 512
-#define JTB 1024
-#endif
 namespace moe {
 namespace {
+
+__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, uint32_t on) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst),
+               "l"(src), "r"(on)
+               : "memory");
+}
 
 // The rows that a block walks (blockIdx.x, + gridDim.x, ..), N arrays of them, D - 1 rows
 // ahead of their use.  A warp owns 256 V neighbouring columns, vector i of a lane is
@@ -49,20 +51,25 @@ struct RowStream {
   int64_t step;         // from one of the block's rows to the next
   uint32_t ring;        // this warp's part
   int put, get;         // stages
-  uint32_t copies;      // a bit for each piece of a row that exists
+  uint32_t copies;      // a bit for each piece of the arrays' rows that exists
   bool in[V];           // the lane's vectors exist
+  uint32_t present;     // a bit for each array that exists
 
   __device__ __forceinline__ void init(uint4* smem, const E* const (&p)[N], int H) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int first = warp * 256 * V;
-    copies = 0;
+    uint32_t row = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       in[i] = first + i * 256 + lane * 8 < H;
 #pragma unroll
       for (int w = 0; w < W; ++w)
-        if (first + i * 256 + (w * 32 + lane) * (8 / W) < H) copies |= 1u << (i * W + w);
+        if (first + i * 256 + (w * 32 + lane) * (8 / W) < H) row |= 1u << (i * W + w);
     }
+    copies = present = 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (p[n]) present |= 1u << n, copies |= row << (n * V * W);
     const int own = D > 0 ? lane * 16 : lane * 16 * W;
 #pragma unroll
     for (int n = 0; n < N; ++n)
@@ -82,10 +89,9 @@ struct RowStream {
       const uint32_t dst = ring + put * WARP_BYTES + (threadIdx.x & 31) * 16;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        if (!src[n]) continue;
 #pragma unroll
         for (int i = 0; i < V * W; ++i)
-          if (copies & (1u << i)) cp_async16(dst + (n * V * W + i) * 512, src[n] + i * 512, 16);
+          cp_async16_if(dst + (n * V * W + i) * 512, src[n] + i * 512, copies & (1u << (n * V * W + i)));
         src[n] += step;
       }
       put = put + 1 == D ? 0 : put + 1;
@@ -107,7 +113,7 @@ struct RowStream {
                      : "=r"(r.u[w].x), "=r"(r.u[w].y), "=r"(r.u[w].z), "=r"(r.u[w].w) : "r"(at) : "memory");
       } else {
         r.u[w] = make_uint4(0u, 0u, 0u, 0u);
-        if (src[n] && in[i]) r.u[w] = *reinterpret_cast<const uint4*>(src[n] + i * 512 * W + w * 16);
+        if ((present >> n & 1) && in[i]) r.u[w] = *reinterpret_cast<const uint4*>(src[n] + i * 512 * W + w * 16);
       }
     }
   }
@@ -117,8 +123,7 @@ struct RowStream {
       get = get + 1 == D ? 0 : get + 1;
     } else {
 #pragma unroll
-      for (int n = 0; n < N; ++n)
-        if (src[n]) src[n] += step;
+      for (int n = 0; n < N; ++n) src[n] += step;
     }
   }
 };
@@ -165,7 +170,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) join_fwd_kernel(con
   const int c0 = (threadIdx.x >> 5) * 256 * V + lane * 8;     // of vector 0
   // the weights, and a row's terms between its two passes, in registers where these
   // allow (twice unpacked, a vector takes a third more instructions)
-  constexpr bool KEEP = V == 1 || MAXT <= 256;
+  constexpr bool KEEP = V == 1 || MAXT <= 512;
   constexpr int K = KEEP ? V : 1;
   float2 wp[K][4], w[K][4];
   auto weights = [&](int i) {
@@ -198,8 +203,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) join_fwd_kernel(con
       if (!KEEP) weights(i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        t[k][j] = mul2(scale2, rr[i].pair(j));
-        q[k][j] = mul2(ry[i].pair(j), wp[k][j]);
+        t[k][j] = __fmul2_rn(scale2, rr[i].pair(j));
+        q[k][j] = __fmul2_rn(ry[i].pair(j), wp[k][j]);
       }
     };
     float2 yy = make_float2(0.f, 0.f), tt = yy, tq = yy, qq = yy;
@@ -212,18 +217,18 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) join_fwd_kernel(con
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 y = ry[i].pair(j);
-        yy = fma2(y, y, yy);
+        yy = __ffma2_rn(y, y, yy);
         if (OUT != kNoNorm) {
-          tt = fma2(t[k][j], t[k][j], tt);
-          tq = fma2(t[k][j], q[k][j], tq);
-          qq = fma2(q[k][j], q[k][j], qq);
+          tt = __ffma2_rn(t[k][j], t[k][j], tt);
+          tq = __ffma2_rn(t[k][j], q[k][j], tq);
+          qq = __ffma2_rn(q[k][j], q[k][j], qq);
         }
       }
     }
     rows.next();
     float4 s = make_float4(yy.x + yy.y, tt.x + tt.y, tq.x + tq.y, qq.x + qq.y);
     if (OUT != kNoNorm)
-      s = block_sum4(s, part[flip]);
+      s = block_sum4<MAXT>(s, part[flip]);
     else if (a.post_norm)
       s.x = block_sum(s.x, part[flip]);
     const float rs_y = a.post_norm ? rsqrtf(s.x * inv_H + a.eps) : 1.f;
@@ -242,7 +247,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) join_fwd_kernel(con
           if (!KEEP) terms(i);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 r = fma2(f2, q[KEEP ? i : 0][j], t[KEEP ? i : 0][j]);
+            const float2 r = __ffma2_rn(f2, q[KEEP ? i : 0][j], t[KEEP ? i : 0][j]);
             if (rows.in[i]) ss = fmaf(r.x, r.x, fmaf(r.y, r.y, ss));     // (an infinite f makes NaN of zeros)
           }
         }
@@ -264,11 +269,11 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) join_fwd_kernel(con
       float2 r[4], n[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        r[j] = fma2(f2, q[k][j], t[k][j]);
-        if (OUT != kNoNorm) n[j] = mul2(mul2(r[j], rs2), w[k][j]);
+        r[j] = __ffma2_rn(f2, q[k][j], t[k][j]);
+        if (OUT != kNoNorm) n[j] = __fmul2_rn(__fmul2_rn(r[j], rs2), w[k][j]);
       }
-      if (rows.in[i]) store8(total + i * 256, &r[0].x);
-      if (OUT == kSameType && rows.in[i]) store8(reinterpret_cast<E*>(n_out) + i * 256, &n[0].x);
+      store8_if(total + i * 256, r, rows.in[i]);
+      if (OUT == kSameType) store8_if(reinterpret_cast<E*>(n_out) + i * 256, n, rows.in[i]);
       if (OUT == kE4m3) store_e4m3(n, rows.in[i], reinterpret_cast<uint8_t*>(n_out) + i * 256, s_out + i * 8);
     }
     const int64_t step = static_cast<int64_t>(gridDim.x) * H;
@@ -350,11 +355,11 @@ __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 1) join_bwd_kernel(con
       if (!KEEP) weights(i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        yhat[j] = mul2(ry[i].pair(j), rs_y2);
+        yhat[j] = __fmul2_rn(ry[i].pair(j), rs_y2);
         u[j] = rt[i].pair(j);
         if (NEXT) {
-          rhat[j] = mul2(rr[k].pair(j), rs2);
-          u[j] = fma2(rs2, mul2(rn[k].pair(j), w[0][j]), u[j]);
+          rhat[j] = __fmul2_rn(rr[k].pair(j), rs2);
+          u[j] = __ffma2_rn(rs2, __fmul2_rn(rn[k].pair(j), w[0][j]), u[j]);
         }
       }
     };
@@ -371,20 +376,20 @@ __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 1) join_bwd_kernel(con
       terms(i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 q = mul2(yhat[j], wp[0][j]);
+        const float2 q = __fmul2_rn(yhat[j], wp[0][j]);
         if (NEXT) {
-          const float2 g = mul2(rn[k].pair(j), rhat[j]);
-          s1 = fma2(g, w[0][j], s1);
-          s3 = fma2(rhat[j], q, s3);
-          dw[k][j].x += g.x, dw[k][j].y += g.y;
+          const float2 g = __fmul2_rn(rn[k].pair(j), rhat[j]);
+          s1 = __ffma2_rn(g, w[0][j], s1);
+          s3 = __ffma2_rn(rhat[j], q, s3);
+          dw[k][j] = __ffma2_rn(rn[k].pair(j), rhat[j], dw[k][j]);
         }
-        s2 = fma2(u[j], q, s2);
+        s2 = __ffma2_rn(u[j], q, s2);
       }
     }
     rows.next();
     float m = 0.f, dot;
     if (NEXT) {
-      const float4 s = block_sum4(make_float4(s1.x + s1.y, s2.x + s2.y, s3.x + s3.y, 0.f), part[flip]);
+      const float4 s = block_sum4<MAXT>(make_float4(s1.x + s1.y, s2.x + s2.y, s3.x + s3.y, 0.f), part[flip]);
       m = rs * s.x * inv_H;
       dot = fmaf(-m, s.z, s.y);
     } else {
@@ -399,16 +404,14 @@ __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 1) join_bwd_kernel(con
       float2 oy[4], od[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 dr = NEXT ? fma2(m2, rhat[j], u[j]) : u[j];
-        od[j] = mul2(scale2, dr);
-        const float2 dp = mul2(gate2, dr);
-        dwp[i][j] = fma2(dp, yhat[j], dwp[i][j]);
-        oy[j] = mul2(rs_y2, fma2(back2, yhat[j], mul2(dp, wp[0][j])));
+        const float2 dr = NEXT ? __ffma2_rn(m2, rhat[j], u[j]) : u[j];
+        od[j] = __fmul2_rn(scale2, dr);
+        const float2 dp = __fmul2_rn(gate2, dr);
+        dwp[i][j] = __ffma2_rn(dp, yhat[j], dwp[i][j]);
+        oy[j] = __fmul2_rn(rs_y2, __ffma2_rn(back2, yhat[j], __fmul2_rn(dp, wp[0][j])));
       }
-      if (rows.in[i]) {
-        store8(dy + i * 256, &oy[0].x);
-        store8(d_residual + i * 256, &od[0].x);
-      }
+      store8_if(dy + i * 256, oy, rows.in[i]);
+      store8_if(d_residual + i * 256, od, rows.in[i]);
     }
     const int64_t step = static_cast<int64_t>(gridDim.x) * H;
     dy += step, d_residual += step;
@@ -446,8 +449,14 @@ __global__ void __launch_bounds__(1024) join_dweight_kernel(const float* __restr
   if (lane == 0 && blockIdx.x * 32 + grp < H) out[blockIdx.x * 32 + grp] = t;
 }
 
-// A launch: threads of V vectors each, and blocks.  The ring needs a few rows per block
-// to pay.
+// Threads of a launch's resident blocks per SM, where one block does not have more: fewer
+// threads with more registers beat more threads (forward of 16384 x 4096 with e4m3: 512
+// threads 76 us, 768 of at most 85 registers 124; backward of 16384 x 4096: 768 threads
+// 125 us, 1024 130, of 32768 x 1024 74 and 82).
+constexpr int kFwdThreads = 512;
+constexpr int kBwdThreads = 768;
+
+// Threads of v vectors each, and blocks.  The ring needs a few rows per block to pay.
 struct JoinLaunch {
   int threads, blocks, smem;
 };
@@ -472,12 +481,15 @@ cudaError_t launch_join_ring(const JoinFwd& a, const JoinLaunch& l, cudaStream_t
 
 template <typename E, int OUT>
 cudaError_t launch_join_fwd(const JoinFwd& a, int sms, cudaStream_t st) {
+  // two vectors per thread halve what a row costs beside its columns (16384 x 4096 with
+  // e4m3: 147 us with one), four run out of registers (109)
   const int v = a.H <= 512 ? 1 : 2;
-  const bool small = a.H <= 256 * 8 * v;      // at most 256 threads, more registers for each
-  const JoinLaunch l = join_launch(a.T, a.H, v, RowStream<E, 2, 1, kAhead>::bytes(32) * v, small ? JTH : 1024, 24, sms);
+  const bool small = a.H <= 256 * 8 * v, wide = a.H <= 256 * 16 * v;      // at most 256 threads, more registers for each
+  const JoinLaunch l = join_launch(a.T, a.H, v, RowStream<E, 2, 1, kAhead>::bytes(32) * v, small ? kFwdThreads : 1024, 24, sms);
   if (l.blocks > 0 && a.T > l.blocks) {
     if (v == 1) return launch_join_ring<E, OUT, 1, 256>(a, l, st);
     if (small) return launch_join_ring<E, OUT, 2, 256>(a, l, st);
+    if (wide) return launch_join_ring<E, OUT, 2, 512>(a, l, st);
     return launch_join_ring<E, OUT, 2, 1024>(a, l, st);
   }
   // few rows: a block for each, as many threads as there are
@@ -495,7 +507,7 @@ cudaError_t launch_join_fwd(const JoinFwd& a, int sms, cudaStream_t st) {
 // *blocks: of the launch, each of which leaves its sums in a.part.
 template <typename E, bool NEXT, int V, int MAXT>
 cudaError_t launch_join_bwd_v(const JoinBwd& a, int sms, int* blocks, cudaStream_t st) {
-  JoinLaunch l = join_launch(a.T, a.H, V, RowStream<E, NEXT ? 4 : 2, V, kAhead>::bytes(32), JTB, 8, sms);
+  JoinLaunch l = join_launch(a.T, a.H, V, RowStream<E, NEXT ? 4 : 2, V, kAhead>::bytes(32), kBwdThreads, 8, sms);
   if (l.blocks > 0 && a.T > l.blocks) {
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = allow_smem(join_bwd_kernel<E, NEXT, V, kAhead, MAXT>, ready);
@@ -513,9 +525,13 @@ cudaError_t launch_join_bwd_v(const JoinBwd& a, int sms, int* blocks, cudaStream
 template <typename E, bool NEXT>
 cudaError_t launch_join_bwd(const JoinBwd& a, int sms, int* blocks, cudaStream_t st) {
   const int warps = (a.H + 255) / 256;
-  if (warps <= 12) return launch_join_bwd_v<E, NEXT, 1, 384>(a, sms, blocks, st);
-  if (warps <= 32) return launch_join_bwd_v<E, NEXT, 1, 1024>(a, sms, blocks, st);
-  if (warps <= 64) return launch_join_bwd_v<E, NEXT, 2, 1024>(a, sms, blocks, st);
+  // one vector per thread up to 4096 columns; more than 80 registers where one block
+  // per SM is all that the ring or the threads leave room for (8192 x 2880 fp32: 93 us
+  // with up to 128 registers, 109 with 80; bf16, two blocks: 57 and 52)
+  if (warps <= (sizeof(E) == 4 ? 8 : 12)) return launch_join_bwd_v<E, NEXT, 1, 384>(a, sms, blocks, st);
+  if (warps <= 16) return launch_join_bwd_v<E, NEXT, 1, 512>(a, sms, blocks, st);
+  if (warps <= 32) return launch_join_bwd_v<E, NEXT, 2, 512>(a, sms, blocks, st);
+  if (warps <= 64) return launch_join_bwd_v<E, NEXT, 4, 512>(a, sms, blocks, st);
   return launch_join_bwd_v<E, NEXT, 4, 1024>(a, sms, blocks, st);
 }
 

@@ -8,13 +8,14 @@
 //        + sum over the choices j of e: w_j (dw_j - D).
 // The balance loss is the mean of F over the rows, the z-loss that of l^2.
 //
-// One warp per row: the row's logits stay in registers (E <= 1024, so at most 32
-// per lane), so they are read once and d is written once: bound by memory.  The
-// next row's logits are loaded before this one's arithmetic.  The choices'
-// terms go through a row of shared memory per warp (a lane writes its choice's
-// term where the lane that owns the column picks it up); a row that names an expert
-// twice adds its terms one after the other.  Sums over the rows: per warp and block
-// in a fixed order, then one block over all blocks: no atomics.
+// A row's logits stay in the registers of G lanes, PER in each (a warp for more than 128
+// experts, half of one or a quarter for fewer: what a row costs beside its columns is
+// then shared by two or four rows), so they are read once and d is written once.  The
+// next rows' logits are loaded before this one's arithmetic.  The choices' terms go
+// through a row of shared memory (a lane writes its choice's term where the lane that
+// owns the column picks it up); a row that names an expert twice adds its terms one
+// after the other.  Sums over the rows: per warp and block in a fixed order, then one
+// block over all blocks: no atomics.
 #include <algorithm>
 
 #include "abi_internal.h"
@@ -44,15 +45,27 @@ struct RouteBwd {
   int softmax;             // the losses or their gradients are wanted
 };
 
-__device__ __forceinline__ float warp_max(float v) {
+// Over the G lanes of a row.
+template <int G>
+__device__ __forceinline__ float row_max(float v) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  for (int d = G / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
   return v;
 }
-__device__ __forceinline__ float warp_add(float v) {
+// Four sums at once (two exchanges leave each lane one of the four), in every lane.
+template <int G>
+__device__ __forceinline__ float4 row_sum4(const float4& v) {
+  const int lane = threadIdx.x & 31;
+  const bool odd = lane & 1, high = lane & 2;
+  float a = odd ? v.z : v.x, b = odd ? v.w : v.y;
+  a += __shfl_xor_sync(0xffffffffu, odd ? v.x : v.z, 1);
+  b += __shfl_xor_sync(0xffffffffu, odd ? v.y : v.w, 1);
+  float s = high ? b : a;
+  s += __shfl_xor_sync(0xffffffffu, high ? a : b, 2);
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  return v;
+  for (int d = 4; d < G; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+  return make_float4(__shfl_sync(0xffffffffu, s, 0, G), __shfl_sync(0xffffffffu, s, 2, G),
+                     __shfl_sync(0xffffffffu, s, 1, G), __shfl_sync(0xffffffffu, s, 3, G));
 }
 
 // A running sum with what its roundings took (many rows per warp); beyond fp32's
@@ -66,154 +79,166 @@ struct Sum {
   }
 };
 
-// PER columns per lane.  VEC: groups of four, 4 (lane + 32 i) ..; otherwise
-// lane + 32 i.
-template <int PER, bool VEC>
+// PER columns in each of a row's G lanes.  VEC: groups of four, 4 (g + G i) ..; otherwise
+// g + G i.
+template <int G, int PER, bool VEC>
 struct RouteRow {
-  static __device__ __forceinline__ int col(int i, int lane) {
-    return VEC ? 4 * (lane + 32 * (i / 4)) + i % 4 : lane + 32 * i;
+  static __device__ __forceinline__ int col(int i, int g) {
+    return VEC ? 4 * (g + G * (i / 4)) + i % 4 : g + G * i;
   }
-  static __device__ __forceinline__ void load(const float* row, int E, int lane, float fill, float (&v)[PER]) {
-    if (VEC) {
+  static __device__ __forceinline__ void load(const float* row, int E, int g, bool on, float (&v)[PER]) {
+    constexpr int S = VEC ? 4 : 1;
 #pragma unroll
-      for (int i = 0; i < PER; i += 4) {
-        const int c = col(i, lane);
-        float4 q = make_float4(fill, fill, fill, fill);
-        if (c < E) q = __ldg(reinterpret_cast<const float4*>(row + c));
+    for (int i = 0; i < PER; i += S) {
+      const int c = col(i, g);
+      const bool in = on && c < E;
+      if (VEC) {
+        const float4 q = in ? __ldg(reinterpret_cast<const float4*>(row + c))
+                            : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int c = col(i, lane);
-        v[i] = c < E ? __ldg(row + c) : fill;
+      } else {
+        v[i] = in ? __ldg(row + c) : -INFINITY;
       }
     }
   }
-  static __device__ __forceinline__ void store(float* row, int E, int lane, const float (&v)[PER]) {
-    if (VEC) {
+  static __device__ __forceinline__ void store(float* row, int E, int g, bool on, const float (&v)[PER]) {
+    constexpr int S = VEC ? 4 : 1;
 #pragma unroll
-      for (int i = 0; i < PER; i += 4) {
-        const int c = col(i, lane);
-        if (c < E) *reinterpret_cast<float4*>(row + c) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int c = col(i, lane);
-        if (c < E) row[c] = v[i];
+    for (int i = 0; i < PER; i += S) {
+      const int c = col(i, g);
+      if (on && c < E) {
+        if (VEC)
+          *reinterpret_cast<float4*>(row + c) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        else
+          row[c] = v[i];
       }
     }
   }
 };
 
-template <int PER, bool VEC>
+template <int G, int PER, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps) route_bwd_kernel(const RouteBwd a) {
-  using Row = RouteRow<PER, VEC>;
+  using Row = RouteRow<G, PER, VEC>;
+  constexpr int R = 32 / G;      // rows of a warp
   __shared__ __align__(16) float terms[kWarps][32 * PER];
   __shared__ float sums[kWarps][2];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* term = terms[warp];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane % G, sub = lane / G;
+  float* term = terms[warp] + sub * G * PER;
   const bool chosen = a.dw != nullptr;
   const bool softmax = a.softmax != 0;
   if (chosen)
-    for (int i = lane; i < 32 * PER; i += 32) term[i] = 0.f;
+    for (int i = lane; i < 32 * PER; i += 32) terms[warp][i] = 0.f;
   __syncwarp();
   float f[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int c = Row::col(i, lane);
+    const int c = Row::col(i, g);
     f[i] = a.counts && c < a.E ? static_cast<float>(__ldg(a.counts + c)) * a.f_scale : 0.f;
   }
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-  int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  float next[PER];
-  int n_id = -1;
-  float n_w = 0.f, n_dw = 0.f;
-  auto fetch = [&](int64_t row) {
-    if (softmax) Row::load(a.logits + row * a.E, a.E, lane, -INFINITY, next);
-    if (chosen && lane < a.k) {
-      n_id = __ldg(a.idx + row * a.k + lane);
-      n_w = __ldg(a.w + row * a.k + lane);
-      n_dw = __ldg(a.dw + row * a.k + lane);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * R;
+  struct Ahead {
+    float v[PER];
+    int id;
+    float w, dw;
+  };
+  auto fetch = [&](int64_t row, Ahead& n) {
+    const bool on = row < a.T;
+    if (softmax) Row::load(a.logits + row * a.E, a.E, g, on, n.v);
+    n.id = -1, n.w = n.dw = 0.f;
+    if (chosen && on && g < a.k) {
+      n.id = __ldg(a.idx + row * a.k + g);
+      n.w = __ldg(a.w + row * a.k + g);
+      n.dw = __ldg(a.dw + row * a.k + g);
     }
   };
   Sum sum_F, sum_l;
-  if (t < a.T) fetch(t);
-  for (; t < a.T; t += step) {
-    float v[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = next[i];
-    int id = n_id;
-    const float w = n_w, dw = n_dw;
-    if (t + step < a.T) fetch(t + step);
+  // t: this lane's row; `now` holds it, `next` receives the one after
+  auto work = [&](int64_t t, Ahead& now, Ahead& next) {
+    fetch(t + step, next);
+    const bool on = t < a.T;
     float d[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) d[i] = 0.f;
+    float4 s = make_float4(0.f, 0.f, now.w * now.dw, 0.f);
+    float top = 0.f;
     if (softmax) {
-      float top = v[0];
+      top = now.v[0];
 #pragma unroll
-      for (int i = 1; i < PER; ++i) top = fmaxf(top, v[i]);
-      top = warp_max(top);
+      for (int i = 1; i < PER; ++i) top = fmaxf(top, now.v[i]);
+      top = row_max<G>(top);
       if (top == -INFINITY) top = 0.f;      // every expert masked: p = 0
-      float s = 0.f, F = 0.f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        v[i] = expf(v[i] - top);
-        s += v[i];
-        F = fmaf(v[i], f[i], F);
+        now.v[i] = exp2f((now.v[i] - top) * 1.44269504f);
+        s.x += now.v[i];
+        s.y = fmaf(now.v[i], f[i], s.y);
       }
-      s = warp_add(s);
-      F = warp_add(F);
-      // (a row that is NaN has s = NaN, which is not 0: it stays NaN)
-      const float inv = s == 0.f ? 0.f : 1.f / s;
-      const float l = s == 0.f ? 0.f : top + logf(s);
-      F *= inv;
-      sum_F.add(F);
-      sum_l.add(l * l);
-      const float b = a.balance_T * inv, zl = a.z2_T * l * inv;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) d[i] = v[i] * fmaf(b, f[i] - F, zl);
     }
+    s = row_sum4<G>(s);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) d[i] = 0.f;
     if (chosen) {
-      const bool mine = lane < a.k;
-      if (mine && static_cast<unsigned>(id) >= static_cast<unsigned>(a.E)) {
+      const float D = s.z, c = now.w * (now.dw - D);
+      bool live = on && g < a.k;
+      if (live && static_cast<unsigned>(now.id) >= static_cast<unsigned>(a.E)) {
         record_error(a.err, kErrBadIndex);
-        id = -1;
+        live = false;
       }
-      const float D = warp_add(mine ? w * dw : 0.f);
-      const float c = w * (dw - D);
-      const bool live = mine && id >= 0;
-      // lanes with the same expert (the others have their own number, past all ids)
-      const uint32_t same = __match_any_sync(0xffffffffu, live ? id : kMaxRouteE + lane);
+      // lanes with the same expert of the same row (the others have numbers of their own)
+      const uint32_t same = __match_any_sync(0xffffffffu, live ? now.id + sub * kMaxRouteE : 32 * kMaxRouteE + lane);
       if (__any_sync(0xffffffffu, (same & (same - 1)) != 0)) {
         for (int j = 0; j < a.k; ++j) {
-          if (lane == j && live) term[id] += c;
+          if (g == j && live) term[now.id] += c;
           __syncwarp();
         }
       } else if (live) {
-        term[id] = c;
+        term[now.id] = c;
       }
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < PER; i += VEC ? 4 : 1) {
-        const int col = Row::col(i, lane);
+        const int col = Row::col(i, g);
         if (VEC) {
           const float4 q = *reinterpret_cast<const float4*>(term + col);
-          d[i] += q.x, d[i + 1] += q.y, d[i + 2] += q.z, d[i + 3] += q.w;
+          d[i] = q.x, d[i + 1] = q.y, d[i + 2] = q.z, d[i + 3] = q.w;
         } else {
-          d[i] += term[col];
+          d[i] = term[col];
         }
       }
       __syncwarp();
-      if (live) term[id] = 0.f;
+      if (live) term[now.id] = 0.f;
       __syncwarp();
     }
-    Row::store(a.d + t * a.E, a.E, lane, d);
+    if (softmax) {
+      // (a row that is NaN has s = NaN, which is not 0: it stays NaN)
+      const float inv = s.x == 0.f ? 0.f : __fdividef(1.f, s.x);
+      const float l = s.x == 0.f ? 0.f : top + logf(s.x);
+      const float F = s.y * inv;
+      if (on) {
+        sum_F.add(F);
+        sum_l.add(l * l);
+      }
+      const float b = a.balance_T * inv, rest = fmaf(a.z2_T * l, inv, -b * F);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) d[i] = fmaf(now.v[i], fmaf(b, f[i], rest), d[i]);
+    }
+    Row::store(a.d + t * a.E, a.E, g, on, d);
+  };
+  int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * R + sub;
+  Ahead x, y;
+  fetch(t, x);
+  // (the warp's rows begin together: t - sub is the same in all lanes)
+  for (; t - sub < a.T; t += 2 * step) {
+    work(t, x, y);
+    if (t - sub + step < a.T) work(t + step, y, x);
   }
   if (!a.part) return;
-  if (lane == 0) sums[warp][0] = sum_F.s - sum_F.c, sums[warp][1] = sum_l.s - sum_l.c;
+  float2 v = make_float2(sum_F.s - sum_F.c, sum_l.s - sum_l.c);
+#pragma unroll
+  for (int n = G; n < 32; n <<= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, n);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, n);
+  }
+  if (lane == 0) sums[warp][0] = v.x, sums[warp][1] = v.y;
   __syncthreads();
   if (threadIdx.x < 2) {
     float s = 0.f;
@@ -240,9 +265,15 @@ __global__ void __launch_bounds__(256) route_losses_kernel(const float* __restri
   if (q == 0) losses[i] = static_cast<float>(s[i][0] * inv_T);
 }
 
-template <int PER, bool VEC>
-cudaError_t launch_route_bwd(const RouteBwd& a, int blocks, cudaStream_t st) {
-  route_bwd_kernel<PER, VEC><<<blocks, 32 * kWarps, 0, st>>>(a);
+template <int G, int PER>
+cudaError_t launch_route_bwd(const RouteBwd& a, int sms, int* blocks, cudaStream_t st) {
+  constexpr int R = 32 / G * kWarps;
+  constexpr int per_sm = PER <= 8 ? 4 : (PER <= 16 ? 2 : 1);      // by registers
+  *blocks = static_cast<int>(std::min<int64_t>((a.T + R - 1) / R, std::min(kMaxRouteBlocks, sms * per_sm)));
+  if (a.E % 4 == 0)
+    route_bwd_kernel<G, PER, true><<<*blocks, 32 * kWarps, 0, st>>>(a);
+  else
+    route_bwd_kernel<G, PER, false><<<*blocks, 32 * kWarps, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -291,21 +322,14 @@ moe_status moe_route_bwd(const moe_shape* s, const float* logits, const int32_t*
   a.f_scale = static_cast<float>(s->E / (T * s->k));
   a.softmax = softmax ? 1 : 0;
   const int E = s->E;
-  const int per_sm = E <= 256 ? 8 : (E <= 512 ? 4 : 2);
-  const int blocks = static_cast<int>(std::min<int64_t>(
-      (s->T + kWarps - 1) / kWarps, std::min(kMaxRouteBlocks, sms * per_sm)));
+  int blocks = 0;
   const cudaError_t e = abi_tracked(kAbiRouteBwd, losses ? 2 : 1, st, [&] {
-    cudaError_t r;
-    if (E % 4 == 0)
-      r = E <= 128 ? launch_route_bwd<4, true>(a, blocks, st)
-          : E <= 256 ? launch_route_bwd<8, true>(a, blocks, st)
-          : E <= 512 ? launch_route_bwd<16, true>(a, blocks, st)
-                     : launch_route_bwd<32, true>(a, blocks, st);
-    else
-      r = E <= 128 ? launch_route_bwd<4, false>(a, blocks, st)
-          : E <= 256 ? launch_route_bwd<8, false>(a, blocks, st)
-          : E <= 512 ? launch_route_bwd<16, false>(a, blocks, st)
-                     : launch_route_bwd<32, false>(a, blocks, st);
+    // a choice per lane: k lanes at least
+    const cudaError_t r = E <= 64 && s->k <= 8 ? launch_route_bwd<8, 8>(a, sms, &blocks, st)
+                          : E <= 128 && s->k <= 16 ? launch_route_bwd<16, 8>(a, sms, &blocks, st)
+                          : E <= 256 ? launch_route_bwd<32, 8>(a, sms, &blocks, st)
+                          : E <= 512 ? launch_route_bwd<32, 16>(a, sms, &blocks, st)
+                                     : launch_route_bwd<32, 32>(a, sms, &blocks, st);
     if (r != cudaSuccess || !losses) return r;
     // (may start while the last rows are done)
     cudaLaunchConfig_t cfg = {};

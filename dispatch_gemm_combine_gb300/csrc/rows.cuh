@@ -51,8 +51,9 @@ __device__ __forceinline__ float warp_sum4(const float4& v) {
   return s;
 }
 
-// Four sums over the block, the same in every thread, in a fixed order.  `part` holds
-// 128 floats and may be reused after the next barrier.
+// Four sums over the block of at most MAXT threads, the same in every thread, in a fixed
+// order.  `part` holds 128 floats and may be reused after the next barrier.
+template <int MAXT>
 __device__ __forceinline__ float4 block_sum4(const float4& v, float* part) {
   float s = warp_sum4(v);
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
@@ -60,7 +61,11 @@ __device__ __forceinline__ float4 block_sum4(const float4& v, float* part) {
     if (lane < 4) part[(threadIdx.x >> 5) * 4 + lane] = s;
     __syncthreads();
     s = 0.f;
-    for (int i = lane; i < warps * 4; i += 32) s += part[i];
+#pragma unroll
+    for (int i = 0; i < (MAXT + 255) / 256; ++i) {
+      const float p = part[i * 32 + lane];      // (past the warps: not one of the sums)
+      s += i * 32 + lane < warps * 4 ? p : 0.f;
+    }
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
   }
@@ -73,6 +78,22 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   float d;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// 16 bytes to global memory where `on`, without a branch.
+__device__ __forceinline__ void store16_if(void* p, const uint4& u, bool on) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(p),
+               "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w), "r"(static_cast<int>(on))
+               : "memory");
+}
+__device__ __forceinline__ void store8_if(__nv_bfloat16* p, const float2 (&v)[4], bool on) {
+  store16_if(p, make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y),
+                           pack_bf16(v[3].x, v[3].y)), on);
+}
+__device__ __forceinline__ void store8_if(float* p, const float2 (&v)[4], bool on) {
+  const uint4* u = reinterpret_cast<const uint4*>(&v[0]);
+  store16_if(p, u[0], on);
+  store16_if(p + 4, u[1], on);
 }
 
 // Eight of a row's values as e4m3 codes with their block's scale byte, which four
