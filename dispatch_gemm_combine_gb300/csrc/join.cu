@@ -554,10 +554,10 @@ moe_status moe_join_norm_fwd(int64_t T, int32_t H, int32_t dtype, const void* y,
                              float residual_scale, const void* weight, float eps, void* total, void* n,
                              uint8_t* n_scale, float* rstd_post, float* rstd, moe_stream_t stream) {
   if (!join_dims_ok(T, H, dtype) || !(eps >= 0.f) || !finite(residual_scale)) return MOE_ERR_INVALID_ARG;
-  if ((post_norm != 0 && post_norm != 1) || (n_scale && (!n || H % 32)) || (!n != !weight))
-    return MOE_ERR_INVALID_ARG;
-  if ((rstd_post && !post_norm) || (rstd && !n)) return MOE_ERR_INVALID_ARG;
+  if ((post_norm != 0 && post_norm != 1) || (n_scale && H % 32)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
+  if ((n_scale && !n) || (!n != !weight) || (rstd_post && !post_norm) || (rstd && !n))
+    return MOE_ERR_INVALID_ARG;
   if (!y || !residual || !total || n == total) return MOE_ERR_INVALID_ARG;
   for (const void* p : {y, residual, post_weight, weight, static_cast<const void*>(total),
                         static_cast<const void*>(n)})

@@ -743,7 +743,9 @@ cudaError_t launch_orth_steps(const OrthMaps& maps, const OrthArgs& args, int sm
 //   norm and load   from g, the squares joined over the cluster
 //   gram            each CTA's columns; the CTAs' sums are added in rank order, a share
 //                   of the rows by each, which hands it to all
-//   poly            128 x 128 in every CTA
+//   poly            128 x 128 in every CTA; B as an fp16 value and what it leaves, so its
+//                   rounding, the largest one's share of the error, falls away (the products
+//                   are not what takes the time)
 //   update          in place: a group of 256 columns is overwritten when its product
 //                   is done
 // What bounds it is the chain of dependent steps, not the products.  At most one CTA
@@ -753,7 +755,7 @@ constexpr int kSmallThreads = 512;
 constexpr int kChunkBytes = 128 * 128;            // 128 rows of 64 columns
 constexpr int kMaxSmallChunks = 8;                // per CTA
 constexpr int kMaxSmallRanks = 16;             // (more than 8 where the device can)
-constexpr int kSmallTail = 2 * kChunkBytes + 4 * kChunkBytes + 1024 + 512;   // A, P (B in its first half), alignment, rest
+constexpr int kSmallTail = 2 * kChunkBytes + 4 * kChunkBytes + 1024 + 512;   // A, P (or both parts of B), alignment, rest
 constexpr int kSmallSmemMin = 120 * 1024;
 constexpr int kSmallM = 128;
 constexpr int kSmallN = 8 * kMaxSmallChunks * 64;   // on 8 CTAs
@@ -990,16 +992,20 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
       for (int j = 0; j < 4; ++j) {
         const uint4 u = *reinterpret_cast<const uint4*>(gA + swz(row, c + 8 * j));
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        uint32_t o[4];
+        uint32_t o[4], rest[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-          float lo = fmaf(cA, x.x, cP * v[8 * j + 2 * k]), hi = fmaf(cA, x.y, cP * v[8 * j + 2 * k + 1]);
-          if (row == c + 8 * j + 2 * k) lo += cI;
-          if (row == c + 8 * j + 2 * k + 1) hi += cI;
-          o[k] = pack_half(lo, hi);
+          float b0 = fmaf(cA, x.x, cP * v[8 * j + 2 * k]), b1 = fmaf(cA, x.y, cP * v[8 * j + 2 * k + 1]);
+          if (row == c + 8 * j + 2 * k) b0 += cI;
+          if (row == c + 8 * j + 2 * k + 1) b1 += cI;
+          const __half2 h = __floats2half2_rn(b0, b1);
+          const float2 f = __half22float2(h);
+          o[k] = *reinterpret_cast<const uint32_t*>(&h);
+          rest[k] = pack_half(b0 - f.x, b1 - f.y);
         }
         st_shared_v4u(sB + swz(row, c + 8 * j), o[0], o[1], o[2], o[3]);
+        st_shared_v4u(sB + 2 * kChunkBytes + swz(row, c + 8 * j), rest[0], rest[1], rest[2], rest[3]);
       }
     }
     fence_async_shared();
@@ -1013,9 +1019,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
       for (int b = 0; b < ngroups; ++b) {
         const int cols = min(256, width - 256 * b);
         const uint32_t idesc = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(cols >> 3) << 17) | ((128u >> 4) << 24);
-        for (int k = 0; k < mc / 16; ++k)
-          tc_mma<false>(tmem + 256 * (1 - b), smem_desc_sw128(sB + (k >> 2) * kChunkBytes + (k & 3) * 32, 16, 1024),
-                        smem_desc_sw128(sX + 4 * b * kChunkBytes + k * 16 * 128, kChunkBytes, 1024), idesc, k != 0 ? 1u : 0u);
+        for (int k = 0; k < mc / 16; ++k) {
+          const uint64_t x = smem_desc_sw128(sX + 4 * b * kChunkBytes + k * 16 * 128, kChunkBytes, 1024);
+#pragma unroll
+          for (int part = 0; part < 2; ++part)      // B's fp16 values, and what they left
+            tc_mma<false>(tmem + 256 * (1 - b), smem_desc_sw128(sB + (2 * part + (k >> 2)) * kChunkBytes + (k & 3) * 32, 16, 1024),
+                          x, idesc, (k | part) != 0 ? 1u : 0u);
+        }
         tc_commit(bars + 8 * b);
       }
     }
@@ -1183,7 +1193,8 @@ bool orth_plan(int64_t E, int64_t M, int64_t N, OrthPlan* p) {
   };
   const size_t C = p->chunk;
   p->counters = take(sizeof(int) * 3 * kMaxOrthSteps * C);
-  p->parts = take(sizeof(Squares) * C * p->nparts);
+  // (N x M takes what M x N takes)
+  p->parts = take(sizeof(Squares) * C * static_cast<size_t>(std::max<int64_t>(1, std::min<int64_t>({want, p->n, kMaxParts}))));
   p->x[0] = take(2 * C * p->m * static_cast<size_t>(p->ldx));
   p->x[1] = take(2 * C * p->m * static_cast<size_t>(p->ldx));
   p->a = take(2 * C * p->m * static_cast<size_t>(p->lda));

@@ -11,15 +11,19 @@
 // A row's logits stay in the registers of G lanes, PER in each (a warp for more than 128
 // experts, half of one or a quarter for fewer: what a row costs beside its columns is
 // then shared by two or four rows), so they are read once and d is written once.  The
-// next rows' logits are loaded before this one's arithmetic.  The choices' terms go
-// through a row of shared memory (a lane writes its choice's term where the lane that
-// owns the column picks it up); a row that names an expert twice adds its terms one
-// after the other.  Sums over the rows: per warp and block in a fixed order, then one
-// block over all blocks: no atomics.
+// following rows' logits are copied ahead into shared memory, each warp's into its own
+// part.  The choices' terms go through a row of shared memory (a lane writes its
+// choice's term where the lane that owns the column picks it up); a row that names an
+// expert twice adds its terms one after the other.  Sums over the rows: a lane keeps
+// every G-th row's, then over warp and block in a fixed order, then one block over all
+// blocks: no atomics.
 #include <algorithm>
+#include <atomic>
 
 #include "abi_internal.h"
 #include "common.cuh"
+#include "rows.cuh"
+#include "vec.cuh"
 
 namespace moe {
 namespace {
@@ -68,177 +72,176 @@ __device__ __forceinline__ float4 row_sum4(const float4& v) {
                      __shfl_sync(0xffffffffu, s, 1, G), __shfl_sync(0xffffffffu, s, 3, G));
 }
 
-// A running sum with what its roundings took (many rows per warp); beyond fp32's
-// range it stays infinite.
-struct Sum {
-  float s = 0.f, c = 0.f;
-  __device__ __forceinline__ void add(float v) {
-    const float y = v - c, n = s + y;
-    c = isfinite(n) ? (n - s) - y : 0.f;
-    s = n;
-  }
-};
+// 2^40 e^x for x <= 0: the instruction gives 0 below 2^-126, which is then far below
+// the least fp32 probability.
+__device__ __forceinline__ float exp2_40(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(x, 1.44269504f, 40.f)));
+  return r;
+}
+
+// 4 or 16 bytes to shared memory, without a branch.
+template <int BYTES>
+__device__ __forceinline__ void copy_if(uint32_t dst, const float* src, bool on) {
+  if (BYTES == 16)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst), "l"(src), "r"(static_cast<int>(on)) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.ca.shared.global [%0], [%1], 4;\n\t}" ::"r"(dst), "l"(src), "r"(static_cast<int>(on)) : "memory");
+}
 
 // PER columns in each of a row's G lanes.  VEC: groups of four, 4 (g + G i) ..; otherwise
 // g + G i.
-template <int G, int PER, bool VEC>
-struct RouteRow {
-  static __device__ __forceinline__ int col(int i, int g) {
-    return VEC ? 4 * (g + G * (i / 4)) + i % 4 : g + G * i;
-  }
-  static __device__ __forceinline__ void load(const float* row, int E, int g, bool on, float (&v)[PER]) {
-    constexpr int S = VEC ? 4 : 1;
-#pragma unroll
-    for (int i = 0; i < PER; i += S) {
-      const int c = col(i, g);
-      const bool in = on && c < E;
-      if (VEC) {
-        const float4 q = in ? __ldg(reinterpret_cast<const float4*>(row + c))
-                            : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
-      } else {
-        v[i] = in ? __ldg(row + c) : -INFINITY;
-      }
-    }
-  }
-  static __device__ __forceinline__ void store(float* row, int E, int g, bool on, const float (&v)[PER]) {
-    constexpr int S = VEC ? 4 : 1;
-#pragma unroll
-    for (int i = 0; i < PER; i += S) {
-      const int c = col(i, g);
-      if (on && c < E) {
-        if (VEC)
-          *reinterpret_cast<float4*>(row + c) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-        else
-          row[c] = v[i];
-      }
-    }
-  }
-};
+constexpr int kRowsAhead = 3;
 
 template <int G, int PER, bool VEC>
 __global__ void __launch_bounds__(32 * kWarps) route_bwd_kernel(const RouteBwd a) {
-  using Row = RouteRow<G, PER, VEC>;
-  constexpr int R = 32 / G;      // rows of a warp
-  __shared__ __align__(16) float terms[kWarps][32 * PER];
+  constexpr int R = 32 / G;             // rows of a warp
+  constexpr int S = VEC ? 4 : 1;        // columns side by side
+  constexpr int W = G * PER;            // floats of a row in shared memory
+  extern __shared__ __align__(16) float row_mem[];      // [kWarps][kRowsAhead + 1][R][W]: the last one for the terms
   __shared__ float sums[kWarps][2];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane % G, sub = lane / G;
-  float* term = terms[warp] + sub * G * PER;
   const bool chosen = a.dw != nullptr;
   const bool softmax = a.softmax != 0;
-  if (chosen)
-    for (int i = lane; i < 32 * PER; i += 32) terms[warp][i] = 0.f;
-  __syncwarp();
+  float* mine = row_mem + (warp * (kRowsAhead + 1) * R + sub) * W + g * S;   // this lane's first columns
+  float* terms = row_mem + ((warp * (kRowsAhead + 1) + kRowsAhead) * R + sub) * W;
+  constexpr int stage_floats = R * W;
+  auto col = [&](int i) { return S * (g + G * (i / S)) + i % S; };
+  // columns that do not exist: -inf for the logits
+#pragma unroll
+  for (int q = 0; q <= kRowsAhead; ++q)
+#pragma unroll
+    for (int i = 0; i < PER; ++i) mine[q * stage_floats + (i / S) * G * S + i % S] = q < kRowsAhead ? -INFINITY : 0.f;
   float f[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int c = Row::col(i, g);
-    f[i] = a.counts && c < a.E ? static_cast<float>(__ldg(a.counts + c)) * a.f_scale : 0.f;
-  }
+  for (int i = 0; i < PER; ++i) f[i] = a.counts && col(i) < a.E ? static_cast<float>(__ldg(a.counts + col(i))) * a.f_scale : 0.f;
+  __syncwarp();
+
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * R;
-  struct Ahead {
-    float v[PER];
-    int id;
-    float w, dw;
+  int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * R + sub;
+  int64_t ahead = t;                          // the next row to be copied
+  const uint32_t mine_s = smem_u32(mine);
+  auto copy = [&](int stage) {
+    if (softmax && ahead < a.T) {
+      const float* src = a.logits + ahead * a.E + g * S;
+#pragma unroll
+      for (int i = 0; i < PER; i += S)
+        copy_if<4 * S>(mine_s + (stage * stage_floats + (i / S) * G * S) * 4, src + (i / S) * G * S, col(i) < a.E);
+    }
+    cp_async_commit();
+    ahead += step;
   };
-  auto fetch = [&](int64_t row, Ahead& n) {
-    const bool on = row < a.T;
-    if (softmax) Row::load(a.logits + row * a.E, a.E, g, on, n.v);
-    n.id = -1, n.w = n.dw = 0.f;
-    if (chosen && on && g < a.k) {
-      n.id = __ldg(a.idx + row * a.k + g);
-      n.w = __ldg(a.w + row * a.k + g);
-      n.dw = __ldg(a.dw + row * a.k + g);
+#pragma unroll
+  for (int q = 0; q < kRowsAhead - 1; ++q) copy(q);
+  int id = -1, n_id = -1;
+  float w = 0.f, dw = 0.f, n_w = 0.f, n_dw = 0.f;
+  auto choice = [&](int64_t row) {
+    if (chosen && g < a.k && row < a.T) {
+      n_id = __ldg(a.idx + row * a.k + g);
+      n_w = __ldg(a.w + row * a.k + g);
+      n_dw = __ldg(a.dw + row * a.k + g);
     }
   };
-  Sum sum_F, sum_l;
-  // t: this lane's row; `now` holds it, `next` receives the one after
-  auto work = [&](int64_t t, Ahead& now, Ahead& next) {
-    fetch(t + step, next);
-    const bool on = t < a.T;
-    float d[PER];
-    float4 s = make_float4(0.f, 0.f, now.w * now.dw, 0.f);
+  choice(t);
+  float sum_F = 0.f, sum_l = 0.f;
+  int stage = 0, turn = 0;
+  // (the warp's rows begin together: t - sub is the same in all lanes)
+  for (; t - sub < a.T; t += step) {
+    const bool on = R == 1 || t < a.T;
+    id = n_id, w = n_w, dw = n_dw;
+    choice(t + step);
+    cp_async_wait<kRowsAhead - 2>();
+    copy(stage == 0 ? kRowsAhead - 1 : stage - 1);
+    float4 s = make_float4(0.f, 0.f, w * dw, 0.f);
+    float v[PER];
     float top = 0.f;
     if (softmax) {
-      top = now.v[0];
 #pragma unroll
-      for (int i = 1; i < PER; ++i) top = fmaxf(top, now.v[i]);
+      for (int i = 0; i < PER; i += S) {
+        const float* p = mine + stage * stage_floats + (i / S) * G * S;
+        if (VEC) {
+          const float4 q = *reinterpret_cast<const float4*>(p);
+          v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+        } else {
+          v[i] = *p;
+        }
+      }
+      top = v[0];
+#pragma unroll
+      for (int i = 1; i < PER; ++i) top = fmaxf(top, v[i]);
       top = row_max<G>(top);
       if (top == -INFINITY) top = 0.f;      // every expert masked: p = 0
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        now.v[i] = exp2f((now.v[i] - top) * 1.44269504f);
-        s.x += now.v[i];
-        s.y = fmaf(now.v[i], f[i], s.y);
+        v[i] = exp2_40(v[i] - top);
+        s.x += v[i];
+        s.y = fmaf(v[i], f[i], s.y);
       }
     }
+    stage = stage + 1 == kRowsAhead ? 0 : stage + 1;
     s = row_sum4<G>(s);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) d[i] = 0.f;
+    const float c = w * (dw - s.z);
+    bool live = false;
     if (chosen) {
-      const float D = s.z, c = now.w * (now.dw - D);
-      bool live = on && g < a.k;
-      if (live && static_cast<unsigned>(now.id) >= static_cast<unsigned>(a.E)) {
+      live = on && g < a.k;
+      if (live && static_cast<unsigned>(id) >= static_cast<unsigned>(a.E)) {
         record_error(a.err, kErrBadIndex);
         live = false;
       }
       // lanes with the same expert of the same row (the others have numbers of their own)
-      const uint32_t same = __match_any_sync(0xffffffffu, live ? now.id + sub * kMaxRouteE : 32 * kMaxRouteE + lane);
+      const uint32_t same = __match_any_sync(0xffffffffu, live ? id + sub * kMaxRouteE : 32 * kMaxRouteE + lane);
       if (__any_sync(0xffffffffu, (same & (same - 1)) != 0)) {
         for (int j = 0; j < a.k; ++j) {
-          if (g == j && live) term[now.id] += c;
+          if (g == j && live) terms[id] += c;
           __syncwarp();
         }
       } else if (live) {
-        term[now.id] = c;
+        terms[id] = c;
       }
-      __syncwarp();
-#pragma unroll
-      for (int i = 0; i < PER; i += VEC ? 4 : 1) {
-        const int col = Row::col(i, g);
-        if (VEC) {
-          const float4 q = *reinterpret_cast<const float4*>(term + col);
-          d[i] = q.x, d[i + 1] = q.y, d[i + 2] = q.z, d[i + 3] = q.w;
-        } else {
-          d[i] = term[col];
-        }
-      }
-      __syncwarp();
-      if (live) term[now.id] = 0.f;
       __syncwarp();
     }
+    float b = 0.f, rest = 0.f;
     if (softmax) {
       // (a row that is NaN has s = NaN, which is not 0: it stays NaN)
       const float inv = s.x == 0.f ? 0.f : __fdividef(1.f, s.x);
-      const float l = s.x == 0.f ? 0.f : top + logf(s.x);
+      const float l = s.x == 0.f ? 0.f : top + logf(s.x * 0x1p-40f);
       const float F = s.y * inv;
-      if (on) {
-        sum_F.add(F);
-        sum_l.add(l * l);
+      if (on && g == (turn & (G - 1))) {
+        sum_F += F;
+        sum_l = fmaf(l, l, sum_l);
       }
-      const float b = a.balance_T * inv, rest = fmaf(a.z2_T * l, inv, -b * F);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) d[i] = fmaf(now.v[i], fmaf(b, f[i], rest), d[i]);
+      ++turn;
+      b = a.balance_T * inv, rest = fmaf(a.z2_T * l, inv, -b * F);
     }
-    Row::store(a.d + t * a.E, a.E, g, on, d);
-  };
-  int64_t t = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * R + sub;
-  Ahead x, y;
-  fetch(t, x);
-  // (the warp's rows begin together: t - sub is the same in all lanes)
-  for (; t - sub < a.T; t += 2 * step) {
-    work(t, x, y);
-    if (t - sub + step < a.T) work(t + step, y, x);
+    float* out = a.d + t * a.E + g * S;
+#pragma unroll
+    for (int i = 0; i < PER; i += S) {
+      float d[S];
+      const float* p = terms + g * S + (i / S) * G * S;
+      if (VEC) {
+        const float4 q = *reinterpret_cast<const float4*>(p);
+        d[0] = q.x, d[1 % S] = q.y, d[2 % S] = q.z, d[3 % S] = q.w;
+      } else {
+        d[0] = *p;
+      }
+      if (softmax)
+#pragma unroll
+        for (int j = 0; j < S; ++j) d[j] = fmaf(v[i + j], fmaf(b, f[i + j], rest), d[j]);
+      if (on && col(i) < a.E) {
+        if (VEC)
+          *reinterpret_cast<float4*>(out + (i / S) * G * S) = make_float4(d[0], d[1 % S], d[2 % S], d[3 % S]);
+        else
+          out[(i / S) * G * S] = d[0];
+      }
+    }
+    __syncwarp();
+    if (live) terms[id] = 0.f;
+    __syncwarp();
   }
   if (!a.part) return;
-  float2 v = make_float2(sum_F.s - sum_F.c, sum_l.s - sum_l.c);
-#pragma unroll
-  for (int n = G; n < 32; n <<= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, n);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, n);
-  }
-  if (lane == 0) sums[warp][0] = v.x, sums[warp][1] = v.y;
+  sum_F = warp_sum(sum_F), sum_l = warp_sum(sum_l);
+  if (lane == 0) sums[warp][0] = sum_F, sums[warp][1] = sum_l;
   __syncthreads();
   if (threadIdx.x < 2) {
     float s = 0.f;
@@ -247,34 +250,50 @@ __global__ void __launch_bounds__(32 * kWarps) route_bwd_kernel(const RouteBwd a
   }
 }
 
-// losses[i] = sum of the blocks' sums / T: thread q adds blocks q, q + 128, ...,
-// the threads' sums are added in a tree; in 64 bits.
+// losses[i] = sum of the blocks' sums / T: a thread adds blocks q, q + 256, ..., then the
+// threads' sums by warps: sixteen fp32 additions deep.  (In 64 bits, of which this GPU
+// adds few a clock, the call takes 2 us more.)
 __global__ void __launch_bounds__(256) route_losses_kernel(const float* __restrict__ part, int blocks,
-                                                           double inv_T, float* __restrict__ losses) {
-  __shared__ double s[2][128];
+                                                           float inv_T, float* __restrict__ losses) {
+  __shared__ float s[2][8];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the sums are there
-  const int i = threadIdx.x & 1, q = threadIdx.x >> 1;
-  double v = 0.0;
-  for (int b = q; b < blocks; b += 128) v += static_cast<double>(__ldcg(part + 2 * b + i));
-  s[i][q] = v;
-  __syncthreads();
-  for (int n = 64; n > 0; n >>= 1) {
-    if (q < n) s[i][q] += s[i][q + n];
-    __syncthreads();
+  float2 v[kMaxRouteBlocks / 256];
+#pragma unroll
+  for (int i = 0; i < kMaxRouteBlocks / 256; ++i) {
+    const int b = threadIdx.x + 256 * i;
+    v[i] = b < blocks ? __ldcg(reinterpret_cast<const float2*>(part) + b) : make_float2(0.f, 0.f);
   }
-  if (q == 0) losses[i] = static_cast<float>(s[i][0] * inv_T);
+  float x = 0.f, y = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxRouteBlocks / 256; ++i) x += v[i].x, y += v[i].y;
+  x = warp_sum(x), y = warp_sum(y);
+  if ((threadIdx.x & 31) == 0) s[0][threadIdx.x >> 5] = x, s[1][threadIdx.x >> 5] = y;
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    float t = 0.f;
+    for (int i = 0; i < 8; ++i) t += s[threadIdx.x][i];
+    losses[threadIdx.x] = t * inv_T;
+  }
+}
+
+template <int G, int PER, bool VEC>
+cudaError_t launch_route_bwd_v(const RouteBwd& a, int sms, int* blocks, cudaStream_t st) {
+  constexpr int R = 32 / G * kWarps;
+  constexpr int smem = kWarps * (kRowsAhead + 1) * 32 * PER * static_cast<int>(sizeof(float));
+  // by registers (five blocks of 48 registers spill: 65536 x 256 38 us instead of 33)
+  constexpr int per_sm = std::min(PER <= 8 ? 4 : (PER <= 16 ? 3 : 1), kRingPerSm / smem);
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = allow_smem(route_bwd_kernel<G, PER, VEC>, ready);
+  if (e != cudaSuccess) return e;
+  *blocks = static_cast<int>(std::min<int64_t>((a.T + R - 1) / R, std::min(kMaxRouteBlocks, sms * per_sm)));
+  route_bwd_kernel<G, PER, VEC><<<*blocks, 32 * kWarps, smem, st>>>(a);
+  return cudaGetLastError();
 }
 
 template <int G, int PER>
 cudaError_t launch_route_bwd(const RouteBwd& a, int sms, int* blocks, cudaStream_t st) {
-  constexpr int R = 32 / G * kWarps;
-  constexpr int per_sm = PER <= 8 ? 4 : (PER <= 16 ? 2 : 1);      // by registers
-  *blocks = static_cast<int>(std::min<int64_t>((a.T + R - 1) / R, std::min(kMaxRouteBlocks, sms * per_sm)));
-  if (a.E % 4 == 0)
-    route_bwd_kernel<G, PER, true><<<*blocks, 32 * kWarps, 0, st>>>(a);
-  else
-    route_bwd_kernel<G, PER, false><<<*blocks, 32 * kWarps, 0, st>>>(a);
-  return cudaGetLastError();
+  return a.E % 4 == 0 ? launch_route_bwd_v<G, PER, true>(a, sms, blocks, st)
+                      : launch_route_bwd_v<G, PER, false>(a, sms, blocks, st);
 }
 
 }  // namespace
@@ -341,7 +360,7 @@ moe_status moe_route_bwd(const moe_shape* s, const float* logits, const int32_t*
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, route_losses_kernel, static_cast<const float*>(a.part), blocks, 1.0 / T, losses);
+    return cudaLaunchKernelEx(&cfg, route_losses_kernel, static_cast<const float*>(a.part), blocks, static_cast<float>(1.0 / T), losses);
   });
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

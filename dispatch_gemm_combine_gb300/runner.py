@@ -12,10 +12,11 @@ gives no memory that another stream still has work for.
 
 import torch
 
-from . import (MOE_BF16, MOE_FP32, Shape, alloc_plan, bias_struct, check_device_error, ffn_bwd,
-               ffn_few, ffn_fwd, few_workspace, grad_clip, grad_clip_workspace, grad_table,
-               moe_grad_clip_workspace_size, moe_saved_size, mx_alloc, mx_quantize, mx_struct,
-               plan, route, workspace)
+from . import (MOE_BF16, MOE_FP32, MOE_GATE_UP_INTERLEAVED, Shape, alloc_plan, bias_struct,
+               check_device_error, ffn_bwd, ffn_few, ffn_fwd, few_workspace, grad_clip,
+               grad_clip_workspace, grad_table, moe_grad_clip_workspace_size, moe_saved_size,
+               mx_alloc, mx_quantize, mx_struct, orthogonalize, orthogonalize_workspace, plan, route,
+               route_bwd, route_bwd_workspace, workspace)
 
 _TORCH_DTYPE = {MOE_BF16: torch.bfloat16, MOE_FP32: torch.float32}
 
@@ -121,6 +122,46 @@ class LayerRunner:
         out = (self.dx, self.d_topk_w, self.dw_gate_up, self.dw_down)
         return out + (self.db_gate_up, self.db_down) if with_bias else out
 
+    def route_bwd(self, logits, topk_idx, topk_w, d_topk_w=None, balance=0.0, z=0.0, stream=None):
+        """(d_logits [T,E], losses [2]): the gradient of the router's logits, from the
+        last backward's d_topk_w (or the one given) through the weights that route()
+        made, with `balance` times the load-balancing loss and `z` times the z-loss, and
+        both losses.  The plan must be that of topk_idx, as route() leaves it."""
+        if getattr(self, "ws_route_bwd", None) is None:
+            T, E = self.shape.T, self.shape.E
+            with torch.cuda.stream(stream):
+                self.ws_route_bwd = route_bwd_workspace(self.shape, self.device)
+                self.d_logits = torch.empty((T, E), dtype=torch.float32, device=self.device)
+                self.losses = torch.empty(2, dtype=torch.float32, device=self.device)
+        route_bwd(self.shape, logits, self.d_logits, self.ws_route_bwd, topk_idx, topk_w,
+                  self.d_topk_w if d_topk_w is None else d_topk_w, self.plan_t["counts"], balance, z,
+                  self.losses, stream)
+        return self.d_logits, self.losses
+
+    def orthogonalize(self, gate_up=None, down=None, steps=5, coefs=None, eps=1e-7, scale=1.0,
+                      stream=None):
+        """Orthogonal updates (u_gate_up [E,H,2I], u_down [E,I,H], bf16) of the last
+        backward's weight gradients, or of the tensors given (their momenta, bf16 or
+        fp32): for each expert the gate, the up and the down matrix by itself."""
+        if self.shape.gate_up_layout == MOE_GATE_UP_INTERLEAVED:
+            raise ValueError("orthogonalize: gate and up columns are interleaved, not matrices of their own")
+        gate_up = self.dw_gate_up if gate_up is None else gate_up
+        down = self.dw_down if down is None else down
+        E, H, I = self.shape.E, self.shape.H, self.shape.I
+        if gate_up.shape != (E, H, 2 * I) or down.shape != (E, I, H):
+            raise ValueError("orthogonalize: %s and %s are not the layer's weights' shapes" % (
+                tuple(gate_up.shape), tuple(down.shape)))
+        if getattr(self, "ws_orth", None) is None:
+            with torch.cuda.stream(stream):
+                # (H x I and I x H alike)
+                self.ws_orth = orthogonalize_workspace(down, self.device)
+                self.u_gate_up = torch.empty((E, H, 2 * I), dtype=torch.bfloat16, device=self.device)
+                self.u_down = torch.empty((E, I, H), dtype=torch.bfloat16, device=self.device)
+        for g, u in ((gate_up[:, :, :I], self.u_gate_up[:, :, :I]), (gate_up[:, :, I:], self.u_gate_up[:, :, I:]),
+                     (down, self.u_down)):
+            orthogonalize(g, u, self.ws_orth, steps, coefs, eps, scale, stream)
+        return self.u_gate_up, self.u_down
+
     def clip_grads(self, max_norm, extra=(), stream=None):
         """Scale the last backward's weight gradients (and bias gradients, where it
         gave them), with those of `extra` (tensors), so that their global norm is at
@@ -141,6 +182,7 @@ class LayerRunner:
 
     def check(self, stream=None):
         for ws in (self.ws_plan, self.ws_fwd, self.ws_bwd, getattr(self, "ws_bwd_recompute", None),
-                   getattr(self, "ws_few", None)):
+                   getattr(self, "ws_few", None), getattr(self, "ws_route_bwd", None),
+                   getattr(self, "ws_orth", None)):
             if ws is not None:
                 check_device_error(ws, stream)

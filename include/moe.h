@@ -505,8 +505,9 @@ moe_status moe_route_bwd(const moe_shape* shape, const float* logits, const int3
                          float balance, float z, float* d_logits, float* losses, void* ws,
                          size_t ws_bytes, moe_stream_t stream);
 
-/* Bytes of workspace of moe_orthogonalize (0 for bad dimensions).  It does not grow
- * with E beyond a few hundred MB or one matrix's need (8 bytes an element). */
+/* Bytes of workspace of moe_orthogonalize (0 for bad dimensions): the same for N x M,
+ * no less for more matrices, and beyond about a GB (or one matrix's need, up to 8
+ * bytes an element) not growing with E. */
 size_t moe_orthogonalize_workspace_size(int64_t E, int64_t M, int64_t N);
 
 /* Orthogonal updates by Newton-Schulz products, for each matrix g [M,N] of a batch
@@ -524,9 +525,9 @@ size_t moe_orthogonalize_workspace_size(int64_t E, int64_t M, int64_t N);
  *     strides), otherwise no overlap.
  * The norm is in range for every finite fp32 g.  A matrix of zeros gives zeros; one
  * that holds an infinity or a NaN gives NaN.  The products run in fp16 (11 bits) with
- * fp32 accumulation: against exact arithmetic the result is 1e-3 off where g's
- * singular values are within a factor of about 500 of one another; what lies farther
- * below the largest is amplified with the roundings in it.
+ * fp32 accumulation.  Before its rounding to bf16 the result of a Gaussian g is 1e-3
+ * off in the 2-norm; singular values hundreds of times below the largest are
+ * amplified together with the roundings beside them.
  * Requirements: 1 <= M, N <= 65536, 1 <= steps <= 32, g_ld and out_ld >= N,
  * out_stride >= (M-1)*out_ld + N (E > 1), eps >= 0, scale finite; g and out aligned
  * to their elements (rows on 16 bytes are faster).  E = 0 is a no-op.

@@ -299,6 +299,8 @@ def test_gradient_against_differences():
 def test_empty_and_refused():
     e = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
     moe.join_norm_fwd(e, e, e)
+    f = torch.empty(0, device="cuda")
+    moe.join_norm_fwd(e, e, e, gate=f, weight=torch.ones(64, dtype=torch.bfloat16, device="cuda"), n=e, rstd_post=f, rstd=f)
     dw, dwp = torch.full((64,), 3.0, device="cuda"), torch.full((64,), 3.0, device="cuda")
     moe.join_norm_bwd(e, e, e, d_total=e, post_norm=False, d_post_weight=dwp)
     assert not dwp.any()

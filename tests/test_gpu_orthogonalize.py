@@ -1,8 +1,8 @@
 """Orthogonal updates by Newton-Schulz products, against the iteration in 64 bits.
 
 Two comparisons.  `emulated` computes in 64 bits but rounds where the kernels round to
-fp16 (x_0, and each step's a, b and x, all held with the same power of two): what is
-left between the two is the fp32 accumulation, which tips one rounding in some hundred
+fp16 (x_0, and each step's a, b and x, all held with the same power of two; b not for at
+most 128 rows, where it is held as two fp16 values, 2^-22 of it left out): what is left between the two is the fp32 accumulation, which tips one rounding in some hundred
 the other way, and the output's rounding to bf16, off by at most u = 2^-8 of a value
 and 0.6 u in the 2-norm (a rounding's error is spread over half a step).  The bound is
 u of the 2-norm, so 0.4 u = 1.6e-3 is left for tipped roundings: a tenth of all
@@ -52,7 +52,8 @@ def emulated(g, steps=5, coefs=None, eps=1e-7):
     for i in range(steps):
         c = (coefs or [COEFS] * steps)[i]
         a = h(x @ x.mT)
-        b = h(c[0] * S * S * eye + c[1] * a + c[2] / (S * S) * (a @ a))
+        b = c[0] * S * S * eye + c[1] * a + c[2] / (S * S) * (a @ a)
+        b = b if x.shape[-2] <= 128 else h(b)
         x = b @ x / (S * S)
         x = h(x) if i + 1 < steps else x
     x = x / S

@@ -64,6 +64,11 @@ def test_orthogonalize_refusals(L):
         assert L.moe_orthogonalize_workspace_size(*bad) == 0
     # the workspace is that of the matrices that go through at once
     assert L.moe_orthogonalize_workspace_size(4096, 2880, 2880) == L.moe_orthogonalize_workspace_size(64, 2880, 2880)
+    # that of the transposes, and no less for more matrices
+    for M, N in ((300, 5000), (2880, 2880), (129, 40000), (1000, 1200), (64, 9000)):
+        sizes = [L.moe_orthogonalize_workspace_size(E, M, N) for E in (0, 1, 2, 3, 7, 40, 1000)]
+        assert sizes == [L.moe_orthogonalize_workspace_size(E, N, M) for E in (0, 1, 2, 3, 7, 40, 1000)]
+        assert sizes == sorted(sizes)
     ok = dict(E=2, M=16, N=24, dtype=L.MOE_FP32, g=16, g_ld=24, g_stride=384, steps=5, coefs=None, eps=1e-7, scale=1.0,
               out=16, out_ld=24, out_stride=384, ws=256, ws_bytes=size, stream=None)
 
