@@ -206,25 +206,28 @@ __global__ void __launch_bounds__(256) orth_load_kernel(const OrthIn in, const S
 //
 // Within a unit each CTA loads 128 rows of A and half of B's columns per 64 columns
 // of K into a ring, one thread of the even CTA issues the MMAs, the accumulators are
-// double-buffered in tensor memory and four warps per CTA store them.  Warp roles and
+// double-buffered in tensor memory and eight warps per CTA store them.  Warp roles and
 // unwinding as in the expert layer's grouped products.
 enum OrthPhase : int { kGram = 0, kPoly = 1, kUpdate = 2 };
 
 constexpr int kOrthStages = 6;
 constexpr int kStageBytes = 2 * 128 * 128;
-constexpr int kEpiWarpBytes = 2 * 4096;
+constexpr int kEpiWarps = 8;             // two for each quarter of the tensor memory's lanes
+constexpr int kOrthThreads = 64 + 32 * kEpiWarps;
+constexpr int kTileBytes = 32 * 32 * 2;  // what a warp stores at once
+constexpr int kEpiWarpBytes = 2 * kTileBytes;
 constexpr int kOrthBars = (2 * kOrthStages + 5) * 8 + 16;
-constexpr int kOrthSmem = 1024 + kOrthStages * kStageBytes + 4 * kEpiWarpBytes + kOrthBars;
+constexpr int kOrthSmem = 1024 + kOrthStages * kStageBytes + kEpiWarps * kEpiWarpBytes + kOrthBars;
 constexpr int kMaxOrthSteps = 32;
-constexpr int kUnitArrivals = 8;         // epilogue warps of a pair
+constexpr int kUnitArrivals = 2 * kEpiWarps;   // of a pair
 static_assert(kOrthSmem <= 232448, "shared memory budget");
 
 struct OrthMaps {
   CUtensorMap xk[2];   // X as a K-major operand, rows of A: box {64, 128}
   CUtensorMap xs[2];   //   rows of B: box {64, bn_sym / 2}
   CUtensorMap xn[2];   // X as the MN-major operand of the update: box {64, 64}
-  CUtensorMap xo[2];   // X as a result: box {64, 32}
-  CUtensorMap ak, as, ao, at;   // A likewise; at: mirrored, box {32, 64}
+  CUtensorMap xo[2];   // X as a result: box {32, 32}
+  CUtensorMap ak, as, ao, at;   // A likewise; at: mirrored
   CUtensorMap bk, bo, bt;       // B
 };
 
@@ -235,7 +238,7 @@ struct OrthArgs {
   int bn_sym, nt_sym;    // column tiles of the symmetric products: width and number
   int bn_upd, nt_upd;    // of the update
   int units_sym, units_upd;   // per matrix
-  float S2;              // A and B hold S2 times theirs
+  float S2, inv_S2;      // A and B hold S2 times theirs
   float out_scale;       // scale / S
   const __half* A;       // [batch][m][lda]
   int lda;
@@ -306,6 +309,24 @@ __device__ __forceinline__ void st_shared_v4u(uint32_t addr, uint32_t a, uint32_
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// Halves of a shared-memory descriptor (128-byte swizzle, 1024 bytes between groups of
+// eight rows): the low one with the address and the leading offset, the high one fixed.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return ((saddr >> 4) & 0x3fffu) | ((lbo_bytes >> 4) << 16);
+}
+__device__ __forceinline__ void orth_mma(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+  tc_mma2(d_tmem, static_cast<uint64_t>(hi) << 32 | a_lo, static_cast<uint64_t>(hi) << 32 | b_lo, idesc, accumulate);
+}
+
+// One lane of the (whole, converged) warp: unlike a comparison with the lane's number it
+// leaves the compiler's knowledge of what is the same in all lanes alone.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r) : : "memory");
+  return r != 0;
+}
+
 __device__ __forceinline__ int load_acquire(const int* p) {
   int v;
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -326,67 +347,51 @@ __device__ __forceinline__ bool orth_wait(const OrthArgs& a, const OrthUnit& u, 
   const uint64_t t0 = global_timer_ns();
   while (load_acquire(c) < target) {
     if (global_timer_ns() - t0 > timeout_ns) return false;
-    __nanosleep(32);
   }
   return true;
 }
 
-// Sixteen-bit values of a 32 x 64 tile (lane: row) to out[r0 + row][col + ...] or, with
-// `flip`, to its transpose, through the warp's stage of 4 KB.
+// Byte of 16-byte piece j of row r in a 32 x 32 tile of 16-bit values in the 64-byte
+// swizzle.
+__device__ __forceinline__ uint32_t tile_piece(int r, int j) { return r * 64 + ((j ^ ((r >> 1) & 3)) << 4); }
+
+// The bf16 values of a 32 x 32 tile (lane: row) to out[r0 + row][col + ...] or, with `flip`,
+// to its transpose, through the warp's stage of 2 KB.
 __device__ __forceinline__ void store_out(const OrthArgs& a, __nv_bfloat16* out, int r0, int col, int rows, int cols,
-                                          const float (&v)[64], uint8_t* stage_g, uint32_t stage_s, int lane) {
+                                          const float (&v)[32], uint8_t* stage_g, uint32_t stage_s, int lane) {
   __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(stage_g);
+  // rows of the stage are rows of out: the tile's own, or its columns
   if (!a.flip) {
-    // 32 rows of 64, 16-byte pieces at piece ^ (row & 7)
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      st_shared_v4u(stage_s + lane * 128 + ((j ^ (lane & 7)) << 4), pack_bf16(v[8 * j], v[8 * j + 1]),
-                    pack_bf16(v[8 * j + 2], v[8 * j + 3]), pack_bf16(v[8 * j + 4], v[8 * j + 5]),
-                    pack_bf16(v[8 * j + 6], v[8 * j + 7]));
-    __syncwarp();
-    if (a.vec) {
-      for (int r = lane >> 3; r < rows; r += 4) {
-        const int p = lane & 7;
-        const uint4 u = *reinterpret_cast<const uint4*>(stage_g + r * 128 + ((p ^ (r & 7)) << 4));
-        __nv_bfloat16* d = out + static_cast<int64_t>(r0 + r) * a.out_ld + col + 8 * p;
-        if (8 * p + 8 <= cols) {
-          *reinterpret_cast<uint4*>(d) = u;
-        } else {
-          const __nv_bfloat16* s = reinterpret_cast<const __nv_bfloat16*>(&u);
-          for (int k = 0; 8 * p + k < cols; ++k) d[k] = s[k];
-        }
-      }
-    } else {
-      for (int r = 0; r < rows; ++r)
-        for (int k = lane; k < cols; k += 32)
-          out[static_cast<int64_t>(r0 + r) * a.out_ld + col + k] = h[r * 64 + (((k >> 3) ^ (r & 7)) << 3) + (k & 7)];
-    }
+    for (int j = 0; j < 4; ++j)
+      st_shared_v4u(stage_s + tile_piece(lane, j), pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                    pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
   } else {
-    // the tile's columns are rows of out: 64 rows of 32
 #pragma unroll
-    for (int j = 0; j < 64; ++j) h[j * 32 + lane] = __float2bfloat16_rn(v[j]);
-    __syncwarp();
-    if (a.vec) {
-      for (int r = lane >> 2; r < cols; r += 8) {
-        const int p = lane & 3;
-        const uint4 u = *reinterpret_cast<const uint4*>(stage_g + r * 64 + p * 16);
-        __nv_bfloat16* d = out + static_cast<int64_t>(col + r) * a.out_ld + r0 + 8 * p;
-        if (8 * p + 8 <= rows) {
-          *reinterpret_cast<uint4*>(d) = u;
-        } else {
-          const __nv_bfloat16* s = reinterpret_cast<const __nv_bfloat16*>(&u);
-          for (int k = 0; 8 * p + k < rows; ++k) d[k] = s[k];
-        }
+    for (int j = 0; j < 32; ++j) h[tile_piece(j, lane >> 3) / 2 + (lane & 7)] = __float2bfloat16_rn(v[j]);
+  }
+  __syncwarp();
+  const int or0 = a.flip ? col : r0, oc0 = a.flip ? r0 : col, n = a.flip ? cols : rows, len = a.flip ? rows : cols;
+  if (a.vec) {
+    for (int r = lane >> 2; r < n; r += 8) {
+      const int p = lane & 3;
+      const uint4 u = *reinterpret_cast<const uint4*>(stage_g + tile_piece(r, p));
+      __nv_bfloat16* d = out + static_cast<int64_t>(or0 + r) * a.out_ld + oc0 + 8 * p;
+      if (8 * p + 8 <= len) {
+        *reinterpret_cast<uint4*>(d) = u;
+      } else {
+        const __nv_bfloat16* s = reinterpret_cast<const __nv_bfloat16*>(&u);
+        for (int k = 0; 8 * p + k < len; ++k) d[k] = s[k];
       }
-    } else {
-      for (int r = 0; r < cols; ++r)
-        if (lane < rows) out[static_cast<int64_t>(col + r) * a.out_ld + r0 + lane] = h[r * 32 + lane];
     }
+  } else if (lane < len) {
+    for (int r = 0; r < n; ++r)
+      out[static_cast<int64_t>(or0 + r) * a.out_ld + oc0 + lane] = h[tile_piece(r, lane >> 3) / 2 + (lane & 7)];
   }
   __syncwarp();
 }
 
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(kOrthThreads, 1)
     orth_steps_kernel(const __grid_constant__ OrthMaps maps, const __grid_constant__ OrthArgs args) {
   constexpr int STAGES = kOrthStages;
   extern __shared__ uint8_t smem_raw[];
@@ -394,7 +399,7 @@ __global__ void __launch_bounds__(192, 1)
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (sbase - raw);
   const uint32_t s_epi = sbase + STAGES * kStageBytes;
-  const uint32_t bars = s_epi + 4 * kEpiWarpBytes;
+  const uint32_t bars = s_epi + kEpiWarps * kEpiWarpBytes;
   const uint32_t full_bar = bars;                    // [STAGES]
   const uint32_t empty_bar = bars + 8 * STAGES;      // [STAGES]
   const uint32_t tfull_bar = bars + 16 * STAGES;     // [2]
@@ -417,11 +422,13 @@ __global__ void __launch_bounds__(192, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(tfull_bar + 8 * s, 1);
-      mbar_init(tempty_bar + 8 * s, 8);   // one lane of every epilogue warp of the pair
+      mbar_init(tempty_bar + 8 * s, 2 * kEpiWarps);   // one lane of every epilogue warp of the pair
     }
     mbar_init(drain_bar, 1);
     fence_barrier_init();
   }
+  if (warp == 2 && lane < static_cast<int>(sizeof(OrthMaps) / sizeof(CUtensorMap)))
+    prefetch_tmap(reinterpret_cast<const CUtensorMap*>(&maps) + lane);
   if (warp == 1) {
     tmem_alloc2(tmem_slot, 512);
     tmem_relinquish2();
@@ -444,60 +451,58 @@ __global__ void __launch_bounds__(192, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const uint32_t full_l = mapa_shared(full_bar, 0);   // the leader's, for the bytes of both
-      int stage = 0;
-      uint32_t phase = 0;
-      int64_t issued = 0;
-      bool ok = true;
-      for (int t = unit0; t < total && ok; t += ustride) {
-        const OrthUnit u = orth_unit(args, t);
-        if (!orth_wait(args, u, tmo)) {
-          record_error(args.err, kErrTimeout);
+    const uint32_t full_l = mapa_shared(full_bar, 0);   // the leader's, for the bytes of both
+    int stage = 0;
+    uint32_t phase = 0;
+    int64_t issued = 0;
+    bool ok = true;
+    for (int t = unit0; t < total && ok; t += ustride) {
+      const OrthUnit u = orth_unit(args, t);
+      if (!__all_sync(0xffffffffu, orth_wait(args, u, tmo))) {
+        if (lane == 0) record_error(args.err, kErrTimeout);
+        break;
+      }
+      asm volatile("fence.proxy.async;" ::: "memory");   // the loads see what the wait saw
+      const int x = u.step & 1;
+      const CUtensorMap* am = u.kind == kGram ? &maps.xk[x] : (u.kind == kPoly ? &maps.ak : &maps.bk);
+      const CUtensorMap* bm = u.kind == kGram ? &maps.xs[x] : (u.kind == kPoly ? &maps.as : &maps.xn[x]);
+      const bool upd = u.kind == kUpdate, two = upd && args.bn_upd == 256;
+      const uint32_t bytes = 128 * 128 + (upd ? (two ? 2 : 1) * 64 * 128 : args.bn_sym / 2 * 128);
+      const int ra = u.i * 256 + crank * 128, rb = u.c0 + crank * (u.nn >> 1);
+      const int nkb = num_kb(u);
+      for (int kb = 0; kb < nkb; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_wait(empty_bar + 8 * stage, phase ^ 1u, tmo))) {
+          if (lane == 0) record_error(args.err, kErrTimeout);
+          ok = false;
           break;
         }
-        asm volatile("fence.proxy.async;" ::: "memory");   // the loads see what the wait saw
-        const int x = u.step & 1;
-        const CUtensorMap* am = u.kind == kGram ? &maps.xk[x] : (u.kind == kPoly ? &maps.ak : &maps.bk);
-        const CUtensorMap* bm = u.kind == kGram ? &maps.xs[x] : (u.kind == kPoly ? &maps.as : &maps.xn[x]);
-        const int chunks = args.bn_upd == 256 ? 2 : 1;
-        const uint32_t bytes = 128 * 128 + (u.kind == kUpdate ? chunks * 64 * 128 : args.bn_sym / 2 * 128);
-        const int ra = u.i * 256 + crank * 128, rb = u.c0 + crank * (u.nn >> 1);
-        const int nkb = num_kb(u);
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(empty_bar + 8 * stage, phase ^ 1u, tmo)) {
-            record_error(args.err, kErrTimeout);
-            ok = false;
-            break;
-          }
-          const uint32_t sA = sbase + stage * kStageBytes, sB = sA + 128 * 128;
-          const uint32_t fb = full_l + 8 * stage;
+        const uint32_t sA = sbase + stage * kStageBytes, sB = sA + 128 * 128;
+        const uint32_t fb = full_l + 8 * stage;
+        const int k0 = kb * 64;
+        if (elect_one()) {
           if (leader) mbar_arrive_expect_tx(full_bar + 8 * stage, 2 * bytes);
-          tma_load_3d_g2(sA, am, fb, kb * 64, ra, u.e);
-          if (u.kind == kUpdate) {
-            tma_load_3d_g2(sB, bm, fb, rb, kb * 64, u.e);
-            if (chunks == 2) tma_load_3d_g2(sB + 64 * 128, bm, fb, rb + 64, kb * 64, u.e);
-          } else {
-            tma_load_3d_g2(sB, bm, fb, kb * 64, rb, u.e);
-          }
-          ++issued;
-          ring_next(stage, phase);
+          tma_load_3d_g2(sA, am, fb, k0, ra, u.e);
+          tma_load_3d_g2(sB, bm, fb, upd ? rb : k0, upd ? k0 : rb, u.e);
+          if (two) tma_load_3d_g2(sB + 64 * 128, bm, fb, rb + 64, k0, u.e);
         }
+        __syncwarp();
+        ++issued;
+        ring_next(stage, phase);
       }
-      // Before the CTAs may exit, every load issued must have landed: the leader's
-      // full barriers count the bytes of both.
-      if (leader) {
-        for (int s = 0; s < STAGES; ++s) {
-          const int64_t n_s = issued > s ? (issued - 1 - s) / STAGES + 1 : 0;
-          if (n_s > 0 && !mbar_wait(full_bar + 8 * s, static_cast<uint32_t>((n_s - 1) & 1), kDrain))
-            record_error(args.err, kErrTimeout);
-        }
+    }
+    // Before the CTAs may exit, every load issued must have landed: the leader's
+    // full barriers count the bytes of both.
+    if (leader && lane == 0) {
+      for (int s = 0; s < STAGES; ++s) {
+        const int64_t n_s = issued > s ? (issued - 1 - s) / STAGES + 1 : 0;
+        if (n_s > 0 && !mbar_wait(full_bar + 8 * s, static_cast<uint32_t>((n_s - 1) & 1), kDrain))
+          record_error(args.err, kErrTimeout);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (leader && lane == 0) {
+    if (leader) {
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
@@ -506,47 +511,55 @@ __global__ void __launch_bounds__(192, 1)
         const bool b_mn = u.kind == kUpdate;
         const uint32_t idesc = orth_idesc(b_mn, u.nn);
         const int nkb = num_kb(u);
+        // descriptors of stage 0, and what a step of 16 columns of K adds to B's: one
+        // thread issues everything, so each instruction of this loop counts
+        const uint32_t a0 = desc_lo(sbase, 16), b0 = desc_lo(sbase + 128 * 128, b_mn ? 64 * 128 : 16);
+        const uint32_t b_step = b_mn ? 16 * 128 / 16 : 32 / 16;
         // (the producer has waited for this unit's matrix before; its wait and the
         // loads may take two limits)
-        if (!mbar_wait(tempty_bar + 8 * acc, acc_phase ^ 1u, tmo)) {
-          record_error(args.err, kErrTimeout);
+        if (!__all_sync(0xffffffffu, mbar_wait(tempty_bar + 8 * acc, acc_phase ^ 1u, tmo))) {
+          if (lane == 0) record_error(args.err, kErrTimeout);
           break;
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
+        uint64_t limit = 2 * tmo;
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(full_bar + 8 * stage, phase, kb == 0 ? 2 * tmo : tmo)) {
-            record_error(args.err, kErrTimeout);
+          if (!__all_sync(0xffffffffu, mbar_wait(full_bar + 8 * stage, phase, limit))) {
+            if (lane == 0) record_error(args.err, kErrTimeout);
             ok = false;
             break;
           }
+          limit = tmo;
           tc_fence_after();
-          const uint32_t sA = sbase + stage * kStageBytes, sB = sA + 128 * 128;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t ad = smem_desc_sw128(sA + kk * 32, 16, 1024);
-            const uint64_t bd = b_mn ? smem_desc_sw128(sB + kk * 16 * 128, 64 * 128, 1024)
-                                     : smem_desc_sw128(sB + kk * 32, 16, 1024);
-            tc_mma2(d_tmem, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+          const uint32_t ad = a0 + stage * (kStageBytes / 16), bd = b0 + stage * (kStageBytes / 16);
+          if (elect_one()) {
+            orth_mma(d_tmem, ad, bd, idesc, kb != 0 ? 1u : 0u);
+            orth_mma(d_tmem, ad + 2, bd + b_step, idesc, 1u);
+            orth_mma(d_tmem, ad + 4, bd + 2 * b_step, idesc, 1u);
+            orth_mma(d_tmem, ad + 6, bd + 3 * b_step, idesc, 1u);
+            // the slot is free in both CTAs once these MMAs have read it
+            tc_commit2_mc(empty_bar + 8 * stage, kPairMask);
           }
-          // the slot is free in both CTAs once these MMAs have read it
-          tc_commit2_mc(empty_bar + 8 * stage, kPairMask);
+          __syncwarp();
           ring_next(stage, phase);
         }
         if (!ok) break;
-        tc_commit2_mc(tfull_bar + 8 * acc, kPairMask);
+        if (elect_one()) tc_commit2_mc(tfull_bar + 8 * acc, kPairMask);
+        __syncwarp();
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
       // one more commit arrives in both CTAs once everything issued has completed
-      tc_commit2_mc(drain_bar, kPairMask);
+      if (elect_one()) tc_commit2_mc(drain_bar, kPairMask);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;             // tensor-memory lanes, and rows of the CTA's 128
+    const int first = warp < 6 ? 0 : 32;   // every other 32 columns
     uint8_t* stage_g = gbase + (s_epi - sbase) + (warp - 2) * kEpiWarpBytes;
     const uint32_t stage_s = s_epi + (warp - 2) * kEpiWarpBytes;
     int buf = 0;
@@ -555,19 +568,28 @@ __global__ void __launch_bounds__(192, 1)
     for (int t = unit0; t < total; t += ustride) {
       const OrthUnit u = orth_unit(args, t);
       const int r0 = u.i * 256 + crank * 128 + q * 32;
+      const bool last = u.kind == kUpdate && u.step + 1 == args.steps;
+      const int cols = u.kind == kUpdate ? args.n : args.m;
+      const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
+      const float cI = args.coefs[u.step][0] * args.S2, cA = args.coefs[u.step][1];
+      const float ds = u.kind == kGram ? 1.f
+                       : u.kind == kPoly ? args.coefs[u.step][2] * args.inv_S2
+                                         : (last ? args.out_scale : 1.f) * args.inv_S2;
+      const CUtensorMap* om = u.kind == kGram ? &maps.ao : (u.kind == kPoly ? &maps.bo : &maps.xo[1 - (u.step & 1)]);
+      const CUtensorMap* tm = u.kind == kGram ? &maps.at : &maps.bt;
       int good = 1;
-      uint4 ax[8];      // poly: A's values of the chunk, ahead of the products
+      uint4 ax[4];      // poly: A's values of the columns, ahead of the products
       auto fetch_a = [&](int col) {
         const __half* p = args.A + u.e * args.astride + static_cast<int64_t>(r0 + lane) * args.lda + col;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)      // lda: a multiple of 8, as col is
+        for (int j = 0; j < 4; ++j)      // lda: a multiple of 8, as col is
           ax[j] = r0 + lane < args.m && col + 8 * j < args.lda ? __ldcg(reinterpret_cast<const uint4*>(p) + j)
                                                                : make_uint4(0u, 0u, 0u, 0u);
       };
       if (u.kind == kPoly) {
         if (lane == 0) good = orth_wait(args, u, 2 * tmo);
         good = __shfl_sync(0xffffffffu, good, 0);
-        if (good) fetch_a(u.c0);
+        if (good) fetch_a(u.c0 + first);
       }
       if (lane == 0 && good) good = mbar_wait(tfull_bar + 8 * acc, acc_phase, 3 * tmo);
       good = __shfl_sync(0xffffffffu, good, 0);
@@ -576,24 +598,15 @@ __global__ void __launch_bounds__(192, 1)
         break;
       }
       tc_fence_after();
-      const bool last = u.kind == kUpdate && u.step + 1 == args.steps;
-      const int cols = u.kind == kUpdate ? args.n : args.m;
-      const uint32_t tacc = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * 256;
-      const float cI = args.coefs[u.step][0] * args.S2, cA = args.coefs[u.step][1];
-      const float ds = u.kind == kGram ? 1.f
-                       : u.kind == kPoly ? args.coefs[u.step][2] / args.S2
-                                         : (last ? args.out_scale : 1.f) / args.S2;
-      const CUtensorMap* om = u.kind == kGram ? &maps.ao : (u.kind == kPoly ? &maps.bo : &maps.xo[1 - (u.step & 1)]);
-      const CUtensorMap* tm = u.kind == kGram ? &maps.at : &maps.bt;
       if (r0 < args.m) {
 #pragma unroll 1
-        for (int c = 0; c < u.nn; c += 64) {
-          float v[64];
-          tmem_ld64(tacc + c, v);
+        for (int c = first; c < u.nn; c += 64) {
+          float v[32];
+          tmem_ld32(tacc + c, v);
           const int row = r0 + lane, col = u.c0 + c;
           if (u.kind == kPoly) {
 #pragma unroll
-            for (int j = 0; j < 64; j += 8) {
+            for (int j = 0; j < 32; j += 8) {
               float x[8];
               const uint32_t w[4] = {ax[j / 8].x, ax[j / 8].y, ax[j / 8].z, ax[j / 8].w};
 #pragma unroll
@@ -610,22 +623,22 @@ __global__ void __launch_bounds__(192, 1)
             if (c + 64 < u.nn) fetch_a(col + 64);
           } else {
 #pragma unroll
-            for (int j = 0; j < 64; ++j) v[j] *= ds;
+            for (int j = 0; j < 32; ++j) v[j] *= ds;
           }
+          if (col >= cols) break;      // (nn is rounded up)
           if (last) {
-            store_out(args, args.out + u.e * args.out_stride, r0, col, min(32, args.m - r0), min(64, cols - col), v,
+            store_out(args, args.out + u.e * args.out_stride, r0, col, min(32, args.m - r0), min(32, cols - col), v,
                       stage_g, stage_s, lane);
             continue;
           }
-          // 32 rows of 64 values, in the 128-byte swizzle, stored by one lane
-          const uint32_t st = stage_s + buf * 4096;
+          // 32 rows of 32 values, stored by one lane
+          const uint32_t st = stage_s + buf * kTileBytes;
           if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            st_shared_v4u(st + lane * 128 + ((j ^ (lane & 7)) << 4), pack_half(v[8 * j], v[8 * j + 1]),
-                          pack_half(v[8 * j + 2], v[8 * j + 3]), pack_half(v[8 * j + 4], v[8 * j + 5]),
-                          pack_half(v[8 * j + 6], v[8 * j + 7]));
+          for (int j = 0; j < 4; ++j)
+            st_shared_v4u(st + tile_piece(lane, j), pack_half(v[8 * j], v[8 * j + 1]), pack_half(v[8 * j + 2], v[8 * j + 3]),
+                          pack_half(v[8 * j + 4], v[8 * j + 5]), pack_half(v[8 * j + 6], v[8 * j + 7]));
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
@@ -634,13 +647,13 @@ __global__ void __launch_bounds__(192, 1)
           }
           buf ^= 1;
           if (u.mirror) {
-            // 64 rows (the tile's columns) of 32 values
-            const uint32_t tt = stage_s + buf * 4096;
+            // the tile's columns as rows
+            const uint32_t tt = stage_s + buf * kTileBytes;
             if (lane == 0) bulk_wait_read<1>();
             __syncwarp();
-            __half* h = reinterpret_cast<__half*>(stage_g + buf * 4096);
+            __half* h = reinterpret_cast<__half*>(stage_g + buf * kTileBytes);
 #pragma unroll
-            for (int j = 0; j < 64; ++j) h[j * 32 + lane] = __float2half_rn(v[j]);
+            for (int j = 0; j < 32; ++j) h[j * 32 + lane] = __float2half_rn(v[j]);
             fence_async_shared();
             __syncwarp();
             if (lane == 0) {
@@ -659,10 +672,9 @@ __global__ void __launch_bounds__(192, 1)
           mbar_arrive(tempty_bar + 8 * acc);
         else
           mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar + 8 * acc, 0));
-        // and, once the stores have landed, the tile to the next phase
         if (!last) {
+          // (a completed bulk store is ordered before what follows without a proxy fence)
           bulk_wait_all();
-          asm volatile("fence.proxy.async;" ::: "memory");
           add_release(args.counters + u.phase * args.batch + u.e, 1);
         }
       }
@@ -699,7 +711,7 @@ cudaError_t orth_pairs(int sms, int* pairs) {
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
-  cfg.blockDim = dim3(192);
+  cfg.blockDim = dim3(kOrthThreads);
   cfg.dynamicSmemBytes = kOrthSmem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -722,7 +734,7 @@ cudaError_t launch_orth_steps(const OrthMaps& maps, const OrthArgs& args, int sm
   const int64_t units = static_cast<int64_t>(args.steps) * args.batch * (2 * args.units_sym + args.units_upd);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(units, pairs)));
-  cfg.blockDim = dim3(192);
+  cfg.blockDim = dim3(kOrthThreads);
   cfg.dynamicSmemBytes = kOrthSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -1260,7 +1272,7 @@ OrthIn orth_in(const void* g, int32_t dtype, int64_t e0, int batch, int64_t M, i
 
 // Width of the column tiles: the one with the least time.  Full tiles are bound by the
 // products, narrower ones by their loads (16 KB for the rows of A whatever their width):
-// in units of a full tile's 256 they take 183 and 152, and each about 32 for its start
+// in units of a full tile's 256 they take 164 and 148, and each about 32 for its start
 // and end.  One matrix alone waits for each phase's last tiles, several fill one
 // another's.
 template <typename F>
@@ -1269,7 +1281,7 @@ int orth_width(const F& units, int batch, int pairs) {
   double least = 1e300;
   for (int bn = 256; bn >= 64; bn /= 2) {
     const double waves = static_cast<double>(units(bn)) * batch / pairs;
-    const double each = 32 + (bn == 256 ? 256 : bn == 128 ? 183 : 152);
+    const double each = 32 + (bn == 256 ? 256 : bn == 128 ? 164 : 148);
     const double t = (batch == 1 ? std::ceil(waves) : std::max(1.0, waves)) * each;
     if (t < least) least = t, best = bn;
   }
@@ -1287,7 +1299,7 @@ void orth_tiles(OrthArgs* a, int pairs) {
 }
 
 bool orth_maps(OrthMaps* t, const OrthPlan& p, const OrthArgs& a, __half* const* x, const __half* A, const __half* B) {
-  const auto SW = CU_TENSOR_MAP_SWIZZLE_128B, NOSW = CU_TENSOR_MAP_SWIZZLE_NONE;
+  const auto SW = CU_TENSOR_MAP_SWIZZLE_128B, SW64 = CU_TENSOR_MAP_SWIZZLE_64B, NOSW = CU_TENSOR_MAP_SWIZZLE_NONE;
   const uint64_t m = p.m, n = p.n, C = a.batch, lda = p.lda;
   const uint32_t bs = a.bn_sym / 2;
   bool ok = true;
@@ -1295,11 +1307,11 @@ bool orth_maps(OrthMaps* t, const OrthPlan& p, const OrthArgs& a, __half* const*
     ok = ok && abi_map_half(&t->xk[i], x[i], n, m, C, p.ldx, 64, 128, SW) &&
          abi_map_half(&t->xs[i], x[i], n, m, C, p.ldx, 64, bs, SW) &&
          abi_map_half(&t->xn[i], x[i], n, m, C, p.ldx, 64, 64, SW) &&
-         abi_map_half(&t->xo[i], x[i], n, m, C, p.ldx, 64, 32, SW);
+         abi_map_half(&t->xo[i], x[i], n, m, C, p.ldx, 32, 32, SW64);
   return ok && abi_map_half(&t->ak, A, m, m, C, lda, 64, 128, SW) && abi_map_half(&t->as, A, m, m, C, lda, 64, bs, SW) &&
-         abi_map_half(&t->ao, A, m, m, C, lda, 64, 32, SW) && abi_map_half(&t->at, A, m, m, C, lda, 32, 64, NOSW) &&
-         abi_map_half(&t->bk, B, m, m, C, lda, 64, 128, SW) && abi_map_half(&t->bo, B, m, m, C, lda, 64, 32, SW) &&
-         abi_map_half(&t->bt, B, m, m, C, lda, 32, 64, NOSW);
+         abi_map_half(&t->ao, A, m, m, C, lda, 32, 32, SW64) && abi_map_half(&t->at, A, m, m, C, lda, 32, 32, NOSW) &&
+         abi_map_half(&t->bk, B, m, m, C, lda, 64, 128, SW) && abi_map_half(&t->bo, B, m, m, C, lda, 32, 32, SW64) &&
+         abi_map_half(&t->bt, B, m, m, C, lda, 32, 32, NOSW);
 }
 
 }  // namespace
@@ -1369,7 +1381,7 @@ moe_status moe_orthogonalize(int64_t E, int64_t M, int64_t N, int32_t dtype, con
   OrthArgs args = {};
   args.m = p.m, args.n = p.n, args.steps = steps;
   args.mt = (p.m + 255) / 256;
-  args.S2 = S * S, args.out_scale = scale / S;
+  args.S2 = S * S, args.inv_S2 = 1.f / args.S2, args.out_scale = scale / S;
   args.A = a, args.lda = p.lda, args.astride = static_cast<int64_t>(p.m) * p.lda;
   args.out_ld = out_ld, args.out_stride = out_stride, args.flip = p.flip;
   args.counters = counters;
