@@ -311,12 +311,12 @@ __device__ __forceinline__ void st_shared_v4u(uint32_t addr, uint32_t a, uint32_
 
 // Halves of a shared-memory descriptor (128-byte swizzle, 1024 bytes between groups of
 // eight rows): the low one with the address and the leading offset, the high one fixed.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
   return ((saddr >> 4) & 0x3fffu) | ((lbo_bytes >> 4) << 16);
 }
 __device__ __forceinline__ void orth_mma(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
-  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
-  tc_mma2(d_tmem, static_cast<uint64_t>(hi) << 32 | a_lo, static_cast<uint64_t>(hi) << 32 | b_lo, idesc, accumulate);
+  tc_mma2(d_tmem, static_cast<uint64_t>(kDescHi) << 32 | a_lo, static_cast<uint64_t>(kDescHi) << 32 | b_lo, idesc, accumulate);
 }
 
 // One lane of the (whole, converged) warp: unlike a comparison with the lane's number it
@@ -797,6 +797,10 @@ __device__ __forceinline__ void st_cluster1(uint32_t addr, float a) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(a) : "memory");
 }
 
+__device__ __forceinline__ void small_mma(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  tc_mma<false>(d_tmem, static_cast<uint64_t>(kDescHi) << 32 | a_lo, static_cast<uint64_t>(kDescHi) << 32 | b_lo, idesc, accumulate);
+}
+
 // Byte of element (row, column) in blocks of 64 columns in the 128-byte swizzle.
 __device__ __forceinline__ uint32_t swz(int r, int c) {
   return (c >> 6) * kChunkBytes + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4) + (c & 7) * 2;
@@ -922,6 +926,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
   const int mc = (a.m + 15) & ~15;               // columns of A and B
   const uint32_t idesc_sym = (1u << 4) | (static_cast<uint32_t>(mc >> 3) << 17) | ((128u >> 4) << 24);
   const float S2 = a.S * a.S;
+  // descriptors: X as the K-major and as the MN-major operand, A, B
+  const uint32_t dX = desc_lo(sX, 16), dXn = desc_lo(sX, kChunkBytes), dA = desc_lo(sA, 16), dB = desc_lo(sB, 16);
   uint32_t phase[2] = {0, 0};
   auto wait = [&](int b) {
     if (!mbar_wait(bars + 8 * b, phase[b], a.timeout_ns)) record_error(a.err, kErrTimeout);
@@ -931,10 +937,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
 
   for (int step = 0; step < a.steps; ++step) {
     // ---- gram
-    if (tid == 0) {
-      for (int k = 0; k < a.chunks * 4; ++k) {
-        const uint64_t d = smem_desc_sw128(sX + (k >> 2) * kChunkBytes + (k & 3) * 32, 16, 1024);
-        tc_mma<false>(tmem, d, d, idesc_sym, k != 0 ? 1u : 0u);
+    if (warp == 0 && elect_one()) {
+#pragma unroll 1
+      for (int c = 0; c < a.chunks; ++c) {
+        const uint32_t d = dX + c * (kChunkBytes / 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) small_mma(tmem, d + 2 * k, d + 2 * k, idesc_sym, c + k != 0 ? 1u : 0u);
       }
       tc_commit(bars);
     }
@@ -985,12 +993,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
       __syncthreads();
     }
     // ---- poly
-    if (tid == 0) {
+    if (warp == 0 && elect_one()) {
       tc_fence_after();
       asm volatile("fence.proxy.async;" ::: "memory");
+#pragma unroll 1
       for (int k = 0; k < mc / 16; ++k) {
-        const uint64_t d = smem_desc_sw128(sA + (k >> 2) * kChunkBytes + (k & 3) * 32, 16, 1024);
-        tc_mma<false>(tmem + 128, d, d, idesc_sym, k != 0 ? 1u : 0u);
+        const uint32_t d = dA + (k >> 2) * (kChunkBytes / 16) + 2 * (k & 3);
+        small_mma(tmem + 128, d, d, idesc_sym, k != 0 ? 1u : 0u);
       }
       tc_commit(bars);
     }
@@ -1026,17 +1035,19 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
     // ---- update: groups of 256 columns, the first into columns 256.. of the tensor
     // memory, the second into 0..255, where gram and poly are done with
     const int ngroups = (a.chunks + 3) >> 2;
-    if (tid == 0) {
+    if (warp == 0 && elect_one()) {
       tc_fence_after();
+#pragma unroll 1
       for (int b = 0; b < ngroups; ++b) {
         const int cols = min(256, width - 256 * b);
         const uint32_t idesc = (1u << 4) | (1u << 16) | (static_cast<uint32_t>(cols >> 3) << 17) | ((128u >> 4) << 24);
+        const uint32_t x = dXn + 4 * b * (kChunkBytes / 16);
+#pragma unroll 1
         for (int k = 0; k < mc / 16; ++k) {
-          const uint64_t x = smem_desc_sw128(sX + 4 * b * kChunkBytes + k * 16 * 128, kChunkBytes, 1024);
-#pragma unroll
-          for (int part = 0; part < 2; ++part)      // B's fp16 values, and what they left
-            tc_mma<false>(tmem + 256 * (1 - b), smem_desc_sw128(sB + (2 * part + (k >> 2)) * kChunkBytes + (k & 3) * 32, 16, 1024),
-                          x, idesc, (k | part) != 0 ? 1u : 0u);
+          const uint32_t d = dB + (k >> 2) * (kChunkBytes / 16) + 2 * (k & 3);
+          // B's fp16 values, and what they left
+          small_mma(tmem + 256 * (1 - b), d, x + k * 128, idesc, k != 0 ? 1u : 0u);
+          small_mma(tmem + 256 * (1 - b), d + 2 * (kChunkBytes / 16), x + k * 128, idesc, 1u);
         }
         tc_commit(bars + 8 * b);
       }
@@ -1089,8 +1100,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
     tc_fence_after();
   }
   // every product has completed before the tensor memory is given back
-  if (tid == 0) {
-    tc_commit(bars + 16);
+  if (warp == 0) {
+    if (elect_one()) tc_commit(bars + 16);
     if (!mbar_wait(bars + 16, 0, 1000000000ull)) record_error(a.err, kErrTimeout);
   }
   __syncthreads();
