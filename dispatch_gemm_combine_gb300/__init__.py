@@ -352,9 +352,10 @@ def _ptr(t):
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
-    # the raw handle of torch.cuda.current_stream(), without the Stream object
-    import torch
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    # the raw handle of torch.cuda.current_stream(), without the Stream object (the
+    # tensors of the call are on the GPU, so torch's part of it is awake)
+    from torch import _C
+    return _C._cuda_getCurrentRawStream(_C._cuda_getDevice())
 
 
 def _check(status, where):

@@ -790,8 +790,8 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void st_cluster2(uint32_t addr, uint32_t a, uint32_t b) {
-  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+__device__ __forceinline__ void st_cluster4u(uint32_t addr, const uint4& u) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w) : "memory");
 }
 __device__ __forceinline__ void st_cluster1(uint32_t addr, float a) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(a) : "memory");
@@ -828,7 +828,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
   uint8_t* gbase = smem_raw + (sbase - raw);
   const uint32_t sX = sbase, sA = sX + a.chunks * kChunkBytes, sP = sA + 2 * kChunkBytes, sB = sP;
   const uint32_t bars = sP + 4 * kChunkBytes, slots = bars + 32, tmem_slot = bars + 24;
-  uint8_t *gX = gbase, *gA = gbase + (sA - sbase);
+  uint8_t *gX = gbase, *gA = gbase + (sA - sbase), *gB = gbase + (sB - sbase);
   const float* gslots = reinterpret_cast<const float*>(gbase + (slots - sbase));   // [ranks][3]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -860,20 +860,27 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
       c = i % (width / 8) * 8;
     }
   };
-  // (groups is a multiple of 2 kSmallThreads: 128 rows of a multiple of 64 columns)
-  constexpr int U = 2;
-  auto fetch = [&](int i0, float (&v)[U][8]) {
+  // up to 3 blocks of columns stay in registers between the two (groups is a multiple
+  // of 2 kSmallThreads: 128 rows of a multiple of 64 columns)
+  constexpr int U = 6;
+  float v[U][8];
+  auto fetch = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      int r, c;
-      at(i0 + u * kSmallThreads, r, c);
-      small_load8<E, FLIP>(a.in, g, r, first + c, v[u]);
+      const int i = i0 + u * kSmallThreads;
+      if (i < groups) {
+        int r, c;
+        at(i, r, c);
+        small_load8<E, FLIP>(a.in, g, r, first + c, v[u]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[u][k] = 0.f;
+      }
     }
   };
   Squares s;
   for (int i = tid; i < groups; i += U * kSmallThreads) {
-    float v[U][8];
-    fetch(i, v);
+    fetch(i);
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -896,13 +903,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
       s.mid += gslots[3 * k], s.big += gslots[3 * k + 1], s.small += gslots[3 * k + 2];
   }
   const float2 f = orth_factor_of(s, a.eps, a.S);
-  for (int i = tid; i < groups; i += U * kSmallThreads) {
-    float v[U][8];
-    fetch(i, v);
+  for (int i0 = tid; i0 < groups; i0 += U * kSmallThreads) {
+    if (groups > U * kSmallThreads) fetch(i0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kSmallThreads;
+      if (i >= groups) break;
       int r, c;
-      at(i + u * kSmallThreads, r, c);
+      at(i, r, c);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[u][k] = v[u][k] * f.x * f.y;
       if (FLIP) {
@@ -966,22 +974,31 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
     if (a.ranks > 1) {
       __syncwarp();
       cluster_sync();
-      const int rows = 128 / a.ranks;
+      // this CTA's share of the rows: the ranks' sums in order, then to all of them
+      // (sent to this CTA's memory from the lanes that hold them, a row each, the sums
+      // take 2 us more a step: neighbours have to be read and written side by side)
+      const int rows = 128 / a.ranks, r0 = rank * rows;
       for (int i = tid; i < rows * 32; i += kSmallThreads) {
-        const int r = rank * rows + (i >> 5), p = i & 31;
+        const int r = r0 + (i >> 5), p = i & 31;
         if (4 * p >= mc) continue;      // (rows past m are zeros, and wanted as such)
         float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-        const uint32_t at_p = sP + r * 512 + (p ^ (r & 7)) * 16;
-        for (int k = 0; k < a.ranks; k += 4) {      // four loads at a time, added in order
-          float4 v[4];
+        const uint32_t from = sP + r * 512 + (p ^ (r & 7)) * 16;
+        for (int k = 0; k < a.ranks; k += 8) {
+          float4 x[8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            v[j] = k + j < a.ranks ? ld_cluster4(mapa_shared(at_p, k + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int j = 0; j < 8; ++j)
+            x[j] = k + j < a.ranks ? ld_cluster4(mapa_shared(from, k + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) t.x += v[j].x, t.y += v[j].y, t.z += v[j].z, t.w += v[j].w;
+          for (int j = 0; j < 8; ++j) t.x += x[j].x, t.y += x[j].y, t.z += x[j].z, t.w += x[j].w;
         }
-        const uint32_t lo = pack_half(t.x, t.y), hi = pack_half(t.z, t.w), at_a = sA + swz(r, 4 * p);
-        for (int k = 0; k < a.ranks; ++k) st_cluster2(mapa_shared(at_a, k), lo, hi);
+        *reinterpret_cast<uint2*>(gA + swz(r, 4 * p)) = make_uint2(pack_half(t.x, t.y), pack_half(t.z, t.w));
+      }
+      __syncthreads();
+      for (int i = tid; i < rows * 16 * a.ranks; i += kSmallThreads) {
+        const int k = i / (rows * 16), j = i - k * (rows * 16), r = r0 + (j >> 4), c = (j & 15) * 8;
+        if (k == rank || c >= mc) continue;
+        const uint4 u = *reinterpret_cast<const uint4*>(gA + swz(r, c));
+        st_cluster4u(mapa_shared(sA + swz(r, c), k), u);
       }
       asm volatile("fence.proxy.async;" ::: "memory");
       tc_fence_before();
@@ -1018,8 +1035,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
         for (int k = 0; k < 4; ++k) {
           const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
           float b0 = fmaf(cA, x.x, cP * v[8 * j + 2 * k]), b1 = fmaf(cA, x.y, cP * v[8 * j + 2 * k + 1]);
-          if (row == c + 8 * j + 2 * k) b0 += cI;
-          if (row == c + 8 * j + 2 * k + 1) b1 += cI;
+          if (c == q * 32) {      // (the warp's diagonal block)
+            if (lane == 8 * j + 2 * k) b0 += cI;
+            if (lane == 8 * j + 2 * k + 1) b1 += cI;
+          }
           const __half2 h = __floats2half2_rn(b0, b1);
           const float2 f = __half22float2(h);
           o[k] = *reinterpret_cast<const uint32_t*>(&h);
@@ -1184,9 +1203,13 @@ int64_t sym_units(int64_t m, int bn) {
   return mt * nt - f * mt * (mt - 1) / 2;
 }
 
-// Matrices go through in chunks of about kChunkUnits tiles of a product, so the
-// workspace does not grow with E.
+// Matrices go through in chunks of about kChunkUnits tiles of a product and at most
+// kChunkBytesMax of workspace (or one matrix's), so the workspace does not grow with E.
 constexpr int kChunkUnits = 1200;
+constexpr int64_t kChunkBytesMax = 1ll << 30;
+
+// The limit of a wait, of which the kernels take up to four at once.
+uint64_t orth_limit() { return std::min<uint64_t>(abi_wait_timeout_ns(), 1ull << 60); }
 
 bool orth_plan(int64_t E, int64_t M, int64_t N, OrthPlan* p) {
   if (E < 0 || M < 1 || N < 1 || M > kMaxOrthSide || N > kMaxOrthSide) return false;
@@ -1203,7 +1226,8 @@ bool orth_plan(int64_t E, int64_t M, int64_t N, OrthPlan* p) {
     return true;
   }
   const int64_t units = sym_units(p->m, 256);
-  p->chunk = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({E, (kChunkUnits + units - 1) / units, 4096})));
+  const int64_t bytes = 4ll * p->m * (p->ldx + p->lda);      // of a matrix: X twice, A and B
+  p->chunk = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({E, (kChunkUnits + units - 1) / units, kChunkBytesMax / bytes})));
   const int64_t want = std::min<int64_t>((M * N + kNormElems - 1) / kNormElems, kNormBlocks / p->chunk);
   p->nparts = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, M, kMaxParts})));
   p->part_rows = static_cast<int>((M + p->nparts - 1) / p->nparts);
@@ -1365,7 +1389,7 @@ moe_status moe_orthogonalize(int64_t E, int64_t M, int64_t N, int32_t dtype, con
     a.eps = eps, a.S = S, a.out_scale = scale / S;
     a.out_ld = out_ld, a.out_stride = out_stride;
     a.err = static_cast<int*>(ws);
-    a.timeout_ns = abi_wait_timeout_ns();
+    a.timeout_ns = orth_limit();
     for (int i = 0; i < steps; ++i)
       for (int k = 0; k < 3; ++k) a.coefs[i][k] = coefs ? coefs[3 * i + k] : kDefaultCoefs[k];
     for (int64_t e0 = 0; e0 < E; e0 += p.chunk) {
@@ -1397,7 +1421,7 @@ moe_status moe_orthogonalize(int64_t E, int64_t M, int64_t N, int32_t dtype, con
   args.out_ld = out_ld, args.out_stride = out_stride, args.flip = p.flip;
   args.counters = counters;
   args.err = static_cast<int*>(ws);
-  args.timeout_ns = abi_wait_timeout_ns();
+  args.timeout_ns = orth_limit();
   for (int i = 0; i < steps; ++i)
     for (int k = 0; k < 3; ++k) args.coefs[i][k] = coefs ? coefs[3 * i + k] : kDefaultCoefs[k];
   for (int64_t e0 = 0; e0 < E; e0 += p.chunk) {

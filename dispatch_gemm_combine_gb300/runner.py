@@ -133,9 +133,10 @@ class LayerRunner:
                 self.ws_route_bwd = route_bwd_workspace(self.shape, self.device)
                 self.d_logits = torch.empty((T, E), dtype=torch.float32, device=self.device)
                 self.losses = torch.empty(2, dtype=torch.float32, device=self.device)
-        route_bwd(self.shape, logits, self.d_logits, self.ws_route_bwd, topk_idx, topk_w,
-                  self.d_topk_w if d_topk_w is None else d_topk_w, self.plan_t["counts"], balance, z,
-                  self.losses, stream)
+        if d_topk_w is None:
+            d_topk_w = getattr(self, "d_topk_w", None)      # (none without a backward)
+        route_bwd(self.shape, logits, self.d_logits, self.ws_route_bwd, topk_idx, topk_w, d_topk_w,
+                  self.plan_t["counts"], balance, z, self.losses, stream)
         return self.d_logits, self.losses
 
     def orthogonalize(self, gate_up=None, down=None, steps=5, coefs=None, eps=1e-7, scale=1.0,

@@ -90,7 +90,7 @@ def check(g, **kw):
 
 
 SHAPES = [(1, 1), (1, 7), (7, 1), (3, 5), (16, 16), (8, 200), (64, 64), (65, 63), (128, 128), (129, 127), (128, 300), (300, 128),
-          (257, 255), (255, 513), (256, 256), (512, 512), (640, 384), (1000, 40), (40, 1001), (511, 1029), (2880, 128), (100, 512), (513, 33), (128, 2049), (4096, 72), (24, 4097)]
+          (257, 255), (255, 513), (256, 256), (512, 512), (640, 384), (1000, 40), (40, 1001), (511, 1029), (2880, 128), (100, 512), (513, 33), (128, 2049), (4096, 72), (24, 4097), (1, 5000), (4100, 3), (130, 20000)]
 
 
 @pytest.mark.parametrize("M,N", SHAPES)
@@ -203,6 +203,28 @@ def test_broadcast_input():
     assert torch.equal(out[0], run(g)) and torch.equal(out[1], out[0]) and torch.equal(out[2], out[0])
 
 
+def test_repeats_bit_for_bit():
+    for shape in ((5, 100, 700), (5, 500, 700), (2, 1500, 700)):
+        g = draw(shape, torch.float32)
+        want = run(g)
+        assert all(torch.equal(run(g), want) for _ in range(3))
+
+
+def test_two_streams_at_once():
+    a, b, c = draw((4, 600, 900), torch.float32), draw((3, 700, 500), torch.bfloat16), draw((9, 60, 900), torch.float32)
+    want = [run(t) for t in (a, b, c)]
+    outs, wss = [torch.zeros_like(w) for w in want], [moe.orthogonalize_workspace(t) for t in (a, b, c)]
+    streams = [torch.cuda.Stream() for _ in want]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for t, o, ws, s in zip((a, b, c), outs, wss, streams):
+            moe.orthogonalize(t, o, ws, stream=s)
+    torch.cuda.synchronize()
+    for ws in wss:
+        moe.check_device_error(ws)
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
 def test_steps_scale_and_coefficients():
     g = draw((2, 150, 280), torch.float32)
     for steps in (1, 2, 8):
@@ -280,3 +302,13 @@ def test_a_wait_that_runs_out_is_reported():
     with pytest.raises(moe.MoeError):
         moe.check_device_error(ws)
     assert torch.equal(run(g, ws=ws), want)
+
+
+def test_waits_without_a_limit():
+    g = draw((2, 300, 300), torch.float32)
+    want = run(g)
+    before = moe.moe_set_wait_timeout_ns(2 ** 64 - 1)
+    try:
+        assert torch.equal(run(g), want)
+    finally:
+        moe.moe_set_wait_timeout_ns(before)

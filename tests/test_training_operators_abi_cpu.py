@@ -64,6 +64,8 @@ def test_orthogonalize_refusals(L):
         assert L.moe_orthogonalize_workspace_size(*bad) == 0
     # the workspace is that of the matrices that go through at once
     assert L.moe_orthogonalize_workspace_size(4096, 2880, 2880) == L.moe_orthogonalize_workspace_size(64, 2880, 2880)
+    for M, N in ((129, 65536), (2880, 5760), (140, 300)):
+        assert L.moe_orthogonalize_workspace_size(1 << 30, M, N) < (5 << 28)
     # that of the transposes, and no less for more matrices
     for M, N in ((300, 5000), (2880, 2880), (129, 40000), (1000, 1200), (64, 9000)):
         sizes = [L.moe_orthogonalize_workspace_size(E, M, N) for E in (0, 1, 2, 3, 7, 40, 1000)]
