@@ -41,11 +41,12 @@ struct RouteBwd {
   const float* dw;
   float* d;
   float* part;      // [blocks][2]: sums of F and of l^2, or null
+  float* losses;
   int* err;
   int64_t T;
   int E, k;
   float balance_T, z2_T;   // balance / T, 2 z / T
-  float f_scale;           // E / (T k)
+  float f_scale, inv_T;    // E / (T k), 1 / T
   int softmax;             // the losses or their gradients are wanted
 };
 
@@ -137,6 +138,8 @@ __global__ void __launch_bounds__(32 * kWarps) route_bwd_kernel(const RouteBwd a
   int id = -1, n_id = -1;
   float w = 0.f, dw = 0.f, n_w = 0.f, n_dw = 0.f;
   auto choice = [&](int64_t row) {
+    // (kept and advanced, the addresses cost a quarter of the warps: 65536 x 256 41 us
+    // instead of 31)
     if (chosen && g < a.k && row < a.T) {
       n_id = __ldg(a.idx + row * a.k + g);
       n_w = __ldg(a.w + row * a.k + g);
@@ -246,7 +249,10 @@ __global__ void __launch_bounds__(32 * kWarps) route_bwd_kernel(const RouteBwd a
   if (threadIdx.x < 2) {
     float s = 0.f;
     for (int i = 0; i < kWarps; ++i) s += sums[i][threadIdx.x];
-    a.part[2 * blockIdx.x + threadIdx.x] = s;
+    if (gridDim.x == 1)
+      a.losses[threadIdx.x] = s * a.inv_T;      // no other block's to be added
+    else
+      a.part[2 * blockIdx.x + threadIdx.x] = s;
   }
 }
 
@@ -286,6 +292,8 @@ cudaError_t launch_route_bwd_v(const RouteBwd& a, int sms, int* blocks, cudaStre
   const cudaError_t e = allow_smem(route_bwd_kernel<G, PER, VEC>, ready);
   if (e != cudaSuccess) return e;
   *blocks = static_cast<int>(std::min<int64_t>((a.T + R - 1) / R, std::min(kMaxRouteBlocks, sms * per_sm)));
+  // two rounds of one block take less than a second kernel for the blocks' sums
+  if (*blocks == 2 && a.losses) *blocks = 1;
   route_bwd_kernel<G, PER, VEC><<<*blocks, 32 * kWarps, smem, st>>>(a);
   return cudaGetLastError();
 }
@@ -338,30 +346,33 @@ moe_status moe_route_bwd(const moe_shape* s, const float* logits, const int32_t*
   a.err = static_cast<int*>(ws);
   a.T = s->T, a.E = s->E, a.k = s->k;
   a.balance_T = static_cast<float>(balance / T), a.z2_T = static_cast<float>(2.0 * z / T);
-  a.f_scale = static_cast<float>(s->E / (T * s->k));
+  a.losses = losses;
+  a.f_scale = static_cast<float>(s->E / (T * s->k)), a.inv_T = static_cast<float>(1.0 / T);
   a.softmax = softmax ? 1 : 0;
   const int E = s->E;
   int blocks = 0;
-  const cudaError_t e = abi_tracked(kAbiRouteBwd, losses ? 2 : 1, st, [&] {
+  cudaError_t e = abi_tracked(kAbiRouteBwd, 1, st, [&] {
     // a choice per lane: k lanes at least
-    const cudaError_t r = E <= 64 && s->k <= 8 ? launch_route_bwd<8, 8>(a, sms, &blocks, st)
-                          : E <= 128 && s->k <= 16 ? launch_route_bwd<16, 8>(a, sms, &blocks, st)
-                          : E <= 256 ? launch_route_bwd<32, 8>(a, sms, &blocks, st)
-                          : E <= 512 ? launch_route_bwd<32, 16>(a, sms, &blocks, st)
-                                     : launch_route_bwd<32, 32>(a, sms, &blocks, st);
-    if (r != cudaSuccess || !losses) return r;
-    // (may start while the last rows are done)
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, route_losses_kernel, static_cast<const float*>(a.part), blocks, static_cast<float>(1.0 / T), losses);
+    return E <= 64 && s->k <= 8     ? launch_route_bwd<8, 8>(a, sms, &blocks, st)
+           : E <= 128 && s->k <= 16 ? launch_route_bwd<16, 8>(a, sms, &blocks, st)
+           : E <= 256               ? launch_route_bwd<32, 8>(a, sms, &blocks, st)
+           : E <= 512               ? launch_route_bwd<32, 16>(a, sms, &blocks, st)
+                                    : launch_route_bwd<32, 32>(a, sms, &blocks, st);
   });
+  if (e == cudaSuccess && losses && blocks > 1)
+    e = abi_tracked(kAbiRouteBwd, 1, st, [&] {
+      // (may start while the last rows are done)
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(1);
+      cfg.blockDim = dim3(256);
+      cfg.stream = st;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+      at[0].val.programmaticStreamSerializationAllowed = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      return cudaLaunchKernelEx(&cfg, route_losses_kernel, static_cast<const float*>(a.part), blocks, a.inv_T, losses);
+    });
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
