@@ -4,9 +4,13 @@
 //   r = residual_scale * residual + gate * p,
 //   n = r * rs * weight,       rs = (mean_h r^2 + eps)^-1/2, rs_y likewise of y,
 //
-// and the gradient.  Forward: as the RMS norm's (norm.cu): a block walks rows, each
-// thread holds 8 * V columns in registers, y and the residual are read once and the
-// outputs written once.  Two sums over a row: of y^2, then of r^2.
+// and the gradient.  Forward: a block walks rows (or has one), y and the residual are
+// read once and the outputs written once.  The sum of r^2 follows from four sums that do
+// not wait for rs_y: with t = residual_scale * residual, q = y * post_weight and
+// f = gate * rs_y, sum r^2 = sum t^2 + f (2 sum t q + f sum q^2), so a row costs one
+// reduction (two, one after the other: 132 us instead of 76 at the size below, with the
+// steps told at RowStream).  Where the terms cancel to less than a quarter of theirs, or
+// leave fp32's range, r^2 is summed once more from r.
 //
 // Backward, with rhat = r * rs, q = y * rs_y * post_weight, v = dn * weight,
 // u = d_total + rs * v:
@@ -14,9 +18,14 @@
 //   D  = sum_h dr q = sum u q - rs m sum rhat q           (the gate's gradient),
 //   dy = rs_y (gate dr post_weight - y rs_y gate D / H),   d_residual = scale dr,
 //   d_post_weight[h] = sum_t gate dr y rs_y,   d_weight[h] = sum_t dn rhat.
-// The three sums over a row (v rhat, u q, rhat q) do not wait for one another, so a
-// row costs one reduction.  The weights' sums stay in registers over a block's rows
-// and are joined by a second kernel in block order: no atomics.
+// The three sums over a row (v rhat, u q, rhat q) do not wait for one another either.
+// The weights' sums stay in registers over a block's rows and are joined by a second
+// kernel in block order: no atomics.
+//
+// Sums are fp32: 8 values a thread and vector, then butterflies over the warp and the
+// warps.  Measured: forward of 16384 x 4096 bf16 with 8-bit output 75 us, 6.3 TB/s (70
+// us in the kernel, memory-bound); backward of 8192 x 2880 51 us, of which 45 in the
+// first kernel (6.3 TB/s) and the rest in the weights' sums and the step to them.
 #include <algorithm>
 #include <atomic>
 
@@ -40,7 +49,8 @@ __device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, uin
 // own part of shared memory and reads them back itself, so no barrier of the block is
 // needed, and all addresses within a row are one register and constants.  Places whose
 // columns or array do not exist hold zeros, which add nothing to a sum: the arithmetic
-// has no branches.  In fp32 a copy instruction covers 512 contiguous bytes, so a lane
+// has no branches (with a branch a vector and 64-bit addresses the forward of 16384 x 4096
+// with e4m3 took 87 us instead of 76, of 253 instructions a warp and vector 175 are left).  In fp32 a copy instruction covers 512 contiguous bytes, so a lane
 // copies other pieces than it reads.  D = 0: loads at their use.
 template <typename E, int N, int V, int D>
 struct RowStream {
