@@ -514,21 +514,25 @@ cudaError_t launch_join_fwd(const JoinFwd& a, int sms, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// *blocks: of the launch, each of which leaves its sums in a.part.
-template <typename E, bool NEXT, int V, int MAXT>
+// *blocks: of the launch, each of which leaves its sums in a.part.  WARPS: the fewest of
+// a block; where their ring does not fit, there is none.
+template <typename E, bool NEXT, int V, int MAXT, int WARPS>
 cudaError_t launch_join_bwd_v(const JoinBwd& a, int sms, int* blocks, cudaStream_t st) {
-  JoinLaunch l = join_launch(a.T, a.H, V, RowStream<E, NEXT ? 4 : 2, V, kAhead>::bytes(32), kBwdThreads, 8, sms);
-  if (l.blocks > 0 && a.T > l.blocks) {
-    static std::atomic<uint64_t> ready{0};
-    const cudaError_t e = allow_smem(join_bwd_kernel<E, NEXT, V, kAhead, MAXT>, ready);
-    if (e != cudaSuccess) return e;
-    join_bwd_kernel<E, NEXT, V, kAhead, MAXT><<<l.blocks, l.threads, l.smem, st>>>(a);
-  } else {
-    const int per_sm = std::max(1, std::min(8, 1024 / l.threads));
-    l.blocks = static_cast<int>(std::min<int64_t>(a.T, static_cast<int64_t>(sms) * per_sm));
-    join_bwd_kernel<E, NEXT, V, 0, MAXT><<<l.blocks, l.threads, 0, st>>>(a);
+  using Rows = RowStream<E, NEXT ? 4 : 2, V, kAhead>;
+  JoinLaunch l = join_launch(a.T, a.H, V, Rows::bytes(32), kBwdThreads, 8, sms);
+  if constexpr (Rows::bytes(32 * WARPS) <= kRingPerSm) {
+    if (l.blocks > 0 && a.T > l.blocks) {
+      static std::atomic<uint64_t> ready{0};
+      const cudaError_t e = allow_smem(join_bwd_kernel<E, NEXT, V, kAhead, MAXT>, ready);
+      if (e != cudaSuccess) return e;
+      join_bwd_kernel<E, NEXT, V, kAhead, MAXT><<<l.blocks, l.threads, l.smem, st>>>(a);
+      *blocks = l.blocks;
+      return cudaGetLastError();
+    }
   }
-  *blocks = l.blocks;
+  const int per_sm = std::max(1, std::min(8, 1024 / l.threads));
+  *blocks = static_cast<int>(std::min<int64_t>(a.T, static_cast<int64_t>(sms) * per_sm));
+  join_bwd_kernel<E, NEXT, V, 0, MAXT><<<*blocks, l.threads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -538,11 +542,11 @@ cudaError_t launch_join_bwd(const JoinBwd& a, int sms, int* blocks, cudaStream_t
   // one vector per thread up to 4096 columns; more than 80 registers where one block
   // per SM is all that the ring or the threads leave room for (8192 x 2880 fp32: 93 us
   // with up to 128 registers, 109 with 80; bf16, two blocks: 57 and 52)
-  if (warps <= (sizeof(E) == 4 ? 8 : 12)) return launch_join_bwd_v<E, NEXT, 1, 384>(a, sms, blocks, st);
-  if (warps <= 16) return launch_join_bwd_v<E, NEXT, 1, 512>(a, sms, blocks, st);
-  if (warps <= 32) return launch_join_bwd_v<E, NEXT, 2, 512>(a, sms, blocks, st);
-  if (warps <= 64) return launch_join_bwd_v<E, NEXT, 4, 512>(a, sms, blocks, st);
-  return launch_join_bwd_v<E, NEXT, 4, 1024>(a, sms, blocks, st);
+  if (warps <= (sizeof(E) == 4 ? 8 : 12)) return launch_join_bwd_v<E, NEXT, 1, 384, 1>(a, sms, blocks, st);
+  if (warps <= 16) return launch_join_bwd_v<E, NEXT, 1, 512, 9>(a, sms, blocks, st);
+  if (warps <= 32) return launch_join_bwd_v<E, NEXT, 2, 512, 9>(a, sms, blocks, st);
+  if (warps <= 64) return launch_join_bwd_v<E, NEXT, 4, 512, 9>(a, sms, blocks, st);
+  return launch_join_bwd_v<E, NEXT, 4, 1024, 17>(a, sms, blocks, st);
 }
 
 bool join_dims_ok(int64_t T, int32_t H, int32_t dtype) {
