@@ -779,6 +779,8 @@ def orthogonalize(g, out, ws, steps=5, coefs=None, eps=1e-7, scale=1.0, stream=N
     if out.shape != g.shape:
         raise ValueError("orthogonalize: out has shape %s for %s" % (tuple(out.shape), tuple(g.shape)))
     if coefs is not None:
+        if len(coefs) == 0 or not 1 <= steps <= 32:
+            raise ValueError("orthogonalize: 1 to 32 steps with three coefficients each")
         rows = [tuple(c) for c in coefs] if hasattr(coefs[0], "__len__") else [tuple(coefs)] * steps
         if len(rows) != steps or any(len(c) != 3 for c in rows):
             raise ValueError("orthogonalize: three coefficients, or %d times three" % steps)

@@ -119,8 +119,8 @@ __device__ __forceinline__ float2 orth_factor_of(const Squares& v, float eps, fl
     pre = 0x1p80f, ss = v.small;
   const float norm = sqrtf(ss) + eps * pre;
   // a matrix of zeros stays zero without eps too; one that holds an infinity or a NaN
-  // is NaN throughout
-  const float f = norm == 0.f ? 0.f : (isfinite(norm) ? S / norm : __int_as_float(0x7fc00000));
+  // is NaN throughout (eps * pre may be infinite beside a finite matrix: x_0 = 0)
+  const float f = norm == 0.f ? 0.f : (isfinite(ss) ? S / norm : __int_as_float(0x7fc00000));
   return make_float2(pre, f);
 }
 
@@ -1377,6 +1377,8 @@ moe_status moe_orthogonalize(int64_t E, int64_t M, int64_t N, int32_t dtype, con
   if (!orth_plan(E, M, N, &p) || (dtype != MOE_BF16 && dtype != MOE_FP32)) return MOE_ERR_INVALID_ARG;
   if (steps < 1 || steps > kMaxOrthSteps || !(eps >= 0.f) || eps - eps != 0.f || scale - scale != 0.f)
     return MOE_ERR_INVALID_ARG;
+  // (scale / S^3 is to be a normal number)
+  if (scale != 0.f && std::fabs(scale) < 0x1p-100f) return MOE_ERR_INVALID_ARG;
   const float S = orth_scale(coefs, steps, p.n);
   if (S == 0.f) return MOE_ERR_INVALID_ARG;
   if (g_ld < N || out_ld < N || g_stride < 0 || out_stride < 0) return MOE_ERR_INVALID_ARG;

@@ -524,13 +524,15 @@ size_t moe_orthogonalize_workspace_size(int64_t E, int64_t M, int64_t N);
  *   out: bf16, laid out by out_stride and out_ld; it may be g itself (bf16, the same
  *     strides), otherwise no overlap.
  * The norm is in range for every finite fp32 g.  A matrix of zeros gives zeros; one
- * that holds an infinity or a NaN gives NaN.  The products run in fp16 (11 bits) with
- * fp32 accumulation.  Before its rounding to bf16 the result of a Gaussian g is 1e-3
- * off in the 2-norm; singular values hundreds of times below the largest are
- * amplified together with the roundings beside them.
+ * that holds an infinity or a NaN gives NaN; one whose norm lies a thousand times and
+ * more below eps loses accuracy (x_0 is held in fp16) and in the end becomes zeros.
+ * The products run in fp16 (11 bits) with fp32 accumulation.  Before its rounding to
+ * bf16 the result of a Gaussian g is 1e-3 off in the 2-norm; singular values hundreds
+ * of times below the largest are amplified together with the roundings beside them.
  * Requirements: 1 <= M, N <= 65536, 1 <= steps <= 32, g_ld and out_ld >= N,
- * out_stride >= (M-1)*out_ld + N (E > 1), eps >= 0, scale finite; g and out aligned
- * to their elements (rows on 16 bytes are faster).  E = 0 is a no-op.
+ * out_stride >= (M-1)*out_ld + N (E > 1), eps >= 0 and finite, scale finite and 0 or
+ * at least 2^-100 in magnitude; g and out aligned to their elements (rows on 16 bytes
+ * are faster).  E = 0 is a no-op.
  * ws: moe_orthogonalize_workspace_size(E, M, N) bytes. */
 moe_status moe_orthogonalize(int64_t E, int64_t M, int64_t N, int32_t dtype, const void* g,
                              int64_t g_ld, int64_t g_stride, int32_t steps, const float* coefs,

@@ -147,6 +147,27 @@ def test_zeros_and_non_finite_matrices_stay_apart():
             assert rel(out[::4], exact(g[::4], eps=eps)) <= U + 1.7e-2
 
 
+@pytest.mark.parametrize("M,N", [(70, 130), (300, 200)])
+def test_norms_far_below_eps(M, N):
+    """x_0 = g / (|g| + eps) is small, not NaN, where eps leaves fp32's range beside the
+    norm (scaled by 2^80 for matrices below 2^-20)."""
+    g = draw((2, M, N), torch.float32, std=1e-12)
+    check(g, eps=float(g.double().square().sum((-2, -1)).sqrt().max()) * 100)
+    for eps in (1e15, 1e20, 3e38):
+        assert not run(g, eps=eps).any()
+    g[1, 3, 4] = float("nan")
+    out = run(g, eps=1e20)
+    assert not out[0].any() and torch.isnan(out[1]).all()
+
+
+def test_small_scales():
+    """The least scale: out is a bf16 normal number's size, fp32 holds scale / S^3."""
+    g = draw((2, 70, 130), torch.float32)
+    check(g, scale=2.0 ** -100)
+    check(draw((2, 200, 130), torch.float32), scale=-2.0 ** -100)
+    assert not run(g, scale=0.0).any()
+
+
 def test_rank_one_and_equal_rows():
     """Where g has one singular value, what the roundings of x leave beside its
     direction grows by c0 a step: a rounding of x_j (2.8e-4 of its norm, which is at

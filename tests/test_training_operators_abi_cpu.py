@@ -87,6 +87,24 @@ def test_orthogonalize_refusals(L):
     assert L.moe_orthogonalize(**dict(ok, E=0, g=None, out=None, ws=None, ws_bytes=0)) == L.MOE_OK
 
 
+def test_orthogonalize_refuses_scales_that_fp32_loses(L):
+    size = L.moe_orthogonalize_workspace_size(2, 16, 24)
+    ok = dict(E=2, M=16, N=24, dtype=L.MOE_FP32, g=16, g_ld=24, g_stride=384, steps=5, coefs=None, eps=1e-7, scale=1.0,
+              out=16, out_ld=24, out_stride=384, ws=256, ws_bytes=size, stream=None)
+    for scale in (1e-38, -1e-38, 2.0 ** -101, 1e-45):
+        assert L.moe_orthogonalize(**dict(ok, scale=scale)) == L.MOE_ERR_INVALID_ARG
+    # (E = 0: nothing is launched)
+    for scale in (0.0, 2.0 ** -100, -1.0):
+        assert L.moe_orthogonalize(**dict(ok, E=0, scale=scale)) == L.MOE_OK
+
+
+def test_helpers_refuse_coefficients(L):
+    x = torch.zeros((4, 64), dtype=torch.bfloat16)
+    for coefs, steps in (([], 0), ([], 5), ((1.0, 2.0), 5), ([(1.0, 2.0, 3.0)], 2), ((1.0, 2.0, 3.0), 10 ** 9), ((1.0, 2.0, 3.0), -1)):
+        with pytest.raises(ValueError, match="coefficients"):
+            L.orthogonalize(x, x, torch.zeros(8, dtype=torch.uint8), steps=steps, coefs=coefs)
+
+
 def test_helpers_refuse_tensors_on_the_host(L):
     x = torch.zeros((4, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
