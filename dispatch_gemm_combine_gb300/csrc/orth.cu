@@ -761,8 +761,8 @@ cudaError_t launch_orth_steps(const OrthMaps& maps, const OrthArgs& args, int sm
 // columns of X [128 rows, zeros past m], in the 128-byte swizzle: one layout serves as
 // the K-major operand of the gram and as the MN-major one of the update.
 //   norm and load   from g, the squares joined over the cluster
-//   gram            each CTA's columns; the CTAs' sums are added in rank order, a share
-//                   of the rows by each, which hands it to all
+//   gram            each CTA's columns; the CTAs' sums on and above the diagonal are added
+//                   in a fixed order, a share of the rows by each, which hands it to all
 //   poly            128 x 128 in every CTA; B as an fp16 value and what it leaves, so its
 //                   rounding, the largest one's share of the error, falls away (the products
 //                   are not what takes the time)
@@ -774,7 +774,6 @@ cudaError_t launch_orth_steps(const OrthMaps& maps, const OrthArgs& args, int sm
 constexpr int kSmallThreads = 512;
 constexpr int kChunkBytes = 128 * 128;            // 128 rows of 64 columns
 constexpr int kMaxSmallChunks = 8;                // per CTA
-constexpr int kMaxSmallRanks = 16;             // (more than 8 where the device can)
 constexpr int kSmallTail = 2 * kChunkBytes + 4 * kChunkBytes + 1024 + 512;   // A, P (or both parts of B), alignment, rest
 constexpr int kSmallSmemMin = 120 * 1024;
 constexpr int kSmallM = 128;
@@ -836,7 +835,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
   uint8_t* gbase = smem_raw + (sbase - raw);
   const uint32_t sX = sbase, sA = sX + a.chunks * kChunkBytes, sP = sA + 2 * kChunkBytes, sB = sP;
   const uint32_t bars = sP + 4 * kChunkBytes, slots = bars + 32, tmem_slot = bars + 24;
-  uint8_t *gX = gbase, *gA = gbase + (sA - sbase), *gB = gbase + (sB - sbase);
+  uint8_t *gX = gbase, *gA = gbase + (sA - sbase);
   const float* gslots = reinterpret_cast<const float*>(gbase + (slots - sbase));   // [ranks][3]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -982,36 +981,59 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
     if (a.ranks > 1) {
       __syncwarp();
       cluster_sync();
-      // this CTA's share of the rows: the ranks' sums in order, then to all of them
-      // (sent to this CTA's memory from the lanes that hold them, a row each, the sums
-      // take 2 us more a step: neighbours have to be read and written side by side)
-      const int rows = 128 / a.ranks, r0 = rank * rows;
-      for (int i = tid; i < rows * 32; i += kSmallThreads) {
-        const int r = r0 + (i >> 5), p = i & 31;
-        if (4 * p >= mc) continue;      // (rows past m are zeros, and wanted as such)
+      // this CTA's share of the rows, some of each 32: the ranks' sums from its own on
+      // (all from rank 0 on, they wait for one another there: 0.8 us more a step), then to
+      // all of them.  A lane takes four columns, with more than eight ranks two lanes take
+      // the same four, of eight ranks each; two neighbours' sums are 16 bytes, which the
+      // lanes that hold them send to a part of the ranks each.  Columns of the 32 x 32
+      // blocks below the diagonal are not sent but mirrored where they arrive (0.8 us less
+      // a step): what the cluster's network carries, 14 bytes a clock and SM, is what this
+      // takes, by asynchronous copies too.
+      const int rows = 128 / a.ranks, each = rows / 4;      // of a block of 32
+      const bool halves = a.ranks > 8;
+      for (int i = tid; i < (rows << (halves ? 6 : 5)); i += kSmallThreads) {   // (whole warps)
+        const int o = i >> (halves ? 6 : 5), block = o / each, r = block * 32 + rank * each + o % each;
+        const int p = halves ? (i >> 1 & 16) + (lane & 15) : lane, k0 = halves ? lane >> 4 << 3 : 0;
+        const bool in = 4 * p < mc && p >= 8 * block;      // (rows past m are zeros, and wanted as such)
         float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
         const uint32_t from = sP + r * 512 + (p ^ (r & 7)) * 16;
-        for (int k = 0; k < a.ranks; k += 8) {
-          float4 x[8];
+        float4 x[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            x[j] = k + j < a.ranks ? ld_cluster4(mapa_shared(from, k + j)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < 8; ++j)
+          x[j] = in && k0 + j < a.ranks ? ld_cluster4(mapa_shared(from, (rank + k0 + j) & (a.ranks - 1)))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) t.x += x[j].x, t.y += x[j].y, t.z += x[j].z, t.w += x[j].w;
+        for (int j = 0; j < 8; ++j) t.x += x[j].x, t.y += x[j].y, t.z += x[j].z, t.w += x[j].w;
+        if (halves) {
+          t.x += __shfl_xor_sync(0xffffffffu, t.x, 16), t.y += __shfl_xor_sync(0xffffffffu, t.y, 16);
+          t.z += __shfl_xor_sync(0xffffffffu, t.z, 16), t.w += __shfl_xor_sync(0xffffffffu, t.w, 16);
         }
-        *reinterpret_cast<uint2*>(gA + swz(r, 4 * p)) = make_uint2(pack_half(t.x, t.y), pack_half(t.z, t.w));
-      }
-      __syncthreads();
-      for (int i = tid; i < rows * 16 * a.ranks; i += kSmallThreads) {
-        const int k = i / (rows * 16), j = i - k * (rows * 16), r = r0 + (j >> 4), c = (j & 15) * 8;
-        if (k == rank || c >= mc) continue;
-        const uint4 u = *reinterpret_cast<const uint4*>(gA + swz(r, c));
-        st_cluster4u(mapa_shared(sA + swz(r, c), k), u);
+        const uint32_t u0 = pack_half(t.x, t.y), u1 = pack_half(t.z, t.w);
+        const uint32_t v0 = __shfl_xor_sync(0xffffffffu, u0, 1), v1 = __shfl_xor_sync(0xffffffffu, u1, 1);
+        const uint4 u = lane & 1 ? make_uint4(v0, v1, u0, u1) : make_uint4(u0, u1, v0, v1);
+        const uint32_t to = sA + swz(r, 4 * (p & ~1));
+        for (int k = halves ? (lane & 1) + (lane >> 4 << 1) : lane & 1; in && k < a.ranks; k += halves ? 4 : 2)
+          st_cluster4u(mapa_shared(to, (rank + k) & (a.ranks - 1)), u);
       }
       asm volatile("fence.proxy.async;" ::: "memory");
-      tc_fence_before();
       __syncwarp();
       cluster_sync();
+      // rows of the blocks below the diagonal, eight columns at a time
+      for (int i = warp; i < 24; i += kSmallThreads / 32) {
+        const int t = i >> 2, block = t < 1 ? 1 : (t < 3 ? 2 : 3);      // (1,0) (2,0) (2,1) (3,0) ..
+        const int r = block * 32 + lane, c = (t - block * (block - 1) / 2) * 32 + (i & 3) * 8;
+        if (block * 32 >= mc) break;
+        uint32_t u[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          u[k] = r < mc ? *reinterpret_cast<const uint16_t*>(gA + swz(c + 2 * k, r)) |
+                              static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(gA + swz(c + 2 * k + 1, r))) << 16
+                        : 0u;
+        st_shared_v4u(sA + swz(r, c), u[0], u[1], u[2], u[3]);
+      }
+      fence_async_shared();
+      tc_fence_before();
+      __syncthreads();
     } else {
       fence_async_shared();
       tc_fence_before();
@@ -1097,11 +1119,26 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
           for (int j = 0; j < 4; ++j)
             st_shared_v4u(sX + swz(row, xc + 8 * j), pack_half(v[8 * j], v[8 * j + 1]), pack_half(v[8 * j + 2], v[8 * j + 3]),
                           pack_half(v[8 * j + 4], v[8 * j + 5]), pack_half(v[8 * j + 6], v[8 * j + 7]));
+        } else if (FLIP && a.vec) {
+          // a warp's rows lie side by side: two lanes' rows of every other column each
+          const int col = first + xc, live = a.n - col, odd = lane & 1, r = row & ~1;
+          __nv_bfloat16* o = a.out + e * a.out_stride + static_cast<int64_t>(col + odd) * a.out_ld + r;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+            const uint32_t u = odd ? pack_bf16(other, v[j + 1]) : pack_bf16(v[j], other);
+            if (j + odd < live) {
+              if (r + 1 < a.m)
+                *reinterpret_cast<uint32_t*>(o) = u;
+              else if (r < a.m)
+                *o = __ushort_as_bfloat16(static_cast<uint16_t>(u));
+            }
+            o += 2 * a.out_ld;
+          }
         } else if (row < a.m) {
           const int col = first + xc, live = a.n - col;    // columns that exist, from here
           __nv_bfloat16* out = a.out + e * a.out_stride;
           if (FLIP) {
-            // a warp's rows lie side by side
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (j < live) out[static_cast<int64_t>(col + j) * a.out_ld + row] = __float2bfloat16_rn(v[j]);
@@ -1136,17 +1173,18 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
 }
 
 // CTAs per matrix: the number with the least time.  Measured, five steps at m = 128: 16
-// us, 3.3 for each block of 64 columns of a CTA, and 9 + 4 log2(r) for the exchanges in a
-// cluster of r (512 columns: 43.9 us on one CTA, 41.4 on 4; 2048: 61.9 on 4, 49.6 on
-// 16).  Matrices that do not fit at once go in waves, with whole clusters in each of the
-// eight groups of SMs (32 of 64 x 512: 31 us on 4, 88 on 8).
-void orth_small_ranks(OrthSmall* a, int batch, int most, int sms) {
+// us, 4.4 for each block of 64 columns of a CTA, and 17 + r / 5 for the exchanges in a
+// cluster of r (512 columns: 51.4 us on one CTA, 41.3 on 4, 40.3 on 8; 2048: 53.5 on 8,
+// 45.4 on 16).  Matrices that do not fit at once go in waves (8 of 128 x 2880: 98 us on 16
+// CTAs each, of which this GPU holds 7, 62 on 8).
+constexpr int kRankLogs = 5;      // 1, 2, 4, 8, 16
+void orth_small_ranks(OrthSmall* a, int batch, const int (&clusters)[kRankLogs]) {
   double least = 1e300;
-  for (int r = 1, log = 0; r <= most; r *= 2, ++log) {
-    const int chunks = (a->n + 64 * r - 1) / (64 * r);
-    if (chunks > kMaxSmallChunks) continue;
-    const int slots = r == 1 ? sms : std::max(1, sms / 8 / r) * 8;
-    const double t = std::ceil(static_cast<double>(batch) / slots) * (16 + 3.3 * chunks + (r > 1 ? 9 + 4 * log : 0));
+  for (int log = 0; log < kRankLogs; ++log) {
+    const int r = 1 << log, chunks = (a->n + 64 * r - 1) / (64 * r);
+    if (chunks > kMaxSmallChunks || clusters[log] == 0) continue;
+    const double waves = std::ceil(static_cast<double>(batch) / clusters[log]);
+    const double t = waves * (16 + 4.4 * chunks + (r > 1 ? 17 + 0.2 * r : 0));
     if (t < least) least = t, a->ranks = r, a->chunks = chunks;
   }
 }
@@ -1165,22 +1203,30 @@ cudaError_t launch_orth_small(OrthSmall& a, int batch, int sms, cudaStream_t st)
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(kSmallThreads);
-  static std::atomic<int> known[64];      // the largest cluster, once per device
-  int most = known[dev & 63].load(std::memory_order_relaxed);
-  if (most == 0) {
+  // the clusters of each size that fit the device at once, asked for once per device
+  static std::atomic<int> known[64][kRankLogs];
+  static std::atomic<uint64_t> ready{0};
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(kMaxSmallRanks);
-    cfg.dynamicSmemBytes = kMost;
-    attr[0].val.clusterDim.x = kMaxSmallRanks;
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-    if (e != cudaSuccess) (void)cudaGetLastError(), n = 0;
-    most = n > 0 ? kMaxSmallRanks : 8;
-    known[dev & 63].store(most, std::memory_order_relaxed);
+    known[dev & 63][0].store(sms, std::memory_order_relaxed);
+    for (int log = 1; log < kRankLogs; ++log) {
+      cfg.gridDim = dim3(sms >> log << log);
+      cfg.dynamicSmemBytes = kMost;
+      attr[0].val.clusterDim.x = 1 << log;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) (void)cudaGetLastError(), n = 0;
+      known[dev & 63][log].store(n, std::memory_order_relaxed);
+    }
+    ready.fetch_or(bit, std::memory_order_release);
   }
-  orth_small_ranks(&a, batch, most, sms);
+  int clusters[kRankLogs];
+  for (int log = 0; log < kRankLogs; ++log) clusters[log] = known[dev & 63][log].load(std::memory_order_relaxed);
+  a.ranks = 0;
+  orth_small_ranks(&a, batch, clusters);
+  if (a.ranks == 0) return cudaErrorLaunchOutOfResources;
   cfg.gridDim = dim3(static_cast<unsigned>(batch * a.ranks));
   cfg.dynamicSmemBytes = std::max(kSmallSmemMin, a.chunks * kChunkBytes + kSmallTail);
   cfg.stream = st;

@@ -108,6 +108,12 @@ def test_more_matrices_than_a_launch_takes():
     check(draw((1301, 24, 16), torch.float32))
 
 
+@pytest.mark.parametrize("E,M,N", [(5, 33, 900), (9, 1500, 97), (20, 128, 1100), (9, 2880, 47), (40, 100, 250), (2, 128, 4096)])
+def test_clusters_in_waves(E, M, N):
+    """Narrow matrices on clusters, more of them than fit at once."""
+    check(draw((E, M, N), torch.bfloat16))
+
+
 def test_singular_values_and_vectors():
     """Of a matrix with known singular values: the result has its vectors."""
     q = lambda n, s: torch.linalg.qr(torch.randn((n, 96), generator=torch.Generator().manual_seed(s), dtype=torch.float64))[0]  # noqa: E731
