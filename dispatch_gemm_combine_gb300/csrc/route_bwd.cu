@@ -16,7 +16,7 @@
 // choice's term where the lane that owns the column picks it up); a row that names an
 // expert twice adds its terms one after the other.  Sums over the rows: a lane keeps
 // every G-th row's, then over warp and block in a fixed order, then one block over all
-// blocks: no atomics.
+// blocks, in their order too.
 //
 // Measured: 65536 x 256, top-8, 31 us (28 in the kernel): 300 instructions a row and the
 // latency of its shuffles, at 29 warps per SM, hold it at two thirds of the memory's
@@ -33,6 +33,7 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxRouteE = 1024;
 constexpr int kMaxRouteK = 32;
 constexpr int kMaxRouteBlocks = 8 * 256;   // of any device
@@ -44,7 +45,8 @@ struct RouteBwd {
   const int* counts;
   const float* dw;
   float* d;
-  float* part;      // [blocks][2]: sums of F and of l^2, or null
+  float2* part;     // [blocks]: sums of F and of l^2, or null
+  unsigned* done;   // blocks whose sums are there, 0 between calls; or null: a second kernel adds
   float* losses;
   int* err;
   int64_t T;
@@ -94,12 +96,35 @@ __device__ __forceinline__ void copy_if(uint32_t dst, const float* src, bool on)
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.ca.shared.global [%0], [%1], 4;\n\t}" ::"r"(dst), "l"(src), "r"(static_cast<int>(on)) : "memory");
 }
 
+// losses[i] = sum of the blocks' sums / T: a thread adds blocks q, q + 256, ..., then the
+// threads' sums by warps: sixteen fp32 additions deep.  (In 64 bits, of which this GPU
+// adds few a clock, the call takes 2 us more.)
+__device__ __forceinline__ void add_blocks(const float2* part, int blocks, float inv_T, float* losses, float (&sums)[kWarps][2]) {
+  float2 v[kMaxRouteBlocks / kThreads];
+#pragma unroll
+  for (int i = 0; i < kMaxRouteBlocks / kThreads; ++i) {
+    const int b = threadIdx.x + kThreads * i;
+    v[i] = b < blocks ? __ldcg(part + b) : make_float2(0.f, 0.f);
+  }
+  float x = 0.f, y = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxRouteBlocks / kThreads; ++i) x += v[i].x, y += v[i].y;
+  x = warp_sum(x), y = warp_sum(y);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5][0] = x, sums[threadIdx.x >> 5][1] = y;
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    float t = 0.f;
+    for (int i = 0; i < kWarps; ++i) t += sums[i][threadIdx.x];
+    losses[threadIdx.x] = t * inv_T;
+  }
+}
+
 // PER columns in each of a row's G lanes.  VEC: groups of four, 4 (g + G i) ..; otherwise
 // g + G i.
 constexpr int kRowsAhead = 3;
 
 template <int G, int PER, bool VEC>
-__global__ void __launch_bounds__(32 * kWarps) route_bwd_kernel(const RouteBwd a) {
+__global__ void __launch_bounds__(kThreads) route_bwd_kernel(const RouteBwd a) {
   constexpr int R = 32 / G;             // rows of a warp
   constexpr int S = VEC ? 4 : 1;        // columns side by side
   constexpr int W = G * PER;            // floats of a row in shared memory
@@ -250,44 +275,33 @@ __global__ void __launch_bounds__(32 * kWarps) route_bwd_kernel(const RouteBwd a
   sum_F = warp_sum(sum_F), sum_l = warp_sum(sum_l);
   if (lane == 0) sums[warp][0] = sum_F, sums[warp][1] = sum_l;
   __syncthreads();
-  if (threadIdx.x < 2) {
-    float s = 0.f;
-    for (int i = 0; i < kWarps; ++i) s += sums[i][threadIdx.x];
-    if (gridDim.x == 1)
-      a.losses[threadIdx.x] = s * a.inv_T;      // no other block's to be added
-    else
-      a.part[2 * blockIdx.x + threadIdx.x] = s;
+  bool last = false;
+  if (threadIdx.x == 0) {
+    float2 v = make_float2(0.f, 0.f);
+    for (int i = 0; i < kWarps; ++i) v.x += sums[i][0], v.y += sums[i][1];
+    if (gridDim.x == 1) {      // no other block's to be added
+      a.losses[0] = v.x * a.inv_T, a.losses[1] = v.y * a.inv_T;
+    } else {
+      __stcg(a.part + blockIdx.x, v);
+      if (a.done) {
+        __threadfence();
+        last = atomicInc(a.done, gridDim.x - 1) == gridDim.x - 1;      // (back to 0)
+      }
+    }
   }
+  if (!a.done || !__syncthreads_or(last)) return;
+  __threadfence();
+  add_blocks(a.part, gridDim.x, a.inv_T, a.losses, sums);
 }
 
-// losses[i] = sum of the blocks' sums / T: a thread adds blocks q, q + 256, ..., then the
-// threads' sums by warps: sixteen fp32 additions deep.  (In 64 bits, of which this GPU
-// adds few a clock, the call takes 2 us more.)
-__global__ void __launch_bounds__(256) route_losses_kernel(const float* __restrict__ part, int blocks,
-                                                           float inv_T, float* __restrict__ losses) {
-  __shared__ float s[2][8];
+__global__ void __launch_bounds__(kThreads) route_losses_kernel(const float2* part, int blocks, float inv_T, float* losses) {
+  __shared__ float sums[kWarps][2];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the sums are there
-  float2 v[kMaxRouteBlocks / 256];
-#pragma unroll
-  for (int i = 0; i < kMaxRouteBlocks / 256; ++i) {
-    const int b = threadIdx.x + 256 * i;
-    v[i] = b < blocks ? __ldcg(reinterpret_cast<const float2*>(part) + b) : make_float2(0.f, 0.f);
-  }
-  float x = 0.f, y = 0.f;
-#pragma unroll
-  for (int i = 0; i < kMaxRouteBlocks / 256; ++i) x += v[i].x, y += v[i].y;
-  x = warp_sum(x), y = warp_sum(y);
-  if ((threadIdx.x & 31) == 0) s[0][threadIdx.x >> 5] = x, s[1][threadIdx.x >> 5] = y;
-  __syncthreads();
-  if (threadIdx.x < 2) {
-    float t = 0.f;
-    for (int i = 0; i < 8; ++i) t += s[threadIdx.x][i];
-    losses[threadIdx.x] = t * inv_T;
-  }
+  add_blocks(part, blocks, inv_T, losses, sums);
 }
 
 template <int G, int PER, bool VEC>
-cudaError_t launch_route_bwd_v(const RouteBwd& a, int sms, int* blocks, cudaStream_t st) {
+cudaError_t launch_route_bwd_v(RouteBwd& a, int sms, int* blocks, cudaStream_t st) {
   constexpr int R = 32 / G * kWarps;
   constexpr int smem = kWarps * (kRowsAhead + 1) * 32 * PER * static_cast<int>(sizeof(float));
   // by registers (five blocks of 48 registers spill: 65536 x 256 38 us instead of 33)
@@ -295,15 +309,21 @@ cudaError_t launch_route_bwd_v(const RouteBwd& a, int sms, int* blocks, cudaStre
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = allow_smem(route_bwd_kernel<G, PER, VEC>, ready);
   if (e != cudaSuccess) return e;
-  *blocks = static_cast<int>(std::min<int64_t>((a.T + R - 1) / R, std::min(kMaxRouteBlocks, sms * per_sm)));
-  // two rounds of one block take less than a second kernel for the blocks' sums
+  const int most = std::min(kMaxRouteBlocks, sms * per_sm);
+  *blocks = static_cast<int>(std::min<int64_t>((a.T + R - 1) / R, most));
+  // two rounds of one block take less than the sum of two blocks' sums
   if (*blocks == 2 && a.losses) *blocks = 1;
-  route_bwd_kernel<G, PER, VEC><<<*blocks, 32 * kWarps, smem, st>>>(a);
+  // where each block has one round, launches take longer than the kernel: the block that
+  // comes last adds the sums (8192 x 128: a call 8.6 us, 10.5 with a second kernel; the GPU
+  // alone, in a graph, 6.5 and 5.7); otherwise the second kernel, which starts while the
+  // last rows are done (16384 x 512: a call 14.5 us, 16.3 without it)
+  if (a.T > static_cast<int64_t>(most) * R) a.done = nullptr;
+  route_bwd_kernel<G, PER, VEC><<<*blocks, kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
 template <int G, int PER>
-cudaError_t launch_route_bwd(const RouteBwd& a, int sms, int* blocks, cudaStream_t st) {
+cudaError_t launch_route_bwd(RouteBwd& a, int sms, int* blocks, cudaStream_t st) {
   return a.E % 4 == 0 ? launch_route_bwd_v<G, PER, true>(a, sms, blocks, st)
                       : launch_route_bwd_v<G, PER, false>(a, sms, blocks, st);
 }
@@ -346,7 +366,8 @@ moe_status moe_route_bwd(const moe_shape* s, const float* logits, const int32_t*
   RouteBwd a;
   a.logits = softmax ? logits : nullptr, a.idx = topk_idx, a.w = topk_w, a.dw = d_topk_w;
   a.counts = softmax ? counts : nullptr, a.d = d_logits;
-  a.part = losses ? reinterpret_cast<float*>(static_cast<char*>(ws) + 256) : nullptr;
+  a.part = losses ? reinterpret_cast<float2*>(static_cast<char*>(ws) + 256) : nullptr;
+  a.done = losses ? reinterpret_cast<unsigned*>(static_cast<char*>(ws) + 64) : nullptr;
   a.err = static_cast<int*>(ws);
   a.T = s->T, a.E = s->E, a.k = s->k;
   a.balance_T = static_cast<float>(balance / T), a.z2_T = static_cast<float>(2.0 * z / T);
@@ -363,19 +384,19 @@ moe_status moe_route_bwd(const moe_shape* s, const float* logits, const int32_t*
            : E <= 512               ? launch_route_bwd<32, 16>(a, sms, &blocks, st)
                                     : launch_route_bwd<32, 32>(a, sms, &blocks, st);
   });
-  if (e == cudaSuccess && losses && blocks > 1)
+  if (e == cudaSuccess && losses && blocks > 1 && !a.done)
     e = abi_tracked(kAbiRouteBwd, 1, st, [&] {
       // (may start while the last rows are done)
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(1);
-      cfg.blockDim = dim3(256);
+      cfg.blockDim = dim3(kThreads);
       cfg.stream = st;
       cudaLaunchAttribute at[1];
       at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
       at[0].val.programmaticStreamSerializationAllowed = 1;
       cfg.attrs = at;
       cfg.numAttrs = 1;
-      return cudaLaunchKernelEx(&cfg, route_losses_kernel, static_cast<const float*>(a.part), blocks, a.inv_T, losses);
+      return cudaLaunchKernelEx(&cfg, route_losses_kernel, static_cast<const float2*>(a.part), blocks, a.inv_T, losses);
     });
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

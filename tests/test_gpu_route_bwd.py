@@ -180,6 +180,36 @@ def test_repeats_bit_for_bit_and_in_a_graph():
     assert torch.equal(d.cpu(), d0) and torch.equal(losses.cpu(), l0)
 
 
+def test_sizes_in_turn_on_one_workspace():
+    """Calls of one block, of one round of many and of several rounds: each leaves the
+    workspace as the others want it."""
+    ws, cases, want = moe.route_bwd_workspace(moe.Shape(20000, 8, 8, 64, 4)), [], []
+    for T in (5, 20000, 700, 33, 2000, 20000, 64, 1):
+        shape = moe.Shape(T, 8, 8, 64, 4)
+        logits = torch.randn((T, 64), generator=torch.Generator().manual_seed(T)).cuda()
+        counts = torch.full((64,), T // 16 + 1, dtype=torch.int32, device="cuda")
+        args = (shape, logits, counts, torch.zeros_like(logits), torch.zeros(2, device="cuda"))
+        cases.append(args)
+        fresh = [torch.zeros_like(logits), torch.zeros(2, device="cuda")]
+        moe.route_bwd(shape, logits, fresh[0], moe.route_bwd_workspace(shape), counts=counts, balance=0.1, z=0.1, losses=fresh[1])
+        p = torch.softmax(logits.double(), -1)
+        f = counts.double() * 64 / (T * 4)
+        exact = torch.stack(((p @ f).mean(), torch.logsumexp(logits.double(), -1).square().mean()))
+        # sums of positive terms, at most some 40 fp32 additions deep
+        assert torch.all((fresh[1].double() - exact).abs() <= 64 * 2.0 ** -24 * exact)
+        want.append(fresh)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for shape, logits, counts, d, losses in cases:
+            moe.route_bwd(shape, logits, d, ws, counts=counts, balance=0.1, z=0.1, losses=losses)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for (_, _, _, d, losses), (wd, wl) in zip(cases, want):
+            assert torch.equal(d, wd) and torch.equal(losses, wl)
+            d.zero_(), losses.zero_()
+
+
 def test_refusals():
     c = Case(4, 16, 2)
     shape = moe.Shape(4, 8, 8, 16, 2)
