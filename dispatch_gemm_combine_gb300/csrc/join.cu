@@ -65,9 +65,9 @@ struct RowStream {
   bool in[V];           // the lane's vectors exist
   uint32_t present;     // a bit for each array that exists
 
-  __device__ __forceinline__ void init(uint4* smem, const E* const (&p)[N], int H) {
+  // The rows at, at + each, ..; this warp's columns from `first` on.
+  __device__ __forceinline__ void init(uint4* smem, const E* const (&p)[N], int H, int at, int each, int first) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int first = warp * 256 * V;
     uint32_t row = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -83,8 +83,8 @@ struct RowStream {
     const int own = D > 0 ? lane * 16 : lane * 16 * W;
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      src[n] = p[n] ? reinterpret_cast<const char*>(p[n] + static_cast<int64_t>(blockIdx.x) * H + first) + own : nullptr;
-    step = static_cast<int64_t>(gridDim.x) * H * sizeof(E);
+      src[n] = p[n] ? reinterpret_cast<const char*>(p[n] + static_cast<int64_t>(at) * H + first) + own : nullptr;
+    step = static_cast<int64_t>(each) * H * sizeof(E);
     put = get = 0;
     if (D > 0) {
       ring = smem_u32(smem) + warp * (D * WARP_BYTES);
@@ -114,11 +114,12 @@ struct RowStream {
     cp_async_wait<D >= 2 ? D - 2 : 0>();
     if (W > 1) __syncwarp();
   }
-  __device__ __forceinline__ void take(int n, int i, Raw8<E>& r) const {
+  __device__ __forceinline__ void take(int n, int i, Raw8<E>& r) const { take(n, i, r, get); }
+  __device__ __forceinline__ void take(int n, int i, Raw8<E>& r, int stage) const {
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       if (D > 0) {
-        const uint32_t at = ring + get * WARP_BYTES + (n * V + i) * W * 512 + (threadIdx.x & 31) * (16 * W) + w * 16;
+        const uint32_t at = ring + stage * WARP_BYTES + (n * V + i) * W * 512 + (threadIdx.x & 31) * (16 * W) + w * 16;
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(r.u[w].x), "=r"(r.u[w].y), "=r"(r.u[w].z), "=r"(r.u[w].w) : "r"(at) : "memory");
       } else {
@@ -173,7 +174,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) join_fwd_kernel(con
   __shared__ float part[2][128];
   const int H = a.H, count = block_rows(a.T);
   RowStream<E, 2, V, D> rows;
-  rows.init(ring_mem, {static_cast<const E*>(a.y), static_cast<const E*>(a.residual)}, H);
+  rows.init(ring_mem, {static_cast<const E*>(a.y), static_cast<const E*>(a.residual)}, H, blockIdx.x, gridDim.x,
+            (threadIdx.x >> 5) * 256 * V);
 #pragma unroll
   for (int d = 0; d < D - 1; ++d) rows.issue(d < count);
   const int lane = threadIdx.x & 31;
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 1) join_bwd_kernel(con
   {
     const E* p[N] = {static_cast<const E*>(a.y), static_cast<const E*>(a.d_total)};
     if (NEXT) p[N - 2] = static_cast<const E*>(a.dn), p[N - 1] = static_cast<const E*>(a.total);
-    rows.init(ring_mem, p, H);
+    rows.init(ring_mem, p, H, blockIdx.x, gridDim.x, (threadIdx.x >> 5) * 256 * V);
   }
 #pragma unroll
   for (int d = 0; d < D - 1; ++d) rows.issue(d < count);
@@ -437,6 +439,161 @@ __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 1) join_bwd_kernel(con
   }
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// The same for wide rows: a cluster of `ranks` CTAs takes a row, 512 columns a warp, and a
+// row's second pass comes after the next one's first: what the warps' sums take through
+// the cluster is then hidden, and a row stays in the ring until its second pass, so only
+// the weights and their sums are kept in registers.  (One CTA with four vectors a thread
+// spills and has no room for a ring: 4096 x 16384 bf16 275 us instead of 165, 1024 x 32768
+// fp32 592 instead of 192.)  Each warp sends its sums to all CTAs; one that is a row ahead
+// of another has passed the barrier before, so four rows' sums have to have room.
+template <typename E, bool NEXT>
+__global__ void __launch_bounds__(512, 1) join_bwd_wide_kernel(const JoinBwd a, int ranks) {
+  constexpr int V = 2, N = NEXT ? 4 : 2;
+  extern __shared__ uint4 ring_mem[];
+  __shared__ float part[4][256];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, rank = cluster_ctarank();
+  const int H = a.H, first_row = blockIdx.x / ranks, clusters = gridDim.x / ranks;
+  const int count = static_cast<int>((a.T - first_row + clusters - 1) / clusters);
+  const int first = (rank * warps + warp) * 256 * V, c0 = first + lane * 8;     // of vector 0
+  RowStream<E, N, V, kAhead> rows;
+  {
+    const E* p[N] = {static_cast<const E*>(a.y), static_cast<const E*>(a.d_total)};
+    if (NEXT) p[N - 2] = static_cast<const E*>(a.dn), p[N - 1] = static_cast<const E*>(a.total);
+    rows.init(ring_mem, p, H, first_row, clusters, first);
+  }
+  rows.issue(true);
+  rows.issue(count > 1);
+  // lane l sends sum l & 3 to rank l >> 2
+  const uint32_t send = mapa_shared(smem_u32(part) + ((rank * warps + warp) * 4 + (lane & 3)) * 4, (lane >> 2) % ranks);
+  cluster_sync();      // the others' shared memory is there
+  Raw8<E> wp[V], w[V];      // (packed; loaded again in each pass, a row waits for them: 4096 x 16384 179 us)
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    wp[i].ones(), w[i].ones();
+    if (a.post_weight && rows.in[i]) wp[i].load(static_cast<const E*>(a.post_weight) + c0 + i * 256);
+    if (NEXT && rows.in[i]) w[i].load(static_cast<const E*>(a.weight) + c0 + i * 256);
+  }
+  float2 dw[NEXT ? V : 1][4], dwp[V][4];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dwp[i][j] = dw[NEXT ? i : 0][j] = make_float2(0.f, 0.f);
+  const float inv_H = 1.f / static_cast<float>(H);
+  const int64_t at0 = static_cast<int64_t>(first_row) * H + c0;
+  E *dy = static_cast<E*>(a.dy) + at0, *d_residual = static_cast<E*>(a.d_residual) + at0;
+  const float2 scale2 = make_float2(a.scale, a.scale);
+  float rstds = 0.f, posts = 1.f, gates = 1.f;      // of 32 rows, one per lane
+  float rs = 0.f, rs_y = 1.f, gate = 1.f;           // of the row of the first pass
+  float2 u[4], rhat[4], yhat[4];
+  Raw8<E> rn;
+  // u = d_total + rs dn weight, rhat, yhat of vector i
+  auto terms = [&](int i, int stage, float r, float ry) {
+    const float2 r2 = make_float2(r, r), ry2 = make_float2(ry, ry);
+    Raw8<E> x, t, rr;
+    rows.take(0, i, x, stage);
+    rows.take(1, i, t, stage);
+    if (NEXT) {
+      rows.take(N - 2, i, rn, stage);
+      rows.take(N - 1, i, rr, stage);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      yhat[j] = __fmul2_rn(x.pair(j), ry2);
+      u[j] = t.pair(j);
+      if (NEXT) {
+        rhat[j] = __fmul2_rn(rr.pair(j), r2);
+        u[j] = __ffma2_rn(r2, __fmul2_rn(rn.pair(j), w[i].pair(j)), u[j]);
+      }
+    }
+  };
+  // a row's sums, on their way to all CTAs
+  auto first_pass = [&](int row, int stage) {
+    if ((row & 31) == 0 && row + lane < count) {
+      const int64_t mine = first_row + static_cast<int64_t>(row + lane) * clusters;
+      if (NEXT) rstds = __ldg(a.rstd + mine);
+      if (a.rstd_post) posts = __ldg(a.rstd_post + mine);
+      if (a.gate) gates = __ldg(a.gate + mine);
+    }
+    rs = NEXT ? __shfl_sync(0xffffffffu, rstds, row & 31) : 0.f;
+    rs_y = __shfl_sync(0xffffffffu, posts, row & 31);
+    gate = __shfl_sync(0xffffffffu, gates, row & 31);
+    rows.wait();
+    float2 s1 = make_float2(0.f, 0.f), s2 = s1, s3 = s1;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      terms(i, stage, rs, rs_y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 q = __fmul2_rn(yhat[j], wp[i].pair(j));
+        if (NEXT) {
+          s1 = __ffma2_rn(__fmul2_rn(rn.pair(j), rhat[j]), w[i].pair(j), s1);
+          s3 = __ffma2_rn(rhat[j], q, s3);
+          dw[i][j] = __ffma2_rn(rn.pair(j), rhat[j], dw[i][j]);
+        }
+        s2 = __ffma2_rn(u[j], q, s2);
+      }
+    }
+    const float s = warp_sum4(make_float4(s1.x + s1.y, s2.x + s2.y, s3.x + s3.y, 0.f));
+    if (lane < 4 * ranks)
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(send + (row & 3) * 1024), "f"(s) : "memory");
+    __syncwarp();
+  };
+  first_pass(0, 0);
+  cluster_arrive();
+  int stage = 0;
+  for (int row = 0; row < count; ++row) {
+    const bool more = row + 1 < count;
+    const float rs_0 = rs, rs_y_0 = rs_y, gate_0 = gate;
+    const int next = stage + 1 == kAhead ? 0 : stage + 1;
+    __syncwarp();      // all lanes have done with the row that is overwritten
+    rows.issue(row + 2 < count);
+    if (more) first_pass(row + 1, next);
+    cluster_wait();
+    if (more) cluster_arrive();
+    float s = 0.f;
+    for (int i = lane; i < ranks * warps * 4; i += 32) s += part[row & 3][i];
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    const float sum1 = __shfl_sync(0xffffffffu, s, 0), sum2 = __shfl_sync(0xffffffffu, s, 2), sum3 = __shfl_sync(0xffffffffu, s, 1);
+    const float m = NEXT ? rs_0 * sum1 * inv_H : 0.f, dot = NEXT ? fmaf(-m, sum3, sum2) : sum2;
+    if (a.d_gate && rank == 0 && threadIdx.x == 0) a.d_gate[first_row + static_cast<int64_t>(row) * clusters] = dot;
+    const float back = a.rstd_post ? -gate_0 * dot * inv_H : 0.f;
+    const float2 m2 = make_float2(-m, -m), gate2 = make_float2(gate_0, gate_0), back2 = make_float2(back, back);
+    const float2 rs_y2 = make_float2(rs_y_0, rs_y_0);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      terms(i, stage, rs_0, rs_y_0);
+      float2 oy[4], od[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 dr = NEXT ? __ffma2_rn(m2, rhat[j], u[j]) : u[j];
+        od[j] = __fmul2_rn(scale2, dr);
+        const float2 dp = __fmul2_rn(gate2, dr);
+        dwp[i][j] = __ffma2_rn(dp, yhat[j], dwp[i][j]);
+        oy[j] = __fmul2_rn(rs_y2, __ffma2_rn(back2, yhat[j], __fmul2_rn(dp, wp[i].pair(j))));
+      }
+      store8_if(dy + i * 256, oy, rows.in[i]);
+      store8_if(d_residual + i * 256, od, rows.in[i]);
+    }
+    const int64_t step = static_cast<int64_t>(clusters) * H;
+    dy += step, d_residual += step;
+    stage = next;
+  }
+  if (a.part) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (rows.in[i]) {
+        const int64_t at = static_cast<int64_t>(first_row) * H + c0 + i * 256;
+        if (NEXT) store8(a.part + at, &dw[NEXT ? i : 0][0].x);
+        store8(a.part + static_cast<int64_t>(clusters) * H + at, &dwp[i][0].x);
+      }
+  }
+}
+
 // out[which][c] = sum of the blocks' partial sums, as norm.cu's: 32 columns by 32
 // groups of blocks per thread block, each group in block order, then the groups.
 __global__ void __launch_bounds__(1024) join_dweight_kernel(const float* __restrict__ part, int blocks, int H,
@@ -536,6 +693,47 @@ cudaError_t launch_join_bwd_v(const JoinBwd& a, int sms, int* blocks, cudaStream
   return cudaGetLastError();
 }
 
+// The same for wide rows: as few CTAs a row as fit an SM by twos, or by ones where eight do
+// not suffice.
+template <typename E, bool NEXT>
+cudaError_t launch_join_bwd_wide(const JoinBwd& a, int sms, int* blocks, cudaStream_t st) {
+  constexpr int kWarpBytes = RowStream<E, NEXT ? 4 : 2, 2, kAhead>::bytes(32);
+  constexpr int kTwo = std::min(8, kRingPerSm / 2 / kWarpBytes), kOne = std::min(16, kRingPerSm / kWarpBytes);
+  auto kern = join_bwd_wide_kernel<E, NEXT>;
+  int ranks = 1, log = 0;
+  const int most = a.H <= 8 * kTwo * 512 ? kTwo : kOne;
+  while ((a.H + 512 * ranks - 1) / (512 * ranks) > most) ranks *= 2, ++log;
+  const int warps = (a.H + 512 * ranks - 1) / (512 * ranks);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(kern, ready);
+  if (e != cudaSuccess) return e;
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ranks, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.stream = st;
+  // the clusters that fit the device at once, asked for once per device and shape
+  cfg.blockDim = dim3(32 * warps);
+  cfg.dynamicSmemBytes = warps * kWarpBytes;
+  static std::atomic<int> known[64][4][17];
+  int fit = known[dev & 63][log][warps].load(std::memory_order_relaxed);
+  if (fit == 0) {
+    cfg.gridDim = dim3(8 * sms >> log << log);
+    e = cudaOccupancyMaxActiveClusters(&fit, kern, &cfg);
+    if (e != cudaSuccess) return e;
+    if (fit < 1) return cudaErrorLaunchOutOfResources;
+    known[dev & 63][log][warps].store(fit, std::memory_order_relaxed);
+  }
+  *blocks = static_cast<int>(std::min<int64_t>(a.T, std::min(fit, kMaxBwdBlocks)));
+  cfg.gridDim = dim3(*blocks * ranks);
+  return cudaLaunchKernelEx(&cfg, kern, a, ranks);
+}
+
 template <typename E, bool NEXT>
 cudaError_t launch_join_bwd(const JoinBwd& a, int sms, int* blocks, cudaStream_t st) {
   const int warps = (a.H + 255) / 256;
@@ -544,9 +742,11 @@ cudaError_t launch_join_bwd(const JoinBwd& a, int sms, int* blocks, cudaStream_t
   // with up to 128 registers, 109 with 80; bf16, two blocks: 57 and 52)
   if (warps <= (sizeof(E) == 4 ? 8 : 12)) return launch_join_bwd_v<E, NEXT, 1, 384, 1>(a, sms, blocks, st);
   if (warps <= 16) return launch_join_bwd_v<E, NEXT, 1, 512, 9>(a, sms, blocks, st);
-  if (warps <= 32) return launch_join_bwd_v<E, NEXT, 2, 512, 9>(a, sms, blocks, st);
-  if (warps <= 64) return launch_join_bwd_v<E, NEXT, 4, 512, 9>(a, sms, blocks, st);
-  return launch_join_bwd_v<E, NEXT, 4, 1024, 17>(a, sms, blocks, st);
+  // two up to 8192 in bf16 (8192 x 8192: 157 us, on clusters 161; 4096 x 8192 fp32, whose
+  // ring does not fit: 198 and 154)
+  if constexpr (sizeof(E) == 2)
+    if (warps <= 32) return launch_join_bwd_v<E, NEXT, 2, 512, 9>(a, sms, blocks, st);
+  return launch_join_bwd_wide<E, NEXT>(a, sms, blocks, st);
 }
 
 bool join_dims_ok(int64_t T, int32_t H, int32_t dtype) {

@@ -256,6 +256,19 @@ def test_backward_over_inputs(T, dtype, dy, d_residual):
     Grad(T, 264, DT[dtype]).check_bwd(dy=dy, d_residual=d_residual)
 
 
+@pytest.mark.parametrize("T,H", [(1, 8208), (150, 9000), (320, 8712), (230, 16384), (90, 16392), (161, 32768)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_backward_of_wide_rows(T, H, dtype):
+    """Rows on several CTAs, one row and several for each."""
+    Grad(T, H, DT[dtype]).check_bwd()
+    Grad(T, H, DT[dtype], next_norm=False, post_norm=False, gate=False).check_bwd()
+    c = Grad(T, H, DT[dtype], d_total=False, scale=0.5)
+    a, b = c.check_bwd(), c.run_bwd()
+    assert all(torch.equal(a[k], b[k]) for k in a)
+    a = c.run_bwd(dy="dn", d_residual="y")
+    assert all(torch.equal(a[k], b[k]) for k in a)
+
+
 def test_backward_without_weight_gradients():
     Grad(700, 2880, torch.bfloat16).check_bwd(sums=False)
 
