@@ -324,13 +324,20 @@ __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 1) join_bwd_kernel(con
   const int lane = threadIdx.x & 31;
   const int c0 = (threadIdx.x >> 5) * 256 * V + lane * 8;     // of vector 0
   // the weights, and a row's terms between its two passes, in registers where these allow
-  constexpr bool KEEP = V == 1;
-  constexpr int K = KEEP ? V : 1;
-  float2 wp[K][4], w[K][4];
+  // (with two vectors the weights are packed and the row is read from the ring again: with
+  // all of it in registers or the weights loaded in each pass, 8192 x 5152 112 us, not 91)
+  constexpr bool KEEP = V == 1, AGAIN = !KEEP && D > 0;
+  float2 wp[1][4], w[1][4];
+  Raw8<E> wp_raw[V], w_raw[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    wp_raw[i].ones(), w_raw[i].ones();
+    if (a.post_weight && rows.in[i]) wp_raw[i].load(static_cast<const E*>(a.post_weight) + c0 + i * 256);
+    if (NEXT && rows.in[i]) w_raw[i].load(static_cast<const E*>(a.weight) + c0 + i * 256);
+  }
   auto weights = [&](int i) {
-    const E* pw = static_cast<const E*>(a.post_weight);
-    load_weights(pw ? pw + c0 + i * 256 : pw, rows.in[i], wp[KEEP ? i : 0]);
-    if (NEXT) load_weights(static_cast<const E*>(a.weight) + c0 + i * 256, rows.in[i], w[KEEP ? i : 0]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) wp[0][j] = wp_raw[i].pair(j), w[0][j] = w_raw[i].pair(j);
   };
   if (KEEP) weights(0);
   float2 dw[NEXT ? V : 1][4], dwp[V][4];
@@ -359,16 +366,26 @@ __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 1) join_bwd_kernel(con
     rows.wait();
     rows.issue(row + D - 1 < count);
     const float2 rs2 = make_float2(rs, rs), rs_y2 = make_float2(rs_y, rs_y);
-    Raw8<E> ry[V], rt[V], rn[NEXT ? V : 1], rr[NEXT ? V : 1];
+    constexpr int R = AGAIN ? 1 : V;
+    Raw8<E> ry[R], rt[R], rn[NEXT ? R : 1], rr[NEXT ? R : 1];
+    auto take = [&](int i) {
+      const int r = AGAIN ? 0 : i, k = NEXT ? r : 0;
+      rows.take(0, i, ry[r]);
+      rows.take(1, i, rt[r]);
+      if (NEXT) {
+        rows.take(N - 2, i, rn[k]);
+        rows.take(N - 1, i, rr[k]);
+      }
+    };
     float2 u[4], rhat[4], yhat[4];
     // u = d_total + rs dn weight, rhat, yhat of vector i
     auto terms = [&](int i) {
-      const int k = NEXT ? i : 0;
+      const int r = AGAIN ? 0 : i, k = NEXT ? r : 0;
       if (!KEEP) weights(i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        yhat[j] = __fmul2_rn(ry[i].pair(j), rs_y2);
-        u[j] = rt[i].pair(j);
+        yhat[j] = __fmul2_rn(ry[r].pair(j), rs_y2);
+        u[j] = rt[r].pair(j);
         if (NEXT) {
           rhat[j] = __fmul2_rn(rr[k].pair(j), rs2);
           u[j] = __ffma2_rn(rs2, __fmul2_rn(rn[k].pair(j), w[0][j]), u[j]);
@@ -378,13 +395,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 1) join_bwd_kernel(con
     float2 s1 = make_float2(0.f, 0.f), s2 = s1, s3 = s1;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int k = NEXT ? i : 0;
-      rows.take(0, i, ry[i]);
-      rows.take(1, i, rt[i]);
-      if (NEXT) {
-        rows.take(N - 2, i, rn[k]);
-        rows.take(N - 1, i, rr[k]);
-      }
+      const int k = NEXT && !AGAIN ? i : 0;
+      take(i);
       terms(i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -393,12 +405,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 1) join_bwd_kernel(con
           const float2 g = __fmul2_rn(rn[k].pair(j), rhat[j]);
           s1 = __ffma2_rn(g, w[0][j], s1);
           s3 = __ffma2_rn(rhat[j], q, s3);
-          dw[k][j] = __ffma2_rn(rn[k].pair(j), rhat[j], dw[k][j]);
+          dw[i][j] = __ffma2_rn(rn[k].pair(j), rhat[j], dw[i][j]);
         }
         s2 = __ffma2_rn(u[j], q, s2);
       }
     }
-    rows.next();
+    if (!AGAIN) rows.next();
     float m = 0.f, dot;
     if (NEXT) {
       const float4 s = block_sum4<MAXT>(make_float4(s1.x + s1.y, s2.x + s2.y, s3.x + s3.y, 0.f), part[flip]);
@@ -412,6 +424,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 1) join_bwd_kernel(con
     const float2 m2 = make_float2(-m, -m), gate2 = make_float2(gate, gate), back2 = make_float2(back, back);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+      if (AGAIN) take(i);
       if (!KEEP) terms(i);
       float2 oy[4], od[4];
 #pragma unroll
@@ -425,6 +438,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 384 ? 2 : 1) join_bwd_kernel(con
       store8_if(dy + i * 256, oy, rows.in[i]);
       store8_if(d_residual + i * 256, od, rows.in[i]);
     }
+    if (AGAIN) rows.next();
     const int64_t step = static_cast<int64_t>(gridDim.x) * H;
     dy += step, d_residual += step;
   }
@@ -742,7 +756,7 @@ cudaError_t launch_join_bwd(const JoinBwd& a, int sms, int* blocks, cudaStream_t
   // with up to 128 registers, 109 with 80; bf16, two blocks: 57 and 52)
   if (warps <= (sizeof(E) == 4 ? 8 : 12)) return launch_join_bwd_v<E, NEXT, 1, 384, 1>(a, sms, blocks, st);
   if (warps <= 16) return launch_join_bwd_v<E, NEXT, 1, 512, 9>(a, sms, blocks, st);
-  // two up to 8192 in bf16 (8192 x 8192: 157 us, on clusters 161; 4096 x 8192 fp32, whose
+  // two up to 8192 in bf16 (8192 x 8192: 145 us, on clusters 161; 4096 x 8192 fp32, whose
   // ring does not fit: 198 and 154)
   if constexpr (sizeof(E) == 2)
     if (warps <= 32) return launch_join_bwd_v<E, NEXT, 2, 512, 9>(a, sms, blocks, st);
