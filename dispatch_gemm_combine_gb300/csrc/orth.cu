@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         if (lane == 0) record_error(args.err, kErrTimeout);
         break;
       }
-      asm volatile("fence.proxy.async;" ::: "memory");   // the loads see what the wait saw
+      asm volatile("fence.proxy.async.global;" ::: "memory");   // the loads see what the wait saw
       const int x = u.step & 1;
       const CUtensorMap* am = u.kind == kGram ? &maps.xk[x] : (u.kind == kPoly ? &maps.ak : &maps.bk);
       const CUtensorMap* bm = u.kind == kGram ? &maps.xs[x] : (u.kind == kPoly ? &maps.as : &maps.xn[x]);
