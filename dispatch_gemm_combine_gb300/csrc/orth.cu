@@ -25,7 +25,7 @@
 //
 // Measured, five steps: 4 of 2880 x 2880 fp32 1.33 - 1.44 ms (by the clock that the power
 // leaves), 8 of 2816 x 2816 at 1.66 PFLOP/s of what is needed, at the rate that a library
-// product sustains; 6 of 333 x 1001 115 us and 8 of 128 x 128 25 us, both bound by the
+// product sustains; 6 of 333 x 1001 110 us and 8 of 128 x 128 23 us, both bound by the
 // chain of dependent steps.
 #include <algorithm>
 #include <atomic>
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         if (lane == 0) record_error(args.err, kErrTimeout);
         break;
       }
-      asm volatile("fence.proxy.async.global;" ::: "memory");   // the loads see what the wait saw
+      asm volatile("fence.proxy.async.global;" ::: "memory");   // the loads see what the wait saw (a fence for all memory: 6 of 333 x 1001 116 us)
       const int x = u.step & 1;
       const CUtensorMap* am = u.kind == kGram ? &maps.xk[x] : (u.kind == kPoly ? &maps.ak : &maps.bk);
       const CUtensorMap* bm = u.kind == kGram ? &maps.xs[x] : (u.kind == kPoly ? &maps.as : &maps.xn[x]);
@@ -1015,9 +1015,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
         for (int k = halves ? (lane & 1) + (lane >> 4 << 1) : lane & 1; in && k < a.ranks; k += halves ? 4 : 2)
           st_cluster4u(mapa_shared(to, (rank + k) & (a.ranks - 1)), u);
       }
-      asm volatile("fence.proxy.async;" ::: "memory");
       __syncwarp();
       cluster_sync();
+      // (what the others stored is behind the barrier, and before the fence below)
       // rows of the blocks below the diagonal, eight columns at a time
       for (int i = warp; i < 24; i += kSmallThreads / 32) {
         const int t = i >> 2, block = t < 1 ? 1 : (t < 3 ? 2 : 3);      // (1,0) (2,0) (2,1) (3,0) ..
@@ -1042,7 +1042,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1) orth_small_kernel(const __gr
     // ---- poly
     if (warp == 0 && elect_one()) {
       tc_fence_after();
-      asm volatile("fence.proxy.async;" ::: "memory");
 #pragma unroll 1
       for (int k = 0; k < mc / 16; ++k) {
         const uint32_t d = dA + (k >> 2) * (kChunkBytes / 16) + 2 * (k & 3);
