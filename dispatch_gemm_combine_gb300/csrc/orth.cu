@@ -224,10 +224,10 @@ constexpr int kEpiWarps = 8;             // two for each quarter of the tensor m
 constexpr int kOrthThreads = 64 + 32 * kEpiWarps;
 constexpr int kTileBytes = 32 * 32 * 2;  // what a warp stores at once
 constexpr int kEpiWarpBytes = 2 * kTileBytes;
-constexpr int kOrthBars = (2 * kOrthStages + 5) * 8 + 16;
+constexpr int kOrthBars = (2 * kOrthStages + 5) * 8 + 32;
 constexpr int kOrthSmem = 1024 + kOrthStages * kStageBytes + kEpiWarps * kEpiWarpBytes + kOrthBars;
 constexpr int kMaxOrthSteps = 32;
-constexpr int kUnitArrivals = 2 * kEpiWarps;   // of a pair
+constexpr int kUnitArrivals = 2;               // one per CTA
 static_assert(kOrthSmem <= 232448, "shared memory budget");
 
 struct OrthMaps {
@@ -345,6 +345,14 @@ __device__ __forceinline__ void add_release(int* p, int v) {
   asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
+// To a count in shared memory; what is done before it, in any of the warps that have
+// counted, is before what the last one does.
+__device__ __forceinline__ uint32_t add_cta(uint32_t addr, uint32_t v) {
+  uint32_t old;
+  asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(v) : "memory");
+  return old;
+}
+
 // Wait until the unit's matrix has finished the phase before: false when that takes
 // longer than the limit.
 __device__ __forceinline__ bool orth_wait(const OrthArgs& a, const OrthUnit& u, uint64_t timeout_ns) {
@@ -414,6 +422,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   const uint32_t tempty_bar = tfull_bar + 16;        // [2]
   const uint32_t drain_bar = tempty_bar + 16;        // end of the MMA stream
   const uint32_t tmem_slot = drain_bar + 8;
+  const uint32_t stored = tmem_slot + 8;             // [4]: warps that have stored a unit
   volatile uint32_t* tmem_slot_g = reinterpret_cast<volatile uint32_t*>(gbase + (tmem_slot - sbase));
 
   const int warp = threadIdx.x >> 5;
@@ -434,6 +443,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     }
     mbar_init(drain_bar, 1);
     fence_barrier_init();
+    st_shared_v4u(stored, 0u, 0u, 0u, 0u);
   }
   if (warp == 2 && lane < static_cast<int>(sizeof(OrthMaps) / sizeof(CUtensorMap)))
     prefetch_tmap(reinterpret_cast<const CUtensorMap*>(&maps) + lane);
@@ -571,6 +581,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     uint8_t* stage_g = gbase + (s_epi - sbase) + (warp - 2) * kEpiWarpBytes;
     const uint32_t stage_s = s_epi + (warp - 2) * kEpiWarpBytes;
     int buf = 0;
+    int unit = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = unit0; t < total; t += ustride) {
@@ -683,7 +694,11 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         if (!last) {
           // (a completed bulk store is ordered before what follows without a proxy fence)
           bulk_wait_all();
-          add_release(args.counters + u.phase * args.batch + u.e, 1);
+          // the last of the CTA's warps tells the others: releases and additions to one
+          // address are dear (each warp for itself, 6 x 333 x 1001 111 us instead of 101).  (A
+          // warp is at most two units ahead of another, so four units' counts do not meet)
+          if ((add_cta(stored + (unit & 3) * 4, 1) & (kEpiWarps - 1)) == kEpiWarps - 1)
+            add_release(args.counters + u.phase * args.batch + u.e, 1);
         }
       }
       __syncwarp();
@@ -691,6 +706,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         acc = 0;
         acc_phase ^= 1u;
       }
+      ++unit;
     }
     if (lane == 0) bulk_wait_all();
     __syncwarp();
