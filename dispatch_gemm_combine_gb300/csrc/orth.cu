@@ -224,7 +224,7 @@ constexpr int kEpiWarps = 8;             // two for each quarter of the tensor m
 constexpr int kOrthThreads = 64 + 32 * kEpiWarps;
 constexpr int kTileBytes = 32 * 32 * 2;  // what a warp stores at once
 constexpr int kEpiWarpBytes = 2 * kTileBytes;
-constexpr int kOrthBars = (2 * kOrthStages + 5) * 8 + 32;
+constexpr int kOrthBars = (2 * kOrthStages + 5) * 8 + 40;
 constexpr int kOrthSmem = 1024 + kOrthStages * kStageBytes + kEpiWarps * kEpiWarpBytes + kOrthBars;
 constexpr int kMaxOrthSteps = 32;
 constexpr int kUnitArrivals = 2;               // one per CTA
@@ -353,6 +353,20 @@ __device__ __forceinline__ uint32_t add_cta(uint32_t addr, uint32_t v) {
   return old;
 }
 
+__device__ __forceinline__ void store_release_cta(uint32_t addr, int v) {
+  asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+// Wait until the count has come to v: false when that takes longer than the limit.
+__device__ __forceinline__ bool wait_count_cta(uint32_t addr, int v, uint64_t timeout_ns) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t i = 1;; ++i) {
+    int now;
+    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(now) : "r"(addr) : "memory");
+    if (now >= v) return true;
+    if ((i & 31u) == 0 && global_timer_ns() - t0 > timeout_ns) return false;
+  }
+}
+
 // Wait until the unit's matrix has finished the phase before: false when that takes
 // longer than the limit.
 __device__ __forceinline__ bool orth_wait(const OrthArgs& a, const OrthUnit& u, uint64_t timeout_ns) {
@@ -423,6 +437,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   const uint32_t drain_bar = tempty_bar + 16;        // end of the MMA stream
   const uint32_t tmem_slot = drain_bar + 8;
   const uint32_t stored = tmem_slot + 8;             // [4]: warps that have stored a unit
+  const uint32_t begun = stored + 16;                // units whose matrix the producer has waited for
   volatile uint32_t* tmem_slot_g = reinterpret_cast<volatile uint32_t*>(gbase + (tmem_slot - sbase));
 
   const int warp = threadIdx.x >> 5;
@@ -444,6 +459,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     mbar_init(drain_bar, 1);
     fence_barrier_init();
     st_shared_v4u(stored, 0u, 0u, 0u, 0u);
+    store_release_cta(begun, 0);
   }
   if (warp == 2 && lane < static_cast<int>(sizeof(OrthMaps) / sizeof(CUtensorMap)))
     prefetch_tmap(reinterpret_cast<const CUtensorMap*>(&maps) + lane);
@@ -473,6 +489,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     int stage = 0;
     uint32_t phase = 0;
     int64_t issued = 0;
+    int unit = 0;
     bool ok = true;
     for (int t = unit0; t < total && ok; t += ustride) {
       const OrthUnit u = orth_unit(args, t);
@@ -480,6 +497,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         if (lane == 0) record_error(args.err, kErrTimeout);
         break;
       }
+      if (lane == 0) store_release_cta(begun, ++unit);
       asm volatile("fence.proxy.async.global;" ::: "memory");   // the loads see what the wait saw (a fence for all memory: 6 of 333 x 1001 116 us)
       const int x = u.step & 1;
       const CUtensorMap* am = u.kind == kGram ? &maps.xk[x] : (u.kind == kPoly ? &maps.ak : &maps.bk);
@@ -606,7 +624,9 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
                                                                : make_uint4(0u, 0u, 0u, 0u);
       };
       if (u.kind == kPoly) {
-        if (lane == 0) good = orth_wait(args, u, 2 * tmo);
+        // (the producer's word for it: polls of the counters by all warps slow the others
+        // down)
+        if (lane == 0) good = wait_count_cta(begun, unit + 1, 2 * tmo);
         good = __shfl_sync(0xffffffffu, good, 0);
         if (good) fetch_a(u.c0 + first);
       }
