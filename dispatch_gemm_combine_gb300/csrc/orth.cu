@@ -25,7 +25,7 @@
 //
 // Measured, five steps: 4 of 2880 x 2880 fp32 1.33 - 1.44 ms (by the clock that the power
 // leaves), 8 of 2816 x 2816 at 1.66 PFLOP/s of what is needed, at the rate that a library
-// product sustains; 6 of 333 x 1001 110 us and 8 of 128 x 128 23 us, both bound by the
+// product sustains; 6 of 333 x 1001 101 us and 8 of 128 x 128 23 us, both bound by the
 // chain of dependent steps.
 #include <algorithm>
 #include <atomic>
@@ -1394,19 +1394,26 @@ OrthIn orth_in(const void* g, int32_t dtype, int64_t e0, int batch, int64_t M, i
   return OrthIn{p, ld, stride, static_cast<int>(M), static_cast<int>(N), rows_on_16(p, es, ld, stride, batch)};
 }
 
-// Width of the column tiles: the one with the least time.  Full tiles are bound by the
-// products, narrower ones by their loads (16 KB for the rows of A whatever their width):
-// in units of a full tile's 256 they take 164 and 148, and each about 32 for its start
-// and end.  One matrix alone waits for each phase's last tiles, several fill one
-// another's.
+// Width of the column tiles of a product with kb blocks of K: the one with the least time,
+// in cycles.  A block takes 512 (bound by the products), 328 or 296 (narrower tiles are
+// bound by their loads: 16 KB for the rows of A whatever their width); beside them, once,
+// the start, the last tile's results (twice as many to store where they are mirrored) and the
+// word to the next phase.  One matrix alone waits for each phase's last tiles, several fill
+// one another's gaps, from the second round on.  (8 x 1000 x 1000: 256 columns for both
+// kinds 278 us, 128 for the symmetric ones 248; 32 x 140 x 500: 128 and 256 99, 64 and 128 90.)
 template <typename F>
-int orth_width(const F& units, int batch, int pairs) {
+int orth_width(const F& units, int batch, int pairs, double kb, bool sym) {
   int best = 256;
   double least = 1e300;
   for (int bn = 256; bn >= 64; bn /= 2) {
-    const double waves = static_cast<double>(units(bn)) * batch / pairs;
-    const double each = 32 + (bn == 256 ? 256 : bn == 128 ? 164 : 148);
-    const double t = (batch == 1 ? std::ceil(waves) : std::max(1.0, waves)) * each;
+    double waves = static_cast<double>(units(bn)) * batch / pairs;
+    if (batch == 1)
+      waves = std::ceil(waves);
+    else if (waves < 2)
+      waves = waves <= 1 ? 1 : waves + 0.3 * (2 - waves);
+    const double block = bn == 256 ? 512 : bn == 128 ? 328 : 296;
+    const double once = bn == 64 ? 4500 : bn == 128 ? (sym ? 6000 : 5600) : (sym ? 10000 : 7000);
+    const double t = waves * kb * block + once;
     if (t < least) least = t, best = bn;
   }
   return best;
@@ -1414,10 +1421,11 @@ int orth_width(const F& units, int batch, int pairs) {
 
 void orth_tiles(OrthArgs* a, int pairs) {
   const auto upd = [&](int bn) { return static_cast<int64_t>(a->mt) * ((a->n + bn - 1) / bn); };
-  int bn = orth_width([&](int w) { return sym_units(a->m, w); }, a->batch, pairs);
+  const double kb_m = (a->m + 63) / 64, kb_n = (a->n + 63) / 64;
+  int bn = orth_width([&](int w) { return sym_units(a->m, w); }, a->batch, pairs, (kb_n + kb_m) / 2, true);
   a->bn_sym = bn, a->nt_sym = (a->m + bn - 1) / bn;
   a->units_sym = static_cast<int>(sym_units(a->m, bn));
-  bn = orth_width(upd, a->batch, pairs);
+  bn = orth_width(upd, a->batch, pairs, kb_m, false);
   a->bn_upd = bn, a->nt_upd = (a->n + bn - 1) / bn;
   a->units_upd = static_cast<int>(upd(bn));
 }
