@@ -1396,7 +1396,7 @@ OrthIn orth_in(const void* g, int32_t dtype, int64_t e0, int batch, int64_t M, i
 
 // Width of the column tiles of a product with kb blocks of K: the one with the least time,
 // in cycles.  A block takes 512 (bound by the products), 328 or 296 (narrower tiles are
-// bound by their loads: 16 KB for the rows of A whatever their width); beside them, once,
+// bound by what the producer and the issuer do for a block); beside them, once,
 // the start, the last tile's results (twice as many to store where they are mirrored) and the
 // word to the next phase.  One matrix alone waits for each phase's last tiles, several fill
 // one another's gaps, from the second round on.  (8 x 1000 x 1000: 256 columns for both
