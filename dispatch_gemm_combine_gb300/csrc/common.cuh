@@ -281,6 +281,41 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
                : "memory");
 }
 
+// The same on a barrier that also expects `bytes`.  (Relaxed: what the barrier stands
+// for is the bytes, which the copies themselves count.)
+__device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t cluster_addr, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr),
+               "r"(bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Wait until all loads of a pair's ring have landed.  The leader's full barrier of a
+// slot (`full_bar` + 8 slot) takes one arrival and the bytes of each CTA; n0 and n1 are
+// the slots that the CTAs have taken.  Each CTA waits by its own clock, so after a wait
+// that ran out one may have taken more than the other (STAGES more at most: a slot is
+// taken again after products that waited for both).  The arrivals that the other one
+// left out are made here, so each barrier's last phase ends with the bytes that were
+// loaded.  Called by one thread of the leader when no warp of the pair uses the ring.
+template <int STAGES>
+__device__ __forceinline__ bool drain_pair_loads(uint32_t full_bar, uint32_t n0, uint32_t n1, uint64_t timeout_ns) {
+  const uint32_t n = max(n0, n1);
+  for (uint32_t i = min(n0, n1); i < n; ++i) mbar_arrive(full_bar + 8 * (i % STAGES));
+  bool ok = true;
+  for (uint32_t s = 0; s < min(n, static_cast<uint32_t>(STAGES)); ++s)
+    ok = mbar_wait(full_bar + 8 * s, ((n - 1 - s) / STAGES) & 1u, timeout_ns) && ok;
+  return ok;
+}
+
 // TMA loads of the 2-SM MMA: the box lands in this CTA's shared memory and
 // the byte count completes on `bar`, which may be the leader CTA's barrier.
 __device__ __forceinline__ void tma_load_2d_g2(uint32_t dst, const CUtensorMap* map, uint32_t bar,

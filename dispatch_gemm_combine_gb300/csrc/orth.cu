@@ -438,6 +438,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   const uint32_t tmem_slot = drain_bar + 8;
   const uint32_t stored = tmem_slot + 8;             // [4]: warps that have stored a unit
   const uint32_t begun = stored + 16;                // units whose matrix the producer has waited for
+  const uint32_t issued_slot = begun + 4;            // the leader's [2]: stages that each CTA has loaded
   volatile uint32_t* tmem_slot_g = reinterpret_cast<volatile uint32_t*>(gbase + (tmem_slot - sbase));
 
   const int warp = threadIdx.x >> 5;
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full_bar + 8 * s, 1);
+      mbar_init(full_bar + 8 * s, 2);      // of each CTA's producer
       mbar_init(empty_bar + 8 * s, 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
     const uint32_t full_l = mapa_shared(full_bar, 0);   // the leader's, for the bytes of both
     int stage = 0;
     uint32_t phase = 0;
-    int64_t issued = 0;
+    uint32_t issued = 0;
     int unit = 0;
     bool ok = true;
     for (int t = unit0; t < total && ok; t += ustride) {
@@ -516,7 +517,10 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         const uint32_t fb = full_l + 8 * stage;
         const int k0 = kb * 64;
         if (elect_one()) {
-          if (leader) mbar_arrive_expect_tx(full_bar + 8 * stage, 2 * bytes);
+          if (leader)
+            mbar_arrive_expect_tx(full_bar + 8 * stage, bytes);
+          else
+            mbar_arrive_expect_tx_cluster(fb, bytes);
           tma_load_3d_g2(sA, am, fb, k0, ra, u.e);
           tma_load_3d_g2(sB, bm, fb, upd ? rb : k0, upd ? k0 : rb, u.e);
           if (two) tma_load_3d_g2(sB + 64 * 128, bm, fb, rb + 64, k0, u.e);
@@ -526,15 +530,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         ring_next(stage, phase);
       }
     }
-    // Before the CTAs may exit, every load issued must have landed: the leader's
-    // full barriers count the bytes of both.
-    if (leader && lane == 0) {
-      for (int s = 0; s < STAGES; ++s) {
-        const int64_t n_s = issued > s ? (issued - 1 - s) / STAGES + 1 : 0;
-        if (n_s > 0 && !mbar_wait(full_bar + 8 * s, static_cast<uint32_t>((n_s - 1) & 1), kDrain))
-          record_error(args.err, kErrTimeout);
-      }
-    }
+    if (lane == 0) st_cluster_u32(mapa_shared(issued_slot + 4 * crank, 0), issued);
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -733,11 +729,15 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
   }
 
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();
+  // Before the CTAs may exit, every load that either has issued must have landed.
+  if (leader && warp == 0 && lane == 0 &&
+      !drain_pair_loads<STAGES>(full_bar, ld_shared_u32(issued_slot), ld_shared_u32(issued_slot + 4), kDrain))
+    record_error(args.err, kErrTimeout);
   // Every MMA of the pair has completed once the drain barrier has seen the leader's
   // final commit; only then may tensor memory be freed and the CTAs exit.
   if (warp == 1 && lane == 0 && !mbar_wait(drain_bar, 0, 4 * tmo + kDrain)) record_error(args.err, kErrTimeout);
-  __syncthreads();
+  __syncwarp();
   cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc2(tmem_base, 512);
