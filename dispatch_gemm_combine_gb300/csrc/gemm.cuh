@@ -536,6 +536,7 @@ __global__ void __launch_bounds__(192, 1)
   const uint32_t tempty_bar = tfull_bar + 16;        // [2]
   const uint32_t drain_bar = tempty_bar + 16;        // [1] end of the MMA stream
   const uint32_t tmem_slot = drain_bar + 8;
+  const uint32_t issued_slot = tmem_slot + 8;        // the leader's [2]: slots that each CTA has loaded
   volatile uint32_t* tmem_slot_g =
       reinterpret_cast<volatile uint32_t*>(gbase + (tmem_slot - sbase));
 
@@ -548,7 +549,7 @@ __global__ void __launch_bounds__(192, 1)
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full_bar + 8 * s, 1);
+      mbar_init(full_bar + 8 * s, C::PAIR);   // of each CTA's producer
       mbar_init(empty_bar + 8 * s, 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -612,7 +613,7 @@ __global__ void __launch_bounds__(192, 1)
     const uint32_t full_bar_l = leader_addr(full_bar);
     int stage = 0;
     uint32_t phase = 0;
-    int64_t issued = 0;
+    uint32_t issued = 0;
     bool ok = true;
     for (int t = unit0; t < total && ok; t += ustride) {
       const TileInfo ti = decode_tile<C::BN_OUT, C::kWgrad, C::PAIR, C::SW>(args, t, C::BK, crank);
@@ -647,10 +648,13 @@ __global__ void __launch_bounds__(192, 1)
           // loads its token rows with the 32-row box of maps.a2
           const bool small_b = C::SW && ti.nn <= 64;
           const uint32_t stage_tx = small_b ? C::A_BYTES + 32 * 128 : C::STAGE_BYTES;
-          // the leader expects the bytes of both CTAs of the pair
+          // each CTA of the pair arrives with its own bytes
           if (leader) {
-            mbar_arrive_expect_tx(fb, C::PAIR * stage_tx);
-            if (two) mbar_arrive_expect_tx(fb2, C::PAIR * C::LO_BYTES);
+            mbar_arrive_expect_tx(fb, stage_tx);
+            if (two) mbar_arrive_expect_tx(fb2, C::LO_BYTES);
+          } else {
+            mbar_arrive_expect_tx_cluster(fbt, stage_tx);
+            if (two) mbar_arrive_expect_tx_cluster(fbt2, C::LO_BYTES);
           }
           auto load2 = [&](uint32_t dst, const CUtensorMap* m, int c0, int c1, uint32_t bar = 0) {
             if (bar == 0) bar = fbt;
@@ -746,16 +750,7 @@ __global__ void __launch_bounds__(192, 1)
         if (two) ring_next(stage, phase);
       }
     }
-    // Before the CTAs may exit, every load issued must have landed: the
-    // leader's full barriers count the bytes of both CTAs.
-    if (lane == 0 && leader) {
-      for (int s = 0; s < STAGES; ++s) {
-        const int64_t n_s = (issued > s) ? (issued - 1 - s) / STAGES + 1 : 0;
-        if (n_s > 0 &&
-            !mbar_wait(full_bar + 8 * s, static_cast<uint32_t>((n_s - 1) & 1), kDrainNs))
-          record_error(args.err, kErrTimeout);
-      }
-    }
+    if (lane == 0) st_cluster_u32(mapa_shared(issued_slot + 4 * crank, 0), issued);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -1384,7 +1379,15 @@ __global__ void __launch_bounds__(192, 1)
   }
 
   tc_fence_before();
-  __syncthreads();
+  if constexpr (C::CTA2)
+    cluster_sync();
+  else
+    __syncthreads();
+  // Before the CTAs may exit, every load that either has issued must have landed.
+  if (leader && warp == 0 && lane == 0) {
+    const uint32_t n0 = ld_shared_u32(issued_slot), n1 = C::CTA2 ? ld_shared_u32(issued_slot + 4) : n0;
+    if (!drain_pair_loads<STAGES>(full_bar, n0, n1, kDrainNs)) record_error(args.err, kErrTimeout);
+  }
   // Every MMA of the pair has completed once the drain barrier has seen the
   // leader's final commit; only then may tensor memory be freed and the CTAs
   // exit (the cluster barrier also keeps each CTA alive while its peer may

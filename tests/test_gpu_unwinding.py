@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import dispatch_gemm_combine_gb300 as moe
+from dispatch_gemm_combine_gb300.runner import LayerRunner
 
 pytestmark = pytest.mark.gpu
 
@@ -48,4 +49,32 @@ def test_orthogonal_updates(shape):
             moe.orthogonalize(g, out, ws)
             moe.check_device_error(ws)
             assert torch.equal(out, want)
+    assert failed
+
+
+@pytest.mark.parametrize("T,H,I,E,k,layout", [(2048, 512, 512, 8, 4, 0), (700, 264, 328, 5, 2, 0), (1500, 384, 256, 6, 3, 1)])
+def test_the_layer(T, H, I, E, k, layout):
+    """Forward and backward of the expert layer, whose products run on such pairs too."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+
+    def bf16(*shape, std=1.0):
+        return (std * torch.randn(shape, generator=g, device="cuda")).to(torch.bfloat16)
+
+    x, dy = bf16(T, H), bf16(T, H)
+    wgu, wd = bf16(E, H, 2 * I, std=H ** -0.5), bf16(E, I, H, std=I ** -0.5)
+    r = LayerRunner(T, H, I, E, k, moe.MOE_ACT_SWIGLU, gate_up_layout=layout)
+    idx, w = torch.empty((T, k), dtype=torch.int32, device="cuda"), torch.empty((T, k), device="cuda")
+    r.route(torch.randn((T, E), generator=g, device="cuda"), idx, w)
+    calls = ((r.ws_fwd, lambda: [r.forward(x, idx, w, wgu, wd)]),
+             (r.ws_bwd, lambda: r.backward(dy, x, idx, w, wgu, wd)))
+    want = [[t.clone() for t in call()] for _, call in calls]
+    r.check()
+    failed = 0
+    for ns in LIMITS_NS:
+        for (ws, call), ref in zip(calls, want):
+            with_limit(ns, call)
+            failed += ended_with_error(ws)
+            r.forward(x, idx, w, wgu, wd)      # (the backward takes what a whole forward saved)
+            assert all(torch.equal(a, b) for a, b in zip(call(), ref))
+    r.check()
     assert failed
