@@ -39,10 +39,11 @@ class LayerRunner:
         self.gave_bias = False
         self.ws_clip, self.ws_clips = None, []
         if backward:
+            # zeros: what route_bwd, orthogonalize and clip_grads take before a backward
             self.dx = torch.empty((T, H), dtype=odt, device=device)
-            self.d_topk_w = torch.empty((T, k), dtype=torch.float32, device=device)
-            self.dw_gate_up = torch.empty((E, H, 2 * I), dtype=torch.float32, device=device)
-            self.dw_down = torch.empty((E, I, H), dtype=torch.float32, device=device)
+            self.d_topk_w = torch.zeros((T, k), dtype=torch.float32, device=device)
+            self.dw_gate_up = torch.zeros((E, H, 2 * I), dtype=torch.float32, device=device)
+            self.dw_down = torch.zeros((E, I, H), dtype=torch.float32, device=device)
 
     def plan(self, topk_idx, stream=None):
         plan(self.shape, topk_idx, self.plan_s, self.ws_plan, stream)
@@ -126,15 +127,16 @@ class LayerRunner:
         """(d_logits [T,E], losses [2]): the gradient of the router's logits, from the
         last backward's d_topk_w (or the one given) through the weights that route()
         made, with `balance` times the load-balancing loss and `z` times the z-loss, and
-        both losses.  The plan must be that of topk_idx, as route() leaves it."""
+        both losses.  The plan must be that of topk_idx, as route() leaves it.  Before a
+        backward it is the losses' gradient alone."""
+        if d_topk_w is None:
+            d_topk_w = getattr(self, "d_topk_w", None)      # (none in a runner without a backward)
         if getattr(self, "ws_route_bwd", None) is None:
             T, E = self.shape.T, self.shape.E
             with torch.cuda.stream(stream):
                 self.ws_route_bwd = route_bwd_workspace(self.shape, self.device)
                 self.d_logits = torch.empty((T, E), dtype=torch.float32, device=self.device)
                 self.losses = torch.empty(2, dtype=torch.float32, device=self.device)
-        if d_topk_w is None:
-            d_topk_w = getattr(self, "d_topk_w", None)      # (none without a backward)
         route_bwd(self.shape, logits, self.d_logits, self.ws_route_bwd, topk_idx, topk_w, d_topk_w,
                   self.plan_t["counts"], balance, z, self.losses, stream)
         return self.d_logits, self.losses
@@ -142,8 +144,9 @@ class LayerRunner:
     def orthogonalize(self, gate_up=None, down=None, steps=5, coefs=None, eps=1e-7, scale=1.0,
                       stream=None):
         """Orthogonal updates (u_gate_up [E,H,2I], u_down [E,I,H], bf16) of the last
-        backward's weight gradients, or of the tensors given (their momenta, bf16 or
-        fp32): for each expert the gate, the up and the down matrix by itself."""
+        backward's weight gradients (zeros before the first), or of the tensors given
+        (their momenta, bf16 or fp32): for each expert the gate, the up and the down
+        matrix by itself."""
         if self.shape.gate_up_layout == MOE_GATE_UP_INTERLEAVED:
             raise ValueError("orthogonalize: gate and up columns are interleaved, not matrices of their own")
         gate_up = self.dw_gate_up if gate_up is None else gate_up
