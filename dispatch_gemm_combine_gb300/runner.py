@@ -37,6 +37,7 @@ class LayerRunner:
                       if training else None)
         self.y = torch.empty((T, H), dtype=odt, device=device)
         self.gave_bias = False
+        self.forward_since = False      # a forward has run after the last backward
         self.ws_clip, self.ws_clips = None, []
         if backward:
             # zeros: what route_bwd, orthogonalize and clip_grads take before a backward
@@ -63,6 +64,7 @@ class LayerRunner:
         ffn_fwd(self.shape, x, topk_idx, topk_w, w_gate_up, w_down, self.y, self.ws_fwd,
                 self.plan_s if use_plan else None, None if inference else self.saved, stream,
                 bias_struct(b_gate_up, b_down))
+        self.forward_since = True
         return self.y
 
     def quantize(self, w_gate_up, w_down, stream=None):
@@ -120,17 +122,22 @@ class LayerRunner:
             ws, saved = self.ws_bwd, self.saved
         ffn_bwd(self.shape, dy, x, topk_idx, topk_w, w_gate_up, w_down, self.plan_s, saved,
                 self.dx, self.d_topk_w, self.dw_gate_up, self.dw_down, ws, stream, bias)
+        self.forward_since = False
         out = (self.dx, self.d_topk_w, self.dw_gate_up, self.dw_down)
         return out + (self.db_gate_up, self.db_down) if with_bias else out
 
     def route_bwd(self, logits, topk_idx, topk_w, d_topk_w=None, balance=0.0, z=0.0, stream=None):
         """(d_logits [T,E], losses [2]): the gradient of the router's logits, from the
-        last backward's d_topk_w (or the one given) through the weights that route()
-        made, with `balance` times the load-balancing loss and `z` times the z-loss, and
-        both losses.  The plan must be that of topk_idx, as route() leaves it.  Before a
-        backward it is the losses' gradient alone."""
+        backward's d_topk_w (or the one given) through the weights that route() made,
+        with `balance` times the load-balancing loss and `z` times the z-loss, and both
+        losses.  The plan must be that of topk_idx, as route() leaves it.  Where a
+        forward has run since the last backward, d_topk_w has to be given (that
+        backward's, where it is meant: runner.d_topk_w); a runner without a backward
+        gives the losses' gradient alone."""
         if d_topk_w is None:
             d_topk_w = getattr(self, "d_topk_w", None)      # (none in a runner without a backward)
+            if d_topk_w is not None and self.forward_since:
+                raise ValueError("route_bwd: d_topk_w is of the backward before the last forward; give the one that is meant")
         if getattr(self, "ws_route_bwd", None) is None:
             T, E = self.shape.T, self.shape.E
             with torch.cuda.stream(stream):

@@ -1,5 +1,5 @@
 """What LayerRunner's methods take where no gradient is given: zeros before the first
-backward, whatever the memory held."""
+backward, whatever the memory held, and never the gradient of an earlier step."""
 
 import pytest
 import torch
@@ -47,3 +47,29 @@ def test_before_the_first_backward():
     assert torch.equal(d, want) and torch.equal(losses, want_losses)
     assert not any(u.any() for u in r.orthogonalize())
     assert r.clip_grads(1.0)[0] == 0
+
+
+def test_router_gradient_is_never_of_an_earlier_step():
+    logits, idx, w, x, dy, wgu, wd = inputs()
+    r = runner()
+
+    def forward(**kw):
+        r.route(logits, idx, w)
+        r.forward(x, idx, w, wgu, wd, **kw)
+
+    forward()
+    with pytest.raises(ValueError):
+        r.route_bwd(logits, idx, w)
+    r.backward(dy, x, idx, w, wgu, wd)
+    right = r.route_bwd(logits, idx, w)[0].clone()
+    assert right.any()
+    for kw in ({}, dict(inference=True)):
+        forward(**kw)
+        with pytest.raises(ValueError):
+            r.route_bwd(logits, idx, w, balance=0.1)
+        # ... but the one that is meant may be given
+        assert torch.equal(r.route_bwd(logits, idx, w, r.d_topk_w)[0], right)
+        forward()
+        r.backward(dy, x, idx, w, wgu, wd)
+        assert torch.equal(r.route_bwd(logits, idx, w)[0], right)
+    r.check()
