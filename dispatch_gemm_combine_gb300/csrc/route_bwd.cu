@@ -15,8 +15,8 @@
 // part.  The choices' terms go through a row of shared memory (a lane writes its
 // choice's term where the lane that owns the column picks it up); a row that names an
 // expert twice adds its terms one after the other.  Sums over the rows: a lane keeps
-// every G-th row's, then over warp and block in a fixed order, then one block over all
-// blocks, in their order too.
+// every G-th row's, then over warp and block in a fixed order, then a second kernel
+// over all blocks, in their order too.
 //
 // Measured: 65536 x 256, top-8, 31 us (28 in the kernel): 300 instructions a row and the
 // latency of its shuffles, at 29 warps per SM, hold it at two thirds of the memory's
@@ -46,7 +46,6 @@ struct RouteBwd {
   const float* dw;
   float* d;
   float2* part;     // [blocks]: sums of F and of l^2, or null
-  unsigned* done;   // blocks whose sums are there, 0 between calls; or null: a second kernel adds
   float* losses;
   int* err;
   int64_t T;
@@ -98,8 +97,13 @@ __device__ __forceinline__ void copy_if(uint32_t dst, const float* src, bool on)
 
 // losses[i] = sum of the blocks' sums / T: a thread adds blocks q, q + 256, ..., then the
 // threads' sums by warps: sixteen fp32 additions deep.  (In 64 bits, of which this GPU
-// adds few a clock, the call takes 2 us more.)
-__device__ __forceinline__ void add_blocks(const float2* part, int blocks, float inv_T, float* losses, float (&sums)[kWarps][2]) {
+// adds few a clock, the call takes 2 us more.)  A kernel of its own, which starts while
+// the last rows are done.  (The block that comes last could add them too, 8192 x 128 8.3 us
+// a call among others instead of 10.2, 12.9 alone instead of 11.9, but would be found by a
+// count that the workspace keeps from call to call.)
+__global__ void __launch_bounds__(kThreads) route_losses_kernel(const float2* part, int blocks, float inv_T, float* losses) {
+  __shared__ float sums[kWarps][2];
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the sums are there
   float2 v[kMaxRouteBlocks / kThreads];
 #pragma unroll
   for (int i = 0; i < kMaxRouteBlocks / kThreads; ++i) {
@@ -275,29 +279,14 @@ __global__ void __launch_bounds__(kThreads) route_bwd_kernel(const RouteBwd a) {
   sum_F = warp_sum(sum_F), sum_l = warp_sum(sum_l);
   if (lane == 0) sums[warp][0] = sum_F, sums[warp][1] = sum_l;
   __syncthreads();
-  bool last = false;
   if (threadIdx.x == 0) {
     float2 v = make_float2(0.f, 0.f);
     for (int i = 0; i < kWarps; ++i) v.x += sums[i][0], v.y += sums[i][1];
-    if (gridDim.x == 1) {      // no other block's to be added
+    if (gridDim.x == 1)        // no other block's to be added
       a.losses[0] = v.x * a.inv_T, a.losses[1] = v.y * a.inv_T;
-    } else {
+    else
       __stcg(a.part + blockIdx.x, v);
-      if (a.done) {
-        __threadfence();
-        last = atomicInc(a.done, gridDim.x - 1) == gridDim.x - 1;      // (back to 0)
-      }
-    }
   }
-  if (!a.done || !__syncthreads_or(last)) return;
-  __threadfence();
-  add_blocks(a.part, gridDim.x, a.inv_T, a.losses, sums);
-}
-
-__global__ void __launch_bounds__(kThreads) route_losses_kernel(const float2* part, int blocks, float inv_T, float* losses) {
-  __shared__ float sums[kWarps][2];
-  asm volatile("griddepcontrol.wait;" ::: "memory");   // the sums are there
-  add_blocks(part, blocks, inv_T, losses, sums);
 }
 
 template <int G, int PER, bool VEC>
@@ -313,11 +302,6 @@ cudaError_t launch_route_bwd_v(RouteBwd& a, int sms, int* blocks, cudaStream_t s
   *blocks = static_cast<int>(std::min<int64_t>((a.T + R - 1) / R, most));
   // two rounds of one block take less than the sum of two blocks' sums
   if (*blocks == 2 && a.losses) *blocks = 1;
-  // where each block has one round, launches take longer than the kernel: the block that
-  // comes last adds the sums (8192 x 128: a call 8.6 us, 10.5 with a second kernel; the GPU
-  // alone, in a graph, 6.5 and 5.7); otherwise the second kernel, which starts while the
-  // last rows are done (16384 x 512: a call 14.5 us, 16.3 without it)
-  if (a.T > static_cast<int64_t>(most) * R) a.done = nullptr;
   route_bwd_kernel<G, PER, VEC><<<*blocks, kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
@@ -367,7 +351,6 @@ moe_status moe_route_bwd(const moe_shape* s, const float* logits, const int32_t*
   a.logits = softmax ? logits : nullptr, a.idx = topk_idx, a.w = topk_w, a.dw = d_topk_w;
   a.counts = softmax ? counts : nullptr, a.d = d_logits;
   a.part = losses ? reinterpret_cast<float2*>(static_cast<char*>(ws) + 256) : nullptr;
-  a.done = losses ? reinterpret_cast<unsigned*>(static_cast<char*>(ws) + 64) : nullptr;
   a.err = static_cast<int*>(ws);
   a.T = s->T, a.E = s->E, a.k = s->k;
   a.balance_T = static_cast<float>(balance / T), a.z2_T = static_cast<float>(2.0 * z / T);
@@ -384,7 +367,7 @@ moe_status moe_route_bwd(const moe_shape* s, const float* logits, const int32_t*
            : E <= 512               ? launch_route_bwd<32, 16>(a, sms, &blocks, st)
                                     : launch_route_bwd<32, 32>(a, sms, &blocks, st);
   });
-  if (e == cudaSuccess && losses && blocks > 1 && !a.done)
+  if (e == cudaSuccess && losses && blocks > 1)
     e = abi_tracked(kAbiRouteBwd, 1, st, [&] {
       // (may start while the last rows are done)
       cudaLaunchConfig_t cfg = {};

@@ -226,3 +226,20 @@ def test_refusals():
         moe.route_bwd(shape, v, d, ws, topk_idx=idx.long(), topk_w=w, d_topk_w=dw)
     with pytest.raises(moe.MoeError):
         moe.route_bwd(shape, v, d, ws[:256], z=1.0, counts=counts)
+
+
+@pytest.mark.parametrize("fill", [0x01, 0xA5, 0xFF])
+@pytest.mark.parametrize("T,E,k", [(1000, 128, 4), (5000, 61, 4), (70, 256, 8)])
+def test_only_the_error_word_is_kept_in_the_workspace(T, E, k, fill):
+    """Whatever the rest of the workspace holds, its header too."""
+    c = Case(T, E, k)
+    shape = moe.Shape(T, 8, 8, E, k)
+    ws = moe.route_bwd_workspace(shape)
+    d0, l0, _ = c.run()
+    t = [v.cuda() for v in (c.logits, c.idx, c.w, c.dw, c.counts)]
+    for _ in range(3):
+        ws[4:].fill_(fill)
+        d, losses = torch.zeros((T, E), device="cuda"), torch.zeros(2, device="cuda")
+        moe.route_bwd(shape, t[0], d, ws, t[1], t[2], t[3], t[4], c.balance, c.z, losses)
+        assert torch.equal(d.cpu(), d0) and torch.equal(losses.cpu(), l0)
+    moe.check_device_error(ws)
