@@ -78,14 +78,6 @@ __device__ __forceinline__ float4 row_sum4(const float4& v) {
                      __shfl_sync(0xffffffffu, s, 1, G), __shfl_sync(0xffffffffu, s, 3, G));
 }
 
-// 2^40 e^x for x <= 0: the instruction gives 0 below 2^-126, which is then far below
-// the least fp32 probability.
-__device__ __forceinline__ float exp2_40(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(x, 1.44269504f, 40.f)));
-  return r;
-}
-
 // 4 or 16 bytes to shared memory, without a branch.
 template <int BYTES>
 __device__ __forceinline__ void copy_if(uint32_t dst, const float* src, bool on) {
@@ -210,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) route_bwd_kernel(const RouteBwd a) {
       if (top == -INFINITY) top = 0.f;      // every expert masked: p = 0
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        v[i] = exp2_40(v[i] - top);
+        v[i] = __expf(v[i] - top);
         s.x += v[i];
         s.y = fmaf(v[i], f[i], s.y);
       }
@@ -241,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) route_bwd_kernel(const RouteBwd a) {
     if (softmax) {
       // (a row that is NaN has s = NaN, which is not 0: it stays NaN)
       const float inv = s.x == 0.f ? 0.f : __fdividef(1.f, s.x);
-      const float l = s.x == 0.f ? 0.f : top + logf(s.x * 0x1p-40f);
+      const float l = s.x == 0.f ? 0.f : top + logf(s.x);
       const float F = s.y * inv;
       if (on && g == (turn & (G - 1))) {
         sum_F += F;

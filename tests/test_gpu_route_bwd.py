@@ -243,3 +243,37 @@ def test_only_the_error_word_is_kept_in_the_workspace(T, E, k, fill):
         moe.route_bwd(shape, t[0], d, ws, t[1], t[2], t[3], t[4], c.balance, c.z, losses)
         assert torch.equal(d.cpu(), d0) and torch.equal(losses.cpu(), l0)
     moe.check_device_error(ws)
+
+
+@pytest.mark.parametrize("E", [60, 128, 255, 500, 1024])
+def test_probabilities_to_fp32s_roundings(E):
+    """The error's 2-norm, against roundings that are as likely to go either way (each u32 /
+    sqrt(3) at most): the balance loss's gradient p_e (f_e - F) where one expert alone has
+    tokens, so nothing cancels but in its column, left out here.  The logits' differences
+    are exact.  An exponential and a quotient to 2 ulp each (4 u32 / sqrt(3) = 2.3 u32), a
+    row's sum at most 32 + 5 additions deep but adding the small to the large (2.1 u32 as
+    for 13 of equal size), sum and quotient twice (6.2 u32), the sum of F and eight further
+    roundings: 7.1 u32 in all."""
+    c = Case(600, E, 2, balance=1.0, z=0.0, weights=False)
+    c.logits = (c.logits * 64).round() / 64
+    c.counts.zero_()
+    c.counts[E // 3] = 77
+    d, _, _ = c.run(losses=False)
+    want = c.exact()[0]
+    keep = torch.arange(E) != E // 3
+    err = (d.double() - want)[:, keep].norm() / want[:, keep].norm()
+    assert err <= 8 * U32
+
+
+def test_probabilities_far_below_the_largest():
+    """Down to the least fp32 number: 2 ulp of the exponential and what a subnormal's place
+    rounds (half of 2^-149, times the factors behind it)."""
+    c = Case(1, 200, 2, balance=1.0, z=0.0, weights=False)
+    c.logits[0] = -torch.arange(200) * 0.53125
+    c.counts.zero_()
+    c.counts[0] = 2
+    d, _, _ = c.run(losses=False)
+    want = c.exact()[0]
+    assert d[0, 1:].min() < 0 and d[0, 150] != 0
+    # |d| = p f_0 p_0 with f_0 = E / 2 * 2 / k = 100 here: a subnormal p's half step by 100
+    assert torch.all((d.double() - want).abs()[0, 1:] <= 64 * U32 * want.abs()[0, 1:] + 200 * 2.0 ** -150)
