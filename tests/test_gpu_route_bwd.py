@@ -277,3 +277,13 @@ def test_probabilities_far_below_the_largest():
     assert d[0, 1:].min() < 0 and d[0, 150] != 0
     # |d| = p f_0 p_0 with f_0 = E / 2 * 2 / k = 100 here: a subnormal p's half step by 100
     assert torch.all((d.double() - want).abs()[0, 1:] <= 64 * U32 * want.abs()[0, 1:] + 200 * 2.0 ** -150)
+
+
+@pytest.mark.parametrize("T,E,k", [(100000, 32, 2), (100001, 62, 6), (50000, 128, 16), (50001, 127, 16), (25000, 256, 8), (25001, 255, 8),
+                                   (20000, 512, 8), (20001, 511, 8), (7000, 1024, 32), (7001, 1023, 32)])
+def test_many_rows_per_warp(T, E, k):
+    """At least five rows for each, so that all stages of the copies ahead are used again,
+    and a last round that not all warps have."""
+    Case(T, E, k).check()
+    Case(T, E, k, weights=False, balance=0.3, z=0.0).check()
+    Case(T, E, k, balance=0.0, z=0.0).check(losses=False, counts=False, logits=False)
