@@ -18,7 +18,8 @@
 // fp16 (11 bits) and not bf16 (8 bits): singular values far below the largest grow by
 // up to c0 per step, and with them what the roundings left there; with bf16 operands
 // the result of a Gaussian g is 1e-2 off, with fp16 1.1e-3 (the bf16 output's own
-// rounding: 1.7e-3).  fp16's range is kept by powers of two: X holds S x and A and B
+// rounding: 1.7e-3).  A g of low rank shows it most, 2.5e-2 for rank 32 and 8e-2 for
+// rank 4: what it does not contain is nothing but roundings, grown c0-fold a step.  fp16's range is kept by powers of two: X holds S x and A and B
 // hold S^2 times theirs, S near sqrt(max(M, N)), so that typical values are far from
 // both ends; the coefficients' bounds (checked on the host) keep the largest below
 // 60000.

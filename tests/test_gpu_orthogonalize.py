@@ -339,3 +339,47 @@ def test_waits_without_a_limit():
         assert torch.equal(run(g), want)
     finally:
         moe.moe_set_wait_timeout_ns(before)
+
+
+def roundings(g, steps=5, eps=1e-7):
+    """The error in the 2-norm, relative to the result's, that the fp16 roundings leave.  A
+    rounding has at most 2^-11 / sqrt(3) of its matrix's norm and points anywhere; those of
+    x_j grow by c0 in every step to come, those of a and b reach x through the products (a
+    random matrix times x has its norms' product over the root of m; a's by |c1| + 2 c2
+    s^2) and grow by c0 from the next step on.  They are independent: the root of their
+    squares' sum.  (c0 is the growth of what g does not contain, and more than that of
+    what it does.)"""
+    r = 2.0 ** -11 / math.sqrt(3)
+    x = start(g, eps)
+    x = x.mT if x.shape[-2] > x.shape[-1] else x
+    m, t = x.shape[-2], 0.0
+    c0, c1, c2 = COEFS
+    for j in range(steps):
+        a = x @ x.mT
+        b = c0 * torch.eye(m, dtype=x.dtype, device=x.device) + c1 * a + c2 * (a @ a)
+        n, s2 = float(x.norm()), float(torch.linalg.eigvalsh(a)[-1])
+        to_come = c0 ** (steps - 1 - j)
+        t += (r * n * c0 * to_come) ** 2
+        t += (r * float(a.norm()) * n / math.sqrt(m) * (abs(c1) + 2 * c2 * s2) * to_come) ** 2
+        t += (r * float(b.norm()) * n / math.sqrt(m) * to_come) ** 2
+        x = b @ x
+    return math.sqrt(t) / float(x.norm())
+
+
+SPECTRA = {"falls to 1e-3": lambda k: 1e-3 ** (torch.arange(k) / (k - 1)), "falls to 1e-5": lambda k: 1e-5 ** (torch.arange(k) / (k - 1)),
+           "as 1 / i": lambda k: 1.0 / torch.arange(1, k + 1), "half of the rank": lambda k: (torch.arange(k) < k // 2).float(),
+           "rank 32": lambda k: (torch.arange(k) < 32).float(), "rank 4": lambda k: (torch.arange(k) < 4).float()}
+
+
+@pytest.mark.parametrize("M,N", [(100, 700), (128, 64), (300, 140), (256, 512), (1030, 700)])
+@pytest.mark.parametrize("name", list(SPECTRA))
+def test_gradients_of_less_than_full_rank(M, N, name):
+    """As of an expert with fewer tokens than rows, or singular values that fall off: the
+    largest known case of what fp16 between the steps costs."""
+    k = min(M, N)
+    gen = torch.Generator().manual_seed(8)
+    q = [torch.linalg.qr(torch.randn((n, k), generator=gen, dtype=torch.float64))[0] for n in (M, N)]
+    g = ((q[0] * SPECTRA[name](k).double()) @ q[1].mT).float().cuda()
+    err = rel(run(g), exact(g))
+    assert err <= U + roundings(g)
+    print("%s, %d x %d: %.1e of at most %.1e" % (name, M, N, err, U + roundings(g)))
