@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(192, 1)
     // (one lane issues everything unless the mode keeps the whole warp in
     // step, see GemmCfg::kOneLane)
     if (!C::kOneLane || lane == 0) {
-    // the leader's full barriers, which count the bytes of both CTAs
+    // the leader's full barriers, which take an arrival and the bytes of each CTA
     const uint32_t full_bar_l = leader_addr(full_bar);
     int stage = 0;
     uint32_t phase = 0;

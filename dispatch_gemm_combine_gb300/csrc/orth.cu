@@ -19,13 +19,13 @@
 // up to c0 per step, and with them what the roundings left there; with bf16 operands
 // the result of a Gaussian g is 1e-2 off, with fp16 1.1e-3 (the bf16 output's own
 // rounding: 1.7e-3).  A g of low rank shows it most, 2.5e-2 for rank 32 and 8e-2 for
-// rank 4: what it does not contain is nothing but roundings, grown c0-fold a step.  fp16's range is kept by powers of two: X holds S x and A and B
-// hold S^2 times theirs, S near sqrt(max(M, N)), so that typical values are far from
-// both ends; the coefficients' bounds (checked on the host) keep the largest below
-// 60000.
+// rank 4: what it does not contain is nothing but roundings, grown c0-fold a step.
+// fp16's range is kept by powers of two: X holds S x and A and B hold S^2 times theirs,
+// S near sqrt(max(M, N)), so that typical values are far from both ends; the
+// coefficients' bounds (checked on the host) keep the largest below 60000.
 //
-// Measured, five steps: 4 of 2880 x 2880 fp32 1.33 - 1.44 ms (by the clock that the power
-// leaves), 8 of 2816 x 2816 at 1.66 PFLOP/s of what is needed, at the rate that a library
+// Measured, five steps: 4 of 2880 x 2880 fp32 1.27 ms, 1.48 in a row of them (by the clock
+// that the power leaves), 8 of 2816 x 2816 at 1.66 PFLOP/s of what is needed, at the rate that a library
 // product sustains; 6 of 333 x 1001 101 us and 8 of 128 x 128 23 us, both bound by the
 // chain of dependent steps.
 #include <algorithm>

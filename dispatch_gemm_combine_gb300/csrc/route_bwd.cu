@@ -285,7 +285,8 @@ template <int G, int PER, bool VEC>
 cudaError_t launch_route_bwd_v(RouteBwd& a, int sms, int* blocks, cudaStream_t st) {
   constexpr int R = 32 / G * kWarps;
   constexpr int smem = kWarps * (kRowsAhead + 1) * 32 * PER * static_cast<int>(sizeof(float));
-  // by registers (five blocks of 48 registers spill: 65536 x 256 38 us instead of 33)
+  // by registers (five blocks of 48 registers spill: 65536 x 256 38 us instead of 33), but
+  // for 16 columns one by one: 107 registers leave room for two, and the third one waits
   constexpr int per_sm = std::min(PER <= 8 ? 4 : (PER <= 16 ? 3 : 1), kRingPerSm / smem);
   static std::atomic<uint64_t> ready{0};
   const cudaError_t e = allow_smem(route_bwd_kernel<G, PER, VEC>, ready);
