@@ -18,7 +18,7 @@
 // every G-th row's, then over warp and block in a fixed order, then a second kernel
 // over all blocks, in their order too.
 //
-// Measured: 65536 x 256, top-8, 31 us (28 in the kernel): 300 instructions a row and the
+// Measured: 65536 x 256, top-8, 31 us (29 in the kernel): 300 instructions a row and the
 // latency of its shuffles, at 29 warps per SM, hold it at two thirds of the memory's
 // rate; 65536 x 128 on half warps 19 us (33 on whole ones).
 #include <algorithm>
